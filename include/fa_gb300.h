@@ -20,7 +20,8 @@
  *     device memory per call.  The one exception is a one-time allocation:
  *     fa_sparse_mla_decode allocates a partial-result workspace for a
  *     (device, stream) on the first call there that needs one (see that
- *     entry point).  fa_sparse_mla_decode_noalloc never allocates.
+ *     entry point).  fa_sparse_mla_decode_noalloc never allocates, and
+ *     fa_paged_attn takes its workspace from the caller.
  *     The first call on a device queries device attributes once; make it
  *     before any stream capture that is to contain a call.
  *   - Errors detected on the host (argument checks) are returned before any
@@ -323,6 +324,189 @@ fa_status fa_merge_attn_states(void* out, float* out_lse, const void* prefix_out
                                const float* prefix_lse, const void* suffix_out,
                                const float* suffix_lse, int total_q, int num_heads,
                                int head_dim, fa_stream_t stream);
+
+/*
+ * ---- Serving operators around the attention forward ----------------------
+ *
+ * fa_qk_norm_rope makes q and k ready for fa_varlen_fwd or fa_paged_attn;
+ * fa_paged_kv_append writes new keys and values into a paged 8-bit cache;
+ * fa_paged_attn attends over that cache; fa_paged_kv_gather reads it back as
+ * the packed bf16 tensors fa_varlen_fwd takes.  The method's pages have no
+ * counterpart to these entry points.
+ *
+ * The cache
+ *   k_cache, v_cache  e4m3 [num_pages, num_heads_k, 64, head_dim]: a page
+ *                 holds 64 tokens; all tokens of one head lie together, so
+ *                 that attention reads a (page, head) as one block.
+ *   k_scale, v_scale  fp32 [num_pages, num_heads_k]; a value is code * scale.
+ *                 fa_paged_kv_append keeps them at powers of two between
+ *                 2^-64 and 2^64.  fa_paged_attn and fa_paged_kv_gather take
+ *                 any scale >= 0 within that range (a cache quantised
+ *                 elsewhere).
+ *   page_table    int32 [batch, max_pages_per_seq]: the physical page of each
+ *                 logical page of a sequence.  A page id outside
+ *                 [0, num_pages) names no page: nothing is written there,
+ *                 attention skips its keys, the gather gives zeros.  Entries
+ *                 past a sequence's length are not read.
+ *   head_dim      64, 80, 96 or 128.
+ * cu_seqlens arrays are read through the clamp of fa_varlen_fwd.
+ */
+
+/*
+ * fa_qk_norm_rope -- RMS norm of each head row of q and k and the rotation by
+ * its position, in one pass:
+ *     y = w * x / sqrt(mean(x^2) + eps)           (no weight: y = x)
+ *     (a, b) -> (a cos - b sin, b cos + a sin)    over the pairs of the first
+ *                                                 rot_dim dims of y
+ * in fp32, rounded to bf16 once.
+ *
+ *   q, k          bf16 [num_tokens, heads, head_dim] strided views (strides
+ *                 in elements, rules of fa_varlen_fwd_strided), such as parts
+ *                 of a fused projection.  num_heads or num_heads_k may be 0:
+ *                 that side is then left out (null pointers).
+ *   positions     int32 [num_tokens]; a token whose position is outside
+ *                 [0, max_pos) is skipped: its output rows are left as they
+ *                 were (padding rows of a captured batch: -1).  Not read with
+ *                 rot_dim = 0.
+ *   cos_sin       fp32 [max_pos, rot_dim]: the cosines of a position's
+ *                 rot_dim / 2 angles, then their sines.
+ *   q_weight, k_weight  fp32 [head_dim] or NULL (that side is not normed).
+ *   head_dim      a multiple of 8 up to 256.
+ *   rot_dim       a multiple of 16 up to head_dim; 0 = no rotation (cos_sin
+ *                 and positions may be NULL).
+ *   interleaved   0: pairs (i, i + rot_dim / 2); nonzero: (2i, 2i + 1).
+ *   q_out, k_out  bf16 strided views; each may be its input with the same
+ *                 strides (in place), and overlap nothing else.
+ *
+ * Host errors: FA_ERR_INVALID_ARG (null pointers, sizes, strides, alignment:
+ * 16 bytes for everything but positions, eps negative or not finite),
+ * FA_ERR_UNSUPPORTED (head_dim, more than 2^31 - 1 rows), FA_ERR_ARCH,
+ * FA_ERR_LAUNCH.
+ */
+fa_status fa_qk_norm_rope(const void* q, long long q_row_stride, long long q_head_stride,
+                          const void* k, long long k_row_stride, long long k_head_stride,
+                          const int* positions, const float* cos_sin, const float* q_weight,
+                          const float* k_weight, int num_tokens, int num_heads, int num_heads_k,
+                          int head_dim, int rot_dim, int max_pos, int interleaved, float eps,
+                          void* q_out, long long q_out_row_stride, long long q_out_head_stride,
+                          void* k_out, long long k_out_row_stride, long long k_out_head_stride,
+                          fa_stream_t stream);
+
+/*
+ * fa_paged_kv_append -- writes the new keys and values of every sequence into
+ * its pages, the keys normed and rotated on the way (as fa_qk_norm_rope does,
+ * from one rounding: fp32 to e4m3).
+ *
+ *   k, v          bf16 [total_new, num_heads_k, head_dim] strided views.
+ *   cu_seqlens    int32 [batch + 1]: sequence b's new tokens.
+ *   seq_lens      int32 [batch]: its length with the new tokens; they take
+ *                 the positions [seq_lens[b] - n, seq_lens[b]), which are
+ *                 also their angles.  The same array goes to fa_paged_attn.
+ *                 With seq_lens[b] < n nothing of the sequence is written.
+ *   k_weight      fp32 [head_dim] or NULL (keys not normed).
+ *   cos_sin, rot_dim, max_pos, interleaved  as fa_qk_norm_rope; rot_dim = 0
+ *                 for keys that are rotated already (max_pos is then
+ *                 ignored).
+ * Positions from 64 * max_pages_per_seq on, and from max_pos on with a
+ * rotation, are not written.
+ *
+ * Scale of a (page, head): the smallest power of two with amax <= 448 scale
+ * over the finite values of the page's tokens.  A page whose first slots were
+ * filled by earlier calls keeps its scale or raises it; its earlier codes are
+ * then rounded again to the new one.  A call that writes slot 0 of a page
+ * starts the page afresh.  Infinities saturate, NaN stays NaN.  Slots behind
+ * the new tokens are left as they were.
+ *
+ * A page may be written for one sequence of a call only: pages that sequences
+ * share are full ones.  (Two writers of one page race for its scale and
+ * codes; no other page is touched.)
+ *
+ * Host errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED (head_dim, sizes past
+ * 32-bit indices), FA_ERR_ARCH, FA_ERR_LAUNCH.
+ */
+fa_status fa_paged_kv_append(const void* k, long long k_row_stride, long long k_head_stride,
+                             const void* v, long long v_row_stride, long long v_head_stride,
+                             const int* cu_seqlens, const int* seq_lens, const int* page_table,
+                             int batch, int total_new, int num_heads_k, int head_dim,
+                             int num_pages, int max_pages_per_seq, const float* k_weight,
+                             float eps, const float* cos_sin, int rot_dim, int max_pos,
+                             int interleaved, void* k_cache, void* v_cache, float* k_scale,
+                             float* v_scale, fa_stream_t stream);
+
+/*
+ * fa_paged_attn -- attention of each sequence's query rows (one of a decode
+ * step, several drafts, a chunk) over its cached keys and values:
+ *     O = softmax(softmax_scale * Q Kt + mask) V
+ *
+ *   q             bf16 [total_q, num_heads, head_dim] strided view; query
+ *                 head h reads head h / (num_heads / num_heads_k) of the
+ *                 cache.
+ *   cu_seqlens_q  int32 [batch + 1]: sequence b's query rows.
+ *   seq_lens      int32 [batch]: keys of each sequence in the cache, clamped
+ *                 to [0, 64 * max_pages_per_seq].
+ *   causal        nonzero: row i of n sees key j iff j <= seq_len - n + i.
+ *                 (0: every key; a chunk's own keys can then come from
+ *                 fa_varlen_fwd and be merged by fa_merge_attn_states.)
+ *   window_left   -1, or row i sees only j >= seq_len - n + i - window_left.
+ *   max_seqlen_q, max_seqlen_k  host hints only (0 = unknown): they steer the
+ *                 launch shape, never the result beyond rounding.
+ *   out           bf16 [total_q, num_heads, head_dim]; lse fp32 [num_heads,
+ *                 total_q] natural log, or NULL.
+ *   workspace     caller-owned device scratch of at least the bytes
+ *                 fa_paged_attn_plan gives, 16-byte aligned (NULL if 0).  Its
+ *                 contents need not be initialised and do not outlive the
+ *                 call; calls that can overlap in time need one each (two
+ *                 captured graphs that may replay together included).
+ *
+ * A row with no visible key gets O = 0 and LSE = -inf; rows of q behind the
+ * last sequence are left as they were.  Keys a row does not see never reach
+ * it, whatever they hold, but for one case: the value of a NaN code that some
+ * other row of the same sequence in the call sees spreads to it.
+ *
+ * Host errors: FA_ERR_INVALID_ARG (among them a workspace that is too small),
+ * FA_ERR_UNSUPPORTED (head_dim, sizes past 32-bit indices), FA_ERR_ARCH,
+ * FA_ERR_LAUNCH.
+ */
+fa_status fa_paged_attn(const void* q, long long q_row_stride, long long q_head_stride,
+                        const void* k_cache, const void* v_cache, const float* k_scale,
+                        const float* v_scale, const int* cu_seqlens_q, const int* seq_lens,
+                        const int* page_table, int batch, int total_q, int num_heads,
+                        int num_heads_k, int head_dim, int num_pages, int max_pages_per_seq,
+                        int max_seqlen_q, int max_seqlen_k, float softmax_scale, int causal,
+                        int window_left, void* out, float* lse, void* workspace,
+                        size_t workspace_bytes, fa_stream_t stream);
+
+/*
+ * fa_paged_attn_plan -- the launch shape and the workspace of a fa_paged_attn
+ * call of these sizes on the current device, without launching anything.
+ *
+ *   *grid             CTAs of the launch (0 when total_q = 0)
+ *   *rows_per_tile    query rows (tokens x heads of one group) of a tile
+ *   *workspace_bytes  scratch the call needs
+ *
+ * Host errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED (head_dim), FA_ERR_ARCH.
+ */
+fa_status fa_paged_attn_plan(int batch, int total_q, int num_heads, int num_heads_k, int head_dim,
+                             int max_seqlen_q, int* grid, int* rows_per_tile,
+                             size_t* workspace_bytes);
+
+/*
+ * fa_paged_kv_gather -- the first n = cu_seqlens[b + 1] - cu_seqlens[b]
+ * cached tokens of every sequence as packed bf16 tensors, the k and v (with
+ * cu_seqlens as cu_seqlens_k) of a fa_varlen_fwd call: a long chunk of
+ * queries against its whole context.  code * scale is rounded once (not at
+ * all under a power-of-two scale, down to bf16's subnormals).
+ *
+ *   k_out, v_out  bf16 [total_k, num_heads_k, head_dim], written; rows behind
+ *                 the last sequence are left as they were.  Positions whose
+ *                 page is not in the table or not in the cache read as zero.
+ *
+ * Host errors: as fa_paged_kv_append.
+ */
+fa_status fa_paged_kv_gather(const void* k_cache, const void* v_cache, const float* k_scale,
+                             const float* v_scale, const int* cu_seqlens, const int* page_table,
+                             int batch, int total_k, int num_heads_k, int head_dim, int num_pages,
+                             int max_pages_per_seq, void* k_out, void* v_out, fa_stream_t stream);
 
 /*
  * fa_get_device_status -- reads and clears the library's device status word

@@ -21,11 +21,24 @@ Entry points (same names as the C ABI):
                                out, lse=None, stream=None)
   fa_merge_attn_states(prefix_out, prefix_lse, suffix_out, suffix_lse,
                        out=None, out_lse=None, stream=None)
+  fa_qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=1e-6,
+                  interleaved=False, q_out=None, k_out=None, stream=None)
+  fa_paged_kv_append(k, v, cu_seqlens, seq_lens, page_table, k_cache, v_cache, k_scale,
+                     v_scale, cos_sin=None, k_weight=None, eps=1e-6, interleaved=False,
+                     stream=None)
+  fa_paged_attn(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, seq_lens, page_table,
+                max_seqlen_q=0, max_seqlen_k=0, softmax_scale=None, causal=True,
+                window_left=-1, out=None, lse=None, return_lse=False, workspace=None,
+                stream=None)
+  fa_paged_attn_plan(batch, total_q, num_heads, num_heads_k, head_dim, max_seqlen_q=0)
+  fa_paged_kv_gather(k_cache, v_cache, k_scale, v_scale, cu_seqlens, page_table, total_k,
+                     k_out=None, v_out=None, stream=None)
   fa_get_device_status()
   fa_set_wait_limit_ns(ns)
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -44,7 +57,8 @@ LIB_PATH = os.path.join(_PKG, "libfa_gb300.so")
 # Exported C symbols (kept in sync with include/fa_gb300.h; a CPU test checks).
 EXPORTS = ("fa_varlen_fwd", "fa_varlen_fwd_plan", "fa_varlen_fwd_strided", "fa_sparse_mla_decode",
            "fa_sparse_mla_decode_plan", "fa_sparse_mla_decode_noalloc", "fa_merge_attn_states",
-           "fa_get_device_status", "fa_set_wait_limit_ns", "fa_status_string")
+           "fa_qk_norm_rope", "fa_paged_kv_append", "fa_paged_attn", "fa_paged_attn_plan",
+           "fa_paged_kv_gather", "fa_get_device_status", "fa_set_wait_limit_ns", "fa_status_string")
 
 _lib = None
 
@@ -89,6 +103,21 @@ def load_library():
     lib.fa_sparse_mla_decode_noalloc.restype = i32
     lib.fa_merge_attn_states.argtypes = [p, p, p, p, p, p, i32, i32, i32, p]
     lib.fa_merge_attn_states.restype = i32
+    lib.fa_qk_norm_rope.argtypes = [p, i64, i64, p, i64, i64, p, p, p, p, i32, i32, i32, i32,
+                                    i32, i32, i32, f32, p, i64, i64, p, i64, i64, p]
+    lib.fa_qk_norm_rope.restype = i32
+    lib.fa_paged_kv_append.argtypes = [p, i64, i64, p, i64, i64, p, p, p, i32, i32, i32, i32, i32,
+                                       i32, p, f32, p, i32, i32, i32, p, p, p, p, p]
+    lib.fa_paged_kv_append.restype = i32
+    size = ctypes.c_size_t
+    lib.fa_paged_attn.argtypes = [p, i64, i64, p, p, p, p, p, p, p, i32, i32, i32, i32, i32, i32,
+                                  i32, i32, i32, f32, i32, i32, p, p, p, size, p]
+    lib.fa_paged_attn.restype = i32
+    lib.fa_paged_attn_plan.argtypes = [i32, i32, i32, i32, i32, i32, pi, pi,
+                                       ctypes.POINTER(size)]
+    lib.fa_paged_attn_plan.restype = i32
+    lib.fa_paged_kv_gather.argtypes = [p, p, p, p, p, p, i32, i32, i32, i32, i32, i32, p, p, p]
+    lib.fa_paged_kv_gather.restype = i32
     lib.fa_set_wait_limit_ns.argtypes = [ctypes.c_ulonglong]
     lib.fa_set_wait_limit_ns.restype = i32
     lib.fa_get_device_status.argtypes = []
@@ -313,6 +342,253 @@ def fa_merge_attn_states(prefix_out, prefix_lse, suffix_out, suffix_lse, out=Non
     if st != FA_OK:
         raise FaError(st, "fa_merge_attn_states")
     return out, out_lse
+
+
+@contextlib.contextmanager
+def _on(stream, **tensors):
+    """Checks that the given tensors (None: left out) are on one CUDA device,
+    makes it and the call's stream current, and yields the stream pointer.
+    What is allocated inside belongs to that stream."""
+    import torch
+    device = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    with torch.cuda.stream(stream):
+        yield ctypes.c_void_p(stream.cuda_stream)
+
+
+def _shape(t, name, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _check_rope(cos_sin, weights, d):
+    """rot_dim and max_pos of a rotation table (None: no rotation)."""
+    import torch
+    for name, w in weights:
+        if w is not None:
+            _check(w, name, torch.float32, 1)
+            _shape(w, name, (d,))
+    if cos_sin is None:
+        return 0, 0
+    _check(cos_sin, "cos_sin", torch.float32, 2)
+    return cos_sin.shape[1], cos_sin.shape[0]
+
+
+def _check_cache(k_cache, v_cache, k_scale, v_scale, cu_seqlens, page_table):
+    """(batch, pages, kv heads, head dim, pages of a sequence) of a cache."""
+    import torch
+    _check(k_cache, "k_cache", torch.float8_e4m3fn, 4)
+    _check(v_cache, "v_cache", torch.float8_e4m3fn, 4)
+    _check(k_scale, "k_scale", torch.float32, 2)
+    _check(v_scale, "v_scale", torch.float32, 2)
+    _check(cu_seqlens, "cu_seqlens", torch.int32, 1)
+    _check(page_table, "page_table", torch.int32, 2)
+    pages, hk, page, d = k_cache.shape
+    if page != 64:
+        raise ValueError(f"a cache page has 64 tokens, got {page}")
+    _shape(v_cache, "v_cache", k_cache.shape)
+    _shape(k_scale, "k_scale", (pages, hk))
+    _shape(v_scale, "v_scale", (pages, hk))
+    batch = cu_seqlens.shape[0] - 1
+    if page_table.shape[0] != batch:
+        raise ValueError("page_table must have one row per sequence")
+    return batch, pages, hk, d, page_table.shape[1]
+
+
+def fa_qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=1e-6,
+                    interleaved=False, q_out=None, k_out=None, stream=None):
+    """Per-head RMS norm of q and k with the position rotation, in one pass;
+    see fa_qk_norm_rope in include/fa_gb300.h.
+
+    q [T, H, d], k [T, H_k, d] bf16 (strided views allowed; either may be
+    None), positions [T] int32, cos_sin [max_pos, rot_dim] fp32 (cosines, then
+    sines; None: no rotation, positions may be None too), weights [d] fp32 or
+    None (no norm).  Returns (q_out, k_out), contiguous unless given; q_out=q
+    works in place.
+    """
+    import torch
+    lib = load_library()
+    given = [(n, t) for n, t in (("q", q), ("k", k)) if t is not None]
+    if not given:
+        raise ValueError("one of q and k is needed")
+    for name, t in given:
+        _check(t, name, torch.bfloat16, 3, view=True)
+    T, _, d = given[0][1].shape
+    if len(given) == 2 and (k.shape[0] != T or k.shape[2] != d):
+        raise ValueError(f"k shape {tuple(k.shape)} inconsistent with q")
+    rot, max_pos = _check_rope(cos_sin, (("q_weight", q_weight), ("k_weight", k_weight)), d)
+    if positions is not None:
+        _check(positions, "positions", torch.int32, 1)
+        _shape(positions, "positions", (T,))
+    elif rot:
+        raise ValueError("positions are needed for the rotation")
+    with _on(stream, q=q, k=k, positions=positions, cos_sin=cos_sin, q_weight=q_weight,
+             k_weight=k_weight, q_out=q_out, k_out=k_out) as sp:
+        sides = []
+        for name, t, o in (("q_out", q, q_out), ("k_out", k, k_out)):
+            if t is None:
+                if o is not None:
+                    raise ValueError(f"{name} without its input")
+                sides.append((None, 0, 0, 0, None, 0, 0))
+                continue
+            if o is None:
+                o = torch.empty(t.shape, dtype=torch.bfloat16, device=t.device)
+            _check(o, name, torch.bfloat16, 3, view=True)
+            _shape(o, name, t.shape)
+            sides.append((t, t.stride(0), t.stride(1), t.shape[1], o, o.stride(0), o.stride(1)))
+        (q, qr, qh, H, q_out, qor, qoh), (k, kr, kh, Hk, k_out, kor, koh) = sides
+        st = lib.fa_qk_norm_rope(
+            _ptr(q), qr, qh, _ptr(k), kr, kh, _ptr(positions), _ptr(cos_sin), _ptr(q_weight),
+            _ptr(k_weight), T, H, Hk, d, rot, max_pos, int(bool(interleaved)), float(eps),
+            _ptr(q_out), qor, qoh, _ptr(k_out), kor, koh, sp)
+    if st != FA_OK:
+        raise FaError(st, "fa_qk_norm_rope")
+    return q_out, k_out
+
+
+def fa_paged_kv_append(k, v, cu_seqlens, seq_lens, page_table, k_cache, v_cache, k_scale,
+                       v_scale, cos_sin=None, k_weight=None, eps=1e-6, interleaved=False,
+                       stream=None):
+    """Writes new keys (normed and rotated on the way) and values into the
+    paged 8-bit cache; see fa_paged_kv_append in include/fa_gb300.h.
+
+    k, v [total, H_k, d] bf16 (strided views allowed), cu_seqlens [batch+1] and
+    seq_lens [batch] int32 (lengths with the new tokens), page_table [batch,
+    pages of a sequence] int32, caches [pages, H_k, 64, d] float8_e4m3fn and
+    scales [pages, H_k] fp32, updated in place.
+    """
+    import torch
+    lib = load_library()
+    for name, t in (("k", k), ("v", v)):
+        _check(t, name, torch.bfloat16, 3, view=True)
+    batch, pages, hk, d, width = _check_cache(k_cache, v_cache, k_scale, v_scale, cu_seqlens,
+                                              page_table)
+    _check(seq_lens, "seq_lens", torch.int32, 1)
+    _shape(seq_lens, "seq_lens", (batch,))
+    _shape(k, "k", (k.shape[0], hk, d))
+    _shape(v, "v", k.shape)
+    rot, max_pos = _check_rope(cos_sin, (("k_weight", k_weight),), d)
+    with _on(stream, k=k, v=v, cu_seqlens=cu_seqlens, seq_lens=seq_lens, page_table=page_table,
+             k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
+             cos_sin=cos_sin, k_weight=k_weight) as sp:
+        st = lib.fa_paged_kv_append(
+            _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0), v.stride(1),
+            _ptr(cu_seqlens), _ptr(seq_lens), _ptr(page_table), batch, k.shape[0], hk, d, pages,
+            width, _ptr(k_weight), float(eps), _ptr(cos_sin), rot, max_pos,
+            int(bool(interleaved)), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+            sp)
+    if st != FA_OK:
+        raise FaError(st, "fa_paged_kv_append")
+
+
+def fa_paged_attn_plan(batch, total_q, num_heads, num_heads_k, head_dim, max_seqlen_q=0):
+    """(grid, rows_per_tile, workspace_bytes) of a fa_paged_attn call of these
+    sizes on the current device; see fa_paged_attn_plan in
+    include/fa_gb300.h."""
+    lib = load_library()
+    g, r, w = ctypes.c_int(0), ctypes.c_int(0), ctypes.c_size_t(0)
+    st = lib.fa_paged_attn_plan(int(batch), int(total_q), int(num_heads), int(num_heads_k),
+                                int(head_dim), int(max_seqlen_q), ctypes.byref(g),
+                                ctypes.byref(r), ctypes.byref(w))
+    if st != FA_OK:
+        raise FaError(st, "fa_paged_attn_plan")
+    return g.value, r.value, w.value
+
+
+def fa_paged_attn(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, seq_lens, page_table,
+                  max_seqlen_q=0, max_seqlen_k=0, softmax_scale=None, causal=True,
+                  window_left=-1, out=None, lse=None, return_lse=False, workspace=None,
+                  stream=None):
+    """Attention of a few query rows per sequence over the paged 8-bit cache;
+    see fa_paged_attn in include/fa_gb300.h.
+
+    q [total_q, H, d] bf16 (strided view allowed), caches and scales as
+    fa_paged_kv_append, cu_seqlens_q [batch+1], seq_lens [batch] and
+    page_table [batch, pages of a sequence] int32.  Returns out [total_q, H, d]
+    bf16, or (out, lse [H, total_q] fp32) if an lse buffer is given or
+    return_lse is set.  workspace: a uint8 CUDA tensor of the bytes
+    fa_paged_attn_plan gives; None allocates one for the call.
+    """
+    import torch
+    lib = load_library()
+    _check(q, "q", torch.bfloat16, 3, view=True)
+    batch, pages, hk, d, width = _check_cache(k_cache, v_cache, k_scale, v_scale, cu_seqlens_q,
+                                              page_table)
+    _check(seq_lens, "seq_lens", torch.int32, 1)
+    _shape(seq_lens, "seq_lens", (batch,))
+    T, H, dq = q.shape
+    if dq != d:
+        raise ValueError(f"q has head dim {dq}, the cache {d}")
+    if softmax_scale is None:
+        softmax_scale = d ** -0.5
+    with _on(stream, q=q, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
+             cu_seqlens_q=cu_seqlens_q, seq_lens=seq_lens, page_table=page_table, out=out,
+             lse=lse, workspace=workspace) as sp:
+        if out is None:
+            out = torch.empty((T, H, d), dtype=torch.bfloat16, device=q.device)
+        else:
+            _check(out, "out", torch.bfloat16, 3)
+            _shape(out, "out", (T, H, d))
+        if lse is None and return_lse:
+            lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+        if lse is not None:
+            _check(lse, "lse", torch.float32, 2)
+            _shape(lse, "lse", (H, T))
+        if workspace is None:
+            _, _, need = fa_paged_attn_plan(batch, T, H, hk, d, max_seqlen_q)
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        else:
+            _check(workspace, "workspace", torch.uint8, 1)
+        st = lib.fa_paged_attn(
+            _ptr(q), q.stride(0), q.stride(1), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+            _ptr(v_scale), _ptr(cu_seqlens_q), _ptr(seq_lens), _ptr(page_table), batch, T, H, hk,
+            d, pages, width, int(max_seqlen_q), int(max_seqlen_k), float(softmax_scale),
+            int(bool(causal)), int(window_left), _ptr(out), _ptr(lse), _ptr(workspace),
+            0 if workspace is None else workspace.numel(), sp)
+    if st != FA_OK:
+        raise FaError(st, "fa_paged_attn")
+    return (out, lse) if lse is not None else out
+
+
+def fa_paged_kv_gather(k_cache, v_cache, k_scale, v_scale, cu_seqlens, page_table, total_k,
+                       k_out=None, v_out=None, stream=None):
+    """The first cu_seqlens[b+1] - cu_seqlens[b] cached tokens of each sequence
+    as packed bf16 k and v [total_k, H_k, d], ready for fa_varlen_fwd; see
+    fa_paged_kv_gather in include/fa_gb300.h.  total_k is cu_seqlens[-1], on
+    the host."""
+    import torch
+    lib = load_library()
+    batch, pages, hk, d, width = _check_cache(k_cache, v_cache, k_scale, v_scale, cu_seqlens,
+                                              page_table)
+    with _on(stream, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
+             cu_seqlens=cu_seqlens, page_table=page_table, k_out=k_out, v_out=v_out) as sp:
+        outs = []
+        for name, o in (("k_out", k_out), ("v_out", v_out)):
+            if o is None:
+                o = torch.empty((total_k, hk, d), dtype=torch.bfloat16, device=k_cache.device)
+            _check(o, name, torch.bfloat16, 3)
+            _shape(o, name, (total_k, hk, d))
+            outs.append(o)
+        st = lib.fa_paged_kv_gather(
+            _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(cu_seqlens),
+            _ptr(page_table), batch, int(total_k), hk, d, pages, width, _ptr(outs[0]),
+            _ptr(outs[1]), sp)
+    if st != FA_OK:
+        raise FaError(st, "fa_paged_kv_gather")
+    return outs[0], outs[1]
 
 
 def fa_set_wait_limit_ns(ns: int) -> None:

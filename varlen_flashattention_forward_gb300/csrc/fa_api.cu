@@ -23,6 +23,7 @@
 
 #include "../../include/fa_gb300.h"
 #include "decode_plan.h"
+#include "host_common.h"
 #include "merge_kernel.cuh"
 #include "sparse_decode_kernel.cuh"
 #include "varlen_fwd_kernel.cuh"
@@ -95,10 +96,7 @@ fa_status device_info(DeviceInfo** out) {
   return d.arch_ok ? FA_OK : FA_ERR_ARCH;
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+using fa::EncodeTiledFn;
 
 EncodeTiledFn encode_fn() {
   static EncodeTiledFn fn = nullptr;
@@ -221,25 +219,27 @@ fa::VarlenLaunch launch_shape(int sm_count, int batch, int total_q, int total_k,
   return L;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+bool aligned(const void* p, uintptr_t a) { return fa::is_aligned(p, a); }
 
 int tail_width(int d) { return ((d + 15) / 16 * 16) % 64; }
 
 }  // namespace
 
-namespace {
+namespace fa {
 
-// A strided [tokens, heads, dim] view: innermost dimension contiguous, head
-// and token strides multiples of 16 bytes, no element reachable two ways.
-bool valid_view(long long row_stride, long long head_stride, int heads, int dim) {
-  if (row_stride <= 0 || head_stride <= 0) return false;
-  if (row_stride % 8 != 0 || head_stride % 8 != 0) return false;
-  if (head_stride < dim) return false;
-  if (row_stride < (long long)(heads - 1) * head_stride + dim) return false;
-  return row_stride < (1ll << 37) && head_stride < (1ll << 37);  // TMA stride range
+fa_status device_facts(DeviceFacts* out) {
+  DeviceInfo* dev = nullptr;
+  const fa_status st = device_info(&dev);
+  if (st != FA_OK) return st;
+  out->sm_count = dev->sm_count;
+  out->status = dev->status;
+  out->wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  return FA_OK;
 }
 
-}  // namespace
+EncodeTiledFn tensor_map_encoder() { return encode_fn(); }
+
+}  // namespace fa
 
 extern "C" fa_status fa_varlen_fwd(const void* q, const void* k, const void* v,
                                    const int* cu_seqlens_q, const int* cu_seqlens_k, int batch,
@@ -284,9 +284,9 @@ extern "C" fa_status fa_varlen_fwd_strided(
   else if (d_qk == 128 && d_v == 128) launch = fa::launch_varlen_128_128;
   else if (d_qk == 192 && d_v == 128) launch = fa::launch_varlen_192_128;
   if (!launch) return FA_ERR_UNSUPPORTED;
-  if (!valid_view(q_row_stride, q_head_stride, num_heads, d_qk) ||
-      (total_k > 0 && (!valid_view(k_row_stride, k_head_stride, num_heads_k, d_qk) ||
-                       !valid_view(v_row_stride, v_head_stride, num_heads_k, d_v))))
+  if (!fa::is_valid_view(q_row_stride, q_head_stride, num_heads, d_qk) ||
+      (total_k > 0 && (!fa::is_valid_view(k_row_stride, k_head_stride, num_heads_k, d_qk) ||
+                       !fa::is_valid_view(v_row_stride, v_head_stride, num_heads_k, d_v))))
     return FA_ERR_INVALID_ARG;
   // Token indices are 32-bit in the kernel.
   if ((int64_t)total_q * num_heads > INT32_MAX || (int64_t)total_k * num_heads_k > INT32_MAX)

@@ -1,0 +1,283 @@
+// fa_paged.cu -- host side of the serving entry points around the attention
+// forward: q/k norm with rotation, and the paged 8-bit cache (append, gather,
+// attention).  Argument checks, launch shapes, launches; nothing here copies
+// data, synchronises or allocates.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "host_common.h"
+#include "paged_attn_kernel.cuh"
+#include "paged_kv_kernels.cuh"
+#include "qk_norm_rope_kernel.cuh"
+
+using fa::is_aligned;
+using fa::is_valid_view;
+
+namespace {
+
+bool cache_dim(int d) { return d == 64 || d == 80 || d == 96 || d == 128; }
+
+fa_status launched() { return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH; }
+
+// Checks that the rotation arguments share.
+bool valid_rope(const float* cos_sin, int rot_dim, int max_pos, int head_dim) {
+  if (rot_dim < 0 || rot_dim % 16 != 0 || rot_dim > head_dim || max_pos < 0) return false;
+  return rot_dim == 0 || (cos_sin != nullptr && is_aligned(cos_sin, 16) && max_pos > 0);
+}
+
+// Sizes of the cache and the arrays that come with it.
+fa_status check_cache(const void* k_cache, const void* v_cache, const float* k_scale,
+                      const float* v_scale, const int* cu, const int* page_table, int batch,
+                      int total, int heads_k, int head_dim, int num_pages, int max_pages) {
+  if (!k_cache || !v_cache || !k_scale || !v_scale || !cu || !page_table) return FA_ERR_INVALID_ARG;
+  if (batch < 1 || total < 0 || heads_k < 1 || num_pages < 1 || max_pages < 1)
+    return FA_ERR_INVALID_ARG;
+  if (!is_aligned(k_cache, 16) || !is_aligned(v_cache, 16) || !is_aligned(k_scale, 4) ||
+      !is_aligned(v_scale, 4) || !is_aligned(cu, 4) || !is_aligned(page_table, 4))
+    return FA_ERR_INVALID_ARG;
+  if (!cache_dim(head_dim)) return FA_ERR_UNSUPPORTED;
+  // Positions of a sequence, (page, head) cells and packed rows are 32-bit.
+  if ((int64_t)max_pages * fa::kPageTokens > INT32_MAX || (int64_t)num_pages * heads_k > INT32_MAX ||
+      (int64_t)total * heads_k > INT32_MAX || heads_k > 32767)
+    return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+}  // namespace
+
+extern "C" fa_status fa_qk_norm_rope(const void* q, long long q_row_stride,
+                                     long long q_head_stride, const void* k,
+                                     long long k_row_stride, long long k_head_stride,
+                                     const int* positions, const float* cos_sin,
+                                     const float* q_weight, const float* k_weight, int num_tokens,
+                                     int num_heads, int num_heads_k, int head_dim, int rot_dim,
+                                     int max_pos, int interleaved, float eps, void* q_out,
+                                     long long q_out_row_stride, long long q_out_head_stride,
+                                     void* k_out, long long k_out_row_stride,
+                                     long long k_out_head_stride, fa_stream_t stream) {
+  if (num_tokens < 0 || num_heads < 0 || num_heads_k < 0 || num_heads + num_heads_k < 1)
+    return FA_ERR_INVALID_ARG;
+  if (num_tokens > 0 && ((num_heads > 0 && (!q || !q_out)) || (num_heads_k > 0 && (!k || !k_out))))
+    return FA_ERR_INVALID_ARG;
+  if (head_dim < 8 || !valid_rope(cos_sin, rot_dim, max_pos, head_dim)) return FA_ERR_INVALID_ARG;
+  if (rot_dim > 0 && num_tokens > 0 && !positions) return FA_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return FA_ERR_INVALID_ARG;
+  if (!is_aligned(q, 16) || !is_aligned(k, 16) || !is_aligned(q_out, 16) ||
+      !is_aligned(k_out, 16) || !is_aligned(positions, 4) || !is_aligned(q_weight, 16) ||
+      !is_aligned(k_weight, 16))
+    return FA_ERR_INVALID_ARG;
+  if (head_dim % 8 != 0 || head_dim > 256) return FA_ERR_UNSUPPORTED;
+  if ((num_heads > 0 && (!is_valid_view(q_row_stride, q_head_stride, num_heads, head_dim) ||
+                         !is_valid_view(q_out_row_stride, q_out_head_stride, num_heads, head_dim))) ||
+      (num_heads_k > 0 &&
+       (!is_valid_view(k_row_stride, k_head_stride, num_heads_k, head_dim) ||
+        !is_valid_view(k_out_row_stride, k_out_head_stride, num_heads_k, head_dim))))
+    return FA_ERR_INVALID_ARG;
+  if ((int64_t)num_tokens * ((int64_t)num_heads + num_heads_k) > INT32_MAX)
+    return FA_ERR_UNSUPPORTED;
+  fa::DeviceFacts dev;
+  const fa_status st = fa::device_facts(&dev);
+  if (st != FA_OK) return st;
+  if (num_tokens == 0) return FA_OK;
+
+  fa::QkNormRopeArgs a;
+  a.q = {static_cast<const uint16_t*>(q), static_cast<uint16_t*>(q_out), q_row_stride,
+         q_head_stride, q_out_row_stride, q_out_head_stride, q_weight};
+  a.k = {static_cast<const uint16_t*>(k), static_cast<uint16_t*>(k_out), k_row_stride,
+         k_head_stride, k_out_row_stride, k_out_head_stride, k_weight};
+  a.heads = num_heads;
+  a.heads_k = num_heads_k;
+  a.dim = head_dim;
+  a.inv_dim = 1.f / (float)head_dim;
+  a.eps = eps;
+  a.rope = {cos_sin, rot_dim, interleaved != 0};
+  a.positions = rot_dim > 0 ? positions : nullptr;
+  a.max_pos = max_pos;
+  const int lanes = head_dim <= 64 ? 8 : head_dim <= 128 ? 16 : 32;
+  a.groups = num_heads + num_heads_k;
+  a.units = (long long)num_tokens * a.groups;
+  const unsigned grid = (unsigned)((a.units * lanes + 255) / 256);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (lanes == 8) fa::qk_norm_rope_kernel<8, 1><<<grid, 256, 0, s>>>(a);
+  else if (lanes == 16) fa::qk_norm_rope_kernel<16, 1><<<grid, 256, 0, s>>>(a);
+  else fa::qk_norm_rope_kernel<32, 1><<<grid, 256, 0, s>>>(a);
+  return launched();
+}
+
+extern "C" fa_status fa_paged_kv_append(
+    const void* k, long long k_row_stride, long long k_head_stride, const void* v,
+    long long v_row_stride, long long v_head_stride, const int* cu_seqlens, const int* seq_lens,
+    const int* page_table, int batch, int total_new, int num_heads_k, int head_dim, int num_pages,
+    int max_pages_per_seq, const float* k_weight, float eps, const float* cos_sin, int rot_dim,
+    int max_pos, int interleaved, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+    fa_stream_t stream) {
+  if (!seq_lens || !is_aligned(seq_lens, 4)) return FA_ERR_INVALID_ARG;
+  if (total_new > 0 && (!k || !v)) return FA_ERR_INVALID_ARG;
+  fa_status st = check_cache(k_cache, v_cache, k_scale, v_scale, cu_seqlens, page_table, batch,
+                             total_new, num_heads_k, head_dim, num_pages, max_pages_per_seq);
+  if (st != FA_OK) return st;
+  if (!valid_rope(cos_sin, rot_dim, max_pos, head_dim) || !(eps >= 0.f) || !std::isfinite(eps))
+    return FA_ERR_INVALID_ARG;
+  if (!is_aligned(k, 16) || !is_aligned(v, 16) || !is_aligned(k_weight, 4))
+    return FA_ERR_INVALID_ARG;
+  if (total_new > 0 && (!is_valid_view(k_row_stride, k_head_stride, num_heads_k, head_dim) ||
+                        !is_valid_view(v_row_stride, v_head_stride, num_heads_k, head_dim)))
+    return FA_ERR_INVALID_ARG;
+  fa::DeviceFacts dev;
+  st = fa::device_facts(&dev);
+  if (st != FA_OK) return st;
+  if (total_new == 0) return FA_OK;
+
+  fa::KvAppendArgs a;
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.k_row = k_row_stride;
+  a.k_head = k_head_stride;
+  a.v_row = v_row_stride;
+  a.v_head = v_head_stride;
+  a.cu = cu_seqlens;
+  a.seq_lens = seq_lens;
+  a.page_table = page_table;
+  a.batch = batch;
+  a.total = total_new;
+  a.heads = num_heads_k;
+  a.dim = head_dim;
+  a.max_pages = max_pages_per_seq;
+  a.num_pages = num_pages;
+  a.limit = max_pages_per_seq * fa::kPageTokens;
+  if (rot_dim > 0) a.limit = std::min(a.limit, max_pos);
+  a.k_cache = static_cast<uint8_t*>(k_cache);
+  a.v_cache = static_cast<uint8_t*>(v_cache);
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.k_weight = k_weight;
+  a.inv_dim = 1.f / (float)head_dim;
+  a.eps = eps;
+  a.rope = {cos_sin, rot_dim, interleaved != 0};
+  // n new tokens of a sequence touch at most (n + 62) / 64 + 1 pages, and n.
+  const long long chunks =
+      std::min<long long>(total_new, total_new / fa::kPageTokens + 2ll * batch);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool step = (long long)total_new < 16ll * batch;
+  if (step) {
+    if (head_dim <= 64) fa::kv_append_step_kernel<8><<<(unsigned)chunks, 256, 0, s>>>(a);
+    else fa::kv_append_step_kernel<16><<<(unsigned)chunks, 256, 0, s>>>(a);
+  } else {
+    const dim3 grid((unsigned)chunks, 2 * num_heads_k);
+    if (head_dim <= 64) fa::kv_append_prompt_kernel<8><<<grid, 128, 0, s>>>(a);
+    else fa::kv_append_prompt_kernel<16><<<grid, 128, 0, s>>>(a);
+  }
+  return launched();
+}
+
+extern "C" fa_status fa_paged_kv_gather(const void* k_cache, const void* v_cache,
+                                        const float* k_scale, const float* v_scale,
+                                        const int* cu_seqlens, const int* page_table, int batch,
+                                        int total_k, int num_heads_k, int head_dim, int num_pages,
+                                        int max_pages_per_seq, void* k_out, void* v_out,
+                                        fa_stream_t stream) {
+  if (total_k > 0 && (!k_out || !v_out)) return FA_ERR_INVALID_ARG;
+  if (!is_aligned(k_out, 16) || !is_aligned(v_out, 16)) return FA_ERR_INVALID_ARG;
+  fa_status st = check_cache(k_cache, v_cache, k_scale, v_scale, cu_seqlens, page_table, batch,
+                             total_k, num_heads_k, head_dim, num_pages, max_pages_per_seq);
+  if (st != FA_OK) return st;
+  fa::DeviceFacts dev;
+  st = fa::device_facts(&dev);
+  if (st != FA_OK) return st;
+  if (total_k == 0) return FA_OK;
+  fa::KvGatherArgs a;
+  a.k_cache = static_cast<const uint8_t*>(k_cache);
+  a.v_cache = static_cast<const uint8_t*>(v_cache);
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.cu = cu_seqlens;
+  a.page_table = page_table;
+  a.batch = batch;
+  a.total = total_k;
+  a.heads = num_heads_k;
+  a.dim = head_dim;
+  a.max_pages = max_pages_per_seq;
+  a.num_pages = num_pages;
+  a.k = static_cast<uint16_t*>(k_out);
+  a.v = static_cast<uint16_t*>(v_out);
+  const long long pages =
+      std::min<long long>(total_k, total_k / fa::kPageTokens + (long long)batch);
+  fa::kv_gather_kernel<<<dim3((unsigned)pages, 2), 256, 0,
+                         reinterpret_cast<cudaStream_t>(stream)>>>(a);
+  return launched();
+}
+
+extern "C" fa_status fa_paged_attn_plan(int batch, int total_q, int num_heads, int num_heads_k,
+                                        int head_dim, int max_seqlen_q, int* grid,
+                                        int* rows_per_tile, size_t* workspace_bytes) {
+  if (!grid || !rows_per_tile || !workspace_bytes) return FA_ERR_INVALID_ARG;
+  if (batch < 1 || total_q < 0 || num_heads < 1 || num_heads_k < 1 ||
+      num_heads % num_heads_k != 0 || max_seqlen_q < 0)
+    return FA_ERR_INVALID_ARG;
+  if (!cache_dim(head_dim)) return FA_ERR_UNSUPPORTED;
+  fa::DeviceFacts dev;
+  const fa_status st = fa::device_facts(&dev);
+  if (st != FA_OK) return st;
+  *grid = total_q;
+  *rows_per_tile = 1;
+  *workspace_bytes = 0;
+  return FA_OK;
+}
+
+extern "C" fa_status fa_paged_attn(const void* q, long long q_row_stride, long long q_head_stride,
+                                   const void* k_cache, const void* v_cache, const float* k_scale,
+                                   const float* v_scale, const int* cu_seqlens_q,
+                                   const int* seq_lens, const int* page_table, int batch,
+                                   int total_q, int num_heads, int num_heads_k, int head_dim,
+                                   int num_pages, int max_pages_per_seq, int max_seqlen_q,
+                                   int max_seqlen_k, float softmax_scale, int causal,
+                                   int window_left, void* out, float* lse, void* workspace,
+                                   size_t workspace_bytes, fa_stream_t stream) {
+  if ((total_q > 0 && (!q || !out)) || !seq_lens) return FA_ERR_INVALID_ARG;
+  fa_status st = check_cache(k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, page_table, batch,
+                             total_q, num_heads_k, head_dim, num_pages, max_pages_per_seq);
+  if (st != FA_OK) return st;
+  if (num_heads < 1 || num_heads % num_heads_k != 0 || max_seqlen_q < 0 || max_seqlen_k < 0 ||
+      window_left < -1 || !(softmax_scale > 0.f) || !std::isfinite(softmax_scale))
+    return FA_ERR_INVALID_ARG;
+  if (!is_aligned(q, 16) || !is_aligned(out, 16) || !is_aligned(lse, 4) ||
+      !is_aligned(seq_lens, 4) || !is_aligned(workspace, 16))
+    return FA_ERR_INVALID_ARG;
+  if (total_q > 0 && !is_valid_view(q_row_stride, q_head_stride, num_heads, head_dim))
+    return FA_ERR_INVALID_ARG;
+  if ((int64_t)total_q * num_heads > INT32_MAX || num_heads > 65535) return FA_ERR_UNSUPPORTED;
+  fa::DeviceFacts dev;
+  st = fa::device_facts(&dev);
+  if (st != FA_OK) return st;
+  if (total_q == 0) return FA_OK;
+  (void)workspace_bytes;
+  fa::PagedAttnArgs a;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_row = q_row_stride;
+  a.q_head = q_head_stride;
+  a.k_cache = static_cast<const uint8_t*>(k_cache);
+  a.v_cache = static_cast<const uint8_t*>(v_cache);
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.cu = cu_seqlens_q;
+  a.seq_lens = seq_lens;
+  a.page_table = page_table;
+  a.batch = batch;
+  a.total_q = total_q;
+  a.heads = num_heads;
+  a.heads_k = num_heads_k;
+  a.dim = head_dim;
+  a.max_pages = max_pages_per_seq;
+  a.num_pages = num_pages;
+  a.scale = softmax_scale;
+  a.causal = causal;
+  a.window = window_left;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  fa::paged_attn_rows_kernel<<<dim3(total_q, num_heads), 128, 0,
+                               reinterpret_cast<cudaStream_t>(stream)>>>(a);
+  return launched();
+}

@@ -1,0 +1,330 @@
+// paged_kv_kernels.cuh -- writing the paged 8-bit key/value cache, and reading
+// it back as packed bf16.
+//
+// Cache: e4m3 [pages, kv heads, 64 tokens, dim] with one fp32 scale for each
+// (page, kv head); a value is code * scale.  The scale is the smallest power
+// of two that keeps the largest value of the page within 448, the largest
+// e4m3 number, so that moving codes to a larger scale only drops bits at the
+// subnormal end.  A page that is filled over several calls only ever raises
+// its scale, and ends with the one that writing it at once would have given.
+#pragma once
+
+#include <cstdint>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "paged_index.h"
+#include "rope_row.cuh"
+#include "sm103_ptx.cuh"
+
+namespace fa {
+
+constexpr float kE4m3Max = 448.f;
+// Scales stay within 2^-64 .. 2^64: their products with scores and sums of
+// the attention stay far inside fp32.
+constexpr int kScaleExpMax = 64;
+
+// Smallest power of two s with amax <= 448 s, clamped (amax finite, >= 0).
+__device__ __forceinline__ float scale_for(float amax) {
+  // amax / 512 = m 2^e with m in [0.5, 1), and 448 = 512 * 0.875.
+  int e;
+  const float m = frexpf(amax * (1.f / 512.f), &e);
+  if (m > 0.875f) ++e;
+  if (!(amax > 0.f)) e = -kScaleExpMax;
+  e = imin(imax(e, -kScaleExpMax), kScaleExpMax);
+  return ldexpf(1.f, e);
+}
+
+// Two fp32 values as e4m3 codes (round to nearest even, saturating at 448,
+// NaN kept): lo in bits 0..7.
+__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// Two e4m3 codes as f16x2 (exact).
+__device__ __forceinline__ uint32_t unpack_e4m3x2(uint32_t codes) {
+  uint32_t d;
+  const uint16_t c = (uint16_t)codes;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(c));
+  return d;
+}
+__device__ __forceinline__ float2 f16x2_floats(uint32_t h) {
+  float2 f;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\t"
+      "cvt.f32.f16 %1, h;\n\t}"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(h));
+  return f;
+}
+
+// The sequence and the place within it of work unit x, where sequence b has
+// count(b) units, in order.  Called by the whole block (at most 1024 threads,
+// whole warps); found.seq is -1 if there is no such unit.
+struct FoundUnit {
+  int seq, at;
+};
+template <typename Count>
+__device__ __forceinline__ FoundUnit find_unit(int x, int batch, Count count) {
+  __shared__ int s_warp[32];
+  __shared__ FoundUnit s_found;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  if (tid == 0) s_found.seq = -1;
+  long long before = 0;  // units of the sequences of earlier turns
+  for (int b0 = 0; b0 < batch; b0 += blockDim.x) {
+    const int b = b0 + tid;
+    const int c = b < batch ? count(b) : 0;
+    int sum = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (lane == 31) s_warp[warp] = sum;
+    __syncthreads();
+    long long lo = before;
+    int all = 0;
+    for (int w = 0; w < warps; ++w) {
+      if (w < warp) lo += s_warp[w];
+      all += s_warp[w];
+    }
+    lo += sum - c;
+    if (x >= lo && x < lo + c) {
+      s_found.seq = b;
+      s_found.at = (int)(x - lo);
+    }
+    before += all;
+    __syncthreads();
+    if (before > x) break;
+  }
+  __syncthreads();
+  return s_found;
+}
+
+// ------------------------------------------------------------------ append
+struct KvAppendArgs {
+  const uint16_t *k, *v;
+  long long k_row, k_head, v_row, v_head;
+  const int *cu, *seq_lens, *page_table;
+  int batch, total, heads, dim, max_pages, num_pages;
+  int limit;  // positions that exist
+  uint8_t *k_cache, *v_cache;
+  float *k_scale, *v_scale;
+  const float* k_weight;  // or null
+  float inv_dim, eps;
+  RopeParams rope;
+};
+
+// One item: the new tokens of one page and head, keys or values, taken by a
+// team of TEAM warps (TEAM = 1 or the block).  Rows go ROWS at a time to each
+// LANES-lane group; an item of at most TEAM * ROWS * (32 / LANES) rows is held
+// in registers between the maximum and the rounding, a longer one is loaded
+// again for the second pass.
+template <int LANES, int ROWS, int TEAM>
+__device__ __forceinline__ void append_item(const KvAppendArgs& a, int page, int head, bool is_k,
+                                            int slot, int count, int row0, int pos0, int team_warp,
+                                            float* s_amax) {
+  constexpr int kGroups = 32 / LANES;            // rows of a warp at once
+  constexpr int kPass = TEAM * ROWS * kGroups;   // rows of the team's pass
+  const int lane = threadIdx.x & 31;
+  const int sub = lane % LANES, dim0 = sub * 8;
+  const bool in_dim = dim0 < a.dim;
+  const uint16_t* src = is_k ? a.k + head * a.k_head : a.v + head * a.v_head;
+  const long long stride = is_k ? a.k_row : a.v_row;
+  const size_t cell = (size_t)page * a.heads + head;
+  uint8_t* codes = (is_k ? a.k_cache : a.v_cache) + cell * kPageTokens * a.dim;
+  float* scale = (is_k ? a.k_scale : a.v_scale) + cell;
+  const bool norm = is_k && a.k_weight != nullptr;
+  const bool turn = is_k && a.rope.rot_dim > 0;
+  const float old = slot > 0 ? *scale : 0.f;
+  float w[8];
+  if (norm && in_dim) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = __ldg(a.k_weight + dim0 + j);
+  }
+  float x[ROWS][8];
+  float amax = 0.f;
+  auto row_of = [&](int pass, int i) {
+    return pass * kPass + (i * TEAM + team_warp) * kGroups + lane / LANES;
+  };
+  auto load = [&](int pass) {
+    uint4 raw[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      const int r = row_of(pass, i);
+      raw[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < count && in_dim)
+        raw[i] = __ldg(reinterpret_cast<const uint4*>(src + (long long)(row0 + r) * stride + dim0));
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      unpack_bf16x8(raw[i], x[i]);
+      if (norm) norm_row<LANES>(x[i], w, a.inv_dim, a.eps);
+      if (turn) {
+        const int r = row_of(pass, i);
+        RopeRow t;
+        if (r < count) load_rope(a.rope, pos0 + r, dim0, &t);
+        rotate_row<LANES>(x[i], a.rope, t, dim0);
+      }
+    }
+  };
+  const int passes = (count + kPass - 1) / kPass;
+  for (int p = 0; p < passes; ++p) {
+    load(p);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      if (row_of(p, i) < count && in_dim) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          // Infinite and NaN values take no part in the scale: an infinity
+          // saturates and a NaN stays one, and the rest of the page keeps
+          // its precision.
+          const float v = fabsf(x[i][j]);
+          if (v <= 3.402823466e38f) amax = fmaxf(amax, v);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  if constexpr (TEAM > 1) {
+    if (lane == 0) s_amax[team_warp] = amax;
+    __syncthreads();  // (also: every warp has read the old scale)
+#pragma unroll
+    for (int i = 0; i < TEAM; ++i) amax = fmaxf(amax, s_amax[i]);
+  }
+  const float s = fmaxf(scale_for(amax), old);
+  const float inv = 1.f / s;
+  __syncwarp();
+  if (lane == 0 && team_warp == 0) *scale = s;
+  for (int p = 0; p < passes; ++p) {
+    if (passes > 1) load(p);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      const int r = row_of(p, i);
+      if (r < count && in_dim) {
+        uint2 c;
+        c.x = pack_e4m3x2(x[i][0] * inv, x[i][1] * inv) |
+              pack_e4m3x2(x[i][2] * inv, x[i][3] * inv) << 16;
+        c.y = pack_e4m3x2(x[i][4] * inv, x[i][5] * inv) |
+              pack_e4m3x2(x[i][6] * inv, x[i][7] * inv) << 16;
+        *reinterpret_cast<uint2*>(codes + (size_t)(slot + r) * a.dim + dim0) = c;
+      }
+    }
+  }
+  // Earlier tokens of the page follow a scale that has grown.
+  if (slot > 0 && s > old) {
+    const float f = old * inv;
+    const int words = slot * a.dim / 4;
+    uint32_t* c = reinterpret_cast<uint32_t*>(codes);
+    for (int i = team_warp * 32 + lane; i < words; i += TEAM * 32) {
+      const uint32_t u = c[i];
+      const float2 lo = f16x2_floats(unpack_e4m3x2(u)), hi = f16x2_floats(unpack_e4m3x2(u >> 16));
+      c[i] = pack_e4m3x2(lo.x * f, lo.y * f) | pack_e4m3x2(hi.x * f, hi.y * f) << 16;
+    }
+  }
+}
+
+// The page of the cache and the rows that chunk x (page by page of each
+// sequence's new tokens) fills; false if there is nothing to write.
+__device__ __forceinline__ bool append_chunk(const KvAppendArgs& a, int x, int* page, PageSpan* sp,
+                                             int* row0, int* pos0) {
+  auto span = [&](int b, int* lo) {
+    const RowRange r = row_range(__ldg(a.cu + b), __ldg(a.cu + b + 1), a.total);
+    *lo = r.lo;
+    return append_span(r.n, __ldg(a.seq_lens + b), a.limit);
+  };
+  const FoundUnit u = find_unit(x, a.batch, [&](int b) {
+    int lo;
+    const AppendSpan s = span(b, &lo);
+    return pages_touched(s.first, s.n);
+  });
+  if (u.seq < 0) return false;
+  int lo;
+  const AppendSpan s = span(u.seq, &lo);
+  const int p = s.first / kPageTokens + u.at;
+  *sp = page_span(s.first, s.n, p);
+  *row0 = lo + sp->row;
+  *pos0 = s.first + sp->row;
+  *page = checked_page(__ldg(a.page_table + (size_t)u.seq * a.max_pages + p), a.num_pages);
+  return *page >= 0;
+}
+
+// Few tokens of each sequence: a block takes a chunk, its warps the 2 * heads
+// items of it, one warp an item.
+template <int LANES>
+__global__ void __launch_bounds__(256) kv_append_step_kernel(const KvAppendArgs a) {
+  int page, row0, pos0;
+  PageSpan sp;
+  if (!append_chunk(a, blockIdx.x, &page, &sp, &row0, &pos0)) return;
+  for (int i = threadIdx.x >> 5; i < 2 * a.heads; i += blockDim.x >> 5)
+    append_item<LANES, 1, 1>(a, page, i >> 1, (i & 1) == 0, sp.slot, sp.count, row0, pos0, 0,
+                             nullptr);
+}
+
+// Many tokens: a block of 4 warps takes one item, whose up to 64 rows it
+// holds in registers.
+template <int LANES>
+__global__ void __launch_bounds__(128) kv_append_prompt_kernel(const KvAppendArgs a) {
+  __shared__ float s_amax[4];
+  int page, row0, pos0;
+  PageSpan sp;
+  if (!append_chunk(a, blockIdx.x, &page, &sp, &row0, &pos0)) return;
+  append_item<LANES, 16 * LANES / 32, 4>(a, page, blockIdx.y >> 1, (blockIdx.y & 1) == 0, sp.slot,
+                                         sp.count, row0, pos0, threadIdx.x >> 5, s_amax);
+}
+
+// ------------------------------------------------------------------ gather
+struct KvGatherArgs {
+  const uint8_t *k_cache, *v_cache;
+  const float *k_scale, *v_scale;
+  const int *cu, *page_table;
+  int batch, total, heads, dim, max_pages, num_pages;
+  uint16_t *k, *v;
+};
+
+// A block takes one page of one sequence; each thread 16 codes at a time.
+// Positions whose page is not in the cache (or not in the table) read as zero.
+__global__ void __launch_bounds__(256) kv_gather_kernel(const KvGatherArgs a) {
+  const FoundUnit u = find_unit(blockIdx.x, a.batch, [&](int b) {
+    const RowRange r = row_range(__ldg(a.cu + b), __ldg(a.cu + b + 1), a.total);
+    return pages_touched(0, r.n);
+  });
+  if (u.seq < 0) return;
+  const RowRange r = row_range(__ldg(a.cu + u.seq), __ldg(a.cu + u.seq + 1), a.total);
+  const PageSpan sp = page_span(0, r.n, u.at);
+  const int page =
+      u.at < a.max_pages
+          ? checked_page(__ldg(a.page_table + (size_t)u.seq * a.max_pages + u.at), a.num_pages)
+          : -1;
+  const int per_row = a.dim / 16;
+  const int per_token = a.heads * per_row;
+  const uint8_t* cache = blockIdx.y ? a.v_cache : a.k_cache;
+  const float* scales = blockIdx.y ? a.v_scale : a.k_scale;
+  uint16_t* out = blockIdx.y ? a.v : a.k;
+  for (int i = threadIdx.x; i < sp.count * per_token; i += blockDim.x) {
+    const int t = i / per_token, j = i - t * per_token;
+    const int h = j / per_row, c = j - h * per_row;
+    uint32_t w[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+    if (page >= 0) {
+      const size_t cell = (size_t)page * a.heads + h;
+      const uint4 code = __ldg(reinterpret_cast<const uint4*>(
+          cache + (cell * kPageTokens + sp.slot + t) * a.dim + c * 16));
+      const float s = __ldg(scales + cell);
+      const uint32_t cw[4] = {code.x, code.y, code.z, code.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 lo = f16x2_floats(unpack_e4m3x2(cw[k]));
+        const float2 hi = f16x2_floats(unpack_e4m3x2(cw[k] >> 16));
+        w[2 * k] = ptx::pack_bf16x2(lo.x * s, lo.y * s);
+        w[2 * k + 1] = ptx::pack_bf16x2(hi.x * s, hi.y * s);
+      }
+    }
+    uint4* dst = reinterpret_cast<uint4*>(out + ((size_t)(r.lo + sp.row + t) * a.heads + h) * a.dim +
+                                          c * 16);
+    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+}  // namespace fa
