@@ -26,3 +26,39 @@ void probe_key_range(int i0, int i1, int n, int len, int held, int causal, int w
   out[1] = r.hi;
 }
 }
+
+// Walks every CTA's range; writes (cta, seq, head, row_tile, tile0, count,
+// part_lo, unit_count) of each segment and returns how many there are (at
+// most `most`), -1 past that.
+extern "C" int probe_walk(const int* cu, const int* lens, int batch, int total_q, int heads_k,
+                          int group, int rows, int causal, int window, int held, int ctas, int most,
+                          int* out) {
+  fa::AttnShape s = {heads_k, group, rows, causal, window, held};
+  auto seq_of = [&](int b, fa::RowRange* q, int* len) {
+    *q = fa::row_range(cu[b], cu[b + 1], total_q);
+    *len = lens[b];
+  };
+  long long pre[4097];
+  pre[0] = 0;
+  for (int b = 0; b < batch; ++b) {
+    fa::RowRange q;
+    int len;
+    seq_of(b, &q, &len);
+    pre[b + 1] = pre[b] + heads_k * fa::head_tiles(s, q.n, len);
+  }
+  auto before = [&](int b) { return pre[b]; };
+  int found = 0;
+  for (int c = 0; c < ctas; ++c) {
+    fa::SegmentWalk w;
+    fa::Segment g;
+    fa::walk_begin(&w, fa::range_start(pre[batch], ctas, c), fa::range_start(pre[batch], ctas, c + 1),
+                   batch, before);
+    while (fa::walk_next(&w, s, before, seq_of, &g)) {
+      if (found == most) return -1;
+      const int v[8] = {c, g.seq, g.head, g.row_tile, g.tile0, g.count, g.part_lo, g.unit_count};
+      for (int k = 0; k < 8; ++k) out[8 * found + k] = v[k];
+      ++found;
+    }
+  }
+  return found;
+}

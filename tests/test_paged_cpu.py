@@ -278,3 +278,63 @@ def test_python_refuses_inconsistent_norm_rope_calls(lib):
                lambda: fa.fa_qk_norm_rope(q, k, pos, tab, q_weight=torch.zeros(32))):
         with pytest.raises(ValueError):
             fn()
+
+
+# ------------------------------------------------------------ work split
+def walk(probe, q_lens, lens, hk, group, rows, causal, window, held, ctas):
+    cu = [0]
+    for n in q_lens:
+        cu.append(cu[-1] + n)
+    arr = lambda x: (ctypes.c_int * len(x))(*x)  # noqa: E731
+    most = 200000
+    out = (ctypes.c_int * (8 * most))()
+    n = probe.probe_walk(arr(cu), arr(lens), len(lens), cu[-1], hk, group, rows, causal, window,
+                         held, ctas, most, out)
+    assert n >= 0
+    return [tuple(out[8 * i:8 * i + 8]) for i in range(n)]
+
+
+def test_segments_cover_every_tile_once(probe):
+    rng = random.Random(2)
+    for trial in range(400):
+        batch = rng.choice([1, 2, 5, 30])
+        q_lens = [rng.choice([0, 1, 1, 2, 7, 40]) for _ in range(batch)]
+        held = 64 * rng.randrange(1, 60)
+        lens = [rng.choice([0, 1, 64, 127, 128, 129, rng.randrange(0, 4000), -3])
+                for _ in range(batch)]
+        hk, group, rows = rng.choice([1, 2, 8]), rng.choice([1, 3, 4, 16, 40]), rng.choice([16, 64])
+        causal, window = rng.randrange(2), rng.choice([-1, 0, 100, 1000])
+        ctas = rng.choice([1, 2, 7, 152])
+        segs = walk(probe, q_lens, lens, hk, group, rows, causal, window, held, ctas)
+        want = {}
+        for b, (n, ln) in enumerate(zip(q_lens, lens)):
+            for h in range(hk):
+                for t in range(-(-n * group // rows)):
+                    i0, i1 = t * rows // group, (min((t + 1) * rows, n * group) - 1) // group
+                    keys = min(max(ln, 0), held)
+                    hi = min(keys, ln - n + i1 + 1) if causal else keys
+                    lo = max(0, ln - n + i0 - window) if window >= 0 else 0
+                    want[b, h, t] = (lo // 128, -(-hi // 128)) if hi > lo else None
+        got = {}
+        per_cta = [0] * ctas
+        for c, b, h, t, tile0, count, part_lo, unit_count in segs:
+            assert count > 0 and 0 <= part_lo and part_lo + count <= unit_count
+            per_cta[c] += count
+            got.setdefault((b, h, t), []).append((tile0, count, part_lo, unit_count))
+        assert set(got) == set(want)
+        assert max(per_cta) - min(per_cta) <= 1
+        for key, parts in got.items():
+            at = parts[0][0]
+            assert parts[0][2] == 0
+            for tile0, count, part_lo, unit_count in parts:
+                assert tile0 == at and tile0 - parts[0][0] == part_lo
+                at += count
+            assert at - parts[0][0] == parts[0][3]
+            if want[key] is None:
+                assert parts[0][3] == 1
+            else:
+                assert (parts[0][0], at) == want[key]
+        # At most a CTA's first and last segment hold part of a unit.
+        for c in range(ctas):
+            mine = [s for s in segs if s[0] == c]
+            assert all(s[5] == s[7] for s in mine[1:-1])

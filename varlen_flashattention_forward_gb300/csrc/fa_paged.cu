@@ -3,9 +3,12 @@
 // attention).  Argument checks, launch shapes, launches; nothing here copies
 // data, synchronises or allocates.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "host_common.h"
@@ -17,6 +20,77 @@ using fa::is_aligned;
 using fa::is_valid_view;
 
 namespace {
+
+// Launch shape of fa_paged_attn.  Rows of a tile: the smallest of 16, 32 and
+// 64 that holds a sequence's rows (the max_seqlen_q hint, else the mean, times
+// the heads of a group), so that its keys are read once.
+struct AttnLaunch {
+  int grid, rows, dim;  // CTAs, rows of a tile, padded head dim
+  size_t o_bytes, lse_bytes, meta_bytes;
+  size_t bytes() const { return o_bytes + lse_bytes + meta_bytes; }
+};
+AttnLaunch attn_launch(int sm_count, int batch, int total_q, int group, int head_dim,
+                       int max_seqlen_q) {
+  AttnLaunch l;
+  const long long tokens =
+      max_seqlen_q > 0 ? max_seqlen_q : ((long long)total_q + batch - 1) / batch;
+  const long long rows = tokens * group;
+  l.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  l.dim = head_dim <= 64 ? 64 : 128;
+  l.grid = sm_count;
+  l.o_bytes = (size_t)2 * l.grid * l.rows * l.dim * sizeof(float);
+  l.lse_bytes = (size_t)2 * l.grid * l.rows * sizeof(float);
+  l.meta_bytes = (size_t)2 * l.grid * sizeof(int4);
+  return l;
+}
+
+// The cache as [num_pages * heads, 64, head_dim] bytes; a box is one (page,
+// head), its rows padded with zeros to the kernel's head dim.
+bool encode_cache(CUtensorMap* m, const void* base, int head_dim, int cells, int row) {
+  const fa::EncodeTiledFn fn = fa::tensor_map_encoder();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)fa::kPageTokens, (cuuint64_t)cells};
+  cuuint64_t strides[2] = {(cuuint64_t)head_dim, (cuuint64_t)head_dim * fa::kPageTokens};
+  cuuint32_t box[3] = {(cuuint32_t)row, (cuuint32_t)fa::kPageTokens, 1u};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int N>
+cudaError_t launch_attn(const CUtensorMap& k_map, const CUtensorMap& v_map,
+                        const fa::PagedAttnArgs& a, int grid, cudaStream_t stream) {
+  // Set once per device; concurrent first calls may both set it (the call is
+  // idempotent), the flag itself is atomic.
+  static std::atomic<bool> attr_done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  const int smem = (int)fa::paged_smem<D, N>();
+  if (!attr_done[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(fa::paged_attn_kernel<D, N>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    attr_done[dev].store(true, std::memory_order_release);
+  }
+  fa::paged_attn_kernel<D, N><<<grid, fa::kPagedThreads, smem, stream>>>(k_map, v_map, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || grid < 2) return e;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = dim3(grid - 1, N);
+  cfg.blockDim = dim3(D);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fa::paged_merge_kernel<D, N>, a);
+}
 
 bool cache_dim(int d) { return d == 64 || d == 80 || d == 96 || d == 128; }
 
@@ -221,9 +295,11 @@ extern "C" fa_status fa_paged_attn_plan(int batch, int total_q, int num_heads, i
   fa::DeviceFacts dev;
   const fa_status st = fa::device_facts(&dev);
   if (st != FA_OK) return st;
-  *grid = total_q;
-  *rows_per_tile = 1;
-  *workspace_bytes = 0;
+  const AttnLaunch l =
+      attn_launch(dev.sm_count, batch, total_q, num_heads / num_heads_k, head_dim, max_seqlen_q);
+  *grid = total_q > 0 ? l.grid : 0;
+  *rows_per_tile = l.rows;
+  *workspace_bytes = total_q > 0 ? l.bytes() : 0;
   return FA_OK;
 }
 
@@ -253,31 +329,54 @@ extern "C" fa_status fa_paged_attn(const void* q, long long q_row_stride, long l
   st = fa::device_facts(&dev);
   if (st != FA_OK) return st;
   if (total_q == 0) return FA_OK;
-  (void)workspace_bytes;
+  const int group = num_heads / num_heads_k;
+  const AttnLaunch l = attn_launch(dev.sm_count, batch, total_q, group, head_dim, max_seqlen_q);
+  if (!workspace || workspace_bytes < l.bytes()) return FA_ERR_INVALID_ARG;
+  CUtensorMap k_map, v_map;
+  if (!encode_cache(&k_map, k_cache, head_dim, num_pages * num_heads_k, l.dim) ||
+      !encode_cache(&v_map, v_cache, head_dim, num_pages * num_heads_k, l.dim))
+    return FA_ERR_LAUNCH;
   fa::PagedAttnArgs a;
   a.q = static_cast<const uint16_t*>(q);
   a.q_row = q_row_stride;
   a.q_head = q_head_stride;
-  a.k_cache = static_cast<const uint8_t*>(k_cache);
-  a.v_cache = static_cast<const uint8_t*>(v_cache);
   a.k_scale = k_scale;
   a.v_scale = v_scale;
-  a.cu = cu_seqlens_q;
-  a.seq_lens = seq_lens;
-  a.page_table = page_table;
-  a.batch = batch;
   a.total_q = total_q;
   a.heads = num_heads;
-  a.heads_k = num_heads_k;
   a.dim = head_dim;
   a.max_pages = max_pages_per_seq;
   a.num_pages = num_pages;
-  a.scale = softmax_scale;
-  a.causal = causal;
-  a.window = window_left;
+  a.shape = {num_heads_k, group, l.rows, causal != 0, window_left,
+             max_pages_per_seq * fa::kPageTokens};
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
-  fa::paged_attn_rows_kernel<<<dim3(total_q, num_heads), 128, 0,
-                               reinterpret_cast<cudaStream_t>(stream)>>>(a);
-  return launched();
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.part_o = reinterpret_cast<float*>(ws);
+  a.part_lse = reinterpret_cast<float*>(ws + l.o_bytes);
+  a.meta = reinterpret_cast<int4*>(ws + l.o_bytes + l.lse_bytes);
+  a.status = dev.status;
+  a.wait_limit_ns = dev.wait_limit_ns;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  // A launch holds the tile counts of kPagedMaxBatch sequences in shared
+  // memory; a larger batch runs as consecutive launches, which share the
+  // workspace in stream order.
+  for (int b0 = 0; b0 < batch; b0 += fa::kPagedMaxBatch) {
+    a.batch = std::min(batch - b0, fa::kPagedMaxBatch);
+    a.cu = cu_seqlens_q + b0;
+    a.seq_lens = seq_lens + b0;
+    a.page_table = page_table + (size_t)b0 * max_pages_per_seq;
+    cudaError_t e;
+    if (l.dim == 64)
+      e = l.rows == 16   ? launch_attn<64, 16>(k_map, v_map, a, l.grid, s)
+          : l.rows == 32 ? launch_attn<64, 32>(k_map, v_map, a, l.grid, s)
+                         : launch_attn<64, 64>(k_map, v_map, a, l.grid, s);
+    else
+      e = l.rows == 16   ? launch_attn<128, 16>(k_map, v_map, a, l.grid, s)
+          : l.rows == 32 ? launch_attn<128, 32>(k_map, v_map, a, l.grid, s)
+                         : launch_attn<128, 64>(k_map, v_map, a, l.grid, s);
+    if (e != cudaSuccess) return FA_ERR_LAUNCH;
+  }
+  return FA_OK;
 }

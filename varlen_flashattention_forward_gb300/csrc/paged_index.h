@@ -97,4 +97,137 @@ FA_HD KeyRange key_range(int i0, int i1, int n, int len, int held, bool causal, 
   return r;
 }
 
+// ---------------------------------------------------- attention work split
+// A work unit is one row tile (`rows` of the n * group rows of a sequence and
+// kv head, row = token * group + head of the group) against its key tiles of
+// kTileKeys keys.  Units are numbered by sequence, then head, then row tile;
+// their key tiles, in that order, are cut into equal contiguous ranges, one
+// for each CTA.
+constexpr int kTileKeys = 128;
+
+struct AttnShape {
+  int heads_k, group, rows;  // kv heads, query heads of one, rows of a tile
+  int causal, window, held;  // held: positions of the page table
+};
+
+FA_HD int row_tiles(const AttnShape& s, int n) {
+  return (int)(((long long)n * s.group + s.rows - 1) / s.rows);
+}
+// Keys of row tile t of a sequence with n query rows and len keys.
+FA_HD KeyRange tile_keys(const AttnShape& s, int t, int n, int len) {
+  const long long r0 = (long long)t * s.rows;
+  long long r1 = r0 + s.rows;
+  if (r1 > (long long)n * s.group) r1 = (long long)n * s.group;
+  return key_range((int)(r0 / s.group), (int)((r1 - 1) / s.group), n, len, s.held, s.causal != 0,
+                   s.window);
+}
+// First key tile and number of key tiles; a unit without keys keeps one (all
+// masked), which writes its empty rows.
+struct TileRange {
+  int first, count;
+};
+FA_HD TileRange key_tiles(const KeyRange& k) {
+  TileRange t;
+  t.first = k.lo / kTileKeys;
+  t.count = k.hi > k.lo ? (int)(((long long)k.hi + kTileKeys - 1) / kTileKeys) - t.first : 1;
+  return t;
+}
+// Key tiles of all row tiles of one (sequence, head).
+FA_HD long long head_tiles(const AttnShape& s, int n, int len) {
+  long long sum = 0;
+  const int m = n > 0 ? row_tiles(s, n) : 0;
+  for (int t = 0; t < m; ++t) sum += key_tiles(tile_keys(s, t, n, len)).count;
+  return sum;
+}
+
+// Start of CTA c's range of `total` tiles among `ctas`: the first
+// total % ctas ranges are one tile longer.
+FA_HD long long range_start(long long total, int ctas, int c) {
+  const long long q = total / ctas, r = total % ctas;
+  return c * q + (c < r ? c : r);
+}
+
+// Walks the segments of a range: the part of each unit's tiles inside it.
+// before[b] is the number of tiles of the sequences before b (batch + 1
+// entries).
+struct Segment {
+  int seq, head, row_tile;
+  RowRange q;        // the sequence's query rows
+  int len;           // its keys
+  KeyRange keys;     // of the row tile
+  int tile0;         // first key tile of the segment (tile t: keys 128 t ..)
+  int count;         // its key tiles
+  int part_lo, unit_count;  // place of tile0 among the unit's tiles, and their number
+};
+struct SegmentWalk {
+  long long at, end;  // tiles done, end of the range
+  int seq, head, row_tile;
+  long long in_unit;  // tiles of the current unit that are done
+};
+
+template <typename Before>
+FA_HD void walk_begin(SegmentWalk* w, long long lo, long long hi, int batch, const Before& before) {
+  w->at = lo;
+  w->end = hi;
+  int a = 0, b = batch;  // before(a) <= lo < before(b)
+  while (b - a > 1) {
+    const int m = (a + b) >> 1;
+    if (before(m) <= lo) a = m; else b = m;
+  }
+  w->seq = a;
+  w->head = -1;  // place within the sequence still to be found
+  w->row_tile = 0;
+  w->in_unit = 0;
+}
+
+// The next segment, or false at the end of the range.  seq_of(b, &q, &len)
+// gives a sequence's query rows and keys.
+template <typename Before, typename SeqOf>
+FA_HD bool walk_next(SegmentWalk* w, const AttnShape& s, const Before& before, const SeqOf& seq_of,
+                     Segment* g) {
+  if (w->at >= w->end) return false;
+  if (w->head < 0) {
+    while (before(w->seq + 1) <= w->at) ++w->seq;  // sequences without query rows
+    seq_of(w->seq, &g->q, &g->len);
+    const long long in_seq = w->at - before(w->seq);
+    const long long per_head = (before(w->seq + 1) - before(w->seq)) / s.heads_k;
+    w->head = (int)(in_seq / per_head);
+    long long left = in_seq - w->head * per_head;
+    w->row_tile = 0;
+    for (;;) {
+      const int c = key_tiles(tile_keys(s, w->row_tile, g->q.n, g->len)).count;
+      if (left < c) break;
+      left -= c;
+      ++w->row_tile;
+    }
+    w->in_unit = left;
+  } else {
+    seq_of(w->seq, &g->q, &g->len);
+  }
+  g->seq = w->seq;
+  g->head = w->head;
+  g->row_tile = w->row_tile;
+  g->keys = tile_keys(s, w->row_tile, g->q.n, g->len);
+  const TileRange t = key_tiles(g->keys);
+  long long n = t.count - w->in_unit;
+  if (n > w->end - w->at) n = w->end - w->at;
+  g->tile0 = t.first + (int)w->in_unit;
+  g->count = (int)n;
+  g->part_lo = (int)w->in_unit;
+  g->unit_count = t.count;
+  w->at += n;
+  w->in_unit += n;
+  if (w->in_unit == t.count) {
+    w->in_unit = 0;
+    if (++w->row_tile == row_tiles(s, g->q.n)) {
+      w->row_tile = 0;
+      if (++w->head == s.heads_k) {
+        w->head = -1;
+        ++w->seq;
+      }
+    }
+  }
+  return true;
+}
+
 }  // namespace fa

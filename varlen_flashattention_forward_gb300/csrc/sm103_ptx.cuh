@@ -265,6 +265,40 @@ __device__ __forceinline__ void mma_ss4_elect(uint32_t d_tmem, uint64_t a_desc, 
       : "memory");
 }
 
+// kSteps K=32 steps D (+)= A * B of 8-bit floats (kind::f8f6f4), both operands
+// K-major in shared memory, from one elected lane of a converged warp; the
+// first step overwrites D.  A step is 32 bytes further along each row.
+template <int kSteps>
+__device__ __forceinline__ void mma_f8_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                             uint32_t idesc) {
+  static_assert(kSteps == 2 || kSteps == 4, "64 or 128 bytes of a row");
+  if constexpr (kSteps == 4) {
+    asm volatile(
+        "{\n\t.reg .pred e, one, zero;\n\t.reg .b64 da, db;\n\t"
+        "setp.eq.u32 one, 0, 0;\n\tsetp.ne.u32 zero, 0, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, zero;\n\t"
+        "add.s64 da, %1, 2;\n\tadd.s64 db, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, one;\n\t"
+        "add.s64 da, %1, 4;\n\tadd.s64 db, %2, 4;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, one;\n\t"
+        "add.s64 da, %1, 6;\n\tadd.s64 db, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, one;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred e, one, zero;\n\t.reg .b64 da, db;\n\t"
+        "setp.eq.u32 one, 0, 0;\n\tsetp.ne.u32 zero, 0, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, zero;\n\t"
+        "add.s64 da, %1, 2;\n\tadd.s64 db, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, one;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc)
+        : "memory");
+  }
+}
+
 __device__ __forceinline__ void mbar_arrive_elect(uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
@@ -471,6 +505,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// Packs two fp32 into f16x2 (round to nearest even): lo goes to bits 0..15.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
 // Packs two fp32 into bf16x2 (round to nearest even): lo goes to bits 0..15.
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t d;
@@ -565,6 +606,19 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(uint32_t M, uint32_t N,
                                                       bool a_mn_major, bool b_mn_major) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn_major ? 1u : 0u) << 15) |
          ((b_mn_major ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// The same with f16 A and B (format 0).
+__host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N, bool a_mn_major,
+                                                     bool b_mn_major) {
+  return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
+         ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// Instruction descriptor for kind::f8f6f4 with e4m3 A and B (format 0), both
+// K-major, and fp32 accumulation.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N) {
+  return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
 }  // namespace ptx

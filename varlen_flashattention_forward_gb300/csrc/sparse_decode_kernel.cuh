@@ -54,6 +54,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "named_bar.cuh"
 #include "sm103_ptx.cuh"
 #include "varlen_fwd_kernel.cuh"  // kStatusTimeout, bounded waits
 
@@ -137,38 +138,6 @@ constexpr size_t kDecodeSmem = 1024 + kQBytes + 2 * kStageBytes +
 static_assert(kDecodeSmem <= 232448, "decode shared memory exceeds the per-CTA limit");
 static_assert((kQBytes + 2 * kStageBytes + sizeof(int) * kDecodeMaxTopk) % 16 == 0,
               "control block must stay 16-byte aligned");
-
-__device__ __forceinline__ void named_bar_sync(int id, int n) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
-}
-
-// Barrier over n threads that also ANDs a predicate (all must pass).
-__device__ __forceinline__ int named_bar_and(int id, int n, int pred) {
-  int r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 q, %1, 0;\n\t"
-      "bar.red.and.pred p, %2, %3, q;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r)
-      : "r"(pred), "r"(id), "r"(n)
-      : "memory");
-  return r;
-}
-
-// Barrier over n threads that also ORs a predicate.
-__device__ __forceinline__ int named_bar_or(int id, int n, int pred) {
-  int r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 q, %1, 0;\n\t"
-      "bar.red.or.pred p, %2, %3, q;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r)
-      : "r"(pred), "r"(id), "r"(n)
-      : "memory");
-  return r;
-}
 
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
