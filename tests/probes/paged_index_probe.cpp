@@ -38,13 +38,15 @@ extern "C" int probe_walk(const int* cu, const int* lens, int batch, int total_q
     *q = fa::row_range(cu[b], cu[b + 1], total_q);
     *len = lens[b];
   };
-  long long pre[4097];
+  int pre[4097];
+  long long sum = 0;
   pre[0] = 0;
   for (int b = 0; b < batch; ++b) {
     fa::RowRange q;
     int len;
     seq_of(b, &q, &len);
-    pre[b + 1] = pre[b] + heads_k * fa::head_tiles(s, q.n, len);
+    sum += heads_k * fa::head_tiles(s, q.n, len);
+    pre[b + 1] = fa::capped_tiles(sum);
   }
   auto before = [&](int b) { return pre[b]; };
   int found = 0;

@@ -40,6 +40,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 FA_OK = 0
@@ -147,6 +148,8 @@ def _stream_ptr(stream):
 
 
 def _check(t, name, dtype, ndim, view=False):
+    if t.dtype is dtype and t.dim() == ndim and not view and t.is_contiguous():
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != ndim:
@@ -344,32 +347,47 @@ def fa_merge_attn_states(prefix_out, prefix_lse, suffix_out, suffix_lse, out=Non
     return out, out_lse
 
 
-@contextlib.contextmanager
-def _on(stream, **tensors):
-    """Checks that the given tensors (None: left out) are on one CUDA device,
-    makes it and the call's stream current, and yields the stream pointer.
-    What is allocated inside belongs to that stream."""
+def _device(tensors, stream):
+    """The one CUDA device that the named tensors (None: left out) are on, and
+    a context that makes it and the call's stream current where they are not:
+    what is allocated in it belongs to that stream."""
     import torch
-    device = None
-    for name, t in tensors.items():
+    index = None
+    for name, t in tensors:
         if t is None:
             continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-    with torch.cuda.stream(stream):
-        yield ctypes.c_void_p(stream.cuda_stream)
+        i = t.get_device()
+        if i != index:
+            if i < 0:
+                raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
+            if index is not None:
+                raise ValueError(f"{name} is on {t.device}, other tensors on cuda:{index}")
+            index = i
+    if stream is not None:
+        if stream.device.index != index:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
+        return index, torch.cuda.stream(stream)
+    if index != torch.cuda.current_device():
+        return index, torch.cuda.device(index)
+    return index, _NO_CONTEXT
+
+
+_NO_CONTEXT = contextlib.nullcontext()
+
+
+def _raw_stream(index):
+    """Pointer of the current stream of a device."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _p(t):
+    """A tensor's address for an argument declared c_void_p (None: NULL)."""
+    return None if t is None else t.data_ptr()
 
 
 def _shape(t, name, shape):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -434,8 +452,10 @@ def fa_qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=
         _shape(positions, "positions", (T,))
     elif rot:
         raise ValueError("positions are needed for the rotation")
-    with _on(stream, q=q, k=k, positions=positions, cos_sin=cos_sin, q_weight=q_weight,
-             k_weight=k_weight, q_out=q_out, k_out=k_out) as sp:
+    index, here = _device((("q", q), ("k", k), ("positions", positions), ("cos_sin", cos_sin),
+                           ("q_weight", q_weight), ("k_weight", k_weight), ("q_out", q_out),
+                           ("k_out", k_out)), stream)
+    with here:
         sides = []
         for name, t, o in (("q_out", q, q_out), ("k_out", k, k_out)):
             if t is None:
@@ -445,14 +465,15 @@ def fa_qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=
                 continue
             if o is None:
                 o = torch.empty(t.shape, dtype=torch.bfloat16, device=t.device)
-            _check(o, name, torch.bfloat16, 3, view=True)
-            _shape(o, name, t.shape)
-            sides.append((t, t.stride(0), t.stride(1), t.shape[1], o, o.stride(0), o.stride(1)))
+            else:
+                _check(o, name, torch.bfloat16, 3, view=True)
+                _shape(o, name, t.shape)
+            sides.append((t, *t.stride()[:2], t.shape[1], o, *o.stride()[:2]))
         (q, qr, qh, H, q_out, qor, qoh), (k, kr, kh, Hk, k_out, kor, koh) = sides
         st = lib.fa_qk_norm_rope(
-            _ptr(q), qr, qh, _ptr(k), kr, kh, _ptr(positions), _ptr(cos_sin), _ptr(q_weight),
-            _ptr(k_weight), T, H, Hk, d, rot, max_pos, int(bool(interleaved)), float(eps),
-            _ptr(q_out), qor, qoh, _ptr(k_out), kor, koh, sp)
+            _p(q), qr, qh, _p(k), kr, kh, _p(positions), _p(cos_sin), _p(q_weight), _p(k_weight),
+            T, H, Hk, d, rot, max_pos, bool(interleaved), eps, _p(q_out), qor, qoh, _p(k_out),
+            kor, koh, _raw_stream(index))
     if st != FA_OK:
         raise FaError(st, "fa_qk_norm_rope")
     return q_out, k_out
@@ -480,15 +501,19 @@ def fa_paged_kv_append(k, v, cu_seqlens, seq_lens, page_table, k_cache, v_cache,
     _shape(k, "k", (k.shape[0], hk, d))
     _shape(v, "v", k.shape)
     rot, max_pos = _check_rope(cos_sin, (("k_weight", k_weight),), d)
-    with _on(stream, k=k, v=v, cu_seqlens=cu_seqlens, seq_lens=seq_lens, page_table=page_table,
-             k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
-             cos_sin=cos_sin, k_weight=k_weight) as sp:
+    index, here = _device((("k", k), ("v", v), ("cu_seqlens", cu_seqlens),
+                           ("seq_lens", seq_lens), ("page_table", page_table),
+                           ("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale),
+                           ("v_scale", v_scale), ("cos_sin", cos_sin), ("k_weight", k_weight)),
+                          stream)
+    kr, kh, _ = k.stride()
+    vr, vh, _ = v.stride()
+    with here:
         st = lib.fa_paged_kv_append(
-            _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0), v.stride(1),
-            _ptr(cu_seqlens), _ptr(seq_lens), _ptr(page_table), batch, k.shape[0], hk, d, pages,
-            width, _ptr(k_weight), float(eps), _ptr(cos_sin), rot, max_pos,
-            int(bool(interleaved)), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-            sp)
+            _p(k), kr, kh, _p(v), vr, vh, _p(cu_seqlens), _p(seq_lens), _p(page_table), batch,
+            k.shape[0], hk, d, pages, width, _p(k_weight), eps, _p(cos_sin), rot, max_pos,
+            bool(interleaved), _p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale),
+            _raw_stream(index))
     if st != FA_OK:
         raise FaError(st, "fa_paged_kv_append")
 
@@ -533,34 +558,43 @@ def fa_paged_attn(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, seq_lens,
         raise ValueError(f"q has head dim {dq}, the cache {d}")
     if softmax_scale is None:
         softmax_scale = d ** -0.5
-    with _on(stream, q=q, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
-             cu_seqlens_q=cu_seqlens_q, seq_lens=seq_lens, page_table=page_table, out=out,
-             lse=lse, workspace=workspace) as sp:
+    index, here = _device((("q", q), ("k_cache", k_cache), ("v_cache", v_cache),
+                           ("k_scale", k_scale), ("v_scale", v_scale),
+                           ("cu_seqlens_q", cu_seqlens_q), ("seq_lens", seq_lens),
+                           ("page_table", page_table), ("out", out), ("lse", lse),
+                           ("workspace", workspace)), stream)
+    with here:
         if out is None:
             out = torch.empty((T, H, d), dtype=torch.bfloat16, device=q.device)
         else:
             _check(out, "out", torch.bfloat16, 3)
             _shape(out, "out", (T, H, d))
-        if lse is None and return_lse:
-            lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
         if lse is not None:
             _check(lse, "lse", torch.float32, 2)
             _shape(lse, "lse", (H, T))
+        elif return_lse:
+            lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
         if workspace is None:
-            _, _, need = fa_paged_attn_plan(batch, T, H, hk, d, max_seqlen_q)
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            need = _attn_workspace(index, batch, T, H, hk, d, max_seqlen_q)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         else:
             _check(workspace, "workspace", torch.uint8, 1)
+            need = workspace.shape[0]
+        qr, qh, _ = q.stride()
         st = lib.fa_paged_attn(
-            _ptr(q), q.stride(0), q.stride(1), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-            _ptr(v_scale), _ptr(cu_seqlens_q), _ptr(seq_lens), _ptr(page_table), batch, T, H, hk,
-            d, pages, width, int(max_seqlen_q), int(max_seqlen_k), float(softmax_scale),
-            int(bool(causal)), int(window_left), _ptr(out), _ptr(lse), _ptr(workspace),
-            0 if workspace is None else workspace.numel(), sp)
+            _p(q), qr, qh, _p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale), _p(cu_seqlens_q),
+            _p(seq_lens), _p(page_table), batch, T, H, hk, d, pages, width, max_seqlen_q,
+            max_seqlen_k, softmax_scale, bool(causal), window_left, _p(out), _p(lse),
+            _p(workspace), need, _raw_stream(index))
     if st != FA_OK:
         raise FaError(st, "fa_paged_attn")
     return (out, lse) if lse is not None else out
+
+
+@functools.lru_cache(maxsize=1024)
+def _attn_workspace(index, batch, total_q, num_heads, num_heads_k, head_dim, max_seqlen_q):
+    """Workspace bytes of a fa_paged_attn call on the current device `index`."""
+    return fa_paged_attn_plan(batch, total_q, num_heads, num_heads_k, head_dim, max_seqlen_q)[2]
 
 
 def fa_paged_kv_gather(k_cache, v_cache, k_scale, v_scale, cu_seqlens, page_table, total_k,
@@ -573,19 +607,22 @@ def fa_paged_kv_gather(k_cache, v_cache, k_scale, v_scale, cu_seqlens, page_tabl
     lib = load_library()
     batch, pages, hk, d, width = _check_cache(k_cache, v_cache, k_scale, v_scale, cu_seqlens,
                                               page_table)
-    with _on(stream, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
-             cu_seqlens=cu_seqlens, page_table=page_table, k_out=k_out, v_out=v_out) as sp:
+    index, here = _device((("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale),
+                           ("v_scale", v_scale), ("cu_seqlens", cu_seqlens),
+                           ("page_table", page_table), ("k_out", k_out), ("v_out", v_out)),
+                          stream)
+    with here:
         outs = []
         for name, o in (("k_out", k_out), ("v_out", v_out)):
             if o is None:
                 o = torch.empty((total_k, hk, d), dtype=torch.bfloat16, device=k_cache.device)
-            _check(o, name, torch.bfloat16, 3)
-            _shape(o, name, (total_k, hk, d))
+            else:
+                _check(o, name, torch.bfloat16, 3)
+                _shape(o, name, (total_k, hk, d))
             outs.append(o)
         st = lib.fa_paged_kv_gather(
-            _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(cu_seqlens),
-            _ptr(page_table), batch, int(total_k), hk, d, pages, width, _ptr(outs[0]),
-            _ptr(outs[1]), sp)
+            _p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale), _p(cu_seqlens), _p(page_table),
+            batch, total_k, hk, d, pages, width, _p(outs[0]), _p(outs[1]), _raw_stream(index))
     if st != FA_OK:
         raise FaError(st, "fa_paged_kv_gather")
     return outs[0], outs[1]

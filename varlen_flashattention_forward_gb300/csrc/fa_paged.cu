@@ -37,7 +37,7 @@ AttnLaunch attn_launch(int sm_count, int batch, int total_q, int group, int head
   const long long rows = tokens * group;
   l.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
   l.dim = head_dim <= 64 ? 64 : 128;
-  l.grid = sm_count;
+  l.grid = std::min(sm_count, fa::kPagedMaxGrid);
   l.o_bytes = (size_t)2 * l.grid * l.rows * l.dim * sizeof(float);
   l.lse_bytes = (size_t)2 * l.grid * l.rows * sizeof(float);
   l.meta_bytes = (size_t)2 * l.grid * sizeof(int4);
@@ -360,10 +360,16 @@ extern "C" fa_status fa_paged_attn(const void* q, long long q_row_stride, long l
   a.wait_limit_ns = dev.wait_limit_ns;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // A launch holds the tile counts of kPagedMaxBatch sequences in shared
-  // memory; a larger batch runs as consecutive launches, which share the
-  // workspace in stream order.
-  for (int b0 = 0; b0 < batch; b0 += fa::kPagedMaxBatch) {
-    a.batch = std::min(batch - b0, fa::kPagedMaxBatch);
+  // memory and numbers its tiles in 32 bits; a larger batch runs as
+  // consecutive launches, which share the workspace in stream order.
+  const long long per_row_tile =
+      (long long)num_heads_k * ((long long)max_pages_per_seq * fa::kPageTokens / fa::kTileKeys + 1);
+  const long long row_tiles = (long long)total_q * group / l.rows;
+  const long long fit = fa::kMaxTiles / per_row_tile - row_tiles;
+  if (fit < 1) return FA_ERR_UNSUPPORTED;
+  const int step = (int)std::min<long long>(fa::kPagedMaxBatch, fit);
+  for (int b0 = 0; b0 < batch; b0 += step) {
+    a.batch = std::min(batch - b0, step);
     a.cu = cu_seqlens_q + b0;
     a.seq_lens = seq_lens + b0;
     a.page_table = page_table + (size_t)b0 * max_pages_per_seq;

@@ -29,19 +29,25 @@
 // maximum m is taken over x', so that P' = 2^(x' - m + 7) stays below 2^15;
 // the row sum adds 2^(x - m + 7).
 //
-//   producer warp 10    walks the segments, loads page ids and scales ahead,
+//   producer warp       walks the segments, loads page ids and scales ahead,
 //                       and TMA-loads the pages of each tile (128-byte
 //                       swizzle; 64-byte at dim 64) into a K and a V ring;
-//   Q warp 11           splits each segment's rows into hi and lo;
-//   S issuer warp 8     St(i) as soon as K(i) has landed;
-//   converter warps 4-7 V(i) to f16, rows nobody sees as zeros (they may hold
+//   Q warp              splits each segment's rows into hi and lo;
+//   S issuer warp       St(i) as soon as K(i) has landed;
+//   converter warps     V(i) to f16, rows nobody sees as zeros (they may hold
 //                       anything, and 0 * NaN is NaN);
-//   softmax warps 0-3   thread = key: masks, the vote on a new maximum (only
+//   softmax             thread = key: masks, the vote on a new maximum (only
 //                       when some score passes m by 2^8 is the maximum taken,
 //                       O rescaled and the sums adjusted), exp2, Pt;
-//   PV issuer warp 9    Ot += Vt Pt.
+//   PV issuer           Ot += Vt Pt.
 //
-// TMEM: St at [0, 4N) (two buffers of 2N columns), Ot at [4N, 6N) (two).
+// One tile's softmax is a chain of waits (S, the vote, the P buffer) about
+// as long as a tile's bytes take to arrive, so two warpgroups run it, on even
+// and on odd tiles.  Each has its own running maximum, sums and Ot, and they
+// are joined at the end of a segment like the parts of a split unit.
+//
+// TMEM: St at [0, 4N) (two buffers of 2N columns), Ot at [4N, 8N) (of two
+// segments and two warpgroups).
 #pragma once
 
 #include <cstddef>
@@ -57,11 +63,14 @@
 
 namespace fa {
 
-constexpr int kPagedThreads = 384;
-// Register split (launch: 168 x 384 = 64512): softmax 128 x 232, converters
-// 128 x 88, control 128 x 96 = 53248.
-constexpr uint32_t kPagedSoftmaxRegs = 232;
-constexpr uint32_t kPagedConvertRegs = 88;
+// Warps 0-7 softmax, 8-11 converters, 12 S issuer, 13 PV issuer, 14 producer,
+// 15 Q.
+constexpr int kPagedThreads = 512;
+constexpr int kConvertWarp = 8, kSWarp = 12, kPvWarp = 13, kLoadWarp = 14;
+// Register split (launch: 128 x 512 = 65536): softmax 256 x 160, converters
+// 128 x 80, control 128 x 96 = 63488.
+constexpr uint32_t kPagedSoftmaxRegs = 160;
+constexpr uint32_t kPagedConvertRegs = 80;
 constexpr uint32_t kPagedControlRegs = 96;
 constexpr int kPagedMaxBatch = 1024;  // sequences of one launch
 constexpr int kPagedInfo = 8;         // tile descriptors in flight
@@ -109,7 +118,7 @@ struct PagedCfg {
   static constexpr uint32_t kSwP = N == 64   ? ptx::kLayoutSw128
                                    : N == 32 ? ptx::kLayoutSw64
                                              : ptx::kLayoutSw32;
-  static constexpr uint32_t kTmemCols = N == 16 ? 128 : N == 32 ? 256 : 512;
+  static constexpr uint32_t kTmemCols = 8 * N;
   // Offsets from a 1024-byte boundary.
   static constexpr int kK = 0;
   static constexpr int kV = kK + NK * kTileBytes;
@@ -128,19 +137,25 @@ struct alignas(16) PagedCtl {
   uint64_t p_full[2], pv_done[2];   // Pt written (128) / PV complete
   uint64_t q_full[2], q_free[2];    // Q terms written (32) / last S of the segment
   uint64_t qs_full[4];              // row scales written (32)
-  uint64_t o_free[2];               // Ot read out (128)
+  uint64_t o_free[2];               // Ot of a segment read out (256)
   uint64_t drain, drain_pv;         // everything an issuer started is complete
   uint32_t tmem_base;
   volatile int abort_flag;
   TileInfo info[kPagedInfo];
   alignas(16) float qs[4][64];      // row scale * softmax scale * log2(e)
-  alignas(16) float red[4][64];     // per-warp partial maxima / sums
-  alignas(16) float m_used[64];     // running maximum - bias
-  alignas(16) float alpha[64];      // rescale factors; at the end reciprocal sums
-  long long warp_sum[kPagedThreads / 32];
-  long long before[kPagedMaxBatch + 1];
+  // Per softmax warpgroup: per-warp partial maxima or sums, the running
+  // maximum less the bias (0 while no key was seen), rescale factors.
+  alignas(16) float red[2][4][64];
+  alignas(16) float m_used[2][64];
+  alignas(16) float alpha[2][64];
+  // By segment parity and warpgroup: maximum so far (-inf: no key seen) and,
+  // at the segment's end, the sum.  (Two copies: a warpgroup may begin the
+  // next segment while the other still joins this one.)
+  float end_m[2][2][64], end_l[2][2][64];
+  float weight[2][2][64];            // [reader][warpgroup] factors of its Ot
+  long long warp_tiles[kPagedThreads / 32];
+  int before[kPagedMaxBatch + 1];
 };
-
 // (16-byte loads of these.)
 static_assert(offsetof(PagedCtl, qs) % 16 == 0 && offsetof(PagedCtl, m_used) % 16 == 0, "align");
 
@@ -148,6 +163,7 @@ template <int D, int N>
 constexpr size_t paged_smem() {
   return 1024 + PagedCfg<D, N>::kCtl + sizeof(PagedCtl);
 }
+static_assert(sizeof(PagedCtl) < 16384, "control block");
 static_assert(paged_smem<128, 64>() <= 232448, "shared memory exceeds the per-CTA limit");
 static_assert(paged_smem<128, 32>() <= 232448, "shared memory exceeds the per-CTA limit");
 
@@ -212,7 +228,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       init(cb->pv_done[s], 1);
       init(cb->q_full[s], 32);
       init(cb->q_free[s], 1);
-      init(cb->o_free[s], 128);
+      init(cb->o_free[s], 256);
     }
     init(cb->drain, 1);
     init(cb->drain_pv, 1);
@@ -220,11 +236,11 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     ptx::fence_mbar_init();
     a.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
   }
-  if (warp == 8) {
+  if (warp == kSWarp) {
     ptx::tmem_alloc(ptx::smem_u32(&cb->tmem_base), C::kTmemCols);
     ptx::tmem_relinquish();
   }
-  if (warp == 10 && lane == 0) {
+  if (warp == kLoadWarp && lane == 0) {
     ptx::prefetch_tmap(&k_map);
     ptx::prefetch_tmap(&v_map);
   }
@@ -234,12 +250,12 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     long long base = 0;
     for (int b0 = 0; b0 < a.batch; b0 += kPagedThreads) {
       const int b = b0 + tid;
-      long long n = 0;
+      int n = 0;
       if (b < a.batch) {
         RowRange q;
         int len;
         seq_of(b, &q, &len);
-        n = sh.heads_k * head_tiles(sh, q.n, len);
+        n = capped_tiles(sh.heads_k * head_tiles(sh, q.n, len));
       }
       long long sum = n;
 #pragma unroll
@@ -247,15 +263,15 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         const long long v = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += v;
       }
-      if (lane == 31) cb->warp_sum[warp] = sum;
+      if (lane == 31) cb->warp_tiles[warp] = sum;
       __syncthreads();
       long long all = 0, lo = base;
 #pragma unroll
       for (int w = 0; w < kPagedThreads / 32; ++w) {
-        if (w < warp) lo += cb->warp_sum[w];
-        all += cb->warp_sum[w];
+        if (w < warp) lo += cb->warp_tiles[w];
+        all += cb->warp_tiles[w];
       }
-      if (b < a.batch) cb->before[b + 1] = lo + sum;
+      if (b < a.batch) cb->before[b + 1] = capped_tiles(lo + sum);
       base += all;
       __syncthreads();
     }
@@ -266,7 +282,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = cb->tmem_base;
   auto before = [&](int b) { return cb->before[b]; };
-  const long long total = cb->before[a.batch];
+  const int total = cb->before[a.batch];
   const int cta = blockIdx.x, ctas = gridDim.x;
   SegmentWalk walk;
   walk_begin(&walk, range_start(total, ctas, cta), range_start(total, ctas, cta + 1), a.batch,
@@ -277,14 +293,17 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     return wait_warp(ptx::smem_u32(&b), (uint32_t)parity, abort_flag, a.status, a.wait_limit_ns);
   };
 
-  if (warp >= 4 && warp < 8) {
+  if (warp >= kConvertWarp && warp < kSWarp) {
     ptx::regs_dec<kPagedConvertRegs>();
     // ------------------------------------------------------------ converters
-    // Thread t: 16-byte unit u = t % (D / 16) of rows t / (D / 16) + k * 128 / (D / 16).
-    constexpr int kUnits = D / 16;          // 8 or 4 units of a row
-    constexpr int kRows = 128 / kUnits;     // rows at once
-    const int t = tid - 128;
-    const int u = t % kUnits, r0 = t / kUnits;
+    // A thread takes 16-byte units (16 codes) of a row.  Eight neighbouring
+    // lanes take four units of the rows r and r ^ 5 (r even): under the
+    // swizzles their eight 16-byte loads, and their eight stores of either
+    // half, then lie in different banks.
+    constexpr int kChunks = D / 64;          // 64-dim chunks of an f16 row
+    constexpr int kIters = 128 * (D / 16) / 128;
+    const int t = tid - 32 * kConvertWarp;
+    const int u4 = t & 3, odd = (t >> 2) & 1, group = t >> 3;
     bool ok = true;
     int i = 0;
     while (ok && walk_next(&walk, sh, before, seq_of, &g)) {
@@ -294,44 +313,51 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         if (!ok) break;
         const TileInfo& ti = cb->info[i % kPagedInfo];
         const int lo = ti.lo, hi = ti.hi, held = ti.held;
+        const bool all = lo == 0 && hi == kTileKeys && held == 3;
+        const uint8_t* src = smem + C::kV + slot * C::kTileBytes;
+        uint4 c[kIters];
+        auto place = [&](int k, int* r, int* chunk) {
+          const int id = group + 16 * k;  // of 64 row pairs x chunks
+          *chunk = id % kChunks;
+          const int even = 2 * (id / kChunks);
+          *r = odd ? even ^ 5 : even;
+        };
+#pragma unroll
+        for (int k = 0; k < kIters; ++k) {
+          int r, ch;
+          place(k, &r, &ch);
+          const int u = ch * 4 + u4;
+          const int us = D == 128 ? (u ^ (r & 7)) : (u ^ ((r >> 1) & 3));
+          c[k] = *reinterpret_cast<const uint4*>(src + r * C::kRow + us * 16);
+          if (!all && (r < lo || r >= hi || !((held >> (r >> 6)) & 1)))
+            c[k] = make_uint4(0u, 0u, 0u, 0u);
+        }
         if (i >= 2) {
           ok = wait(cb->pv_done[hb], ((i >> 1) - 1) & 1);
           if (!ok) break;
         }
-        const uint8_t* src = smem + C::kV + slot * C::kTileBytes;
         uint8_t* dst = smem + C::kVh + hb * C::kVhBytes;
 #pragma unroll
-        for (int k = 0; k < kUnits; ++k) {
-          const int r = r0 + k * kRows;
-          const int us = D == 128 ? (u ^ (r & 7)) : (u ^ ((r >> 1) & 3));
-          uint4 c = *reinterpret_cast<const uint4*>(src + r * C::kRow + us * 16);
-          if (r < lo || r >= hi || !((held >> (r >> 6)) & 1)) c = make_uint4(0u, 0u, 0u, 0u);
-          uint4 h0, h1;
-          h0.x = unpack_e4m3x2(c.x);
-          h0.y = unpack_e4m3x2(c.x >> 16);
-          h0.z = unpack_e4m3x2(c.y);
-          h0.w = unpack_e4m3x2(c.y >> 16);
-          h1.x = unpack_e4m3x2(c.z);
-          h1.y = unpack_e4m3x2(c.z >> 16);
-          h1.z = unpack_e4m3x2(c.w);
-          h1.w = unpack_e4m3x2(c.w >> 16);
-          // f16 rows of 128 bytes in chunks of 64 dims, 128-byte swizzle;
-          // lanes of the upper chunk store their second half first, so that
-          // the eight lanes of a row hit eight different 16-byte banks.
-          uint8_t* row = dst + (u >> 2) * (kTileKeys * 128) + r * 128;
-          const int p0 = ((u & 3) * 2) ^ (r & 7), p1 = p0 ^ 1;
-          const bool swap = u >= 4;
-          *reinterpret_cast<uint4*>(row + (swap ? p1 : p0) * 16) = swap ? h1 : h0;
-          *reinterpret_cast<uint4*>(row + (swap ? p0 : p1) * 16) = swap ? h0 : h1;
+        for (int k = 0; k < kIters; ++k) {
+          int r, ch;
+          place(k, &r, &ch);
+          uint8_t* row = dst + ch * (kTileKeys * 128) + r * 128;
+          const int p0 = (2 * u4) ^ (r & 7);
+          *reinterpret_cast<uint4*>(row + p0 * 16) =
+              make_uint4(unpack_e4m3x2(c[k].x), unpack_e4m3x2(c[k].x >> 16),
+                         unpack_e4m3x2(c[k].y), unpack_e4m3x2(c[k].y >> 16));
+          *reinterpret_cast<uint4*>(row + (p0 ^ 1) * 16) =
+              make_uint4(unpack_e4m3x2(c[k].z), unpack_e4m3x2(c[k].z >> 16),
+                         unpack_e4m3x2(c[k].w), unpack_e4m3x2(c[k].w >> 16));
         }
         ptx::fence_proxy_async_smem();
         ptx::mbar_arrive(ptx::smem_u32(&cb->vh_full[hb]));
         ptx::mbar_arrive(ptx::smem_u32(&cb->v_free[slot]));
       }
     }
-  } else if (warp >= 8) {
+  } else if (warp >= kSWarp) {
     ptx::regs_dec<kPagedControlRegs>();
-    if (warp == 8) {
+    if (warp == kSWarp) {
       // ---------------------------------------------------------- S issuer
       constexpr uint32_t idesc = ptx::idesc_e4m3_f32(128, 2 * N);
       bool ok = true;
@@ -359,7 +385,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       }
       ptx::mma_commit_elect(ptx::smem_u32(&cb->drain));
       wait_drain_warp(ptx::smem_u32(&cb->drain), 0, a.status);
-    } else if (warp == 9) {
+    } else if (warp == kPvWarp) {
       // --------------------------------------------------------- PV issuer
       constexpr uint32_t idesc = ptx::idesc_f16_f32(D, N, true, true);
       bool ok = true;
@@ -377,8 +403,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
                                              kTileKeys * 128, 1024, ptx::kLayoutSw128);
           const uint64_t bd = ptx::smem_desc(ptx::smem_u32(smem + C::kP + hb * C::kPBytes),
                                              8 * C::kPRow, 8 * C::kPRow, C::kSwP);
-          const uint32_t d = tmem + 4 * N + (seg & 1) * N;
-          ptx::mma_ss4_elect<16 * 128 / 16, 16 * C::kPRow / 16>(d, ad, bd, idesc, n > 0 ? 1u : 0u);
+          const uint32_t d = tmem + 4 * N + (seg & 1) * 2 * N + hb * N;
+          ptx::mma_ss4_elect<16 * 128 / 16, 16 * C::kPRow / 16>(d, ad, bd, idesc, n > 1 ? 1u : 0u);
           ptx::mma_ss4_elect<16 * 128 / 16, 16 * C::kPRow / 16>(
               d, ptx::desc_add(ad, 64 * 128), ptx::desc_add(bd, 64 * C::kPRow), idesc, 1u);
           ptx::mma_commit_elect(ptx::smem_u32(&cb->pv_done[hb]));
@@ -386,7 +412,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       }
       ptx::mma_commit_elect(ptx::smem_u32(&cb->drain_pv));
       wait_drain_warp(ptx::smem_u32(&cb->drain_pv), 0, a.status);
-    } else if (warp == 10) {
+    } else if (warp == kLoadWarp) {
       // ---------------------------------------------------------- producer
       test_load_delay(a.wait_limit_ns);
       bool ok = true;
@@ -504,15 +530,14 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
 #pragma unroll
             for (int o = kLanes / 2; o > 0; o >>= 1)
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            int e;
-            frexpf(mx * (1.f / 256.f), &e);  // mx * 2^-e in [128, 256)
-            if (!(mx > 0.f)) e = 0;
-            // Two factors: 2^-e itself may be past fp32 for tiny rows.
-            const float f0 = ldexpf(1.f, -(e / 2)), f1 = ldexpf(1.f, -(e - e / 2));
+            // mx in [2^e, 2^(e+1)) goes to [128, 256).  (Rows below 2^-100 keep
+            // a smaller size; their scores are zero in fp32 all the same.)
+            const int e = imax((int)(__float_as_uint(mx) >> 23) - 127, -100);
+            const float f = __uint_as_float((uint32_t)(7 - e + 127) << 23);
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const float y0 = x[2 * k] * f0 * f1, y1 = x[2 * k + 1] * f0 * f1;
+              const float y0 = x[2 * k] * f, y1 = x[2 * k + 1] * f;
               hi[k] = pack_e4m3x2(y0, y1);
               const float2 b = f16x2_floats(unpack_e4m3x2(hi[k]));
               lo[k] = pack_e4m3x2(y0 - b.x, y1 - b.y);
@@ -527,9 +552,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             *reinterpret_cast<uint2*>(q_s + place(N + n)) =
                 make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
             if (sub == 0)
-              cb->qs[seg & 3][n] = mx < __int_as_float(0x7f800000)
-                                       ? ldexpf(a.scale_log2, e)
-                                       : __int_as_float(0x7fffffff);
+              cb->qs[seg & 3][n] =
+                  mx < __int_as_float(0x7f800000)
+                      ? a.scale_log2 * __uint_as_float((uint32_t)(e - 7 + 127) << 23)
+                      : __int_as_float(0x7fffffff);
           }
         }
         ptx::fence_proxy_async_smem();
@@ -541,150 +567,160 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     ptx::regs_inc<kPagedSoftmaxRegs>();
     // -------------------------------------------------------------- softmax
     const float neg_inf = -__int_as_float(0x7f800000);
-    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-    const int key = tid;           // of the tile
+    const int wg = warp >> 2;             // tiles i with i % 2 == wg
+    const int key = tid & 127;            // of the tile
     const int page = key >> 6;
+    const int bar = 1 + 4 * wg;           // named barriers bar .. bar + 2; 4: both warpgroups
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_tmem = tmem + lane_base + wg * 2 * N;
+    float (*red)[64] = cb->red[wg];
+    float* m_used = cb->m_used[wg];
+    float* alpha = cb->alpha[wg];
+    uint8_t* prow = smem + C::kP + wg * C::kPBytes + key * C::kPRow;
     float l[N];
     bool ok = true;
-    int i = 0;
+    int i = 0;          // tiles before the segment
     for (int seg = 0; ok && walk_next(&walk, sh, before, seq_of, &g); ++seg) {
       const int row0 = g.row_tile * N;
       const int rows = imin(N, g.q.n * sh.group - row0);
       const int tok0 = row0 / sh.group, tok1 = (row0 + rows - 1) / sh.group;
       const long long at0 = (long long)g.len - g.q.n + tok0;  // position of the first row
+      const uint32_t o_tmem = tmem + lane_base + 4 * N + (seg & 1) * 2 * N + wg * N;
 #pragma unroll
       for (int n = 0; n < N; ++n) l[n] = 0.f;
-      if (tid < N) cb->m_used[tid] = neg_inf;
-      ok = wait(cb->qs_full[seg & 3], (seg >> 2) & 1);
-      ok = named_bar_and(3, 128, ok);
-      if (!ok) break;
-      float c[N];
-#pragma unroll
-      for (int n = 0; n < N; n += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(&cb->qs[seg & 3][n]);
-        c[n] = v.x; c[n + 1] = v.y; c[n + 2] = v.z; c[n + 3] = v.w;
-      }
-      for (int t = 0; t < g.count; ++t, ++i) {
-        const int sb = i & 1;
-        ok = wait(cb->info_full[i % kPagedInfo], (i / kPagedInfo) & 1);
-        if (ok) ok = wait(cb->s_full[sb], (i >> 1) & 1);
-        // (Every wait is followed by a warpgroup-wide agreement, so that no
-        // warp is left alone at a later named barrier.)
-        ok = named_bar_and(3, 128, ok);
-        if (!ok) break;
-        ptx::tc_fence_after();
-        const TileInfo& ti = cb->info[i % kPagedInfo];
+      // Rows that have seen no key yet have no maximum; while there are any
+      // (`unset`), every tile takes the slow path below.
+      bool unset = true;
+      const float* c = cb->qs[seg & 3];
+      float* end_m = cb->end_m[seg & 1][wg];
+      const int first = (i & 1) == wg ? 0 : 1;  // this warpgroup's first tile of the segment
+      for (int t = first; t < g.count; t += 2) {
+        const int at = i + t;  // tile of the CTA's range
+        const uint32_t phase = (uint32_t)(at >> 1) & 1;
+        // (A warp whose wait has given up still joins the vote below, after
+        // which the whole warpgroup leaves.)
+        if (t == first) ok = wait(cb->qs_full[seg & 3], (seg >> 2) & 1);
+        if (ok) ok = wait(cb->info_full[at % kPagedInfo], (at / kPagedInfo) & 1);
+        const TileInfo& ti = cb->info[at % kPagedInfo];
         const float ks = ti.ks[page], vs = ti.vs[page], lv = ti.lv[page];
         const bool seen = key >= ti.lo && key < ti.hi && ((ti.held >> page) & 1);
+        if (ok) ok = wait(cb->s_full[wg], phase);
+        ptx::tc_fence_after();
         float x[N];
 #pragma unroll
         for (int n0 = 0; n0 < N; n0 += 16) {
           uint32_t hi[16], lo[16];
-          ptx::tmem_ld16(tmem + lane_base + sb * 2 * N + n0, hi);
-          ptx::tmem_ld16(tmem + lane_base + sb * 2 * N + N + n0, lo);
+          ptx::tmem_ld16(s_tmem + n0, hi);
+          ptx::tmem_ld16(s_tmem + N + n0, lo);
           ptx::tmem_wait_ld();
           ptx::reg_fence16(hi);
           ptx::reg_fence16(lo);
 #pragma unroll
-          for (int n = 0; n < 16; ++n) {
-            const float s = __uint_as_float(hi[n]) + __uint_as_float(lo[n]);
-            x[n0 + n] = seen ? s * (c[n0 + n] * ks) : neg_inf;
+          for (int n = 0; n < 16; n += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(c + n0 + n);
+            x[n0 + n] = (__uint_as_float(hi[n]) + __uint_as_float(lo[n])) * (f.x * ks);
+            x[n0 + n + 1] = (__uint_as_float(hi[n + 1]) + __uint_as_float(lo[n + 1])) * (f.y * ks);
+            x[n0 + n + 2] = (__uint_as_float(hi[n + 2]) + __uint_as_float(lo[n + 2])) * (f.z * ks);
+            x[n0 + n + 3] = (__uint_as_float(hi[n + 3]) + __uint_as_float(lo[n + 3])) * (f.w * ks);
           }
         }
         ptx::tc_fence_before();
-        ptx::mbar_arrive(ptx::smem_u32(&cb->s_free[sb]));
+        ptx::mbar_arrive(ptx::smem_u32(&cb->s_free[wg]));
+        if (!seen) {
+#pragma unroll
+          for (int n = 0; n < N; ++n) x[n] = neg_inf;
+        }
         // Rows of several tokens see different keys: mask the tiles at the
         // edges row by row.
         if (tok0 != tok1) {
-          const long long j = (long long)(g.tile0 + t) * kTileKeys + key;
-          const long long j0 = j - key;
+          const long long j0 = (long long)(g.tile0 + t) * kTileKeys, j = j0 + key;
           const bool edge = (sh.causal && j0 + kTileKeys - 1 > at0) ||
                             (sh.window >= 0 && j0 < at0 + (tok1 - tok0) - sh.window);
           if (edge) {
             for (int tok = tok0; tok <= tok1; ++tok) {
-              const long long at = at0 + (tok - tok0);
-              const bool out = (sh.causal && j > at) || (sh.window >= 0 && j < at - sh.window);
+              const long long pos = at0 + (tok - tok0);
+              const bool out = (sh.causal && j > pos) || (sh.window >= 0 && j < pos - sh.window);
               if (out) {
-                const int first = tok * sh.group - row0;
+                const int lo = tok * sh.group - row0;
 #pragma unroll
                 for (int n = 0; n < N; ++n)
-                  if (n >= first && n < first + sh.group) x[n] = neg_inf;
+                  if (n >= lo && n < lo + sh.group) x[n] = neg_inf;
               }
             }
           }
         }
+        // Pt's buffer was last read by the PV of this warpgroup's last tile.
+        if (ok && at >= 2) ok = wait(cb->pv_done[wg], phase ^ 1);
         // A new maximum is due where a score passes the old one by 2^8.
-        int need = 0;
+        float over = neg_inf;
+        if (!unset) {
 #pragma unroll
-        for (int n0 = 0; n0 < N; n0 += 4) {
-          const float4 m = *reinterpret_cast<const float4*>(&cb->m_used[n0]);
-          need |= x[n0] + lv > m.x + kRescaleLog2 + kPagedBias;
-          need |= x[n0 + 1] + lv > m.y + kRescaleLog2 + kPagedBias;
-          need |= x[n0 + 2] + lv > m.z + kRescaleLog2 + kPagedBias;
-          need |= x[n0 + 3] + lv > m.w + kRescaleLog2 + kPagedBias;
+          for (int n = 0; n < N; n += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(m_used + n);
+            over = ptx::max3(over, x[n] - m.x, x[n + 1] - m.y);
+            over = ptx::max3(over, x[n + 2] - m.z, x[n + 3] - m.w);
+          }
         }
-        if (named_bar_or(2, 128, need)) {
+        const int need = unset || !ok || over + lv > kRescaleLog2 + kPagedBias;
+        if (named_bar_or(bar, 128, need)) {
+          ok = named_bar_and(bar + 1, 128, ok);
+          if (!ok) break;
           float v[N];
 #pragma unroll
           for (int n = 0; n < N; ++n) v[n] = x[n] + lv;
           warp_transpose_reduce<N, true>(v, lane);
           if ((lane & 1) == 0) {
 #pragma unroll
-            for (int k = 0; k < N / 16; ++k) cb->red[warp][16 * k + (lane >> 1)] = v[k];
+            for (int k = 0; k < N / 16; ++k) red[warp & 3][16 * k + (lane >> 1)] = v[k];
           }
-          named_bar_sync(1, 128);
-          if (tid < N) {
-            const float mt = fmaxf(fmaxf(cb->red[0][tid], cb->red[1][tid]),
-                                   fmaxf(cb->red[2][tid], cb->red[3][tid])) - kPagedBias;
-            const float mu = cb->m_used[tid];
+          named_bar_sync(bar + 2, 128);
+          int none = 0;
+          if (key < N) {
+            const float mt = fmaxf(fmaxf(red[0][key], red[1][key]),
+                                   fmaxf(red[2][key], red[3][key])) - kPagedBias;
+            const bool had = t != first && end_m[key] != neg_inf;
+            const float mu = had ? m_used[key] : neg_inf;
             float al = 1.f;
             if (mt > mu) {
-              al = mu == neg_inf ? 0.f : ptx::ex2(mu - mt);
-              cb->m_used[tid] = mt;
+              al = had ? ptx::ex2(mu - mt) : 0.f;
+              m_used[key] = mt;
+              end_m[key] = mt;
+            } else if (!had) {
+              m_used[key] = 0.f;
+              end_m[key] = neg_inf;
             }
-            cb->alpha[tid] = al;
+            none = key < rows && end_m[key] == neg_inf;
+            alpha[key] = al;
           }
-          named_bar_sync(1, 128);
+          unset = named_bar_or(bar, 128, none);
 #pragma unroll
-          for (int n = 0; n < N; ++n) l[n] *= cb->alpha[n];
-          if (t > 0) {
-            // Ot holds the segment's earlier tiles: wait for their last PV.
-            ok = wait(cb->pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1);
-            ok = named_bar_and(3, 128, ok);
-            if (!ok) break;
+          for (int n = 0; n < N; ++n) l[n] *= alpha[n];
+          if (t != first) {
+            // Ot holds this warpgroup's earlier tiles, whose last PV is done.
             ptx::tc_fence_after();
 #pragma unroll
             for (int n0 = 0; n0 < N; n0 += 16) {
               uint32_t o[16];
-              const uint32_t addr = tmem + lane_base + 4 * N + (seg & 1) * N + n0;
-              ptx::tmem_ld16(addr, o);
+              ptx::tmem_ld16(o_tmem + n0, o);
               ptx::tmem_wait_ld();
               ptx::reg_fence16(o);
 #pragma unroll
               for (int k = 0; k < 16; ++k)
-                o[k] = __float_as_uint(__uint_as_float(o[k]) * cb->alpha[n0 + k]);
-              ptx::tmem_st16(addr, o);
+                o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha[n0 + k]);
+              ptx::tmem_st16(o_tmem + n0, o);
             }
             ptx::tmem_wait_st();
           }
         }
-        // Pt row of this key.  The buffer's last reader was PV(i - 2).
-        if (i >= 2) {
-          ok = wait(cb->pv_done[sb], ((i >> 1) - 1) & 1);
-          ok = named_bar_and(3, 128, ok);
-          if (!ok) break;
-        }
-        uint8_t* prow = smem + C::kP + sb * C::kPBytes + key * C::kPRow;
+        // Pt row of this key.
 #pragma unroll
         for (int n0 = 0; n0 < N; n0 += 8) {
           uint32_t w[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float2 m = *reinterpret_cast<const float2*>(&cb->m_used[n0 + 2 * k]);
-            // (A row that has seen no key yet: its scores are -inf, and so
-            // must not meet the maximum -inf.)
-            const float p0 = ptx::ex2(x[n0 + 2 * k] - (m.x == neg_inf ? 0.f : m.x));
-            const float p1 = ptx::ex2(x[n0 + 2 * k + 1] - (m.y == neg_inf ? 0.f : m.y));
+            const float2 m = *reinterpret_cast<const float2*>(m_used + n0 + 2 * k);
+            const float p0 = ptx::ex2(x[n0 + 2 * k] - m.x);
+            const float p1 = ptx::ex2(x[n0 + 2 * k + 1] - m.y);
             l[n0 + 2 * k] += p0;
             l[n0 + 2 * k + 1] += p1;
             w[k] = ptx::pack_f16x2(p0 * vs, p1 * vs);
@@ -696,62 +732,92 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         }
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
-        ptx::mbar_arrive(ptx::smem_u32(&cb->p_full[sb]));
+        ptx::mbar_arrive(ptx::smem_u32(&cb->p_full[wg]));
       }
-      if (!ok) break;
 
       // ------------------------------------------------------ segment output
+      // (Votes and barriers of both warpgroups from here on; one that has
+      // given up joins the first.)
+      const int last = i + g.count - 1;  // of the segment's tiles
+      i += g.count;
       const bool whole = g.count == g.unit_count;
       const int slot = 2 * cta + (seg == 0 ? 0 : 1);
-      if (!whole && g.part_lo == 0 && tid == 0) {
-        // The unit starts here: tell the merge how many CTAs share it.
-        const long long unit_end = walk.at - g.count + g.unit_count;
-        int parts = 1;
-        while (cta + parts < ctas && range_start(total, ctas, cta + parts) < unit_end) ++parts;
-        a.meta[2 * cta] = make_int4(parts, g.q.lo, row0, g.head);
-        a.meta[2 * cta + 1] = make_int4(rows, slot, 0, 0);
-      }
-      warp_transpose_reduce<N, false>(l, lane);
-      if ((lane & 1) == 0) {
+      if (ok) {
+        warp_transpose_reduce<N, false>(l, lane);
+        if ((lane & 1) == 0) {
 #pragma unroll
-        for (int k = 0; k < N / 16; ++k) cb->red[warp][16 * k + (lane >> 1)] = l[k];
+          for (int k = 0; k < N / 16; ++k) red[warp & 3][16 * k + (lane >> 1)] = l[k];
+        }
+        named_bar_sync(bar + 2, 128);
+        if (key < N) {
+          cb->end_l[seg & 1][wg][key] =
+              (red[0][key] + red[1][key]) + (red[2][key] + red[3][key]);
+          if (first >= g.count) end_m[key] = neg_inf;  // no tile here
+        }
+        for (int k = 0; ok && k < 2 && k < g.count; ++k)
+          ok = wait(cb->pv_done[(last - k) & 1], ((last - k) >> 1) & 1);
       }
-      named_bar_sync(1, 128);
-      if (tid < N) {
-        const float sum = (cb->red[0][tid] + cb->red[1][tid]) + (cb->red[2][tid] + cb->red[3][tid]);
-        // (0: no key seen; a NaN stays one.)
-        cb->alpha[tid] = sum == 0.f ? 0.f : 1.f / sum;
-        const float l2 = sum == 0.f ? neg_inf : cb->m_used[tid] + log2f(sum);
-        if (tid < rows) {
+      ok = named_bar_and(4, 256, ok);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      if (key < N) {
+        // Weights of the two warpgroups' Ot: 2^(m - M) / sum; a warpgroup
+        // that saw no key has m = -inf (or a NaN sum) and nothing to add.
+        const float m0 = cb->end_m[seg & 1][0][key], m1 = cb->end_m[seg & 1][1][key];
+        const float l0 = cb->end_l[seg & 1][0][key], l1 = cb->end_l[seg & 1][1][key];
+        const float top = fmaxf(m0, m1);
+        const float base = top == neg_inf ? 0.f : top;
+        const float e0 = m0 == neg_inf ? (l0 == 0.f ? 0.f : l0) : ptx::ex2(m0 - base);
+        const float e1 = m1 == neg_inf ? (l1 == 0.f ? 0.f : l1) : ptx::ex2(m1 - base);
+        const float sum = e0 * l0 + e1 * l1;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (a NaN stays one)
+        cb->weight[wg][0][key] = e0 * inv;
+        cb->weight[wg][1][key] = e1 * inv;
+        const float l2 = sum == 0.f ? neg_inf : base + log2f(sum);
+        if (wg == 0 && key < rows) {
           if (!whole) {
-            a.part_lse[(size_t)slot * N + tid] = l2;
+            a.part_lse[(size_t)slot * N + key] = l2;
           } else if (a.lse) {
-            const int tok = (row0 + tid) / sh.group, h = (row0 + tid) - tok * sh.group;
+            const int tok = (row0 + key) / sh.group, h = (row0 + key) - tok * sh.group;
             a.lse[(size_t)(g.head * sh.group + h) * a.total_q + g.q.lo + tok] =
                 l2 * 0.69314718055994531f;
           }
         }
       }
-      named_bar_sync(1, 128);
-      ok = wait(cb->pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1);
-      ok = named_bar_and(3, 128, ok);
-      if (!ok) break;
-      ptx::tc_fence_after();
+      if (!whole && g.part_lo == 0 && tid == 0) {
+        // The unit starts here: tell the merge how many CTAs share it.
+        const int unit_end = walk.at - g.count + g.unit_count;
+        int parts = 1;
+        while (cta + parts < ctas && range_start(total, ctas, cta + parts) < unit_end) ++parts;
+        a.meta[2 * cta] = make_int4(parts, g.q.lo, row0, g.head);
+        a.meta[2 * cta + 1] = make_int4(rows, slot, 0, 0);
+      }
+      named_bar_sync(bar + 2, 128);
       // Dim of this thread's lane: row of a 128-row accumulator, or of a
       // 64-row one, which uses the first 16 lanes of each warp's 32.
-      const int d = D == 128 ? tid : warp * 16 + lane;
+      const int d = D == 128 ? key : (warp & 3) * 16 + lane;
       const bool live = d < a.dim && (D == 128 || lane < 16);
+      const uint32_t o0 = tmem + lane_base + 4 * N + (seg & 1) * 2 * N;
+      // A segment of one tile has the Ot of one warpgroup only.
+      const bool two = g.count > 1;
+      const int only = last & 1;
 #pragma unroll 1
-      for (int n0 = 0; n0 < rows; n0 += 16) {
-        uint32_t o[16];
-        ptx::tmem_ld16(tmem + lane_base + 4 * N + (seg & 1) * N + n0, o);
+      for (int n0 = 8 * wg; n0 < rows; n0 += 16) {
+        uint32_t oa[8], ob[8];
+        ptx::tmem_ld8(o0 + (two ? 0 : only * N) + n0, oa);
+        ptx::tmem_ld8(o0 + (two ? N : only * N) + n0, ob);
         ptx::tmem_wait_ld();
-        ptx::reg_fence16(o);
+        ptx::reg_fence8(oa);
+        ptx::reg_fence8(ob);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
+        for (int k = 0; k < 8; ++k) {
           const int n = n0 + k;
           if (live && n < rows) {
-            const float v = __uint_as_float(o[k]) * cb->alpha[n];
+            const float wa = cb->weight[wg][two ? 0 : only][n];
+            const float wb = two ? cb->weight[wg][1][n] : 0.f;
+            // (Weight 0: the Ot may hold anything.)
+            const float v = (wa == 0.f ? 0.f : wa * __uint_as_float(oa[k])) +
+                            (wb == 0.f ? 0.f : wb * __uint_as_float(ob[k]));
             if (whole) {
               const int tok = (row0 + n) / sh.group, h = (row0 + n) - tok * sh.group;
               a.out[((size_t)(g.q.lo + tok) * a.heads + g.head * sh.group + h) * a.dim + d] =
@@ -764,41 +830,62 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       }
       ptx::tc_fence_before();
       ptx::mbar_arrive(ptx::smem_u32(&cb->o_free[seg & 1]));
-      named_bar_sync(1, 128);  // alpha is read before the next segment writes it
     }
   }
 
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == kSWarp) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, C::kTmemCols);
   }
 }
 
-// Joins the parts of the units that CTA boundaries cut.  Block (c, y): the
-// unit that starts in CTA c and ends in a later one, rows y of it.
+// Joins the parts of the units that CTA boundaries cut.  Block (c, n): row n
+// of the unit that starts in CTA c and ends in a later one.
 // O = sum_p w_p O_p, w_p = 2^(lse_p - LSE): the parts are summed in CTA order,
-// so the result does not depend on timing.
+// so the result does not depend on timing.  A unit can have as many parts as
+// there are CTAs, so every LSE is loaded at once and eight partials at a time.
+constexpr int kPagedMaxGrid = 512;  // CTAs of an attention launch
+
 template <int D, int N>
 __global__ void __launch_bounds__(D) paged_merge_kernel(const PagedAttnArgs a) {
-  const int c = blockIdx.x, tid = threadIdx.x;
+  __shared__ float s_w[kPagedMaxGrid];
+  __shared__ float s_red[D / 32];
+  const int c = blockIdx.x, n = blockIdx.y, tid = threadIdx.x;
   ptx::grid_dependency_wait();
-  const int4 m0 = a.meta[2 * c];
-  if (m0.x == 0) return;
-  const int4 m1 = a.meta[2 * c + 1];
-  const int n = blockIdx.y;
-  if (n >= m1.x) return;
+  const int4 m0 = a.meta[2 * c], m1 = a.meta[2 * c + 1];
+  const int parts = m0.x;
+  if (parts == 0 || n >= m1.x) return;
   auto slot = [&](int p) { return p == 0 ? m1.y : 2 * (c + p); };
   const float neg_inf = -__int_as_float(0x7f800000);
   float top = neg_inf;
-  for (int p = 0; p < m0.x; ++p) top = fmaxf(top, a.part_lse[(size_t)slot(p) * N + n]);
+  for (int p = tid; p < parts; p += D) {
+    const float v = a.part_lse[(size_t)slot(p) * N + n];
+    s_w[p] = v;
+    top = fmaxf(top, v);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if ((tid & 31) == 0) s_red[tid >> 5] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < D / 32; ++w) top = fmaxf(top, s_red[w]);
   float sum = 0.f, acc = 0.f;
-  for (int p = 0; p < m0.x; ++p) {
-    const float lp = a.part_lse[(size_t)slot(p) * N + n];
-    const float w = lp == neg_inf ? 0.f : ptx::ex2(lp - top);
-    sum += w;
-    acc = fmaf(w, a.part_o[((size_t)slot(p) * N + n) * D + tid], acc);
+  for (int p0 = 0; p0 < parts; p0 += 8) {
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      v[k] = p0 + k < parts ? a.part_o[((size_t)slot(p0 + k) * N + n) * D + tid] : 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (p0 + k < parts) {
+        const float lp = s_w[p0 + k];
+        const float w = lp == neg_inf ? 0.f : ptx::ex2(lp - top);
+        sum += w;
+        acc = fmaf(w, v[k], acc);
+      }
+    }
   }
   const int row = m0.z + n, g = a.shape.group;
   const int tok = row / g, h = m0.w * g + row - tok * g;

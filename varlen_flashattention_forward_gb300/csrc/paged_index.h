@@ -110,16 +110,17 @@ struct AttnShape {
   int causal, window, held;  // held: positions of the page table
 };
 
+// n * group is at most the number of query rows of the call, below 2^31.
 FA_HD int row_tiles(const AttnShape& s, int n) {
-  return (int)(((long long)n * s.group + s.rows - 1) / s.rows);
+  return (int)(((unsigned)n * (unsigned)s.group + s.rows - 1) / (unsigned)s.rows);
 }
 // Keys of row tile t of a sequence with n query rows and len keys.
 FA_HD KeyRange tile_keys(const AttnShape& s, int t, int n, int len) {
-  const long long r0 = (long long)t * s.rows;
-  long long r1 = r0 + s.rows;
-  if (r1 > (long long)n * s.group) r1 = (long long)n * s.group;
-  return key_range((int)(r0 / s.group), (int)((r1 - 1) / s.group), n, len, s.held, s.causal != 0,
-                   s.window);
+  const unsigned r0 = (unsigned)t * s.rows, all = (unsigned)n * s.group;
+  unsigned r1 = r0 + s.rows;
+  if (r1 > all) r1 = all;
+  return key_range((int)(r0 / (unsigned)s.group), (int)((r1 - 1) / (unsigned)s.group), n, len,
+                   s.held, s.causal != 0, s.window);
 }
 // First key tile and number of key tiles; a unit without keys keeps one (all
 // masked), which writes its empty rows.
@@ -129,7 +130,7 @@ struct TileRange {
 FA_HD TileRange key_tiles(const KeyRange& k) {
   TileRange t;
   t.first = k.lo / kTileKeys;
-  t.count = k.hi > k.lo ? (int)(((long long)k.hi + kTileKeys - 1) / kTileKeys) - t.first : 1;
+  t.count = k.hi > k.lo ? (int)(((unsigned)k.hi + kTileKeys - 1) / kTileKeys) - t.first : 1;
   return t;
 }
 // Key tiles of all row tiles of one (sequence, head).
@@ -140,16 +141,22 @@ FA_HD long long head_tiles(const AttnShape& s, int n, int len) {
   return sum;
 }
 
+// Tile numbers are 32-bit.  The host splits a batch so that those of a launch
+// stay below 2^31 where cu_seqlens is well formed; a count past that (from
+// overlapping sequences) stops at the limit, and tiles past it are not done.
+constexpr int kMaxTiles = 0x7fffffff;
+FA_HD int capped_tiles(long long n) { return n < kMaxTiles ? (int)n : kMaxTiles; }
+
 // Start of CTA c's range of `total` tiles among `ctas`: the first
 // total % ctas ranges are one tile longer.
-FA_HD long long range_start(long long total, int ctas, int c) {
-  const long long q = total / ctas, r = total % ctas;
+FA_HD int range_start(int total, int ctas, int c) {
+  const int q = (int)((unsigned)total / (unsigned)ctas), r = total - q * ctas;
   return c * q + (c < r ? c : r);
 }
 
 // Walks the segments of a range: the part of each unit's tiles inside it.
-// before[b] is the number of tiles of the sequences before b (batch + 1
-// entries).
+// before(b) is the number of tiles of the sequences before b (b up to the
+// batch).
 struct Segment {
   int seq, head, row_tile;
   RowRange q;        // the sequence's query rows
@@ -160,13 +167,13 @@ struct Segment {
   int part_lo, unit_count;  // place of tile0 among the unit's tiles, and their number
 };
 struct SegmentWalk {
-  long long at, end;  // tiles done, end of the range
+  int at, end;  // tiles done, end of the range
   int seq, head, row_tile;
-  long long in_unit;  // tiles of the current unit that are done
+  int in_unit;  // tiles of the current unit that are done
 };
 
 template <typename Before>
-FA_HD void walk_begin(SegmentWalk* w, long long lo, long long hi, int batch, const Before& before) {
+FA_HD void walk_begin(SegmentWalk* w, int lo, int hi, int batch, const Before& before) {
   w->at = lo;
   w->end = hi;
   int a = 0, b = batch;  // before(a) <= lo < before(b)
@@ -189,10 +196,10 @@ FA_HD bool walk_next(SegmentWalk* w, const AttnShape& s, const Before& before, c
   if (w->head < 0) {
     while (before(w->seq + 1) <= w->at) ++w->seq;  // sequences without query rows
     seq_of(w->seq, &g->q, &g->len);
-    const long long in_seq = w->at - before(w->seq);
-    const long long per_head = (before(w->seq + 1) - before(w->seq)) / s.heads_k;
-    w->head = (int)(in_seq / per_head);
-    long long left = in_seq - w->head * per_head;
+    const int in_seq = w->at - before(w->seq);
+    const int per_head = capped_tiles(head_tiles(s, g->q.n, g->len));
+    w->head = (int)((unsigned)in_seq / (unsigned)per_head);
+    int left = in_seq - w->head * per_head;
     w->row_tile = 0;
     for (;;) {
       const int c = key_tiles(tile_keys(s, w->row_tile, g->q.n, g->len)).count;
@@ -209,11 +216,11 @@ FA_HD bool walk_next(SegmentWalk* w, const AttnShape& s, const Before& before, c
   g->row_tile = w->row_tile;
   g->keys = tile_keys(s, w->row_tile, g->q.n, g->len);
   const TileRange t = key_tiles(g->keys);
-  long long n = t.count - w->in_unit;
+  int n = t.count - w->in_unit;
   if (n > w->end - w->at) n = w->end - w->at;
-  g->tile0 = t.first + (int)w->in_unit;
-  g->count = (int)n;
-  g->part_lo = (int)w->in_unit;
+  g->tile0 = t.first + w->in_unit;
+  g->count = n;
+  g->part_lo = w->in_unit;
   g->unit_count = t.count;
   w->at += n;
   w->in_unit += n;
