@@ -29,10 +29,14 @@
 // maximum m is taken over x', so that P' = 2^(x' - m + 7) stays below 2^15;
 // the row sum adds 2^(x - m + 7).
 //
-//   producer warp       walks the segments, loads page ids and scales ahead,
-//                       and TMA-loads the pages of each tile (128-byte
-//                       swizzle; 64-byte at dim 64) into a K and a V ring;
-//   Q warp              splits each segment's rows into hi and lo;
+//   planner warp        walks the segments, publishes each one with its first
+//                       page ids and scales in a ring that the other warps
+//                       read, and splits its rows of Q into hi and lo; it
+//                       runs ahead, so that short segments do not wait for
+//                       its chain of dependent loads;
+//   producer warp       TMA-loads the pages of each tile (128-byte swizzle;
+//                       64-byte at dim 64) into a K and a V ring, with the
+//                       next page ids and scales of long segments under way;
 //   S issuer warp       St(i) as soon as K(i) has landed;
 //   converter warps     V(i) to f16, rows nobody sees as zeros (they may hold
 //                       anything, and 0 * NaN is NaN);
@@ -64,7 +68,7 @@
 namespace fa {
 
 // Warps 0-7 softmax, 8-11 converters, 12 S issuer, 13 PV issuer, 14 producer,
-// 15 Q.
+// 15 planner.
 constexpr int kPagedThreads = 512;
 constexpr int kConvertWarp = 8, kSWarp = 12, kPvWarp = 13, kLoadWarp = 14;
 // Register split (launch: 128 x 512 = 65536): softmax 256 x 160, converters
@@ -74,6 +78,9 @@ constexpr uint32_t kPagedConvertRegs = 80;
 constexpr uint32_t kPagedControlRegs = 96;
 constexpr int kPagedMaxBatch = 1024;  // sequences of one launch
 constexpr int kPagedInfo = 8;         // tile descriptors in flight
+constexpr int kPagedPlans = 4;        // segment descriptors in flight
+constexpr int kPlanReaders = 15;      // warps that read them
+constexpr int kPlanTiles = 16;        // tiles whose pages are looked up at once
 constexpr float kPagedBias = 7.f;     // P' is held times 2^7
 
 struct PagedAttnArgs {
@@ -103,6 +110,21 @@ struct TileInfo {
   int held;                   // bit p: page p of the tile is in the cache
 };
 
+// One segment, for every warp; count = 0 ends the range.
+struct SegPlan {
+  int count, tile0;            // key tiles
+  int lo, hi;                  // keys that some row sees
+  int seq, head;
+  int q0, row0, rows;          // the sequence's first q row; rows of the tile
+  int tok0, tok1;              // tokens of its first and last row
+  long long at0;               // position of tok0
+  int whole;                   // covers its unit
+  int unit_end;                // where the unit starts in this segment but does
+                               // not end: the tile number behind it, else -1
+  int id[2 * kPlanTiles];      // pages of the first tiles (-1: none)
+  float ks[2 * kPlanTiles], vs[2 * kPlanTiles];
+};
+
 template <int D, int N>
 struct PagedCfg {
   static constexpr int kRow = D;                       // bytes of a K or V row
@@ -114,7 +136,8 @@ struct PagedCfg {
   static constexpr int kPBytes = kTileKeys * kPRow;
   static constexpr int kQBytes = 2 * N * kRow;
   static constexpr int NK = N == 64 ? 3 : 4;
-  static constexpr int NV = N == 64 ? 2 : N == 32 ? 3 : 4;
+  static constexpr int NV = N == 64 ? 2 : 3;
+  static constexpr int NQ = N == 16 ? 4 : 2;
   static constexpr uint32_t kSwP = N == 64   ? ptx::kLayoutSw128
                                    : N == 32 ? ptx::kLayoutSw64
                                              : ptx::kLayoutSw32;
@@ -125,33 +148,36 @@ struct PagedCfg {
   static constexpr int kVh = kV + NV * kTileBytes;
   static constexpr int kP = kVh + 2 * kVhBytes;
   static constexpr int kQ = kP + 2 * kPBytes;
-  static constexpr int kCtl = kQ + 2 * kQBytes;
+  static constexpr int kCtl = kQ + NQ * kQBytes;
 };
 
 struct alignas(16) PagedCtl {
+  uint64_t plan_full[kPagedPlans], plan_free[kPagedPlans];  // segment published / read (15)
+  uint64_t scale_full[kPagedPlans];                         // its scales too
   uint64_t k_full[4], k_free[4];    // K slot landed (TMA bytes) / read by its S MMA
   uint64_t v_full[4], v_free[4];    // V slot landed / converted (128 arrivals)
   uint64_t info_full[kPagedInfo];
   uint64_t vh_full[2];              // f16 V written (128)
   uint64_t s_full[2], s_free[2];    // St computed / loaded (128)
   uint64_t p_full[2], pv_done[2];   // Pt written (128) / PV complete
-  uint64_t q_full[2], q_free[2];    // Q terms written (32) / last S of the segment
-  uint64_t qs_full[4];              // row scales written (32)
-  uint64_t o_free[2];               // Ot of a segment read out (256)
+  uint64_t q_full[4], q_free[4];    // Q terms written (32) / last S of the segment
+  uint64_t qs_full[kPagedPlans];    // row scales written (32)
+  uint64_t o_free[2];               // Ot of a segment read out (8 warps)
   uint64_t drain, drain_pv;         // everything an issuer started is complete
   uint32_t tmem_base;
   volatile int abort_flag;
   TileInfo info[kPagedInfo];
-  alignas(16) float qs[4][64];      // row scale * softmax scale * log2(e)
+  SegPlan plan[kPagedPlans];
+  alignas(16) float qs[kPagedPlans][64];      // row scale * softmax scale * log2(e)
   // Per softmax warpgroup: per-warp partial maxima or sums, the running
   // maximum less the bias (0 while no key was seen), rescale factors.
   alignas(16) float red[2][4][64];
   alignas(16) float m_used[2][64];
   alignas(16) float alpha[2][64];
-  // By segment parity and warpgroup: maximum so far (-inf: no key seen) and,
-  // at the segment's end, the sum.  (Two copies: a warpgroup may begin the
-  // next segment while the other still joins this one.)
-  float end_m[2][2][64], end_l[2][2][64];
+  // By segment (mod 4) and warpgroup: maximum so far (-inf: no key seen) and,
+  // at the segment's end, the sum.  (A warpgroup may be up to three segments
+  // ahead of the other, which still reads these.)
+  float end_m[kPagedPlans][2][64], end_l[kPagedPlans][2][64];
   float weight[2][2][64];            // [reader][warpgroup] factors of its Ot
   long long warp_tiles[kPagedThreads / 32];
   int before[kPagedMaxBatch + 1];
@@ -192,6 +218,17 @@ __device__ __forceinline__ void warp_transpose_reduce(float* v, int lane) {
   }
 }
 
+// Page `lane` of the tiles from `tile` on, `count` of which are left: its id,
+// or -1 where it is not needed or not in the cache.
+__device__ __forceinline__ int page_for(const PagedAttnArgs& a, const int* table, int tile,
+                                        int count, int lane, int key_lo, int key_hi) {
+  const int p = tile * 2 + lane;
+  if (lane / 2 >= count || (long long)p * kPageTokens >= key_hi ||
+      (long long)(p + 1) * kPageTokens <= key_lo)
+    return -1;
+  return checked_page(__ldg(table + p), a.num_pages);
+}
+
 template <int D, int N>
 __global__ void __launch_bounds__(kPagedThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap k_map,
@@ -213,10 +250,15 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   if (tid == 0) {
     auto init = [&](uint64_t& b, uint32_t n) { ptx::mbar_init(ptx::smem_u32(&b), n); };
     for (int s = 0; s < 4; ++s) {
+      init(cb->plan_full[s], 1);
+      init(cb->plan_free[s], kPlanReaders);
+      init(cb->scale_full[s], 1);
       init(cb->k_full[s], 1);
       init(cb->k_free[s], 1);
       init(cb->v_full[s], 1);
       init(cb->v_free[s], 128);
+      init(cb->q_full[s], 32);
+      init(cb->q_free[s], 1);
       init(cb->qs_full[s], 32);
     }
     for (int s = 0; s < kPagedInfo; ++s) init(cb->info_full[s], 1);
@@ -226,9 +268,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       init(cb->s_free[s], 128);
       init(cb->p_full[s], 128);
       init(cb->pv_done[s], 1);
-      init(cb->q_full[s], 32);
-      init(cb->q_free[s], 1);
-      init(cb->o_free[s], 256);
+      init(cb->o_free[s], 8);
     }
     init(cb->drain, 1);
     init(cb->drain_pv, 1);
@@ -284,13 +324,19 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   auto before = [&](int b) { return cb->before[b]; };
   const int total = cb->before[a.batch];
   const int cta = blockIdx.x, ctas = gridDim.x;
-  SegmentWalk walk;
-  walk_begin(&walk, range_start(total, ctas, cta), range_start(total, ctas, cta + 1), a.batch,
-             before);
-  Segment g;
   // Slot n of a ring of size R: slot n % R, phase parity (n / R) & 1.
   auto wait = [&](uint64_t& b, int parity) {
     return wait_warp(ptx::smem_u32(&b), (uint32_t)parity, abort_flag, a.status, a.wait_limit_ns);
+  };
+  // The descriptor of segment number seg; every warp that reads it lets it go
+  // with plan_done once it has what it needs.
+  auto plan_of = [&](int seg, bool* ok) -> const SegPlan& {
+    *ok = wait(cb->plan_full[seg % kPagedPlans], (seg / kPagedPlans) & 1);
+    return cb->plan[seg % kPagedPlans];
+  };
+  auto plan_done = [&](int seg) {
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->plan_free[seg % kPagedPlans]));
   };
 
   if (warp >= kConvertWarp && warp < kSWarp) {
@@ -306,10 +352,16 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     const int u4 = t & 3, odd = (t >> 2) & 1, group = t >> 3;
     bool ok = true;
     int i = 0;
-    while (ok && walk_next(&walk, sh, before, seq_of, &g)) {
-      for (int n = 0; n < g.count; ++n, ++i) {
+    for (int seg = 0; ok; ++seg) {
+      const SegPlan& plan = plan_of(seg, &ok);
+      if (!ok) break;
+      const int count = plan.count;
+      plan_done(seg);
+      if (count == 0) break;
+      for (int n = 0; n < count; ++n, ++i) {
         const int slot = i % C::NV, hb = i & 1;
         ok = wait(cb->v_full[slot], (i / C::NV) & 1);
+        if (ok) ok = wait(cb->info_full[i % kPagedInfo], (i / kPagedInfo) & 1);
         if (!ok) break;
         const TileInfo& ti = cb->info[i % kPagedInfo];
         const int lo = ti.lo, hi = ti.hi, held = ti.held;
@@ -362,12 +414,18 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       constexpr uint32_t idesc = ptx::idesc_e4m3_f32(128, 2 * N);
       bool ok = true;
       int i = 0;
-      for (int seg = 0; ok && walk_next(&walk, sh, before, seq_of, &g); ++seg) {
-        ok = wait(cb->q_full[seg & 1], (seg >> 1) & 1);
+      for (int seg = 0; ok; ++seg) {
+        const SegPlan& plan = plan_of(seg, &ok);
         if (!ok) break;
-        const uint64_t qd = ptx::smem_desc(ptx::smem_u32(smem + C::kQ + (seg & 1) * C::kQBytes), 16,
+        const int count = plan.count;
+        plan_done(seg);
+        if (count == 0) break;
+        const int qb = seg % C::NQ;
+        ok = wait(cb->q_full[qb], (seg / C::NQ) & 1);
+        if (!ok) break;
+        const uint64_t qd = ptx::smem_desc(ptx::smem_u32(smem + C::kQ + qb * C::kQBytes), 16,
                                            8 * C::kRow, C::kSwK);
-        for (int n = 0; n < g.count; ++n, ++i) {
+        for (int n = 0; n < count; ++n, ++i) {
           const int slot = i % C::NK;
           ok = wait(cb->k_full[slot], (i / C::NK) & 1);
           if (ok && i >= 2) ok = wait(cb->s_free[i & 1], ((i >> 1) - 1) & 1);
@@ -381,7 +439,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
           ptx::mma_commit_elect(ptx::smem_u32(&cb->k_free[slot]));
         }
         if (!ok) break;
-        ptx::mma_commit_elect(ptx::smem_u32(&cb->q_free[seg & 1]));
+        ptx::mma_commit_elect(ptx::smem_u32(&cb->q_free[qb]));
       }
       ptx::mma_commit_elect(ptx::smem_u32(&cb->drain));
       wait_drain_warp(ptx::smem_u32(&cb->drain), 0, a.status);
@@ -390,9 +448,14 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       constexpr uint32_t idesc = ptx::idesc_f16_f32(D, N, true, true);
       bool ok = true;
       int i = 0;
-      for (int seg = 0; ok && walk_next(&walk, sh, before, seq_of, &g); ++seg) {
+      for (int seg = 0; ok; ++seg) {
+        const SegPlan& plan = plan_of(seg, &ok);
+        if (!ok) break;
+        const int count = plan.count;
+        plan_done(seg);
+        if (count == 0) break;
         if (seg >= 2) ok = wait(cb->o_free[seg & 1], ((seg >> 1) - 1) & 1);
-        for (int n = 0; ok && n < g.count; ++n, ++i) {
+        for (int n = 0; ok && n < count; ++n, ++i) {
           const int hb = i & 1;
           ok = wait(cb->vh_full[hb], (i >> 1) & 1);
           if (ok) ok = wait(cb->p_full[hb], (i >> 1) & 1);
@@ -417,69 +480,78 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       test_load_delay(a.wait_limit_ns);
       bool ok = true;
       int i = 0, kn = 0, vn = 0;  // tiles; K and V loads issued
-      while (ok && walk_next(&walk, sh, before, seq_of, &g)) {
-        const int* table = a.page_table + (size_t)g.seq * a.max_pages;
-        // Lane l holds page l of a batch of 16 tiles: its id, or -1 where the
-        // tile needs no such page, and its scales.
-        int id = -1;
-        float ks = 0.f, vs = 0.f, lv = 0.f;
-        for (int n = 0; n < g.count; ++n, ++i) {
-          if (n % 16 == 0) {
-            const int p = (g.tile0 + n) * 2 + lane;
-            id = -1;
-            ks = vs = 0.f;
-            lv = -kScaleExpMax;
-            if (n + lane / 2 < g.count && p * (long long)kPageTokens < g.keys.hi &&
-                (p + 1) * (long long)kPageTokens > g.keys.lo)
-              id = checked_page(__ldg(table + p), a.num_pages);
-            if (id >= 0) {
-              const size_t cell = (size_t)id * sh.heads_k + g.head;
-              ks = __ldg(a.k_scale + cell);
-              vs = __ldg(a.v_scale + cell);
-              lv = fmaxf(log2f(vs), -(float)kScaleExpMax);
-            }
+      for (int seg = 0; ok; ++seg) {
+        const SegPlan& plan = plan_of(seg, &ok);
+        if (!ok) break;
+        const int count = plan.count, tile0 = plan.tile0, key_lo = plan.lo, key_hi = plan.hi;
+        const int head = plan.head;
+        const int* table = a.page_table + (size_t)plan.seq * a.max_pages;
+        // Lane l holds page l of kPlanTiles tiles: its id, or -1 where the
+        // tile needs no such page, and its scales; next_* those of the tiles
+        // after them, the ids asked for at the first tile, the scales halfway.
+        int id = plan.id[lane], next_id = -1;
+        float ks = 0.f, vs = 0.f, next_ks = 0.f, next_vs = 0.f;
+        if (count == 0) {
+          plan_done(seg);
+          break;
+        }
+        for (int n = 0; n < count; ++n, ++i) {
+          const int in = n % kPlanTiles;
+          if (n > 0 && in == 0) {
+            id = next_id;
+            ks = next_ks;
+            vs = next_vs;
           }
-          const int l0 = (n % 16) * 2;
-          const int id0 = __shfl_sync(0xffffffffu, id, l0), id1 = __shfl_sync(0xffffffffu, id, l0 + 1);
-          const int ks_slot = i % C::NK, vs_slot = i % C::NV;
-          if (i >= C::NK) ok = wait(cb->k_free[ks_slot], (i / C::NK - 1) & 1);
-          if (!ok) break;
-          TileInfo* ti = &cb->info[i % kPagedInfo];
-          if ((lane & ~1) == l0) {
-            ti->ks[lane & 1] = ks;
-            ti->vs[lane & 1] = vs;
-            ti->lv[lane & 1] = lv;
+          if (in == 0 && n + kPlanTiles < count)
+            next_id = page_for(a, table, tile0 + n + kPlanTiles, count - n - kPlanTiles, lane,
+                               key_lo, key_hi);
+          if (in == kPlanTiles / 2 && n + kPlanTiles / 2 < count) {
+            next_ks = next_id >= 0 ? __ldg(a.k_scale + (size_t)next_id * sh.heads_k + head) : 0.f;
+            next_vs = next_id >= 0 ? __ldg(a.v_scale + (size_t)next_id * sh.heads_k + head) : 0.f;
           }
+          const int id0 = __shfl_sync(0xffffffffu, id, 2 * in);
+          const int id1 = __shfl_sync(0xffffffffu, id, 2 * in + 1);
           const int held = (id0 >= 0 ? 1 : 0) | (id1 >= 0 ? 2 : 0);
           const uint32_t bytes = ((held & 1) + (held >> 1)) * C::kPageBytes;
+          auto load = [&](const CUtensorMap* map, uint64_t& full, uint8_t* slot) {
+            if (lane == 0) {
+              const uint32_t bar = ptx::smem_u32(&full), dst = ptx::smem_u32(slot);
+              ptx::mbar_arrive_expect_tx(bar, bytes);
+              if (id0 >= 0) ptx::tma_load_3d(dst, map, bar, 0, 0, id0 * sh.heads_k + head);
+              if (id1 >= 0)
+                ptx::tma_load_3d(dst + C::kPageBytes, map, bar, 0, 0, id1 * sh.heads_k + head);
+            }
+          };
+          const int sk = i % C::NK, sv = i % C::NV;
+          if (i >= C::NK) ok = wait(cb->k_free[sk], (i / C::NK - 1) & 1);
+          if (!ok) break;
+          load(&k_map, cb->k_full[sk], smem + C::kK + sk * C::kTileBytes);
+          ++kn;
+          if (i >= C::NV) ok = wait(cb->v_free[sv], (i / C::NV - 1) & 1);
+          if (!ok) break;
+          load(&v_map, cb->v_full[sv], smem + C::kV + sv * C::kTileBytes);
+          ++vn;
+          if (n == 0) {
+            ok = wait(cb->scale_full[seg % kPagedPlans], (seg / kPagedPlans) & 1);
+            if (!ok) break;
+            ks = plan.ks[lane];
+            vs = plan.vs[lane];
+            plan_done(seg);
+          }
+          TileInfo* ti = &cb->info[i % kPagedInfo];
+          if ((lane >> 1) == in) {
+            ti->ks[lane & 1] = ks;
+            ti->vs[lane & 1] = vs;
+            ti->lv[lane & 1] = fmaxf(log2f(vs), -(float)kScaleExpMax);
+          }
           if (lane == 0) {
-            const long long key0 = (long long)(g.tile0 + n) * kTileKeys;
-            ti->lo = (int)(g.keys.lo > key0 ? g.keys.lo - key0 : 0);
-            ti->hi = (int)(g.keys.hi < key0 + kTileKeys ? g.keys.hi - key0 : kTileKeys);
+            const int key0 = (tile0 + n) * kTileKeys;
+            ti->lo = imax(key_lo - key0, 0);
+            ti->hi = imin(key_hi - key0, kTileKeys);
             ti->held = held;
           }
           __syncwarp();
-          if (lane == 0) {
-            ptx::mbar_arrive(ptx::smem_u32(&cb->info_full[i % kPagedInfo]));
-            const uint32_t bar = ptx::smem_u32(&cb->k_full[ks_slot]);
-            const uint32_t dst = ptx::smem_u32(smem + C::kK + ks_slot * C::kTileBytes);
-            ptx::mbar_arrive_expect_tx(bar, bytes);
-            if (id0 >= 0) ptx::tma_load_3d(dst, &k_map, bar, 0, 0, id0 * sh.heads_k + g.head);
-            if (id1 >= 0)
-              ptx::tma_load_3d(dst + C::kPageBytes, &k_map, bar, 0, 0, id1 * sh.heads_k + g.head);
-          }
-          ++kn;
-          if (i >= C::NV) ok = wait(cb->v_free[vs_slot], (i / C::NV - 1) & 1);
-          if (!ok) break;
-          if (lane == 0) {
-            const uint32_t bar = ptx::smem_u32(&cb->v_full[vs_slot]);
-            const uint32_t dst = ptx::smem_u32(smem + C::kV + vs_slot * C::kTileBytes);
-            ptx::mbar_arrive_expect_tx(bar, bytes);
-            if (id0 >= 0) ptx::tma_load_3d(dst, &v_map, bar, 0, 0, id0 * sh.heads_k + g.head);
-            if (id1 >= 0)
-              ptx::tma_load_3d(dst + C::kPageBytes, &v_map, bar, 0, 0, id1 * sh.heads_k + g.head);
-          }
-          ++vn;
+          if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->info_full[i % kPagedInfo]));
         }
       }
       // Every copy this CTA started lands before it exits.
@@ -488,31 +560,88 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       for (int s = 0; s < C::NV && s < vn; ++s)
         wait_drain_warp(ptx::smem_u32(&cb->v_full[s]), ((vn - 1 - s) / C::NV) & 1, a.status);
     } else {
-      // ------------------------------------------------------------ Q warp
-      constexpr int kLanes = D / 8;           // lanes of a row, 8 dims each
-      constexpr int kGroups = 32 / kLanes;
+      // ----------------------------------------------------------- planner
+      constexpr int kLanes = D / 8;           // lanes of a Q row, 8 dims each
+      constexpr int kGroups = 32 / kLanes;    // rows at once
+      constexpr int kBatch = N == 16 ? N / kGroups : 4;  // loads in flight
       const int sub = lane % kLanes, dim0 = sub * 8;
+      SegmentWalk walk;
+      walk_begin(&walk, range_start(total, ctas, cta), range_start(total, ctas, cta + 1), a.batch,
+                 before);
+      Segment g = {};
+      auto pages = [&]() {
+        return page_for(a, a.page_table + (size_t)g.seq * a.max_pages, g.tile0, g.count, lane,
+                        g.keys.lo, g.keys.hi);
+      };
+      bool more = walk_next(&walk, sh, before, seq_of, &g);
+      int id = more ? pages() : -1;
       bool ok = true;
-      for (int seg = 0; ok && walk_next(&walk, sh, before, seq_of, &g); ++seg) {
-        if (seg >= 2) ok = wait(cb->q_free[seg & 1], ((seg >> 1) - 1) & 1);
+      for (int seg = 0;; ++seg) {
+        const int slot = seg % kPagedPlans;
+        if (seg >= kPagedPlans) ok = wait(cb->plan_free[slot], (seg / kPagedPlans - 1) & 1);
         if (!ok) break;
-        const int row0 = g.row_tile * N;
-        const int rows = imin(N, g.q.n * sh.group - row0);
-        uint8_t* q_s = smem + C::kQ + (seg & 1) * C::kQBytes;  // N rows of hi, N of lo
-        constexpr int kBatch = 4;
-        for (int j0 = 0; j0 < N; j0 += kGroups * kBatch) {
-          uint4 raw[kBatch];
+        SegPlan& plan = cb->plan[slot];
+        if (!more) {
+          if (lane == 0) {
+            plan.count = 0;
+            ptx::mbar_arrive(ptx::smem_u32(&cb->plan_full[slot]));
+          }
+          break;
+        }
+        const int head = g.head, group = sh.group, q0 = g.q.lo;
+        const int row0 = g.row_tile * N, rows = imin(N, g.q.n * group - row0);
+        plan.id[lane] = id;
+        if (lane == 0) {
+          plan.count = g.count;
+          plan.tile0 = g.tile0;
+          plan.lo = g.keys.lo;
+          plan.hi = g.keys.hi;
+          plan.seq = g.seq;
+          plan.head = head;
+          plan.q0 = q0;
+          plan.row0 = row0;
+          plan.rows = rows;
+          plan.tok0 = row0 / group;
+          plan.tok1 = (row0 + rows - 1) / group;
+          plan.at0 = (long long)g.len - g.q.n + plan.tok0;
+          plan.whole = g.count == g.unit_count;
+          plan.unit_end =
+              g.part_lo == 0 && g.count < g.unit_count ? walk.at - g.count + g.unit_count : -1;
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->plan_full[slot]));
+        // Scales and the first rows of Q under way, then the next segment's
+        // pages.
+        const size_t cell = (size_t)imax(id, 0) * sh.heads_k + head;
+        const float ks = id >= 0 ? __ldg(a.k_scale + cell) : 0.f;
+        const float vs = id >= 0 ? __ldg(a.v_scale + cell) : 0.f;
+        uint4 raw[kBatch];
+        auto load_rows = [&](int j0) {
 #pragma unroll
           for (int j = 0; j < kBatch; ++j) {
             const int n = j0 + j * kGroups + lane / kLanes;
             raw[j] = make_uint4(0u, 0u, 0u, 0u);
             if (n < rows && dim0 < a.dim) {
-              const int tok = (row0 + n) / sh.group, h = (row0 + n) - tok * sh.group;
+              const int tok = (row0 + n) / group, h = (row0 + n) - tok * group;
               raw[j] = __ldg(reinterpret_cast<const uint4*>(
-                  a.q + (long long)(g.q.lo + tok) * a.q_row +
-                  (long long)(g.head * sh.group + h) * a.q_head + dim0));
+                  a.q + (long long)(q0 + tok) * a.q_row + (long long)(head * group + h) * a.q_head +
+                  dim0));
             }
           }
+        };
+        load_rows(0);
+        more = walk_next(&walk, sh, before, seq_of, &g);
+        id = more ? pages() : -1;
+        plan.ks[lane] = ks;
+        plan.vs[lane] = vs;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->scale_full[slot]));
+        const int qb = seg % C::NQ;
+        if (seg >= C::NQ) ok = wait(cb->q_free[qb], (seg / C::NQ - 1) & 1);
+        if (!ok) break;
+        uint8_t* q_s = smem + C::kQ + qb * C::kQBytes;  // N rows of hi, N of lo
+        for (int j0 = 0; j0 < N; j0 += kGroups * kBatch) {
+          if (j0 > 0) load_rows(j0);
 #pragma unroll
           for (int j = 0; j < kBatch; ++j) {
             const int n = j0 + j * kGroups + lane / kLanes;
@@ -552,15 +681,15 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             *reinterpret_cast<uint2*>(q_s + place(N + n)) =
                 make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
             if (sub == 0)
-              cb->qs[seg & 3][n] =
+              cb->qs[seg % kPagedPlans][n] =
                   mx < __int_as_float(0x7f800000)
                       ? a.scale_log2 * __uint_as_float((uint32_t)(e - 7 + 127) << 23)
                       : __int_as_float(0x7fffffff);
           }
         }
         ptx::fence_proxy_async_smem();
-        ptx::mbar_arrive(ptx::smem_u32(&cb->qs_full[seg & 3]));
-        ptx::mbar_arrive(ptx::smem_u32(&cb->q_full[seg & 1]));
+        ptx::mbar_arrive(ptx::smem_u32(&cb->qs_full[slot]));
+        ptx::mbar_arrive(ptx::smem_u32(&cb->q_full[qb]));
       }
     }
   } else {
@@ -580,26 +709,40 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     float l[N];
     bool ok = true;
     int i = 0;          // tiles before the segment
-    for (int seg = 0; ok && walk_next(&walk, sh, before, seq_of, &g); ++seg) {
-      const int row0 = g.row_tile * N;
-      const int rows = imin(N, g.q.n * sh.group - row0);
-      const int tok0 = row0 / sh.group, tok1 = (row0 + rows - 1) / sh.group;
-      const long long at0 = (long long)g.len - g.q.n + tok0;  // position of the first row
+    for (int seg = 0; ok; ++seg) {
+      const SegPlan& plan = plan_of(seg, &ok);
+      const int count = plan.count, tile0 = plan.tile0, q0 = plan.q0, head = plan.head;
+      const int row0 = plan.row0, rows = plan.rows, tok0 = plan.tok0, tok1 = plan.tok1;
+      const int whole = plan.whole, unit_end = plan.unit_end;
+      const long long at0 = plan.at0;
+      // (A warpgroup goes through a segment as one.)
+      ok = named_bar_and(bar + 1, 128, ok);
+      if (!ok) break;
+      if (count == 0) break;
       const uint32_t o_tmem = tmem + lane_base + 4 * N + (seg & 1) * 2 * N + wg * N;
+      const int first = (i & 1) == wg ? 0 : 1;  // this warpgroup's first tile of the segment
+      const int last = i + count - 1;           // of the segment's tiles
+      // A segment of one tile is its warpgroup's alone; the other one goes on
+      // to the next.
+      const bool alone = count == 1;
+      if (alone && first != 0) {
+        plan_done(seg);
+        ++i;
+        continue;
+      }
 #pragma unroll
       for (int n = 0; n < N; ++n) l[n] = 0.f;
       // Rows that have seen no key yet have no maximum; while there are any
       // (`unset`), every tile takes the slow path below.
       bool unset = true;
-      const float* c = cb->qs[seg & 3];
-      float* end_m = cb->end_m[seg & 1][wg];
-      const int first = (i & 1) == wg ? 0 : 1;  // this warpgroup's first tile of the segment
-      for (int t = first; t < g.count; t += 2) {
+      const float* c = cb->qs[seg % kPagedPlans];
+      float* end_m = cb->end_m[seg % kPagedPlans][wg];
+      for (int t = first; t < count; t += 2) {
         const int at = i + t;  // tile of the CTA's range
         const uint32_t phase = (uint32_t)(at >> 1) & 1;
         // (A warp whose wait has given up still joins the vote below, after
         // which the whole warpgroup leaves.)
-        if (t == first) ok = wait(cb->qs_full[seg & 3], (seg >> 2) & 1);
+        if (t == first) ok = wait(cb->qs_full[seg % kPagedPlans], (seg / kPagedPlans) & 1);
         if (ok) ok = wait(cb->info_full[at % kPagedInfo], (at / kPagedInfo) & 1);
         const TileInfo& ti = cb->info[at % kPagedInfo];
         const float ks = ti.ks[page], vs = ti.vs[page], lv = ti.lv[page];
@@ -633,8 +776,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         // Rows of several tokens see different keys: mask the tiles at the
         // edges row by row.
         if (tok0 != tok1) {
-          const long long j0 = (long long)(g.tile0 + t) * kTileKeys, j = j0 + key;
-          const bool edge = (sh.causal && j0 + kTileKeys - 1 > at0) ||
+          const long long j0 = (long long)(tile0 + t) * kTileKeys, j = j0 + key;
+          const bool edge = (sh.causal && j0 > at0 - (kTileKeys - 1)) ||
                             (sh.window >= 0 && j0 < at0 + (tok1 - tok0) - sh.window);
           if (edge) {
             for (int tok = tok0; tok <= tok1; ++tok) {
@@ -736,11 +879,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       }
 
       // ------------------------------------------------------ segment output
-      // (Votes and barriers of both warpgroups from here on; one that has
-      // given up joins the first.)
-      const int last = i + g.count - 1;  // of the segment's tiles
-      i += g.count;
-      const bool whole = g.count == g.unit_count;
+      // (A warpgroup that has given up joins the first barrier.)
+      i += count;
       const int slot = 2 * cta + (seg == 0 ? 0 : 1);
       if (ok) {
         warp_transpose_reduce<N, false>(l, lane);
@@ -748,23 +888,23 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
 #pragma unroll
           for (int k = 0; k < N / 16; ++k) red[warp & 3][16 * k + (lane >> 1)] = l[k];
         }
-        named_bar_sync(bar + 2, 128);
-        if (key < N) {
-          cb->end_l[seg & 1][wg][key] =
-              (red[0][key] + red[1][key]) + (red[2][key] + red[3][key]);
-          if (first >= g.count) end_m[key] = neg_inf;  // no tile here
-        }
-        for (int k = 0; ok && k < 2 && k < g.count; ++k)
+        for (int k = 0; ok && k < 2 && k < count; ++k)
           ok = wait(cb->pv_done[(last - k) & 1], ((last - k) >> 1) & 1);
+        named_bar_sync(bar + 2, 128);
+        if (key < N)
+          cb->end_l[seg % kPagedPlans][wg][key] =
+              (red[0][key] + red[1][key]) + (red[2][key] + red[3][key]);
       }
-      ok = named_bar_and(4, 256, ok);
+      ok = alone ? named_bar_and(bar + 1, 128, ok) : named_bar_and(4, 256, ok);
       if (!ok) break;
       ptx::tc_fence_after();
       if (key < N) {
         // Weights of the two warpgroups' Ot: 2^(m - M) / sum; a warpgroup
         // that saw no key has m = -inf (or a NaN sum) and nothing to add.
-        const float m0 = cb->end_m[seg & 1][0][key], m1 = cb->end_m[seg & 1][1][key];
-        const float l0 = cb->end_l[seg & 1][0][key], l1 = cb->end_l[seg & 1][1][key];
+        const float m0 = alone ? end_m[key] : cb->end_m[seg % kPagedPlans][0][key];
+        const float m1 = alone ? neg_inf : cb->end_m[seg % kPagedPlans][1][key];
+        const float l0 = alone ? cb->end_l[seg % kPagedPlans][wg][key] : cb->end_l[seg % kPagedPlans][0][key];
+        const float l1 = alone ? 0.f : cb->end_l[seg % kPagedPlans][1][key];
         const float top = fmaxf(m0, m1);
         const float base = top == neg_inf ? 0.f : top;
         const float e0 = m0 == neg_inf ? (l0 == 0.f ? 0.f : l0) : ptx::ex2(m0 - base);
@@ -774,23 +914,22 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         cb->weight[wg][0][key] = e0 * inv;
         cb->weight[wg][1][key] = e1 * inv;
         const float l2 = sum == 0.f ? neg_inf : base + log2f(sum);
-        if (wg == 0 && key < rows) {
+        if ((alone || wg == 0) && key < rows) {
           if (!whole) {
             a.part_lse[(size_t)slot * N + key] = l2;
           } else if (a.lse) {
             const int tok = (row0 + key) / sh.group, h = (row0 + key) - tok * sh.group;
-            a.lse[(size_t)(g.head * sh.group + h) * a.total_q + g.q.lo + tok] =
+            a.lse[(size_t)(head * sh.group + h) * a.total_q + q0 + tok] =
                 l2 * 0.69314718055994531f;
           }
         }
       }
-      if (!whole && g.part_lo == 0 && tid == 0) {
+      if (unit_end >= 0 && key == 0 && (alone || wg == 0)) {
         // The unit starts here: tell the merge how many CTAs share it.
-        const int unit_end = walk.at - g.count + g.unit_count;
         int parts = 1;
         while (cta + parts < ctas && range_start(total, ctas, cta + parts) < unit_end) ++parts;
-        a.meta[2 * cta] = make_int4(parts, g.q.lo, row0, g.head);
         a.meta[2 * cta + 1] = make_int4(rows, slot, 0, 0);
+        a.meta[2 * cta] = make_int4(parts, q0, row0, head);
       }
       named_bar_sync(bar + 2, 128);
       // Dim of this thread's lane: row of a 128-row accumulator, or of a
@@ -798,14 +937,13 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       const int d = D == 128 ? key : (warp & 3) * 16 + lane;
       const bool live = d < a.dim && (D == 128 || lane < 16);
       const uint32_t o0 = tmem + lane_base + 4 * N + (seg & 1) * 2 * N;
-      // A segment of one tile has the Ot of one warpgroup only.
-      const bool two = g.count > 1;
-      const int only = last & 1;
+      // Rows: eight at a time by each warpgroup in turn, or all by the one
+      // that is alone, whose Ot is then the only one.
 #pragma unroll 1
-      for (int n0 = 8 * wg; n0 < rows; n0 += 16) {
+      for (int n0 = alone ? 0 : 8 * wg; n0 < rows; n0 += alone ? 8 : 16) {
         uint32_t oa[8], ob[8];
-        ptx::tmem_ld8(o0 + (two ? 0 : only * N) + n0, oa);
-        ptx::tmem_ld8(o0 + (two ? N : only * N) + n0, ob);
+        ptx::tmem_ld8(o0 + (alone ? wg * N : 0) + n0, oa);
+        ptx::tmem_ld8(o0 + (alone ? wg * N : N) + n0, ob);
         ptx::tmem_wait_ld();
         ptx::reg_fence8(oa);
         ptx::reg_fence8(ob);
@@ -813,14 +951,13 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         for (int k = 0; k < 8; ++k) {
           const int n = n0 + k;
           if (live && n < rows) {
-            const float wa = cb->weight[wg][two ? 0 : only][n];
-            const float wb = two ? cb->weight[wg][1][n] : 0.f;
             // (Weight 0: the Ot may hold anything.)
+            const float wa = cb->weight[wg][0][n], wb = cb->weight[wg][1][n];
             const float v = (wa == 0.f ? 0.f : wa * __uint_as_float(oa[k])) +
                             (wb == 0.f ? 0.f : wb * __uint_as_float(ob[k]));
             if (whole) {
               const int tok = (row0 + n) / sh.group, h = (row0 + n) - tok * sh.group;
-              a.out[((size_t)(g.q.lo + tok) * a.heads + g.head * sh.group + h) * a.dim + d] =
+              a.out[((size_t)(q0 + tok) * a.heads + head * sh.group + h) * a.dim + d] =
                   (uint16_t)ptx::pack_bf16x2(v, 0.f);
             } else {
               a.part_o[((size_t)slot * N + n) * D + d] = v;
@@ -829,7 +966,15 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         }
       }
       ptx::tc_fence_before();
-      ptx::mbar_arrive(ptx::smem_u32(&cb->o_free[seg & 1]));
+      __syncwarp();
+      if (lane == 0) {
+        const uint32_t bar_o = ptx::smem_u32(&cb->o_free[seg & 1]);
+        ptx::mbar_arrive(bar_o);
+        if (alone) ptx::mbar_arrive(bar_o);  // for the other warpgroup
+      }
+      // Only now: the planner writes over this segment's row scales, and the
+      // other warpgroup over its maxima, four segments on at the earliest.
+      plan_done(seg);
     }
   }
 
