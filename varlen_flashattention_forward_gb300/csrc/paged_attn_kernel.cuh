@@ -29,14 +29,13 @@
 // maximum m is taken over x', so that P' = 2^(x' - m + 7) stays below 2^15;
 // the row sum adds 2^(x - m + 7).
 //
-//   planner warp        walks the segments, publishes each one with its first
-//                       page ids and scales in a ring that the other warps
-//                       read, and splits its rows of Q into hi and lo; it
-//                       runs ahead, so that short segments do not wait for
-//                       its chain of dependent loads;
+//   planner warp        walks the segments and publishes them in a ring, a
+//                       batch of up to 16 tiles at a time with the places and
+//                       scales of its pages; splits each segment's rows of Q
+//                       into hi and lo.  It runs ahead, so that nobody else
+//                       waits for its chains of dependent loads;
 //   producer warp       TMA-loads the pages of each tile (128-byte swizzle;
-//                       64-byte at dim 64) into a K and a V ring, with the
-//                       next page ids and scales of long segments under way;
+//                       64-byte at dim 64) into a K and a V ring;
 //   S issuer warp       St(i) as soon as K(i) has landed;
 //   converter warps     V(i) to f16, rows nobody sees as zeros (they may hold
 //                       anything, and 0 * NaN is NaN);
@@ -77,10 +76,9 @@ constexpr uint32_t kPagedSoftmaxRegs = 160;
 constexpr uint32_t kPagedConvertRegs = 80;
 constexpr uint32_t kPagedControlRegs = 96;
 constexpr int kPagedMaxBatch = 1024;  // sequences of one launch
-constexpr int kPagedInfo = 8;         // tile descriptors in flight
-constexpr int kPagedPlans = 4;        // segment descriptors in flight
+constexpr int kPagedPlans = 4;        // batches in flight
 constexpr int kPlanReaders = 15;      // warps that read them
-constexpr int kPlanTiles = 16;        // tiles whose pages are looked up at once
+constexpr int kPlanTiles = 16;        // tiles of a batch
 constexpr float kPagedBias = 7.f;     // P' is held times 2^7
 
 struct PagedAttnArgs {
@@ -103,26 +101,28 @@ struct PagedAttnArgs {
   uint64_t wait_limit_ns;
 };
 
-// One 128-key tile, for the softmax and the converters.
-struct TileInfo {
-  float ks[2], vs[2], lv[2];  // K scale, V scale and its log2, of the two pages
-  int lo, hi;                 // keys of the tile that some row sees, [lo, hi)
-  int held;                   // bit p: page p of the tile is in the cache
+// A page of a batch: its (page, head) cell of the cache, -1 where there is
+// none, and its scales.
+struct PagePlan {
+  float ks, vs, lv;  // K scale, V scale and its log2
+  int held;          // 1: in the cache
 };
 
-// One segment, for every warp; count = 0 ends the range.
-struct SegPlan {
-  int count, tile0;            // key tiles
-  int lo, hi;                  // keys that some row sees
-  int seq, head;
-  int q0, row0, rows;          // the sequence's first q row; rows of the tile
+// Up to kPlanTiles tiles of one segment, for every warp; count = 0 ends the
+// range.
+struct alignas(16) BatchPlan {
+  PagePlan page[2 * kPlanTiles];
+  int cell[2 * kPlanTiles];
+  int count, tile0;            // key tiles of the batch
+  int first, last;             // it begins, ends the segment
+  int lo, hi;                  // keys that some row of the segment sees
+  int head, q0, row0, rows;    // first q row of the sequence; rows of the tile
   int tok0, tok1;              // tokens of its first and last row
   long long at0;               // position of tok0
-  int whole;                   // covers its unit
+  int tiles;                   // of the segment
+  int whole;                   // the segment covers its unit
   int unit_end;                // where the unit starts in this segment but does
                                // not end: the tile number behind it, else -1
-  int id[2 * kPlanTiles];      // pages of the first tiles (-1: none)
-  float ks[2 * kPlanTiles], vs[2 * kPlanTiles];
 };
 
 template <int D, int N>
@@ -151,12 +151,12 @@ struct PagedCfg {
   static constexpr int kCtl = kQ + NQ * kQBytes;
 };
 
+template <int N>
 struct alignas(16) PagedCtl {
-  uint64_t plan_full[kPagedPlans], plan_free[kPagedPlans];  // segment published / read (15)
+  uint64_t plan_full[kPagedPlans], plan_free[kPagedPlans];  // batch published / read (15)
   uint64_t scale_full[kPagedPlans];                         // its scales too
   uint64_t k_full[4], k_free[4];    // K slot landed (TMA bytes) / read by its S MMA
   uint64_t v_full[4], v_free[4];    // V slot landed / converted (128 arrivals)
-  uint64_t info_full[kPagedInfo];
   uint64_t vh_full[2];              // f16 V written (128)
   uint64_t s_full[2], s_free[2];    // St computed / loaded (128)
   uint64_t p_full[2], pv_done[2];   // Pt written (128) / PV complete
@@ -166,30 +166,24 @@ struct alignas(16) PagedCtl {
   uint64_t drain, drain_pv;         // everything an issuer started is complete
   uint32_t tmem_base;
   volatile int abort_flag;
-  TileInfo info[kPagedInfo];
-  SegPlan plan[kPagedPlans];
-  alignas(16) float qs[kPagedPlans][64];      // row scale * softmax scale * log2(e)
-  // Per softmax warpgroup: per-warp partial maxima or sums, the running
-  // maximum less the bias (0 while no key was seen), rescale factors.
-  alignas(16) float red[2][4][64];
-  alignas(16) float m_used[2][64];
-  alignas(16) float alpha[2][64];
+  BatchPlan plan[kPagedPlans];
+  alignas(16) float qs[kPagedPlans][N];      // row scale * softmax scale * log2(e)
+  // Per softmax warpgroup: per-warp partial maxima or sums, minus the running
+  // maximum (less the bias; 0 while no key was seen), rescale factors.
+  alignas(16) float red[2][4][N];
+  alignas(16) float neg_m[2][N];
+  alignas(16) float alpha[2][N];
   // By segment (mod 4) and warpgroup: maximum so far (-inf: no key seen) and,
   // at the segment's end, the sum.  (A warpgroup may be up to three segments
   // ahead of the other, which still reads these.)
-  float end_m[kPagedPlans][2][64], end_l[kPagedPlans][2][64];
-  float weight[2][2][64];            // [reader][warpgroup] factors of its Ot
+  float end_m[kPagedPlans][2][N], end_l[kPagedPlans][2][N];
   long long warp_tiles[kPagedThreads / 32];
   int before[kPagedMaxBatch + 1];
 };
-// (16-byte loads of these.)
-static_assert(offsetof(PagedCtl, qs) % 16 == 0 && offsetof(PagedCtl, m_used) % 16 == 0, "align");
-
 template <int D, int N>
 constexpr size_t paged_smem() {
-  return 1024 + PagedCfg<D, N>::kCtl + sizeof(PagedCtl);
+  return 1024 + PagedCfg<D, N>::kCtl + sizeof(PagedCtl<N>);
 }
-static_assert(sizeof(PagedCtl) < 16384, "control block");
 static_assert(paged_smem<128, 64>() <= 232448, "shared memory exceeds the per-CTA limit");
 static_assert(paged_smem<128, 32>() <= 232448, "shared memory exceeds the per-CTA limit");
 
@@ -218,17 +212,6 @@ __device__ __forceinline__ void warp_transpose_reduce(float* v, int lane) {
   }
 }
 
-// Page `lane` of the tiles from `tile` on, `count` of which are left: its id,
-// or -1 where it is not needed or not in the cache.
-__device__ __forceinline__ int page_for(const PagedAttnArgs& a, const int* table, int tile,
-                                        int count, int lane, int key_lo, int key_hi) {
-  const int p = tile * 2 + lane;
-  if (lane / 2 >= count || (long long)p * kPageTokens >= key_hi ||
-      (long long)(p + 1) * kPageTokens <= key_lo)
-    return -1;
-  return checked_page(__ldg(table + p), a.num_pages);
-}
-
 template <int D, int N>
 __global__ void __launch_bounds__(kPagedThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap k_map,
@@ -237,7 +220,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  PagedCtl* cb = reinterpret_cast<PagedCtl*>(smem + C::kCtl);
+  PagedCtl<N>* cb = reinterpret_cast<PagedCtl<N>*>(smem + C::kCtl);
   volatile int* abort_flag = &cb->abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const AttnShape& sh = a.shape;
@@ -247,7 +230,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   };
 
   ptx::grid_launch_dependents();
-  if (tid == 0) {
+  if (warp == kLoadWarp && lane == 0) {
     auto init = [&](uint64_t& b, uint32_t n) { ptx::mbar_init(ptx::smem_u32(&b), n); };
     for (int s = 0; s < 4; ++s) {
       init(cb->plan_full[s], 1);
@@ -261,7 +244,6 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       init(cb->q_free[s], 1);
       init(cb->qs_full[s], 32);
     }
-    for (int s = 0; s < kPagedInfo; ++s) init(cb->info_full[s], 1);
     for (int s = 0; s < 2; ++s) {
       init(cb->vh_full[s], 128);
       init(cb->s_full[s], 1);
@@ -274,21 +256,22 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     init(cb->drain_pv, 1);
     cb->abort_flag = 0;
     ptx::fence_mbar_init();
-    a.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+    ptx::prefetch_tmap(&k_map);
+    ptx::prefetch_tmap(&v_map);
   }
   if (warp == kSWarp) {
     ptx::tmem_alloc(ptx::smem_u32(&cb->tmem_base), C::kTmemCols);
     ptx::tmem_relinquish();
   }
-  if (warp == kLoadWarp && lane == 0) {
-    ptx::prefetch_tmap(&k_map);
-    ptx::prefetch_tmap(&v_map);
-  }
-  // Tiles of the sequences before each one: a scan over the batch, the same
-  // in every CTA.
-  {
+  // Tiles of the sequences before each one: a scan over the batch by the
+  // softmax warps, the same in every CTA.
+  if (warp < 8) {
+    if (tid == 0) {
+      cb->before[0] = 0;
+      a.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+    }
     long long base = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += kPagedThreads) {
+    for (int b0 = 0; b0 < a.batch; b0 += 256) {
       const int b = b0 + tid;
       int n = 0;
       if (b < a.batch) {
@@ -304,18 +287,17 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         if (lane >= o) sum += v;
       }
       if (lane == 31) cb->warp_tiles[warp] = sum;
-      __syncthreads();
+      named_bar_sync(1, 256);
       long long all = 0, lo = base;
 #pragma unroll
-      for (int w = 0; w < kPagedThreads / 32; ++w) {
+      for (int w = 0; w < 8; ++w) {
         if (w < warp) lo += cb->warp_tiles[w];
         all += cb->warp_tiles[w];
       }
       if (b < a.batch) cb->before[b + 1] = capped_tiles(lo + sum);
       base += all;
-      __syncthreads();
+      named_bar_sync(1, 256);
     }
-    if (tid == 0) cb->before[0] = 0;
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -328,15 +310,15 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   auto wait = [&](uint64_t& b, int parity) {
     return wait_warp(ptx::smem_u32(&b), (uint32_t)parity, abort_flag, a.status, a.wait_limit_ns);
   };
-  // The descriptor of segment number seg; every warp that reads it lets it go
-  // with plan_done once it has what it needs.
-  auto plan_of = [&](int seg, bool* ok) -> const SegPlan& {
-    *ok = wait(cb->plan_full[seg % kPagedPlans], (seg / kPagedPlans) & 1);
-    return cb->plan[seg % kPagedPlans];
+  // Batch number b of the range; every warp that reads it lets it go with
+  // plan_done once it has what it needs.
+  auto plan_of = [&](int b, bool* ok) -> const BatchPlan& {
+    *ok = wait(cb->plan_full[b % kPagedPlans], (b / kPagedPlans) & 1);
+    return cb->plan[b % kPagedPlans];
   };
-  auto plan_done = [&](int seg) {
+  auto plan_done = [&](int b) {
     __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->plan_free[seg % kPagedPlans]));
+    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->plan_free[b % kPagedPlans]));
   };
 
   if (warp >= kConvertWarp && warp < kSWarp) {
@@ -345,66 +327,73 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     // A thread takes 16-byte units (16 codes) of a row.  Eight neighbouring
     // lanes take four units of the rows r and r ^ 5 (r even): under the
     // swizzles their eight 16-byte loads, and their eight stores of either
-    // half, then lie in different banks.
+    // half, then lie in different banks.  Its rows are a multiple of 8 apart,
+    // so that the swizzle is the same for all of them.
     constexpr int kChunks = D / 64;          // 64-dim chunks of an f16 row
-    constexpr int kIters = 128 * (D / 16) / 128;
+    constexpr int kIters = D / 16;           // units of a thread
+    constexpr int kStep = 32 / kChunks;      // its rows' distance
     const int t = tid - 32 * kConvertWarp;
-    const int u4 = t & 3, odd = (t >> 2) & 1, group = t >> 3;
+    const int u4 = t & 3, pair = t >> 3, chunk = pair % kChunks;
+    const int even = 2 * (pair / kChunks), r0 = (t & 4) ? even ^ 5 : even;
+    const int u = chunk * 4 + u4;
+    const int us = D == 128 ? (u ^ (r0 & 7)) : (u ^ ((r0 >> 1) & 3));
+    const uint8_t* src0 = smem + C::kV + r0 * C::kRow + us * 16;
+    const int p0 = (2 * u4) ^ (r0 & 7);
+    uint8_t* dst0 = smem + C::kVh + chunk * (kTileKeys * 128) + r0 * 128 + p0 * 16;
+    uint8_t* dst1 = smem + C::kVh + chunk * (kTileKeys * 128) + r0 * 128 + (p0 ^ 1) * 16;
     bool ok = true;
-    int i = 0;
-    for (int seg = 0; ok; ++seg) {
-      const SegPlan& plan = plan_of(seg, &ok);
+    int i = 0, slot = 0;
+    uint32_t v_phase = 0;
+    for (int b = 0; ok; ++b) {
+      const BatchPlan& plan = plan_of(b, &ok);
       if (!ok) break;
-      const int count = plan.count;
-      plan_done(seg);
+      const int count = plan.count, tile0 = plan.tile0, key_lo = plan.lo, key_hi = plan.hi;
       if (count == 0) break;
+      // (held is written with the scales)
+      ok = wait(cb->scale_full[b % kPagedPlans], (b / kPagedPlans) & 1);
+      if (!ok) break;
+      const unsigned held = __ballot_sync(0xffffffffu, plan.page[lane].held != 0);
+      plan_done(b);
       for (int n = 0; n < count; ++n, ++i) {
-        const int slot = i % C::NV, hb = i & 1;
-        ok = wait(cb->v_full[slot], (i / C::NV) & 1);
-        if (ok) ok = wait(cb->info_full[i % kPagedInfo], (i / kPagedInfo) & 1);
+        const int hb = i & 1;
+        ok = wait(cb->v_full[slot], v_phase);
         if (!ok) break;
-        const TileInfo& ti = cb->info[i % kPagedInfo];
-        const int lo = ti.lo, hi = ti.hi, held = ti.held;
-        const bool all = lo == 0 && hi == kTileKeys && held == 3;
-        const uint8_t* src = smem + C::kV + slot * C::kTileBytes;
+        const uint8_t* src = src0 + slot * C::kTileBytes;
         uint4 c[kIters];
-        auto place = [&](int k, int* r, int* chunk) {
-          const int id = group + 16 * k;  // of 64 row pairs x chunks
-          *chunk = id % kChunks;
-          const int even = 2 * (id / kChunks);
-          *r = odd ? even ^ 5 : even;
-        };
 #pragma unroll
-        for (int k = 0; k < kIters; ++k) {
-          int r, ch;
-          place(k, &r, &ch);
-          const int u = ch * 4 + u4;
-          const int us = D == 128 ? (u ^ (r & 7)) : (u ^ ((r >> 1) & 3));
-          c[k] = *reinterpret_cast<const uint4*>(src + r * C::kRow + us * 16);
-          if (!all && (r < lo || r >= hi || !((held >> (r >> 6)) & 1)))
-            c[k] = make_uint4(0u, 0u, 0u, 0u);
+        for (int k = 0; k < kIters; ++k)
+          c[k] = *reinterpret_cast<const uint4*>(src + k * kStep * C::kRow);
+        const int key0 = (tile0 + n) * kTileKeys;
+        const int lo = key_lo - key0, hi = key_hi - key0;
+        const unsigned pages = (held >> (2 * n)) & 3;
+        if (lo > 0 || hi < kTileKeys || pages != 3) {
+#pragma unroll
+          for (int k = 0; k < kIters; ++k) {
+            const int r = r0 + k * kStep;
+            if (r < lo || r >= hi || !((pages >> (r >> 6)) & 1)) c[k] = make_uint4(0u, 0u, 0u, 0u);
+          }
         }
         if (i >= 2) {
           ok = wait(cb->pv_done[hb], ((i >> 1) - 1) & 1);
           if (!ok) break;
         }
-        uint8_t* dst = smem + C::kVh + hb * C::kVhBytes;
 #pragma unroll
         for (int k = 0; k < kIters; ++k) {
-          int r, ch;
-          place(k, &r, &ch);
-          uint8_t* row = dst + ch * (kTileKeys * 128) + r * 128;
-          const int p0 = (2 * u4) ^ (r & 7);
-          *reinterpret_cast<uint4*>(row + p0 * 16) =
+          const int at = hb * C::kVhBytes + k * kStep * 128;
+          *reinterpret_cast<uint4*>(dst0 + at) =
               make_uint4(unpack_e4m3x2(c[k].x), unpack_e4m3x2(c[k].x >> 16),
                          unpack_e4m3x2(c[k].y), unpack_e4m3x2(c[k].y >> 16));
-          *reinterpret_cast<uint4*>(row + (p0 ^ 1) * 16) =
+          *reinterpret_cast<uint4*>(dst1 + at) =
               make_uint4(unpack_e4m3x2(c[k].z), unpack_e4m3x2(c[k].z >> 16),
                          unpack_e4m3x2(c[k].w), unpack_e4m3x2(c[k].w >> 16));
         }
         ptx::fence_proxy_async_smem();
         ptx::mbar_arrive(ptx::smem_u32(&cb->vh_full[hb]));
         ptx::mbar_arrive(ptx::smem_u32(&cb->v_free[slot]));
+        if (++slot == C::NV) {
+          slot = 0;
+          v_phase ^= 1;
+        }
       }
     }
   } else if (warp >= kSWarp) {
@@ -413,33 +402,42 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       // ---------------------------------------------------------- S issuer
       constexpr uint32_t idesc = ptx::idesc_e4m3_f32(128, 2 * N);
       bool ok = true;
-      int i = 0;
-      for (int seg = 0; ok; ++seg) {
-        const SegPlan& plan = plan_of(seg, &ok);
+      int i = 0, seg = 0, slot = 0;
+      uint32_t k_phase = 0;
+      uint64_t qd = 0;
+      for (int b = 0; ok; ++b) {
+        const BatchPlan& plan = plan_of(b, &ok);
         if (!ok) break;
-        const int count = plan.count;
-        plan_done(seg);
+        const int count = plan.count, first = plan.first, last = plan.last;
+        plan_done(b);
         if (count == 0) break;
         const int qb = seg % C::NQ;
-        ok = wait(cb->q_full[qb], (seg / C::NQ) & 1);
-        if (!ok) break;
-        const uint64_t qd = ptx::smem_desc(ptx::smem_u32(smem + C::kQ + qb * C::kQBytes), 16,
-                                           8 * C::kRow, C::kSwK);
+        if (first) {
+          ok = wait(cb->q_full[qb], (seg / C::NQ) & 1);
+          if (!ok) break;
+          qd = ptx::smem_desc(ptx::smem_u32(smem + C::kQ + qb * C::kQBytes), 16, 8 * C::kRow,
+                              C::kSwK);
+        }
         for (int n = 0; n < count; ++n, ++i) {
-          const int slot = i % C::NK;
-          ok = wait(cb->k_full[slot], (i / C::NK) & 1);
+          ok = wait(cb->k_full[slot], k_phase);
           if (ok && i >= 2) ok = wait(cb->s_free[i & 1], ((i >> 1) - 1) & 1);
           if (!ok) break;
-          // (Q was written through the generic proxy; its writers fenced.)
           ptx::tc_fence_after();
           const uint64_t kd = ptx::smem_desc(
               ptx::smem_u32(smem + C::kK + slot * C::kTileBytes), 16, 8 * C::kRow, C::kSwK);
           ptx::mma_f8_elect<D / 32>(tmem + (i & 1) * 2 * N, kd, qd, idesc);
           ptx::mma_commit_elect(ptx::smem_u32(&cb->s_full[i & 1]));
           ptx::mma_commit_elect(ptx::smem_u32(&cb->k_free[slot]));
+          if (++slot == C::NK) {
+            slot = 0;
+            k_phase ^= 1;
+          }
         }
         if (!ok) break;
-        ptx::mma_commit_elect(ptx::smem_u32(&cb->q_free[qb]));
+        if (last) {
+          ptx::mma_commit_elect(ptx::smem_u32(&cb->q_free[qb]));
+          ++seg;
+        }
       }
       ptx::mma_commit_elect(ptx::smem_u32(&cb->drain));
       wait_drain_warp(ptx::smem_u32(&cb->drain), 0, a.status);
@@ -447,15 +445,15 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       // --------------------------------------------------------- PV issuer
       constexpr uint32_t idesc = ptx::idesc_f16_f32(D, N, true, true);
       bool ok = true;
-      int i = 0;
-      for (int seg = 0; ok; ++seg) {
-        const SegPlan& plan = plan_of(seg, &ok);
+      int i = 0, seg = 0, in_seg = 0;
+      for (int b = 0; ok; ++b) {
+        const BatchPlan& plan = plan_of(b, &ok);
         if (!ok) break;
-        const int count = plan.count;
-        plan_done(seg);
+        const int count = plan.count, last = plan.last;
+        plan_done(b);
         if (count == 0) break;
-        if (seg >= 2) ok = wait(cb->o_free[seg & 1], ((seg >> 1) - 1) & 1);
-        for (int n = 0; ok && n < count; ++n, ++i) {
+        if (in_seg == 0 && seg >= 2) ok = wait(cb->o_free[seg & 1], ((seg >> 1) - 1) & 1);
+        for (int n = 0; ok && n < count; ++n, ++i, ++in_seg) {
           const int hb = i & 1;
           ok = wait(cb->vh_full[hb], (i >> 1) & 1);
           if (ok) ok = wait(cb->p_full[hb], (i >> 1) & 1);
@@ -467,91 +465,60 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
           const uint64_t bd = ptx::smem_desc(ptx::smem_u32(smem + C::kP + hb * C::kPBytes),
                                              8 * C::kPRow, 8 * C::kPRow, C::kSwP);
           const uint32_t d = tmem + 4 * N + (seg & 1) * 2 * N + hb * N;
-          ptx::mma_ss4_elect<16 * 128 / 16, 16 * C::kPRow / 16>(d, ad, bd, idesc, n > 1 ? 1u : 0u);
+          ptx::mma_ss4_elect<16 * 128 / 16, 16 * C::kPRow / 16>(d, ad, bd, idesc,
+                                                                in_seg > 1 ? 1u : 0u);
           ptx::mma_ss4_elect<16 * 128 / 16, 16 * C::kPRow / 16>(
               d, ptx::desc_add(ad, 64 * 128), ptx::desc_add(bd, 64 * C::kPRow), idesc, 1u);
           ptx::mma_commit_elect(ptx::smem_u32(&cb->pv_done[hb]));
+        }
+        if (last) {
+          ++seg;
+          in_seg = 0;
         }
       }
       ptx::mma_commit_elect(ptx::smem_u32(&cb->drain_pv));
       wait_drain_warp(ptx::smem_u32(&cb->drain_pv), 0, a.status);
     } else if (warp == kLoadWarp) {
       // ---------------------------------------------------------- producer
+      // Lanes 0 and 1 issue the two pages of a tile with one instruction.
       test_load_delay(a.wait_limit_ns);
       bool ok = true;
-      int i = 0, kn = 0, vn = 0;  // tiles; K and V loads issued
-      for (int seg = 0; ok; ++seg) {
-        const SegPlan& plan = plan_of(seg, &ok);
+      int kn = 0, vn = 0, sk = 0, sv = 0;  // loads issued and slots of K and V
+      uint32_t k_phase = 1, v_phase = 1;   // (the first turn finds its slots free)
+      for (int b = 0; ok; ++b) {
+        const BatchPlan& plan = plan_of(b, &ok);
         if (!ok) break;
-        const int count = plan.count, tile0 = plan.tile0, key_lo = plan.lo, key_hi = plan.hi;
-        const int head = plan.head;
-        const int* table = a.page_table + (size_t)plan.seq * a.max_pages;
-        // Lane l holds page l of kPlanTiles tiles: its id, or -1 where the
-        // tile needs no such page, and its scales; next_* those of the tiles
-        // after them, the ids asked for at the first tile, the scales halfway.
-        int id = plan.id[lane], next_id = -1;
-        float ks = 0.f, vs = 0.f, next_ks = 0.f, next_vs = 0.f;
-        if (count == 0) {
-          plan_done(seg);
-          break;
-        }
-        for (int n = 0; n < count; ++n, ++i) {
-          const int in = n % kPlanTiles;
-          if (n > 0 && in == 0) {
-            id = next_id;
-            ks = next_ks;
-            vs = next_vs;
-          }
-          if (in == 0 && n + kPlanTiles < count)
-            next_id = page_for(a, table, tile0 + n + kPlanTiles, count - n - kPlanTiles, lane,
-                               key_lo, key_hi);
-          if (in == kPlanTiles / 2 && n + kPlanTiles / 2 < count) {
-            next_ks = next_id >= 0 ? __ldg(a.k_scale + (size_t)next_id * sh.heads_k + head) : 0.f;
-            next_vs = next_id >= 0 ? __ldg(a.v_scale + (size_t)next_id * sh.heads_k + head) : 0.f;
-          }
-          const int id0 = __shfl_sync(0xffffffffu, id, 2 * in);
-          const int id1 = __shfl_sync(0xffffffffu, id, 2 * in + 1);
-          const int held = (id0 >= 0 ? 1 : 0) | (id1 >= 0 ? 2 : 0);
+        const int count = plan.count;
+        const int cell = plan.cell[lane];
+        plan_done(b);
+        if (count == 0) break;
+        for (int n = 0; n < count; ++n) {
+          const int mine = __shfl_sync(0xffffffffu, cell, 2 * n + (lane & 1));
+          const unsigned held = __ballot_sync(0xffffffffu, mine >= 0) & 3;
           const uint32_t bytes = ((held & 1) + (held >> 1)) * C::kPageBytes;
           auto load = [&](const CUtensorMap* map, uint64_t& full, uint8_t* slot) {
-            if (lane == 0) {
-              const uint32_t bar = ptx::smem_u32(&full), dst = ptx::smem_u32(slot);
-              ptx::mbar_arrive_expect_tx(bar, bytes);
-              if (id0 >= 0) ptx::tma_load_3d(dst, map, bar, 0, 0, id0 * sh.heads_k + head);
-              if (id1 >= 0)
-                ptx::tma_load_3d(dst + C::kPageBytes, map, bar, 0, 0, id1 * sh.heads_k + head);
-            }
+            const uint32_t bar = ptx::smem_u32(&full);
+            if (lane == 0) ptx::mbar_arrive_expect_tx(bar, bytes);
+            __syncwarp();
+            if (lane < 2 && mine >= 0)
+              ptx::tma_load_3d(ptx::smem_u32(slot) + lane * C::kPageBytes, map, bar, 0, 0, mine);
           };
-          const int sk = i % C::NK, sv = i % C::NV;
-          if (i >= C::NK) ok = wait(cb->k_free[sk], (i / C::NK - 1) & 1);
+          ok = wait(cb->k_free[sk], k_phase);
           if (!ok) break;
           load(&k_map, cb->k_full[sk], smem + C::kK + sk * C::kTileBytes);
           ++kn;
-          if (i >= C::NV) ok = wait(cb->v_free[sv], (i / C::NV - 1) & 1);
+          if (++sk == C::NK) {
+            sk = 0;
+            k_phase ^= 1;
+          }
+          ok = wait(cb->v_free[sv], v_phase);
           if (!ok) break;
           load(&v_map, cb->v_full[sv], smem + C::kV + sv * C::kTileBytes);
           ++vn;
-          if (n == 0) {
-            ok = wait(cb->scale_full[seg % kPagedPlans], (seg / kPagedPlans) & 1);
-            if (!ok) break;
-            ks = plan.ks[lane];
-            vs = plan.vs[lane];
-            plan_done(seg);
+          if (++sv == C::NV) {
+            sv = 0;
+            v_phase ^= 1;
           }
-          TileInfo* ti = &cb->info[i % kPagedInfo];
-          if ((lane >> 1) == in) {
-            ti->ks[lane & 1] = ks;
-            ti->vs[lane & 1] = vs;
-            ti->lv[lane & 1] = fmaxf(log2f(vs), -(float)kScaleExpMax);
-          }
-          if (lane == 0) {
-            const int key0 = (tile0 + n) * kTileKeys;
-            ti->lo = imax(key_lo - key0, 0);
-            ti->hi = imin(key_hi - key0, kTileKeys);
-            ti->held = held;
-          }
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->info_full[i % kPagedInfo]));
         }
       }
       // Every copy this CTA started lands before it exits.
@@ -569,18 +536,27 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       walk_begin(&walk, range_start(total, ctas, cta), range_start(total, ctas, cta + 1), a.batch,
                  before);
       Segment g = {};
-      auto pages = [&]() {
-        return page_for(a, a.page_table + (size_t)g.seq * a.max_pages, g.tile0, g.count, lane,
-                        g.keys.lo, g.keys.hi);
+      int n0 = 0;  // tiles of the segment in earlier batches
+      // Lane l: page l of the batch's tiles, as its cell of the cache, or -1
+      // where it is not needed or not there.
+      auto cells = [&]() {
+        const int p = (g.tile0 + n0) * 2 + lane;
+        if (n0 + lane / 2 >= g.count || (long long)p * kPageTokens >= g.keys.hi ||
+            (long long)(p + 1) * kPageTokens <= g.keys.lo)
+          return -1;
+        const int id = checked_page(
+            __ldg(a.page_table + (size_t)g.seq * a.max_pages + p), a.num_pages);
+        return id < 0 ? -1 : id * sh.heads_k + g.head;
       };
       bool more = walk_next(&walk, sh, before, seq_of, &g);
-      int id = more ? pages() : -1;
+      int cell = more ? cells() : -1;
       bool ok = true;
-      for (int seg = 0;; ++seg) {
-        const int slot = seg % kPagedPlans;
-        if (seg >= kPagedPlans) ok = wait(cb->plan_free[slot], (seg / kPagedPlans - 1) & 1);
+      int seg = 0;
+      for (int b = 0;; ++b) {
+        const int slot = b % kPagedPlans;
+        if (b >= kPagedPlans) ok = wait(cb->plan_free[slot], (b / kPagedPlans - 1) & 1);
         if (!ok) break;
-        SegPlan& plan = cb->plan[slot];
+        BatchPlan& plan = cb->plan[slot];
         if (!more) {
           if (lane == 0) {
             plan.count = 0;
@@ -590,31 +566,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         }
         const int head = g.head, group = sh.group, q0 = g.q.lo;
         const int row0 = g.row_tile * N, rows = imin(N, g.q.n * group - row0);
-        plan.id[lane] = id;
-        if (lane == 0) {
-          plan.count = g.count;
-          plan.tile0 = g.tile0;
-          plan.lo = g.keys.lo;
-          plan.hi = g.keys.hi;
-          plan.seq = g.seq;
-          plan.head = head;
-          plan.q0 = q0;
-          plan.row0 = row0;
-          plan.rows = rows;
-          plan.tok0 = row0 / group;
-          plan.tok1 = (row0 + rows - 1) / group;
-          plan.at0 = (long long)g.len - g.q.n + plan.tok0;
-          plan.whole = g.count == g.unit_count;
-          plan.unit_end =
-              g.part_lo == 0 && g.count < g.unit_count ? walk.at - g.count + g.unit_count : -1;
-        }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->plan_full[slot]));
-        // Scales and the first rows of Q under way, then the next segment's
-        // pages.
-        const size_t cell = (size_t)imax(id, 0) * sh.heads_k + head;
-        const float ks = id >= 0 ? __ldg(a.k_scale + cell) : 0.f;
-        const float vs = id >= 0 ? __ldg(a.v_scale + cell) : 0.f;
+        const bool first = n0 == 0, last = g.count - n0 <= kPlanTiles;
         uint4 raw[kBatch];
         auto load_rows = [&](int j0) {
 #pragma unroll
@@ -629,188 +581,386 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             }
           }
         };
-        load_rows(0);
-        more = walk_next(&walk, sh, before, seq_of, &g);
-        id = more ? pages() : -1;
-        plan.ks[lane] = ks;
-        plan.vs[lane] = vs;
+        if (first) load_rows(0);  // (ahead of the pages' loads in the memory system)
+        plan.cell[lane] = cell;
+        if (lane == 0) {
+          plan.count = imin(g.count - n0, kPlanTiles);
+          plan.tile0 = g.tile0 + n0;
+          plan.first = first;
+          plan.last = last;
+          plan.lo = g.keys.lo;
+          plan.hi = g.keys.hi;
+          plan.head = head;
+          plan.q0 = q0;
+          plan.row0 = row0;
+          plan.rows = rows;
+          plan.tok0 = row0 / group;
+          plan.tok1 = (row0 + rows - 1) / group;
+          plan.at0 = (long long)g.len - g.q.n + plan.tok0;
+          plan.tiles = g.count;
+          plan.whole = g.count == g.unit_count;
+          plan.unit_end =
+              g.part_lo == 0 && g.count < g.unit_count ? walk.at - g.count + g.unit_count : -1;
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->plan_full[slot]));
+        // The scales under way, then the next batch's pages.
+        const int held = cell >= 0;
+        const float ks = held ? __ldg(a.k_scale + cell) : 0.f;
+        const float vs = held ? __ldg(a.v_scale + cell) : 0.f;
+        auto advance = [&]() {
+          n0 += kPlanTiles;
+          if (last) {
+            n0 = 0;
+            more = walk_next(&walk, sh, before, seq_of, &g);
+          }
+          cell = more ? cells() : -1;
+        };
+        // (The first segment's S waits for its Q: look ahead after that.)
+        if (b > 0) advance();
+        plan.page[lane] = {ks, vs, fmaxf(log2f(vs), -(float)kScaleExpMax), held};
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->scale_full[slot]));
-        const int qb = seg % C::NQ;
-        if (seg >= C::NQ) ok = wait(cb->q_free[qb], (seg / C::NQ - 1) & 1);
-        if (!ok) break;
-        uint8_t* q_s = smem + C::kQ + qb * C::kQBytes;  // N rows of hi, N of lo
-        for (int j0 = 0; j0 < N; j0 += kGroups * kBatch) {
-          if (j0 > 0) load_rows(j0);
+        if (first) {
+          const int qb = seg % C::NQ;
+          if (seg >= C::NQ) ok = wait(cb->q_free[qb], (seg / C::NQ - 1) & 1);
+          if (!ok) break;
+          uint8_t* q_s = smem + C::kQ + qb * C::kQBytes;  // N rows of hi, N of lo
+          for (int j0 = 0; j0 < N; j0 += kGroups * kBatch) {
+            if (j0 > 0) load_rows(j0);
 #pragma unroll
-          for (int j = 0; j < kBatch; ++j) {
-            const int n = j0 + j * kGroups + lane / kLanes;
-            float x[8];
-            unpack_bf16x8(raw[j], x);
-            float mx = 0.f;
-            bool finite = true;
+            for (int j = 0; j < kBatch; ++j) {
+              const int n = j0 + j * kGroups + lane / kLanes;
+              float x[8];
+              unpack_bf16x8(raw[j], x);
+              float mx = 0.f;
+              bool finite = true;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              finite = finite && fabsf(x[k]) <= 3.402823466e38f;
-              mx = fmaxf(mx, fabsf(x[k]));
+              for (int k = 0; k < 8; ++k) {
+                finite = finite && fabsf(x[k]) <= 3.402823466e38f;
+                mx = fmaxf(mx, fabsf(x[k]));
+              }
+              // A row with an infinity or a NaN gets NaN scores.
+              if (!finite) mx = __int_as_float(0x7f800000);
+#pragma unroll
+              for (int o = kLanes / 2; o > 0; o >>= 1)
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              // mx in [2^e, 2^(e+1)) goes to [128, 256).  (Rows below 2^-100
+              // keep a smaller size; their scores are zero in fp32 all the
+              // same.)
+              const int e = imax((int)(__float_as_uint(mx) >> 23) - 127, -100);
+              const float f = __uint_as_float((uint32_t)(7 - e + 127) << 23);
+              uint32_t hi[4], lo[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float y0 = x[2 * k] * f, y1 = x[2 * k + 1] * f;
+                hi[k] = pack_e4m3x2(y0, y1);
+                const float2 h2 = f16x2_floats(unpack_e4m3x2(hi[k]));
+                lo[k] = pack_e4m3x2(y0 - h2.x, y1 - h2.y);
+              }
+              auto place = [&](int r) {
+                const int unit = dim0 >> 4;
+                const int us = D == 128 ? (unit ^ (r & 7)) : (unit ^ ((r >> 1) & 3));
+                return r * C::kRow + us * 16 + (dim0 & 8);
+              };
+              *reinterpret_cast<uint2*>(q_s + place(n)) =
+                  make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+              *reinterpret_cast<uint2*>(q_s + place(N + n)) =
+                  make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+              if (sub == 0)
+                cb->qs[seg % kPagedPlans][n] =
+                    mx < __int_as_float(0x7f800000)
+                        ? a.scale_log2 * __uint_as_float((uint32_t)(e - 7 + 127) << 23)
+                        : __int_as_float(0x7fffffff);
             }
-            // A row with an infinity or a NaN gets NaN scores.
-            if (!finite) mx = __int_as_float(0x7f800000);
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1)
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            // mx in [2^e, 2^(e+1)) goes to [128, 256).  (Rows below 2^-100 keep
-            // a smaller size; their scores are zero in fp32 all the same.)
-            const int e = imax((int)(__float_as_uint(mx) >> 23) - 127, -100);
-            const float f = __uint_as_float((uint32_t)(7 - e + 127) << 23);
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float y0 = x[2 * k] * f, y1 = x[2 * k + 1] * f;
-              hi[k] = pack_e4m3x2(y0, y1);
-              const float2 b = f16x2_floats(unpack_e4m3x2(hi[k]));
-              lo[k] = pack_e4m3x2(y0 - b.x, y1 - b.y);
-            }
-            auto place = [&](int r) {
-              const int unit = dim0 >> 4;
-              const int us = D == 128 ? (unit ^ (r & 7)) : (unit ^ ((r >> 1) & 3));
-              return r * C::kRow + us * 16 + (dim0 & 8);
-            };
-            *reinterpret_cast<uint2*>(q_s + place(n)) =
-                make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-            *reinterpret_cast<uint2*>(q_s + place(N + n)) =
-                make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-            if (sub == 0)
-              cb->qs[seg % kPagedPlans][n] =
-                  mx < __int_as_float(0x7f800000)
-                      ? a.scale_log2 * __uint_as_float((uint32_t)(e - 7 + 127) << 23)
-                      : __int_as_float(0x7fffffff);
           }
+          ptx::fence_proxy_async_smem();
+          ptx::mbar_arrive(ptx::smem_u32(&cb->qs_full[seg % kPagedPlans]));
+          ptx::mbar_arrive(ptx::smem_u32(&cb->q_full[qb]));
         }
-        ptx::fence_proxy_async_smem();
-        ptx::mbar_arrive(ptx::smem_u32(&cb->qs_full[slot]));
-        ptx::mbar_arrive(ptx::smem_u32(&cb->q_full[qb]));
+        if (last) ++seg;
+        if (b == 0) advance();
       }
     }
   } else {
     ptx::regs_inc<kPagedSoftmaxRegs>();
     // -------------------------------------------------------------- softmax
     const float neg_inf = -__int_as_float(0x7f800000);
+    const unsigned full = 0xffffffffu;
     const int wg = warp >> 2;             // tiles i with i % 2 == wg
     const int key = tid & 127;            // of the tile
     const int page = key >> 6;
     const int bar = 1 + 4 * wg;           // named barriers bar .. bar + 2; 4: both warpgroups
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_tmem = tmem + lane_base + wg * 2 * N;
-    float (*red)[64] = cb->red[wg];
-    float* m_used = cb->m_used[wg];
+    float (*red)[N] = cb->red[wg];
+    float* neg_m = cb->neg_m[wg];
     float* alpha = cb->alpha[wg];
     uint8_t* prow = smem + C::kP + wg * C::kPBytes + key * C::kPRow;
-    float l[N];
+    // At 16 rows the factors and maxima stay in registers (pairs), for more
+    // they are read from shared memory.
+    constexpr int kHeld = N == 16 ? N / 2 : 1;
+    uint64_t c_held[kHeld], m_held[kHeld];
+    auto pair = [](const float* p, int n) { return *reinterpret_cast<const uint64_t*>(p + n); };
     bool ok = true;
-    int i = 0;          // tiles before the segment
-    for (int seg = 0; ok; ++seg) {
-      const SegPlan& plan = plan_of(seg, &ok);
-      const int count = plan.count, tile0 = plan.tile0, q0 = plan.q0, head = plan.head;
-      const int row0 = plan.row0, rows = plan.rows, tok0 = plan.tok0, tok1 = plan.tok1;
-      const int whole = plan.whole, unit_end = plan.unit_end;
+    int i = 0;  // tiles before the batch
+
+    // The output of a segment is written once the next one's first tile is
+    // under way (`due`), by when its last P V has long been done.
+    struct {
+      int seg, batch, last, q0, row0, rows, head;
+      bool alone, whole, due;
+      int unit_end;
+    } done;
+    done.due = false;
+    // The warpgroups meet at barrier 4, once for each segment they share and
+    // once more at the end, unless one has learnt there that the other gave
+    // up (`parted`): so neither waits there for one that has left.
+    bool parted = false;
+    // Each warpgroup knows the PV of its own last tile of the segment to be
+    // done before they meet: from the wait for Pt's buffer in a tile after it
+    // (`later`), or by waiting here.  (Not both: with that tile's PV complete
+    // the barrier's phase may have come round again.)
+    auto finish = [&](bool later) -> bool {
+      done.due = false;
+      const bool alone = done.alone;
+      const int rows = done.rows, row0 = done.row0, head = done.head;
+      const int ring = done.seg % kPagedPlans;
+      const int slot = 2 * cta + (done.seg == 0 ? 0 : 1);
+      const int mine = (done.last & 1) == wg ? done.last : done.last - 1;
+      bool good = later || wait(cb->pv_done[wg], (mine >> 1) & 1);
+      ptx::tc_fence_before();
+      good = alone ? named_bar_and(bar + 1, 128, good) : named_bar_and(4, 256, good);
+      if (!good) {
+        parted = !alone;
+        return false;
+      }
+      ptx::tc_fence_after();
+      // Lane n: weights of row n's two Ot (lane n - 32 has a second row at 64
+      // rows): 2^(m - M) / sum; a warpgroup that saw no key has m = -inf (or
+      // a NaN sum) and nothing to add.
+      float wa[(N + 31) / 32], wb[(N + 31) / 32];
+#pragma unroll
+      for (int r = 0; r < (N + 31) / 32; ++r) {
+        const int n = lane + 32 * r;
+        wa[r] = wb[r] = 0.f;
+        if (n < N) {
+          const int w0 = alone ? wg : 0;
+          const float m0 = cb->end_m[ring][w0][n], l0 = cb->end_l[ring][w0][n];
+          const float m1 = alone ? neg_inf : cb->end_m[ring][1][n];
+          const float l1 = alone ? 0.f : cb->end_l[ring][1][n];
+          const float top = fmaxf(m0, m1);
+          const float base = top == neg_inf ? 0.f : top;
+          const float e0 = m0 == neg_inf ? (l0 == 0.f ? 0.f : l0) : ptx::ex2(m0 - base);
+          const float e1 = m1 == neg_inf ? (l1 == 0.f ? 0.f : l1) : ptx::ex2(m1 - base);
+          const float sum = e0 * l0 + e1 * l1;
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (a NaN stays one)
+          wa[r] = e0 * inv;
+          wb[r] = e1 * inv;
+          if (n < rows && (warp & 3) == 0 && (alone || wg == 0)) {
+            const float l2 = sum == 0.f ? neg_inf : base + log2f(sum);
+            if (!done.whole) {
+              a.part_lse[(size_t)slot * N + n] = l2;
+            } else if (a.lse) {
+              const int tok = (row0 + n) / sh.group, h = (row0 + n) - tok * sh.group;
+              a.lse[(size_t)(head * sh.group + h) * a.total_q + done.q0 + tok] =
+                  l2 * 0.69314718055994531f;
+            }
+          }
+        }
+      }
+      if (done.unit_end >= 0 && key == 0 && (alone || wg == 0)) {
+        // The unit starts here: tell the merge how many CTAs share it.
+        int parts = 1;
+        while (cta + parts < ctas && range_start(total, ctas, cta + parts) < done.unit_end) ++parts;
+        a.meta[2 * cta + 1] = make_int4(rows, slot, 0, 0);
+        a.meta[2 * cta] = make_int4(parts, done.q0, row0, head);
+      }
+      // Dim of this thread's lane: row of a 128-row accumulator, or of a
+      // 64-row one, which uses the first 16 lanes of each warp's 32.
+      const int d = D == 128 ? key : (warp & 3) * 16 + lane;
+      const bool live = d < a.dim && (D == 128 || lane < 16);
+      const uint32_t o0 = tmem + lane_base + 4 * N + (done.seg & 1) * 2 * N;
+      // Rows: eight at a time by each warpgroup in turn, or all by the one
+      // that is alone, whose Ot is then the only one.
+#pragma unroll 1
+      for (int n0 = alone ? 0 : 8 * wg; n0 < rows; n0 += alone ? 8 : 16) {
+        uint32_t oa[8], ob[8];
+        ptx::tmem_ld8(o0 + (alone ? wg * N : 0) + n0, oa);
+        ptx::tmem_ld8(o0 + (alone ? wg * N : N) + n0, ob);
+        ptx::tmem_wait_ld();
+        ptx::reg_fence8(oa);
+        ptx::reg_fence8(ob);
+        int tok = (row0 + n0) / sh.group, h = (row0 + n0) - tok * sh.group;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int n = n0 + k;
+          const float fa = __shfl_sync(full, N == 64 && n >= 32 ? wa[(N + 31) / 32 - 1] : wa[0], n & 31);
+          const float fb = __shfl_sync(full, N == 64 && n >= 32 ? wb[(N + 31) / 32 - 1] : wb[0], n & 31);
+          if (live && n < rows) {
+            // (Weight 0: the Ot may hold anything.)
+            const float v = (fa == 0.f ? 0.f : fa * __uint_as_float(oa[k])) +
+                            (fb == 0.f ? 0.f : fb * __uint_as_float(ob[k]));
+            if (done.whole) {
+              a.out[((size_t)(done.q0 + tok) * a.heads + head * sh.group + h) * a.dim + d] =
+                  (uint16_t)ptx::pack_bf16x2(v, 0.f);
+            } else {
+              a.part_o[((size_t)slot * N + n) * D + d] = v;
+            }
+          }
+          if (++h == sh.group) {
+            h = 0;
+            ++tok;
+          }
+        }
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        const uint32_t bar_o = ptx::smem_u32(&cb->o_free[done.seg & 1]);
+        ptx::mbar_arrive(bar_o);
+        if (alone) ptx::mbar_arrive(bar_o);  // for the other warpgroup
+      }
+      // Only now: the planner writes over the segment's row scales, and the
+      // other warpgroup over its maxima, four batches on at the earliest.
+      plan_done(done.batch);
+      return true;
+    };
+
+    int seg = 0, seg0 = 0;  // segment, its first tile
+    uint64_t l[N / 2];
+    bool unset = true;
+    for (int b = 0; ok; ++b) {
+      const BatchPlan& plan = plan_of(b, &ok);
+      if (ok && plan.count > 0) ok = wait(cb->scale_full[b % kPagedPlans], (b / kPagedPlans) & 1);
+      const int count = plan.count, tile0 = plan.tile0, rows = plan.rows;
+      const int tok0 = plan.tok0, tok1 = plan.tok1, row0 = plan.row0;
       const long long at0 = plan.at0;
-      // (A warpgroup goes through a segment as one.)
+      if (plan.first) seg0 = i;
+      // This warpgroup's first tile of the batch and of the segment.
+      const int first = (i & 1) == wg ? 0 : 1;
+      const int start = seg0 + ((seg0 & 1) == wg ? 0 : 1);
+      // (A warpgroup goes through a batch as one.)
       ok = named_bar_and(bar + 1, 128, ok);
       if (!ok) break;
-      if (count == 0) break;
-      const uint32_t o_tmem = tmem + lane_base + 4 * N + (seg & 1) * 2 * N + wg * N;
-      const int first = (i & 1) == wg ? 0 : 1;  // this warpgroup's first tile of the segment
-      const int last = i + count - 1;           // of the segment's tiles
       // A segment of one tile is its warpgroup's alone; the other one goes on
       // to the next.
-      const bool alone = count == 1;
-      if (alone && first != 0) {
-        plan_done(seg);
+      const bool alone = plan.tiles == 1;
+      if (count == 0 || (alone && first != 0)) {
+        if (done.due) ok = finish(false);
+        if (count == 0) break;
+        plan_done(b);
         ++i;
+        ++seg;
         continue;
       }
-#pragma unroll
-      for (int n = 0; n < N; ++n) l[n] = 0.f;
-      // Rows that have seen no key yet have no maximum; while there are any
-      // (`unset`), every tile takes the slow path below.
-      bool unset = true;
+      const uint32_t o_tmem = tmem + lane_base + 4 * N + (seg & 1) * 2 * N + wg * N;
       const float* c = cb->qs[seg % kPagedPlans];
       float* end_m = cb->end_m[seg % kPagedPlans][wg];
+      if (plan.first) {
+#pragma unroll
+        for (int n = 0; n < N / 2; ++n) l[n] = 0;
+        // Rows that have seen no key yet have no maximum (0 stands in for
+        // it); while there are any (`unset`), every tile takes the slow path
+        // below.
+        unset = true;
+        ok = wait(cb->qs_full[seg % kPagedPlans], (seg / kPagedPlans) & 1);
+        if (key < N) neg_m[key] = 0.f;
+        ok = named_bar_and(bar + 1, 128, ok);
+        if (!ok) break;
+        if constexpr (N == 16) {
+#pragma unroll
+          for (int n = 0; n < N; n += 2) {
+            c_held[n / 2] = pair(c, n);
+            m_held[n / 2] = 0;
+          }
+        }
+      }
       for (int t = first; t < count; t += 2) {
         const int at = i + t;  // tile of the CTA's range
         const uint32_t phase = (uint32_t)(at >> 1) & 1;
-        // (A warp whose wait has given up still joins the vote below, after
+        const PagePlan pp = plan.page[2 * t + page];
+        const float ks = pp.ks, vs = pp.vs, lv = pp.lv;
+        // Rows of several tokens see different keys: the tiles at the edges
+        // are masked row by row.
+        const long long j0 = (long long)(tile0 + t) * kTileKeys, j = j0 + key;
+        const bool all = j0 >= plan.lo && j0 + kTileKeys <= plan.hi;
+        const bool seen = j >= plan.lo && j < plan.hi && pp.held;
+        const bool edge = tok0 != tok1 && ((sh.causal && j0 + kTileKeys - 1 > at0) ||
+                                           (sh.window >= 0 && j0 < at0 + (tok1 - tok0) - sh.window));
+        // (A warp whose wait has given up still joins the votes below, after
         // which the whole warpgroup leaves.)
-        if (t == first) ok = wait(cb->qs_full[seg % kPagedPlans], (seg / kPagedPlans) & 1);
-        if (ok) ok = wait(cb->info_full[at % kPagedInfo], (at / kPagedInfo) & 1);
-        const TileInfo& ti = cb->info[at % kPagedInfo];
-        const float ks = ti.ks[page], vs = ti.vs[page], lv = ti.lv[page];
-        const bool seen = key >= ti.lo && key < ti.hi && ((ti.held >> page) & 1);
         if (ok) ok = wait(cb->s_full[wg], phase);
+        // Pt's buffer was last read by the PV of this warpgroup's last tile.
+        if (ok && at >= 2) ok = wait(cb->pv_done[wg], phase ^ 1);
         ptx::tc_fence_after();
-        float x[N];
+        const uint64_t ks2 = ptx::f2_pack(ks, ks);
+        uint64_t x[N / 2];  // score less the maximum, log2
+        // Once, or again with a new maximum.
+        for (bool settled = false;; settled = true) {
 #pragma unroll
-        for (int n0 = 0; n0 < N; n0 += 16) {
-          uint32_t hi[16], lo[16];
-          ptx::tmem_ld16(s_tmem + n0, hi);
-          ptx::tmem_ld16(s_tmem + N + n0, lo);
-          ptx::tmem_wait_ld();
-          ptx::reg_fence16(hi);
-          ptx::reg_fence16(lo);
+          for (int n0 = 0; n0 < N; n0 += 16) {
+            uint32_t qh[16], ql[16];
+            ptx::tmem_ld16(s_tmem + n0, qh);
+            ptx::tmem_ld16(s_tmem + N + n0, ql);
+            ptx::tmem_wait_ld();
+            ptx::reg_fence16(qh);
+            ptx::reg_fence16(ql);
 #pragma unroll
-          for (int n = 0; n < 16; n += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(c + n0 + n);
-            x[n0 + n] = (__uint_as_float(hi[n]) + __uint_as_float(lo[n])) * (f.x * ks);
-            x[n0 + n + 1] = (__uint_as_float(hi[n + 1]) + __uint_as_float(lo[n + 1])) * (f.y * ks);
-            x[n0 + n + 2] = (__uint_as_float(hi[n + 2]) + __uint_as_float(lo[n + 2])) * (f.z * ks);
-            x[n0 + n + 3] = (__uint_as_float(hi[n + 3]) + __uint_as_float(lo[n + 3])) * (f.w * ks);
+            for (int n = 0; n < 16; n += 2) {
+              const uint64_t c2 = N == 16 ? c_held[(n0 + n) / 2 % kHeld] : pair(c, n0 + n);
+              const uint64_t m2 = N == 16 ? m_held[(n0 + n) / 2 % kHeld] : pair(neg_m, n0 + n);
+              const uint64_t h2 = ptx::f2_pack(__uint_as_float(qh[n]), __uint_as_float(qh[n + 1]));
+              const uint64_t l2 = ptx::f2_pack(__uint_as_float(ql[n]), __uint_as_float(ql[n + 1]));
+              x[(n0 + n) / 2] = ptx::fma2(ptx::add2(h2, l2), ptx::mul2(c2, ks2), m2);
+            }
           }
-        }
-        ptx::tc_fence_before();
-        ptx::mbar_arrive(ptx::smem_u32(&cb->s_free[wg]));
-        if (!seen) {
+          if (!(all && pp.held) && !seen) {
 #pragma unroll
-          for (int n = 0; n < N; ++n) x[n] = neg_inf;
-        }
-        // Rows of several tokens see different keys: mask the tiles at the
-        // edges row by row.
-        if (tok0 != tok1) {
-          const long long j0 = (long long)(tile0 + t) * kTileKeys, j = j0 + key;
-          const bool edge = (sh.causal && j0 > at0 - (kTileKeys - 1)) ||
-                            (sh.window >= 0 && j0 < at0 + (tok1 - tok0) - sh.window);
+            for (int n = 0; n < N / 2; ++n) x[n] = ptx::f2_pack(neg_inf, neg_inf);
+          }
           if (edge) {
             for (int tok = tok0; tok <= tok1; ++tok) {
               const long long pos = at0 + (tok - tok0);
               const bool out = (sh.causal && j > pos) || (sh.window >= 0 && j < pos - sh.window);
               if (out) {
-                const int lo = tok * sh.group - row0;
+                const int r0 = tok * sh.group - row0, r1 = r0 + sh.group;
 #pragma unroll
-                for (int n = 0; n < N; ++n)
-                  if (n >= lo && n < lo + sh.group) x[n] = neg_inf;
+                for (int n = 0; n < N / 2; ++n) {
+                  float u, v;
+                  ptx::f2_unpack(x[n], u, v);
+                  if (2 * n >= r0 && 2 * n < r1) u = neg_inf;
+                  if (2 * n + 1 >= r0 && 2 * n + 1 < r1) v = neg_inf;
+                  x[n] = ptx::f2_pack(u, v);
+                }
               }
             }
           }
-        }
-        // Pt's buffer was last read by the PV of this warpgroup's last tile.
-        if (ok && at >= 2) ok = wait(cb->pv_done[wg], phase ^ 1);
-        // A new maximum is due where a score passes the old one by 2^8.
-        float over = neg_inf;
-        if (!unset) {
+          if (settled) break;
+          if (!unset) {
+            // A new maximum is due where a score passes the old one by 2^8.
+            float over = neg_inf;
 #pragma unroll
-          for (int n = 0; n < N; n += 4) {
-            const float4 m = *reinterpret_cast<const float4*>(m_used + n);
-            over = ptx::max3(over, x[n] - m.x, x[n + 1] - m.y);
-            over = ptx::max3(over, x[n + 2] - m.z, x[n + 3] - m.w);
+            for (int n = 0; n < N / 2; ++n) {
+              float u, v;
+              ptx::f2_unpack(x[n], u, v);
+              over = ptx::max3(over, u, v);
+            }
+            const int need = !ok || over + lv > kRescaleLog2 + kPagedBias;
+            if (!named_bar_or(bar, 128, need)) break;
           }
-        }
-        const int need = unset || !ok || over + lv > kRescaleLog2 + kPagedBias;
-        if (named_bar_or(bar, 128, need)) {
           ok = named_bar_and(bar + 1, 128, ok);
           if (!ok) break;
           float v[N];
 #pragma unroll
-          for (int n = 0; n < N; ++n) v[n] = x[n] + lv;
+          for (int n = 0; n < N; n += 2) {
+            const uint64_t m2 = N == 16 ? m_held[n / 2 % kHeld] : pair(neg_m, n);
+            float u0, u1, m0, m1;
+            ptx::f2_unpack(x[n / 2], u0, u1);
+            ptx::f2_unpack(m2, m0, m1);
+            v[n] = u0 - m0 + lv;
+            v[n + 1] = u1 - m1 + lv;
+          }
           warp_transpose_reduce<N, true>(v, lane);
           if ((lane & 1) == 0) {
 #pragma unroll
@@ -821,26 +971,27 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
           if (key < N) {
             const float mt = fmaxf(fmaxf(red[0][key], red[1][key]),
                                    fmaxf(red[2][key], red[3][key])) - kPagedBias;
-            const bool had = t != first && end_m[key] != neg_inf;
-            const float mu = had ? m_used[key] : neg_inf;
+            const float mu = at == start ? neg_inf : end_m[key];
             float al = 1.f;
             if (mt > mu) {
-              al = had ? ptx::ex2(mu - mt) : 0.f;
-              m_used[key] = mt;
+              al = mu == neg_inf ? 0.f : ptx::ex2(mu - mt);
+              neg_m[key] = -mt;
               end_m[key] = mt;
-            } else if (!had) {
-              m_used[key] = 0.f;
+            } else if (at == start) {
               end_m[key] = neg_inf;
             }
             none = key < rows && end_m[key] == neg_inf;
             alpha[key] = al;
           }
           unset = named_bar_or(bar, 128, none);
+          if constexpr (N == 16) {
 #pragma unroll
-          for (int n = 0; n < N; ++n) l[n] *= alpha[n];
-          if (t != first) {
+            for (int n = 0; n < N; n += 2) m_held[n / 2 % kHeld] = pair(neg_m, n);
+          }
+          if (at != start) {
+#pragma unroll
+            for (int n = 0; n < N; n += 2) l[n / 2] = ptx::mul2(l[n / 2], pair(alpha, n));
             // Ot holds this warpgroup's earlier tiles, whose last PV is done.
-            ptx::tc_fence_after();
 #pragma unroll
             for (int n0 = 0; n0 < N; n0 += 16) {
               uint32_t o[16];
@@ -855,18 +1006,22 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             ptx::tmem_wait_st();
           }
         }
+        if (!ok) break;
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(ptx::smem_u32(&cb->s_free[wg]));
         // Pt row of this key.
+        const uint64_t vs2 = ptx::f2_pack(vs, vs);
 #pragma unroll
         for (int n0 = 0; n0 < N; n0 += 8) {
           uint32_t w[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float2 m = *reinterpret_cast<const float2*>(m_used + n0 + 2 * k);
-            const float p0 = ptx::ex2(x[n0 + 2 * k] - m.x);
-            const float p1 = ptx::ex2(x[n0 + 2 * k + 1] - m.y);
-            l[n0 + 2 * k] += p0;
-            l[n0 + 2 * k + 1] += p1;
-            w[k] = ptx::pack_f16x2(p0 * vs, p1 * vs);
+            float u, v;
+            ptx::f2_unpack(x[n0 / 2 + k], u, v);
+            const uint64_t p2 = ptx::f2_pack(ptx::ex2(u), ptx::ex2(v));
+            l[n0 / 2 + k] = ptx::add2(l[n0 / 2 + k], p2);
+            ptx::f2_unpack(ptx::mul2(p2, vs2), u, v);
+            w[k] = ptx::pack_f16x2(u, v);
           }
           const int un = n0 / 8;
           const int us = N == 64 ? (un ^ (key & 7))
@@ -874,108 +1029,45 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
           *reinterpret_cast<uint4*>(prow + us * 16) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         ptx::fence_proxy_async_smem();
-        ptx::tc_fence_before();
         ptx::mbar_arrive(ptx::smem_u32(&cb->p_full[wg]));
-      }
-
-      // ------------------------------------------------------ segment output
-      // (A warpgroup that has given up joins the first barrier.)
-      i += count;
-      const int slot = 2 * cta + (seg == 0 ? 0 : 1);
-      if (ok) {
-        warp_transpose_reduce<N, false>(l, lane);
-        if ((lane & 1) == 0) {
-#pragma unroll
-          for (int k = 0; k < N / 16; ++k) red[warp & 3][16 * k + (lane >> 1)] = l[k];
+        if (at == start && done.due) {
+          ok = finish(true);
+          if (!ok) break;
         }
-        for (int k = 0; ok && k < 2 && k < count; ++k)
-          ok = wait(cb->pv_done[(last - k) & 1], ((last - k) >> 1) & 1);
-        named_bar_sync(bar + 2, 128);
-        if (key < N)
-          cb->end_l[seg % kPagedPlans][wg][key] =
-              (red[0][key] + red[1][key]) + (red[2][key] + red[3][key]);
       }
-      ok = alone ? named_bar_and(bar + 1, 128, ok) : named_bar_and(4, 256, ok);
       if (!ok) break;
-      ptx::tc_fence_after();
-      if (key < N) {
-        // Weights of the two warpgroups' Ot: 2^(m - M) / sum; a warpgroup
-        // that saw no key has m = -inf (or a NaN sum) and nothing to add.
-        const float m0 = alone ? end_m[key] : cb->end_m[seg % kPagedPlans][0][key];
-        const float m1 = alone ? neg_inf : cb->end_m[seg % kPagedPlans][1][key];
-        const float l0 = alone ? cb->end_l[seg % kPagedPlans][wg][key] : cb->end_l[seg % kPagedPlans][0][key];
-        const float l1 = alone ? 0.f : cb->end_l[seg % kPagedPlans][1][key];
-        const float top = fmaxf(m0, m1);
-        const float base = top == neg_inf ? 0.f : top;
-        const float e0 = m0 == neg_inf ? (l0 == 0.f ? 0.f : l0) : ptx::ex2(m0 - base);
-        const float e1 = m1 == neg_inf ? (l1 == 0.f ? 0.f : l1) : ptx::ex2(m1 - base);
-        const float sum = e0 * l0 + e1 * l1;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (a NaN stays one)
-        cb->weight[wg][0][key] = e0 * inv;
-        cb->weight[wg][1][key] = e1 * inv;
-        const float l2 = sum == 0.f ? neg_inf : base + log2f(sum);
-        if ((alone || wg == 0) && key < rows) {
-          if (!whole) {
-            a.part_lse[(size_t)slot * N + key] = l2;
-          } else if (a.lse) {
-            const int tok = (row0 + key) / sh.group, h = (row0 + key) - tok * sh.group;
-            a.lse[(size_t)(head * sh.group + h) * a.total_q + q0 + tok] =
-                l2 * 0.69314718055994531f;
-          }
-        }
+      i += count;
+      if (!plan.last) {
+        plan_done(b);
+        continue;
       }
-      if (unit_end >= 0 && key == 0 && (alone || wg == 0)) {
-        // The unit starts here: tell the merge how many CTAs share it.
-        int parts = 1;
-        while (cta + parts < ctas && range_start(total, ctas, cta + parts) < unit_end) ++parts;
-        a.meta[2 * cta + 1] = make_int4(rows, slot, 0, 0);
-        a.meta[2 * cta] = make_int4(parts, q0, row0, head);
+      // The segment's sums; its output comes later.
+      float v[N];
+#pragma unroll
+      for (int n = 0; n < N; n += 2) ptx::f2_unpack(l[n / 2], v[n], v[n + 1]);
+      warp_transpose_reduce<N, false>(v, lane);
+      if ((lane & 1) == 0) {
+#pragma unroll
+        for (int k = 0; k < N / 16; ++k) red[warp & 3][16 * k + (lane >> 1)] = v[k];
       }
       named_bar_sync(bar + 2, 128);
-      // Dim of this thread's lane: row of a 128-row accumulator, or of a
-      // 64-row one, which uses the first 16 lanes of each warp's 32.
-      const int d = D == 128 ? key : (warp & 3) * 16 + lane;
-      const bool live = d < a.dim && (D == 128 || lane < 16);
-      const uint32_t o0 = tmem + lane_base + 4 * N + (seg & 1) * 2 * N;
-      // Rows: eight at a time by each warpgroup in turn, or all by the one
-      // that is alone, whose Ot is then the only one.
-#pragma unroll 1
-      for (int n0 = alone ? 0 : 8 * wg; n0 < rows; n0 += alone ? 8 : 16) {
-        uint32_t oa[8], ob[8];
-        ptx::tmem_ld8(o0 + (alone ? wg * N : 0) + n0, oa);
-        ptx::tmem_ld8(o0 + (alone ? wg * N : N) + n0, ob);
-        ptx::tmem_wait_ld();
-        ptx::reg_fence8(oa);
-        ptx::reg_fence8(ob);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int n = n0 + k;
-          if (live && n < rows) {
-            // (Weight 0: the Ot may hold anything.)
-            const float wa = cb->weight[wg][0][n], wb = cb->weight[wg][1][n];
-            const float v = (wa == 0.f ? 0.f : wa * __uint_as_float(oa[k])) +
-                            (wb == 0.f ? 0.f : wb * __uint_as_float(ob[k]));
-            if (whole) {
-              const int tok = (row0 + n) / sh.group, h = (row0 + n) - tok * sh.group;
-              a.out[((size_t)(q0 + tok) * a.heads + head * sh.group + h) * a.dim + d] =
-                  (uint16_t)ptx::pack_bf16x2(v, 0.f);
-            } else {
-              a.part_o[((size_t)slot * N + n) * D + d] = v;
-            }
-          }
-        }
-      }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        const uint32_t bar_o = ptx::smem_u32(&cb->o_free[seg & 1]);
-        ptx::mbar_arrive(bar_o);
-        if (alone) ptx::mbar_arrive(bar_o);  // for the other warpgroup
-      }
-      // Only now: the planner writes over this segment's row scales, and the
-      // other warpgroup over its maxima, four segments on at the earliest.
-      plan_done(seg);
+      if (key < N)
+        cb->end_l[seg % kPagedPlans][wg][key] =
+            (red[0][key] + red[1][key]) + (red[2][key] + red[3][key]);
+      done.seg = seg;
+      done.batch = b;
+      done.last = i - 1;
+      done.q0 = plan.q0;
+      done.row0 = row0;
+      done.rows = rows;
+      done.head = plan.head;
+      done.alone = alone;
+      done.whole = plan.whole;
+      done.unit_end = plan.unit_end;
+      done.due = true;
+      ++seg;
     }
+    if (!parted) named_bar_and(4, 256, ok);
   }
 
   ptx::tc_fence_before();
