@@ -117,6 +117,7 @@ struct alignas(16) BatchPlan {
   int first, last;             // it begins, ends the segment
   int lo, hi;                  // keys that some row of the segment sees
   int head, q0, row0, rows;    // first q row of the sequence; rows of the tile
+  int out[64], lse[64];        // of each row: its place in O (rows) and in the LSE
   int tok0, tok1;              // tokens of its first and last row
   long long at0;               // position of tok0
   int tiles;                   // of the segment
@@ -187,29 +188,49 @@ constexpr size_t paged_smem() {
 static_assert(paged_smem<128, 64>() <= 232448, "shared memory exceeds the per-CTA limit");
 static_assert(paged_smem<128, 32>() <= 232448, "shared memory exceeds the per-CTA limit");
 
-// Maximum (kMax) or sum over the 32 lanes of a warp of each of V values (V a
-// multiple of 16 up to 64), by repeated halving.  Lane l ends with value
-// l / 2 of each 16 in v[g], g < V / 16 (both lanes of a pair hold it).
-template <int V, bool kMax>
-__device__ __forceinline__ void warp_transpose_reduce(float* v, int lane) {
-#pragma unroll
-  for (int g = 0; g < V / 16; ++g) {
-    float* x = v + 16 * g;
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int o = 16 >> s, half = 8 >> s;
-      const bool upper = (lane & o) != 0;
-#pragma unroll
-      for (int i = 0; i < half; ++i) {
-        const float send = upper ? x[i] : x[i + half];
-        const float keep = upper ? x[i + half] : x[i];
-        const float recv = __shfl_xor_sync(0xffffffffu, send, o);
-        x[i] = kMax ? fmaxf(keep, recv) : keep + recv;
+// Bounded wait of a warp (see wait_warp), in as few instructions as will do:
+// the clock starts at the 256th probe.  (A launch reads the kernel's
+// instructions from L2 or DRAM beside the cache's bytes, and there are many
+// waits in it.)
+__device__ __forceinline__ bool paged_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                           unsigned int* status, uint64_t limit_ns) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t spin = 1; !__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity)); ++spin) {
+    if ((spin & 255u) != 0 && limit_ns >= kShortWaitNs) continue;
+    int give_up = 0;
+    if ((threadIdx.x & 31) == 0) {
+      const uint64_t now = ptx::globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > limit_ns) {
+        atomicOr(status, kStatusTimeout);
+        *abort_flag = 1;
       }
+      give_up = *abort_flag;
     }
-    const float recv = __shfl_xor_sync(0xffffffffu, x[0], 1);
-    v[g] = kMax ? fmaxf(x[0], recv) : x[0] + recv;
+    if (__shfl_sync(0xffffffffu, give_up, 0)) return false;
   }
+  return true;
+}
+
+// Maximum (kMax) or sum over the 32 lanes of a warp of each of 16 values, by
+// repeated halving: lanes 2k and 2k + 1 return that of value k.
+template <bool kMax>
+__device__ __forceinline__ float warp_transpose_reduce16(float* x, int lane) {
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int o = 16 >> s, half = 8 >> s;
+    const bool upper = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float send = upper ? x[i] : x[i + half];
+      const float keep = upper ? x[i + half] : x[i];
+      const float recv = __shfl_xor_sync(0xffffffffu, send, o);
+      x[i] = kMax ? fmaxf(keep, recv) : keep + recv;
+    }
+  }
+  const float recv = __shfl_xor_sync(0xffffffffu, x[0], 1);
+  return kMax ? fmaxf(x[0], recv) : x[0] + recv;
 }
 
 template <int D, int N>
@@ -232,6 +253,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   ptx::grid_launch_dependents();
   if (warp == kLoadWarp && lane == 0) {
     auto init = [&](uint64_t& b, uint32_t n) { ptx::mbar_init(ptx::smem_u32(&b), n); };
+#pragma unroll 1
     for (int s = 0; s < 4; ++s) {
       init(cb->plan_full[s], 1);
       init(cb->plan_free[s], kPlanReaders);
@@ -271,6 +293,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       a.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
     }
     long long base = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < a.batch; b0 += 256) {
       const int b = b0 + tid;
       int n = 0;
@@ -308,7 +331,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   const int cta = blockIdx.x, ctas = gridDim.x;
   // Slot n of a ring of size R: slot n % R, phase parity (n / R) & 1.
   auto wait = [&](uint64_t& b, int parity) {
-    return wait_warp(ptx::smem_u32(&b), (uint32_t)parity, abort_flag, a.status, a.wait_limit_ns);
+    return paged_wait(ptx::smem_u32(&b), (uint32_t)parity, abort_flag, a.status, a.wait_limit_ns);
   };
   // Batch number b of the range; every warp that reads it lets it go with
   // plan_done once it has what it needs.
@@ -354,6 +377,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       if (!ok) break;
       const unsigned held = __ballot_sync(0xffffffffu, plan.page[lane].held != 0);
       plan_done(b);
+#pragma unroll 1
       for (int n = 0; n < count; ++n, ++i) {
         const int hb = i & 1;
         ok = wait(cb->v_full[slot], v_phase);
@@ -418,6 +442,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
           qd = ptx::smem_desc(ptx::smem_u32(smem + C::kQ + qb * C::kQBytes), 16, 8 * C::kRow,
                               C::kSwK);
         }
+#pragma unroll 1
         for (int n = 0; n < count; ++n, ++i) {
           ok = wait(cb->k_full[slot], k_phase);
           if (ok && i >= 2) ok = wait(cb->s_free[i & 1], ((i >> 1) - 1) & 1);
@@ -453,6 +478,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         plan_done(b);
         if (count == 0) break;
         if (in_seg == 0 && seg >= 2) ok = wait(cb->o_free[seg & 1], ((seg >> 1) - 1) & 1);
+#pragma unroll 1
         for (int n = 0; ok && n < count; ++n, ++i, ++in_seg) {
           const int hb = i & 1;
           ok = wait(cb->vh_full[hb], (i >> 1) & 1);
@@ -492,6 +518,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         const int cell = plan.cell[lane];
         plan_done(b);
         if (count == 0) break;
+#pragma unroll 1
         for (int n = 0; n < count; ++n) {
           const int mine = __shfl_sync(0xffffffffu, cell, 2 * n + (lane & 1));
           const unsigned held = __ballot_sync(0xffffffffu, mine >= 0) & 3;
@@ -522,8 +549,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         }
       }
       // Every copy this CTA started lands before it exits.
+#pragma unroll 1
       for (int s = 0; s < C::NK && s < kn; ++s)
         wait_drain_warp(ptx::smem_u32(&cb->k_full[s]), ((kn - 1 - s) / C::NK) & 1, a.status);
+#pragma unroll 1
       for (int s = 0; s < C::NV && s < vn; ++s)
         wait_drain_warp(ptx::smem_u32(&cb->v_full[s]), ((vn - 1 - s) / C::NV) & 1, a.status);
     } else {
@@ -536,7 +565,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       walk_begin(&walk, range_start(total, ctas, cta), range_start(total, ctas, cta + 1), a.batch,
                  before);
       Segment g = {};
-      int n0 = 0;  // tiles of the segment in earlier batches
+      int n0;  // tiles of the segment in earlier batches
       // Lane l: page l of the batch's tiles, as its cell of the cache, or -1
       // where it is not needed or not there.
       auto cells = [&]() {
@@ -548,138 +577,170 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             __ldg(a.page_table + (size_t)g.seq * a.max_pages + p), a.num_pages);
         return id < 0 ? -1 : id * sh.heads_k + g.head;
       };
-      bool more = walk_next(&walk, sh, before, seq_of, &g);
-      int cell = more ? cells() : -1;
+      bool more = true, last = true;
+      int cell = -1, seg = 0;
       bool ok = true;
-      int seg = 0;
-      for (int b = 0;; ++b) {
-        const int slot = b % kPagedPlans;
-        if (b >= kPagedPlans) ok = wait(cb->plan_free[slot], (b / kPagedPlans - 1) & 1);
-        if (!ok) break;
+      n0 = -kPlanTiles;
+      for (int b = -1;; ++b) {
+        const int slot = b & (kPagedPlans - 1);
         BatchPlan& plan = cb->plan[slot];
-        if (!more) {
-          if (lane == 0) {
-            plan.count = 0;
-            ptx::mbar_arrive(ptx::smem_u32(&cb->plan_full[slot]));
-          }
-          break;
-        }
-        const int head = g.head, group = sh.group, q0 = g.q.lo;
-        const int row0 = g.row_tile * N, rows = imin(N, g.q.n * group - row0);
-        const bool first = n0 == 0, last = g.count - n0 <= kPlanTiles;
+        const bool first = n0 == 0, ends = last;
         uint4 raw[kBatch];
+        int rows = 0, row_q = 0, row_h = 0;  // rows; lane's row: token and head
         auto load_rows = [&](int j0) {
 #pragma unroll
           for (int j = 0; j < kBatch; ++j) {
             const int n = j0 + j * kGroups + lane / kLanes;
+            const int tok = __shfl_sync(0xffffffffu, row_q, n & 31);
+            const int h = __shfl_sync(0xffffffffu, row_h, n & 31);
             raw[j] = make_uint4(0u, 0u, 0u, 0u);
-            if (n < rows && dim0 < a.dim) {
-              const int tok = (row0 + n) / group, h = (row0 + n) - tok * group;
+            if (n < rows && dim0 < a.dim)
               raw[j] = __ldg(reinterpret_cast<const uint4*>(
-                  a.q + (long long)(q0 + tok) * a.q_row + (long long)(head * group + h) * a.q_head +
-                  dim0));
-            }
+                  a.q + (long long)tok * a.q_row + (long long)h * a.q_head + dim0));
           }
         };
-        if (first) load_rows(0);  // (ahead of the pages' loads in the memory system)
-        plan.cell[lane] = cell;
-        if (lane == 0) {
-          plan.count = imin(g.count - n0, kPlanTiles);
-          plan.tile0 = g.tile0 + n0;
-          plan.first = first;
-          plan.last = last;
-          plan.lo = g.keys.lo;
-          plan.hi = g.keys.hi;
-          plan.head = head;
-          plan.q0 = q0;
-          plan.row0 = row0;
-          plan.rows = rows;
-          plan.tok0 = row0 / group;
-          plan.tok1 = (row0 + rows - 1) / group;
-          plan.at0 = (long long)g.len - g.q.n + plan.tok0;
-          plan.tiles = g.count;
-          plan.whole = g.count == g.unit_count;
-          plan.unit_end =
-              g.part_lo == 0 && g.count < g.unit_count ? walk.at - g.count + g.unit_count : -1;
-        }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->plan_full[slot]));
-        // The scales under way, then the next batch's pages.
-        const int held = cell >= 0;
-        const float ks = held ? __ldg(a.k_scale + cell) : 0.f;
-        const float vs = held ? __ldg(a.v_scale + cell) : 0.f;
-        auto advance = [&]() {
-          n0 += kPlanTiles;
-          if (last) {
-            n0 = 0;
-            more = walk_next(&walk, sh, before, seq_of, &g);
-          }
-          cell = more ? cells() : -1;
+        auto place_rows = [&](int n0r) {  // rows n0r + lane: token, head
+          const int row = g.row_tile * N + n0r + lane;
+          const int tok = (int)((unsigned)row / (unsigned)sh.group);
+          row_q = g.q.lo + tok;
+          row_h = g.head * sh.group + row - tok * sh.group;
         };
-        // (The first segment's S waits for its Q: look ahead after that.)
-        if (b > 0) advance();
-        plan.page[lane] = {ks, vs, fmaxf(log2f(vs), -(float)kScaleExpMax), held};
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->scale_full[slot]));
-        if (first) {
-          const int qb = seg % C::NQ;
-          if (seg >= C::NQ) ok = wait(cb->q_free[qb], (seg / C::NQ - 1) & 1);
+        float ks = 0.f, vs = 0.f;
+        if (b >= 0) {
+          if (b >= kPagedPlans) ok = wait(cb->plan_free[slot], (b / kPagedPlans - 1) & 1);
           if (!ok) break;
-          uint8_t* q_s = smem + C::kQ + qb * C::kQBytes;  // N rows of hi, N of lo
-          for (int j0 = 0; j0 < N; j0 += kGroups * kBatch) {
-            if (j0 > 0) load_rows(j0);
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-              const int n = j0 + j * kGroups + lane / kLanes;
-              float x[8];
-              unpack_bf16x8(raw[j], x);
-              float mx = 0.f;
-              bool finite = true;
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                finite = finite && fabsf(x[k]) <= 3.402823466e38f;
-                mx = fmaxf(mx, fabsf(x[k]));
-              }
-              // A row with an infinity or a NaN gets NaN scores.
-              if (!finite) mx = __int_as_float(0x7f800000);
-#pragma unroll
-              for (int o = kLanes / 2; o > 0; o >>= 1)
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-              // mx in [2^e, 2^(e+1)) goes to [128, 256).  (Rows below 2^-100
-              // keep a smaller size; their scores are zero in fp32 all the
-              // same.)
-              const int e = imax((int)(__float_as_uint(mx) >> 23) - 127, -100);
-              const float f = __uint_as_float((uint32_t)(7 - e + 127) << 23);
-              uint32_t hi[4], lo[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float y0 = x[2 * k] * f, y1 = x[2 * k + 1] * f;
-                hi[k] = pack_e4m3x2(y0, y1);
-                const float2 h2 = f16x2_floats(unpack_e4m3x2(hi[k]));
-                lo[k] = pack_e4m3x2(y0 - h2.x, y1 - h2.y);
-              }
-              auto place = [&](int r) {
-                const int unit = dim0 >> 4;
-                const int us = D == 128 ? (unit ^ (r & 7)) : (unit ^ ((r >> 1) & 3));
-                return r * C::kRow + us * 16 + (dim0 & 8);
-              };
-              *reinterpret_cast<uint2*>(q_s + place(n)) =
-                  make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-              *reinterpret_cast<uint2*>(q_s + place(N + n)) =
-                  make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-              if (sub == 0)
-                cb->qs[seg % kPagedPlans][n] =
-                    mx < __int_as_float(0x7f800000)
-                        ? a.scale_log2 * __uint_as_float((uint32_t)(e - 7 + 127) << 23)
-                        : __int_as_float(0x7fffffff);
+          if (!more) {
+            if (lane == 0) {
+              plan.count = 0;
+              ptx::mbar_arrive(ptx::smem_u32(&cb->plan_full[slot]));
+            }
+            break;
+          }
+          rows = imin(N, g.q.n * sh.group - g.row_tile * N);
+#pragma unroll 1
+          for (int n = N > 32 ? 32 : 0; n >= 0; n -= 32) {
+            place_rows(n);
+            if (n + lane < N) {
+              plan.out[n + lane] = row_q * a.heads + row_h;
+              plan.lse[n + lane] = row_h * a.total_q + row_q;
             }
           }
-          ptx::fence_proxy_async_smem();
-          ptx::mbar_arrive(ptx::smem_u32(&cb->qs_full[seg % kPagedPlans]));
-          ptx::mbar_arrive(ptx::smem_u32(&cb->q_full[qb]));
+          if (first) load_rows(0);  // (ahead of the pages' loads in the memory system)
+          plan.cell[lane] = cell;
+          if (lane == 0) {
+            const int row0 = g.row_tile * N;
+            plan.count = imin(g.count - n0, kPlanTiles);
+            plan.tile0 = g.tile0 + n0;
+            plan.first = first;
+            plan.last = ends;
+            plan.lo = g.keys.lo;
+            plan.hi = g.keys.hi;
+            plan.head = g.head;
+            plan.q0 = g.q.lo;
+            plan.row0 = row0;
+            plan.rows = rows;
+            plan.tok0 = row0 / sh.group;
+            plan.tok1 = (row0 + rows - 1) / sh.group;
+            plan.at0 = (long long)g.len - g.q.n + plan.tok0;
+            plan.tiles = g.count;
+            plan.whole = g.count == g.unit_count;
+            plan.unit_end =
+                g.part_lo == 0 && g.count < g.unit_count ? walk.at - g.count + g.unit_count : -1;
+          }
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->plan_full[slot]));
+          // The scales under way.
+          if (cell >= 0) {
+            ks = __ldg(a.k_scale + cell);
+            vs = __ldg(a.v_scale + cell);
+          }
         }
-        if (last) ++seg;
-        if (b == 0) advance();
+        const int held = cell >= 0;
+        // Then the next batch's pages and this one's scales and Q, in this
+        // order but for the first, whose Q is waited for.
+#pragma unroll 1
+        for (int step = 0; step < 2; ++step) {
+          if ((step == 0) == (b != 0)) {
+            // ---- on to the next batch
+            n0 += kPlanTiles;
+            if (ends) {
+              n0 = 0;
+              more = walk_next(&walk, sh, before, seq_of, &g);
+            }
+            last = g.count - n0 <= kPlanTiles;
+            cell = more ? cells() : -1;
+          } else if (b >= 0) {
+            // ---- scales and Q
+            plan.page[lane] = {ks, vs, fmaxf(log2f(vs), -(float)kScaleExpMax), held};
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->scale_full[slot]));
+            if (!first) continue;
+            const int qb = seg % C::NQ;
+            if (seg >= C::NQ) ok = wait(cb->q_free[qb], (seg / C::NQ - 1) & 1);
+            if (!ok) break;
+            uint8_t* q_s = smem + C::kQ + qb * C::kQBytes;  // N rows of hi, N of lo
+#pragma unroll 1
+            for (int j0 = 0; j0 < N; j0 += kGroups * kBatch) {
+              if (j0 > 0) {
+                // (Row numbers of the second 32 rows replace the first's.)
+                if (N > 32 && j0 == 32) {
+                  row_q = plan.out[32 + lane] / a.heads;
+                  row_h = plan.out[32 + lane] - row_q * a.heads;
+                }
+                load_rows(j0);
+              }
+#pragma unroll 1
+              for (int j = 0; j < kBatch; ++j) {
+                const int n = j0 + j * kGroups + lane / kLanes;
+                float x[8];
+                unpack_bf16x8(raw[j], x);
+                float mx = 0.f;
+                bool finite = true;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  finite = finite && fabsf(x[k]) <= 3.402823466e38f;
+                  mx = fmaxf(mx, fabsf(x[k]));
+                }
+                // A row with an infinity or a NaN gets NaN scores.
+                if (!finite) mx = __int_as_float(0x7f800000);
+#pragma unroll
+                for (int o = kLanes / 2; o > 0; o >>= 1)
+                  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                // mx in [2^e, 2^(e+1)) goes to [128, 256).  (Rows below 2^-100
+                // keep a smaller size; their scores are zero in fp32 all the
+                // same.)
+                const int e = imax((int)(__float_as_uint(mx) >> 23) - 127, -100);
+                const float f = __uint_as_float((uint32_t)(7 - e + 127) << 23);
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const float y0 = x[2 * k] * f, y1 = x[2 * k + 1] * f;
+                  hi[k] = pack_e4m3x2(y0, y1);
+                  const float2 h2 = f16x2_floats(unpack_e4m3x2(hi[k]));
+                  lo[k] = pack_e4m3x2(y0 - h2.x, y1 - h2.y);
+                }
+                // (Rows n and N + n have the same place in the swizzle.)
+                const int unit = dim0 >> 4;
+                const int us = D == 128 ? (unit ^ (n & 7)) : (unit ^ ((n >> 1) & 3));
+                uint8_t* at = q_s + n * C::kRow + us * 16 + (dim0 & 8);
+                *reinterpret_cast<uint2*>(at) =
+                    make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+                *reinterpret_cast<uint2*>(at + N * C::kRow) =
+                    make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+                if (sub == 0)
+                  cb->qs[seg % kPagedPlans][n] =
+                      mx < __int_as_float(0x7f800000)
+                          ? a.scale_log2 * __uint_as_float((uint32_t)(e - 7 + 127) << 23)
+                          : __int_as_float(0x7fffffff);
+              }
+            }
+            ptx::fence_proxy_async_smem();
+            ptx::mbar_arrive(ptx::smem_u32(&cb->qs_full[seg % kPagedPlans]));
+            ptx::mbar_arrive(ptx::smem_u32(&cb->q_full[qb]));
+          }
+        }
+        if (!ok) break;
+        if (b >= 0 && ends) ++seg;
       }
     }
   } else {
@@ -708,9 +769,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     // The output of a segment is written once the next one's first tile is
     // under way (`due`), by when its last P V has long been done.
     struct {
-      int seg, batch, last, q0, row0, rows, head;
-      bool alone, whole, due;
-      int unit_end;
+      int seg, batch, last;
+      bool alone, due;
     } done;
     done.due = false;
     // The warpgroups meet at barrier 4, once for each segment they share and
@@ -724,7 +784,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     auto finish = [&](bool later) -> bool {
       done.due = false;
       const bool alone = done.alone;
-      const int rows = done.rows, row0 = done.row0, head = done.head;
+      const BatchPlan& plan = cb->plan[done.batch % kPagedPlans];  // the segment's last
+      const int rows = plan.rows;
       const int ring = done.seg % kPagedPlans;
       const int slot = 2 * cta + (done.seg == 0 ? 0 : 1);
       const int mine = (done.last & 1) == wg ? done.last : done.last - 1;
@@ -759,22 +820,20 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
           wb[r] = e1 * inv;
           if (n < rows && (warp & 3) == 0 && (alone || wg == 0)) {
             const float l2 = sum == 0.f ? neg_inf : base + log2f(sum);
-            if (!done.whole) {
+            if (!plan.whole)
               a.part_lse[(size_t)slot * N + n] = l2;
-            } else if (a.lse) {
-              const int tok = (row0 + n) / sh.group, h = (row0 + n) - tok * sh.group;
-              a.lse[(size_t)(head * sh.group + h) * a.total_q + done.q0 + tok] =
-                  l2 * 0.69314718055994531f;
-            }
+            else if (a.lse)
+              a.lse[plan.lse[n]] = l2 * 0.69314718055994531f;
           }
         }
       }
-      if (done.unit_end >= 0 && key == 0 && (alone || wg == 0)) {
+      if (plan.unit_end >= 0 && key == 0 && (alone || wg == 0)) {
         // The unit starts here: tell the merge how many CTAs share it.
         int parts = 1;
-        while (cta + parts < ctas && range_start(total, ctas, cta + parts) < done.unit_end) ++parts;
+#pragma unroll 1
+        while (cta + parts < ctas && range_start(total, ctas, cta + parts) < plan.unit_end) ++parts;
         a.meta[2 * cta + 1] = make_int4(rows, slot, 0, 0);
-        a.meta[2 * cta] = make_int4(parts, done.q0, row0, head);
+        a.meta[2 * cta] = make_int4(parts, plan.q0, plan.row0, plan.head);
       }
       // Dim of this thread's lane: row of a 128-row accumulator, or of a
       // 64-row one, which uses the first 16 lanes of each warp's 32.
@@ -791,7 +850,6 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         ptx::tmem_wait_ld();
         ptx::reg_fence8(oa);
         ptx::reg_fence8(ob);
-        int tok = (row0 + n0) / sh.group, h = (row0 + n0) - tok * sh.group;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int n = n0 + k;
@@ -801,16 +859,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             // (Weight 0: the Ot may hold anything.)
             const float v = (fa == 0.f ? 0.f : fa * __uint_as_float(oa[k])) +
                             (fb == 0.f ? 0.f : fb * __uint_as_float(ob[k]));
-            if (done.whole) {
-              a.out[((size_t)(done.q0 + tok) * a.heads + head * sh.group + h) * a.dim + d] =
-                  (uint16_t)ptx::pack_bf16x2(v, 0.f);
-            } else {
+            if (plan.whole)
+              a.out[(size_t)plan.out[n] * a.dim + d] = (uint16_t)ptx::pack_bf16x2(v, 0.f);
+            else
               a.part_o[((size_t)slot * N + n) * D + d] = v;
-            }
-          }
-          if (++h == sh.group) {
-            h = 0;
-            ++tok;
           }
         }
       }
@@ -846,18 +898,11 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       // A segment of one tile is its warpgroup's alone; the other one goes on
       // to the next.
       const bool alone = plan.tiles == 1;
-      if (count == 0 || (alone && first != 0)) {
-        if (done.due) ok = finish(false);
-        if (count == 0) break;
-        plan_done(b);
-        ++i;
-        ++seg;
-        continue;
-      }
+      const bool skip = count == 0 || (alone && first != 0);
       const uint32_t o_tmem = tmem + lane_base + 4 * N + (seg & 1) * 2 * N + wg * N;
       const float* c = cb->qs[seg % kPagedPlans];
       float* end_m = cb->end_m[seg % kPagedPlans][wg];
-      if (plan.first) {
+      if (plan.first && !skip) {
 #pragma unroll
         for (int n = 0; n < N / 2; ++n) l[n] = 0;
         // Rows that have seen no key yet have no maximum (0 stands in for
@@ -876,8 +921,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
           }
         }
       }
-      for (int t = first; t < count; t += 2) {
+      // The batch's tiles; a batch that is skipped comes by for what is due.
+      for (int t = first; t < count || skip; t += 2) {
         const int at = i + t;  // tile of the CTA's range
+        if (!skip) {
         const uint32_t phase = (uint32_t)(at >> 1) & 1;
         const PagePlan pp = plan.page[2 * t + page];
         const float ks = pp.ks, vs = pp.vs, lv = pp.lv;
@@ -920,6 +967,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             for (int n = 0; n < N / 2; ++n) x[n] = ptx::f2_pack(neg_inf, neg_inf);
           }
           if (edge) {
+#pragma unroll 1
             for (int tok = tok0; tok <= tok1; ++tok) {
               const long long pos = at0 + (tok - tok0);
               const bool out = (sh.causal && j > pos) || (sh.window >= 0 && j < pos - sh.window);
@@ -951,20 +999,20 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
           }
           ok = named_bar_and(bar + 1, 128, ok);
           if (!ok) break;
-          float v[N];
 #pragma unroll
-          for (int n = 0; n < N; n += 2) {
-            const uint64_t m2 = N == 16 ? m_held[n / 2 % kHeld] : pair(neg_m, n);
-            float u0, u1, m0, m1;
-            ptx::f2_unpack(x[n / 2], u0, u1);
-            ptx::f2_unpack(m2, m0, m1);
-            v[n] = u0 - m0 + lv;
-            v[n + 1] = u1 - m1 + lv;
-          }
-          warp_transpose_reduce<N, true>(v, lane);
-          if ((lane & 1) == 0) {
+          for (int n0 = 0; n0 < N; n0 += 16) {
+            float v[16];
 #pragma unroll
-            for (int k = 0; k < N / 16; ++k) red[warp & 3][16 * k + (lane >> 1)] = v[k];
+            for (int n = 0; n < 16; n += 2) {
+              const uint64_t m2 = N == 16 ? m_held[n / 2 % kHeld] : pair(neg_m, n0 + n);
+              float u0, u1, m0, m1;
+              ptx::f2_unpack(x[(n0 + n) / 2], u0, u1);
+              ptx::f2_unpack(m2, m0, m1);
+              v[n] = u0 - m0 + lv;
+              v[n + 1] = u1 - m1 + lv;
+            }
+            const float top = warp_transpose_reduce16<true>(v, lane);
+            if ((lane & 1) == 0) red[warp & 3][n0 + (lane >> 1)] = top;
           }
           named_bar_sync(bar + 2, 128);
           int none = 0;
@@ -1030,25 +1078,30 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         }
         ptx::fence_proxy_async_smem();
         ptx::mbar_arrive(ptx::smem_u32(&cb->p_full[wg]));
-        if (at == start && done.due) {
-          ok = finish(true);
-          if (!ok) break;
         }
+        if (done.due && (skip || at == start)) ok = finish(!skip);
+        if (skip || !ok) break;
       }
-      if (!ok) break;
+      if (!ok || count == 0) break;
+      if (skip) {
+        plan_done(b);
+        ++i;
+        ++seg;
+        continue;
+      }
       i += count;
       if (!plan.last) {
         plan_done(b);
         continue;
       }
       // The segment's sums; its output comes later.
-      float v[N];
 #pragma unroll
-      for (int n = 0; n < N; n += 2) ptx::f2_unpack(l[n / 2], v[n], v[n + 1]);
-      warp_transpose_reduce<N, false>(v, lane);
-      if ((lane & 1) == 0) {
+      for (int n0 = 0; n0 < N; n0 += 16) {
+        float v[16];
 #pragma unroll
-        for (int k = 0; k < N / 16; ++k) red[warp & 3][16 * k + (lane >> 1)] = v[k];
+        for (int n = 0; n < 16; n += 2) ptx::f2_unpack(l[(n0 + n) / 2], v[n], v[n + 1]);
+        const float sum = warp_transpose_reduce16<false>(v, lane);
+        if ((lane & 1) == 0) red[warp & 3][n0 + (lane >> 1)] = sum;
       }
       named_bar_sync(bar + 2, 128);
       if (key < N)
@@ -1057,13 +1110,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       done.seg = seg;
       done.batch = b;
       done.last = i - 1;
-      done.q0 = plan.q0;
-      done.row0 = row0;
-      done.rows = rows;
-      done.head = plan.head;
       done.alone = alone;
-      done.whole = plan.whole;
-      done.unit_end = plan.unit_end;
       done.due = true;
       ++seg;
     }

@@ -10,8 +10,10 @@
 
 #if defined(__CUDACC__)
 #define FA_HD __host__ __device__ __forceinline__
+#define FA_ROLLED _Pragma("unroll 1")  // short code over speed
 #else
 #define FA_HD inline
+#define FA_ROLLED
 #endif
 
 namespace fa {
@@ -137,6 +139,7 @@ FA_HD TileRange key_tiles(const KeyRange& k) {
 FA_HD long long head_tiles(const AttnShape& s, int n, int len) {
   long long sum = 0;
   const int m = n > 0 ? row_tiles(s, n) : 0;
+  FA_ROLLED
   for (int t = 0; t < m; ++t) sum += key_tiles(tile_keys(s, t, n, len)).count;
   return sum;
 }
@@ -177,6 +180,7 @@ FA_HD void walk_begin(SegmentWalk* w, int lo, int hi, int batch, const Before& b
   w->at = lo;
   w->end = hi;
   int a = 0, b = batch;  // before(a) <= lo < before(b)
+  FA_ROLLED
   while (b - a > 1) {
     const int m = (a + b) >> 1;
     if (before(m) <= lo) a = m; else b = m;
@@ -194,6 +198,7 @@ FA_HD bool walk_next(SegmentWalk* w, const AttnShape& s, const Before& before, c
                      Segment* g) {
   if (w->at >= w->end) return false;
   if (w->head < 0) {
+    FA_ROLLED
     while (before(w->seq + 1) <= w->at) ++w->seq;  // sequences without query rows
     seq_of(w->seq, &g->q, &g->len);
     const int in_seq = w->at - before(w->seq);
@@ -201,6 +206,7 @@ FA_HD bool walk_next(SegmentWalk* w, const AttnShape& s, const Before& before, c
     w->head = (int)((unsigned)in_seq / (unsigned)per_head);
     int left = in_seq - w->head * per_head;
     w->row_tile = 0;
+    FA_ROLLED
     for (;;) {
       const int c = key_tiles(tile_keys(s, w->row_tile, g->q.n, g->len)).count;
       if (left < c) break;
