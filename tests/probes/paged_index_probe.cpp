@@ -45,8 +45,8 @@ extern "C" int probe_walk(const int* cu, const int* lens, int batch, int total_q
     fa::RowRange q;
     int len;
     seq_of(b, &q, &len);
-    sum += heads_k * fa::head_tiles(s, q.n, len);
-    pre[b + 1] = fa::capped_tiles(sum);
+    sum += heads_k * fa::head_cost(s, q.n, len);
+    pre[b + 1] = fa::capped_cost(sum);
   }
   auto before = [&](int b) { return pre[b]; };
   int found = 0;
@@ -57,7 +57,14 @@ extern "C" int probe_walk(const int* cu, const int* lens, int batch, int total_q
                    batch, before);
     while (fa::walk_next(&w, s, before, seq_of, &g)) {
       if (found == most) return -1;
-      const int v[8] = {c, g.seq, g.head, g.row_tile, g.tile0, g.count, g.part_lo, g.unit_count};
+      // A part that is not the unit's last ends where the CTA's range does.
+      if (g.part_lo + g.count < g.unit_count && w.at != w.end) return -2;
+      // The parts a merge would look for: CTAs whose range starts in the unit.
+      int parts = 1;
+      while (c + parts < ctas && fa::range_start(pre[batch], ctas, c + parts) < g.unit_end) ++parts;
+      const int v[8] = {c,      g.seq,   g.head,    g.row_tile,
+                        g.tile0, g.count, g.part_lo, g.part_lo == 0 ? g.unit_count + 65536 * parts
+                                                                     : g.unit_count};
       for (int k = 0; k < 8; ++k) out[8 * found + k] = v[k];
       ++found;
     }

@@ -316,13 +316,19 @@ def test_segments_cover_every_tile_once(probe):
                     lo = max(0, ln - n + i0 - window) if window >= 0 else 0
                     want[b, h, t] = (lo // 128, -(-hi // 128)) if hi > lo else None
         got = {}
-        per_cta = [0] * ctas
+        where = {}
+        expect = {}
         for c, b, h, t, tile0, count, part_lo, unit_count in segs:
+            if part_lo == 0:
+                expect[b, h, t] = unit_count >> 16
+                unit_count &= 65535
             assert count > 0 and 0 <= part_lo and part_lo + count <= unit_count
-            per_cta[c] += count
+            where.setdefault((b, h, t), []).append(c)
             got.setdefault((b, h, t), []).append((tile0, count, part_lo, unit_count))
         assert set(got) == set(want)
-        assert max(per_cta) - min(per_cta) <= 1
+        # A split unit's parts are in neighbouring CTAs, as many as announced.
+        for key, cs in where.items():
+            assert cs == list(range(cs[0], cs[0] + len(cs))) and len(cs) == expect[key]
         for key, parts in got.items():
             at = parts[0][0]
             assert parts[0][2] == 0
@@ -337,4 +343,4 @@ def test_segments_cover_every_tile_once(probe):
         # At most a CTA's first and last segment hold part of a unit.
         for c in range(ctas):
             mine = [s for s in segs if s[0] == c]
-            assert all(s[5] == s[7] for s in mine[1:-1])
+            assert all(s[5] == s[7] & 65535 for s in mine[1:-1])

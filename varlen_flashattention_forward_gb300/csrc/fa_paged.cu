@@ -363,9 +363,10 @@ extern "C" fa_status fa_paged_attn(const void* q, long long q_row_stride, long l
   // memory and numbers its tiles in 32 bits; a larger batch runs as
   // consecutive launches, which share the workspace in stream order.
   const long long per_row_tile =
-      (long long)num_heads_k * ((long long)max_pages_per_seq * fa::kPageTokens / fa::kTileKeys + 1);
+      (long long)num_heads_k *
+      ((long long)max_pages_per_seq * fa::kPageTokens / fa::kTileKeys + 1 + fa::kUnitCost);
   const long long row_tiles = (long long)total_q * group / l.rows;
-  const long long fit = fa::kMaxTiles / per_row_tile - row_tiles;
+  const long long fit = fa::kMaxCost / per_row_tile - row_tiles;
   if (fit < 1) return FA_ERR_UNSUPPORTED;
   const int step = (int)std::min<long long>(fa::kPagedMaxBatch, fit);
   for (int b0 = 0; b0 < batch; b0 += step) {

@@ -4,7 +4,7 @@
 // Rows: the `group` query heads of one kv head times the sequence's query
 // tokens (row = token * group + head), N of them (16, 32 or 64) to a tile.
 // The work is every row tile's 128-key tiles; CTA c takes an equal contiguous
-// range of them (paged_index.h), whatever the lengths, and walks it as
+// range of their costs (paged_index.h), whatever the lengths, and walks it as
 // segments, one per unit it touches.  A segment that covers its unit writes O
 // and the LSE, one that covers a part writes a normalised fp32 partial and
 // its LSE, and paged_merge_kernel joins the parts.
@@ -123,7 +123,7 @@ struct alignas(16) BatchPlan {
   int tiles;                   // of the segment
   int whole;                   // the segment covers its unit
   int unit_end;                // where the unit starts in this segment but does
-                               // not end: the tile number behind it, else -1
+                               // not end: the cost up to its end, else -1
 };
 
 template <int D, int N>
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     ptx::tmem_alloc(ptx::smem_u32(&cb->tmem_base), C::kTmemCols);
     ptx::tmem_relinquish();
   }
-  // Tiles of the sequences before each one: a scan over the batch by the
+  // Cost of the sequences before each one: a scan over the batch by the
   // softmax warps, the same in every CTA.
   if (warp < 8) {
     if (tid == 0) {
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         RowRange q;
         int len;
         seq_of(b, &q, &len);
-        n = capped_tiles(sh.heads_k * head_tiles(sh, q.n, len));
+        n = capped_cost(sh.heads_k * head_cost(sh, q.n, len));
       }
       long long sum = n;
 #pragma unroll
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         if (w < warp) lo += cb->warp_tiles[w];
         all += cb->warp_tiles[w];
       }
-      if (b < a.batch) cb->before[b + 1] = capped_tiles(lo + sum);
+      if (b < a.batch) cb->before[b + 1] = capped_cost(lo + sum);
       base += all;
       named_bar_sync(1, 256);
     }
@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             plan.tiles = g.count;
             plan.whole = g.count == g.unit_count;
             plan.unit_end =
-                g.part_lo == 0 && g.count < g.unit_count ? walk.at - g.count + g.unit_count : -1;
+                g.part_lo == 0 && g.count < g.unit_count ? g.unit_end : -1;
           }
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->plan_full[slot]));
@@ -1129,7 +1129,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
 // of the unit that starts in CTA c and ends in a later one.
 // O = sum_p w_p O_p, w_p = 2^(lse_p - LSE): the parts are summed in CTA order,
 // so the result does not depend on timing.  A unit can have as many parts as
-// there are CTAs, so every LSE is loaded at once and eight partials at a time.
+// there are CTAs, so every LSE is loaded at once and 16 partials at a time.
 constexpr int kPagedMaxGrid = 512;  // CTAs of an attention launch
 
 template <int D, int N>
@@ -1142,12 +1142,20 @@ __global__ void __launch_bounds__(D) paged_merge_kernel(const PagedAttnArgs a) {
   const int parts = m0.x;
   if (parts == 0 || n >= m1.x) return;
   auto slot = [&](int p) { return p == 0 ? m1.y : 2 * (c + p); };
+  constexpr int kAtOnce = 16;
+  float v[kAtOnce];
+  auto load = [&](int p0) {
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k)
+      v[k] = p0 + k < parts ? a.part_o[((size_t)slot(p0 + k) * N + n) * D + tid] : 0.f;
+  };
+  load(0);
   const float neg_inf = -__int_as_float(0x7f800000);
   float top = neg_inf;
   for (int p = tid; p < parts; p += D) {
-    const float v = a.part_lse[(size_t)slot(p) * N + n];
-    s_w[p] = v;
-    top = fmaxf(top, v);
+    const float lp = a.part_lse[(size_t)slot(p) * N + n];
+    s_w[p] = lp;
+    top = fmaxf(top, lp);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -1156,13 +1164,11 @@ __global__ void __launch_bounds__(D) paged_merge_kernel(const PagedAttnArgs a) {
 #pragma unroll
   for (int w = 0; w < D / 32; ++w) top = fmaxf(top, s_red[w]);
   float sum = 0.f, acc = 0.f;
-  for (int p0 = 0; p0 < parts; p0 += 8) {
-    float v[8];
+#pragma unroll 1
+  for (int p0 = 0; p0 < parts; p0 += kAtOnce) {
+    if (p0 > 0) load(p0);
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      v[k] = p0 + k < parts ? a.part_o[((size_t)slot(p0 + k) * N + n) * D + tid] : 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < kAtOnce; ++k) {
       if (p0 + k < parts) {
         const float lp = s_w[p0 + k];
         const float w = lp == neg_inf ? 0.f : ptx::ex2(lp - top);

@@ -102,10 +102,13 @@ FA_HD KeyRange key_range(int i0, int i1, int n, int len, int held, bool causal, 
 // ---------------------------------------------------- attention work split
 // A work unit is one row tile (`rows` of the n * group rows of a sequence and
 // kv head, row = token * group + head of the group) against its key tiles of
-// kTileKeys keys.  Units are numbered by sequence, then head, then row tile;
-// their key tiles, in that order, are cut into equal contiguous ranges, one
-// for each CTA.
+// kTileKeys keys.  Units come by sequence, then head, then row tile.  A unit
+// costs its key tiles and kUnitCost more, for what a CTA does once for each
+// (its rows of Q, the first maximum, its output); the costs, in that order,
+// are cut into equal contiguous ranges, one for each CTA.  A unit's first
+// kUnitCost places hold no tile, so a cut among them leaves it whole.
 constexpr int kTileKeys = 128;
+constexpr int kUnitCost = 4;  // in tiles
 
 struct AttnShape {
   int heads_k, group, rows;  // kv heads, query heads of one, rows of a tile
@@ -135,31 +138,31 @@ FA_HD TileRange key_tiles(const KeyRange& k) {
   t.count = k.hi > k.lo ? (int)(((unsigned)k.hi + kTileKeys - 1) / kTileKeys) - t.first : 1;
   return t;
 }
-// Key tiles of all row tiles of one (sequence, head).
-FA_HD long long head_tiles(const AttnShape& s, int n, int len) {
+// Cost of all row tiles of one (sequence, head).
+FA_HD long long head_cost(const AttnShape& s, int n, int len) {
   long long sum = 0;
   const int m = n > 0 ? row_tiles(s, n) : 0;
   FA_ROLLED
-  for (int t = 0; t < m; ++t) sum += key_tiles(tile_keys(s, t, n, len)).count;
+  for (int t = 0; t < m; ++t) sum += kUnitCost + key_tiles(tile_keys(s, t, n, len)).count;
   return sum;
 }
 
-// Tile numbers are 32-bit.  The host splits a batch so that those of a launch
-// stay below 2^31 where cu_seqlens is well formed; a count past that (from
-// overlapping sequences) stops at the limit, and tiles past it are not done.
-constexpr int kMaxTiles = 0x7fffffff;
-FA_HD int capped_tiles(long long n) { return n < kMaxTiles ? (int)n : kMaxTiles; }
+// Costs are 32-bit.  The host splits a batch so that those of a launch stay
+// below 2^31 where cu_seqlens is well formed; a sum past that (from
+// overlapping sequences) stops at the limit, and what lies behind it is not
+// done.
+constexpr int kMaxCost = 0x7fffffff;
+FA_HD int capped_cost(long long n) { return n < kMaxCost ? (int)n : kMaxCost; }
 
-// Start of CTA c's range of `total` tiles among `ctas`: the first
-// total % ctas ranges are one tile longer.
+// Start of CTA c's range of `total` among `ctas`: the first total % ctas
+// ranges are one longer.
 FA_HD int range_start(int total, int ctas, int c) {
   const int q = (int)((unsigned)total / (unsigned)ctas), r = total - q * ctas;
   return c * q + (c < r ? c : r);
 }
 
 // Walks the segments of a range: the part of each unit's tiles inside it.
-// before(b) is the number of tiles of the sequences before b (b up to the
-// batch).
+// before(b) is the cost of the sequences before b (b up to the batch).
 struct Segment {
   int seq, head, row_tile;
   RowRange q;        // the sequence's query rows
@@ -168,11 +171,12 @@ struct Segment {
   int tile0;         // first key tile of the segment (tile t: keys 128 t ..)
   int count;         // its key tiles
   int part_lo, unit_count;  // place of tile0 among the unit's tiles, and their number
+  int unit_end;      // cost up to the end of the unit
 };
 struct SegmentWalk {
-  int at, end;  // tiles done, end of the range
+  int at, end;  // cost done, end of the range
   int seq, head, row_tile;
-  int in_unit;  // tiles of the current unit that are done
+  int in_unit;  // cost of the current unit that is done
 };
 
 template <typename Before>
@@ -196,51 +200,59 @@ FA_HD void walk_begin(SegmentWalk* w, int lo, int hi, int batch, const Before& b
 template <typename Before, typename SeqOf>
 FA_HD bool walk_next(SegmentWalk* w, const AttnShape& s, const Before& before, const SeqOf& seq_of,
                      Segment* g) {
-  if (w->at >= w->end) return false;
-  if (w->head < 0) {
-    FA_ROLLED
-    while (before(w->seq + 1) <= w->at) ++w->seq;  // sequences without query rows
-    seq_of(w->seq, &g->q, &g->len);
-    const int in_seq = w->at - before(w->seq);
-    const int per_head = capped_tiles(head_tiles(s, g->q.n, g->len));
-    w->head = (int)((unsigned)in_seq / (unsigned)per_head);
-    int left = in_seq - w->head * per_head;
-    w->row_tile = 0;
-    FA_ROLLED
-    for (;;) {
-      const int c = key_tiles(tile_keys(s, w->row_tile, g->q.n, g->len)).count;
-      if (left < c) break;
-      left -= c;
-      ++w->row_tile;
-    }
-    w->in_unit = left;
-  } else {
-    seq_of(w->seq, &g->q, &g->len);
-  }
-  g->seq = w->seq;
-  g->head = w->head;
-  g->row_tile = w->row_tile;
-  g->keys = tile_keys(s, w->row_tile, g->q.n, g->len);
-  const TileRange t = key_tiles(g->keys);
-  int n = t.count - w->in_unit;
-  if (n > w->end - w->at) n = w->end - w->at;
-  g->tile0 = t.first + w->in_unit;
-  g->count = n;
-  g->part_lo = w->in_unit;
-  g->unit_count = t.count;
-  w->at += n;
-  w->in_unit += n;
-  if (w->in_unit == t.count) {
-    w->in_unit = 0;
-    if (++w->row_tile == row_tiles(s, g->q.n)) {
+  FA_ROLLED
+  while (w->at < w->end) {
+    if (w->head < 0) {
+      FA_ROLLED
+      while (before(w->seq + 1) <= w->at) ++w->seq;  // sequences without query rows
+      seq_of(w->seq, &g->q, &g->len);
+      const int in_seq = w->at - before(w->seq);
+      const int per_head = capped_cost(head_cost(s, g->q.n, g->len));
+      w->head = (int)((unsigned)in_seq / (unsigned)per_head);
+      int left = in_seq - w->head * per_head;
       w->row_tile = 0;
-      if (++w->head == s.heads_k) {
-        w->head = -1;
-        ++w->seq;
+      FA_ROLLED
+      for (;;) {
+        const int c = kUnitCost + key_tiles(tile_keys(s, w->row_tile, g->q.n, g->len)).count;
+        if (left < c) break;
+        left -= c;
+        ++w->row_tile;
+      }
+      w->in_unit = left;
+    } else {
+      seq_of(w->seq, &g->q, &g->len);
+    }
+    g->seq = w->seq;
+    g->head = w->head;
+    g->row_tile = w->row_tile;
+    g->keys = tile_keys(s, w->row_tile, g->q.n, g->len);
+    const TileRange t = key_tiles(g->keys);
+    const int cost = kUnitCost + t.count;
+    int n = cost - w->in_unit;
+    if (n > w->end - w->at) n = w->end - w->at;
+    const int lo = w->in_unit > kUnitCost ? w->in_unit - kUnitCost : 0;
+    const int hi = w->in_unit + n > kUnitCost ? w->in_unit + n - kUnitCost : 0;
+    g->tile0 = t.first + lo;
+    g->count = hi - lo;
+    g->part_lo = lo;
+    g->unit_count = t.count;
+    w->at += n;
+    w->in_unit += n;
+    // (Past the limit of 32 bits the unit ends with the range.)
+    g->unit_end = cost - w->in_unit < kMaxCost - w->at ? w->at + (cost - w->in_unit) : kMaxCost;
+    if (w->in_unit == cost) {
+      w->in_unit = 0;
+      if (++w->row_tile == row_tiles(s, g->q.n)) {
+        w->row_tile = 0;
+        if (++w->head == s.heads_k) {
+          w->head = -1;
+          ++w->seq;
+        }
       }
     }
+    if (g->count > 0) return true;
   }
-  return true;
+  return false;
 }
 
 }  // namespace fa
