@@ -359,8 +359,8 @@ extern "C" fa_status fa_paged_attn(const void* q, long long q_row_stride, long l
   a.status = dev.status;
   a.wait_limit_ns = dev.wait_limit_ns;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  // A launch holds the tile counts of kPagedMaxBatch sequences in shared
-  // memory and numbers its tiles in 32 bits; a larger batch runs as
+  // A launch holds the costs of paged_max_batch sequences in shared
+  // memory and counts them in 32 bits; a larger batch runs as
   // consecutive launches, which share the workspace in stream order.
   const long long per_row_tile =
       (long long)num_heads_k *
@@ -368,7 +368,7 @@ extern "C" fa_status fa_paged_attn(const void* q, long long q_row_stride, long l
   const long long row_tiles = (long long)total_q * group / l.rows;
   const long long fit = fa::kMaxCost / per_row_tile - row_tiles;
   if (fit < 1) return FA_ERR_UNSUPPORTED;
-  const int step = (int)std::min<long long>(fa::kPagedMaxBatch, fit);
+  const int step = (int)std::min<long long>(fa::paged_max_batch(l.rows), fit);
   for (int b0 = 0; b0 < batch; b0 += step) {
     a.batch = std::min(batch - b0, step);
     a.cu = cu_seqlens_q + b0;

@@ -75,7 +75,8 @@ constexpr int kConvertWarp = 8, kSWarp = 12, kPvWarp = 13, kLoadWarp = 14;
 constexpr uint32_t kPagedSoftmaxRegs = 160;
 constexpr uint32_t kPagedConvertRegs = 80;
 constexpr uint32_t kPagedControlRegs = 96;
-constexpr int kPagedMaxBatch = 1024;  // sequences of one launch
+// Sequences of one launch (their costs are held in shared memory).
+constexpr int paged_max_batch(int rows) { return rows == 64 ? 512 : 1024; }
 constexpr int kPagedPlans = 4;        // batches in flight
 constexpr int kPlanReaders = 15;      // warps that read them
 constexpr int kPlanTiles = 16;        // tiles of a batch
@@ -110,6 +111,7 @@ struct PagePlan {
 
 // Up to kPlanTiles tiles of one segment, for every warp; count = 0 ends the
 // range.
+template <int N>
 struct alignas(16) BatchPlan {
   PagePlan page[2 * kPlanTiles];
   int cell[2 * kPlanTiles];
@@ -117,8 +119,9 @@ struct alignas(16) BatchPlan {
   int first, last;             // it begins, ends the segment
   int lo, hi;                  // keys that some row of the segment sees
   int head, q0, row0, rows;    // first q row of the sequence; rows of the tile
-  int out[64], lse[64];        // of each row: its place in O (rows) and in the LSE
+  int out[N], lse[N];          // of each row: its place in O (rows) and in the LSE
   int tok0, tok1;              // tokens of its first and last row
+  alignas(16) int token[N];    // of each row, from tok0
   long long at0;               // position of tok0
   int tiles;                   // of the segment
   int whole;                   // the segment covers its unit
@@ -167,19 +170,20 @@ struct alignas(16) PagedCtl {
   uint64_t drain, drain_pv;         // everything an issuer started is complete
   uint32_t tmem_base;
   volatile int abort_flag;
-  BatchPlan plan[kPagedPlans];
+  BatchPlan<N> plan[kPagedPlans];
   alignas(16) float qs[kPagedPlans][N];      // row scale * softmax scale * log2(e)
-  // Per softmax warpgroup: per-warp partial maxima or sums, minus the running
-  // maximum (less the bias; 0 while no key was seen), rescale factors.
+  // Per softmax warpgroup: of each two rows, the scales and minus the running
+  // maxima (less the bias; 0 while no key was seen); per-warp partial maxima
+  // or sums; rescale factors.
+  alignas(16) float factor[2][N / 2][4];
   alignas(16) float red[2][4][N];
-  alignas(16) float neg_m[2][N];
   alignas(16) float alpha[2][N];
   // By segment (mod 4) and warpgroup: maximum so far (-inf: no key seen) and,
   // at the segment's end, the sum.  (A warpgroup may be up to three segments
   // ahead of the other, which still reads these.)
   float end_m[kPagedPlans][2][N], end_l[kPagedPlans][2][N];
   long long warp_tiles[kPagedThreads / 32];
-  int before[kPagedMaxBatch + 1];
+  int before[paged_max_batch(N) + 1];
 };
 template <int D, int N>
 constexpr size_t paged_smem() {
@@ -196,7 +200,8 @@ __device__ __forceinline__ bool paged_wait(uint32_t bar, uint32_t parity, volati
                                            unsigned int* status, uint64_t limit_ns) {
   uint64_t t0 = 0;
 #pragma unroll 1
-  for (uint32_t spin = 1; !__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity)); ++spin) {
+  for (uint32_t spin = 1;
+       __builtin_expect(!__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity)), 0); ++spin) {
     if ((spin & 255u) != 0 && limit_ns >= kShortWaitNs) continue;
     int give_up = 0;
     if ((threadIdx.x & 31) == 0) {
@@ -335,7 +340,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   };
   // Batch number b of the range; every warp that reads it lets it go with
   // plan_done once it has what it needs.
-  auto plan_of = [&](int b, bool* ok) -> const BatchPlan& {
+  auto plan_of = [&](int b, bool* ok) -> const BatchPlan<N>& {
     *ok = wait(cb->plan_full[b % kPagedPlans], (b / kPagedPlans) & 1);
     return cb->plan[b % kPagedPlans];
   };
@@ -368,7 +373,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     int i = 0, slot = 0;
     uint32_t v_phase = 0;
     for (int b = 0; ok; ++b) {
-      const BatchPlan& plan = plan_of(b, &ok);
+      const BatchPlan<N>& plan = plan_of(b, &ok);
       if (!ok) break;
       const int count = plan.count, tile0 = plan.tile0, key_lo = plan.lo, key_hi = plan.hi;
       if (count == 0) break;
@@ -390,7 +395,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         const int key0 = (tile0 + n) * kTileKeys;
         const int lo = key_lo - key0, hi = key_hi - key0;
         const unsigned pages = (held >> (2 * n)) & 3;
-        if (lo > 0 || hi < kTileKeys || pages != 3) {
+        if (__builtin_expect(lo > 0 || hi < kTileKeys || pages != 3, 0)) {
 #pragma unroll
           for (int k = 0; k < kIters; ++k) {
             const int r = r0 + k * kStep;
@@ -430,7 +435,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       uint32_t k_phase = 0;
       uint64_t qd = 0;
       for (int b = 0; ok; ++b) {
-        const BatchPlan& plan = plan_of(b, &ok);
+        const BatchPlan<N>& plan = plan_of(b, &ok);
         if (!ok) break;
         const int count = plan.count, first = plan.first, last = plan.last;
         plan_done(b);
@@ -472,7 +477,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       bool ok = true;
       int i = 0, seg = 0, in_seg = 0;
       for (int b = 0; ok; ++b) {
-        const BatchPlan& plan = plan_of(b, &ok);
+        const BatchPlan<N>& plan = plan_of(b, &ok);
         if (!ok) break;
         const int count = plan.count, last = plan.last;
         plan_done(b);
@@ -512,7 +517,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       int kn = 0, vn = 0, sk = 0, sv = 0;  // loads issued and slots of K and V
       uint32_t k_phase = 1, v_phase = 1;   // (the first turn finds its slots free)
       for (int b = 0; ok; ++b) {
-        const BatchPlan& plan = plan_of(b, &ok);
+        const BatchPlan<N>& plan = plan_of(b, &ok);
         if (!ok) break;
         const int count = plan.count;
         const int cell = plan.cell[lane];
@@ -583,7 +588,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       n0 = -kPlanTiles;
       for (int b = -1;; ++b) {
         const int slot = b & (kPagedPlans - 1);
-        BatchPlan& plan = cb->plan[slot];
+        BatchPlan<N>& plan = cb->plan[slot];
         const bool first = n0 == 0, ends = last;
         uint4 raw[kBatch];
         int rows = 0, row_q = 0, row_h = 0;  // rows; lane's row: token and head
@@ -623,6 +628,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             if (n + lane < N) {
               plan.out[n + lane] = row_q * a.heads + row_h;
               plan.lse[n + lane] = row_h * a.total_q + row_q;
+              plan.token[n + lane] =
+                  row_q - g.q.lo - (int)((unsigned)(g.row_tile * N) / (unsigned)sh.group);
             }
           }
           if (first) load_rows(0);  // (ahead of the pages' loads in the memory system)
@@ -671,7 +678,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             cell = more ? cells() : -1;
           } else if (b >= 0) {
             // ---- scales and Q
-            plan.page[lane] = {ks, vs, fmaxf(log2f(vs), -(float)kScaleExpMax), held};
+            plan.page[lane] = PagePlan{ks, vs, fmaxf(log2f(vs), -(float)kScaleExpMax), held};
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->scale_full[slot]));
             if (!first) continue;
@@ -755,13 +762,15 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_tmem = tmem + lane_base + wg * 2 * N;
     float (*red)[N] = cb->red[wg];
-    float* neg_m = cb->neg_m[wg];
     float* alpha = cb->alpha[wg];
     uint8_t* prow = smem + C::kP + wg * C::kPBytes + key * C::kPRow;
-    // At 16 rows the factors and maxima stay in registers (pairs), for more
-    // they are read from shared memory.
+    // Scales and maxima of the rows, in pairs: at 16 rows they stay in
+    // registers, for more they are read from shared memory, both of a pair at
+    // once.
     constexpr int kHeld = N == 16 ? N / 2 : 1;
-    uint64_t c_held[kHeld], m_held[kHeld];
+    ulonglong2 f_held[kHeld] = {};
+    ulonglong2* factor = reinterpret_cast<ulonglong2*>(cb->factor[wg]);
+    auto factor_of = [&](int n) { return N == 16 ? f_held[n % kHeld] : factor[n]; };
     auto pair = [](const float* p, int n) { return *reinterpret_cast<const uint64_t*>(p + n); };
     bool ok = true;
     int i = 0;  // tiles before the batch
@@ -784,7 +793,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     auto finish = [&](bool later) -> bool {
       done.due = false;
       const bool alone = done.alone;
-      const BatchPlan& plan = cb->plan[done.batch % kPagedPlans];  // the segment's last
+      const BatchPlan<N>& plan = cb->plan[done.batch % kPagedPlans];  // the segment's last
       const int rows = plan.rows;
       const int ring = done.seg % kPagedPlans;
       const int slot = 2 * cta + (done.seg == 0 ? 0 : 1);
@@ -883,10 +892,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     uint64_t l[N / 2];
     bool unset = true;
     for (int b = 0; ok; ++b) {
-      const BatchPlan& plan = plan_of(b, &ok);
+      const BatchPlan<N>& plan = plan_of(b, &ok);
       if (ok && plan.count > 0) ok = wait(cb->scale_full[b % kPagedPlans], (b / kPagedPlans) & 1);
       const int count = plan.count, tile0 = plan.tile0, rows = plan.rows;
-      const int tok0 = plan.tok0, tok1 = plan.tok1, row0 = plan.row0;
+      const int tok0 = plan.tok0, tok1 = plan.tok1;
       const long long at0 = plan.at0;
       if (plan.first) seg0 = i;
       // This warpgroup's first tile of the batch and of the segment.
@@ -910,82 +919,94 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         // below.
         unset = true;
         ok = wait(cb->qs_full[seg % kPagedPlans], (seg / kPagedPlans) & 1);
-        if (key < N) neg_m[key] = 0.f;
+        if (key < N) {
+          cb->factor[wg][key / 2][key & 1] = c[key];
+          cb->factor[wg][key / 2][2 + (key & 1)] = 0.f;
+        }
         ok = named_bar_and(bar + 1, 128, ok);
         if (!ok) break;
         if constexpr (N == 16) {
 #pragma unroll
-          for (int n = 0; n < N; n += 2) {
-            c_held[n / 2] = pair(c, n);
-            m_held[n / 2] = 0;
-          }
+          for (int n = 0; n < N / 2; ++n) f_held[n] = factor[n];
         }
       }
-      // The batch's tiles; a batch that is skipped comes by for what is due.
-      for (int t = first; t < count || skip; t += 2) {
-        const int at = i + t;  // tile of the CTA's range
-        if (!skip) {
-        const uint32_t phase = (uint32_t)(at >> 1) & 1;
-        const PagePlan pp = plan.page[2 * t + page];
-        const float ks = pp.ks, vs = pp.vs, lv = pp.lv;
-        // Rows of several tokens see different keys: the tiles at the edges
-        // are masked row by row.
-        const long long j0 = (long long)(tile0 + t) * kTileKeys, j = j0 + key;
-        const bool all = j0 >= plan.lo && j0 + kTileKeys <= plan.hi;
-        const bool seen = j >= plan.lo && j < plan.hi && pp.held;
-        const bool edge = tok0 != tok1 && ((sh.causal && j0 + kTileKeys - 1 > at0) ||
-                                           (sh.window >= 0 && j0 < at0 + (tok1 - tok0) - sh.window));
-        // (A warp whose wait has given up still joins the votes below, after
-        // which the whole warpgroup leaves.)
-        if (ok) ok = wait(cb->s_full[wg], phase);
-        // Pt's buffer was last read by the PV of this warpgroup's last tile.
-        if (ok && at >= 2) ok = wait(cb->pv_done[wg], phase ^ 1);
-        ptx::tc_fence_after();
-        const uint64_t ks2 = ptx::f2_pack(ks, ks);
+      // The tiles in a loop of their own, so that its instructions lie
+      // together; it is left for a new maximum (`slow`), which comes back to
+      // the same tile, and after a segment's first tile for the output that
+      // is due.  A batch that is skipped comes by for that alone.
+      bool settled = false;  // the tile's maximum is known to do
+      for (int t = first;;) {
+        const int stop = done.due ? imin(start - i + 1, count) : count;
+        bool slow = false;
         uint64_t x[N / 2];  // score less the maximum, log2
-        // Once, or again with a new maximum.
-        for (bool settled = false;; settled = true) {
+        float lv = 0.f;
+#pragma unroll 1
+        for (; t < stop && !skip; t += 2) {
+          const int at = i + t;  // tile of the CTA's range
+          const uint32_t phase = (uint32_t)(at >> 1) & 1;
+          const PagePlan pp = plan.page[2 * t + page];
+          lv = pp.lv;
+          const int j0 = (tile0 + t) * kTileKeys;
+          const bool seen = j0 + key >= plan.lo && (unsigned)(j0 + key) < (unsigned)plan.hi && pp.held;
+          // Rows of several tokens see different keys: the tiles at the edges
+          // are masked row by row.
+          const bool edge =
+              tok0 != tok1 &&
+              ((sh.causal && (long long)j0 + kTileKeys - 1 > at0) ||
+               (sh.window >= 0 && (long long)j0 < at0 + (tok1 - tok0) - sh.window));
+          // (A warp whose wait has given up still joins the votes below,
+          // after which the whole warpgroup leaves.)
+          if (ok) ok = wait(cb->s_full[wg], phase);
+          // Pt's buffer was last read by the PV of this warpgroup's last tile.
+          if (ok && at >= 2) ok = wait(cb->pv_done[wg], phase ^ 1);
+          ptx::tc_fence_after();
+          const uint64_t ks2 = ptx::f2_pack(pp.ks, pp.ks);
+          constexpr int kLoad = N < 32 ? N : 32;  // rows loaded at once
 #pragma unroll
-          for (int n0 = 0; n0 < N; n0 += 16) {
-            uint32_t qh[16], ql[16];
-            ptx::tmem_ld16(s_tmem + n0, qh);
-            ptx::tmem_ld16(s_tmem + N + n0, ql);
+          for (int n0 = 0; n0 < N; n0 += kLoad) {
+            uint32_t qh[kLoad], ql[kLoad];
+#pragma unroll
+            for (int n = 0; n < kLoad; n += 16) {
+              ptx::tmem_ld16(s_tmem + n0 + n, qh + n);
+              ptx::tmem_ld16(s_tmem + N + n0 + n, ql + n);
+            }
             ptx::tmem_wait_ld();
-            ptx::reg_fence16(qh);
-            ptx::reg_fence16(ql);
 #pragma unroll
-            for (int n = 0; n < 16; n += 2) {
-              const uint64_t c2 = N == 16 ? c_held[(n0 + n) / 2 % kHeld] : pair(c, n0 + n);
-              const uint64_t m2 = N == 16 ? m_held[(n0 + n) / 2 % kHeld] : pair(neg_m, n0 + n);
+            for (int n = 0; n < kLoad; n += 16) {
+              ptx::reg_fence16(qh + n);
+              ptx::reg_fence16(ql + n);
+            }
+#pragma unroll
+            for (int n = 0; n < kLoad; n += 2) {
+              const ulonglong2 f = factor_of((n0 + n) / 2);
               const uint64_t h2 = ptx::f2_pack(__uint_as_float(qh[n]), __uint_as_float(qh[n + 1]));
               const uint64_t l2 = ptx::f2_pack(__uint_as_float(ql[n]), __uint_as_float(ql[n + 1]));
-              x[(n0 + n) / 2] = ptx::fma2(ptx::add2(h2, l2), ptx::mul2(c2, ks2), m2);
+              x[(n0 + n) / 2] = ptx::fma2(ptx::add2(h2, l2), ptx::mul2(f.x, ks2), f.y);
             }
           }
-          if (!(all && pp.held) && !seen) {
+          if (edge) {
+            // Row n stands at at0 + token[n].
+            const long long r = (long long)j0 + key - at0;
+            const long long w = r + sh.window;
+            const int lo = sh.causal ? (int)(r < kMaxCost ? (r > -1 ? r : -1) : kMaxCost) : -1;
+            const int hi = sh.window < 0 ? kMaxCost : (int)(w < kMaxCost ? (w > -1 ? w : -1) : kMaxCost);
+#pragma unroll
+            for (int n = 0; n < N; n += 4) {
+              const int4 o = *reinterpret_cast<const int4*>(plan.token + n);
+              float u, v;
+              ptx::f2_unpack(x[n / 2], u, v);
+              x[n / 2] = ptx::f2_pack(o.x >= lo && o.x <= hi ? u : neg_inf,
+                                      o.y >= lo && o.y <= hi ? v : neg_inf);
+              ptx::f2_unpack(x[n / 2 + 1], u, v);
+              x[n / 2 + 1] = ptx::f2_pack(o.z >= lo && o.z <= hi ? u : neg_inf,
+                                          o.w >= lo && o.w <= hi ? v : neg_inf);
+            }
+          }
+          if (!seen) {
 #pragma unroll
             for (int n = 0; n < N / 2; ++n) x[n] = ptx::f2_pack(neg_inf, neg_inf);
           }
-          if (edge) {
-#pragma unroll 1
-            for (int tok = tok0; tok <= tok1; ++tok) {
-              const long long pos = at0 + (tok - tok0);
-              const bool out = (sh.causal && j > pos) || (sh.window >= 0 && j < pos - sh.window);
-              if (out) {
-                const int r0 = tok * sh.group - row0, r1 = r0 + sh.group;
-#pragma unroll
-                for (int n = 0; n < N / 2; ++n) {
-                  float u, v;
-                  ptx::f2_unpack(x[n], u, v);
-                  if (2 * n >= r0 && 2 * n < r1) u = neg_inf;
-                  if (2 * n + 1 >= r0 && 2 * n + 1 < r1) v = neg_inf;
-                  x[n] = ptx::f2_pack(u, v);
-                }
-              }
-            }
-          }
-          if (settled) break;
-          if (!unset) {
+          if (!settled) {
             // A new maximum is due where a score passes the old one by 2^8.
             float over = neg_inf;
 #pragma unroll
@@ -994,20 +1015,49 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
               ptx::f2_unpack(x[n], u, v);
               over = ptx::max3(over, u, v);
             }
-            const int need = !ok || over + lv > kRescaleLog2 + kPagedBias;
-            if (!named_bar_or(bar, 128, need)) break;
+            const int need = unset || !ok || over + lv > kRescaleLog2 + kPagedBias;
+            if (named_bar_or(bar, 128, need)) {
+              slow = true;
+              break;
+            }
           }
+          settled = false;
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(ptx::smem_u32(&cb->s_free[wg]));
+          // Pt row of this key.
+          const uint64_t vs2 = ptx::f2_pack(pp.vs, pp.vs);
+#pragma unroll
+          for (int n0 = 0; n0 < N; n0 += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float u, v;
+              ptx::f2_unpack(x[n0 / 2 + k], u, v);
+              const uint64_t p2 = ptx::f2_pack(ptx::ex2(u), ptx::ex2(v));
+              l[n0 / 2 + k] = ptx::add2(l[n0 / 2 + k], p2);
+              ptx::f2_unpack(ptx::mul2(p2, vs2), u, v);
+              w[k] = ptx::pack_f16x2(u, v);
+            }
+            const int un = n0 / 8;
+            const int us = N == 64 ? (un ^ (key & 7))
+                                   : N == 32 ? (un ^ ((key >> 1) & 3)) : (un ^ ((key >> 2) & 1));
+            *reinterpret_cast<uint4*>(prow + us * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          ptx::fence_proxy_async_smem();
+          ptx::mbar_arrive(ptx::smem_u32(&cb->p_full[wg]));
+        }
+        if (slow) {
           ok = named_bar_and(bar + 1, 128, ok);
           if (!ok) break;
+          const int at = i + t;
 #pragma unroll
           for (int n0 = 0; n0 < N; n0 += 16) {
             float v[16];
 #pragma unroll
             for (int n = 0; n < 16; n += 2) {
-              const uint64_t m2 = N == 16 ? m_held[n / 2 % kHeld] : pair(neg_m, n0 + n);
               float u0, u1, m0, m1;
               ptx::f2_unpack(x[(n0 + n) / 2], u0, u1);
-              ptx::f2_unpack(m2, m0, m1);
+              ptx::f2_unpack(factor_of((n0 + n) / 2).y, m0, m1);
               v[n] = u0 - m0 + lv;
               v[n + 1] = u1 - m1 + lv;
             }
@@ -1023,7 +1073,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             float al = 1.f;
             if (mt > mu) {
               al = mu == neg_inf ? 0.f : ptx::ex2(mu - mt);
-              neg_m[key] = -mt;
+              cb->factor[wg][key / 2][2 + (key & 1)] = -mt;
               end_m[key] = mt;
             } else if (at == start) {
               end_m[key] = neg_inf;
@@ -1034,7 +1084,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
           unset = named_bar_or(bar, 128, none);
           if constexpr (N == 16) {
 #pragma unroll
-            for (int n = 0; n < N; n += 2) m_held[n / 2 % kHeld] = pair(neg_m, n);
+            for (int n = 0; n < N / 2; ++n) f_held[n] = factor[n];
           }
           if (at != start) {
 #pragma unroll
@@ -1053,34 +1103,14 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             }
             ptx::tmem_wait_st();
           }
+          settled = true;
+          continue;
         }
-        if (!ok) break;
-        ptx::tc_fence_before();
-        ptx::mbar_arrive(ptx::smem_u32(&cb->s_free[wg]));
-        // Pt row of this key.
-        const uint64_t vs2 = ptx::f2_pack(vs, vs);
-#pragma unroll
-        for (int n0 = 0; n0 < N; n0 += 8) {
-          uint32_t w[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float u, v;
-            ptx::f2_unpack(x[n0 / 2 + k], u, v);
-            const uint64_t p2 = ptx::f2_pack(ptx::ex2(u), ptx::ex2(v));
-            l[n0 / 2 + k] = ptx::add2(l[n0 / 2 + k], p2);
-            ptx::f2_unpack(ptx::mul2(p2, vs2), u, v);
-            w[k] = ptx::pack_f16x2(u, v);
-          }
-          const int un = n0 / 8;
-          const int us = N == 64 ? (un ^ (key & 7))
-                                 : N == 32 ? (un ^ ((key >> 1) & 3)) : (un ^ ((key >> 2) & 1));
-          *reinterpret_cast<uint4*>(prow + us * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (done.due && (skip || t > start - i)) {
+          ok = finish(!skip);
+          if (!ok) break;
         }
-        ptx::fence_proxy_async_smem();
-        ptx::mbar_arrive(ptx::smem_u32(&cb->p_full[wg]));
-        }
-        if (done.due && (skip || at == start)) ok = finish(!skip);
-        if (skip || !ok) break;
+        if (skip || t >= count) break;
       }
       if (!ok || count == 0) break;
       if (skip) {
