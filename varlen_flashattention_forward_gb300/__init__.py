@@ -148,8 +148,9 @@ def _stream_ptr(stream):
 
 
 def _check(t, name, dtype, ndim, view=False):
-    if t.dtype is dtype and t.dim() == ndim and not view and t.is_contiguous():
-        return
+    if t.dtype is dtype and t.dim() == ndim:
+        if t.is_contiguous() or (view and t.stride(-1) == 1):
+            return
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != ndim:

@@ -94,6 +94,11 @@ cudaError_t launch_attn(const CUtensorMap& k_map, const CUtensorMap& v_map,
 
 bool cache_dim(int d) { return d == 64 || d == 80 || d == 96 || d == 128; }
 
+// Threads (one a 16-byte piece of a row) an SM should have before
+// fa_qk_norm_rope takes eight heads together.
+constexpr int kNormRopeWide = 8192;
+constexpr int kNormRopeRows = 4;
+
 fa_status launched() { return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH; }
 
 // Checks that the rotation arguments share.
@@ -171,13 +176,24 @@ extern "C" fa_status fa_qk_norm_rope(const void* q, long long q_row_stride,
   a.positions = rot_dim > 0 ? positions : nullptr;
   a.max_pos = max_pos;
   const int lanes = head_dim <= 64 ? 8 : head_dim <= 128 ? 16 : 32;
-  a.groups = num_heads + num_heads_k;
-  a.units = (long long)num_tokens * a.groups;
-  const unsigned grid = (unsigned)((a.units * lanes + 255) / 256);
+  // Four heads of a token together, so that table and weights are loaded
+  // once for them; one at a time where that would leave SMs idle.
+  const long long all = (long long)num_tokens * (num_heads + num_heads_k);
+  const int rows = all * lanes >= (long long)kNormRopeWide * dev.sm_count ? kNormRopeRows : 1;
+  a.groups_q = (num_heads + rows - 1) / rows;
+  a.groups = a.groups_q + (num_heads_k + rows - 1) / rows;
+  a.units = (unsigned)((long long)num_tokens * a.groups);
+  const unsigned grid = (unsigned)(((long long)a.units * lanes + 255) / 256);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (lanes == 8) fa::qk_norm_rope_kernel<8, 1><<<grid, 256, 0, s>>>(a);
-  else if (lanes == 16) fa::qk_norm_rope_kernel<16, 1><<<grid, 256, 0, s>>>(a);
-  else fa::qk_norm_rope_kernel<32, 1><<<grid, 256, 0, s>>>(a);
+  if (rows == 1) {
+    if (lanes == 8) fa::qk_norm_rope_kernel<8, 1><<<grid, 256, 0, s>>>(a);
+    else if (lanes == 16) fa::qk_norm_rope_kernel<16, 1><<<grid, 256, 0, s>>>(a);
+    else fa::qk_norm_rope_kernel<32, 1><<<grid, 256, 0, s>>>(a);
+  } else {
+    if (lanes == 8) fa::qk_norm_rope_kernel<8, kNormRopeRows><<<grid, 256, 0, s>>>(a);
+    else if (lanes == 16) fa::qk_norm_rope_kernel<16, kNormRopeRows><<<grid, 256, 0, s>>>(a);
+    else fa::qk_norm_rope_kernel<32, kNormRopeRows><<<grid, 256, 0, s>>>(a);
+  }
   return launched();
 }
 
@@ -236,13 +252,22 @@ extern "C" fa_status fa_paged_kv_append(
       std::min<long long>(total_new, total_new / fa::kPageTokens + 2ll * batch);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool step = (long long)total_new < 16ll * batch;
+  const int items = 2 * num_heads_k;
   if (step) {
-    if (head_dim <= 64) fa::kv_append_step_kernel<8><<<(unsigned)chunks, 256, 0, s>>>(a);
-    else fa::kv_append_step_kernel<16><<<(unsigned)chunks, 256, 0, s>>>(a);
+    const int threads = 32 * std::min(items, 16);
+    if (head_dim <= 64) fa::kv_append_step_kernel<8><<<(unsigned)chunks, threads, 0, s>>>(a);
+    else fa::kv_append_step_kernel<16><<<(unsigned)chunks, threads, 0, s>>>(a);
   } else {
-    const dim3 grid((unsigned)chunks, 2 * num_heads_k);
-    if (head_dim <= 64) fa::kv_append_prompt_kernel<8><<<grid, 128, 0, s>>>(a);
-    else fa::kv_append_prompt_kernel<16><<<grid, 128, 0, s>>>(a);
+    // Blocks of 256 threads, 128 at 64 dims; as few items each as leave all
+    // of them resident at once, three (six) an SM.
+    const int threads = head_dim <= 64 ? 128 : 256;
+    const long long slots = 768ll / threads * dev.sm_count;
+    const long long blocks = std::max<long long>(1, std::min<long long>(items, slots / chunks));
+    a.per_block = (int)((items + blocks - 1) / blocks);
+    const dim3 grid((unsigned)chunks, (items + a.per_block - 1) / a.per_block);
+    const size_t table = (size_t)fa::kPageTokens * rot_dim * sizeof(float);
+    if (head_dim <= 64) fa::kv_append_prompt_kernel<8><<<grid, threads, table, s>>>(a);
+    else fa::kv_append_prompt_kernel<16><<<grid, threads, table, s>>>(a);
   }
   return launched();
 }

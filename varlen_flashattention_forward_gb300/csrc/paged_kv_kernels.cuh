@@ -113,6 +113,12 @@ struct KvAppendArgs {
   const float* k_weight;  // or null
   float inv_dim, eps;
   RopeParams rope;
+  int per_block;  // items of a block (prompt kernel)
+};
+
+struct AppendChunk {
+  int page, slot, count;  // the page, its first new slot and their number
+  int row0, pos0;         // row and position of the first
 };
 
 // One item: the new tokens of one page and head, keys or values, taken by a
@@ -121,114 +127,170 @@ struct KvAppendArgs {
 // in registers between the maximum and the rounding, a longer one is loaded
 // again for the second pass.
 template <int LANES, int ROWS, int TEAM>
-__device__ __forceinline__ void append_item(const KvAppendArgs& a, int page, int head, bool is_k,
-                                            int slot, int count, int row0, int pos0, int team_warp,
-                                            float* s_amax) {
-  constexpr int kGroups = 32 / LANES;            // rows of a warp at once
-  constexpr int kPass = TEAM * ROWS * kGroups;   // rows of the team's pass
-  const int lane = threadIdx.x & 31;
-  const int sub = lane % LANES, dim0 = sub * 8;
-  const bool in_dim = dim0 < a.dim;
-  const uint16_t* src = is_k ? a.k + head * a.k_head : a.v + head * a.v_head;
-  const long long stride = is_k ? a.k_row : a.v_row;
-  const size_t cell = (size_t)page * a.heads + head;
-  uint8_t* codes = (is_k ? a.k_cache : a.v_cache) + cell * kPageTokens * a.dim;
-  float* scale = (is_k ? a.k_scale : a.v_scale) + cell;
-  const bool norm = is_k && a.k_weight != nullptr;
-  const bool turn = is_k && a.rope.rot_dim > 0;
-  const float old = slot > 0 ? *scale : 0.f;
+struct AppendItem {
+  static constexpr int kGroups = 32 / LANES;           // rows of a warp at once
+  static constexpr int kPass = TEAM * ROWS * kGroups;  // rows of the team's pass
+  const KvAppendArgs& a;
+  const AppendChunk ch;
+  const float* table;  // row of the chunk's first position
+  int team_warp, lane, sub;
+  RowPieces p;
   float w[8];
-  if (norm && in_dim) {
+  // The current item.
+  bool is_k;
+  const uint16_t* src;
+  long long stride;
+  uint8_t* codes;
+  float* scale;
+  float old;
+  RowBits raw[ROWS];
+  int turn_no = 0;
+
+  __device__ __forceinline__ AppendItem(const KvAppendArgs& a_, const AppendChunk& c, int tw,
+                                        const float* table_)
+      : a(a_), ch(c), table(table_), team_warp(tw) {
+    lane = threadIdx.x & 31;
+    sub = lane % LANES;
+    p = row_pieces(a.rope, sub, a.dim);
+    if (a.k_weight && p.a >= 0) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = __ldg(a.k_weight + dim0 + j);
+      for (int j = 0; j < 4; ++j) {
+        w[j] = __ldg(a.k_weight + p.a + j);
+        w[4 + j] = __ldg(a.k_weight + p.b + j);
+      }
+    }
   }
-  float x[ROWS][8];
-  float amax = 0.f;
-  auto row_of = [&](int pass, int i) {
+  __device__ __forceinline__ int row_of(int pass, int i) const {
     return pass * kPass + (i * TEAM + team_warp) * kGroups + lane / LANES;
-  };
-  auto load = [&](int pass) {
-    uint4 raw[ROWS];
+  }
+  __device__ __forceinline__ void load(int pass) {
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
       const int r = row_of(pass, i);
-      raw[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < count && in_dim)
-        raw[i] = __ldg(reinterpret_cast<const uint4*>(src + (long long)(row0 + r) * stride + dim0));
-    }
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-      unpack_bf16x8(raw[i], x[i]);
-      if (norm) norm_row<LANES>(x[i], w, a.inv_dim, a.eps);
-      if (turn) {
-        const int r = row_of(pass, i);
-        RopeRow t;
-        if (r < count) load_rope(a.rope, pos0 + r, dim0, &t);
-        rotate_row<LANES>(x[i], a.rope, t, dim0);
+      raw[i].a = raw[i].b = make_uint2(0u, 0u);
+      if (r < ch.count && p.a >= 0) {
+        const uint16_t* row = src + (long long)(ch.row0 + r) * stride;
+        raw[i].a = __ldg(reinterpret_cast<const uint2*>(row + p.a));
+        raw[i].b = __ldg(reinterpret_cast<const uint2*>(row + p.b));
       }
     }
-  };
-  const int passes = (count + kPass - 1) / kPass;
-  for (int p = 0; p < passes; ++p) {
-    load(p);
+  }
+  // Item number `item` of the chunk (head item / 2, values if even): its first
+  // loads under way.
+  __device__ __forceinline__ void begin(int item) {
+    const int head = item >> 1;
+    is_k = (item & 1) != 0;
+    src = is_k ? a.k + head * a.k_head : a.v + head * a.v_head;
+    stride = is_k ? a.k_row : a.v_row;
+    const size_t cell = (size_t)ch.page * a.heads + head;
+    codes = (is_k ? a.k_cache : a.v_cache) + cell * kPageTokens * a.dim;
+    scale = (is_k ? a.k_scale : a.v_scale) + cell;
+    old = ch.slot > 0 ? *scale : 0.f;
+    load(0);
+  }
+  __device__ __forceinline__ void values(int pass, float (*x)[8]) {
+    const bool turn = is_k && p.turns;
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-      if (row_of(p, i) < count && in_dim) {
+      unpack_row(raw[i], x[i]);
+      if (is_k && a.k_weight) norm_row<LANES>(x[i], w, a.inv_dim, a.eps);
+      const int r = row_of(pass, i);
+      if (turn && r < ch.count)
+        rotate_row(x[i], a.rope, load_rope(a.rope, table + r * a.rope.rot_dim, sub));
+    }
+  }
+  // The item that begin() has under way; `next` (an item, or -1) is under way
+  // when it returns.
+  __device__ __forceinline__ void finish(int next, float* s_amax) {
+    float x[ROWS][8];
+    float amax = 0.f;
+    const int passes = (ch.count + kPass - 1) / kPass;
+#pragma unroll 1
+    for (int ps = 0; ps < passes; ++ps) {
+      if (ps > 0) load(ps);
+      values(ps, x);
+      // Infinite and NaN values take no part in the scale: an infinity
+      // saturates and a NaN stays one, and the rest of the page keeps its
+      // precision.  (Rows and lanes past the end hold zeros; the maximum
+      // passes over NaN by itself.)
+      float top = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          // Infinite and NaN values take no part in the scale: an infinity
-          // saturates and a NaN stays one, and the rest of the page keeps
-          // its precision.
-          const float v = fabsf(x[i][j]);
-          if (v <= 3.402823466e38f) amax = fmaxf(amax, v);
+      for (int i = 0; i < ROWS; ++i) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2)
+          top = ptx::max3(top, fabsf(x[i][j]), fabsf(x[i][j + 1]));
+      }
+      if (__builtin_expect(!(top <= 3.402823466e38f), 0)) {
+        top = 0.f;
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float v = fabsf(x[i][j]);
+            if (v <= 3.402823466e38f) top = fmaxf(top, v);
+          }
+        }
+      }
+      amax = fmaxf(amax, top);
+    }
+    uint8_t* const codes_ = codes;
+    float* const scale_ = scale;
+    const float old_ = old;
+    if (passes == 1 && next >= 0) begin(next);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if constexpr (TEAM > 1) {
+      // (Two rows in turn: those of the last item may still be being read.)
+      float* row = s_amax + turn_no * TEAM;
+      turn_no ^= 1;
+      if (lane == 0) row[team_warp] = amax;
+      __syncthreads();  // (and every warp has read the old scale)
+#pragma unroll
+      for (int i = 0; i < TEAM; ++i) amax = fmaxf(amax, row[i]);
+    }
+    const float s = fmaxf(scale_for(amax), old_);
+    const float inv = 1.f / s;
+    __syncwarp();
+    if (lane == 0 && team_warp == 0) *scale_ = s;
+#pragma unroll 1
+    for (int ps = 0; ps < passes; ++ps) {
+      if (passes > 1) {
+        load(ps);
+        values(ps, x);
+      }
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) {
+        const int r = row_of(ps, i);
+        if (r < ch.count && p.a >= 0) {
+          uint8_t* row = codes_ + (size_t)(ch.slot + r) * a.dim;
+          *reinterpret_cast<uint32_t*>(row + p.a) =
+              pack_e4m3x2(x[i][0] * inv, x[i][1] * inv) |
+              pack_e4m3x2(x[i][2] * inv, x[i][3] * inv) << 16;
+          *reinterpret_cast<uint32_t*>(row + p.b) =
+              pack_e4m3x2(x[i][4] * inv, x[i][5] * inv) |
+              pack_e4m3x2(x[i][6] * inv, x[i][7] * inv) << 16;
         }
       }
     }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if constexpr (TEAM > 1) {
-    if (lane == 0) s_amax[team_warp] = amax;
-    __syncthreads();  // (also: every warp has read the old scale)
-#pragma unroll
-    for (int i = 0; i < TEAM; ++i) amax = fmaxf(amax, s_amax[i]);
-  }
-  const float s = fmaxf(scale_for(amax), old);
-  const float inv = 1.f / s;
-  __syncwarp();
-  if (lane == 0 && team_warp == 0) *scale = s;
-  for (int p = 0; p < passes; ++p) {
-    if (passes > 1) load(p);
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-      const int r = row_of(p, i);
-      if (r < count && in_dim) {
-        uint2 c;
-        c.x = pack_e4m3x2(x[i][0] * inv, x[i][1] * inv) |
-              pack_e4m3x2(x[i][2] * inv, x[i][3] * inv) << 16;
-        c.y = pack_e4m3x2(x[i][4] * inv, x[i][5] * inv) |
-              pack_e4m3x2(x[i][6] * inv, x[i][7] * inv) << 16;
-        *reinterpret_cast<uint2*>(codes + (size_t)(slot + r) * a.dim + dim0) = c;
+    // Earlier tokens of the page follow a scale that has grown.
+    if (ch.slot > 0 && s > old_) {
+      const float f = old_ * inv;
+      const int words = ch.slot * a.dim / 4;
+      uint32_t* c = reinterpret_cast<uint32_t*>(codes_);
+#pragma unroll 4
+      for (int i = team_warp * 32 + lane; i < words; i += TEAM * 32) {
+        const uint32_t u = c[i];
+        const float2 lo = f16x2_floats(unpack_e4m3x2(u)), hi = f16x2_floats(unpack_e4m3x2(u >> 16));
+        c[i] = pack_e4m3x2(lo.x * f, lo.y * f) | pack_e4m3x2(hi.x * f, hi.y * f) << 16;
       }
     }
+    if (passes > 1 && next >= 0) begin(next);
   }
-  // Earlier tokens of the page follow a scale that has grown.
-  if (slot > 0 && s > old) {
-    const float f = old * inv;
-    const int words = slot * a.dim / 4;
-    uint32_t* c = reinterpret_cast<uint32_t*>(codes);
-    for (int i = team_warp * 32 + lane; i < words; i += TEAM * 32) {
-      const uint32_t u = c[i];
-      const float2 lo = f16x2_floats(unpack_e4m3x2(u)), hi = f16x2_floats(unpack_e4m3x2(u >> 16));
-      c[i] = pack_e4m3x2(lo.x * f, lo.y * f) | pack_e4m3x2(hi.x * f, hi.y * f) << 16;
-    }
-  }
-}
+};
 
 // The page of the cache and the rows that chunk x (page by page of each
 // sequence's new tokens) fills; false if there is nothing to write.
-__device__ __forceinline__ bool append_chunk(const KvAppendArgs& a, int x, int* page, PageSpan* sp,
-                                             int* row0, int* pos0) {
+__device__ __forceinline__ bool append_chunk(const KvAppendArgs& a, int x, AppendChunk* c) {
   auto span = [&](int b, int* lo) {
     const RowRange r = row_range(__ldg(a.cu + b), __ldg(a.cu + b + 1), a.total);
     *lo = r.lo;
@@ -243,35 +305,59 @@ __device__ __forceinline__ bool append_chunk(const KvAppendArgs& a, int x, int* 
   int lo;
   const AppendSpan s = span(u.seq, &lo);
   const int p = s.first / kPageTokens + u.at;
-  *sp = page_span(s.first, s.n, p);
-  *row0 = lo + sp->row;
-  *pos0 = s.first + sp->row;
-  *page = checked_page(__ldg(a.page_table + (size_t)u.seq * a.max_pages + p), a.num_pages);
-  return *page >= 0;
+  const PageSpan sp = page_span(s.first, s.n, p);
+  c->slot = sp.slot;
+  c->count = sp.count;
+  c->row0 = lo + sp.row;
+  c->pos0 = s.first + sp.row;
+  c->page = checked_page(__ldg(a.page_table + (size_t)u.seq * a.max_pages + p), a.num_pages);
+  return c->page >= 0;
 }
 
 // Few tokens of each sequence: a block takes a chunk, its warps the 2 * heads
 // items of it, one warp an item.
 template <int LANES>
-__global__ void __launch_bounds__(256) kv_append_step_kernel(const KvAppendArgs a) {
-  int page, row0, pos0;
-  PageSpan sp;
-  if (!append_chunk(a, blockIdx.x, &page, &sp, &row0, &pos0)) return;
-  for (int i = threadIdx.x >> 5; i < 2 * a.heads; i += blockDim.x >> 5)
-    append_item<LANES, 1, 1>(a, page, i >> 1, (i & 1) == 0, sp.slot, sp.count, row0, pos0, 0,
-                             nullptr);
+__global__ void __launch_bounds__(512, 2) kv_append_step_kernel(const KvAppendArgs a) {
+  AppendChunk ch;
+  if (!append_chunk(a, blockIdx.x, &ch)) return;
+  AppendItem<LANES, 1, 1> it(a, ch, 0, a.rope.table + (long long)ch.pos0 * a.rope.rot_dim);
+  const int items = 2 * a.heads, warps = blockDim.x >> 5;
+  int i = threadIdx.x >> 5;
+  if (i >= items) return;
+  it.begin(i);
+  for (; i < items; i += warps) it.finish(i + warps < items ? i + warps : -1, nullptr);
 }
 
-// Many tokens: a block of 4 warps takes one item, whose up to 64 rows it
-// holds in registers.
+// Many tokens: a block of LANES / 2 warps (4 rows of each lane group fill a
+// page) takes `a.per_block` items of a chunk in turn, with the next one's rows
+// under way.  The positions' table rows (32 KB of 64 positions of 128 dims)
+// come into shared memory for all of them, under the first values.
 template <int LANES>
-__global__ void __launch_bounds__(128) kv_append_prompt_kernel(const KvAppendArgs a) {
-  __shared__ float s_amax[4];
-  int page, row0, pos0;
-  PageSpan sp;
-  if (!append_chunk(a, blockIdx.x, &page, &sp, &row0, &pos0)) return;
-  append_item<LANES, 16 * LANES / 32, 4>(a, page, blockIdx.y >> 1, (blockIdx.y & 1) == 0, sp.slot,
-                                         sp.count, row0, pos0, threadIdx.x >> 5, s_amax);
+__global__ void __launch_bounds__(16 * LANES, 48 / LANES)
+    kv_append_prompt_kernel(const KvAppendArgs a) {
+  constexpr int kTeam = LANES / 2;
+  extern __shared__ __align__(16) float s_table[];
+  __shared__ float s_amax[2 * kTeam];
+  AppendChunk ch;
+  if (!append_chunk(a, blockIdx.x, &ch)) return;
+  const float4* rows =
+      reinterpret_cast<const float4*>(a.rope.table + (long long)ch.pos0 * a.rope.rot_dim);
+  for (int k = threadIdx.x; k < ch.count * a.rope.rot_dim / 4; k += blockDim.x)
+    ptx::cp_async_16(ptx::smem_u32(s_table) + k * 16, rows + k);
+  AppendItem<LANES, 4, kTeam> it(a, ch, threadIdx.x >> 5, s_table);
+  int i = blockIdx.y * a.per_block;
+  const int end = imin(i + a.per_block, 2 * a.heads);
+  it.begin(i);
+  bool have_table = false;
+  for (; i < end; ++i) {
+    if (it.is_k && !have_table) {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncthreads();
+      have_table = true;
+    }
+    it.finish(i + 1 < end ? i + 1 : -1, s_amax);
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ gather
