@@ -164,15 +164,16 @@ struct AppendItem {
     return pass * kPass + (i * TEAM + team_warp) * kGroups + lane / LANES;
   }
   __device__ __forceinline__ void load(int pass) {
+    const uint16_t* row = src + (long long)(ch.row0 + row_of(pass, 0)) * stride + p.a;
+    const long long step = (long long)(TEAM * kGroups) * stride;
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-      const int r = row_of(pass, i);
       raw[i].a = raw[i].b = make_uint2(0u, 0u);
-      if (r < ch.count && p.a >= 0) {
-        const uint16_t* row = src + (long long)(ch.row0 + r) * stride;
-        raw[i].a = __ldg(reinterpret_cast<const uint2*>(row + p.a));
-        raw[i].b = __ldg(reinterpret_cast<const uint2*>(row + p.b));
+      if (row_of(pass, i) < ch.count && p.a >= 0) {
+        raw[i].a = __ldg(reinterpret_cast<const uint2*>(row));
+        raw[i].b = __ldg(reinterpret_cast<const uint2*>(row + (p.b - p.a)));
       }
+      row += step;
     }
   }
   // Item number `item` of the chunk (head item / 2, values if even): its first
@@ -204,7 +205,7 @@ struct AppendItem {
   __device__ __forceinline__ void finish(int next, float* s_amax) {
     float x[ROWS][8];
     float amax = 0.f;
-    const int passes = (ch.count + kPass - 1) / kPass;
+    const int passes = kPass >= kPageTokens ? 1 : (ch.count + kPass - 1) / kPass;
 #pragma unroll 1
     for (int ps = 0; ps < passes; ++ps) {
       if (ps > 0) load(ps);
@@ -258,11 +259,11 @@ struct AppendItem {
         load(ps);
         values(ps, x);
       }
+      uint8_t* at = codes_ + (ch.slot + row_of(ps, 0)) * a.dim;
 #pragma unroll
       for (int i = 0; i < ROWS; ++i) {
-        const int r = row_of(ps, i);
-        if (r < ch.count && p.a >= 0) {
-          uint8_t* row = codes_ + (size_t)(ch.slot + r) * a.dim;
+        uint8_t* row = at + i * (TEAM * kGroups) * a.dim;
+        if (row_of(ps, i) < ch.count && p.a >= 0) {
           *reinterpret_cast<uint32_t*>(row + p.a) =
               pack_e4m3x2(x[i][0] * inv, x[i][1] * inv) |
               pack_e4m3x2(x[i][2] * inv, x[i][3] * inv) << 16;
