@@ -98,6 +98,7 @@ bool cache_dim(int d) { return d == 64 || d == 80 || d == 96 || d == 128; }
 // fa_qk_norm_rope takes eight heads together.
 constexpr int kNormRopeWide = 8192;
 constexpr int kNormRopeRows = 4;
+constexpr int kNormRopeBlocks = 4;  // resident blocks of an SM
 
 fa_status launched() { return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH; }
 
@@ -183,7 +184,8 @@ extern "C" fa_status fa_qk_norm_rope(const void* q, long long q_row_stride,
   a.groups_q = (num_heads + rows - 1) / rows;
   a.groups = a.groups_q + (num_heads_k + rows - 1) / rows;
   a.units = (unsigned)((long long)num_tokens * a.groups);
-  const unsigned grid = (unsigned)(((long long)a.units * lanes + 255) / 256);
+  const unsigned grid = (unsigned)std::min<long long>(((long long)a.units * lanes + 255) / 256,
+                                                      kNormRopeBlocks * (long long)dev.sm_count);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (rows == 1) {
     if (lanes == 8) fa::qk_norm_rope_kernel<8, 1><<<grid, 256, 0, s>>>(a);

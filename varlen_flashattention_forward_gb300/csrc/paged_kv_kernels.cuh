@@ -135,7 +135,7 @@ struct AppendItem {
   const float* table;  // row of the chunk's first position
   int team_warp, lane, sub;
   RowPieces p;
-  float w[8];
+  uint64_t w[4];
   // The current item.
   bool is_k;
   const uint16_t* src;
@@ -152,13 +152,7 @@ struct AppendItem {
     lane = threadIdx.x & 31;
     sub = lane % LANES;
     p = row_pieces(a.rope, sub, a.dim);
-    if (a.k_weight && p.a >= 0) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        w[j] = __ldg(a.k_weight + p.a + j);
-        w[4 + j] = __ldg(a.k_weight + p.b + j);
-      }
-    }
+    if (a.k_weight && p.a >= 0) load_weights(a.k_weight, p, w);
   }
   __device__ __forceinline__ int row_of(int pass, int i) const {
     return pass * kPass + (i * TEAM + team_warp) * kGroups + lane / LANES;
@@ -189,7 +183,7 @@ struct AppendItem {
     old = ch.slot > 0 ? *scale : 0.f;
     load(0);
   }
-  __device__ __forceinline__ void values(int pass, float (*x)[8]) {
+  __device__ __forceinline__ void values(int pass, uint64_t (*x)[4]) {
     const bool turn = is_k && p.turns;
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
@@ -203,7 +197,7 @@ struct AppendItem {
   // The item that begin() has under way; `next` (an item, or -1) is under way
   // when it returns.
   __device__ __forceinline__ void finish(int next, float* s_amax) {
-    float x[ROWS][8];
+    uint64_t x[ROWS][4];
     float amax = 0.f;
     const int passes = kPass >= kPageTokens ? 1 : (ch.count + kPass - 1) / kPass;
 #pragma unroll 1
@@ -218,17 +212,22 @@ struct AppendItem {
 #pragma unroll
       for (int i = 0; i < ROWS; ++i) {
 #pragma unroll
-        for (int j = 0; j < 8; j += 2)
-          top = ptx::max3(top, fabsf(x[i][j]), fabsf(x[i][j + 1]));
+        for (int j = 0; j < 4; ++j) {
+          float u, v;
+          ptx::f2_unpack(x[i][j], u, v);
+          top = ptx::max3(top, fabsf(u), fabsf(v));
+        }
       }
       if (__builtin_expect(!(top <= 3.402823466e38f), 0)) {
         top = 0.f;
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float v = fabsf(x[i][j]);
-            if (v <= 3.402823466e38f) top = fmaxf(top, v);
+          for (int j = 0; j < 4; ++j) {
+            float u, v;
+            ptx::f2_unpack(x[i][j], u, v);
+            if (fabsf(u) <= 3.402823466e38f) top = fmaxf(top, fabsf(u));
+            if (fabsf(v) <= 3.402823466e38f) top = fmaxf(top, fabsf(v));
           }
         }
       }
@@ -251,6 +250,7 @@ struct AppendItem {
     }
     const float s = fmaxf(scale_for(amax), old_);
     const float inv = 1.f / s;
+    const uint64_t inv2 = ptx::f2_pack(inv, inv);
     __syncwarp();
     if (lane == 0 && team_warp == 0) *scale_ = s;
 #pragma unroll 1
@@ -264,12 +264,14 @@ struct AppendItem {
       for (int i = 0; i < ROWS; ++i) {
         uint8_t* row = at + i * (TEAM * kGroups) * a.dim;
         if (row_of(ps, i) < ch.count && p.a >= 0) {
+          float f[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            ptx::f2_unpack(ptx::mul2(x[i][j], inv2), f[2 * j], f[2 * j + 1]);
           *reinterpret_cast<uint32_t*>(row + p.a) =
-              pack_e4m3x2(x[i][0] * inv, x[i][1] * inv) |
-              pack_e4m3x2(x[i][2] * inv, x[i][3] * inv) << 16;
+              pack_e4m3x2(f[0], f[1]) | pack_e4m3x2(f[2], f[3]) << 16;
           *reinterpret_cast<uint32_t*>(row + p.b) =
-              pack_e4m3x2(x[i][4] * inv, x[i][5] * inv) |
-              pack_e4m3x2(x[i][6] * inv, x[i][7] * inv) << 16;
+              pack_e4m3x2(f[4], f[5]) | pack_e4m3x2(f[6], f[7]) << 16;
         }
       }
     }

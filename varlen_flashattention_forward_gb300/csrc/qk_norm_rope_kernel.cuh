@@ -38,59 +38,56 @@ template <int LANES, int ROWS>
 __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const QkNormRopeArgs a) {
   const int sub = threadIdx.x % LANES;
   const RowPieces p = row_pieces(a.rope, sub, a.dim);
-  const unsigned unit = (blockIdx.x * 256u + threadIdx.x) / LANES;
-  const bool real = unit < a.units;
-  const unsigned token = real ? unit / (unsigned)a.groups : 0;
-  const int group = real ? (int)(unit - token * a.groups) : 0;
-  const bool is_q = group < a.groups_q;
-  const QkSide& side = is_q ? a.q : a.k;
-  const int head0 = (is_q ? group : group - a.groups_q) * ROWS;
-  const int rows = (is_q ? a.heads : a.heads_k) - head0;  // (may be over ROWS)
-  int pos = 0;
-  bool live = real && p.a >= 0;
-  if (a.positions) {
-    pos = __ldg(a.positions + token);
-    live = live && pos >= 0 && pos < a.max_pos;
-  }
-  const uint16_t* in = side.in + (long long)token * side.in_row + (long long)head0 * side.in_head;
-  RowBits raw[ROWS];
-#pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    raw[i].a = raw[i].b = make_uint2(0u, 0u);
-    // (Not through the read-only path: the output may be the input.)
-    if (live && i < rows) {
-      raw[i].a = *reinterpret_cast<const uint2*>(in + i * side.in_head + p.a);
-      raw[i].b = *reinterpret_cast<const uint2*>(in + i * side.in_head + p.b);
-    }
-  }
-  RopeRow t;
-  const bool turn = live && p.turns;
-  if (turn) t = load_rope(a.rope, a.rope.table + (long long)pos * a.rope.rot_dim, sub);
+  const bool whole = whole_pieces(a.rope);
   const bool any_weight = a.q.weight != nullptr || a.k.weight != nullptr;
-  const float* wp = side.weight;
-  float w[8];
+  // (Every lane of a warp goes through every turn, for the shuffles.)
+  const unsigned per_grid = gridDim.x * (256u / LANES);
+  for (unsigned first = (blockIdx.x * 256u + (threadIdx.x & ~31u)) / LANES; first < a.units;
+       first += per_grid) {
+    const unsigned unit = first + (threadIdx.x & 31u) / LANES;
+    const bool real = unit < a.units;
+    const unsigned token = real ? unit / (unsigned)a.groups : 0;
+    const int group = real ? (int)(unit - token * a.groups) : 0;
+    const bool is_q = group < a.groups_q;
+    const QkSide& side = is_q ? a.q : a.k;
+    const int head0 = (is_q ? group : group - a.groups_q) * ROWS;
+    const int rows = (is_q ? a.heads : a.heads_k) - head0;  // (may be over ROWS)
+    const int pos = a.positions ? __ldg(a.positions + token) : 0;
+    const bool live = real && p.a >= 0 && (!a.positions || (pos >= 0 && pos < a.max_pos));
+    const uint16_t* in = side.in + (long long)token * side.in_row + (long long)head0 * side.in_head;
+    RowBits raw[ROWS];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) w[j] = 1.f;
-  if (wp && p.a >= 0) {
-    const float4 w0 = __ldg(reinterpret_cast<const float4*>(wp + p.a));
-    const float4 w1 = __ldg(reinterpret_cast<const float4*>(wp + p.b));
-    w[0] = w0.x; w[1] = w0.y; w[2] = w0.z; w[3] = w0.w;
-    w[4] = w1.x; w[5] = w1.y; w[6] = w1.z; w[7] = w1.w;
-  }
-  uint16_t* out = side.out + (long long)token * side.out_row + (long long)head0 * side.out_head;
+    for (int i = 0; i < ROWS; ++i) {
+      raw[i].a = raw[i].b = make_uint2(0u, 0u);
+      // (Not through the read-only path: the output may be the input.)
+      if (live && i < rows) raw[i] = load_row(in + i * side.in_head, p, whole);
+    }
+    RopeRow t;
+    const bool turn = live && p.turns;
+    if (turn) t = load_rope(a.rope, a.rope.table + (long long)pos * a.rope.rot_dim, sub);
+    const float* wp = side.weight;
+    uint64_t w[4];
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    float x[8];
-    unpack_row(raw[i], x);
-    // (A warp can hold rows of q and of k: every lane goes through the
-    // shuffles, a side without a weight is scaled by 1.)
-    if (any_weight) norm_row<LANES>(x, w, a.inv_dim, a.eps, wp != nullptr);
-    if (turn) rotate_row(x, a.rope, t);
-    if (live && i < rows) {
-      *reinterpret_cast<uint2*>(out + i * side.out_head + p.a) =
-          make_uint2(ptx::pack_bf16x2(x[0], x[1]), ptx::pack_bf16x2(x[2], x[3]));
-      *reinterpret_cast<uint2*>(out + i * side.out_head + p.b) =
-          make_uint2(ptx::pack_bf16x2(x[4], x[5]), ptx::pack_bf16x2(x[6], x[7]));
+    for (int j = 0; j < 4; ++j) w[j] = ptx::f2_pack(1.f, 1.f);
+    if (wp && p.a >= 0) load_weights(wp, p, w);
+    uint16_t* out = side.out + (long long)token * side.out_row + (long long)head0 * side.out_head;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      uint64_t x[4];
+      unpack_row(raw[i], x);
+      // (A warp can hold rows of q and of k: every lane goes through the
+      // shuffles, a side without a weight is scaled by 1.)
+      if (any_weight) norm_row<LANES>(x, w, a.inv_dim, a.eps, wp != nullptr);
+      if (turn) rotate_row(x, a.rope, t);
+      if (live && i < rows) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ptx::f2_unpack(x[j], f[2 * j], f[2 * j + 1]);
+        RowBits v;
+        v.a = make_uint2(ptx::pack_bf16x2(f[0], f[1]), ptx::pack_bf16x2(f[2], f[3]));
+        v.b = make_uint2(ptx::pack_bf16x2(f[4], f[5]), ptx::pack_bf16x2(f[6], f[7]));
+        store_row(out + i * side.out_head, p, whole, v);
+      }
     }
   }
 }
