@@ -439,14 +439,23 @@ def fa_qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=
     """
     import torch
     lib = load_library()
-    given = [(n, t) for n, t in (("q", q), ("k", k)) if t is not None]
-    if not given:
+    bf16 = torch.bfloat16
+    if q is not None:
+        _check(q, "q", bf16, 3, view=True)
+        T, H, d = q.shape
+        qr, qh, _ = q.stride()
+    if k is not None:
+        _check(k, "k", bf16, 3, view=True)
+        Tk, Hk, dk = k.shape
+        kr, kh, _ = k.stride()
+        if q is None:
+            T, H, d, qr, qh = Tk, 0, dk, 0, 0
+        elif Tk != T or dk != d:
+            raise ValueError(f"k shape {tuple(k.shape)} inconsistent with q")
+    elif q is None:
         raise ValueError("one of q and k is needed")
-    for name, t in given:
-        _check(t, name, torch.bfloat16, 3, view=True)
-    T, _, d = given[0][1].shape
-    if len(given) == 2 and (k.shape[0] != T or k.shape[2] != d):
-        raise ValueError(f"k shape {tuple(k.shape)} inconsistent with q")
+    else:
+        Hk, kr, kh = 0, 0, 0
     rot, max_pos = _check_rope(cos_sin, (("q_weight", q_weight), ("k_weight", k_weight)), d)
     if positions is not None:
         _check(positions, "positions", torch.int32, 1)
@@ -457,20 +466,21 @@ def fa_qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=
                            ("q_weight", q_weight), ("k_weight", k_weight), ("q_out", q_out),
                            ("k_out", k_out)), stream)
     with here:
-        sides = []
-        for name, t, o in (("q_out", q, q_out), ("k_out", k, k_out)):
-            if t is None:
-                if o is not None:
-                    raise ValueError(f"{name} without its input")
-                sides.append((None, 0, 0, 0, None, 0, 0))
-                continue
-            if o is None:
-                o = torch.empty(t.shape, dtype=torch.bfloat16, device=t.device)
-            else:
-                _check(o, name, torch.bfloat16, 3, view=True)
-                _shape(o, name, t.shape)
-            sides.append((t, *t.stride()[:2], t.shape[1], o, *o.stride()[:2]))
-        (q, qr, qh, H, q_out, qor, qoh), (k, kr, kh, Hk, k_out, kor, koh) = sides
+        qor = qoh = kor = koh = 0
+        if q is not None and q_out is None:
+            q_out = torch.empty((T, H, d), dtype=bf16, device=q.device)
+            qor, qoh = H * d, d
+        elif q_out is not None:
+            _check(q_out, "q_out", bf16, 3, view=True)
+            _shape(q_out, "q_out", (T, H, d))
+            qor, qoh, _ = q_out.stride()
+        if k is not None and k_out is None:
+            k_out = torch.empty((T, Hk, d), dtype=bf16, device=k.device)
+            kor, koh = Hk * d, d
+        elif k_out is not None:
+            _check(k_out, "k_out", bf16, 3, view=True)
+            _shape(k_out, "k_out", (T, Hk, d))
+            kor, koh, _ = k_out.stride()
         st = lib.fa_qk_norm_rope(
             _p(q), qr, qh, _p(k), kr, kh, _p(positions), _p(cos_sin), _p(q_weight), _p(k_weight),
             T, H, Hk, d, rot, max_pos, bool(interleaved), eps, _p(q_out), qor, qoh, _p(k_out),

@@ -213,7 +213,7 @@ extern "C" fa_status fa_paged_kv_append(
   if (st != FA_OK) return st;
   if (!valid_rope(cos_sin, rot_dim, max_pos, head_dim) || !(eps >= 0.f) || !std::isfinite(eps))
     return FA_ERR_INVALID_ARG;
-  if (!is_aligned(k, 16) || !is_aligned(v, 16) || !is_aligned(k_weight, 4))
+  if (!is_aligned(k, 16) || !is_aligned(v, 16) || !is_aligned(k_weight, 16))
     return FA_ERR_INVALID_ARG;
   if (total_new > 0 && (!is_valid_view(k_row_stride, k_head_stride, num_heads_k, head_dim) ||
                         !is_valid_view(v_row_stride, v_head_stride, num_heads_k, head_dim)))
@@ -257,8 +257,11 @@ extern "C" fa_status fa_paged_kv_append(
   const int items = 2 * num_heads_k;
   if (step) {
     const int threads = 32 * std::min(items, 16);
-    if (head_dim <= 64) fa::kv_append_step_kernel<8><<<(unsigned)chunks, threads, 0, s>>>(a);
-    else fa::kv_append_step_kernel<16><<<(unsigned)chunks, threads, 0, s>>>(a);
+    auto run = [&](auto kernel) { kernel<<<(unsigned)chunks, threads, 0, s>>>(a); };
+    if (head_dim <= 64)
+      run(interleaved ? fa::kv_append_step_kernel<8, true> : fa::kv_append_step_kernel<8, false>);
+    else
+      run(interleaved ? fa::kv_append_step_kernel<16, true> : fa::kv_append_step_kernel<16, false>);
   } else {
     // Blocks of 256 threads, 128 at 64 dims; as few items each as leave all
     // of them resident at once, three (six) an SM.
@@ -268,8 +271,12 @@ extern "C" fa_status fa_paged_kv_append(
     a.per_block = (int)((items + blocks - 1) / blocks);
     const dim3 grid((unsigned)chunks, (items + a.per_block - 1) / a.per_block);
     const size_t table = (size_t)fa::kPageTokens * rot_dim * sizeof(float);
-    if (head_dim <= 64) fa::kv_append_prompt_kernel<8><<<grid, threads, table, s>>>(a);
-    else fa::kv_append_prompt_kernel<16><<<grid, threads, table, s>>>(a);
+    auto run = [&](auto kernel) { kernel<<<grid, threads, table, s>>>(a); };
+    if (head_dim <= 64)
+      run(interleaved ? fa::kv_append_prompt_kernel<8, true> : fa::kv_append_prompt_kernel<8, false>);
+    else
+      run(interleaved ? fa::kv_append_prompt_kernel<16, true>
+                      : fa::kv_append_prompt_kernel<16, false>);
   }
   return launched();
 }

@@ -133,8 +133,9 @@ __device__ __forceinline__ void norm_row(uint64_t* x, const uint64_t* w, float i
 }
 
 // Rotates the lane's pairs of dims in place.
-__device__ __forceinline__ void rotate_row(uint64_t* x, const RopeParams& r, const RopeRow& t) {
-  if (r.interleaved) {
+template <bool INTERLEAVED>
+__device__ __forceinline__ void rotate_row(uint64_t* x, const RopeRow& t) {
+  if constexpr (INTERLEAVED) {
     float c[4], s[4];
     ptx::f2_unpack(t.c[0], c[0], c[1]);
     ptx::f2_unpack(t.c[1], c[2], c[3]);
@@ -158,12 +159,12 @@ __device__ __forceinline__ void rotate_row(uint64_t* x, const RopeParams& r, con
 
 // The lane's 8 weights as pairs.
 __device__ __forceinline__ void load_weights(const float* w, const RowPieces& p, uint64_t* out) {
-  const int at[2] = {p.a, p.b};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    out[2 * i] = ptx::f2_pack(__ldg(w + at[i]), __ldg(w + at[i] + 1));
-    out[2 * i + 1] = ptx::f2_pack(__ldg(w + at[i] + 2), __ldg(w + at[i] + 3));
-  }
+  const float4 u = __ldg(reinterpret_cast<const float4*>(w + p.a));
+  const float4 v = __ldg(reinterpret_cast<const float4*>(w + p.b));
+  out[0] = ptx::f2_pack(u.x, u.y);
+  out[1] = ptx::f2_pack(u.z, u.w);
+  out[2] = ptx::f2_pack(v.x, v.y);
+  out[3] = ptx::f2_pack(v.z, v.w);
 }
 
 }  // namespace fa
