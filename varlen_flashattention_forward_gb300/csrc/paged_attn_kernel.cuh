@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         };
         auto place_rows = [&](int n0r) {  // rows n0r + lane: token, head
           const int row = g.row_tile * N + n0r + lane;
-          const int tok = (int)((unsigned)row / (unsigned)sh.group);
+          const int tok = token_of(sh, row);
           row_q = g.q.lo + tok;
           row_h = g.head * sh.group + row - tok * sh.group;
         };
@@ -628,8 +628,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             if (n + lane < N) {
               plan.out[n + lane] = row_q * a.heads + row_h;
               plan.lse[n + lane] = row_h * a.total_q + row_q;
-              plan.token[n + lane] =
-                  row_q - g.q.lo - (int)((unsigned)(g.row_tile * N) / (unsigned)sh.group);
+              plan.token[n + lane] = row_q - g.q.lo - token_of(sh, g.row_tile * N);
             }
           }
           if (first) load_rows(0);  // (ahead of the pages' loads in the memory system)
@@ -646,21 +645,29 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             plan.q0 = g.q.lo;
             plan.row0 = row0;
             plan.rows = rows;
-            plan.tok0 = row0 / sh.group;
-            plan.tok1 = (row0 + rows - 1) / sh.group;
+            plan.tok0 = token_of(sh, row0);
+            plan.tok1 = token_of(sh, row0 + rows - 1);
             plan.at0 = (long long)g.len - g.q.n + plan.tok0;
             plan.tiles = g.count;
             plan.whole = g.count == g.unit_count;
             plan.unit_end =
                 g.part_lo == 0 && g.count < g.unit_count ? g.unit_end : -1;
           }
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->plan_full[slot]));
           // The scales under way.
           if (cell >= 0) {
             ks = __ldg(a.k_scale + cell);
             vs = __ldg(a.v_scale + cell);
           }
+          // The first batch is not published before its scales and rows of Q
+          // are here: behind the first K and V tiles of all SMs (17 MB) they
+          // would take some 3 us.
+          if (b == 0) {
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+              asm volatile("" ::"r"(raw[j].x), "f"(ks), "f"(vs) : "memory");
+          }
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->plan_full[slot]));
         }
         const int held = cell >= 0;
         // Then the next batch's pages and this one's scales and Q, in this
@@ -699,6 +706,15 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
 #pragma unroll 1
               for (int j = 0; j < kBatch; ++j) {
                 const int n = j0 + j * kGroups + lane / kLanes;
+                if (j0 + j * kGroups >= rows) {
+                  // Rows past the last: zeros.
+                  const int us = D == 128 ? ((dim0 >> 4) ^ (n & 7)) : ((dim0 >> 4) ^ ((n >> 1) & 3));
+                  uint8_t* at = q_s + n * C::kRow + us * 16 + (dim0 & 8);
+                  *reinterpret_cast<uint2*>(at) = make_uint2(0u, 0u);
+                  *reinterpret_cast<uint2*>(at + N * C::kRow) = make_uint2(0u, 0u);
+                  if (sub == 0) cb->qs[seg % kPagedPlans][n] = a.scale_log2;
+                  continue;
+                }
                 float x[8];
                 unpack_bf16x8(raw[j], x);
                 float mx = 0.f;

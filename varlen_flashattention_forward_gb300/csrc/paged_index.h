@@ -113,7 +113,21 @@ constexpr int kUnitCost = 4;  // in tiles
 struct AttnShape {
   int heads_k, group, rows;  // kv heads, query heads of one, rows of a tile
   int causal, window, held;  // held: positions of the page table
+  unsigned group_inverse;    // floor(2^32 / group), 2^32 - 1 for 1
 };
+inline unsigned inverse_of(int group) {
+  return group > 1 ? (unsigned)((1ull << 32) / (unsigned)group) : 0xffffffffu;
+}
+// row / group: the product with the inverse is the quotient or one less.
+FA_HD int token_of(const AttnShape& s, unsigned row) {
+#if defined(__CUDA_ARCH__)
+  unsigned q = __umulhi(row, s.group_inverse);
+#else
+  unsigned q = (unsigned)(((unsigned long long)row * s.group_inverse) >> 32);
+#endif
+  if (row - q * s.group >= (unsigned)s.group) ++q;
+  return (int)q;
+}
 
 // n * group is at most the number of query rows of the call, below 2^31.
 FA_HD int row_tiles(const AttnShape& s, int n) {
@@ -124,8 +138,7 @@ FA_HD KeyRange tile_keys(const AttnShape& s, int t, int n, int len) {
   const unsigned r0 = (unsigned)t * s.rows, all = (unsigned)n * s.group;
   unsigned r1 = r0 + s.rows;
   if (r1 > all) r1 = all;
-  return key_range((int)(r0 / (unsigned)s.group), (int)((r1 - 1) / (unsigned)s.group), n, len,
-                   s.held, s.causal != 0, s.window);
+  return key_range(token_of(s, r0), token_of(s, r1 - 1), n, len, s.held, s.causal != 0, s.window);
 }
 // First key tile and number of key tiles; a unit without keys keeps one (all
 // masked), which writes its empty rows.
@@ -207,9 +220,15 @@ FA_HD bool walk_next(SegmentWalk* w, const AttnShape& s, const Before& before, c
       while (before(w->seq + 1) <= w->at) ++w->seq;  // sequences without query rows
       seq_of(w->seq, &g->q, &g->len);
       const int in_seq = w->at - before(w->seq);
+      // (The sequence's cost without the cap, so that no head is past the last.)
       const int per_head = capped_cost(head_cost(s, g->q.n, g->len));
-      w->head = (int)((unsigned)in_seq / (unsigned)per_head);
-      int left = in_seq - w->head * per_head;
+      int left = in_seq;
+      w->head = 0;
+      FA_ROLLED
+      while (left >= per_head) {
+        left -= per_head;
+        ++w->head;
+      }
       w->row_tile = 0;
       FA_ROLLED
       for (;;) {
