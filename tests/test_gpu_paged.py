@@ -647,3 +647,186 @@ def test_two_streams_at_once(cuda_device):
                                True, -1)
         for o, lse in got[i]:
             compare_attn(o.cpu(), lse.cpu(), *want)
+
+
+# ------------------------------------------------- shapes of tiles and calls
+@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("tokens,rows", [(1, 16), (7, 32), (13, 64)])
+def test_attn_row_tiles(cuda_device, d, tokens, rows):
+    assert fa.fa_paged_attn_plan(2, 2 * tokens, 8, 2, d, tokens)[1] == rows
+    check_attn([tokens, max(1, tokens - 2)], [700, 260], 8, 2, d, seed=d + tokens)
+    check_attn([tokens, 1], [300, 70], 8, 2, d, window=100, seed=d + tokens + 1)
+
+
+@pytest.mark.parametrize("hint", [1, 3, 1000])
+def test_attn_wrong_hints_do_not_matter(cuda_device, hint):
+    gen = torch.Generator().manual_seed(53)
+    lens, q_lens = [200, 65], [5, 2]
+    pages, num = plain.make_pages(lens, gen)
+    (kc, ks), (vc, vs) = (plain.make_cache(lens, pages, num, 2, 64, gen) for _ in range(2))
+    q = torch.randn((7, 8, 64), generator=gen).bfloat16()
+    cpu = (q, kc, vc, ks, vs, plain.cum(q_lens), torch.tensor(lens, dtype=torch.int32), pages)
+    o, lse = fa.fa_paged_attn(*dev(*cpu), max_seqlen_q=hint, max_seqlen_k=hint, return_lse=True)
+    want = plain.attention(q, kc, vc, ks, vs, [0, 5, 7], lens, pages, 0.125, True, -1)
+    compare_attn(o.cpu(), lse.cpu(), *want)
+
+
+def test_attn_batches_of_several_launches(cuda_device):
+    # 1024 sequences to a launch, 512 with 64-row tiles.
+    lens = [1 + 29 * i % 130 for i in range(1300)]
+    check_attn([1] * 1300, lens, 2, 1, 64, seed=54)
+    lens = [9 + 29 * i % 130 for i in range(700)]
+    check_attn([1 + i % 9 for i in range(700)], lens, 8, 1, 64, seed=55)
+
+
+def test_attn_given_workspace(cuda_device):
+    gen = torch.Generator().manual_seed(56)
+    lens = [3000, 129]
+    pages, num = plain.make_pages(lens, gen)
+    (kc, ks), (vc, vs) = (plain.make_cache(lens, pages, num, 2, 64, gen) for _ in range(2))
+    q = torch.randn((2, 8, 64), generator=gen).bfloat16()
+    args = dev(q, kc, vc, ks, vs, plain.cum([1, 1]), torch.tensor(lens, dtype=torch.int32), pages)
+    need = fa.fa_paged_attn_plan(2, 2, 8, 2, 64, 1)[2]
+    ws = torch.full((need + 16,), 255, dtype=torch.uint8, device="cuda")  # NaN as fp32
+    want = plain.attention(q, kc, vc, ks, vs, [0, 1, 2], lens, pages, 0.125, True, -1)
+    for _ in range(2):
+        o, lse = fa.fa_paged_attn(*args, max_seqlen_q=1, return_lse=True, workspace=ws[:need])
+        compare_attn(o.cpu(), lse.cpu(), *want)
+    assert (ws[need:] == 255).all()
+    for bad in (ws[:need - 16], ws[8:need + 8]):
+        with pytest.raises(fa.FaError) as e:
+            fa.fa_paged_attn(*args, max_seqlen_q=1, workspace=bad)
+        assert e.value.status == fa.FA_ERR_INVALID_ARG
+
+
+def test_attn_special_queries_and_scales(cuda_device):
+    # A NaN or an infinity in a row of q makes that row NaN and no other; a
+    # page whose V scale is 0 adds zeros, not NaN.
+    gen = torch.Generator().manual_seed(57)
+    lens = [200]
+    pages, num = plain.make_pages(lens, gen)
+    (kc, ks), (vc, vs) = (plain.make_cache(lens, pages, num, 1, 64, gen) for _ in range(2))
+    vs[pages[0, 1]] = 0.0
+    q = torch.randn((2, 4, 64), generator=gen).bfloat16()
+    q[0, 1, 3], q[1, 2, 60], q[1, 0] = math.nan, math.inf, 0.0
+    cpu = (q, kc, vc, ks, vs, plain.cum([2]), torch.tensor(lens, dtype=torch.int32), pages)
+    o, lse = (t.cpu() for t in fa.fa_paged_attn(*dev(*cpu), return_lse=True))
+    bad = torch.zeros((2, 4), dtype=torch.bool)
+    bad[0, 1] = bad[1, 2] = True
+    assert torch.isnan(o[bad]).all() and torch.isnan(lse.t()[bad]).all()
+    q[bad] = 0.0
+    wo, wl, w, a = plain.attention(q, kc, vc, ks, vs, [0, 2], lens, pages, 0.125, True, -1)
+    o[bad], wo[bad], lse.t()[bad], wl.t()[bad] = 0.0, 0.0, 0.0, 0.0
+    compare_attn(o, lse, wo, wl, w, a)
+
+
+def test_attn_nan_keys_behind_a_row_do_not_reach_it(cuda_device):
+    gen = torch.Generator().manual_seed(58)
+    lens = [130]
+    pages, num = plain.make_pages(lens, gen)
+    (kc, ks), (vc, vs) = (plain.make_cache(lens, pages, num, 1, 64, gen) for _ in range(2))
+    kc.view(torch.uint8)[pages[0, 2], 0, 1] = plain.NAN_CODE  # the key of the last row
+    q = torch.randn((3, 4, 64), generator=gen).bfloat16()
+    cpu = (q, kc, vc, ks, vs, plain.cum([3]), torch.tensor(lens, dtype=torch.int32), pages)
+    o, lse = (t.cpu() for t in fa.fa_paged_attn(*dev(*cpu), return_lse=True))
+    assert torch.isnan(o[2]).all() and torch.isnan(lse[:, 2]).all()
+    # The first two rows, against a cache without that key.
+    wo, wl, w, a = plain.attention(q[:2], kc, vc, ks, vs, [0, 2], [129], pages, 0.125, True, -1)
+    compare_attn(o[:2], lse[:, :2], wo, wl, w, a)
+
+
+def test_attn_shared_pages(cuda_device):
+    # Sequences with a common prefix name the same pages.
+    gen = torch.Generator().manual_seed(59)
+    lens = [300, 300, 192]
+    pages, num = plain.make_pages(lens, gen)
+    pages[1, :3] = pages[0, :3]
+    pages[2, :3] = pages[0, :3]
+    (kc, ks), (vc, vs) = (plain.make_cache(lens, pages, num, 2, 128, gen) for _ in range(2))
+    q = torch.randn((3, 8, 128), generator=gen).bfloat16()
+    cpu = (q, kc, vc, ks, vs, plain.cum([1, 1, 1]), torch.tensor(lens, dtype=torch.int32), pages)
+    o, lse = fa.fa_paged_attn(*dev(*cpu), return_lse=True)
+    want = plain.attention(q, kc, vc, ks, vs, [0, 1, 2, 3], lens, pages, 128 ** -0.5, True, -1)
+    compare_attn(o.cpu(), lse.cpu(), *want)
+
+
+def test_two_graphs_replayed_at_once(cuda_device):
+    """Each captured call has the workspace of its own capture."""
+    gen = torch.Generator().manual_seed(63)
+    graphs = []
+    for i in range(2):
+        lens = [4000 - 700 * i, 300]
+        pages, num = plain.make_pages(lens, gen)
+        (kc, ks), (vc, vs) = (plain.make_cache(lens, pages, num, 2, 64, gen) for _ in range(2))
+        q = torch.randn((2, 8, 64), generator=gen).bfloat16()
+        cpu = (q, kc, vc, ks, vs, plain.cum([1, 1]), torch.tensor(lens, dtype=torch.int32), pages)
+        args, s, g = dev(*cpu), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            fa.fa_paged_attn(*args, return_lse=True)
+        s.synchronize()
+        with torch.cuda.graph(g, stream=s):
+            out = fa.fa_paged_attn(*args, return_lse=True)
+        graphs.append((cpu, args, s, g, out))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for _, _, s, g, _ in graphs:
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for (q, kc, vc, ks, vs, cu, lens, pages), _, _, _, (o, lse) in graphs:
+        want = plain.attention(q, kc, vc, ks, vs, cu.tolist(), lens.tolist(), pages, 0.125, True, -1)
+        compare_attn(o.cpu(), lse.cpu(), *want)
+
+
+def test_attn_wait_limit_runs_out_then_recovers(cuda_device):
+    """Under a 1 us limit the kernel's waits run out: it reports the timeout,
+    unwinds and returns, and the same call then succeeds under the default."""
+    assert fa.fa_get_device_status() == fa.FA_OK
+    gen = torch.Generator().manual_seed(64)
+    lens = [3000, 200, 64]
+    pages, num = plain.make_pages(lens, gen)
+    (kc, ks), (vc, vs) = (plain.make_cache(lens, pages, num, 2, 128, gen) for _ in range(2))
+    q = torch.randn((4, 8, 128), generator=gen).bfloat16()
+    cpu = (q, kc, vc, ks, vs, plain.cum([1, 2, 1]), torch.tensor(lens, dtype=torch.int32), pages)
+    args = dev(*cpu)
+    try:
+        fa.fa_set_wait_limit_ns(1000)
+        fa.fa_paged_attn(*args, return_lse=True)
+        torch.cuda.synchronize()
+        assert fa.fa_get_device_status() == fa.FA_ERR_DEVICE_TIMEOUT
+    finally:
+        fa.fa_set_wait_limit_ns(0)
+    assert fa.fa_get_device_status() == fa.FA_OK
+    o, lse = fa.fa_paged_attn(*args, return_lse=True)
+    want = plain.attention(q, kc, vc, ks, vs, [0, 1, 3, 4], lens, pages, 128 ** -0.5, True, -1)
+    compare_attn(o.cpu(), lse.cpu(), *want)
+    assert fa.fa_get_device_status() == fa.FA_OK
+
+
+def test_append_then_attend_on_a_given_stream(cuda_device):
+    """Append and attention of one cache on one side stream, given by hand."""
+    gen = torch.Generator().manual_seed(65)
+    pages, num = plain.make_pages([200, 70], gen)
+    kc = torch.zeros((num, 2, 64, 64), dtype=torch.float8_e4m3fn, device="cuda")
+    vc, ks, vs = kc.clone(), torch.zeros((num, 2), device="cuda"), torch.zeros((num, 2),
+                                                                             device="cuda")
+    kv = torch.randn((270, 4, 64), generator=gen).bfloat16()
+    q = torch.randn((2, 4, 64), generator=gen).bfloat16()
+    cu, lens = plain.cum([200, 70]), torch.tensor([200, 70], dtype=torch.int32)
+    kvd, qd, cud, lensd, pd, one = dev(kv, q, cu, lens, pages, plain.cum([1, 1]))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    fa.fa_paged_kv_append(kvd[:, :2], kvd[:, 2:], cud, lensd, pd, kc, vc, ks, vs, stream=s)
+    o, lse = fa.fa_paged_attn(qd, kc, vc, ks, vs, one, lensd, pd, return_lse=True, stream=s)
+    s.synchronize()
+    want = plain.attention(q, kc.cpu(), vc.cpu(), ks.cpu(), vs.cpu(), [0, 1, 2], [200, 70], pages,
+                           0.125, True, -1)
+    compare_attn(o.cpu(), lse.cpu(), *want)
+
+
+@pytest.mark.parametrize("d", [64, 80, 128])
+def test_append_by_either_kernel(cuda_device, d):
+    # Both kernels (few tokens a sequence, many) on the same positions.
+    check_append([100] + [0] * 30, [20] + [5] * 30, 2, d, 16 * (d // 16), True, seed=66 + d)
+    check_append([100, 30], [20, 5], 2, d, 16 * (d // 16), True, seed=67 + d)
