@@ -348,27 +348,22 @@ def fa_merge_attn_states(prefix_out, prefix_lse, suffix_out, suffix_lse, out=Non
     return out, out_lse
 
 
-def _device(tensors, stream):
-    """The one CUDA device that the named tensors (None: left out) are on, and
-    a context that makes it and the call's stream current where they are not:
+def _device(stream, first, *others):
+    """Index of the CUDA device that the tensors (None: left out) are on, and a
+    context that makes it and the call's stream current where they are not:
     what is allocated in it belongs to that stream."""
     import torch
-    index = None
-    for name, t in tensors:
-        if t is None:
-            continue
-        i = t.get_device()
-        if i != index:
-            if i < 0:
-                raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
-            if index is not None:
-                raise ValueError(f"{name} is on {t.device}, other tensors on cuda:{index}")
-            index = i
+    index = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors on {t.device} and {first.device}: one CUDA device is needed")
+    if index < 0:
+        raise ValueError(f"CUDA tensors are needed, got {first.device}")
     if stream is not None:
         if stream.device.index != index:
             raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
         return index, torch.cuda.stream(stream)
-    if index != torch.cuda.current_device():
+    if index != torch._C._cuda_getDevice():
         return index, torch.cuda.device(index)
     return index, _NO_CONTEXT
 
@@ -408,22 +403,35 @@ def _check_rope(cos_sin, weights, d):
 def _check_cache(k_cache, v_cache, k_scale, v_scale, cu_seqlens, page_table):
     """(batch, pages, kv heads, head dim, pages of a sequence) of a cache."""
     import torch
-    _check(k_cache, "k_cache", torch.float8_e4m3fn, 4)
-    _check(v_cache, "v_cache", torch.float8_e4m3fn, 4)
-    _check(k_scale, "k_scale", torch.float32, 2)
-    _check(v_scale, "v_scale", torch.float32, 2)
-    _check(cu_seqlens, "cu_seqlens", torch.int32, 1)
-    _check(page_table, "page_table", torch.int32, 2)
-    pages, hk, page, d = k_cache.shape
+    f8, f32, i32 = torch.float8_e4m3fn, torch.float32, torch.int32
+    # (In one expression: these calls are made at every decode step.)
+    if not (k_cache.dtype is f8 and v_cache.dtype is f8 and k_scale.dtype is f32
+            and v_scale.dtype is f32 and cu_seqlens.dtype is i32 and page_table.dtype is i32
+            and k_cache.dim() == 4 and k_scale.dim() == 2 and cu_seqlens.dim() == 1
+            and page_table.dim() == 2 and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and k_scale.is_contiguous() and v_scale.is_contiguous()
+            and cu_seqlens.is_contiguous() and page_table.is_contiguous()):
+        _check(k_cache, "k_cache", f8, 4)
+        _check(v_cache, "v_cache", f8, 4)
+        _check(k_scale, "k_scale", f32, 2)
+        _check(v_scale, "v_scale", f32, 2)
+        _check(cu_seqlens, "cu_seqlens", i32, 1)
+        _check(page_table, "page_table", i32, 2)
+    shape = k_cache.shape
+    pages, hk, page, d = shape
     if page != 64:
         raise ValueError(f"a cache page has 64 tokens, got {page}")
-    _shape(v_cache, "v_cache", k_cache.shape)
-    _shape(k_scale, "k_scale", (pages, hk))
-    _shape(v_scale, "v_scale", (pages, hk))
+    if v_cache.shape != shape:
+        _shape(v_cache, "v_cache", shape)
+    scales = (pages, hk)
+    if k_scale.shape != scales or v_scale.shape != scales:
+        _shape(k_scale, "k_scale", scales)
+        _shape(v_scale, "v_scale", scales)
+    rows, width = page_table.shape
     batch = cu_seqlens.shape[0] - 1
-    if page_table.shape[0] != batch:
+    if rows != batch:
         raise ValueError("page_table must have one row per sequence")
-    return batch, pages, hk, d, page_table.shape[1]
+    return batch, pages, hk, d, width
 
 
 def fa_qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=1e-6,
@@ -462,9 +470,8 @@ def fa_qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=
         _shape(positions, "positions", (T,))
     elif rot:
         raise ValueError("positions are needed for the rotation")
-    index, here = _device((("q", q), ("k", k), ("positions", positions), ("cos_sin", cos_sin),
-                           ("q_weight", q_weight), ("k_weight", k_weight), ("q_out", q_out),
-                           ("k_out", k_out)), stream)
+    index, here = _device(stream, k if q is None else q, k, positions, cos_sin, q_weight, k_weight,
+                          q_out, k_out)
     with here:
         qor = qoh = kor = koh = 0
         if q is not None and q_out is None:
@@ -512,19 +519,16 @@ def fa_paged_kv_append(k, v, cu_seqlens, seq_lens, page_table, k_cache, v_cache,
     _shape(k, "k", (k.shape[0], hk, d))
     _shape(v, "v", k.shape)
     rot, max_pos = _check_rope(cos_sin, (("k_weight", k_weight),), d)
-    index, here = _device((("k", k), ("v", v), ("cu_seqlens", cu_seqlens),
-                           ("seq_lens", seq_lens), ("page_table", page_table),
-                           ("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale),
-                           ("v_scale", v_scale), ("cos_sin", cos_sin), ("k_weight", k_weight)),
-                          stream)
+    index, here = _device(stream, k, v, cu_seqlens, seq_lens, page_table, k_cache, v_cache,
+                          k_scale, v_scale, cos_sin, k_weight)
     kr, kh, _ = k.stride()
     vr, vh, _ = v.stride()
     with here:
         st = lib.fa_paged_kv_append(
-            _p(k), kr, kh, _p(v), vr, vh, _p(cu_seqlens), _p(seq_lens), _p(page_table), batch,
-            k.shape[0], hk, d, pages, width, _p(k_weight), eps, _p(cos_sin), rot, max_pos,
-            bool(interleaved), _p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale),
-            _raw_stream(index))
+            k.data_ptr(), kr, kh, v.data_ptr(), vr, vh, cu_seqlens.data_ptr(),
+            seq_lens.data_ptr(), page_table.data_ptr(), batch, k.shape[0], hk, d, pages, width,
+            _p(k_weight), eps, _p(cos_sin), rot, max_pos, bool(interleaved), k_cache.data_ptr(),
+            v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), _raw_stream(index))
     if st != FA_OK:
         raise FaError(st, "fa_paged_kv_append")
 
@@ -569,11 +573,8 @@ def fa_paged_attn(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, seq_lens,
         raise ValueError(f"q has head dim {dq}, the cache {d}")
     if softmax_scale is None:
         softmax_scale = d ** -0.5
-    index, here = _device((("q", q), ("k_cache", k_cache), ("v_cache", v_cache),
-                           ("k_scale", k_scale), ("v_scale", v_scale),
-                           ("cu_seqlens_q", cu_seqlens_q), ("seq_lens", seq_lens),
-                           ("page_table", page_table), ("out", out), ("lse", lse),
-                           ("workspace", workspace)), stream)
+    index, here = _device(stream, q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, seq_lens,
+                          page_table, out, lse, workspace)
     with here:
         if out is None:
             out = torch.empty((T, H, d), dtype=torch.bfloat16, device=q.device)
@@ -593,10 +594,11 @@ def fa_paged_attn(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, seq_lens,
             need = workspace.shape[0]
         qr, qh, _ = q.stride()
         st = lib.fa_paged_attn(
-            _p(q), qr, qh, _p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale), _p(cu_seqlens_q),
-            _p(seq_lens), _p(page_table), batch, T, H, hk, d, pages, width, max_seqlen_q,
-            max_seqlen_k, softmax_scale, bool(causal), window_left, _p(out), _p(lse),
-            _p(workspace), need, _raw_stream(index))
+            q.data_ptr(), qr, qh, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), cu_seqlens_q.data_ptr(), seq_lens.data_ptr(),
+            page_table.data_ptr(), batch, T, H, hk, d, pages, width, max_seqlen_q, max_seqlen_k,
+            softmax_scale, bool(causal), window_left, out.data_ptr(), _p(lse),
+            workspace.data_ptr(), need, _raw_stream(index))
     if st != FA_OK:
         raise FaError(st, "fa_paged_attn")
     return (out, lse) if lse is not None else out
@@ -618,25 +620,27 @@ def fa_paged_kv_gather(k_cache, v_cache, k_scale, v_scale, cu_seqlens, page_tabl
     lib = load_library()
     batch, pages, hk, d, width = _check_cache(k_cache, v_cache, k_scale, v_scale, cu_seqlens,
                                               page_table)
-    index, here = _device((("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale),
-                           ("v_scale", v_scale), ("cu_seqlens", cu_seqlens),
-                           ("page_table", page_table), ("k_out", k_out), ("v_out", v_out)),
-                          stream)
+    index, here = _device(stream, k_cache, v_cache, k_scale, v_scale, cu_seqlens, page_table,
+                          k_out, v_out)
     with here:
-        outs = []
-        for name, o in (("k_out", k_out), ("v_out", v_out)):
-            if o is None:
-                o = torch.empty((total_k, hk, d), dtype=torch.bfloat16, device=k_cache.device)
-            else:
-                _check(o, name, torch.bfloat16, 3)
-                _shape(o, name, (total_k, hk, d))
-            outs.append(o)
+        shape = (total_k, hk, d)
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
+        else:
+            _check(k_out, "k_out", torch.bfloat16, 3)
+            _shape(k_out, "k_out", shape)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
+        else:
+            _check(v_out, "v_out", torch.bfloat16, 3)
+            _shape(v_out, "v_out", shape)
         st = lib.fa_paged_kv_gather(
-            _p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale), _p(cu_seqlens), _p(page_table),
-            batch, total_k, hk, d, pages, width, _p(outs[0]), _p(outs[1]), _raw_stream(index))
+            k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            cu_seqlens.data_ptr(), page_table.data_ptr(), batch, total_k, hk, d, pages, width,
+            k_out.data_ptr(), v_out.data_ptr(), _raw_stream(index))
     if st != FA_OK:
         raise FaError(st, "fa_paged_kv_gather")
-    return outs[0], outs[1]
+    return k_out, v_out
 
 
 def fa_set_wait_limit_ns(ns: int) -> None:
