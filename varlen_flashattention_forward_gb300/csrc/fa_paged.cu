@@ -257,11 +257,8 @@ extern "C" fa_status fa_paged_kv_append(
   const int items = 2 * num_heads_k;
   if (step) {
     const int threads = 32 * std::min(items, 16);
-    auto run = [&](auto kernel) { kernel<<<(unsigned)chunks, threads, 0, s>>>(a); };
-    if (head_dim <= 64)
-      run(interleaved ? fa::kv_append_step_kernel<8, true> : fa::kv_append_step_kernel<8, false>);
-    else
-      run(interleaved ? fa::kv_append_step_kernel<16, true> : fa::kv_append_step_kernel<16, false>);
+    if (head_dim <= 64) fa::kv_append_step_kernel<8><<<(unsigned)chunks, threads, 0, s>>>(a);
+    else fa::kv_append_step_kernel<16><<<(unsigned)chunks, threads, 0, s>>>(a);
   } else {
     // Blocks of 256 threads, 128 at 64 dims; as few items each as leave all
     // of them resident at once, three (six) an SM.
@@ -271,12 +268,8 @@ extern "C" fa_status fa_paged_kv_append(
     a.per_block = (int)((items + blocks - 1) / blocks);
     const dim3 grid((unsigned)chunks, (items + a.per_block - 1) / a.per_block);
     const size_t table = (size_t)fa::kPageTokens * rot_dim * sizeof(float);
-    auto run = [&](auto kernel) { kernel<<<grid, threads, table, s>>>(a); };
-    if (head_dim <= 64)
-      run(interleaved ? fa::kv_append_prompt_kernel<8, true> : fa::kv_append_prompt_kernel<8, false>);
-    else
-      run(interleaved ? fa::kv_append_prompt_kernel<16, true>
-                      : fa::kv_append_prompt_kernel<16, false>);
+    if (head_dim <= 64) fa::kv_append_prompt_kernel<8><<<grid, threads, table, s>>>(a);
+    else fa::kv_append_prompt_kernel<16><<<grid, threads, table, s>>>(a);
   }
   return launched();
 }

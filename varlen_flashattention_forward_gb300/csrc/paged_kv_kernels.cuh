@@ -24,14 +24,15 @@ constexpr float kE4m3Max = 448.f;
 // the attention stay far inside fp32.
 constexpr int kScaleExpMax = 64;
 
-// Exponent e of the smallest power of two with amax <= 448 * 2^e, clamped, from
-// the bits of amax (finite, >= 0): 448 = 1.75 * 2^8.
-__device__ __forceinline__ int scale_exponent(uint32_t amax_bits) {
-  const int e = (int)(amax_bits >> 23) - (127 + 8) + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-  return imin(imax(e, -kScaleExpMax), kScaleExpMax);
-}
-__device__ __forceinline__ float power_of_two(int e) {  // |e| < 127
-  return __uint_as_float((uint32_t)(e + 127) << 23);
+// Smallest power of two s with amax <= 448 s, clamped (amax finite, >= 0).
+__device__ __forceinline__ float scale_for(float amax) {
+  // amax / 512 = m 2^e with m in [0.5, 1), and 448 = 512 * 0.875.
+  int e;
+  const float m = frexpf(amax * (1.f / 512.f), &e);
+  if (m > 0.875f) ++e;
+  if (!(amax > 0.f)) e = -kScaleExpMax;
+  e = imin(imax(e, -kScaleExpMax), kScaleExpMax);
+  return ldexpf(1.f, e);
 }
 
 // Two fp32 values as e4m3 codes (round to nearest even, saturating at 448,
@@ -125,7 +126,7 @@ struct AppendChunk {
 // LANES-lane group; an item of at most TEAM * ROWS * (32 / LANES) rows is held
 // in registers between the maximum and the rounding, a longer one is loaded
 // again for the second pass.
-template <int LANES, int ROWS, int TEAM, bool INTERLEAVED>
+template <int LANES, int ROWS, int TEAM>
 struct AppendItem {
   static constexpr int kGroups = 32 / LANES;           // rows of a warp at once
   static constexpr int kPass = TEAM * ROWS * kGroups;  // rows of the team's pass
@@ -190,106 +191,71 @@ struct AppendItem {
       if (is_k && a.k_weight) norm_row<LANES>(x[i], w, a.inv_dim, a.eps);
       const int r = row_of(pass, i);
       if (turn && r < ch.count)
-        rotate_row<INTERLEAVED>(x[i], load_rope(a.rope, table + r * a.rope.rot_dim, sub));
+        rotate_row(x[i], a.rope, load_rope(a.rope, table + r * a.rope.rot_dim, sub));
     }
   }
-  // Goes through items first, first + step, ... below `end`: each one's rows
-  // are under way while the one before it is rounded.  `table_ready` is called
-  // before the first key.
-  template <typename Ready>
-  __device__ __forceinline__ void run(int first, int end, int step, uint32_t* s_amax,
-                                      Ready table_ready) {
+  // The item that begin() has under way; `next` (an item, or -1) is under way
+  // when it returns.
+  __device__ __forceinline__ void finish(int next, float* s_amax) {
+    uint64_t x[ROWS][4];
+    float amax = 0.f;
+    const int passes = kPass >= kPageTokens ? 1 : (ch.count + kPass - 1) / kPass;
 #pragma unroll 1
-    for (int i = first - step; i < end; i += step) {
-      const int next = i + step < end ? i + step : -1;
-      if (i >= first) {
-        if (is_k) table_ready();
-        measure();
-      }
-      uint8_t* const codes_ = codes;
-      float* const scale_ = scale;
-      const float old_ = old;
-      if (held() && next >= 0) begin(next);
-      if (i >= first) round(codes_, scale_, old_, s_amax);
-      if (!held() && next >= 0) begin(next);
-    }
-  }
-  // Whether an item stays in registers from the maximum to the rounding.
-  __device__ __forceinline__ bool held() const {
-    return kPass >= kPageTokens || ch.count <= kPass;
-  }
-  __device__ __forceinline__ int passes() const {
-    return kPass >= kPageTokens ? 1 : (ch.count + kPass - 1) / kPass;
-  }
-  uint64_t x[ROWS][4];
-  float amax;
-
-  // The largest finite value of the item that begin() has under way.
-  __device__ __forceinline__ void measure() {
-    amax = 0.f;
-#pragma unroll 1
-    for (int ps = 0; ps < passes(); ++ps) {
+    for (int ps = 0; ps < passes; ++ps) {
       if (ps > 0) load(ps);
       values(ps, x);
       // Infinite and NaN values take no part in the scale: an infinity
       // saturates and a NaN stays one, and the rest of the page keeps its
       // precision.  (Rows and lanes past the end hold zeros; the maximum
       // passes over NaN by itself.)
-      float most = 0.f;
+      float top = 0.f;
 #pragma unroll
       for (int i = 0; i < ROWS; ++i) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           float u, v;
           ptx::f2_unpack(x[i][j], u, v);
-          most = ptx::max3(most, fabsf(u), fabsf(v));
+          top = ptx::max3(top, fabsf(u), fabsf(v));
         }
       }
-      if (__builtin_expect(!(most <= 3.402823466e38f), 0)) {
-        most = 0.f;
+      if (__builtin_expect(!(top <= 3.402823466e38f), 0)) {
+        top = 0.f;
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             float u, v;
             ptx::f2_unpack(x[i][j], u, v);
-            if (fabsf(u) <= 3.402823466e38f) most = fmaxf(most, fabsf(u));
-            if (fabsf(v) <= 3.402823466e38f) most = fmaxf(most, fabsf(v));
+            if (fabsf(u) <= 3.402823466e38f) top = fmaxf(top, fabsf(u));
+            if (fabsf(v) <= 3.402823466e38f) top = fmaxf(top, fabsf(v));
           }
         }
       }
-      amax = fmaxf(amax, most);
+      amax = fmaxf(amax, top);
     }
-  }
-
-  __device__ __forceinline__ void round(uint8_t* codes_, float* scale_, float old_,
-                                        uint32_t* s_amax) {
-    // (Floats >= 0 order as their bits do.)
-    uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
+    uint8_t* const codes_ = codes;
+    float* const scale_ = scale;
+    const float old_ = old;
+    if (passes == 1 && next >= 0) begin(next);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     if constexpr (TEAM > 1) {
       // (Two rows in turn: those of the last item may still be being read.)
-      uint32_t* row = s_amax + turn_no * TEAM;
+      float* row = s_amax + turn_no * TEAM;
       turn_no ^= 1;
-      if (lane == 0) row[team_warp] = top;
+      if (lane == 0) row[team_warp] = amax;
       __syncthreads();  // (and every warp has read the old scale)
 #pragma unroll
-      for (int i = 0; i < TEAM; i += 4) {
-        const uint4 v = *reinterpret_cast<const uint4*>(row + i);
-        top = max(max(top, max(v.x, v.y)), max(v.z, v.w));
-      }
+      for (int i = 0; i < TEAM; ++i) amax = fmaxf(amax, row[i]);
     }
-    const int e = scale_exponent(top);
-    float s = power_of_two(e), inv = power_of_two(-e);
-    if (old_ > s) {
-      s = old_;
-      inv = 1.f / old_;
-    }
+    const float s = fmaxf(scale_for(amax), old_);
+    const float inv = 1.f / s;
     const uint64_t inv2 = ptx::f2_pack(inv, inv);
     __syncwarp();
     if (lane == 0 && team_warp == 0) *scale_ = s;
 #pragma unroll 1
-    for (int ps = 0; ps < passes(); ++ps) {
-      if (!held()) {
+    for (int ps = 0; ps < passes; ++ps) {
+      if (passes > 1) {
         load(ps);
         values(ps, x);
       }
@@ -314,13 +280,14 @@ struct AppendItem {
       const float f = old_ * inv;
       const int words = ch.slot * a.dim / 4;
       uint32_t* c = reinterpret_cast<uint32_t*>(codes_);
-#pragma unroll 1
+#pragma unroll 4
       for (int i = team_warp * 32 + lane; i < words; i += TEAM * 32) {
         const uint32_t u = c[i];
         const float2 lo = f16x2_floats(unpack_e4m3x2(u)), hi = f16x2_floats(unpack_e4m3x2(u >> 16));
         c[i] = pack_e4m3x2(lo.x * f, lo.y * f) | pack_e4m3x2(hi.x * f, hi.y * f) << 16;
       }
     }
+    if (passes > 1 && next >= 0) begin(next);
   }
 };
 
@@ -352,42 +319,47 @@ __device__ __forceinline__ bool append_chunk(const KvAppendArgs& a, int x, Appen
 
 // Few tokens of each sequence: a block takes a chunk, its warps the 2 * heads
 // items of it, one warp an item.
-template <int LANES, bool INTERLEAVED>
+template <int LANES>
 __global__ void __launch_bounds__(512, 2) kv_append_step_kernel(const KvAppendArgs a) {
   AppendChunk ch;
   if (!append_chunk(a, blockIdx.x, &ch)) return;
-  AppendItem<LANES, 1, 1, INTERLEAVED> it(
-      a, ch, 0, a.rope.table + (long long)ch.pos0 * a.rope.rot_dim);
-  it.run(threadIdx.x >> 5, 2 * a.heads, blockDim.x >> 5, nullptr, [] {});
+  AppendItem<LANES, 1, 1> it(a, ch, 0, a.rope.table + (long long)ch.pos0 * a.rope.rot_dim);
+  const int items = 2 * a.heads, warps = blockDim.x >> 5;
+  int i = threadIdx.x >> 5;
+  if (i >= items) return;
+  it.begin(i);
+  for (; i < items; i += warps) it.finish(i + warps < items ? i + warps : -1, nullptr);
 }
 
 // Many tokens: a block of LANES / 2 warps (4 rows of each lane group fill a
 // page) takes `a.per_block` items of a chunk in turn, with the next one's rows
 // under way.  The positions' table rows (32 KB of 64 positions of 128 dims)
 // come into shared memory for all of them, under the first values.
-template <int LANES, bool INTERLEAVED>
+template <int LANES>
 __global__ void __launch_bounds__(16 * LANES, 48 / LANES)
     kv_append_prompt_kernel(const KvAppendArgs a) {
   constexpr int kTeam = LANES / 2;
   extern __shared__ __align__(16) float s_table[];
-  __shared__ __align__(16) uint32_t s_amax[2 * kTeam];
+  __shared__ float s_amax[2 * kTeam];
   AppendChunk ch;
   if (!append_chunk(a, blockIdx.x, &ch)) return;
   const float4* rows =
       reinterpret_cast<const float4*>(a.rope.table + (long long)ch.pos0 * a.rope.rot_dim);
-#pragma unroll 1
   for (int k = threadIdx.x; k < ch.count * a.rope.rot_dim / 4; k += blockDim.x)
     ptx::cp_async_16(ptx::smem_u32(s_table) + k * 16, rows + k);
-  AppendItem<LANES, 4, kTeam, INTERLEAVED> it(a, ch, threadIdx.x >> 5, s_table);
-  const int first = blockIdx.y * a.per_block;
+  AppendItem<LANES, 4, kTeam> it(a, ch, threadIdx.x >> 5, s_table);
+  int i = blockIdx.y * a.per_block;
+  const int end = imin(i + a.per_block, 2 * a.heads);
+  it.begin(i);
   bool have_table = false;
-  it.run(first, imin(first + a.per_block, 2 * a.heads), 1, s_amax, [&] {
-    if (!have_table) {
+  for (; i < end; ++i) {
+    if (it.is_k && !have_table) {
       asm volatile("cp.async.wait_all;" ::: "memory");
       __syncthreads();
       have_table = true;
     }
-  });
+    it.finish(i + 1 < end ? i + 1 : -1, s_amax);
+  }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 

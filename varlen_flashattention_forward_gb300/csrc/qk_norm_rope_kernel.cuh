@@ -78,10 +78,7 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const QkNormRopeArgs 
       // (A warp can hold rows of q and of k: every lane goes through the
       // shuffles, a side without a weight is scaled by 1.)
       if (any_weight) norm_row<LANES>(x, w, a.inv_dim, a.eps, wp != nullptr);
-      if (turn) {
-        if (a.rope.interleaved) rotate_row<true>(x, t);
-        else rotate_row<false>(x, t);
-      }
+      if (turn) rotate_row(x, a.rope, t);
       if (live && i < rows) {
         float f[8];
 #pragma unroll

@@ -133,9 +133,8 @@ __device__ __forceinline__ void norm_row(uint64_t* x, const uint64_t* w, float i
 }
 
 // Rotates the lane's pairs of dims in place.
-template <bool INTERLEAVED>
-__device__ __forceinline__ void rotate_row(uint64_t* x, const RopeRow& t) {
-  if constexpr (INTERLEAVED) {
+__device__ __forceinline__ void rotate_row(uint64_t* x, const RopeParams& r, const RopeRow& t) {
+  if (r.interleaved) {
     float c[4], s[4];
     ptx::f2_unpack(t.c[0], c[0], c[1]);
     ptx::f2_unpack(t.c[1], c[2], c[3]);
