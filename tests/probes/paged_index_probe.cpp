@@ -33,7 +33,7 @@ void probe_key_range(int i0, int i1, int n, int len, int held, int causal, int w
 extern "C" int probe_walk(const int* cu, const int* lens, int batch, int total_q, int heads_k,
                           int group, int rows, int causal, int window, int held, int ctas, int most,
                           int* out) {
-  fa::AttnShape s = {heads_k, group, rows, causal, window, held, fa::inverse_of(group)};
+  fa::AttnShape s = {heads_k, group, rows, causal, window, held};
   auto seq_of = [&](int b, fa::RowRange* q, int* len) {
     *q = fa::row_range(cu[b], cu[b + 1], total_q);
     *len = lens[b];
@@ -70,9 +70,4 @@ extern "C" int probe_walk(const int* cu, const int* lens, int batch, int total_q
     }
   }
   return found;
-}
-
-extern "C" int probe_token_of(unsigned row, int group) {
-  fa::AttnShape s = {1, group, 16, 0, -1, 64, fa::inverse_of(group)};
-  return fa::token_of(s, row);
 }

@@ -344,14 +344,3 @@ def test_segments_cover_every_tile_once(probe):
         for c in range(ctas):
             mine = [s for s in segs if s[0] == c]
             assert all(s[5] == s[7] & 65535 for s in mine[1:-1])
-
-
-def test_rows_divide_exactly(probe):
-    rng = random.Random(3)
-    for group in [1, 2, 3, 4, 5, 7, 8, 16, 40, 127, 128, 1000, 65535, INT_MAX]:
-        rows = [0, 1, group - 1, group, group + 1, INT_MAX, INT_MAX - 1] + [
-            rng.randrange(0, 2 ** 31) for _ in range(200)] + [
-            k * group + d for k in (1, 2, 1000, 2 ** 31 // group - 1) for d in (-1, 0, 1)]
-        for row in rows:
-            if 0 <= row <= INT_MAX:
-                assert probe.probe_token_of(row, group) == row // group, (row, group)

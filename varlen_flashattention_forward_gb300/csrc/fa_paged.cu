@@ -375,7 +375,7 @@ extern "C" fa_status fa_paged_attn(const void* q, long long q_row_stride, long l
   a.max_pages = max_pages_per_seq;
   a.num_pages = num_pages;
   a.shape = {num_heads_k, group, l.rows, causal != 0, window_left,
-             max_pages_per_seq * fa::kPageTokens, fa::inverse_of(group)};
+             max_pages_per_seq * fa::kPageTokens};
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;

@@ -70,9 +70,9 @@ namespace fa {
 // 15 planner.
 constexpr int kPagedThreads = 512;
 constexpr int kConvertWarp = 8, kSWarp = 12, kPvWarp = 13, kLoadWarp = 14;
-// Register split (launch: 128 x 512 = 65536): softmax 256 x 160, converters
-// 128 x 80, control 128 x 96 = 63488.
-constexpr uint32_t kPagedSoftmaxRegs = 160;
+// Register split (launch: 128 x 512 = 65536): softmax 256 x 168, converters
+// 128 x 80, control 128 x 96 = 65536.
+constexpr uint32_t kPagedSoftmaxRegs = 168;
 constexpr uint32_t kPagedConvertRegs = 80;
 constexpr uint32_t kPagedControlRegs = 96;
 // Sequences of one launch (their costs are held in shared memory).

@@ -113,21 +113,8 @@ constexpr int kUnitCost = 4;  // in tiles
 struct AttnShape {
   int heads_k, group, rows;  // kv heads, query heads of one, rows of a tile
   int causal, window, held;  // held: positions of the page table
-  unsigned group_inverse;    // floor(2^32 / group), 2^32 - 1 for 1
 };
-inline unsigned inverse_of(int group) {
-  return group > 1 ? (unsigned)((1ull << 32) / (unsigned)group) : 0xffffffffu;
-}
-// row / group: the product with the inverse is the quotient or one less.
-FA_HD int token_of(const AttnShape& s, unsigned row) {
-#if defined(__CUDA_ARCH__)
-  unsigned q = __umulhi(row, s.group_inverse);
-#else
-  unsigned q = (unsigned)(((unsigned long long)row * s.group_inverse) >> 32);
-#endif
-  if (row - q * s.group >= (unsigned)s.group) ++q;
-  return (int)q;
-}
+FA_HD int token_of(const AttnShape& s, unsigned row) { return (int)(row / (unsigned)s.group); }
 
 // n * group is at most the number of query rows of the call, below 2^31.
 FA_HD int row_tiles(const AttnShape& s, int n) {
@@ -222,13 +209,8 @@ FA_HD bool walk_next(SegmentWalk* w, const AttnShape& s, const Before& before, c
       const int in_seq = w->at - before(w->seq);
       // (The sequence's cost without the cap, so that no head is past the last.)
       const int per_head = capped_cost(head_cost(s, g->q.n, g->len));
-      int left = in_seq;
-      w->head = 0;
-      FA_ROLLED
-      while (left >= per_head) {
-        left -= per_head;
-        ++w->head;
-      }
+      w->head = (int)((unsigned)in_seq / (unsigned)per_head);
+      int left = in_seq - w->head * per_head;
       w->row_tile = 0;
       FA_ROLLED
       for (;;) {
