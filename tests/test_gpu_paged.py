@@ -830,3 +830,19 @@ def test_append_by_either_kernel(cuda_device, d):
     # Both kernels (few tokens a sequence, many) on the same positions.
     check_append([100] + [0] * 30, [20] + [5] * 30, 2, d, 16 * (d // 16), True, seed=66 + d)
     check_append([100, 30], [20, 5], 2, d, 16 * (d // 16), True, seed=67 + d)
+
+
+def test_gather_outputs_aligned_to_16_bytes_only(cuda_device):
+    gen = torch.Generator().manual_seed(68)
+    pages, num = plain.make_pages([100], gen)
+    (kc, ks), (vc, vs) = (plain.make_cache([100], pages, num, 2, 64, gen) for _ in range(2))
+    buf = torch.zeros((2, 100 * 2 * 64 + 8), dtype=torch.bfloat16, device="cuda")
+    outs = [b[8:].view(100, 2, 64) for b in buf]
+    assert outs[0].data_ptr() % 32 == 16
+    k, v = fa.fa_paged_kv_gather(*dev(kc, vc, ks, vs, plain.cum([100]), pages), 100, k_out=outs[0],
+                                 v_out=outs[1])
+    assert (buf[:, :8] == 0).all()
+    for got, codes, scale in ((k, kc, ks), (v, vc, vs)):
+        for h in range(2):
+            want, _ = plain.keys_of(0, 100, pages, codes, scale, h)
+            assert torch.equal(got[:, h].cpu().double(), want)

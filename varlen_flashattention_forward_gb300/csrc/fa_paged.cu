@@ -304,9 +304,14 @@ extern "C" fa_status fa_paged_kv_gather(const void* k_cache, const void* v_cache
   a.num_pages = num_pages;
   a.k = static_cast<uint16_t*>(k_out);
   a.v = static_cast<uint16_t*>(v_out);
+  a.wide_stores = is_aligned(k_out, 32) && is_aligned(v_out, 32);
   const long long pages =
       std::min<long long>(total_k, total_k / fa::kPageTokens + (long long)batch);
-  fa::kv_gather_kernel<<<dim3((unsigned)pages, 2), 256, 0,
+  // Blocks of 128 threads where there are enough of them for every SM, else of
+  // 256 (2 x 32768 tokens: 64.4 against 66.4 us; 21 contexts of 1 to 1300
+  // tokens, 500 blocks: 8.3 against 7.9 us).
+  const int threads = 2 * pages >= 8ll * dev.sm_count ? 128 : 256;
+  fa::kv_gather_kernel<<<dim3((unsigned)pages, 2), threads, 0,
                          reinterpret_cast<cudaStream_t>(stream)>>>(a);
   return launched();
 }

@@ -108,7 +108,7 @@ FA_HD KeyRange key_range(int i0, int i1, int n, int len, int held, bool causal, 
 // are cut into equal contiguous ranges, one for each CTA.  A unit's first
 // kUnitCost places hold no tile, so a cut among them leaves it whole.
 constexpr int kTileKeys = 128;
-constexpr int kUnitCost = 4;  // in tiles
+constexpr int kUnitCost = 7;  // in tiles
 
 struct AttnShape {
   int heads_k, group, rows;  // kv heads, query heads of one, rows of a tile
