@@ -23,7 +23,8 @@ namespace {
 
 // Launch shape of fa_paged_attn.  Rows of a tile: the smallest of 16, 32 and
 // 64 that holds a sequence's rows (the max_seqlen_q hint, else the mean, times
-// the heads of a group), so that its keys are read once.
+// the heads of a group), so that its keys are read once.  (4 rows a sequence, 32
+// of 32768 keys, 8 heads of 128 dims: tiles of 16 rows 319 us, 32: 364, 64: 765.)
 struct AttnLaunch {
   int grid, rows, dim;  // CTAs, rows of a tile, padded head dim
   size_t o_bytes, lse_bytes, meta_bytes;
@@ -94,11 +95,19 @@ cudaError_t launch_attn(const CUtensorMap& k_map, const CUtensorMap& v_map,
 
 bool cache_dim(int d) { return d == 64 || d == 80 || d == 96 || d == 128; }
 
-// Threads (one a 16-byte piece of a row) an SM should have before
-// fa_qk_norm_rope takes eight heads together.
+// fa_qk_norm_rope takes kNormRopeRows heads of a token together where an SM has
+// kNormRopeWide threads' work (8 dims of a row each), else one.  64 tokens x 40
+// heads of 128 dims: one 2.25 us, four 2.83; 8192 tokens: 49.2 against 30.1;
+// 4099 tokens x 28 heads of 96 dims: 24.7 against 14.6.
 constexpr int kNormRopeWide = 8192;
 constexpr int kNormRopeRows = 4;
-constexpr int kNormRopeBlocks = 4;  // resident blocks of an SM
+// Blocks of it that an SM gets; they take their units in turn.
+constexpr int kNormRopeBlocks = 4;
+
+// Blocks of 256 threads of the prompt append for an SM (three are resident):
+// 4 x 2048 tokens x 8 heads of 128 dims 3: 20.5, 4 and 6: 16.7, 8: 18.0,
+// 14 (a head each): 21.9 us.
+constexpr int kAppendWave = 4;
 
 fa_status launched() { return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH; }
 
@@ -177,8 +186,8 @@ extern "C" fa_status fa_qk_norm_rope(const void* q, long long q_row_stride,
   a.positions = rot_dim > 0 ? positions : nullptr;
   a.max_pos = max_pos;
   const int lanes = head_dim <= 64 ? 8 : head_dim <= 128 ? 16 : 32;
-  // Four heads of a token together, so that table and weights are loaded
-  // once for them; one at a time where that would leave SMs idle.
+  // Heads of a token together load its table row and the weights once; one at
+  // a time where that would leave SMs idle.
   const long long all = (long long)num_tokens * (num_heads + num_heads_k);
   const int rows = all * lanes >= (long long)kNormRopeWide * dev.sm_count ? kNormRopeRows : 1;
   a.groups_q = (num_heads + rows - 1) / rows;
@@ -260,13 +269,15 @@ extern "C" fa_status fa_paged_kv_append(
     if (head_dim <= 64) fa::kv_append_step_kernel<8><<<(unsigned)chunks, threads, 0, s>>>(a);
     else fa::kv_append_step_kernel<16><<<(unsigned)chunks, threads, 0, s>>>(a);
   } else {
-    // Blocks of 256 threads, 128 at 64 dims; as few items each as leave all
-    // of them resident at once, three (six) an SM.
+    // Blocks of 256 threads, or of 128 at 64 dims; heads each for about
+    // kAppendWave blocks an SM.
     const int threads = head_dim <= 64 ? 128 : 256;
-    const long long slots = 768ll / threads * dev.sm_count;
-    const long long blocks = std::max<long long>(1, std::min<long long>(items, slots / chunks));
-    a.per_block = (int)((items + blocks - 1) / blocks);
-    const dim3 grid((unsigned)chunks, (items + a.per_block - 1) / a.per_block);
+    const long long slots = kAppendWave * 256ll / threads * dev.sm_count;
+    const long long blocks =
+        std::max<long long>(1, std::min<long long>(num_heads_k, slots / (2 * chunks)));
+    a.per_block = (int)((num_heads_k + blocks - 1) / blocks);
+    a.key_blocks = (num_heads_k + a.per_block - 1) / a.per_block;
+    const dim3 grid((unsigned)chunks, 2 * a.key_blocks);
     const size_t table = (size_t)fa::kPageTokens * rot_dim * sizeof(float);
     if (head_dim <= 64) fa::kv_append_prompt_kernel<8><<<grid, threads, table, s>>>(a);
     else fa::kv_append_prompt_kernel<16><<<grid, threads, table, s>>>(a);

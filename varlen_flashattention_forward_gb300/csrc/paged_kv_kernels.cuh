@@ -113,7 +113,7 @@ struct KvAppendArgs {
   const float* k_weight;  // or null
   float inv_dim, eps;
   RopeParams rope;
-  int per_block;  // items of a block (prompt kernel)
+  int per_block, key_blocks;  // heads of a block, blocks for keys (prompt kernel)
 };
 
 struct AppendChunk {
@@ -121,15 +121,16 @@ struct AppendChunk {
   int row0, pos0;         // row and position of the first
 };
 
-// One item: the new tokens of one page and head, keys or values, taken by a
-// team of TEAM warps (TEAM = 1 or the block).  Rows go ROWS at a time to each
-// LANES-lane group; an item of at most TEAM * ROWS * (32 / LANES) rows is held
-// in registers between the maximum and the rounding, a longer one is loaded
-// again for the second pass.
-template <int LANES, int ROWS, int TEAM>
+// One item: the new tokens of one page and head, keys (KEYS) or values, taken
+// by a team of TEAM warps (TEAM = 1 or the block).  Rows go ROWS at a time to
+// each LANES-lane group; an item of at most TEAM * ROWS * (32 / LANES) rows is
+// held in registers between the maximum and the rounding, a longer one is
+// loaded again for the second pass.
+template <int LANES, int ROWS, int TEAM, bool KEYS>
 struct AppendItem {
   static constexpr int kGroups = 32 / LANES;           // rows of a warp at once
   static constexpr int kPass = TEAM * ROWS * kGroups;  // rows of the team's pass
+  static constexpr bool kOnePass = kPass >= kPageTokens;
   const KvAppendArgs& a;
   const AppendChunk ch;
   const float* table;  // row of the chunk's first position
@@ -137,13 +138,12 @@ struct AppendItem {
   RowPieces p;
   uint64_t w[4];
   // The current item.
-  bool is_k;
   const uint16_t* src;
-  long long stride;
   uint8_t* codes;
   float* scale;
   float old;
   RowBits raw[ROWS];
+  uint64_t x[ROWS][4];
   int turn_no = 0;
 
   __device__ __forceinline__ AppendItem(const KvAppendArgs& a_, const AppendChunk& c, int tw,
@@ -151,59 +151,59 @@ struct AppendItem {
       : a(a_), ch(c), table(table_), team_warp(tw) {
     lane = threadIdx.x & 31;
     sub = lane % LANES;
-    p = row_pieces(a.rope, sub, a.dim);
-    if (a.k_weight && p.a >= 0) load_weights(a.k_weight, p, w);
+    if constexpr (KEYS) {
+      p = row_pieces(a.rope, sub, a.dim);
+      if (a.k_weight && p.a >= 0) load_weights(a.k_weight, p, w);
+    } else {
+      p.a = sub * 8 < a.dim ? sub * 8 : -1;
+      p.b = sub * 8 + 4;
+    }
   }
+  __device__ __forceinline__ bool whole() const { return !KEYS || whole_pieces(a.rope); }
   __device__ __forceinline__ int row_of(int pass, int i) const {
     return pass * kPass + (i * TEAM + team_warp) * kGroups + lane / LANES;
   }
   __device__ __forceinline__ void load(int pass) {
-    const uint16_t* row = src + (long long)(ch.row0 + row_of(pass, 0)) * stride + p.a;
+    const long long stride = KEYS ? a.k_row : a.v_row;
+    const uint16_t* row = src + (long long)(ch.row0 + row_of(pass, 0)) * stride;
     const long long step = (long long)(TEAM * kGroups) * stride;
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
       raw[i].a = raw[i].b = make_uint2(0u, 0u);
-      if (row_of(pass, i) < ch.count && p.a >= 0) {
-        raw[i].a = __ldg(reinterpret_cast<const uint2*>(row));
-        raw[i].b = __ldg(reinterpret_cast<const uint2*>(row + (p.b - p.a)));
-      }
+      if (row_of(pass, i) < ch.count && p.a >= 0) raw[i] = load_row(row, p, whole());
       row += step;
     }
   }
-  // Item number `item` of the chunk (head item / 2, values if even): its first
-  // loads under way.
-  __device__ __forceinline__ void begin(int item) {
-    const int head = item >> 1;
-    is_k = (item & 1) != 0;
-    src = is_k ? a.k + head * a.k_head : a.v + head * a.v_head;
-    stride = is_k ? a.k_row : a.v_row;
+  // Head `head` of the chunk: its first loads under way.
+  __device__ __forceinline__ void begin(int head) {
+    src = KEYS ? a.k + head * a.k_head : a.v + head * a.v_head;
     const size_t cell = (size_t)ch.page * a.heads + head;
-    codes = (is_k ? a.k_cache : a.v_cache) + cell * kPageTokens * a.dim;
-    scale = (is_k ? a.k_scale : a.v_scale) + cell;
+    codes = (KEYS ? a.k_cache : a.v_cache) + cell * kPageTokens * a.dim;
+    scale = (KEYS ? a.k_scale : a.v_scale) + cell;
     old = ch.slot > 0 ? *scale : 0.f;
     load(0);
   }
-  __device__ __forceinline__ void values(int pass, uint64_t (*x)[4]) {
-    const bool turn = is_k && p.turns;
+  __device__ __forceinline__ void values(int pass) {
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
       unpack_row(raw[i], x[i]);
-      if (is_k && a.k_weight) norm_row<LANES>(x[i], w, a.inv_dim, a.eps);
-      const int r = row_of(pass, i);
-      if (turn && r < ch.count)
-        rotate_row(x[i], a.rope, load_rope(a.rope, table + r * a.rope.rot_dim, sub));
+      if constexpr (KEYS) {
+        if (a.k_weight) norm_row<LANES>(x[i], w, a.inv_dim, a.eps);
+        const int r = row_of(pass, i);
+        if (p.turns && r < ch.count)
+          rotate_row(x[i], a.rope, load_rope(a.rope, table + r * a.rope.rot_dim, sub));
+      }
     }
   }
-  // The item that begin() has under way; `next` (an item, or -1) is under way
+  // The item that begin() has under way; `next` (a head, or -1) is under way
   // when it returns.
   __device__ __forceinline__ void finish(int next, float* s_amax) {
-    uint64_t x[ROWS][4];
     float amax = 0.f;
-    const int passes = kPass >= kPageTokens ? 1 : (ch.count + kPass - 1) / kPass;
+    const int passes = kOnePass ? 1 : (ch.count + kPass - 1) / kPass;
 #pragma unroll 1
     for (int ps = 0; ps < passes; ++ps) {
       if (ps > 0) load(ps);
-      values(ps, x);
+      values(ps);
       // Infinite and NaN values take no part in the scale: an infinity
       // saturates and a NaN stays one, and the rest of the page keeps its
       // precision.  (Rows and lanes past the end hold zeros; the maximum
@@ -257,7 +257,7 @@ struct AppendItem {
     for (int ps = 0; ps < passes; ++ps) {
       if (passes > 1) {
         load(ps);
-        values(ps, x);
+        values(ps);
       }
       uint8_t* at = codes_ + (ch.slot + row_of(ps, 0)) * a.dim;
 #pragma unroll
@@ -268,10 +268,14 @@ struct AppendItem {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             ptx::f2_unpack(ptx::mul2(x[i][j], inv2), f[2 * j], f[2 * j + 1]);
-          *reinterpret_cast<uint32_t*>(row + p.a) =
-              pack_e4m3x2(f[0], f[1]) | pack_e4m3x2(f[2], f[3]) << 16;
-          *reinterpret_cast<uint32_t*>(row + p.b) =
-              pack_e4m3x2(f[4], f[5]) | pack_e4m3x2(f[6], f[7]) << 16;
+          const uint32_t lo = pack_e4m3x2(f[0], f[1]) | pack_e4m3x2(f[2], f[3]) << 16;
+          const uint32_t hi = pack_e4m3x2(f[4], f[5]) | pack_e4m3x2(f[6], f[7]) << 16;
+          if (whole()) {
+            *reinterpret_cast<uint2*>(row + p.a) = make_uint2(lo, hi);
+          } else {
+            *reinterpret_cast<uint32_t*>(row + p.a) = lo;
+            *reinterpret_cast<uint32_t*>(row + p.b) = hi;
+          }
         }
       }
     }
@@ -280,7 +284,7 @@ struct AppendItem {
       const float f = old_ * inv;
       const int words = ch.slot * a.dim / 4;
       uint32_t* c = reinterpret_cast<uint32_t*>(codes_);
-#pragma unroll 4
+#pragma unroll 1
       for (int i = team_warp * 32 + lane; i < words; i += TEAM * 32) {
         const uint32_t u = c[i];
         const float2 lo = f16x2_floats(unpack_e4m3x2(u)), hi = f16x2_floats(unpack_e4m3x2(u >> 16));
@@ -288,6 +292,11 @@ struct AppendItem {
       }
     }
     if (passes > 1 && next >= 0) begin(next);
+  }
+  // Heads first, first + step, ... below `end`.
+  __device__ __forceinline__ void run(int first, int end, int step, float* s_amax) {
+#pragma unroll 1
+    for (int h = first; h < end; h += step) finish(h + step < end ? h + step : -1, s_amax);
   }
 };
 
@@ -317,24 +326,31 @@ __device__ __forceinline__ bool append_chunk(const KvAppendArgs& a, int x, Appen
   return c->page >= 0;
 }
 
-// Few tokens of each sequence: a block takes a chunk, its warps the 2 * heads
-// items of it, one warp an item.
+// Few tokens of each sequence: a block takes a chunk, its even warps the heads
+// of K and its odd warps those of V, one warp an item.
 template <int LANES>
 __global__ void __launch_bounds__(512, 2) kv_append_step_kernel(const KvAppendArgs a) {
   AppendChunk ch;
   if (!append_chunk(a, blockIdx.x, &ch)) return;
-  AppendItem<LANES, 1, 1> it(a, ch, 0, a.rope.table + (long long)ch.pos0 * a.rope.rot_dim);
-  const int items = 2 * a.heads, warps = blockDim.x >> 5;
-  int i = threadIdx.x >> 5;
-  if (i >= items) return;
-  it.begin(i);
-  for (; i < items; i += warps) it.finish(i + warps < items ? i + warps : -1, nullptr);
+  const int warp = threadIdx.x >> 5, head = warp >> 1, step = blockDim.x >> 6;
+  if (head >= a.heads) return;
+  if (warp & 1) {
+    AppendItem<LANES, 1, 1, false> it(a, ch, 0, nullptr);
+    it.begin(head);
+    it.run(head, a.heads, step, nullptr);
+  } else {
+    AppendItem<LANES, 1, 1, true> it(a, ch, 0,
+                                     a.rope.table + (long long)ch.pos0 * a.rope.rot_dim);
+    it.begin(head);
+    it.run(head, a.heads, step, nullptr);
+  }
 }
 
 // Many tokens: a block of LANES / 2 warps (4 rows of each lane group fill a
-// page) takes `a.per_block` items of a chunk in turn, with the next one's rows
-// under way.  The positions' table rows (32 KB of 64 positions of 128 dims)
-// come into shared memory for all of them, under the first values.
+// page) takes `a.per_block` heads of a chunk in turn, keys (the first
+// a.key_blocks in y) or values, with the next head's rows under way.  The
+// positions' table rows (32 KB of 64 positions of 128 dims) come into shared
+// memory for all its heads.
 template <int LANES>
 __global__ void __launch_bounds__(16 * LANES, 48 / LANES)
     kv_append_prompt_kernel(const KvAppendArgs a) {
@@ -343,24 +359,25 @@ __global__ void __launch_bounds__(16 * LANES, 48 / LANES)
   __shared__ float s_amax[2 * kTeam];
   AppendChunk ch;
   if (!append_chunk(a, blockIdx.x, &ch)) return;
-  const float4* rows =
-      reinterpret_cast<const float4*>(a.rope.table + (long long)ch.pos0 * a.rope.rot_dim);
-  for (int k = threadIdx.x; k < ch.count * a.rope.rot_dim / 4; k += blockDim.x)
-    ptx::cp_async_16(ptx::smem_u32(s_table) + k * 16, rows + k);
-  AppendItem<LANES, 4, kTeam> it(a, ch, threadIdx.x >> 5, s_table);
-  int i = blockIdx.y * a.per_block;
-  const int end = imin(i + a.per_block, 2 * a.heads);
-  it.begin(i);
-  bool have_table = false;
-  for (; i < end; ++i) {
-    if (it.is_k && !have_table) {
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      __syncthreads();
-      have_table = true;
-    }
-    it.finish(i + 1 < end ? i + 1 : -1, s_amax);
+  const bool keys = blockIdx.y < (unsigned)a.key_blocks;
+  const int first = (keys ? blockIdx.y : blockIdx.y - a.key_blocks) * a.per_block;
+  const int end = imin(first + a.per_block, a.heads);
+  if (keys) {
+    const float4* rows =
+        reinterpret_cast<const float4*>(a.rope.table + (long long)ch.pos0 * a.rope.rot_dim);
+#pragma unroll 1
+    for (int k = threadIdx.x; k < ch.count * a.rope.rot_dim / 4; k += blockDim.x)
+      ptx::cp_async_16(ptx::smem_u32(s_table) + k * 16, rows + k);
+    AppendItem<LANES, 4, kTeam, true> it(a, ch, threadIdx.x >> 5, s_table);
+    it.begin(first);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    it.run(first, end, 1, s_amax);
+  } else {
+    AppendItem<LANES, 4, kTeam, false> it(a, ch, threadIdx.x >> 5, nullptr);
+    it.begin(first);
+    it.run(first, end, 1, s_amax);
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ gather

@@ -8,8 +8,9 @@
 // pieces of 4 (8-byte loads) so chosen that both dims of a pair are in one
 // lane: with the half split, lanes below rot_dim / 8 hold dims [4 l, 4 l + 4)
 // and the ones rot_dim / 2 further on.  Rotating then takes no shuffles, and a
-// lane needs 4 angles of the table row, not 8.  (With 16-byte pieces and
-// shuffles, 8192 tokens x 40 heads of 128 dims took 51 us, 33 without.)
+// lane needs 4 angles of the table row, not 8.  (At 8192
+// tokens x 40 heads of 128 dims, 16-byte pieces and shuffles took 51 us where
+// this took 33.)
 //
 // Everything is fp32 from the load on; the caller rounds the result once, so
 // that norm and rotation add no rounding of their own to the bf16 or e4m3
