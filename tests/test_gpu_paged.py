@@ -832,6 +832,16 @@ def test_append_by_either_kernel(cuda_device, d):
     check_append([100, 30], [20, 5], 2, d, 16 * (d // 16), True, seed=67 + d)
 
 
+@pytest.mark.parametrize("d,Hk", [(64, 3), (96, 1), (128, 9)])
+def test_append_of_prompts_and_single_tokens(cuda_device, d, Hk):
+    # Single tokens of many sequences with longer pieces among them, on both
+    # sides of the 16 tokens that one warp takes, behind part-filled pages.
+    check_append([1] * 30 + [150, 16, 17, 1, 0, 64], [37 * i % 130 for i in range(36)], Hk, d,
+                 16 * (d // 32), True, seed=70 + d, interleaved=d == 96)
+    # Many tokens: blocks that take several heads, an odd one left over.
+    check_append([1900, 640], [0, 33], Hk, d, 16 * (d // 32), True, seed=71 + d)
+
+
 def test_gather_outputs_aligned_to_16_bytes_only(cuda_device):
     gen = torch.Generator().manual_seed(68)
     pages, num = plain.make_pages([100], gen)

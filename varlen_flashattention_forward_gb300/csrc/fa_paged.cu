@@ -263,11 +263,10 @@ extern "C" fa_status fa_paged_kv_append(
       std::min<long long>(total_new, total_new / fa::kPageTokens + 2ll * batch);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool step = (long long)total_new < 16ll * batch;
-  const int items = 2 * num_heads_k;
   if (step) {
-    const int threads = 32 * std::min(items, 16);
-    if (head_dim <= 64) fa::kv_append_step_kernel<8><<<(unsigned)chunks, threads, 0, s>>>(a);
-    else fa::kv_append_step_kernel<16><<<(unsigned)chunks, threads, 0, s>>>(a);
+    const unsigned grid = (unsigned)chunks;
+    if (head_dim <= 64) fa::kv_append_step_kernel<8><<<grid, fa::kStepThreads, 0, s>>>(a);
+    else fa::kv_append_step_kernel<16><<<grid, fa::kStepThreads, 0, s>>>(a);
   } else {
     // Blocks of 256 threads, or of 128 at 64 dims; heads each for about
     // kAppendWave blocks an SM.

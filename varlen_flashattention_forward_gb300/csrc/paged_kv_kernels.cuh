@@ -13,6 +13,7 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include "named_bar.cuh"
 #include "paged_index.h"
 #include "rope_row.cuh"
 #include "sm103_ptx.cuh"
@@ -174,6 +175,8 @@ struct AppendItem {
       row += step;
     }
   }
+  // (Keys and values of one block can be two teams of it.)
+  __device__ __forceinline__ void team_sync() const { named_bar_sync(KEYS ? 1 : 2, TEAM * 32); }
   // Head `head` of the chunk: its first loads under way.
   __device__ __forceinline__ void begin(int head) {
     src = KEYS ? a.k + head * a.k_head : a.v + head * a.v_head;
@@ -244,7 +247,7 @@ struct AppendItem {
       float* row = s_amax + turn_no * TEAM;
       turn_no ^= 1;
       if (lane == 0) row[team_warp] = amax;
-      __syncthreads();  // (and every warp has read the old scale)
+      team_sync();  // (and every warp has read the old scale)
 #pragma unroll
       for (int i = 0; i < TEAM; ++i) amax = fmaxf(amax, row[i]);
     }
@@ -327,20 +330,41 @@ __device__ __forceinline__ bool append_chunk(const KvAppendArgs& a, int x, Appen
 }
 
 // Few tokens of each sequence: a block takes a chunk, its even warps the heads
-// of K and its odd warps those of V, one warp an item.
+// of K and its odd warps those of V, one warp an item.  A chunk of more than
+// kStepAlone tokens among them has the whole block as a team, head by head (255
+// sequences with one token and one with 2048, 8 heads of 128 dims: 23.0 us, one
+// warp an item 45.2; 64 sequences of 15 tokens: team 17.6, one warp 12.3).
+// What bounds it is latency, 4.9 us for 256 tokens: launch, search for the block's
+// sequence, its page, rows, maximum, codes, each waiting for the one before.
+constexpr int kStepThreads = 512;
+constexpr int kStepAlone = 16;
 template <int LANES>
-__global__ void __launch_bounds__(512, 2) kv_append_step_kernel(const KvAppendArgs a) {
+__global__ void __launch_bounds__(kStepThreads, 2) kv_append_step_kernel(const KvAppendArgs a) {
+  constexpr int kTeam = kStepThreads / 32;
   AppendChunk ch;
   if (!append_chunk(a, blockIdx.x, &ch)) return;
-  const int warp = threadIdx.x >> 5, head = warp >> 1, step = blockDim.x >> 6;
+  const int warp = threadIdx.x >> 5;
+  const float* table = a.rope.table + (long long)ch.pos0 * a.rope.rot_dim;
+  if (ch.count > kStepAlone) {
+    __shared__ float s_amax[2][2 * kTeam];
+    {
+      AppendItem<LANES, 2, kTeam, true> it(a, ch, warp, table);
+      it.begin(0);
+      it.run(0, a.heads, 1, s_amax[0]);
+    }
+    AppendItem<LANES, 2, kTeam, false> it(a, ch, warp, nullptr);
+    it.begin(0);
+    it.run(0, a.heads, 1, s_amax[1]);
+    return;
+  }
+  const int head = warp >> 1, step = kTeam / 2;
   if (head >= a.heads) return;
   if (warp & 1) {
     AppendItem<LANES, 1, 1, false> it(a, ch, 0, nullptr);
     it.begin(head);
     it.run(head, a.heads, step, nullptr);
   } else {
-    AppendItem<LANES, 1, 1, true> it(a, ch, 0,
-                                     a.rope.table + (long long)ch.pos0 * a.rope.rot_dim);
+    AppendItem<LANES, 1, 1, true> it(a, ch, 0, table);
     it.begin(head);
     it.run(head, a.heads, step, nullptr);
   }
@@ -351,6 +375,10 @@ __global__ void __launch_bounds__(512, 2) kv_append_step_kernel(const KvAppendAr
 // a.key_blocks in y) or values, with the next head's rows under way.  The
 // positions' table rows (32 KB of 64 positions of 128 dims) come into shared
 // memory for all its heads.
+// 4 x 2048 tokens x 8 heads of 128 dims take 16.7 us, 3.1 TB/s: one wave of
+// blocks, of which the launch, the search and the first loads are about half
+// and the issue of the norm's, rotation's and packing's instructions the rest.
+// (One wave of blocks with keys and values in turn and no loads ahead: 19.4.)
 template <int LANES>
 __global__ void __launch_bounds__(16 * LANES, 48 / LANES)
     kv_append_prompt_kernel(const KvAppendArgs a) {
