@@ -98,7 +98,7 @@ bool cache_dim(int d) { return d == 64 || d == 80 || d == 96 || d == 128; }
 // fa_qk_norm_rope takes kNormRopeRows heads of a token together where an SM has
 // kNormRopeWide threads' work (8 dims of a row each), else one.  64 tokens x 40
 // heads of 128 dims: one 2.25 us, four 2.83; 8192 tokens: 49.2 against 30.1;
-// 4099 tokens x 28 heads of 96 dims: 24.7 against 14.6.
+// 5003 tokens x 32 heads of 96 dims: 24.7 against 14.6.
 constexpr int kNormRopeWide = 8192;
 constexpr int kNormRopeRows = 4;
 // Blocks of it that an SM gets; they take their units in turn.

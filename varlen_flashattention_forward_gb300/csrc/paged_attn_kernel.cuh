@@ -51,6 +51,17 @@
 //
 // TMEM: St at [0, 4N) (two buffers of 2N columns), Ot at [4N, 8N) (of two
 // segments and two warpgroups).
+//
+// Bound by HBM where sequences are long: 32 of 32768 keys, 32 query and 8 kv
+// heads of 128 dims, take 319 us, 6.4 TB/s.  What a unit costs besides its
+// bytes (rows of Q, first maximum, output: some 3-4 us of a CTA, part of it
+// under the next unit's first tiles) shows in shorter ones: 64 of 100 to 8192
+// keys, 32 and 4 heads, 63 us, 4.3 TB/s.  With 32 rows a tile the softmax's own
+// latency does: 24 sequences with 2 to 7 rows against windows of 4096 keys, 32
+// and 8 heads of 64 dims, 51 us, 1.6 TB/s.  A single sequence of 8192 keys, 32
+// and 8 heads of 128 dims, takes 17 us: about 8 until the first tile's score,
+// most of them the planner's chain of loads and the first fetch of the kernel's
+// instructions, and 4 for the merge.
 #pragma once
 
 #include <cstddef>
