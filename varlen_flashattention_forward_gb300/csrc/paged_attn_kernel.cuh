@@ -49,8 +49,8 @@
 // and on odd tiles.  Each has its own running maximum, sums and Ot, and they
 // are joined at the end of a segment like the parts of a split unit.
 //
-// TMEM: St at [0, 4N) (two buffers of 2N columns), Ot at [4N, 8N) (of two
-// segments and two warpgroups).
+// TMEM: St in four buffers of 2N columns (two at 64 rows), Ot behind them (of
+// two segments and two warpgroups).
 //
 // Bound by HBM where sequences are long: 32 of 32768 keys, 32 query and 8 kv
 // heads of 128 dims, take 319 us, 6.4 TB/s.  What a unit costs besides its
@@ -150,13 +150,16 @@ struct PagedCfg {
   static constexpr int kPRow = N * 2;
   static constexpr int kPBytes = kTileKeys * kPRow;
   static constexpr int kQBytes = 2 * N * kRow;
-  static constexpr int NK = N == 64 ? 3 : 4;
-  static constexpr int NV = N == 64 ? 2 : 3;
+  static constexpr int NK = D == 64 ? 6 : N == 64 ? 3 : 4;
+  static constexpr int NV = D == 64 ? 6 : N == 64 ? 2 : 3;
+  static constexpr int NS = N == 64 ? 2 : 4;           // St buffers (even and odd tiles)
   static constexpr int NQ = N == 16 ? 4 : 2;
   static constexpr uint32_t kSwP = N == 64   ? ptx::kLayoutSw128
                                    : N == 32 ? ptx::kLayoutSw64
                                              : ptx::kLayoutSw32;
-  static constexpr uint32_t kTmemCols = 8 * N;
+  static constexpr uint32_t kOt = 2 * N * NS;          // TMEM column of Ot
+  static constexpr uint32_t kTmemCols = N == 16 ? 256 : 512;
+  static_assert(kOt + 4 * N <= kTmemCols, "tensor memory");
   // Offsets from a 1024-byte boundary.
   static constexpr int kK = 0;
   static constexpr int kV = kK + NK * kTileBytes;
@@ -170,10 +173,10 @@ template <int N>
 struct alignas(16) PagedCtl {
   uint64_t plan_full[kPagedPlans], plan_free[kPagedPlans];  // batch published / read (15)
   uint64_t scale_full[kPagedPlans];                         // its scales too
-  uint64_t k_full[4], k_free[4];    // K slot landed (TMA bytes) / read by its S MMA
-  uint64_t v_full[4], v_free[4];    // V slot landed / converted (128 arrivals)
+  uint64_t k_full[6], k_free[6];    // K slot landed (TMA bytes) / read by its S MMA
+  uint64_t v_full[6], v_free[6];    // V slot landed / converted (128 arrivals)
   uint64_t vh_full[2];              // f16 V written (128)
-  uint64_t s_full[2], s_free[2];    // St computed / loaded (128)
+  uint64_t s_full[4], s_free[4];    // St computed / loaded (128)
   uint64_t p_full[2], pv_done[2];   // Pt written (128) / PV complete
   uint64_t q_full[4], q_free[4];    // Q terms written (32) / last S of the segment
   uint64_t qs_full[kPagedPlans];    // row scales written (32)
@@ -274,18 +277,21 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       init(cb->plan_full[s], 1);
       init(cb->plan_free[s], kPlanReaders);
       init(cb->scale_full[s], 1);
-      init(cb->k_full[s], 1);
-      init(cb->k_free[s], 1);
-      init(cb->v_full[s], 1);
-      init(cb->v_free[s], 128);
+      init(cb->s_full[s], 1);
+      init(cb->s_free[s], 128);
       init(cb->q_full[s], 32);
       init(cb->q_free[s], 1);
       init(cb->qs_full[s], 32);
     }
+#pragma unroll 1
+    for (int s = 0; s < 6; ++s) {
+      init(cb->k_full[s], 1);
+      init(cb->k_free[s], 1);
+      init(cb->v_full[s], 1);
+      init(cb->v_free[s], 128);
+    }
     for (int s = 0; s < 2; ++s) {
       init(cb->vh_full[s], 128);
-      init(cb->s_full[s], 1);
-      init(cb->s_free[s], 128);
       init(cb->p_full[s], 128);
       init(cb->pv_done[s], 1);
       init(cb->o_free[s], 8);
@@ -461,13 +467,14 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
 #pragma unroll 1
         for (int n = 0; n < count; ++n, ++i) {
           ok = wait(cb->k_full[slot], k_phase);
-          if (ok && i >= 2) ok = wait(cb->s_free[i & 1], ((i >> 1) - 1) & 1);
+          const int sb = i % C::NS;
+          if (ok && i >= C::NS) ok = wait(cb->s_free[sb], (i / C::NS - 1) & 1);
           if (!ok) break;
           ptx::tc_fence_after();
           const uint64_t kd = ptx::smem_desc(
               ptx::smem_u32(smem + C::kK + slot * C::kTileBytes), 16, 8 * C::kRow, C::kSwK);
-          ptx::mma_f8_elect<D / 32>(tmem + (i & 1) * 2 * N, kd, qd, idesc);
-          ptx::mma_commit_elect(ptx::smem_u32(&cb->s_full[i & 1]));
+          ptx::mma_f8_elect<D / 32>(tmem + sb * 2 * N, kd, qd, idesc);
+          ptx::mma_commit_elect(ptx::smem_u32(&cb->s_full[sb]));
           ptx::mma_commit_elect(ptx::smem_u32(&cb->k_free[slot]));
           if (++slot == C::NK) {
             slot = 0;
@@ -506,7 +513,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
                                              kTileKeys * 128, 1024, ptx::kLayoutSw128);
           const uint64_t bd = ptx::smem_desc(ptx::smem_u32(smem + C::kP + hb * C::kPBytes),
                                              8 * C::kPRow, 8 * C::kPRow, C::kSwP);
-          const uint32_t d = tmem + 4 * N + (seg & 1) * 2 * N + hb * N;
+          const uint32_t d = tmem + C::kOt + (seg & 1) * 2 * N + hb * N;
           ptx::mma_ss4_elect<16 * 128 / 16, 16 * C::kPRow / 16>(d, ad, bd, idesc,
                                                                 in_seg > 1 ? 1u : 0u);
           ptx::mma_ss4_elect<16 * 128 / 16, 16 * C::kPRow / 16>(
@@ -622,6 +629,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
           row_h = g.head * sh.group + row - tok * sh.group;
         };
         float ks = 0.f, vs = 0.f;
+        auto publish = [&]() {
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->plan_full[slot]));
+        };
         if (b >= 0) {
           if (b >= kPagedPlans) ok = wait(cb->plan_free[slot], (b / kPagedPlans - 1) & 1);
           if (!ok) break;
@@ -669,37 +680,32 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             ks = __ldg(a.k_scale + cell);
             vs = __ldg(a.v_scale + cell);
           }
+          if (b > 0) publish();
+        }
+        const int held = cell >= 0;
+        // On to the next batch.
+        n0 += kPlanTiles;
+        if (ends) {
+          n0 = 0;
+          more = walk_next(&walk, sh, before, seq_of, &g);
+        }
+        last = g.count - n0 <= kPlanTiles;
+        cell = more ? cells() : -1;
+        if (b >= 0) {
           // The first batch is not published before its scales and rows of Q
-          // are here: behind the first K and V tiles of all SMs (17 MB) they
-          // would take some 3 us.
+          // are here, and the next one's pages asked for: behind the first K
+          // and V tiles of all SMs (17 MB) they would take some 3 us.
           if (b == 0) {
 #pragma unroll
             for (int j = 0; j < kBatch; ++j)
               asm volatile("" ::"r"(raw[j].x), "f"(ks), "f"(vs) : "memory");
+            publish();
           }
+          // Its scales and Q.
+          plan.page[lane] = PagePlan{ks, vs, fmaxf(log2f(vs), -(float)kScaleExpMax), held};
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->plan_full[slot]));
-        }
-        const int held = cell >= 0;
-        // Then the next batch's pages and this one's scales and Q, in this
-        // order but for the first, whose Q is waited for.
-#pragma unroll 1
-        for (int step = 0; step < 2; ++step) {
-          if ((step == 0) == (b != 0)) {
-            // ---- on to the next batch
-            n0 += kPlanTiles;
-            if (ends) {
-              n0 = 0;
-              more = walk_next(&walk, sh, before, seq_of, &g);
-            }
-            last = g.count - n0 <= kPlanTiles;
-            cell = more ? cells() : -1;
-          } else if (b >= 0) {
-            // ---- scales and Q
-            plan.page[lane] = PagePlan{ks, vs, fmaxf(log2f(vs), -(float)kScaleExpMax), held};
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->scale_full[slot]));
-            if (!first) continue;
+          if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->scale_full[slot]));
+          if (first) {
             const int qb = seg % C::NQ;
             if (seg >= C::NQ) ok = wait(cb->q_free[qb], (seg / C::NQ - 1) & 1);
             if (!ok) break;
@@ -772,9 +778,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             ptx::mbar_arrive(ptx::smem_u32(&cb->qs_full[seg % kPagedPlans]));
             ptx::mbar_arrive(ptx::smem_u32(&cb->q_full[qb]));
           }
+          if (ends) ++seg;
         }
-        if (!ok) break;
-        if (b >= 0 && ends) ++seg;
       }
     }
   } else {
@@ -787,7 +792,6 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     const int page = key >> 6;
     const int bar = 1 + 4 * wg;           // named barriers bar .. bar + 2; 4: both warpgroups
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_tmem = tmem + lane_base + wg * 2 * N;
     float (*red)[N] = cb->red[wg];
     float* alpha = cb->alpha[wg];
     uint8_t* prow = smem + C::kP + wg * C::kPBytes + key * C::kPRow;
@@ -875,7 +879,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       // 64-row one, which uses the first 16 lanes of each warp's 32.
       const int d = D == 128 ? key : (warp & 3) * 16 + lane;
       const bool live = d < a.dim && (D == 128 || lane < 16);
-      const uint32_t o0 = tmem + lane_base + 4 * N + (done.seg & 1) * 2 * N;
+      const uint32_t o0 = tmem + lane_base + C::kOt + (done.seg & 1) * 2 * N;
       // Rows: eight at a time by each warpgroup in turn, or all by the one
       // that is alone, whose Ot is then the only one.
 #pragma unroll 1
@@ -935,7 +939,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       // to the next.
       const bool alone = plan.tiles == 1;
       const bool skip = count == 0 || (alone && first != 0);
-      const uint32_t o_tmem = tmem + lane_base + 4 * N + (seg & 1) * 2 * N + wg * N;
+      const uint32_t o_tmem = tmem + lane_base + C::kOt + (seg & 1) * 2 * N + wg * N;
       const float* c = cb->qs[seg % kPagedPlans];
       float* end_m = cb->end_m[seg % kPagedPlans][wg];
       if (plan.first && !skip) {
@@ -983,7 +987,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
                (sh.window >= 0 && (long long)j0 < at0 + (tok1 - tok0) - sh.window));
           // (A warp whose wait has given up still joins the votes below,
           // after which the whole warpgroup leaves.)
-          if (ok) ok = wait(cb->s_full[wg], phase);
+          const int sb = at % C::NS;
+          const uint32_t s_tmem = tmem + lane_base + sb * 2 * N;
+          if (ok) ok = wait(cb->s_full[sb], (at / C::NS) & 1);
           // Pt's buffer was last read by the PV of this warpgroup's last tile.
           if (ok && at >= 2) ok = wait(cb->pv_done[wg], phase ^ 1);
           ptx::tc_fence_after();
@@ -1050,7 +1056,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
           }
           settled = false;
           ptx::tc_fence_before();
-          ptx::mbar_arrive(ptx::smem_u32(&cb->s_free[wg]));
+          ptx::mbar_arrive(ptx::smem_u32(&cb->s_free[sb]));
           // Pt row of this key.
           const uint64_t vs2 = ptx::f2_pack(pp.vs, pp.vs);
 #pragma unroll
