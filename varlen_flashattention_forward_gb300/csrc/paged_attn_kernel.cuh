@@ -58,7 +58,7 @@
 // under the next unit's first tiles) shows in shorter ones: 64 of 100 to 8192
 // keys, 32 and 4 heads, 63 us, 4.3 TB/s.  With 32 rows a tile the softmax's own
 // latency does: 24 sequences with 2 to 7 rows against windows of 4096 keys, 32
-// and 8 heads of 64 dims, 51 us, 1.6 TB/s.  A single sequence of 8192 keys, 32
+// and 8 heads of 64 dims, 49 us, 1.7 TB/s.  A single sequence of 8192 keys, 32
 // and 8 heads of 128 dims, takes 17 us: about 8 until the first tile's score,
 // most of them the planner's chain of loads and the first fetch of the kernel's
 // instructions, and 4 for the merge.
@@ -150,9 +150,14 @@ struct PagedCfg {
   static constexpr int kPRow = N * 2;
   static constexpr int kPBytes = kTileKeys * kPRow;
   static constexpr int kQBytes = 2 * N * kRow;
+  // K and V slots: at 128 dims what fits, at 64 dims (8 KB slots) as many as
+  // gain anything (24 sequences with 2 to 7 rows, windows of 4096: 4 and 3
+  // slots 51.2 us, 6 of each 49.8, 8 the same).
   static constexpr int NK = D == 64 ? 6 : N == 64 ? 3 : 4;
   static constexpr int NV = D == 64 ? 6 : N == 64 ? 2 : 3;
-  static constexpr int NS = N == 64 ? 2 : 4;           // St buffers (even and odd tiles)
+  // St buffers, as many as TMEM holds; with two the same case takes 49.0 us,
+  // with four 48.6 (by then).
+  static constexpr int NS = N == 64 ? 2 : 4;
   static constexpr int NQ = N == 16 ? 4 : 2;
   static constexpr uint32_t kSwP = N == 64   ? ptx::kLayoutSw128
                                    : N == 32 ? ptx::kLayoutSw64

@@ -108,9 +108,9 @@ FA_HD KeyRange key_range(int i0, int i1, int n, int len, int held, bool causal, 
 // are cut into equal contiguous ranges, one for each CTA.  A unit's first
 // kUnitCost places hold no tile, so a cut among them leaves it whole.
 constexpr int kTileKeys = 128;
-// In tiles.  Measured with 2, 4, 6, 8: 64 sequences of 100 to 8192 keys, 4 kv
-// heads of 128 dims 70.0, 64.2, 63.5, 63.1 us; 24 sequences with 2 to 7 rows,
-// windows of 4096, 8 kv heads of 64 dims 56.7, 54.4, 51.1, 52.1.
+// In tiles.  Measured with 5, 6, 7, 8, 9: 64 sequences of 100 to 8192 keys, 4 kv
+// heads of 128 dims 65.0, 62.7, 62.6, 62.4, 63.3 us; 24 sequences with 2 to 7
+// rows, windows of 4096, 8 kv heads of 64 dims 49.7, 48.9, 48.6, 49.1, 50.3.
 constexpr int kUnitCost = 7;
 
 struct AttnShape {
