@@ -856,3 +856,40 @@ def test_gather_outputs_aligned_to_16_bytes_only(cuda_device):
         for h in range(2):
             want, _ = plain.keys_of(0, 100, pages, codes, scale, h)
             assert torch.equal(got[:, h].cpu().double(), want)
+
+
+@pytest.mark.parametrize("d,H,causal", [(64, 128, True), (128, 96, False)])
+def test_attn_groups_wider_than_a_row_tile(cuda_device, d, H, causal):
+    # One kv head for all: the heads of a token fill more than one tile.
+    check_attn([1, 3, 0, 2], [130, 400, 64, 1], H, 1, d, causal=causal, seed=H)
+
+
+def test_cache_past_32_bit_offsets(cuda_device):
+    # The pages at the end of caches of 4.6 GB give what the first ones give.
+    gen = torch.Generator().manual_seed(72)
+    Hk, d, many = 8, 128, 70001
+    counts, lens = [100, 1], [150, 129]
+    pages = torch.tensor([[3, 1, 0], [2, 5, 4]], dtype=torch.int32)
+    kv = torch.randn((101, 2 * Hk, d), generator=gen).bfloat16().cuda()
+    q = torch.randn((2, 32, d), generator=gen).bfloat16().cuda()
+    tab = dev(plain.table(192, d))
+    first = torch.randint(0, 256, (2, 6, Hk, 64, d), generator=gen, dtype=torch.uint8)
+    first[(first & 127) == 127] = 0                              # no NaN
+    got = []
+    for num, ids in ((6, pages), (many, many - 1 - pages)):
+        rows = ids.flatten().long().cuda()
+        kc, vc = (torch.empty((num, Hk, 64, d), dtype=torch.uint8, device="cuda") for _ in "kv")
+        for c, x in ((kc, first[0]), (vc, first[1])):
+            c[rows] = x[pages.flatten().long()].cuda()
+        ks, vs = (torch.full((num, Hk), 2.0 ** -5, device="cuda") for _ in "kv")
+        cache = (kc.view(torch.float8_e4m3fn), vc.view(torch.float8_e4m3fn), ks, vs)
+        lend, idd = dev(torch.tensor(lens, dtype=torch.int32), ids)
+        fa.fa_paged_kv_append(kv[:, :Hk], kv[:, Hk:], dev(plain.cum(counts)), lend, idd, *cache,
+                              cos_sin=tab)
+        o, lse = fa.fa_paged_attn(q, *cache, dev(plain.cum([1, 1])), lend, idd, return_lse=True)
+        k, v = fa.fa_paged_kv_gather(*cache, dev(plain.cum(lens)), idd, sum(lens))
+        got.append([t.cpu() for t in (kc[rows], vc[rows], ks[rows], vs[rows], o, lse, k, v)])
+    assert fa.fa_get_device_status() == fa.FA_OK
+    assert torch.isfinite(got[0][4]).all()
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
