@@ -893,3 +893,9 @@ def test_cache_past_32_bit_offsets(cuda_device):
     assert torch.isfinite(got[0][4]).all()
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+def test_more_sequences_than_a_block_has_threads(cuda_device):
+    check_append([1] * 1100, [i % 130 for i in range(1100)], 1, 64, 0, False, seed=73)
+    check_append([17] * 300, [i % 130 for i in range(300)], 1, 128, 0, False, seed=74)
+    test_gather_is_exact(cuda_device, 64, 1, [i % 3 for i in range(700)])
