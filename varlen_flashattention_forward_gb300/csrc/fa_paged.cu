@@ -21,10 +21,14 @@ using fa::is_valid_view;
 
 namespace {
 
-// Launch shape of fa_paged_attn.  Rows of a tile: the smallest of 16, 32 and
-// 64 that holds a sequence's rows (the max_seqlen_q hint, else the mean, times
-// the heads of a group), so that its keys are read once.  (4 rows a sequence, 32
-// of 32768 keys, 8 heads of 128 dims: tiles of 16 rows 319 us, 32: 364, 64: 765.)
+// Launch shape of fa_paged_attn.  Rows of a tile: 16 where they hold a
+// sequence's rows (the max_seqlen_q hint, else the mean, times the heads of a
+// group), else 32.  (4 rows a sequence, 32 of 32768 keys, 8 heads of 128 dims:
+// 16 rows 319 us, 32: 364.  8 to 28 rows, 24 sequences, windows of 4096 keys, 8
+// heads of 64 dims: 53.6 and 48.7.  Tiles of 64 rows, which read the keys of
+// more rows once, lost to 32 for want of registers and buffers: 52 rows, 24
+// sequences of 2500 to 5000 keys, 8 heads of 128 dims 137 against 114 us, 64 rows
+// and 1 head, 64 sequences of 2000 to 4096 keys 75 against 52.)
 struct AttnLaunch {
   int grid, rows, dim;  // CTAs, rows of a tile, padded head dim
   size_t o_bytes, lse_bytes, meta_bytes;
@@ -36,7 +40,7 @@ AttnLaunch attn_launch(int sm_count, int batch, int total_q, int group, int head
   const long long tokens =
       max_seqlen_q > 0 ? max_seqlen_q : ((long long)total_q + batch - 1) / batch;
   const long long rows = tokens * group;
-  l.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  l.rows = rows <= 16 ? 16 : 32;
   l.dim = head_dim <= 64 ? 64 : 128;
   l.grid = std::min(sm_count, fa::kPagedMaxGrid);
   l.o_bytes = (size_t)2 * l.grid * l.rows * l.dim * sizeof(float);
@@ -401,7 +405,7 @@ extern "C" fa_status fa_paged_attn(const void* q, long long q_row_stride, long l
   a.status = dev.status;
   a.wait_limit_ns = dev.wait_limit_ns;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  // A launch holds the costs of paged_max_batch sequences in shared
+  // A launch holds the costs of kPagedMaxBatch sequences in shared
   // memory and counts them in 32 bits; a larger batch runs as
   // consecutive launches, which share the workspace in stream order.
   const long long per_row_tile =
@@ -410,7 +414,7 @@ extern "C" fa_status fa_paged_attn(const void* q, long long q_row_stride, long l
   const long long row_tiles = (long long)total_q * group / l.rows;
   const long long fit = fa::kMaxCost / per_row_tile - row_tiles;
   if (fit < 1) return FA_ERR_UNSUPPORTED;
-  const int step = (int)std::min<long long>(fa::paged_max_batch(l.rows), fit);
+  const int step = (int)std::min<long long>(fa::kPagedMaxBatch, fit);
   for (int b0 = 0; b0 < batch; b0 += step) {
     a.batch = std::min(batch - b0, step);
     a.cu = cu_seqlens_q + b0;
@@ -418,13 +422,11 @@ extern "C" fa_status fa_paged_attn(const void* q, long long q_row_stride, long l
     a.page_table = page_table + (size_t)b0 * max_pages_per_seq;
     cudaError_t e;
     if (l.dim == 64)
-      e = l.rows == 16   ? launch_attn<64, 16>(k_map, v_map, a, l.grid, s)
-          : l.rows == 32 ? launch_attn<64, 32>(k_map, v_map, a, l.grid, s)
-                         : launch_attn<64, 64>(k_map, v_map, a, l.grid, s);
+      e = l.rows == 16 ? launch_attn<64, 16>(k_map, v_map, a, l.grid, s)
+                       : launch_attn<64, 32>(k_map, v_map, a, l.grid, s);
     else
-      e = l.rows == 16   ? launch_attn<128, 16>(k_map, v_map, a, l.grid, s)
-          : l.rows == 32 ? launch_attn<128, 32>(k_map, v_map, a, l.grid, s)
-                         : launch_attn<128, 64>(k_map, v_map, a, l.grid, s);
+      e = l.rows == 16 ? launch_attn<128, 16>(k_map, v_map, a, l.grid, s)
+                       : launch_attn<128, 32>(k_map, v_map, a, l.grid, s);
     if (e != cudaSuccess) return FA_ERR_LAUNCH;
   }
   return FA_OK;

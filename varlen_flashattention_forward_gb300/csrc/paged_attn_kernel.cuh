@@ -2,7 +2,7 @@
 // paged 8-bit cache, for sm_103a.
 //
 // Rows: the `group` query heads of one kv head times the sequence's query
-// tokens (row = token * group + head), N of them (16, 32 or 64) to a tile.
+// tokens (row = token * group + head), N of them (16 or 32) to a tile.
 // The work is every row tile's 128-key tiles; CTA c takes an equal contiguous
 // range of their costs (paged_index.h), whatever the lengths, and walks it as
 // segments, one per unit it touches.  A segment that covers its unit writes O
@@ -49,8 +49,8 @@
 // and on odd tiles.  Each has its own running maximum, sums and Ot, and they
 // are joined at the end of a segment like the parts of a split unit.
 //
-// TMEM: St in four buffers of 2N columns (two at 64 rows), Ot behind them (of
-// two segments and two warpgroups).
+// TMEM: St in four buffers of 2N columns, Ot behind them (of two segments and
+// two warpgroups).
 //
 // Bound by HBM where sequences are long: 32 of 32768 keys, 32 query and 8 kv
 // heads of 128 dims, take 319 us, 6.4 TB/s.  What a unit costs besides its
@@ -82,12 +82,14 @@ namespace fa {
 constexpr int kPagedThreads = 512;
 constexpr int kConvertWarp = 8, kSWarp = 12, kPvWarp = 13, kLoadWarp = 14;
 // Register split (launch: 128 x 512 = 65536): softmax 256 x 168, converters
-// 128 x 80, control 128 x 96 = 65536.
+// 128 x 80, control 128 x 96 = 65536.  (Softmax 176 and control 80: 62.4
+// instead of 62.9 us at 64 sequences, but 51.0 instead of 48.8 at 32 rows;
+// softmax 176 and converters 64: 335 instead of 316 us at 32 x 32768 keys.)
 constexpr uint32_t kPagedSoftmaxRegs = 168;
 constexpr uint32_t kPagedConvertRegs = 80;
 constexpr uint32_t kPagedControlRegs = 96;
 // Sequences of one launch (their costs are held in shared memory).
-constexpr int paged_max_batch(int rows) { return rows == 64 ? 512 : 1024; }
+constexpr int kPagedMaxBatch = 1024;
 constexpr int kPagedPlans = 4;        // batches in flight
 constexpr int kPlanReaders = 15;      // warps that read them
 constexpr int kPlanTiles = 16;        // tiles of a batch
@@ -153,15 +155,13 @@ struct PagedCfg {
   // K and V slots: at 128 dims what fits, at 64 dims (8 KB slots) as many as
   // gain anything (24 sequences with 2 to 7 rows, windows of 4096: 4 and 3
   // slots 51.2 us, 6 of each 49.8, 8 the same).
-  static constexpr int NK = D == 64 ? 6 : N == 64 ? 3 : 4;
-  static constexpr int NV = D == 64 ? 6 : N == 64 ? 2 : 3;
-  // St buffers, as many as TMEM holds; with two the same case takes 49.0 us,
-  // with four 48.6 (by then).
-  static constexpr int NS = N == 64 ? 2 : 4;
+  static constexpr int NK = D == 64 ? 6 : 4;
+  static constexpr int NV = D == 64 ? 6 : 3;
+  // St buffers, as many as TMEM holds at 32 rows; with two the same case takes
+  // 49.0 us, with four 48.6 (by then).
+  static constexpr int NS = 4;
   static constexpr int NQ = N == 16 ? 4 : 2;
-  static constexpr uint32_t kSwP = N == 64   ? ptx::kLayoutSw128
-                                   : N == 32 ? ptx::kLayoutSw64
-                                             : ptx::kLayoutSw32;
+  static constexpr uint32_t kSwP = N == 32 ? ptx::kLayoutSw64 : ptx::kLayoutSw32;
   static constexpr uint32_t kOt = 2 * N * NS;          // TMEM column of Ot
   static constexpr uint32_t kTmemCols = N == 16 ? 256 : 512;
   static_assert(kOt + 4 * N <= kTmemCols, "tensor memory");
@@ -202,13 +202,12 @@ struct alignas(16) PagedCtl {
   // ahead of the other, which still reads these.)
   float end_m[kPagedPlans][2][N], end_l[kPagedPlans][2][N];
   long long warp_tiles[kPagedThreads / 32];
-  int before[paged_max_batch(N) + 1];
+  int before[kPagedMaxBatch + 1];
 };
 template <int D, int N>
 constexpr size_t paged_smem() {
   return 1024 + PagedCfg<D, N>::kCtl + sizeof(PagedCtl<N>);
 }
-static_assert(paged_smem<128, 64>() <= 232448, "shared memory exceeds the per-CTA limit");
 static_assert(paged_smem<128, 32>() <= 232448, "shared memory exceeds the per-CTA limit");
 
 // Bounded wait of a warp (see wait_warp), in as few instructions as will do:
@@ -627,12 +626,6 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
                   a.q + (long long)tok * a.q_row + (long long)h * a.q_head + dim0));
           }
         };
-        auto place_rows = [&](int n0r) {  // rows n0r + lane: token, head
-          const int row = g.row_tile * N + n0r + lane;
-          const int tok = token_of(sh, row);
-          row_q = g.q.lo + tok;
-          row_h = g.head * sh.group + row - tok * sh.group;
-        };
         float ks = 0.f, vs = 0.f;
         auto publish = [&]() {
           __syncwarp();
@@ -649,13 +642,14 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             break;
           }
           rows = imin(N, g.q.n * sh.group - g.row_tile * N);
-#pragma unroll 1
-          for (int n = N > 32 ? 32 : 0; n >= 0; n -= 32) {
-            place_rows(n);
-            if (n + lane < N) {
-              plan.out[n + lane] = row_q * a.heads + row_h;
-              plan.lse[n + lane] = row_h * a.total_q + row_q;
-              plan.token[n + lane] = row_q - g.q.lo - token_of(sh, g.row_tile * N);
+          {
+            const int row = g.row_tile * N + lane, tok = token_of(sh, row);
+            row_q = g.q.lo + tok;
+            row_h = g.head * sh.group + row - tok * sh.group;
+            if (lane < N) {
+              plan.out[lane] = row_q * a.heads + row_h;
+              plan.lse[lane] = row_h * a.total_q + row_q;
+              plan.token[lane] = tok - token_of(sh, g.row_tile * N);
             }
           }
           if (first) load_rows(0);  // (ahead of the pages' loads in the memory system)
@@ -717,14 +711,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             uint8_t* q_s = smem + C::kQ + qb * C::kQBytes;  // N rows of hi, N of lo
 #pragma unroll 1
             for (int j0 = 0; j0 < N; j0 += kGroups * kBatch) {
-              if (j0 > 0) {
-                // (Row numbers of the second 32 rows replace the first's.)
-                if (N > 32 && j0 == 32) {
-                  row_q = plan.out[32 + lane] / a.heads;
-                  row_h = plan.out[32 + lane] - row_q * a.heads;
-                }
-                load_rows(j0);
-              }
+              if (j0 > 0) load_rows(j0);
 #pragma unroll 1
               for (int j = 0; j < kBatch; ++j) {
                 const int n = j0 + j * kGroups + lane / kLanes;
@@ -842,34 +829,28 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         return false;
       }
       ptx::tc_fence_after();
-      // Lane n: weights of row n's two Ot (lane n - 32 has a second row at 64
-      // rows): 2^(m - M) / sum; a warpgroup that saw no key has m = -inf (or
-      // a NaN sum) and nothing to add.
-      float wa[(N + 31) / 32], wb[(N + 31) / 32];
-#pragma unroll
-      for (int r = 0; r < (N + 31) / 32; ++r) {
-        const int n = lane + 32 * r;
-        wa[r] = wb[r] = 0.f;
-        if (n < N) {
-          const int w0 = alone ? wg : 0;
-          const float m0 = cb->end_m[ring][w0][n], l0 = cb->end_l[ring][w0][n];
-          const float m1 = alone ? neg_inf : cb->end_m[ring][1][n];
-          const float l1 = alone ? 0.f : cb->end_l[ring][1][n];
-          const float top = fmaxf(m0, m1);
-          const float base = top == neg_inf ? 0.f : top;
-          const float e0 = m0 == neg_inf ? (l0 == 0.f ? 0.f : l0) : ptx::ex2(m0 - base);
-          const float e1 = m1 == neg_inf ? (l1 == 0.f ? 0.f : l1) : ptx::ex2(m1 - base);
-          const float sum = e0 * l0 + e1 * l1;
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (a NaN stays one)
-          wa[r] = e0 * inv;
-          wb[r] = e1 * inv;
-          if (n < rows && (warp & 3) == 0 && (alone || wg == 0)) {
-            const float l2 = sum == 0.f ? neg_inf : base + log2f(sum);
-            if (!plan.whole)
-              a.part_lse[(size_t)slot * N + n] = l2;
-            else if (a.lse)
-              a.lse[plan.lse[n]] = l2 * 0.69314718055994531f;
-          }
+      // Lane n: weights of row n's two Ot, 2^(m - M) / sum; a warpgroup that saw
+      // no key has m = -inf (or a NaN sum) and nothing to add.
+      float wa = 0.f, wb = 0.f;
+      if (lane < N) {
+        const int n = lane, w0 = alone ? wg : 0;
+        const float m0 = cb->end_m[ring][w0][n], l0 = cb->end_l[ring][w0][n];
+        const float m1 = alone ? neg_inf : cb->end_m[ring][1][n];
+        const float l1 = alone ? 0.f : cb->end_l[ring][1][n];
+        const float top = fmaxf(m0, m1);
+        const float base = top == neg_inf ? 0.f : top;
+        const float e0 = m0 == neg_inf ? (l0 == 0.f ? 0.f : l0) : ptx::ex2(m0 - base);
+        const float e1 = m1 == neg_inf ? (l1 == 0.f ? 0.f : l1) : ptx::ex2(m1 - base);
+        const float sum = e0 * l0 + e1 * l1;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (a NaN stays one)
+        wa = e0 * inv;
+        wb = e1 * inv;
+        if (n < rows && (warp & 3) == 0 && (alone || wg == 0)) {
+          const float l2 = sum == 0.f ? neg_inf : base + log2f(sum);
+          if (!plan.whole)
+            a.part_lse[(size_t)slot * N + n] = l2;
+          else if (a.lse)
+            a.lse[plan.lse[n]] = l2 * 0.69314718055994531f;
         }
       }
       if (plan.unit_end >= 0 && key == 0 && (alone || wg == 0)) {
@@ -898,8 +879,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int n = n0 + k;
-          const float fa = __shfl_sync(full, N == 64 && n >= 32 ? wa[(N + 31) / 32 - 1] : wa[0], n & 31);
-          const float fb = __shfl_sync(full, N == 64 && n >= 32 ? wb[(N + 31) / 32 - 1] : wb[0], n & 31);
+          const float fa = __shfl_sync(full, wa, n);
+          const float fb = __shfl_sync(full, wb, n);
           if (live && n < rows) {
             // (Weight 0: the Ot may hold anything.)
             const float v = (fa == 0.f ? 0.f : fa * __uint_as_float(oa[k])) +
@@ -999,28 +980,24 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
           if (ok && at >= 2) ok = wait(cb->pv_done[wg], phase ^ 1);
           ptx::tc_fence_after();
           const uint64_t ks2 = ptx::f2_pack(pp.ks, pp.ks);
-          constexpr int kLoad = N < 32 ? N : 32;  // rows loaded at once
+          uint32_t qh[N], ql[N];
 #pragma unroll
-          for (int n0 = 0; n0 < N; n0 += kLoad) {
-            uint32_t qh[kLoad], ql[kLoad];
+          for (int n = 0; n < N; n += 16) {
+            ptx::tmem_ld16(s_tmem + n, qh + n);
+            ptx::tmem_ld16(s_tmem + N + n, ql + n);
+          }
+          ptx::tmem_wait_ld();
 #pragma unroll
-            for (int n = 0; n < kLoad; n += 16) {
-              ptx::tmem_ld16(s_tmem + n0 + n, qh + n);
-              ptx::tmem_ld16(s_tmem + N + n0 + n, ql + n);
-            }
-            ptx::tmem_wait_ld();
+          for (int n = 0; n < N; n += 16) {
+            ptx::reg_fence16(qh + n);
+            ptx::reg_fence16(ql + n);
+          }
 #pragma unroll
-            for (int n = 0; n < kLoad; n += 16) {
-              ptx::reg_fence16(qh + n);
-              ptx::reg_fence16(ql + n);
-            }
-#pragma unroll
-            for (int n = 0; n < kLoad; n += 2) {
-              const ulonglong2 f = factor_of((n0 + n) / 2);
-              const uint64_t h2 = ptx::f2_pack(__uint_as_float(qh[n]), __uint_as_float(qh[n + 1]));
-              const uint64_t l2 = ptx::f2_pack(__uint_as_float(ql[n]), __uint_as_float(ql[n + 1]));
-              x[(n0 + n) / 2] = ptx::fma2(ptx::add2(h2, l2), ptx::mul2(f.x, ks2), f.y);
-            }
+          for (int n = 0; n < N; n += 2) {
+            const ulonglong2 f = factor_of(n / 2);
+            const uint64_t h2 = ptx::f2_pack(__uint_as_float(qh[n]), __uint_as_float(qh[n + 1]));
+            const uint64_t l2 = ptx::f2_pack(__uint_as_float(ql[n]), __uint_as_float(ql[n + 1]));
+            x[n / 2] = ptx::fma2(ptx::add2(h2, l2), ptx::mul2(f.x, ks2), f.y);
           }
           if (edge) {
             // Row n stands at at0 + token[n].
@@ -1077,8 +1054,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
               w[k] = ptx::pack_f16x2(u, v);
             }
             const int un = n0 / 8;
-            const int us = N == 64 ? (un ^ (key & 7))
-                                   : N == 32 ? (un ^ ((key >> 1) & 3)) : (un ^ ((key >> 2) & 1));
+            const int us = N == 32 ? (un ^ ((key >> 1) & 3)) : (un ^ ((key >> 2) & 1));
             *reinterpret_cast<uint4*>(prow + us * 16) = make_uint4(w[0], w[1], w[2], w[3]);
           }
           ptx::fence_proxy_async_smem();
