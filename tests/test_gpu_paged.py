@@ -899,3 +899,58 @@ def test_more_sequences_than_a_block_has_threads(cuda_device):
     check_append([1] * 1100, [i % 130 for i in range(1100)], 1, 64, 0, False, seed=73)
     check_append([17] * 300, [i % 130 for i in range(300)], 1, 128, 0, False, seed=74)
     test_gather_is_exact(cuda_device, 64, 1, [i % 3 for i in range(700)])
+
+
+# ------------------------------------------------------- V scales far apart
+def check_far_scales(scales, tiles, batch, tops=None, hi=1.0, d=64, H=4, seed=80):
+    """`batch` sequences of 128-key tiles whose pages' V scales are scales[t]
+    for tile t (a pair: its two pages), scores 0, or tops[t] (base 2) for all
+    keys of tile t."""
+    gen = torch.Generator().manual_seed(seed)
+    n = 128 * tiles
+    pages, num = plain.make_pages([n] * batch, gen)
+    kc = torch.zeros((num, 1, 64, d), dtype=torch.float8_e4m3fn)
+    vc = (torch.randn((num, 1, 64, d), generator=gen) * hi).to(torch.float8_e4m3fn)
+    ks, vs = torch.ones((num, 1)), torch.zeros((num, 1))
+    q = torch.ones((batch, H, d)).bfloat16()
+    scale = math.log(2) / d
+    for t in range(tiles):
+        pair = scales[t % len(scales)]
+        for i, s in enumerate(pair if isinstance(pair, tuple) else (pair, pair)):
+            vs[pages[:, 2 * t + i].long()] = s
+            if tops:   # score = scale * d * top * ln 2 / ln 2
+                kc.view(torch.uint8)[pages[:, 2 * t + i].long()] = torch.tensor(
+                    tops[t % len(tops)]).to(torch.float8_e4m3fn).view(torch.uint8)
+    o, lse = fa.fa_paged_attn(*dev(q, kc, vc, ks, vs, plain.cum([1] * batch),
+                                   torch.full((batch,), n, dtype=torch.int32), pages),
+                              max_seqlen_q=1, softmax_scale=scale, return_lse=True)
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status() == fa.FA_OK
+    want = plain.attention(q, kc, vc, ks, vs, list(range(batch + 1)), [n] * batch, pages, scale,
+                           True, -1)
+    compare_attn(o.cpu(), lse.cpu(), *want)
+
+
+LO, HI = 2.0 ** -64, 2.0 ** 64
+
+
+@pytest.mark.parametrize("batch,tiles", [(1, 2), (1, 8), (300, 2), (300, 5)])
+@pytest.mark.parametrize("scales", [(LO, HI), (HI, LO), (0.0, HI), (HI, 0.0), ((LO, HI), (HI, LO)),
+                                    (LO, LO, HI, HI), (HI, HI, LO, LO), (LO, 1.0, HI)])
+def test_attn_v_scales_at_both_ends(cuda_device, scales, batch, tiles):
+    """Keys whose V scale is 2^128 below another's (an all-zero page has 2^-64)
+    keep their share of the softmax, whichever tile, warpgroup or CTA they are
+    in.  A key of the small scale adds at most 448 * 2^-25 to an output of at
+    least 2^7 sum |code| of the large one's, far inside the tolerance's 2^-10."""
+    check_far_scales(scales, tiles, batch)
+
+
+@pytest.mark.parametrize("batch,tiles", [(1, 4), (300, 4)])
+@pytest.mark.parametrize("turn", [False, True])
+def test_attn_large_values_under_small_weights(cuda_device, batch, tiles, turn):
+    """Weights of 2^-128 and values of 2^64 beside weights of 1 and values of
+    2^-64: both sides are about half of the output.  (128 is an e4m3 number.)"""
+    scales, tops = (HI, HI, LO, LO), (0.0, 0.0, 128.0, 128.0)
+    if turn:
+        scales, tops = scales[::-1], tops[::-1]
+    check_far_scales(scales, tiles, batch, tops=tops)

@@ -196,7 +196,7 @@ struct alignas(16) PagedCtl {
   // or sums; rescale factors.
   alignas(16) float factor[2][N / 2][4];
   alignas(16) float red[2][4][N];
-  alignas(16) float alpha[2][N];
+  alignas(16) float alpha[2][2 * N];  // of Ot; of the sums, see root_ex2
   // By segment (mod 4) and warpgroup: maximum so far (-inf: no key seen) and,
   // at the segment's end, the sum.  (A warpgroup may be up to three segments
   // ahead of the other, which still reads these.)
@@ -255,6 +255,12 @@ __device__ __forceinline__ float warp_transpose_reduce16(float* x, int lane) {
   const float recv = __shfl_xor_sync(0xffffffffu, x[0], 1);
   return kMax ? fmaxf(x[0], recv) : x[0] + recv;
 }
+
+// The square root of 2^d (d <= 0), to be multiplied by twice: 2^d itself is
+// flushed to zero below 2^-126, and a row sum needs more.  The maximum is one of
+// score + log2(V scale), so under V scales 2^128 apart a sum is up to 2^96 (2^79
+// for each key) where another one that it joins is down to 2^-57.
+__device__ __forceinline__ float root_ex2(float d) { return ptx::ex2(0.5f * d); }
 
 template <int D, int N>
 __global__ void __launch_bounds__(kPagedThreads, 1)
@@ -839,12 +845,13 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         const float l1 = alone ? 0.f : cb->end_l[ring][1][n];
         const float top = fmaxf(m0, m1);
         const float base = top == neg_inf ? 0.f : top;
-        const float e0 = m0 == neg_inf ? (l0 == 0.f ? 0.f : l0) : ptx::ex2(m0 - base);
-        const float e1 = m1 == neg_inf ? (l1 == 0.f ? 0.f : l1) : ptx::ex2(m1 - base);
-        const float sum = e0 * l0 + e1 * l1;
+        const float e0 = m0 == neg_inf ? (l0 == 0.f ? 0.f : l0) : root_ex2(m0 - base);
+        const float e1 = m1 == neg_inf ? (l1 == 0.f ? 0.f : l1) : root_ex2(m1 - base);
+        const float sum = e0 * l0 * e0 + e1 * l1 * e1;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (a NaN stays one)
-        wa = e0 * inv;
-        wb = e1 * inv;
+        // (These may be flushed: Ot goes by the maximum, like P'.)
+        wa = e0 * e0 * inv;
+        wb = e1 * e1 * inv;
         if (n < rows && (warp & 3) == 0 && (alone || wg == 0)) {
           const float l2 = sum == 0.f ? neg_inf : base + log2f(sum);
           if (!plan.whole)
@@ -1086,14 +1093,15 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             const float mu = at == start ? neg_inf : end_m[key];
             float al = 1.f;
             if (mt > mu) {
-              al = mu == neg_inf ? 0.f : ptx::ex2(mu - mt);
+              al = mu == neg_inf ? 0.f : root_ex2(mu - mt);
               cb->factor[wg][key / 2][2 + (key & 1)] = -mt;
               end_m[key] = mt;
             } else if (at == start) {
               end_m[key] = neg_inf;
             }
             none = key < rows && end_m[key] == neg_inf;
-            alpha[key] = al;
+            alpha[key] = al * al;
+            alpha[N + key] = al;
           }
           unset = named_bar_or(bar, 128, none);
           if constexpr (N == 16) {
@@ -1102,7 +1110,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
           }
           if (at != start) {
 #pragma unroll
-            for (int n = 0; n < N; n += 2) l[n / 2] = ptx::mul2(l[n / 2], pair(alpha, n));
+            for (int n = 0; n < N; n += 2) {
+              const uint64_t root = pair(alpha, N + n);
+              l[n / 2] = ptx::mul2(ptx::mul2(l[n / 2], root), root);
+            }
             // Ot holds this warpgroup's earlier tiles, whose last PV is done.
 #pragma unroll
             for (int n0 = 0; n0 < N; n0 += 16) {
@@ -1172,8 +1183,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
 // Joins the parts of the units that CTA boundaries cut.  Block (c, n): row n
 // of the unit that starts in CTA c and ends in a later one.
 // O = sum_p w_p O_p, w_p = 2^(lse_p - LSE): the parts are summed in CTA order,
-// so the result does not depend on timing.  A unit can have as many parts as
-// there are CTAs, so every LSE is loaded at once and 16 partials at a time.
+// so the result does not depend on timing.  (A small weight can meet the larger
+// values, of pages with a larger scale, hence its root.)  A unit can have as many
+// parts as there are CTAs, so every LSE is loaded at once and 16 partials at a
+// time.
 constexpr int kPagedMaxGrid = 512;  // CTAs of an attention launch
 
 template <int D, int N>
@@ -1215,9 +1228,9 @@ __global__ void __launch_bounds__(D) paged_merge_kernel(const PagedAttnArgs a) {
     for (int k = 0; k < kAtOnce; ++k) {
       if (p0 + k < parts) {
         const float lp = s_w[p0 + k];
-        const float w = lp == neg_inf ? 0.f : ptx::ex2(lp - top);
-        sum += w;
-        acc = fmaf(w, v[k], acc);
+        const float w = lp == neg_inf ? 0.f : root_ex2(lp - top);
+        sum = fmaf(w, w, sum);
+        acc = fmaf(w, w * v[k], acc);
       }
     }
   }

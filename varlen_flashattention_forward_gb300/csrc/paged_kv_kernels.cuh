@@ -21,8 +21,9 @@
 namespace fa {
 
 constexpr float kE4m3Max = 448.f;
-// Scales stay within 2^-64 .. 2^64: their products with scores and sums of
-// the attention stay far inside fp32.
+// Scales stay within 2^-64 .. 2^64: the attention's scores, and its sums of
+// weights relative to weight times V scale, then stay inside fp32 (where sums
+// meet, with root_ex2).
 constexpr int kScaleExpMax = 64;
 
 // Smallest power of two s with amax <= 448 s, clamped (amax finite, >= 0).
