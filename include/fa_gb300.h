@@ -11,8 +11,8 @@
  * gathered from a paged 576-wide latent cache.
  *
  * Conventions shared by every entry point
- *   - All tensors are caller-owned device buffers, C-contiguous (except the
- *     q/k/v views fa_varlen_fwd_strided takes), 16-byte aligned.  bf16 means
+ *   - All tensors are caller-owned device buffers, C-contiguous (except where
+ *     an entry point takes row and head strides), 16-byte aligned.  bf16 means
  *     IEEE bfloat16 bit patterns (2 bytes).
  *   - Calls are asynchronous on `stream` (NULL = legacy default stream).  The
  *     library performs no host<->device copy and never synchronises; it only
@@ -179,6 +179,8 @@ fa_status fa_varlen_fwd_plan(int batch, int total_q, int total_k, int num_heads,
  *                 the tensor's last dimension, row stride >= (heads - 1) *
  *                 head stride + last dimension (views do not overlap
  *                 themselves); the innermost dimension is contiguous.
+ *                 The row stride of a single row and the head stride of a
+ *                 single head are not read.
  *   all other arguments and errors as fa_varlen_fwd; a stride that breaks
  *   these rules is FA_ERR_INVALID_ARG.  out and lse stay contiguous.
  *   fa_varlen_fwd is this call with the contiguous strides

@@ -954,3 +954,67 @@ def test_attn_large_values_under_small_weights(cuda_device, batch, tiles, turn):
     if turn:
         scales, tops = scales[::-1], tops[::-1]
     check_far_scales(scales, tiles, batch, tops=tops)
+
+
+# ---------------------------------------------- views with strides of no use
+def turned(x):
+    """x [1, H, d] as the torch-contiguous tensor with the strides (d, d, 1)."""
+    y = torch.empty((x.shape[1], 1, x.shape[2]), dtype=x.dtype, device=x.device).transpose(0, 1)
+    y.copy_(x)
+    assert y.is_contiguous() and y.stride()[:2] == (x.shape[2], x.shape[2])
+    return y
+
+
+@pytest.mark.parametrize("d", [64, 80, 128])
+def test_one_row_turned_round(cuda_device, d):
+    gen = torch.Generator().manual_seed(90 + d)
+    H, Hk = 8, 2
+    q, k, v = dev(*(torch.randn((1, h, d), generator=gen).bfloat16() for h in (H, Hk, Hk)))
+    tab, w, pos = dev(plain.table(200, d), torch.rand(d, generator=gen),
+                      torch.tensor([129], dtype=torch.int32))
+    qo, ko = fa.fa_qk_norm_rope(q, k, pos, tab, w, w)
+    out = [turned(torch.zeros_like(t)) for t in (q, k)]
+    got = fa.fa_qk_norm_rope(turned(q), turned(k), pos, tab, w, w, q_out=out[0], k_out=out[1])
+    assert torch.equal(got[0], qo) and torch.equal(got[1], ko)
+    assert got[0].data_ptr() == out[0].data_ptr()
+    pages, num = plain.make_pages([130], gen)
+    (kc, ks), (vc, vs) = (plain.make_cache([129], pages, num, Hk, d, gen, 0) for _ in range(2))
+    lens, cu = dev(torch.tensor([130], dtype=torch.int32), plain.cum([1]))
+    res = []
+    for kk, vv, qq in ((k, v, qo), (turned(k), turned(v), turned(qo))):
+        c = dev(kc.clone(), vc.clone(), ks.clone(), vs.clone())
+        fa.fa_paged_kv_append(kk, vv, cu, lens, dev(pages), *c, cos_sin=tab)
+        o, lse = fa.fa_paged_attn(qq, *c, cu, lens, dev(pages), return_lse=True)
+        res.append((c[0].view(torch.uint8), c[1].view(torch.uint8), o, lse))
+    for a, b in zip(*res):
+        assert torch.equal(a, b)
+    # Beside a strided tensor fa_varlen_fwd takes its strides too.
+    kv = dev(torch.randn((40, 2 * Hk, d), generator=gen).bfloat16())
+    cuk = dev(plain.cum([40]))
+    a, b = (fa.fa_varlen_fwd(t, kv[:, :Hk], kv[:, Hk:], cu, cuk) for t in (q, turned(q)))
+    assert torch.equal(a, b)
+    q3, cu3 = dev(torch.randn((3, 2 * H, d), generator=gen).bfloat16(), plain.cum([3]))
+    a, b = (fa.fa_varlen_fwd(q3[:, :H], t, u, cu3, cu) for t, u in ((k, v), (turned(k), turned(v))))
+    assert torch.equal(a, b)
+
+
+def test_one_head_with_any_head_stride(cuda_device):
+    gen = torch.Generator().manual_seed(94)
+    T, d = 70, 64
+    buf = dev(torch.randn((T, 3 * d), generator=gen).bfloat16())
+    odd = [buf[:, i * d:(i + 1) * d].as_strided((T, 1, d), (3 * d, 5, 1), i * d) for i in range(3)]
+    plainly = [t.contiguous() for t in odd]
+    tab, pos = dev(plain.table(T, d), torch.arange(T, dtype=torch.int32))
+    pages, num = plain.make_pages([T], gen)
+    lens, cu = dev(torch.tensor([T], dtype=torch.int32), plain.cum([T]))
+    res = []
+    for q, k, v in (odd, plainly):
+        c = [torch.zeros((num, 1, 64, d), dtype=torch.float8_e4m3fn, device="cuda") for _ in "kv"]
+        c += [torch.zeros((num, 1), device="cuda") for _ in "kv"]
+        qn, kn = fa.fa_qk_norm_rope(q, k, pos, tab)
+        fa.fa_paged_kv_append(k, v, cu, lens, dev(pages), *c, cos_sin=tab)
+        o = fa.fa_paged_attn(q, *c, cu, lens, dev(pages))
+        f = fa.fa_varlen_fwd(q, k, v, cu, cu)
+        res.append((qn, kn, c[0].view(torch.uint8), c[1].view(torch.uint8), o, f))
+    for a, b in zip(*res):
+        assert torch.equal(a, b)

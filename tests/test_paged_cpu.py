@@ -344,3 +344,44 @@ def test_segments_cover_every_tile_once(probe):
         for c in range(ctas):
             mine = [s for s in segs if s[0] == c]
             assert all(s[5] == s[7] & 65535 for s in mine[1:-1])
+
+
+# ------------------------------------------------- strides that step nowhere
+def varlen_strided(lib, q=(256, 64), k=(128, 64), v=(128, 64), Tq=5, Tk=5, H=4, Hk=2, d=64):
+    return lib.fa_varlen_fwd_strided(P(0x1000), *q, P(0x2000), *k, P(0x3000), *v, P(0x4000),
+                                     P(0x5000), 1, Tq, Tk, H, Hk, d, d, Tq, Tk, 0.125, 0, -1, -1,
+                                     P(0x6000), None, None)
+
+
+@pytest.mark.parametrize("row,head", [(64, 64), (8, 64), (0, 64), (-3, 64), (77, 72)])
+def test_the_row_stride_of_one_row_is_not_read(lib, row, head):
+    # A contiguous [heads, 1, dim] tensor turned round has the strides (dim,
+    # dim), and they are as good as any.
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    none = (fa.FA_ERR_LAUNCH, fa.FA_ERR_ARCH)
+    assert norm_rope(lib, d=64, rot=64, T=1, qr=row, qh=head, kr=row, kh=head, qor=row, qoh=head,
+                     kor=row, koh=head) in none
+    assert append(lib, T=1, kr=row, kh=head, vr=row, vh=head) in none
+    assert attn(lib, T=1, qr=row, qh=head) in none
+    assert varlen_strided(lib, (row, head), (row, head), (row, head), 1, 1) in none
+    # What is wrong with two rows stays wrong.
+    assert norm_rope(lib, d=64, rot=64, T=2, qr=row, qh=head, kr=256) == INV
+    assert append(lib, T=2, kr=row, kh=head) == INV and attn(lib, T=2, qr=row, qh=head) == INV
+    assert varlen_strided(lib, (row, head)) == INV
+
+
+@pytest.mark.parametrize("head", [1, 0, -64, 63, 2 ** 40])
+def test_the_head_stride_of_one_head_is_not_read(lib, head):
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    none = (fa.FA_ERR_LAUNCH, fa.FA_ERR_ARCH)
+    assert norm_rope(lib, d=64, rot=64, H=1, Hk=1, qr=64, qh=head, kr=72, kh=head, qor=64, qoh=head,
+                     kor=64, koh=head) in none
+    assert append(lib, Hk=1, kr=64, kh=head, vr=64, vh=head) in none
+    assert attn(lib, H=1, Hk=1, qr=64, qh=head) in none
+    assert varlen_strided(lib, (64, head), (64, head), (64, head), H=1, Hk=1) in none
+    assert append(lib, Hk=1, T=1, kr=-1, kh=head, vr=3, vh=head) in none
+    # With two heads it is.
+    assert append(lib, kr=2 ** 37 - 8, kh=head) == INV
+    assert append(lib, Hk=1, kr=56, kh=head) == INV      # rows that overlap

@@ -284,9 +284,10 @@ extern "C" fa_status fa_varlen_fwd_strided(
   else if (d_qk == 128 && d_v == 128) launch = fa::launch_varlen_128_128;
   else if (d_qk == 192 && d_v == 128) launch = fa::launch_varlen_192_128;
   if (!launch) return FA_ERR_UNSUPPORTED;
-  if (!fa::is_valid_view(q_row_stride, q_head_stride, num_heads, d_qk) ||
-      (total_k > 0 && (!fa::is_valid_view(k_row_stride, k_head_stride, num_heads_k, d_qk) ||
-                       !fa::is_valid_view(v_row_stride, v_head_stride, num_heads_k, d_v))))
+  if (!fa::settle_view(total_q, num_heads, d_qk, &q_row_stride, &q_head_stride) ||
+      (total_k > 0 &&
+       (!fa::settle_view(total_k, num_heads_k, d_qk, &k_row_stride, &k_head_stride) ||
+        !fa::settle_view(total_k, num_heads_k, d_v, &v_row_stride, &v_head_stride))))
     return FA_ERR_INVALID_ARG;
   // Token indices are 32-bit in the kernel.
   if ((int64_t)total_q * num_heads > INT32_MAX || (int64_t)total_k * num_heads_k > INT32_MAX)

@@ -17,7 +17,7 @@
 #include "qk_norm_rope_kernel.cuh"
 
 using fa::is_aligned;
-using fa::is_valid_view;
+using fa::settle_view;
 
 namespace {
 
@@ -163,11 +163,12 @@ extern "C" fa_status fa_qk_norm_rope(const void* q, long long q_row_stride,
       !is_aligned(k_weight, 16))
     return FA_ERR_INVALID_ARG;
   if (head_dim % 8 != 0 || head_dim > 256) return FA_ERR_UNSUPPORTED;
-  if ((num_heads > 0 && (!is_valid_view(q_row_stride, q_head_stride, num_heads, head_dim) ||
-                         !is_valid_view(q_out_row_stride, q_out_head_stride, num_heads, head_dim))) ||
+  if ((num_heads > 0 &&
+       (!settle_view(num_tokens, num_heads, head_dim, &q_row_stride, &q_head_stride) ||
+        !settle_view(num_tokens, num_heads, head_dim, &q_out_row_stride, &q_out_head_stride))) ||
       (num_heads_k > 0 &&
-       (!is_valid_view(k_row_stride, k_head_stride, num_heads_k, head_dim) ||
-        !is_valid_view(k_out_row_stride, k_out_head_stride, num_heads_k, head_dim))))
+       (!settle_view(num_tokens, num_heads_k, head_dim, &k_row_stride, &k_head_stride) ||
+        !settle_view(num_tokens, num_heads_k, head_dim, &k_out_row_stride, &k_out_head_stride))))
     return FA_ERR_INVALID_ARG;
   if ((int64_t)num_tokens * ((int64_t)num_heads + num_heads_k) > INT32_MAX)
     return FA_ERR_UNSUPPORTED;
@@ -228,8 +229,9 @@ extern "C" fa_status fa_paged_kv_append(
     return FA_ERR_INVALID_ARG;
   if (!is_aligned(k, 16) || !is_aligned(v, 16) || !is_aligned(k_weight, 16))
     return FA_ERR_INVALID_ARG;
-  if (total_new > 0 && (!is_valid_view(k_row_stride, k_head_stride, num_heads_k, head_dim) ||
-                        !is_valid_view(v_row_stride, v_head_stride, num_heads_k, head_dim)))
+  if (total_new > 0 &&
+      (!settle_view(total_new, num_heads_k, head_dim, &k_row_stride, &k_head_stride) ||
+       !settle_view(total_new, num_heads_k, head_dim, &v_row_stride, &v_head_stride)))
     return FA_ERR_INVALID_ARG;
   fa::DeviceFacts dev;
   st = fa::device_facts(&dev);
@@ -368,7 +370,7 @@ extern "C" fa_status fa_paged_attn(const void* q, long long q_row_stride, long l
   if (!is_aligned(q, 16) || !is_aligned(out, 16) || !is_aligned(lse, 4) ||
       !is_aligned(seq_lens, 4) || !is_aligned(workspace, 16))
     return FA_ERR_INVALID_ARG;
-  if (total_q > 0 && !is_valid_view(q_row_stride, q_head_stride, num_heads, head_dim))
+  if (total_q > 0 && !settle_view(total_q, num_heads, head_dim, &q_row_stride, &q_head_stride))
     return FA_ERR_INVALID_ARG;
   if ((int64_t)total_q * num_heads > INT32_MAX || num_heads > 65535) return FA_ERR_UNSUPPORTED;
   fa::DeviceFacts dev;

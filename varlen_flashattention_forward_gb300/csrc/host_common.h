@@ -31,15 +31,20 @@ inline bool is_aligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }
 
-// A strided [tokens, heads, dim] view of bf16: innermost dimension
-// contiguous, head and token strides multiples of 16 bytes, no element
-// reachable two ways.
-inline bool is_valid_view(long long row_stride, long long head_stride, int heads, int dim) {
-  if (row_stride <= 0 || head_stride <= 0) return false;
-  if (row_stride % 8 != 0 || head_stride % 8 != 0) return false;
-  if (head_stride < dim) return false;
-  if (row_stride < (long long)(heads - 1) * head_stride + dim) return false;
-  return row_stride < (1ll << 37) && head_stride < (1ll << 37);
+// Whether the strides are those of a [rows, heads, dim] view of bf16 (dim a
+// multiple of 8): innermost dimension contiguous, head and row strides multiples
+// of 16 bytes, no element reachable two ways.  A stride that nothing steps by,
+// that of a single head or row, may be anything (a framework leaves what it
+// likes there) and is replaced by an ordinary one.
+inline bool settle_view(int rows, int heads, int dim, long long* row_stride,
+                        long long* head_stride) {
+  constexpr long long kMost = 1ll << 37;  // of a tensor map, in elements
+  if (heads == 1) *head_stride = dim;
+  if (*head_stride < dim || *head_stride % 8 != 0) return false;
+  if (heads > 1 && *head_stride > (kMost - dim) / (heads - 1)) return false;
+  const long long extent = (heads - 1) * *head_stride + dim;
+  if (rows <= 1) *row_stride = extent;
+  return *row_stride >= extent && *row_stride % 8 == 0 && *row_stride < kMost;
 }
 
 }  // namespace fa
