@@ -385,3 +385,20 @@ def test_the_head_stride_of_one_head_is_not_read(lib, head):
     # With two heads it is.
     assert append(lib, kr=2 ** 37 - 8, kh=head) == INV
     assert append(lib, Hk=1, kr=56, kh=head) == INV      # rows that overlap
+
+
+# -------------------------------------------------------------------- build
+def test_the_build_sees_every_file_that_the_sources_include():
+    deps = {os.path.realpath(p) for p in build_ext._deps()}
+    todo, seen = list(build_ext._sources()), set()
+    while todo:
+        path = os.path.realpath(todo.pop())
+        if path in seen:
+            continue
+        seen.add(path)
+        with open(path) as f:
+            for line in f:
+                if line.startswith('#include "'):
+                    todo.append(os.path.join(os.path.dirname(path), line.split('"')[1]))
+    assert any(p.endswith("paged_index.h") for p in seen)
+    assert seen <= deps, sorted(seen - deps)
