@@ -1018,3 +1018,19 @@ def test_one_head_with_any_head_stride(cuda_device):
         res.append((qn, kn, c[0].view(torch.uint8), c[1].view(torch.uint8), o, f))
     for a, b in zip(*res):
         assert torch.equal(a, b)
+
+
+def test_attn_hint_that_changes_in_place(cuda_device):
+    # A hint may be anything with an integer value; one object may hold
+    # another value in the next call, for which another workspace is needed.
+    gen = torch.Generator().manual_seed(95)
+    pages, num = plain.make_pages([200], gen)
+    (kc, ks), (vc, vs) = (plain.make_cache([200], pages, num, 2, 64, gen) for _ in range(2))
+    q = torch.randn((9, 8, 64), generator=gen).bfloat16()
+    cpu = (q, kc, vc, ks, vs, plain.cum([9]), torch.tensor([200], dtype=torch.int32), pages)
+    args, most = dev(*cpu), torch.tensor(1)
+    want = plain.attention(q, kc, vc, ks, vs, [0, 9], [200], pages, 0.125, True, -1)
+    for hint in (1, 9, 1):
+        most.fill_(hint)
+        o, lse = fa.fa_paged_attn(*args, max_seqlen_q=most, max_seqlen_k=most, return_lse=True)
+        compare_attn(o.cpu(), lse.cpu(), *want)

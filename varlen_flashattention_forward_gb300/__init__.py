@@ -571,6 +571,8 @@ def fa_paged_attn(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, seq_lens,
     T, H, dq = q.shape
     if dq != d:
         raise ValueError(f"q has head dim {dq}, the cache {d}")
+    # (Now: the workspace's size is looked up by the values of these sizes.)
+    max_seqlen_q, max_seqlen_k = int(max_seqlen_q), int(max_seqlen_k)
     if softmax_scale is None:
         softmax_scale = d ** -0.5
     index, here = _device(stream, q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, seq_lens,
