@@ -1034,3 +1034,25 @@ def test_attn_hint_that_changes_in_place(cuda_device):
         most.fill_(hint)
         o, lse = fa.fa_paged_attn(*args, max_seqlen_q=most, max_seqlen_k=most, return_lse=True)
         compare_attn(o.cpu(), lse.cpu(), *want)
+
+
+@pytest.mark.parametrize("size", [2 ** 30 - 1, 2 ** 31 - 1])
+def test_windows_past_every_position(cuda_device, size):
+    gen = torch.Generator().manual_seed(96)
+    lens, q_lens = [200, 70], [3, 90]     # the second has rows before its first key
+    pages, num = plain.make_pages(lens, gen)
+    (kc, ks), (vc, vs) = (plain.make_cache(lens, pages, num, 2, 64, gen) for _ in range(2))
+    q = torch.randn((93, 8, 64), generator=gen).bfloat16()
+    args = dev(q, kc, vc, ks, vs, plain.cum(q_lens), torch.tensor(lens, dtype=torch.int32), pages)
+    k, v = dev(*(torch.randn((270, 2, 64), generator=gen).bfloat16() for _ in "kv"))
+    cu, cuk = args[5], dev(plain.cum(lens))
+    for causal in (True, False):
+        a, b = (fa.fa_paged_attn(*args, causal=causal, window_left=w, return_lse=True)
+                for w in (-1, size))
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        assert (a[0] != 0).any(-1).sum() > 500   # (rows of both sequences see keys)
+        for win in ((size, -1), (-1, size), (size, size)):
+            a, b = (fa.fa_varlen_fwd(args[0], k, v, cu, cuk, 90, 200, causal=causal, window_left=l,
+                                     window_right=r, return_lse=True)
+                    for l, r in ((-1, -1), win))
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])

@@ -341,10 +341,12 @@ extern "C" fa_status fa_varlen_fwd_strided(
   args.total_q = total_q;
   args.total_k = total_k;
   args.scale_log2 = softmax_scale * 1.4426950408889634f;
-  args.wl = window_left;
   // Causal is the window's right edge on the bottom-right diagonal
-  // (window_right >= -1, so min(window_right, 0) is 0 whenever causal).
-  args.wr = causal ? 0 : window_right;
+  // (window_right >= -1, so min(window_right, 0) is 0 whenever causal).  A
+  // window past 2^30 is as good as 2^30 (q and out of that many rows alone take
+  // 256 GB), and keeps the kernel's sums with positions within 32 bits.
+  args.wl = std::min(window_left, 1 << 30);
+  args.wr = causal ? 0 : std::min(window_right, 1 << 30);
   args.out = static_cast<uint16_t*>(out);
   args.lse = lse;
   args.status = dev->status;
