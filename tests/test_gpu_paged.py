@@ -1036,7 +1036,7 @@ def test_attn_hint_that_changes_in_place(cuda_device):
         compare_attn(o.cpu(), lse.cpu(), *want)
 
 
-@pytest.mark.parametrize("size", [2 ** 30 - 1, 2 ** 31 - 1])
+@pytest.mark.parametrize("size", [2 ** 30 - 1, 2 ** 31 - 1, 2 ** 32, 2 ** 32 + 3, 2 ** 70])
 def test_windows_past_every_position(cuda_device, size):
     gen = torch.Generator().manual_seed(96)
     lens, q_lens = [200, 70], [3, 90]     # the second has rows before its first key

@@ -402,3 +402,9 @@ def test_the_build_sees_every_file_that_the_sources_include():
                     todo.append(os.path.join(os.path.dirname(path), line.split('"')[1]))
     assert any(p.endswith("paged_index.h") for p in seen)
     assert seen <= deps, sorted(seen - deps)
+
+
+def test_window_sizes_do_not_wrap():
+    got = [fa._window(n) for n in (-2 ** 40, -2 ** 32 + 5, -2, -1, 0, 7, 2 ** 31 - 1, 2 ** 31,
+                                   2 ** 32, 2 ** 32 + 5, 2 ** 64)]
+    assert got == [-2, -2, -2, -1, 0, 7] + [2 ** 31 - 1] * 5

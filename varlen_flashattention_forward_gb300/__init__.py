@@ -147,6 +147,12 @@ def _stream_ptr(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _window(n):
+    """A window's size as a 32-bit argument: sizes past every position mean the
+    same, and what is below -1 stays so (the library refuses it)."""
+    return max(-2, min(int(n), 2 ** 31 - 1))
+
+
 def _check(t, name, dtype, ndim, view=False):
     if t.dtype is dtype and t.dim() == ndim:
         if t.is_contiguous() or (view and t.stride(-1) == 1):
@@ -206,7 +212,7 @@ def fa_varlen_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q=0,
             _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k),
             batch, total_q, total_k, H, H_k, d_qk, d_v, int(max_seqlen_q),
             int(max_seqlen_k), float(softmax_scale), int(bool(causal)),
-            int(window_left), int(window_right), _ptr(out), _ptr(lse),
+            _window(window_left), _window(window_right), _ptr(out), _ptr(lse),
             _stream_ptr(stream))
     else:
         st = lib.fa_varlen_fwd_strided(
@@ -214,7 +220,7 @@ def fa_varlen_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q=0,
             _ptr(v), v.stride(0), v.stride(1), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k),
             batch, total_q, total_k, H, H_k, d_qk, d_v, int(max_seqlen_q),
             int(max_seqlen_k), float(softmax_scale), int(bool(causal)),
-            int(window_left), int(window_right), _ptr(out), _ptr(lse),
+            _window(window_left), _window(window_right), _ptr(out), _ptr(lse),
             _stream_ptr(stream))
     if st != FA_OK:
         raise FaError(st, "fa_varlen_fwd")
@@ -270,8 +276,8 @@ def fa_varlen_fwd_plan(batch, total_q, total_k, num_heads, num_heads_k, d_qk, d_
     g, s, p = ctypes.c_int(0), ctypes.c_int(0), ctypes.c_int(0)
     st = lib.fa_varlen_fwd_plan(int(batch), int(total_q), int(total_k), int(num_heads),
                                 int(num_heads_k), int(d_qk), int(d_v), int(max_seqlen_q),
-                                int(max_seqlen_k), int(bool(causal)), int(window_left),
-                                int(window_right), ctypes.byref(g), ctypes.byref(s),
+                                int(max_seqlen_k), int(bool(causal)), _window(window_left),
+                                _window(window_right), ctypes.byref(g), ctypes.byref(s),
                                 ctypes.byref(p))
     if st != FA_OK:
         raise FaError(st, "fa_varlen_fwd_plan")
@@ -599,7 +605,7 @@ def fa_paged_attn(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, seq_lens,
             q.data_ptr(), qr, qh, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
             v_scale.data_ptr(), cu_seqlens_q.data_ptr(), seq_lens.data_ptr(),
             page_table.data_ptr(), batch, T, H, hk, d, pages, width, max_seqlen_q, max_seqlen_k,
-            softmax_scale, bool(causal), window_left, out.data_ptr(), _p(lse),
+            softmax_scale, bool(causal), _window(window_left), out.data_ptr(), _p(lse),
             workspace.data_ptr(), need, _raw_stream(index))
     if st != FA_OK:
         raise FaError(st, "fa_paged_attn")
