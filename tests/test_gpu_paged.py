@@ -1056,3 +1056,24 @@ def test_windows_past_every_position(cuda_device, size):
                                      window_right=r, return_lse=True)
                     for l, r in ((-1, -1), win))
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("loud", [1.0, 100.0, 1e4])
+def test_attn_queries_with_a_loud_channel(cuda_device, loud):
+    """A row of q is held to 2^-17 of its largest value, here one that meets keys
+    of 0: the scores may be off by 2^-17 max |q| sum |k| scale more."""
+    gen = torch.Generator().manual_seed(97)
+    H, Hk, d, n = 8, 2, 64, 300
+    pages, num = plain.make_pages([n], gen)
+    (kc, ks), (vc, vs) = (plain.make_cache([n], pages, num, Hk, d, gen) for _ in range(2))
+    kc.view(torch.uint8)[:, :, :, 5] = 0
+    q = torch.randn((1, H, d), generator=gen).bfloat16()
+    q[..., 5] = loud
+    cpu = (q, kc, vc, ks, vs, plain.cum([1]), torch.tensor([n], dtype=torch.int32), pages)
+    o, lse = fa.fa_paged_attn(*dev(*cpu), return_lse=True)
+    wo, wl, w, a = plain.attention(q, kc, vc, ks, vs, [0, 1], [n], pages, 0.125, True, -1)
+    for h in range(H):
+        k, _ = plain.keys_of(0, n, pages, kc, ks, h // (H // Hk))
+        # compare_attn takes 2^-15 of a.
+        a[h, 0] += 2.0 ** -2 * 0.125 * float(q[0, h].abs().max()) * float(k.abs().sum(1).max())
+    compare_attn(o.cpu(), lse.cpu(), wo, wl, w, a)

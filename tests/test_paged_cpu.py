@@ -408,3 +408,52 @@ def test_window_sizes_do_not_wrap():
     got = [fa._window(n) for n in (-2 ** 40, -2 ** 32 + 5, -2, -1, 0, 7, 2 ** 31 - 1, 2 ** 31,
                                    2 ** 32, 2 ** 32 + 5, 2 ** 64)]
     assert got == [-2, -2, -2, -1, 0, 7] + [2 ** 31 - 1] * 5
+
+
+# ------------------------------------------- ranges and splits, row for row
+def test_key_ranges_are_no_wider_than_what_the_rows_see(probe):
+    rng = random.Random(3)
+    for _ in range(4000):
+        n = rng.randrange(1, 20)
+        ln = rng.randrange(-5, 400)
+        held = 64 * rng.randrange(1, 8)
+        i0 = rng.randrange(0, n)
+        i1 = rng.randrange(i0, n)
+        causal, window = rng.randrange(2), rng.choice([-1, 0, 1, 70, 300])
+        lo, hi = call(probe.probe_key_range, 2, i0, i1, n, ln, held, causal, window)
+        seen = [j for j in range(min(max(ln, 0), held))
+                if any((not causal or j <= ln - n + i) and (window < 0 or j >= ln - n + i - window)
+                       for i in range(i0, i1 + 1))]
+        assert (lo, hi) == (seen[0], seen[-1] + 1) if seen else lo == hi
+
+
+@pytest.mark.parametrize("rows", [16, 32])
+def test_splits_of_the_kernels_row_tiles(probe, rows):
+    # Every key tile that a row tile needs is in one CTA's range, and no other
+    # is; the ranges' costs differ by one at most.
+    rng = random.Random(rows)
+    for trial in range(150):
+        batch = rng.choice([1, 3, 20])
+        q_lens = [rng.choice([0, 1, 1, 5, 33, 200]) for _ in range(batch)]
+        held = 64 * rng.randrange(1, 60)
+        lens = [rng.choice([0, 1, 128, 129, rng.randrange(0, 4000), -3]) for _ in range(batch)]
+        hk, group = rng.choice([1, 2, 8]), rng.choice([1, 3, 4, 16, 40, 128])
+        causal, window = rng.randrange(2), rng.choice([-1, 0, 100, 1000])
+        ctas = rng.choice([1, 5, 152])
+        segs = walk(probe, q_lens, lens, hk, group, rows, causal, window, held, ctas)
+        want = set()
+        cost = 0
+        for b, (n, ln) in enumerate(zip(q_lens, lens)):
+            for t in range(-(-n * group // rows)):
+                i0, i1 = t * rows // group, min((t + 1) * rows, n * group) - 1
+                lo, hi = call(probe.probe_key_range, 2, i0, i1 // group, n, ln, held, causal,
+                              window)
+                tiles = range(lo // 128, -(-hi // 128)) if hi > lo else [lo // 128]
+                want |= {(b, h, t, j) for h in range(hk) for j in tiles}
+                cost += hk * (7 + len(tiles))
+        got = [(b, h, t, tile0 + i) for _, b, h, t, tile0, count, _, _ in segs for i in range(count)]
+        assert len(got) == len(set(got)) and set(got) == want
+        per_cta = [0] * ctas
+        for s in segs:
+            per_cta[s[0]] += s[5]
+        assert max(per_cta) <= -(-cost // ctas)
