@@ -558,7 +558,8 @@ def fa_paged_attn(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, seq_lens,
                   window_left=-1, out=None, lse=None, return_lse=False, workspace=None,
                   stream=None):
     """Attention of a few query rows per sequence over the paged 8-bit cache;
-    see fa_paged_attn in include/fa_gb300.h.
+    see fa_paged_attn in include/fa_gb300.h.  (From about 64 rows a sequence on,
+    fa_paged_kv_gather and fa_varlen_fwd are faster.)
 
     q [total_q, H, d] bf16 (strided view allowed), caches and scales as
     fa_paged_kv_append, cu_seqlens_q [batch+1], seq_lens [batch] and

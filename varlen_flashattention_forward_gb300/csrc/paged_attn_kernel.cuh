@@ -15,19 +15,19 @@
 //   St[key, row] = K[key, d] . Q[row, d]t     e4m3 x e4m3, M = 128, N = 2 rows
 //   Ot[d, row]  += V[key, d]t . Pt[key, row]  f16 x f16,   M = 128 (64), K = 128
 //
-// K is multiplied as it lies in the cache.  Q is scaled by a power of two to
-// at most 448 and held as the sum of two e4m3 numbers, hi = rn(q) and
-// lo = rn(q - hi): a bf16 significand has 8 bits and the two terms hold 4
-// each, so hi + lo is q exactly down to 2^-10 of the row's largest value and
-// within 2^-18 of it below.  The two terms are N-side neighbours of one MMA
+// K is multiplied as it lies in the cache.  Each row of Q is scaled by a power of
+// two, its largest value into [128, 256), and held as the sum of two e4m3
+// numbers, hi = rn(q) and lo = rn(q - hi): a bf16 significand has 8 bits and the
+// two terms hold 4 each, so hi + lo is q exactly down to 2^-9 of the row's
+// largest value and within 2^-17 of that below (e4m3's step ends at 2^-9).  The two terms are N-side neighbours of one MMA
 // (K is read once for both) and their scores are added in fp32.
 //
 // V goes through registers to f16 (exact), because P needs more than two
 // e4m3 terms can hold: a long row has many small weights, whose sum counts.
-// With f16 P is rounded to 11 bits and kept down to 2^-39 of the largest.
 // The key's V scale is folded into P: x' = x + log2(vs), and the running
 // maximum m is taken over x', so that P' = 2^(x' - m + 7) stays below 2^15;
-// the row sum adds 2^(x - m + 7).
+// the row sum adds 2^(x - m + 7).  As f16, P' has 11 bits down to 2^-14, that is
+// 2^-21 of the maximum, and steps of 2^-24, 2^-31 of it, below.
 //
 //   planner warp        walks the segments and publishes them in a ring, a
 //                       batch of up to 16 tiles at a time with the places and

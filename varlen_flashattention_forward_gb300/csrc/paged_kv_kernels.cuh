@@ -6,7 +6,8 @@
 // of two that keeps the largest value of the page within 448, the largest
 // e4m3 number, so that moving codes to a larger scale only drops bits at the
 // subnormal end.  A page that is filled over several calls only ever raises
-// its scale, and ends with the one that writing it at once would have given.
+// its scale, and ends with the one that writing it at once would have given
+// (unless rows were written over, as after rejected drafts: theirs counts too).
 #pragma once
 
 #include <cstdint>

@@ -3,7 +3,7 @@
 // rope_row.cuh).
 //
 // Bound by HBM: every row is read and written once.  8192 tokens x 40 heads of
-// 128 dims take 30.1 us, 5.7 TB/s; 5003 x 32 of 96 dims 14.6 us, 4.3 TB/s (two
+// 128 dims take 30.1 us, 5.7 TB/s; 5003 x 32 of 96 dims 14.6 us, 4.3 TB/s (four
 // of a group's 16 lanes are past the row); 64 tokens 2.25 us, the launch.  More
 // heads together (eight), more resident blocks or loads of the next unit ahead
 // of the stores all measured slower: reads and writes of the same DRAM pages
