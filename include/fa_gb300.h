@@ -495,6 +495,70 @@ fa_status fa_paged_attn(const void* q, long long q_row_stride, long long q_head_
                         size_t workspace_bytes, fa_stream_t stream);
 
 /*
+ * fa_paged_attn_masked -- fa_paged_attn with two more masks.  Arguments, rules,
+ * workspace (fa_paged_attn_plan's) and errors as there, and
+ *
+ *   sink_tokens   the keys j < sink_tokens stay visible to rows whose window
+ *                 has left them behind (attention sinks): row i sees key j iff
+ *                 j <= p_i (causal) and (j >= p_i - window_left or
+ *                 j < sink_tokens), p_i its position.  Without a window the
+ *                 number says nothing.
+ *   tree_mask     int32 [total_q, tree_words] or NULL with tree_words = 0: the
+ *                 sequence's n query rows are the nodes of a tree of drafted
+ *                 tokens, whose keys are the last n of its seq_len, and bit
+ *                 p % 32 of word p / 32 of row i says whether node i sees the
+ *                 key of node p (its ancestors' and its own; fa_draft_tree
+ *                 makes the masks).  Keys before the nodes' are seen by all of
+ *                 them, within the window: node i stands at position
+ *                 seq_len - n + d_i, d_i its depth, the number of bits of its
+ *                 mask less one.  The nodes' own keys are seen by the bits
+ *                 alone, whatever the window.  Nodes from 32 * tree_words on,
+ *                 and bits past the last node, name no key.  causal is not
+ *                 used then.
+ *
+ * With a tree the value of a NaN code in one of the nodes' keys can reach any
+ * row of its sequence, and not only where some row sees it.
+ *
+ * Host errors: as fa_paged_attn; FA_ERR_INVALID_ARG also for a negative
+ * sink_tokens or tree_words and a mask that is missing, FA_ERR_UNSUPPORTED
+ * for one of more than 2^31 - 1 words.
+ */
+fa_status fa_paged_attn_masked(const void* q, long long q_row_stride, long long q_head_stride,
+                               const void* k_cache, const void* v_cache, const float* k_scale,
+                               const float* v_scale, const int* cu_seqlens_q, const int* seq_lens,
+                               const int* page_table, int batch, int total_q, int num_heads,
+                               int num_heads_k, int head_dim, int num_pages, int max_pages_per_seq,
+                               int max_seqlen_q, int max_seqlen_k, float softmax_scale, int causal,
+                               int window_left, int sink_tokens, const int* tree_mask,
+                               int tree_words, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, fa_stream_t stream);
+
+/*
+ * fa_draft_tree -- the ancestor masks and the positions of drafted trees, from
+ * each node's parent.
+ *
+ *   parents       int32 [total]: within its sequence, the node a node follows
+ *                 (a smaller number), or -1 for one that follows the context.
+ *                 Any other value counts as -1.
+ *   cu_seqlens    int32 [batch + 1]: sequence b's nodes.
+ *   seq_lens      int32 [batch]: length of each sequence with its nodes.
+ *   tree_words    32-bit words of a mask, at least 1: nodes below
+ *                 32 * tree_words are named in it.
+ *   tree_mask     int32 [total, tree_words], written: bit p of a node's mask is
+ *                 set for itself and each of its ancestors.
+ *   positions     int32 [total] or NULL, written: seq_len - n + depth, the
+ *                 position of fa_qk_norm_rope (a node that follows the context
+ *                 has depth 0).
+ * Rows behind the last sequence are left as they were.
+ *
+ * Host errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED (total * tree_words past
+ * 2^31 - 1), FA_ERR_ARCH, FA_ERR_LAUNCH.
+ */
+fa_status fa_draft_tree(const int* parents, const int* cu_seqlens, const int* seq_lens, int batch,
+                        int total, int tree_words, int* tree_mask, int* positions,
+                        fa_stream_t stream);
+
+/*
  * fa_paged_attn_plan -- the launch shape and the workspace of a fa_paged_attn
  * call of these sizes on the current device, without launching anything.
  *

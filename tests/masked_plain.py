@@ -1,0 +1,117 @@
+"""Plain fp64 forms of the masks (sinks, drafted trees), and inputs for their
+tests.  Written from the definitions in include/fa_gb300.h, on the CPU."""
+import math
+import random
+
+import torch
+
+import paged_plain as plain
+
+
+def random_parents(n, seed, roots=0.05, chain=0.3):
+    """Parents of a tree of n nodes: some follow the node before, some any."""
+    rng = random.Random(seed)
+    out = []
+    for i in range(n):
+        if i == 0 or rng.random() < roots:
+            out.append(-1)
+        elif rng.random() < chain:
+            out.append(i - 1)
+        else:
+            out.append(rng.randrange(i))
+    return out
+
+
+def path_of(parents, i):
+    """Node i and its ancestors."""
+    path = [i]
+    while 0 <= parents[path[-1]] < path[-1]:
+        path.append(parents[path[-1]])
+    return path
+
+
+def words_of(nodes, words):
+    """A mask's words (as signed 32-bit numbers) that name `nodes`."""
+    row = [0] * words
+    for p in nodes:
+        if p < 32 * words:
+            row[p // 32] |= 1 << (p % 32)
+    return [w - (1 << 32) if w >> 31 else w for w in row]
+
+
+def tree_masks(trees, words):
+    """int32 [nodes of all trees, words]."""
+    rows = [words_of(path_of(t, i), words) for t in trees for i in range(len(t))]
+    return torch.tensor(rows, dtype=torch.int32).reshape(-1, words)
+
+
+def named(row, p):
+    """Whether bit p of a mask row (signed words) is set."""
+    return p < 32 * len(row) and bool((row[p // 32] >> (p % 32)) & 1)
+
+
+def seen_keys(i, n, length, keys, causal, wl, wr, sinks, row=None):
+    """Truth values of the `keys` first keys for row i of n at bottom-right
+    position length - n + i, or for node i of a tree with mask `row`."""
+    j = torch.arange(keys)
+    ctx = length - n
+    if row is not None:
+        depth = max(sum(bin(w & 0xFFFFFFFF).count("1") for w in row) - 1, 0)
+        at = ctx + depth
+        seen = torch.ones(keys, dtype=torch.bool)
+        if wl >= 0:
+            seen = (j >= at - wl) | (j < sinks)
+        for x in range(max(ctx, 0), keys):
+            seen[x] = named(row, x - ctx)
+        return seen
+    at = ctx + i
+    seen = torch.ones(keys, dtype=torch.bool)
+    if causal:
+        seen &= j <= at
+    elif wr >= 0:
+        seen &= j <= at + wr
+    if wl >= 0:
+        seen &= (j >= at - wl) | (j < sinks)
+    return seen
+
+
+def attend(row, k, v, seen, scale):
+    """(O, LSE, sum p |v|, largest scale * sum |q k|) of one row over keys."""
+    d = v.shape[1]
+    if not seen.any():
+        zero = torch.zeros(d, dtype=torch.float64)
+        return zero, -math.inf, zero, 0.0
+    row = row.double()
+    x = k[seen] @ row * scale
+    top = x.max()
+    p = torch.exp(x - top)
+    return (p @ v[seen] / p.sum(), top + torch.log(p.sum()), p @ v[seen].abs() / p.sum(),
+            (k[seen].abs() @ row.abs()).max() * scale)
+
+
+def paged_attention(q, kc, vc, ks, vs, cu, lens, pages, scale, causal=True, window=-1, sinks=0,
+                    mask=None):
+    """As paged_plain.attention, with the masks."""
+    T, H, d = q.shape
+    hks = kc.shape[1]
+    o = torch.zeros((T, H, d), dtype=torch.float64)
+    w = torch.zeros((T, H, d), dtype=torch.float64)
+    lse = torch.full((H, T), -math.inf, dtype=torch.float64)
+    big = torch.zeros((H, T), dtype=torch.float64)
+    rows = None if mask is None else mask.tolist()
+    for b, length in enumerate(lens):
+        n = cu[b + 1] - cu[b]
+        keys = min(max(length, 0), pages.shape[1] * 64)
+        if n <= 0 or keys == 0:
+            continue
+        seen = [seen_keys(i, n, length, keys, causal, window, -1, sinks,
+                          None if rows is None else rows[cu[b] + i]) for i in range(n)]
+        for hk in range(hks):
+            k, held = plain.keys_of(b, keys, pages, kc, ks, hk)
+            v, _ = plain.keys_of(b, keys, pages, vc, vs, hk)
+            for i in range(n):
+                for h in range(hk * (H // hks), (hk + 1) * (H // hks)):
+                    t = cu[b] + i
+                    o[t, h], lse[h, t], w[t, h], big[h, t] = attend(q[t, h], k, v, seen[i] & held,
+                                                                    scale)
+    return o, lse, w, big

@@ -29,6 +29,8 @@ Entry points (same names as the C ABI):
   fa_paged_attn(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, seq_lens, page_table,
                 max_seqlen_q=0, max_seqlen_k=0, softmax_scale=None, causal=True,
                 window_left=-1, out=None, lse=None, return_lse=False, workspace=None,
+                stream=None, sink_tokens=0, tree_mask=None)
+  fa_draft_tree(parents, cu_seqlens, seq_lens, max_nodes=64, tree_mask=None, positions=None,
                 stream=None)
   fa_paged_attn_plan(batch, total_q, num_heads, num_heads_k, head_dim, max_seqlen_q=0)
   fa_paged_kv_gather(k_cache, v_cache, k_scale, v_scale, cu_seqlens, page_table, total_k,
@@ -59,7 +61,8 @@ LIB_PATH = os.path.join(_PKG, "libfa_gb300.so")
 EXPORTS = ("fa_varlen_fwd", "fa_varlen_fwd_plan", "fa_varlen_fwd_strided", "fa_sparse_mla_decode",
            "fa_sparse_mla_decode_plan", "fa_sparse_mla_decode_noalloc", "fa_merge_attn_states",
            "fa_qk_norm_rope", "fa_paged_kv_append", "fa_paged_attn", "fa_paged_attn_plan",
-           "fa_paged_kv_gather", "fa_get_device_status", "fa_set_wait_limit_ns", "fa_status_string")
+           "fa_paged_attn_masked", "fa_draft_tree", "fa_paged_kv_gather", "fa_get_device_status",
+           "fa_set_wait_limit_ns", "fa_status_string")
 
 _lib = None
 
@@ -114,6 +117,12 @@ def load_library():
     lib.fa_paged_attn.argtypes = [p, i64, i64, p, p, p, p, p, p, p, i32, i32, i32, i32, i32, i32,
                                   i32, i32, i32, f32, i32, i32, p, p, p, size, p]
     lib.fa_paged_attn.restype = i32
+    lib.fa_paged_attn_masked.argtypes = [p, i64, i64, p, p, p, p, p, p, p, i32, i32, i32, i32, i32,
+                                         i32, i32, i32, i32, f32, i32, i32, i32, p, i32, p, p, p,
+                                         size, p]
+    lib.fa_paged_attn_masked.restype = i32
+    lib.fa_draft_tree.argtypes = [p, p, p, i32, i32, i32, p, p, p]
+    lib.fa_draft_tree.restype = i32
     lib.fa_paged_attn_plan.argtypes = [i32, i32, i32, i32, i32, i32, pi, pi,
                                        ctypes.POINTER(size)]
     lib.fa_paged_attn_plan.restype = i32
@@ -556,10 +565,11 @@ def fa_paged_attn_plan(batch, total_q, num_heads, num_heads_k, head_dim, max_seq
 def fa_paged_attn(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, seq_lens, page_table,
                   max_seqlen_q=0, max_seqlen_k=0, softmax_scale=None, causal=True,
                   window_left=-1, out=None, lse=None, return_lse=False, workspace=None,
-                  stream=None):
+                  stream=None, sink_tokens=0, tree_mask=None):
     """Attention of a few query rows per sequence over the paged 8-bit cache;
-    see fa_paged_attn in include/fa_gb300.h.  (From about 64 rows a sequence on,
-    fa_paged_kv_gather and fa_varlen_fwd are faster.)
+    see fa_paged_attn and fa_paged_attn_masked in include/fa_gb300.h.  (From
+    about 64 rows a sequence on, fa_paged_kv_gather and fa_varlen_fwd are
+    faster.)
 
     q [total_q, H, d] bf16 (strided view allowed), caches and scales as
     fa_paged_kv_append, cu_seqlens_q [batch+1], seq_lens [batch] and
@@ -567,6 +577,11 @@ def fa_paged_attn(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, seq_lens,
     bf16, or (out, lse [H, total_q] fp32) if an lse buffer is given or
     return_lse is set.  workspace: a uint8 CUDA tensor of the bytes
     fa_paged_attn_plan gives; None allocates one for the call.
+
+    sink_tokens: the first keys of a sequence that stay visible behind its
+    window.  tree_mask [total_q, words] int32: the query rows are nodes of
+    drafted trees and see the keys of the nodes their bits name (fa_draft_tree),
+    and all keys before; causal is not used then.
     """
     import torch
     lib = load_library()
@@ -578,12 +593,13 @@ def fa_paged_attn(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, seq_lens,
     T, H, dq = q.shape
     if dq != d:
         raise ValueError(f"q has head dim {dq}, the cache {d}")
+    sink_tokens, words = int(sink_tokens), _tree_words(tree_mask, T)
     # (Now: the workspace's size is looked up by the values of these sizes.)
     max_seqlen_q, max_seqlen_k = int(max_seqlen_q), int(max_seqlen_k)
     if softmax_scale is None:
         softmax_scale = d ** -0.5
     index, here = _device(stream, q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, seq_lens,
-                          page_table, out, lse, workspace)
+                          page_table, out, lse, workspace, tree_mask)
     with here:
         if out is None:
             out = torch.empty((T, H, d), dtype=torch.bfloat16, device=q.device)
@@ -602,15 +618,74 @@ def fa_paged_attn(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, seq_lens,
             _check(workspace, "workspace", torch.uint8, 1)
             need = workspace.shape[0]
         qr, qh, _ = q.stride()
-        st = lib.fa_paged_attn(
+        st = lib.fa_paged_attn_masked(
             q.data_ptr(), qr, qh, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
             v_scale.data_ptr(), cu_seqlens_q.data_ptr(), seq_lens.data_ptr(),
             page_table.data_ptr(), batch, T, H, hk, d, pages, width, max_seqlen_q, max_seqlen_k,
-            softmax_scale, bool(causal), _window(window_left), out.data_ptr(), _p(lse),
-            workspace.data_ptr(), need, _raw_stream(index))
+            softmax_scale, bool(causal), _window(window_left), _sinks(sink_tokens), _p(tree_mask),
+            words, out.data_ptr(), _p(lse), workspace.data_ptr(), need, _raw_stream(index))
     if st != FA_OK:
         raise FaError(st, "fa_paged_attn")
     return (out, lse) if lse is not None else out
+
+
+def _sinks(n):
+    """A number of first keys as a 32-bit argument: past every position it means
+    all of them, and what is below 0 stays so (the library refuses it)."""
+    return max(-1, min(int(n), 2 ** 31 - 1))
+
+
+def _tree_words(tree_mask, total):
+    """Words of a row of a tree mask (None: 0)."""
+    if tree_mask is None:
+        return 0
+    import torch
+    _check(tree_mask, "tree_mask", torch.int32, 2)
+    words = tree_mask.shape[1]
+    _shape(tree_mask, "tree_mask", (total, words))
+    if words < 1:
+        raise ValueError("tree_mask must have a word for each row")
+    return words
+
+
+def fa_draft_tree(parents, cu_seqlens, seq_lens, max_nodes=64, tree_mask=None, positions=None,
+                  stream=None):
+    """Ancestor masks and positions of drafted trees; see fa_draft_tree in
+    include/fa_gb300.h.
+
+    parents [total] int32 (within its sequence, -1: follows the context),
+    cu_seqlens [batch+1] int32 (each sequence's nodes), seq_lens [batch] int32
+    (lengths with the nodes), max_nodes the largest tree's nodes.  Returns
+    (tree_mask [total, words] int32, positions [total] int32): the mask of
+    fa_paged_attn and fa_varlen_fwd, the positions of fa_qk_norm_rope.
+    """
+    import torch
+    lib = load_library()
+    i32 = torch.int32
+    _check(parents, "parents", i32, 1)
+    _check(cu_seqlens, "cu_seqlens", i32, 1)
+    _check(seq_lens, "seq_lens", i32, 1)
+    batch, total = cu_seqlens.shape[0] - 1, parents.shape[0]
+    _shape(seq_lens, "seq_lens", (batch,))
+    index, here = _device(stream, parents, cu_seqlens, seq_lens, tree_mask, positions)
+    with here:
+        if tree_mask is None:
+            if max_nodes < 1:
+                raise ValueError(f"max_nodes must be at least 1, got {max_nodes}")
+            tree_mask = torch.empty((total, -(-int(max_nodes) // 32)), dtype=i32,
+                                    device=parents.device)
+        words = _tree_words(tree_mask, total)
+        if positions is None:
+            positions = torch.empty((total,), dtype=i32, device=parents.device)
+        else:
+            _check(positions, "positions", i32, 1)
+            _shape(positions, "positions", (total,))
+        st = lib.fa_draft_tree(parents.data_ptr(), cu_seqlens.data_ptr(), seq_lens.data_ptr(),
+                               batch, total, words, tree_mask.data_ptr(), positions.data_ptr(),
+                               _raw_stream(index))
+    if st != FA_OK:
+        raise FaError(st, "fa_draft_tree")
+    return tree_mask, positions
 
 
 @functools.lru_cache(maxsize=1024)

@@ -1,0 +1,62 @@
+// draft_tree_kernel.cuh -- ancestor masks and positions of drafted trees.
+//
+//   mask(i) = { i } + mask(parent(i)),   position(i) = seq_len - n + depth(i)
+//
+// A thread takes a node and walks up to the root.  Parents are smaller
+// numbers, so the walk passes the words of its mask from the last to the
+// first and writes each once; it takes at most as many steps as there are
+// nodes.  Latency alone bounds it: a launch and the chain of loads, which
+// after the first come from L1 (24 trees of 33 to 64 nodes, about 8 deep: see
+// fa_draft_tree in the design notes' table).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "paged_index.h"
+
+namespace fa {
+
+struct DraftTreeArgs {
+  const int *parents, *cu, *seq_lens;
+  int total, words;
+  int *mask, *positions;
+};
+
+constexpr int kTreeThreads = 64;
+
+// Block (x, b): nodes of sequence b from kTreeThreads * x on, in steps of the
+// grid.
+__global__ void __launch_bounds__(kTreeThreads) draft_tree_kernel(const DraftTreeArgs a) {
+  const int b = blockIdx.y;
+  const RowRange r = row_range(__ldg(a.cu + b), __ldg(a.cu + b + 1), a.total);
+  const long long context = (long long)__ldg(a.seq_lens + b) - r.n;
+  for (int i = blockIdx.x * kTreeThreads + threadIdx.x; i < r.n; i += gridDim.x * kTreeThreads) {
+    int* row = a.mask + (size_t)(r.lo + i) * a.words;
+    int node = i, depth = -1, word = a.words - 1;
+    unsigned bits = 0;
+    while (node >= 0) {
+      const int w = node >> 5;
+      // (Nodes past the mask's words leave no bit.)
+      if (w <= word) {
+        for (; word > w; --word) {
+          row[word] = (int)bits;
+          bits = 0;
+        }
+        bits |= 1u << (node & 31);
+      }
+      ++depth;
+      const int up = __ldg(a.parents + r.lo + node);
+      node = up < node ? up : -1;
+    }
+    for (; word >= 0; --word) {
+      row[word] = (int)bits;
+      bits = 0;
+    }
+    if (a.positions) {
+      const long long p = context + depth;
+      a.positions[r.lo + i] = (int)(p > -0x80000000ll ? p : -0x80000000ll);
+    }
+  }
+}
+
+}  // namespace fa

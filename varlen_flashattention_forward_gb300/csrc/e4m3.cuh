@@ -1,0 +1,51 @@
+// e4m3.cuh -- the 8-bit cache's numbers: codes, and the scale of a page.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "paged_index.h"
+
+namespace fa {
+
+constexpr float kE4m3Max = 448.f;
+// Scales stay within 2^-64 .. 2^64: the attention's scores, and its sums of
+// weights relative to weight times V scale, then stay inside fp32 (where sums
+// meet, with root_ex2).
+constexpr int kScaleExpMax = 64;
+
+// Smallest power of two s with amax <= 448 s, clamped (amax finite, >= 0).
+__device__ __forceinline__ float scale_for(float amax) {
+  // amax / 512 = m 2^e with m in [0.5, 1), and 448 = 512 * 0.875.
+  int e;
+  const float m = frexpf(amax * (1.f / 512.f), &e);
+  if (m > 0.875f) ++e;
+  if (!(amax > 0.f)) e = -kScaleExpMax;
+  e = imin(imax(e, -kScaleExpMax), kScaleExpMax);
+  return ldexpf(1.f, e);
+}
+
+// Two fp32 values as e4m3 codes (round to nearest even, saturating at 448,
+// NaN kept): lo in bits 0..7.
+__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// Two e4m3 codes as f16x2 (exact).
+__device__ __forceinline__ uint32_t unpack_e4m3x2(uint32_t codes) {
+  uint32_t d;
+  const uint16_t c = (uint16_t)codes;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(c));
+  return d;
+}
+__device__ __forceinline__ float2 f16x2_floats(uint32_t h) {
+  float2 f;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\t"
+      "cvt.f32.f16 %1, h;\n\t}"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(h));
+  return f;
+}
+
+}  // namespace fa

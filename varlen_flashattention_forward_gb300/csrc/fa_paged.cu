@@ -12,8 +12,8 @@
 #include <cuda_runtime.h>
 
 #include "host_common.h"
-#include "paged_attn_kernel.cuh"
 #include "paged_kv_kernels.cuh"
+#include "paged_launch.cuh"
 #include "qk_norm_rope_kernel.cuh"
 
 using fa::is_aligned;
@@ -62,39 +62,6 @@ bool encode_cache(CUtensorMap* m, const void* base, int head_dim, int cells, int
             CU_TENSOR_MAP_INTERLEAVE_NONE,
             row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-template <int D, int N>
-cudaError_t launch_attn(const CUtensorMap& k_map, const CUtensorMap& v_map,
-                        const fa::PagedAttnArgs& a, int grid, cudaStream_t stream) {
-  // Set once per device; concurrent first calls may both set it (the call is
-  // idempotent), the flag itself is atomic.
-  static std::atomic<bool> attr_done[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  const int smem = (int)fa::paged_smem<D, N>();
-  if (!attr_done[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(fa::paged_attn_kernel<D, N>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    attr_done[dev].store(true, std::memory_order_release);
-  }
-  fa::paged_attn_kernel<D, N><<<grid, fa::kPagedThreads, smem, stream>>>(k_map, v_map, a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || grid < 2) return e;
-  cudaLaunchConfig_t cfg;
-  std::memset(&cfg, 0, sizeof cfg);
-  cfg.gridDim = dim3(grid - 1, N);
-  cfg.blockDim = dim3(D);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fa::paged_merge_kernel<D, N>, a);
 }
 
 bool cache_dim(int d) { return d == 64 || d == 80 || d == 96 || d == 128; }
@@ -360,6 +327,21 @@ extern "C" fa_status fa_paged_attn(const void* q, long long q_row_stride, long l
                                    int max_seqlen_k, float softmax_scale, int causal,
                                    int window_left, void* out, float* lse, void* workspace,
                                    size_t workspace_bytes, fa_stream_t stream) {
+  return fa_paged_attn_masked(q, q_row_stride, q_head_stride, k_cache, v_cache, k_scale, v_scale,
+                              cu_seqlens_q, seq_lens, page_table, batch, total_q, num_heads,
+                              num_heads_k, head_dim, num_pages, max_pages_per_seq, max_seqlen_q,
+                              max_seqlen_k, softmax_scale, causal, window_left, 0, nullptr, 0, out,
+                              lse, workspace, workspace_bytes, stream);
+}
+
+extern "C" fa_status fa_paged_attn_masked(
+    const void* q, long long q_row_stride, long long q_head_stride, const void* k_cache,
+    const void* v_cache, const float* k_scale, const float* v_scale, const int* cu_seqlens_q,
+    const int* seq_lens, const int* page_table, int batch, int total_q, int num_heads,
+    int num_heads_k, int head_dim, int num_pages, int max_pages_per_seq, int max_seqlen_q,
+    int max_seqlen_k, float softmax_scale, int causal, int window_left, int sink_tokens,
+    const int* tree_mask, int tree_words, void* out, float* lse, void* workspace,
+    size_t workspace_bytes, fa_stream_t stream) {
   if ((total_q > 0 && (!q || !out)) || !seq_lens) return FA_ERR_INVALID_ARG;
   fa_status st = check_cache(k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, page_table, batch,
                              total_q, num_heads_k, head_dim, num_pages, max_pages_per_seq);
@@ -367,12 +349,17 @@ extern "C" fa_status fa_paged_attn(const void* q, long long q_row_stride, long l
   if (num_heads < 1 || num_heads % num_heads_k != 0 || max_seqlen_q < 0 || max_seqlen_k < 0 ||
       window_left < -1 || !(softmax_scale > 0.f) || !std::isfinite(softmax_scale))
     return FA_ERR_INVALID_ARG;
+  if (sink_tokens < 0 || tree_words < 0 || !is_aligned(tree_mask, 4) ||
+      (tree_words > 0 && total_q > 0 && !tree_mask))
+    return FA_ERR_INVALID_ARG;
   if (!is_aligned(q, 16) || !is_aligned(out, 16) || !is_aligned(lse, 4) ||
       !is_aligned(seq_lens, 4) || !is_aligned(workspace, 16))
     return FA_ERR_INVALID_ARG;
   if (total_q > 0 && !settle_view(total_q, num_heads, head_dim, &q_row_stride, &q_head_stride))
     return FA_ERR_INVALID_ARG;
-  if ((int64_t)total_q * num_heads > INT32_MAX || num_heads > 65535) return FA_ERR_UNSUPPORTED;
+  if ((int64_t)total_q * num_heads > INT32_MAX || num_heads > 65535 ||
+      (int64_t)total_q * tree_words > INT32_MAX)
+    return FA_ERR_UNSUPPORTED;
   fa::DeviceFacts dev;
   st = fa::device_facts(&dev);
   if (st != FA_OK) return st;
@@ -396,7 +383,7 @@ extern "C" fa_status fa_paged_attn(const void* q, long long q_row_stride, long l
   a.max_pages = max_pages_per_seq;
   a.num_pages = num_pages;
   a.shape = {num_heads_k, group, l.rows, causal != 0, window_left,
-             max_pages_per_seq * fa::kPageTokens};
+             max_pages_per_seq * fa::kPageTokens, sink_tokens, tree_words > 0};
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
@@ -404,6 +391,8 @@ extern "C" fa_status fa_paged_attn(const void* q, long long q_row_stride, long l
   a.part_o = reinterpret_cast<float*>(ws);
   a.part_lse = reinterpret_cast<float*>(ws + l.o_bytes);
   a.meta = reinterpret_cast<int4*>(ws + l.o_bytes + l.lse_bytes);
+  a.tree_mask = tree_mask;
+  a.tree_words = tree_words;
   a.status = dev.status;
   a.wait_limit_ns = dev.wait_limit_ns;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -415,6 +404,8 @@ extern "C" fa_status fa_paged_attn(const void* q, long long q_row_stride, long l
       ((long long)max_pages_per_seq * fa::kPageTokens / fa::kTileKeys + 1 + fa::kUnitCost);
   const long long row_tiles = (long long)total_q * group / l.rows;
   const long long fit = fa::kMaxCost / per_row_tile - row_tiles;
+  // (Sinks say nothing without a window.)
+  const bool masked = tree_words > 0 || (sink_tokens > 0 && window_left >= 0);
   if (fit < 1) return FA_ERR_UNSUPPORTED;
   const int step = (int)std::min<long long>(fa::kPagedMaxBatch, fit);
   for (int b0 = 0; b0 < batch; b0 += step) {
@@ -422,13 +413,9 @@ extern "C" fa_status fa_paged_attn(const void* q, long long q_row_stride, long l
     a.cu = cu_seqlens_q + b0;
     a.seq_lens = seq_lens + b0;
     a.page_table = page_table + (size_t)b0 * max_pages_per_seq;
-    cudaError_t e;
-    if (l.dim == 64)
-      e = l.rows == 16 ? launch_attn<64, 16>(k_map, v_map, a, l.grid, s)
-                       : launch_attn<64, 32>(k_map, v_map, a, l.grid, s);
-    else
-      e = l.rows == 16 ? launch_attn<128, 16>(k_map, v_map, a, l.grid, s)
-                       : launch_attn<128, 32>(k_map, v_map, a, l.grid, s);
+    const cudaError_t e = masked ? fa::launch_attn_masked(l.dim, l.rows, k_map, v_map, a, l.grid, s)
+                                 : fa::launch_attn_shape<false>(l.dim, l.rows, k_map, v_map, a,
+                                                                l.grid, s);
     if (e != cudaSuccess) return FA_ERR_LAUNCH;
   }
   return FA_OK;

@@ -69,9 +69,10 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "e4m3.cuh"
 #include "named_bar.cuh"
 #include "paged_index.h"
-#include "paged_kv_kernels.cuh"
+#include "rope_row.cuh"                // bf16 rows
 #include "sm103_ptx.cuh"
 #include "varlen_fwd_kernel.cuh"     // bounded waits, status word
 
@@ -113,6 +114,10 @@ struct PagedAttnArgs {
   int4* meta;
   unsigned int* status;
   uint64_t wait_limit_ns;
+  // kMasked only: tree_mask [total_q, tree_words], bit p of row i: it sees the
+  // sequence's p-th node (shape.tree), else null.
+  const int* tree_mask;
+  int tree_words;
 };
 
 // A page of a batch: its (page, head) cell of the cache, -1 where there is
@@ -134,12 +139,19 @@ struct alignas(16) BatchPlan {
   int head, q0, row0, rows;    // first q row of the sequence; rows of the tile
   int out[N], lse[N];          // of each row: its place in O (rows) and in the LSE
   int tok0, tok1;              // tokens of its first and last row
-  alignas(16) int token[N];    // of each row, from tok0
-  long long at0;               // position of tok0
+  // Row n stands at at0 + token[n].  (token: its token, from tok0; with a tree
+  // its depth, and at0 is the first node's key.)
+  alignas(16) int token[N];
+  long long at0;
   int tiles;                   // of the segment
   int whole;                   // the segment covers its unit
   int unit_end;                // where the unit starts in this segment but does
                                // not end: the cost up to its end, else -1
+  // kMasked only: tile t of the batch is key tile tile0 + t, and from gap_at on
+  // `gap` more; keys below sink are seen too; the deepest row; each row's
+  // place in tree_mask.
+  int gap_at, gap, sink, deepest;
+  int mask[N];
 };
 
 template <int D, int N>
@@ -262,7 +274,10 @@ __device__ __forceinline__ float warp_transpose_reduce16(float* x, int lane) {
 // for each key) where another one that it joins is down to 2^-57.
 __device__ __forceinline__ float root_ex2(float d) { return ptx::ex2(0.5f * d); }
 
-template <int D, int N>
+// kMasked: keys that a sliding window leaves behind but for the first ones
+// (shape.sinks), and rows that are nodes of a tree (shape.tree).  The other
+// instantiations are as if there were neither.
+template <int D, int N, bool kMasked>
 __global__ void __launch_bounds__(kPagedThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap k_map,
                       const __grid_constant__ CUtensorMap v_map, const PagedAttnArgs a) {
@@ -333,7 +348,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         RowRange q;
         int len;
         seq_of(b, &q, &len);
-        n = capped_cost(sh.heads_k * head_cost(sh, q.n, len));
+        n = capped_cost(sh.heads_k * head_cost<kMasked>(sh, q.n, len));
       }
       long long sum = n;
 #pragma unroll
@@ -403,6 +418,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       const BatchPlan<N>& plan = plan_of(b, &ok);
       if (!ok) break;
       const int count = plan.count, tile0 = plan.tile0, key_lo = plan.lo, key_hi = plan.hi;
+      const int gap_at = kMasked ? plan.gap_at : 0, gap = kMasked ? plan.gap : 0;
+      const int sink = kMasked ? plan.sink : 0;
       if (count == 0) break;
       // (held is written with the scales)
       ok = wait(cb->scale_full[b % kPagedPlans], (b / kPagedPlans) & 1);
@@ -419,14 +436,16 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
 #pragma unroll
         for (int k = 0; k < kIters; ++k)
           c[k] = *reinterpret_cast<const uint4*>(src + k * kStep * C::kRow);
-        const int key0 = (tile0 + n) * kTileKeys;
+        const int key0 = (tile0 + n + (kMasked && n >= gap_at ? gap : 0)) * kTileKeys;
         const int lo = key_lo - key0, hi = key_hi - key0;
+        const int first = kMasked ? sink - key0 : 0;  // rows below it are seen too
         const unsigned pages = (held >> (2 * n)) & 3;
         if (__builtin_expect(lo > 0 || hi < kTileKeys || pages != 3, 0)) {
 #pragma unroll
           for (int k = 0; k < kIters; ++k) {
             const int r = r0 + k * kStep;
-            if (r < lo || r >= hi || !((pages >> (r >> 6)) & 1)) c[k] = make_uint4(0u, 0u, 0u, 0u);
+            if ((r < lo && !(kMasked && r < first)) || r >= hi || !((pages >> (r >> 6)) & 1))
+              c[k] = make_uint4(0u, 0u, 0u, 0u);
           }
         }
         if (i >= 2) {
@@ -602,9 +621,11 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       // Lane l: page l of the batch's tiles, as its cell of the cache, or -1
       // where it is not needed or not there.
       auto cells = [&]() {
-        const int p = (g.tile0 + n0) * 2 + lane;
+        int p = (g.tile0 + n0) * 2 + lane;
+        if (kMasked) p = tile_of(g.tiles, g.part_lo + n0 + lane / 2) * 2 + (lane & 1);
         if (n0 + lane / 2 >= g.count || (long long)p * kPageTokens >= g.keys.hi ||
-            (long long)(p + 1) * kPageTokens <= g.keys.lo)
+            ((long long)(p + 1) * kPageTokens <= g.keys.lo &&
+             !(kMasked && (long long)p * kPageTokens < g.keys.sink)))
           return -1;
         const int id = checked_page(
             __ldg(a.page_table + (size_t)g.seq * a.max_pages + p), a.num_pages);
@@ -657,14 +678,39 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
               plan.lse[lane] = row_h * a.total_q + row_q;
               plan.token[lane] = tok - token_of(sh, g.row_tile * N);
             }
+            if constexpr (kMasked) {
+              if (sh.tree) {
+                // The nodes' depths: the bits of their masks, less their own.
+                // (A row past the last has the first row's mask.)
+                const int at = (lane < rows ? row_q : g.q.lo) * a.tree_words;
+                int depth = 0;
+                if (sh.window >= 0 && lane < rows) {
+#pragma unroll 1
+                  for (int w = 0; w < a.tree_words; ++w) depth += __popc(__ldg(a.tree_mask + at + w));
+                  depth = imax(depth - 1, 0);
+                }
+                const int deepest = __reduce_max_sync(0xffffffffu, depth);
+                if (lane < N) {
+                  plan.token[lane] = depth;
+                  plan.mask[lane] = at;
+                }
+                if (lane == 0) plan.deepest = deepest;
+              }
+            }
           }
           if (first) load_rows(0);  // (ahead of the pages' loads in the memory system)
           plan.cell[lane] = cell;
           if (lane == 0) {
             const int row0 = g.row_tile * N;
             plan.count = imin(g.count - n0, kPlanTiles);
-            plan.tile0 = g.tile0 + n0;
+            plan.tile0 = kMasked ? tile_of(g.tiles, g.part_lo + n0) : g.tile0 + n0;
             plan.first = first;
+            if constexpr (kMasked) {
+              const int left = g.tiles.head - (g.part_lo + n0);  // tiles before the gap
+              plan.gap_at = imax(left, 0);
+              plan.gap = left > 0 ? g.tiles.first - g.tiles.head : 0;
+              plan.sink = g.keys.sink;
+            }
             plan.last = ends;
             plan.lo = g.keys.lo;
             plan.hi = g.keys.hi;
@@ -674,7 +720,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             plan.rows = rows;
             plan.tok0 = token_of(sh, row0);
             plan.tok1 = token_of(sh, row0 + rows - 1);
-            plan.at0 = (long long)g.len - g.q.n + plan.tok0;
+            plan.at0 = (long long)g.len - g.q.n + (kMasked && sh.tree ? 0 : plan.tok0);
             plan.tiles = g.count;
             plan.whole = g.count == g.unit_count;
             plan.unit_end =
@@ -692,7 +738,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         n0 += kPlanTiles;
         if (ends) {
           n0 = 0;
-          more = walk_next(&walk, sh, before, seq_of, &g);
+          more = walk_next<kMasked>(&walk, sh, before, seq_of, &g);
         }
         last = g.count - n0 <= kPlanTiles;
         cell = more ? cells() : -1;
@@ -970,14 +1016,21 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
           const uint32_t phase = (uint32_t)(at >> 1) & 1;
           const PagePlan pp = plan.page[2 * t + page];
           lv = pp.lv;
-          const int j0 = (tile0 + t) * kTileKeys;
-          const bool seen = j0 + key >= plan.lo && (unsigned)(j0 + key) < (unsigned)plan.hi && pp.held;
+          const int j0 =
+              (tile0 + t + (kMasked && t >= plan.gap_at ? plan.gap : 0)) * kTileKeys;
+          const bool seen = (j0 + key >= plan.lo || (kMasked && j0 + key < plan.sink)) &&
+                            (unsigned)(j0 + key) < (unsigned)plan.hi && pp.held;
           // Rows of several tokens see different keys: the tiles at the edges
           // are masked row by row.
-          const bool edge =
+          bool edge =
               tok0 != tok1 &&
               ((sh.causal && (long long)j0 + kTileKeys - 1 > at0) ||
                (sh.window >= 0 && (long long)j0 < at0 + (tok1 - tok0) - sh.window));
+          if constexpr (kMasked) {
+            if (sh.tree)
+              edge = (long long)j0 + kTileKeys > at0 ||
+                     (sh.window >= 0 && (long long)j0 < at0 + plan.deepest - sh.window);
+          }
           // (A warp whose wait has given up still joins the votes below,
           // after which the whole warpgroup leaves.)
           const int sb = at % C::NS;
@@ -1006,12 +1059,28 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             const uint64_t l2 = ptx::f2_pack(__uint_as_float(ql[n]), __uint_as_float(ql[n + 1]));
             x[n / 2] = ptx::fma2(ptx::add2(h2, l2), ptx::mul2(f.x, ks2), f.y);
           }
-          if (edge) {
+          if (kMasked && edge && sh.tree && (long long)j0 + key >= at0) {
+            // Keys of the nodes: bit r of each row's mask.
+            const long long r = (long long)j0 + key - at0;
+            const bool named = r < 32ll * a.tree_words;
+            const int word = named ? (int)(r >> 5) : 0;
+            const uint32_t bit = named ? 1u << (r & 31) : 0u;
+#pragma unroll
+            for (int n = 0; n < N; n += 2) {
+              const uint32_t m0 = __ldg(a.tree_mask + plan.mask[n] + word);
+              const uint32_t m1 = __ldg(a.tree_mask + plan.mask[n + 1] + word);
+              float u, v;
+              ptx::f2_unpack(x[n / 2], u, v);
+              x[n / 2] = ptx::f2_pack(m0 & bit ? u : neg_inf, m1 & bit ? v : neg_inf);
+            }
+          } else if (edge) {
             // Row n stands at at0 + token[n].
             const long long r = (long long)j0 + key - at0;
             const long long w = r + sh.window;
             const int lo = sh.causal ? (int)(r < kMaxCost ? (r > -1 ? r : -1) : kMaxCost) : -1;
-            const int hi = sh.window < 0 ? kMaxCost : (int)(w < kMaxCost ? (w > -1 ? w : -1) : kMaxCost);
+            const int hi = sh.window < 0 || (kMasked && j0 + key < sh.sinks)
+                               ? kMaxCost
+                               : (int)(w < kMaxCost ? (w > -1 ? w : -1) : kMaxCost);
 #pragma unroll
             for (int n = 0; n < N; n += 4) {
               const int4 o = *reinterpret_cast<const int4*>(plan.token + n);

@@ -84,6 +84,7 @@ FA_HD int checked_page(int id, int num_pages) { return id >= 0 && id < num_pages
 // window >= 0 bounds the keys before it.
 struct KeyRange {
   int lo, hi;
+  int sink;  // and the keys [0, sink), sink <= lo
 };
 FA_HD KeyRange key_range(int i0, int i1, int n, int len, int held, bool causal, int window) {
   KeyRange r;
@@ -96,6 +97,7 @@ FA_HD KeyRange key_range(int i0, int i1, int n, int len, int held, bool causal, 
   if (lo > hi) lo = hi;
   r.lo = (int)lo;
   r.hi = (int)hi;
+  r.sink = 0;
   return r;
 }
 
@@ -116,6 +118,10 @@ constexpr int kUnitCost = 7;
 struct AttnShape {
   int heads_k, group, rows;  // kv heads, query heads of one, rows of a tile
   int causal, window, held;  // held: positions of the page table
+  // Read by the kMasked forms below: first keys that stay visible behind the
+  // window, and whether the rows are nodes of a tree (every row then stands
+  // at the first of them or later, and any of their keys may be seen).
+  int sinks, tree;
 };
 FA_HD int token_of(const AttnShape& s, unsigned row) { return (int)(row / (unsigned)s.group); }
 
@@ -124,29 +130,54 @@ FA_HD int row_tiles(const AttnShape& s, int n) {
   return (int)(((unsigned)n * (unsigned)s.group + s.rows - 1) / (unsigned)s.rows);
 }
 // Keys of row tile t of a sequence with n query rows and len keys.
+template <bool kMasked = false>
 FA_HD KeyRange tile_keys(const AttnShape& s, int t, int n, int len) {
   const unsigned r0 = (unsigned)t * s.rows, all = (unsigned)n * s.group;
   unsigned r1 = r0 + s.rows;
   if (r1 > all) r1 = all;
-  return key_range(token_of(s, r0), token_of(s, r1 - 1), n, len, s.held, s.causal != 0, s.window);
+  const bool tree = kMasked && s.tree;
+  KeyRange k = key_range(tree ? 0 : token_of(s, r0), token_of(s, r1 - 1), n, len, s.held,
+                         !tree && s.causal != 0, s.window);
+  if (kMasked) k.sink = imin(s.sinks, k.lo);
+  return k;
 }
-// First key tile and number of key tiles; a unit without keys keeps one (all
-// masked), which writes its empty rows.
+// The key tiles of a unit, `count` of them: its n-th is tile n of the
+// sequence for n < head (the sinks'), first + n - head behind that.  (head = 0
+// where sinks and window leave no tile out.)  A unit without keys keeps one
+// tile (all masked), which writes its empty rows.
 struct TileRange {
-  int first, count;
+  int first, count, head;
 };
+template <bool kMasked = false>
 FA_HD TileRange key_tiles(const KeyRange& k) {
   TileRange t;
   t.first = k.lo / kTileKeys;
   t.count = k.hi > k.lo ? (int)(((unsigned)k.hi + kTileKeys - 1) / kTileKeys) - t.first : 1;
+  t.head = 0;
+  if (kMasked && k.sink > 0) {
+    const int sinks = (int)(((unsigned)k.sink + kTileKeys - 1) / kTileKeys);
+    if (k.hi <= k.lo) {  // (the window is past the keys that are held)
+      t.first = 0;
+      t.count = sinks;
+    } else if (sinks >= t.first) {
+      t.count += t.first;
+      t.first = 0;
+    } else {
+      t.head = sinks;
+      t.count += sinks;
+    }
+  }
   return t;
 }
+FA_HD int tile_of(const TileRange& t, int n) { return n < t.head ? n : t.first + n - t.head; }
 // Cost of all row tiles of one (sequence, head).
+template <bool kMasked = false>
 FA_HD long long head_cost(const AttnShape& s, int n, int len) {
   long long sum = 0;
   const int m = n > 0 ? row_tiles(s, n) : 0;
   FA_ROLLED
-  for (int t = 0; t < m; ++t) sum += kUnitCost + key_tiles(tile_keys(s, t, n, len)).count;
+  for (int t = 0; t < m; ++t)
+    sum += kUnitCost + key_tiles<kMasked>(tile_keys<kMasked>(s, t, n, len)).count;
   return sum;
 }
 
@@ -171,6 +202,7 @@ struct Segment {
   RowRange q;        // the sequence's query rows
   int len;           // its keys
   KeyRange keys;     // of the row tile
+  TileRange tiles;   // of the unit
   int tile0;         // first key tile of the segment (tile t: keys 128 t ..)
   int count;         // its key tiles
   int part_lo, unit_count;  // place of tile0 among the unit's tiles, and their number
@@ -200,7 +232,7 @@ FA_HD void walk_begin(SegmentWalk* w, int lo, int hi, int batch, const Before& b
 
 // The next segment, or false at the end of the range.  seq_of(b, &q, &len)
 // gives a sequence's query rows and keys.
-template <typename Before, typename SeqOf>
+template <bool kMasked = false, typename Before, typename SeqOf>
 FA_HD bool walk_next(SegmentWalk* w, const AttnShape& s, const Before& before, const SeqOf& seq_of,
                      Segment* g) {
   FA_ROLLED
@@ -211,13 +243,14 @@ FA_HD bool walk_next(SegmentWalk* w, const AttnShape& s, const Before& before, c
       seq_of(w->seq, &g->q, &g->len);
       const int in_seq = w->at - before(w->seq);
       // (The sequence's cost without the cap, so that no head is past the last.)
-      const int per_head = capped_cost(head_cost(s, g->q.n, g->len));
+      const int per_head = capped_cost(head_cost<kMasked>(s, g->q.n, g->len));
       w->head = (int)((unsigned)in_seq / (unsigned)per_head);
       int left = in_seq - w->head * per_head;
       w->row_tile = 0;
       FA_ROLLED
       for (;;) {
-        const int c = kUnitCost + key_tiles(tile_keys(s, w->row_tile, g->q.n, g->len)).count;
+        const int c =
+            kUnitCost + key_tiles<kMasked>(tile_keys<kMasked>(s, w->row_tile, g->q.n, g->len)).count;
         if (left < c) break;
         left -= c;
         ++w->row_tile;
@@ -229,14 +262,15 @@ FA_HD bool walk_next(SegmentWalk* w, const AttnShape& s, const Before& before, c
     g->seq = w->seq;
     g->head = w->head;
     g->row_tile = w->row_tile;
-    g->keys = tile_keys(s, w->row_tile, g->q.n, g->len);
-    const TileRange t = key_tiles(g->keys);
+    g->keys = tile_keys<kMasked>(s, w->row_tile, g->q.n, g->len);
+    const TileRange t = key_tiles<kMasked>(g->keys);
+    g->tiles = t;
     const int cost = kUnitCost + t.count;
     int n = cost - w->in_unit;
     if (n > w->end - w->at) n = w->end - w->at;
     const int lo = w->in_unit > kUnitCost ? w->in_unit - kUnitCost : 0;
     const int hi = w->in_unit + n > kUnitCost ? w->in_unit + n - kUnitCost : 0;
-    g->tile0 = t.first + lo;
+    g->tile0 = kMasked ? tile_of(t, lo) : t.first + lo;
     g->count = hi - lo;
     g->part_lo = lo;
     g->unit_count = t.count;

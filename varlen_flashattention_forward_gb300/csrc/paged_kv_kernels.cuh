@@ -11,98 +11,16 @@
 #pragma once
 
 #include <cstdint>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include "e4m3.cuh"
+#include "find_unit.cuh"
 #include "named_bar.cuh"
 #include "paged_index.h"
 #include "rope_row.cuh"
 #include "sm103_ptx.cuh"
 
 namespace fa {
-
-constexpr float kE4m3Max = 448.f;
-// Scales stay within 2^-64 .. 2^64: the attention's scores, and its sums of
-// weights relative to weight times V scale, then stay inside fp32 (where sums
-// meet, with root_ex2).
-constexpr int kScaleExpMax = 64;
-
-// Smallest power of two s with amax <= 448 s, clamped (amax finite, >= 0).
-__device__ __forceinline__ float scale_for(float amax) {
-  // amax / 512 = m 2^e with m in [0.5, 1), and 448 = 512 * 0.875.
-  int e;
-  const float m = frexpf(amax * (1.f / 512.f), &e);
-  if (m > 0.875f) ++e;
-  if (!(amax > 0.f)) e = -kScaleExpMax;
-  e = imin(imax(e, -kScaleExpMax), kScaleExpMax);
-  return ldexpf(1.f, e);
-}
-
-// Two fp32 values as e4m3 codes (round to nearest even, saturating at 448,
-// NaN kept): lo in bits 0..7.
-__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
-  uint16_t d;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-// Two e4m3 codes as f16x2 (exact).
-__device__ __forceinline__ uint32_t unpack_e4m3x2(uint32_t codes) {
-  uint32_t d;
-  const uint16_t c = (uint16_t)codes;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(c));
-  return d;
-}
-__device__ __forceinline__ float2 f16x2_floats(uint32_t h) {
-  float2 f;
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\t"
-      "cvt.f32.f16 %1, h;\n\t}"
-      : "=f"(f.x), "=f"(f.y)
-      : "r"(h));
-  return f;
-}
-
-// The sequence and the place within it of work unit x, where sequence b has
-// count(b) units, in order.  Called by the whole block (at most 1024 threads,
-// whole warps); found.seq is -1 if there is no such unit.
-struct FoundUnit {
-  int seq, at;
-};
-template <typename Count>
-__device__ __forceinline__ FoundUnit find_unit(int x, int batch, Count count) {
-  __shared__ int s_warp[32];
-  __shared__ FoundUnit s_found;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-  if (tid == 0) s_found.seq = -1;
-  long long before = 0;  // units of the sequences of earlier turns
-  for (int b0 = 0; b0 < batch; b0 += blockDim.x) {
-    const int b = b0 + tid;
-    const int c = b < batch ? count(b) : 0;
-    int sum = c;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += v;
-    }
-    if (lane == 31) s_warp[warp] = sum;
-    __syncthreads();
-    long long lo = before;
-    int all = 0;
-    for (int w = 0; w < warps; ++w) {
-      if (w < warp) lo += s_warp[w];
-      all += s_warp[w];
-    }
-    lo += sum - c;
-    if (x >= lo && x < lo + c) {
-      s_found.seq = b;
-      s_found.at = (int)(x - lo);
-    }
-    before += all;
-    __syncthreads();
-    if (before > x) break;
-  }
-  __syncthreads();
-  return s_found;
-}
 
 // ------------------------------------------------------------------ append
 struct KvAppendArgs {
