@@ -196,6 +196,45 @@ fa_status fa_varlen_fwd_strided(const void* q, long long q_row_stride, long long
                                 int window_right, void* out, float* lse, fa_stream_t stream);
 
 /*
+ * fa_varlen_fwd_masked -- fa_varlen_fwd_strided with two more masks.  Arguments,
+ * rules, launch shape (fa_varlen_fwd_plan's) and errors as there, and
+ *
+ *   sink_tokens   the first keys of each sequence, which stay visible to rows
+ *                 whose window has left them behind (attention sinks): row i at
+ *                 position p_i = i + (Lk - Lq) sees key j iff the causal bound
+ *                 or window_right allows it and j >= p_i - window_left or
+ *                 j < sink_tokens.  With window_left = -1 the number says
+ *                 nothing.
+ *   tree_mask     int32 [total_q, tree_words] or NULL with tree_words = 0: a
+ *                 sequence's Lq query rows are the nodes of a tree of drafted
+ *                 tokens, whose keys are the last Lq of its Lk, and bit p % 32
+ *                 of word p / 32 of row i says whether node i sees the key of
+ *                 node p (fa_draft_tree makes the masks).  Keys before the
+ *                 nodes' are seen by all of them, within the window: node i
+ *                 stands at position Lk - Lq + d_i, d_i its depth, the number
+ *                 of bits of its mask less one.  The nodes' own keys are seen by
+ *                 the bits alone.  Nodes from 32 * tree_words on, and bits past
+ *                 the last node, name no key.  causal is not used then and
+ *                 window_right is -1.
+ *
+ * The path of large trees: fa_paged_kv_gather, then this call (see
+ * fa_paged_attn for where the two cross).
+ *
+ * Host errors: as fa_varlen_fwd_strided; FA_ERR_INVALID_ARG also for a negative
+ * sink_tokens or tree_words, a mask that is missing and a window_right beside
+ * one, FA_ERR_UNSUPPORTED for one of more than 2^31 - 1 words.
+ */
+fa_status fa_varlen_fwd_masked(const void* q, long long q_row_stride, long long q_head_stride,
+                               const void* k, long long k_row_stride, long long k_head_stride,
+                               const void* v, long long v_row_stride, long long v_head_stride,
+                               const int* cu_seqlens_q, const int* cu_seqlens_k, int batch,
+                               int total_q, int total_k, int num_heads, int num_heads_k, int d_qk,
+                               int d_v, int max_seqlen_q, int max_seqlen_k, float softmax_scale,
+                               int causal, int window_left, int window_right, int sink_tokens,
+                               const int* tree_mask, int tree_words, void* out, float* lse,
+                               fa_stream_t stream);
+
+/*
  * fa_sparse_mla_decode -- one query row per token attending over top-k rows
  * gathered from a paged latent cache shared by all heads.  Defined by
  * [mla_sparse] (FlashAttnMLASparseFA4Backend, _fa4_varlen_scalars).

@@ -342,3 +342,187 @@ def test_masked_calls_in_a_graph(cuda_device):
         assert_close(o, lse, want)
         assert pos.cpu().tolist() == [now[b] - n + len(masked.path_of(trees[b], i)) - 1
                                       for b, n in enumerate(q_lens) for i in range(n)]
+
+
+# -------------------------------------------- the packed (bf16) attention
+def check_packed(q_lens, k_lens, H, Hk, d, dv=None, causal=True, wl=-1, wr=-1, sinks=0, trees=None,
+                 words=None, mask=None, seed=0, hints=True, strided=False, size=1.0, only=None):
+    """fa_varlen_fwd with the masks.  P is rounded to bf16 there for the
+    product with v: 2^-8 sum p |v| more than above.  only: heads compared."""
+    gen = torch.Generator().manual_seed(seed)
+    dv = dv or d
+    cu_q, cu_k = plain.cum(q_lens), plain.cum(k_lens)
+    q = (torch.randn((int(cu_q[-1]), H, d), generator=gen) * size).bfloat16()
+    kv = torch.randn((int(cu_k[-1]), Hk, d + dv), generator=gen).bfloat16()
+    k, v = kv[..., :d], kv[..., d:]
+    if trees is not None:
+        mask = masked.tree_masks(trees, words or max(1, -(-max(q_lens) // 32)))
+    kvd = dev(kv)
+    kd, vd = kvd[..., :d], kvd[..., d:]
+    if not strided:
+        kd, vd = kd.contiguous(), vd.contiguous()
+    o, lse = fa.fa_varlen_fwd(dev(q), kd, vd, dev(cu_q), dev(cu_k), max(q_lens) if hints else 0,
+                              max(k_lens) if hints else 0, causal=causal, window_left=wl,
+                              window_right=wr, sink_tokens=sinks,
+                              tree_mask=None if mask is None else dev(mask), return_lse=True)
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status() == fa.FA_OK
+    rows = None if mask is None else mask.tolist()
+    got_o, got_l = o.cpu().double(), lse.cpu().double()
+    for b, (n, length) in enumerate(zip(q_lens, k_lens)):
+        seen = [masked.seen_keys(i, n, length, length, causal, wl, wr, sinks,
+                                 None if rows is None else rows[int(cu_q[b]) + i])
+                for i in range(n)]
+        if not n:
+            continue
+        seen = torch.stack(seen)
+        for h in range(H) if only is None else only:
+            kh = k[cu_k[b]:cu_k[b + 1], h // (H // Hk)].double()
+            vh = v[cu_k[b]:cu_k[b + 1], h // (H // Hk)].double()
+            qh = q[cu_q[b]:cu_q[b + 1], h].double()
+            x = (qh @ kh.t() * d ** -0.5).masked_fill(~seen, -torch.inf)
+            l = torch.logsumexp(x, 1) if length else torch.full((n,), -torch.inf)
+            empty = ~seen.any(1)
+            p = torch.exp(x - torch.where(empty, 0.0, l)[:, None])
+            dx = 2.0 ** -15 * ((qh.abs() @ kh.abs().t()) * d ** -0.5).masked_fill(~seen, 0)
+            dx = dx.amax(1) if length else torch.zeros(n)
+            want, w = p @ vh, p @ vh.abs()
+            tol = 2.0 ** -8 * want.abs() + (2 * dx[:, None] + 2.0 ** -8 + 2.0 ** -10) * w + 1e-30
+            at = slice(int(cu_q[b]), int(cu_q[b + 1]))
+            assert ((got_o[at, h] - want).abs() <= tol).all(), (b, h)
+            assert (got_l[h, at][empty] == -torch.inf).all() and (got_o[at, h][empty] == 0).all()
+            diff = (got_l[h, at] - l).abs()[~empty]
+            assert (diff <= (dx + 2.0 ** -20 * (1 + l.abs()))[~empty]).all(), (b, h)
+    return o, lse
+
+
+DIMS = [(64, 64), (72, 72), (80, 80), (96, 96), (128, 128), (192, 128)]
+
+
+@pytest.mark.parametrize("d,dv", DIMS)
+@pytest.mark.parametrize("wl,sinks", [(100, 4), (0, 1), (300, 130), (128, 257), (1, 10000)])
+def test_packed_sinks(cuda_device, d, dv, wl, sinks):
+    check_packed([700, 1, 129, 0, 260], [700, 600, 129, 5, 900], 4, 4, d, dv, wl=wl, sinks=sinks,
+                 seed=d + wl)
+
+
+@pytest.mark.parametrize("H,Hk", [(8, 2), (8, 1), (32, 2)])
+@pytest.mark.parametrize("q_lens,k_lens", [([1, 1, 3], [900, 64, 500]), ([40, 17], [1000, 17]),
+                                           ([200], [777])])
+def test_packed_sinks_of_grouped_heads(cuda_device, H, Hk, q_lens, k_lens):
+    for d, dv in ((64, 64), (128, 128)):
+        check_packed(q_lens, k_lens, H, Hk, d, dv, wl=150, sinks=5, seed=H)
+
+
+def test_packed_sinks_not_causal(cuda_device):
+    for wr in (-1, 0, 40):
+        check_packed([300, 65], [300, 900], 2, 2, 80, causal=False, wl=70, wr=wr, sinks=9, seed=wr + 1)
+
+
+def test_packed_sinks_of_short_segments_and_more_rows_than_keys(cuda_device):
+    lens = [1 + 7 * i % 64 for i in range(40)]
+    check_packed(lens, lens, 2, 2, 64, wl=9, sinks=3, seed=1)
+    check_packed([100, 70], [30, 70], 2, 1, 64, wl=9, sinks=3, seed=2)
+
+
+@pytest.mark.parametrize("d,dv", [(64, 64), (128, 128), (192, 128)])
+def test_packed_sinks_split_over_clusters(cuda_device, d, dv):
+    # One item's key tiles over several CTAs, the gap inside a part or not.
+    for wl, sinks in ((8000, 4), (12000, 3000), (2500, 140)):
+        assert fa.fa_varlen_fwd_plan(1, 64, 16384, 2, 2, d, dv, 64, 16384, True, wl)[1] > 1
+        check_packed([64], [16384], 2, 2, d, dv, wl=wl, sinks=sinks, seed=wl)
+
+
+def test_packed_sinks_say_nothing_without_a_window(cuda_device):
+    a = check_packed([300], [500], 2, 2, 64, sinks=7, seed=3)
+    b = check_packed([300], [500], 2, 2, 64, seed=3)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("d,dv", DIMS)
+@pytest.mark.parametrize("wl,sinks", [(-1, 0), (100, 5)])
+def test_packed_trees(cuda_device, d, dv, wl, sinks):
+    q_lens = [3, 70, 0, 300, 1]
+    check_packed(q_lens, [130, 70, 9, 900, 600], 4, 2, d, dv, wl=wl, sinks=sinks,
+                 trees=trees_of(q_lens, d, chain=0.7), seed=d, strided=d == 128)
+
+
+@pytest.mark.parametrize("ctx", [0, 1, 31, 32, 63, 97, 127, 128, 400])
+def test_packed_tree_contexts(cuda_device, ctx):
+    for n in (2, 33, 64, 150):
+        check_packed([n], [ctx + n], 8, 2, 64, trees=trees_of([n], n + ctx), wl=200, sinks=1, seed=n)
+
+
+def test_packed_masks_of_any_bits(cuda_device):
+    gen = torch.Generator().manual_seed(25)
+    q_lens = [5, 140, 3]
+    for words in (1, 2, 5, 9):
+        mask = torch.randint(-2 ** 31, 2 ** 31, (148, words), generator=gen).int()
+        mask[0], mask[1], mask[145] = 0, -1, 0
+        for wl in (-1, 30):
+            check_packed(q_lens, [5, 300, 2], 4, 2, 64, mask=mask, wl=wl, sinks=2, seed=26)
+
+
+def test_packed_trees_split_over_clusters_and_many_sequences(cuda_device):
+    check_packed([60], [16384], 8, 2, 128, trees=trees_of([60], 6), seed=4)
+    q_lens = [1 + i % 5 for i in range(2100)]  # two launches
+    check_packed(q_lens, [n + 3 * i % 50 for i, n in enumerate(q_lens)], 1, 1, 64,
+                 trees=trees_of(q_lens, 7), seed=5)
+
+
+def test_packed_large_tree_after_the_gather(cuda_device):
+    # The path of large trees, against the paged attention of the same rows.
+    gen = torch.Generator().manual_seed(34)
+    q_lens, lens = [90, 61], [1000, 300]
+    pages, num = plain.make_pages(lens, gen)
+    (kc, ks), (vc, vs) = (plain.make_cache(lens, pages, num, 2, 128, gen) for _ in range(2))
+    q = torch.randn((151, 8, 128), generator=gen).bfloat16()
+    trees = trees_of(q_lens, 8)
+    qd, kcd, vcd, ksd, vsd, cu, ld, pd = dev(q, kc, vc, ks, vs, plain.cum(q_lens), i32(lens), pages)
+    mask, _ = fa.fa_draft_tree(dev(i32([p for t in trees for p in t])), cu, ld, max_nodes=90)
+    cu_k = dev(plain.cum(lens))
+    k, v = fa.fa_paged_kv_gather(kcd, vcd, ksd, vsd, cu_k, pd, 1300)
+    kw = dict(window_left=400, sink_tokens=3, tree_mask=mask, return_lse=True)
+    a = fa.fa_varlen_fwd(qd, k, v, cu, cu_k, 90, 1000, **kw)
+    b = fa.fa_paged_attn(qd, kcd, vcd, ksd, vsd, cu, ld, pd, **kw)
+    want = masked.paged_attention(q, kc, vc, ks, vs, [0, 90, 151], lens, pages, 128 ** -0.5, True,
+                                  400, 3, masked.tree_masks(trees, 3))
+    assert_close(*b, want)
+    wide = (want[0], want[1], want[2] * 5, want[3])  # (2^-8 sum p |v| more, see check_packed)
+    assert_close(*a, wide)
+
+
+def test_packed_masked_wait_limit_runs_out_then_recovers(cuda_device):
+    gen = torch.Generator().manual_seed(35)
+    q, k, v = (torch.randn((2000, 4, 64), generator=gen).bfloat16().cuda() for _ in range(3))
+    cu = dev(i32([0, 2000]))
+    kw = dict(causal=True, window_left=300, sink_tokens=4)
+    want = fa.fa_varlen_fwd(q, k, v, cu, cu, 2000, 2000, **kw)
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status() == fa.FA_OK
+    fa.fa_set_wait_limit_ns(2000)
+    try:
+        fa.fa_varlen_fwd(q, k, v, cu, cu, 2000, 2000, **kw)
+        assert fa.fa_get_device_status() == fa.FA_ERR_DEVICE_TIMEOUT
+    finally:
+        fa.fa_set_wait_limit_ns(0)
+    got = fa.fa_varlen_fwd(q, k, v, cu, cu, 2000, 2000, **kw)
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status() == fa.FA_OK and torch.equal(got, want)
+
+
+def test_packed_rows_behind_the_last_sequence_and_malformed_cu_seqlens(cuda_device):
+    gen = torch.Generator().manual_seed(36)
+    q, k, v = (torch.randn((200, 2, 64), generator=gen).bfloat16().cuda() for _ in range(3))
+    mask = dev(torch.randint(-2 ** 31, 2 ** 31, (200, 3), generator=gen).int())
+    for cu_q, cu_k in (([0, 90, 150], [0, 200, 200]), ([-5, 300, 20], [7, 3, 400]),
+                       ([50, 20, 60], [0, 2 ** 31 - 1, 9])):
+        for tree in (None, mask):
+            out = torch.full((202, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+            fa.fa_varlen_fwd(q, k, v, *dev(i32(cu_q), i32(cu_k)), causal=True, window_left=20,
+                             sink_tokens=5, tree_mask=tree, out=out[1:-1])
+            torch.cuda.synchronize()
+            assert fa.fa_get_device_status() == fa.FA_OK
+            assert (out[0] == 7).all() and (out[-1] == 7).all()
+            if cu_q[0] == 0:
+                assert (out[151:] == 7).all()

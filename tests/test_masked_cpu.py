@@ -176,3 +176,41 @@ def test_segments_cover_every_seen_tile_once(probe):
                     else:
                         assert at == 1
         assert not got
+
+
+# ------------------------------------------------------- packed attention
+def packed(lib, **kw):
+    a = dict(q=P(0x1000), qr=256, qh=64, k=P(0x2000), kr=256, kh=64, v=P(0x3000), vr=256, vh=64,
+             cq=P(0x4000), ck=P(0x5000), batch=2, total_q=10, total_k=10, H=4, Hk=4, dqk=64, dv=64,
+             mq=0, mk=0, scale=0.125, causal=1, wl=5, wr=-1, sinks=4, mask=P(0x7000), words=1,
+             out=P(0x6000), lse=None)
+    a.update(kw)
+    return lib.fa_varlen_fwd_masked(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(sinks=-1), INV), (dict(words=-1), INV), (dict(mask=None), INV), (dict(mask=P(0x7001)), INV),
+    (dict(wr=0), INV), (dict(words=2 ** 30), UNS), (dict(q=None), INV), (dict(wl=-2), INV),
+    (dict(dqk=100, dv=100), UNS), (dict(kh=60), INV), (dict(H=6), INV),
+])
+def test_masked_varlen_refusals(lib, kw, expect):
+    assert packed(lib, **kw) == expect
+
+
+def test_valid_packed_calls_fail_only_for_want_of_a_gpu(lib):
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    none = (fa.FA_ERR_LAUNCH, fa.FA_ERR_ARCH)
+    assert packed(lib) in none and packed(lib, words=0, mask=None, wr=3) in none
+    assert packed(lib, total_q=0, q=None, out=None, mask=None) in none
+
+
+def test_python_refuses_packed_masks(lib):
+    q = torch.zeros((3, 2, 64), dtype=torch.bfloat16)
+    cu = torch.tensor([0, 3], dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        fa.fa_varlen_fwd(q, q, q, cu, cu, window_left=1, sink_tokens=1)
+    for mask in (torch.zeros((2, 1), dtype=torch.int32), torch.zeros((3, 1)),
+                 torch.zeros((3, 0), dtype=torch.int32)):
+        with pytest.raises((TypeError, ValueError)):
+            fa.fa_varlen_fwd(q, q, q, cu, cu, tree_mask=mask)

@@ -10,7 +10,7 @@ Entry points (same names as the C ABI):
   fa_varlen_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
                 max_seqlen_k, softmax_scale, causal=False, window_left=-1,
                 window_right=-1, out=None, lse=None, return_lse=False,
-                stream=None)
+                stream=None, sink_tokens=0, tree_mask=None)
   fa_varlen_fwd_plan(batch, total_q, total_k, num_heads, num_heads_k, d_qk, d_v,
                      max_seqlen_q=0, max_seqlen_k=0, causal=False, window_left=-1,
                      window_right=-1)
@@ -58,7 +58,8 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libfa_gb300.so")
 
 # Exported C symbols (kept in sync with include/fa_gb300.h; a CPU test checks).
-EXPORTS = ("fa_varlen_fwd", "fa_varlen_fwd_plan", "fa_varlen_fwd_strided", "fa_sparse_mla_decode",
+EXPORTS = ("fa_varlen_fwd", "fa_varlen_fwd_plan", "fa_varlen_fwd_strided", "fa_varlen_fwd_masked",
+           "fa_sparse_mla_decode",
            "fa_sparse_mla_decode_plan", "fa_sparse_mla_decode_noalloc", "fa_merge_attn_states",
            "fa_qk_norm_rope", "fa_paged_kv_append", "fa_paged_attn", "fa_paged_attn_plan",
            "fa_paged_attn_masked", "fa_draft_tree", "fa_paged_kv_gather", "fa_get_device_status",
@@ -92,6 +93,10 @@ def load_library():
                                           i32, i32, i32, i32, i32, i32, i32, i32, f32, i32,
                                           i32, i32, p, p, p]
     lib.fa_varlen_fwd_strided.restype = i32
+    lib.fa_varlen_fwd_masked.argtypes = [p, i64, i64, p, i64, i64, p, i64, i64, p, p, i32, i32, i32,
+                                         i32, i32, i32, i32, i32, i32, f32, i32, i32, i32, i32, p,
+                                         i32, p, p, p]
+    lib.fa_varlen_fwd_masked.restype = i32
     lib.fa_sparse_mla_decode.argtypes = [p, p, p, p, i32, i32, i32, i32, i32,
                                          f32, p, p, p]
     lib.fa_sparse_mla_decode.restype = i32
@@ -182,7 +187,7 @@ def _check(t, name, dtype, ndim, view=False):
 def fa_varlen_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q=0,
                   max_seqlen_k=0, softmax_scale=None, causal=False,
                   window_left=-1, window_right=-1, out=None, lse=None,
-                  return_lse=False, stream=None):
+                  return_lse=False, stream=None, sink_tokens=0, tree_mask=None):
     """Varlen attention forward; see fa_varlen_fwd in include/fa_gb300.h.
 
     q [total_q, H, d_qk], k [total_k, H_k, d_qk], v [total_k, H_k, d_v] bf16
@@ -192,6 +197,11 @@ def fa_varlen_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q=0,
     contiguous last dimension (for example V taken out of a combined
     [tokens, heads, nope + v] buffer); they then go through
     fa_varlen_fwd_strided.
+
+    sink_tokens: the first keys of a sequence that stay visible behind its
+    window.  tree_mask [total_q, words] int32: the query rows are nodes of
+    drafted trees and see the keys of the nodes their bits name (fa_draft_tree),
+    and all keys before; causal is not used then (fa_varlen_fwd_masked).
     """
     import torch
     lib = load_library()
@@ -208,15 +218,32 @@ def fa_varlen_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q=0,
         raise ValueError("cu_seqlens_q and cu_seqlens_k differ in length")
     if softmax_scale is None:
         softmax_scale = d_qk ** -0.5
-    if out is None:
-        out = torch.empty((total_q, H, d_v), dtype=torch.bfloat16, device=q.device)
-    else:
-        _check(out, "out", torch.bfloat16, 3)
-    if lse is None and return_lse:
-        lse = torch.empty((H, total_q), dtype=torch.float32, device=q.device)
-    if lse is not None:
-        _check(lse, "lse", torch.float32, 2)
-    if q.is_contiguous() and k.is_contiguous() and v.is_contiguous():
+    masked, here = sink_tokens != 0 or tree_mask is not None, _NO_CONTEXT
+    if masked:
+        words = _tree_words(tree_mask, total_q)
+        index, here = _device(stream, q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse, tree_mask)
+    with here:
+        if out is None:
+            out = torch.empty((total_q, H, d_v), dtype=torch.bfloat16, device=q.device)
+        else:
+            _check(out, "out", torch.bfloat16, 3)
+        if lse is None and return_lse:
+            lse = torch.empty((H, total_q), dtype=torch.float32, device=q.device)
+        if lse is not None:
+            _check(lse, "lse", torch.float32, 2)
+    if masked:
+        _shape(out, "out", (total_q, H, d_v))
+        if lse is not None:
+            _shape(lse, "lse", (H, total_q))
+        with here:
+            st = lib.fa_varlen_fwd_masked(
+                _ptr(q), q.stride(0), q.stride(1), _ptr(k), k.stride(0), k.stride(1),
+                _ptr(v), v.stride(0), v.stride(1), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k),
+                batch, total_q, total_k, H, H_k, d_qk, d_v, int(max_seqlen_q),
+                int(max_seqlen_k), float(softmax_scale), int(bool(causal)),
+                _window(window_left), _window(window_right), _sinks(sink_tokens), _p(tree_mask),
+                words, _ptr(out), _ptr(lse), _raw_stream(index))
+    elif q.is_contiguous() and k.is_contiguous() and v.is_contiguous():
         st = lib.fa_varlen_fwd(
             _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k),
             batch, total_q, total_k, H, H_k, d_qk, d_v, int(max_seqlen_q),

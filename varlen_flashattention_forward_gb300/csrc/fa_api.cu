@@ -47,6 +47,18 @@ cudaError_t plan_varlen_128_128(const VarlenLaunch&, int*, int*);
 cudaError_t launch_varlen_192_128(const VarlenMaps&, const VarlenArgs&, const VarlenLaunch&,
                                  cudaStream_t);
 cudaError_t plan_varlen_192_128(const VarlenLaunch&, int*, int*);
+cudaError_t launch_masked_64_64(const VarlenMaps&, const VarlenArgs&, const VarlenLaunch&,
+                                 cudaStream_t);
+cudaError_t launch_masked_72_72(const VarlenMaps&, const VarlenArgs&, const VarlenLaunch&,
+                                 cudaStream_t);
+cudaError_t launch_masked_80_80(const VarlenMaps&, const VarlenArgs&, const VarlenLaunch&,
+                                 cudaStream_t);
+cudaError_t launch_masked_96_96(const VarlenMaps&, const VarlenArgs&, const VarlenLaunch&,
+                                 cudaStream_t);
+cudaError_t launch_masked_128_128(const VarlenMaps&, const VarlenArgs&, const VarlenLaunch&,
+                                 cudaStream_t);
+cudaError_t launch_masked_192_128(const VarlenMaps&, const VarlenArgs&, const VarlenLaunch&,
+                                 cudaStream_t);
 }  // namespace fa
 
 // Device status word: bit 0 = a pipeline wait ran out of time.
@@ -262,6 +274,21 @@ extern "C" fa_status fa_varlen_fwd_strided(
     int total_q, int total_k, int num_heads, int num_heads_k, int d_qk, int d_v,
     int max_seqlen_q, int max_seqlen_k, float softmax_scale, int causal, int window_left,
     int window_right, void* out, float* lse, fa_stream_t stream) {
+  return fa_varlen_fwd_masked(q, q_row_stride, q_head_stride, k, k_row_stride, k_head_stride, v,
+                              v_row_stride, v_head_stride, cu_seqlens_q, cu_seqlens_k, batch,
+                              total_q, total_k, num_heads, num_heads_k, d_qk, d_v, max_seqlen_q,
+                              max_seqlen_k, softmax_scale, causal, window_left, window_right, 0,
+                              nullptr, 0, out, lse, stream);
+}
+
+extern "C" fa_status fa_varlen_fwd_masked(
+    const void* q, long long q_row_stride, long long q_head_stride, const void* k,
+    long long k_row_stride, long long k_head_stride, const void* v, long long v_row_stride,
+    long long v_head_stride, const int* cu_seqlens_q, const int* cu_seqlens_k, int batch,
+    int total_q, int total_k, int num_heads, int num_heads_k, int d_qk, int d_v,
+    int max_seqlen_q, int max_seqlen_k, float softmax_scale, int causal, int window_left,
+    int window_right, int sink_tokens, const int* tree_mask, int tree_words, void* out, float* lse,
+    fa_stream_t stream) {
   // ---- host validation (before any CUDA call); q and out may be null only
   // when they have no rows
   if ((total_q > 0 && (!q || !out)) || !cu_seqlens_q || !cu_seqlens_k) return FA_ERR_INVALID_ARG;
@@ -270,6 +297,11 @@ extern "C" fa_status fa_varlen_fwd_strided(
       num_heads % num_heads_k != 0)
     return FA_ERR_INVALID_ARG;
   if (window_left < -1 || window_right < -1) return FA_ERR_INVALID_ARG;
+  if (sink_tokens < 0 || tree_words < 0 || !aligned(tree_mask, 4) ||
+      (tree_words > 0 && ((total_q > 0 && !tree_mask) || window_right >= 0)))
+    return FA_ERR_INVALID_ARG;
+  // (Sinks say nothing without a window.)
+  const bool tree = tree_words > 0, masked = tree || (sink_tokens > 0 && window_left >= 0);
   if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale)) return FA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16) || (k && !aligned(k, 16)) || (v && !aligned(v, 16)) ||
       !aligned(cu_seqlens_q, 4) || !aligned(cu_seqlens_k, 4) || (lse && !aligned(lse, 4)))
@@ -277,12 +309,18 @@ extern "C" fa_status fa_varlen_fwd_strided(
   typedef cudaError_t (*Launcher)(const fa::VarlenMaps&, const fa::VarlenArgs&,
                                   const fa::VarlenLaunch&, cudaStream_t);
   Launcher launch = nullptr;
-  if (d_qk == 64 && d_v == 64) launch = fa::launch_varlen_64_64;
-  else if (d_qk == 72 && d_v == 72) launch = fa::launch_varlen_72_72;
-  else if (d_qk == 80 && d_v == 80) launch = fa::launch_varlen_80_80;
-  else if (d_qk == 96 && d_v == 96) launch = fa::launch_varlen_96_96;
-  else if (d_qk == 128 && d_v == 128) launch = fa::launch_varlen_128_128;
-  else if (d_qk == 192 && d_v == 128) launch = fa::launch_varlen_192_128;
+  if (d_qk == 64 && d_v == 64)
+    launch = masked ? fa::launch_masked_64_64 : fa::launch_varlen_64_64;
+  else if (d_qk == 72 && d_v == 72)
+    launch = masked ? fa::launch_masked_72_72 : fa::launch_varlen_72_72;
+  else if (d_qk == 80 && d_v == 80)
+    launch = masked ? fa::launch_masked_80_80 : fa::launch_varlen_80_80;
+  else if (d_qk == 96 && d_v == 96)
+    launch = masked ? fa::launch_masked_96_96 : fa::launch_varlen_96_96;
+  else if (d_qk == 128 && d_v == 128)
+    launch = masked ? fa::launch_masked_128_128 : fa::launch_varlen_128_128;
+  else if (d_qk == 192 && d_v == 128)
+    launch = masked ? fa::launch_masked_192_128 : fa::launch_varlen_192_128;
   if (!launch) return FA_ERR_UNSUPPORTED;
   if (!fa::settle_view(total_q, num_heads, d_qk, &q_row_stride, &q_head_stride) ||
       (total_k > 0 &&
@@ -290,7 +328,8 @@ extern "C" fa_status fa_varlen_fwd_strided(
         !fa::settle_view(total_k, num_heads_k, d_v, &v_row_stride, &v_head_stride))))
     return FA_ERR_INVALID_ARG;
   // Token indices are 32-bit in the kernel.
-  if ((int64_t)total_q * num_heads > INT32_MAX || (int64_t)total_k * num_heads_k > INT32_MAX)
+  if ((int64_t)total_q * num_heads > INT32_MAX || (int64_t)total_k * num_heads_k > INT32_MAX ||
+      (int64_t)total_q * tree_words > INT32_MAX)
     return FA_ERR_UNSUPPORTED;
 
   DeviceInfo* dev = nullptr;
@@ -346,7 +385,10 @@ extern "C" fa_status fa_varlen_fwd_strided(
   // window past 2^30 is as good as 2^30 (q and out of that many rows alone take
   // 256 GB), and keeps the kernel's sums with positions within 32 bits.
   args.wl = std::min(window_left, 1 << 30);
-  args.wr = causal ? 0 : std::min(window_right, 1 << 30);
+  args.wr = tree ? -1 : causal ? 0 : std::min(window_right, 1 << 30);
+  args.sinks = sink_tokens;
+  args.tree_words = tree_words;
+  args.tree = tree ? tree_mask : nullptr;
   args.out = static_cast<uint16_t*>(out);
   args.lse = lse;
   args.status = dev->status;

@@ -56,6 +56,7 @@
 #include <atomic>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -235,6 +236,12 @@ struct VarlenArgs {
   // heads at once.  0 = one head per tile.
   int pack_shift;
   uint64_t wait_limit_ns;  // pipeline wait limit (bounded waits)
+  // kMasked only: the first keys of a sequence that stay visible behind the
+  // window, and the rows' masks as nodes of a tree ([total_q, tree_words], bit
+  // p: the row sees the key of node p, the sequence's last lq keys), or null.
+  int sinks;
+  int tree_words;
+  const int* tree;
 };
 
 struct VarlenMaps {
@@ -390,6 +397,17 @@ struct WorkItem {
 // Row r of a work item (0 .. 255) is token row0 + (r >> pack_shift) of the
 // sequence and query head head + r % P.
 static_assert(sizeof(WorkItem) == 48, "work item slot size");
+// With sinks an item's key tiles have a gap: its j-th is tile_lo + j, and from
+// j = gap_at on `gap` more.
+struct MaskedItem : WorkItem {
+  int gap_at, gap;
+};
+template <bool kMasked>
+using ItemOf = std::conditional_t<kMasked, MaskedItem, WorkItem>;
+__device__ __forceinline__ int key_tile(const WorkItem& w, int j) { return w.tile_lo + j; }
+__device__ __forceinline__ int key_tile(const MaskedItem& w, int j) {
+  return w.tile_lo + j + (j >= w.gap_at ? w.gap : 0);
+}
 
 // Decoded work items, published by the producer (which runs ahead of the
 // other roles) into a ring in shared memory: decoding an item (a search of
@@ -399,12 +417,13 @@ static_assert(sizeof(WorkItem) == 48, "work item slot size");
 // once the list is built.
 constexpr int kItemSlots = 4;
 constexpr int kItemReaders = 2 + 8;  // the issuer warps and the softmax warps
+template <bool kMasked>
 struct ItemRing {
-  WorkItem slot[kItemSlots];
+  ItemOf<kMasked> slot[kItemSlots];
   uint64_t full[kItemSlots];
   uint64_t free_[kItemSlots];
 };
-static_assert(sizeof(ItemRing) <= 4 * kVarlenThreads, "item ring fits the scan scratch");
+static_assert(sizeof(ItemRing<true>) <= 4 * kVarlenThreads, "item ring fits the scan scratch");
 
 // Short segments: consecutive sequences of 1..kPackMaxLen query rows with as
 // many keys and the same token offsets in Q and K (self-attention over one
@@ -542,6 +561,9 @@ __device__ __forceinline__ int seq_hi(const int* cu, int b, int total) {
   return min(max(__ldg(cu + b + 1), seq_lo(cu, b, total)), total);
 }
 
+// kPacks: short segments share units (not under the masks of kMasked kernels,
+// which go by a row's place in its own sequence).
+template <bool kPacks>
 static __device__ __noinline__ void build_work_list(const int* cu_q, const int* cu_k, int B,
                                                     int total_q, int total_k,
                                                     int num_heads, int pack_shift, int* s_prefix,
@@ -557,7 +579,7 @@ static __device__ __noinline__ void build_work_list(const int* cu_q, const int* 
   for (int b = tid; b < B; b += kVarlenThreads) {
     const int q0 = seq_lo(cu_q, b, total_q), k0 = seq_lo(cu_k, b, total_k);
     const int lq = seq_hi(cu_q, b, total_q) - q0, lk = seq_hi(cu_k, b, total_k) - k0;
-    const bool pack = pack_shift == 0 && lq >= 1 && lq <= kPackMaxLen && lk == lq && k0 == q0;
+    const bool pack = kPacks && pack_shift == 0 && lq >= 1 && lq <= kPackMaxLen && lk == lq && k0 == q0;
     s_prefix[b] = pack ? q0 / kPackBlock : -1;
     s_sorted[b] = lk;
     t_lq[b] = lq;
@@ -664,7 +686,8 @@ static __device__ __noinline__ void build_work_list(const int* cu_q, const int* 
   __syncthreads();
 }
 
-__device__ __forceinline__ WorkItem decode_item(int it, const VarlenArgs& a,
+template <bool kMasked>
+__device__ __forceinline__ ItemOf<kMasked> decode_item(int it, const VarlenArgs& a,
                                                 const int* s_prefix, const int* s_sorted,
                                                 int split, int pack_shift) {
   // Largest sorted position p with prefix[p] <= it (skips empty sequences).
@@ -675,7 +698,7 @@ __device__ __forceinline__ WorkItem decode_item(int it, const VarlenArgs& a,
   }
   const int unit = s_sorted[lo];
   const int r = it - s_prefix[lo];
-  WorkItem w;
+  ItemOf<kMasked> w;
   w.b0 = unit & ((1 << kUnitShift) - 1);
   w.nb = unit >> kUnitShift;
   // Read through the read-only data cache: every role decodes every item,
@@ -698,7 +721,9 @@ __device__ __forceinline__ WorkItem decode_item(int it, const VarlenArgs& a,
   const int row_end = min(w.lq, w.row0 + (1 << tshift));
   w.n_qt = (((row_end - w.row0) << pack_shift) + kBM - 1) / kBM;
   const int off = w.lk - w.lq;
-  const int key_lo = a.wl >= 0 ? max(0, w.row0 + off - a.wl) : 0;
+  // (A tree's nodes all stand at its first one or later.)
+  const int first = kMasked && a.tree ? 0 : w.row0;
+  const int key_lo = a.wl >= 0 ? max(0, first + off - a.wl) : 0;
   const int key_hi = a.wr >= 0 ? min(w.lk, row_end + off + a.wr) : w.lk;
   if (key_hi <= key_lo) {
     w.tile_lo = 0;
@@ -707,12 +732,35 @@ __device__ __forceinline__ WorkItem decode_item(int it, const VarlenArgs& a,
     w.tile_lo = key_lo / kBN;
     w.n_kv = (key_hi + kBN - 1) / kBN - w.tile_lo;
   }
+  if constexpr (kMasked) {
+    w.gap_at = 0x7fffffff;
+    w.gap = 0;
+    const int sinks = min(a.sinks, key_lo);
+    if (w.n_kv > 0 && sinks > 0) {
+      const int head = (sinks + kBN - 1) / kBN;
+      if (head < w.tile_lo) {
+        w.gap_at = head;
+        w.gap = w.tile_lo - head;
+        w.n_kv += head;
+      } else {
+        w.n_kv += w.tile_lo;
+      }
+      w.tile_lo = 0;
+    }
+  }
   if (split > 1) {
     // Split-KV: this CTA's part of the item's KV tiles (its rank in the
     // cluster; parts differ in size by at most one tile, and may be empty).
     const int part = (int)blockIdx.x % split;
     const int p0 = w.n_kv * part / split;
     const int p1 = w.n_kv * (part + 1) / split;
+    if constexpr (kMasked) {
+      if (p0 >= w.gap_at) {  // past the gap
+        w.tile_lo += w.gap;
+        w.gap = 0;
+      }
+      w.gap_at = max(w.gap_at - p0, 0);
+    }
     w.tile_lo += p0;
     w.n_kv = p1 - p0;
   }
@@ -740,6 +788,23 @@ __device__ __forceinline__ void tile_kv_range(const WorkItem& w, int t, int wl, 
     jhi = khi <= 0 ? 0 : min(w.n_kv, (khi + kBN - 1) / kBN - w.tile_lo);
   }
   if (jhi < jlo) jhi = jlo;
+}
+// The same under the masks: from the first tile on, for the sinks.
+__device__ __forceinline__ void masked_kv_range(const MaskedItem& w, int t, const VarlenArgs& a,
+                                                int pack_shift, int& jlo, int& jhi) {
+  jlo = 0;
+  jhi = w.n_kv;
+  if (a.wr < 0 || w.n_kv == 0) return;
+  const int r1 = min(w.lq, w.row0 + (((t + 1) * kBM) >> pack_shift)) - 1;  // last token
+  const int khi = min(w.lk, r1 + (w.lk - w.lq) + a.wr + 1);                // keys < khi
+  const int tiles = khi <= 0 ? 0 : (khi + kBN - 1) / kBN - w.tile_lo;      // without the gap
+  jhi = min(w.n_kv, max(min(tiles, w.gap_at), tiles - w.gap));
+  if (jhi < 0) jhi = 0;
+}
+
+// Bits [0, n) of a word, for any n.
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
 }
 
 // ------------------------------------------------------------ split-KV combine
@@ -778,7 +843,7 @@ static __device__ __noinline__ void split_combine(const VarlenArgs args, uint8_t
   ptx::cluster_arrive_release();
   ptx::cluster_wait_acquire();  // every part is in its CTA's shared memory
   if (it < total_items) {
-    const WorkItem w = decode_item(it, args, s_prefix, s_sorted, S, args.pack_shift);
+    const WorkItem w = decode_item<false>(it, args, s_prefix, s_sorted, S, args.pack_shift);
     const int rows = min(kRowsPerItem, (w.lq - w.row0) << args.pack_shift);
     const int pmask = (1 << args.pack_shift) - 1;
     const int r_lo = rows * rank / S, r_hi = rows * (rank + 1) / S;
@@ -847,11 +912,14 @@ static __device__ __noinline__ void split_combine(const VarlenArgs args, uint8_t
 // launched in clusters of args.split CTAs) and GQA head-group packing
 // (args.pack_shift > 0); the other one compiles with neither (split 1,
 // one head per tile as constants): their extra state would otherwise cost
-// the pipeline loops registers.
-template <int D_QK, int D_V, bool kGeneral>
+// the pipeline loops registers.  kMasked: sinks behind a sliding window, and
+// rows that are nodes of a tree; the other instantiations are as if there were
+// neither.
+template <int D_QK, int D_V, bool kGeneral, bool kMasked>
 __global__ void __launch_bounds__(kVarlenThreads, 1)
     varlen_fwd_kernel(const __grid_constant__ VarlenMaps maps, const VarlenArgs args) {
   using C = VarlenCfg<D_QK, D_V>;
+  using Item = ItemOf<kMasked>;
   const int split = kGeneral ? args.split : 1;
   const int pshift = kGeneral ? args.pack_shift : 0;
   using QK = typename C::QK;
@@ -923,12 +991,12 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
   static_assert(SplitStash<D_V>::kBytes <= 2 * C::q_pairs * C::q_tile_bytes +
                                                NK * C::k_slot_bytes + NV * C::v_slot_bytes,
                 "the split-KV partials fit in the Q tiles and K/V rings");
-  build_work_list(args.cu_q, args.cu_k, args.batch, args.total_q, args.total_k, args.num_heads,
+  build_work_list<!kMasked>(args.cu_q, args.cu_k, args.batch, args.total_q, args.total_k, args.num_heads,
                   pshift, s_prefix, s_sorted, s_part,
                   reinterpret_cast<int*>(k_ring));  // ends with __syncthreads
   if (tid == 0) {
     // The decoded-item ring, in the scan scratch the list builder is done with.
-    ItemRing* rg = reinterpret_cast<ItemRing*>(s_part);
+    ItemRing<kMasked>* rg = reinterpret_cast<ItemRing<kMasked>*>(s_part);
     for (int sl = 0; sl < kItemSlots; ++sl) {
       ptx::mbar_init(ptx::smem_u32(&rg->full[sl]), 1);
       ptx::mbar_init(ptx::smem_u32(&rg->free_[sl]), kItemReaders);
@@ -940,7 +1008,7 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = cb->tmem_base;
   const int total_items = s_prefix[args.batch];
-  ItemRing* const ring = reinterpret_cast<ItemRing*>(s_part);
+  ItemRing<kMasked>* const ring = reinterpret_cast<ItemRing<kMasked>*>(s_part);
 
   if (warp >= 8) {
     ptx::regs_dec<kControlRegs>();
@@ -959,7 +1027,7 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
         for (int r = 0; r * (int)gridDim.x < total_items && ok; ++r) {
           const int it = snake_item(r, split);
           if (it >= total_items) continue;
-          const WorkItem w = decode_item(it, args, s_prefix, s_sorted, split, pshift);
+          const Item w = decode_item<kMasked>(it, args, s_prefix, s_sorted, split, pshift);
           {
             // Publish the item (every one, empty or not: all roles walk the
             // same sequence).
@@ -984,7 +1052,7 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
                 ptx::tma_prefetch_l2_3d(c < QK::full ? &maps.q_full : &maps.q_tail, c * 64,
                                         w.head, row);
             }
-            const int krow = w.k_start + w.tile_lo * kBN;
+            const int krow = w.k_start + key_tile(w, 0) * kBN;
 #pragma unroll
             for (int c = 0; c < QK::chunks; ++c)
               ptx::tma_prefetch_l2_3d(c < QK::full ? &maps.k_full : &maps.k_tail, c * 64,
@@ -1014,7 +1082,8 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
                                row);
           }
           for (int j = 0; j < w.n_kv && ok; ++j) {
-            const int krow = w.k_start + (w.tile_lo + j) * kBN;
+            const int krow = w.k_start + key_tile(w, j) * kBN;
+            const int next_row = kMasked ? w.k_start + key_tile(w, j + 1) * kBN : krow + kBN;
             // K_j into the K ring.
             const uint32_t ks = ring_slot<NK>(kn);
             ok = wait_single(ptx::smem_u32(&cb->k_free[ks]), ((kn / NK) & 1) ^ 1, abort_flag,
@@ -1036,12 +1105,12 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
 #pragma unroll
                 for (int c = 0; c < QK::chunks; ++c)
                   ptx::tma_prefetch_l2_3d(c < QK::full ? &maps.k_full : &maps.k_tail, c * 64,
-                                          w.kv_head, krow + kBN);
+                                          w.kv_head, next_row);
               }
               ++kn;
             }
             if (kGeneral && split > 1 && j + 1 < w.n_kv) {
-              const int prow = krow + kBN;
+              const int prow = next_row;
 #pragma unroll
               for (int c = 0; c < QK::chunks; ++c)
                 ptx::tma_prefetch_l2_3d(c < QK::full ? &maps.k_full : &maps.k_tail, c * 64,
@@ -1153,7 +1222,7 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
         for (int r = 0; r * (int)gridDim.x < total_items && ok; ++r) {
           const int it = snake_item(r, split);
           if (it >= total_items) continue;
-          WorkItem w;
+          Item w;
           {
             const uint32_t sl = (uint32_t)r % kItemSlots;
             ok = wait_warp(ptx::smem_u32(&ring->full[sl]), ((uint32_t)r / kItemSlots) & 1,
@@ -1168,7 +1237,9 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
           // step before (or in the prologue), P V_t(j) at step j.
           int jlo = 0, jhi = 0;
           if (mine) {
-            if (C::tile_ranges)
+            if constexpr (C::tile_ranges && kMasked)
+              masked_kv_range(w, t, args, pshift, jlo, jhi);
+            else if (C::tile_ranges)
               tile_kv_range(w, t, args.wl, args.wr, pshift, jlo, jhi);
             else
               jhi = w.n_kv;
@@ -1368,7 +1439,7 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
     for (int r = 0; r * (int)gridDim.x < total_items && ok; ++r) {
       const int it = snake_item(r, split);
       if (it >= total_items) continue;
-      WorkItem w;
+      Item w;
       {
         const uint32_t sl = (uint32_t)r % kItemSlots;
         ok = wait_warp(ptx::smem_u32(&ring->full[sl]), ((uint32_t)r / kItemSlots) & 1, abort_flag,
@@ -1386,7 +1457,10 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
       const int i = w.row0 + ((t * kBM + row_in_tile) >> pshift);
       const bool row_valid = i < w.lq;
       int jlo = 0, jhi = w.n_kv;  // this tile's key tiles (its issuer walks the same)
-      if (C::tile_ranges) tile_kv_range(w, t, args.wl, args.wr, pshift, jlo, jhi);
+      if constexpr (C::tile_ranges && kMasked)
+        masked_kv_range(w, t, args, pshift, jlo, jhi);
+      else if (C::tile_ranges)
+        tile_kv_range(w, t, args.wl, args.wr, pshift, jlo, jhi);
       // Every row of the tile a token of one sequence (one head per tile):
       // the staged O rows leave with one tensor store instead of one bulk
       // copy per row (128 copies per tile queue up in the copy engine, ahead
@@ -1416,6 +1490,24 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
         hi_i = args.wr >= 0 ? min(w.lk, i + off + args.wr + 1) : w.lk;
         if (hi_i < lo_i) hi_i = lo_i;
       }
+      // kMasked: the keys [0, sink_i) are visible too, and with a tree those
+      // that the row's mask names from key `off` on (hi_i is then at most off).
+      int sink_i = 0;
+      const int* mask_row = nullptr;
+      if constexpr (kMasked) {
+        if (row_valid && args.tree) {
+          mask_row = args.tree + (size_t)(w.q_start + i) * args.tree_words;
+          hi_i = max(off, 0);
+          lo_i = 0;
+          if (args.wl >= 0) {
+            int depth = -1;
+#pragma unroll 1
+            for (int k = 0; k < args.tree_words; ++k) depth += __popc(__ldg(mask_row + k));
+            lo_i = min(max(off + max(depth, 0) - args.wl, 0), hi_i);
+          }
+        }
+        sink_i = min(args.sinks, hi_i);
+      }
       float m_used = neg_inf;  // running max, scaled log2 units
       float l = 0.f;
       for (int j = jlo; j < jhi; ++j) {
@@ -1439,18 +1531,38 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
           ptx::mbar_arrive(ptx::smem_u32(&cb->s_free[t]));
         }
 
-        const int k0 = (w.tile_lo + j) * kBN;
+        const int k0 = key_tile(w, j) * kBN;
         float row_max;
-        if (k0 >= lo_i && k0 + kBN <= hi_i) {
+        if ((k0 >= lo_i || (kMasked && k0 + kBN <= sink_i)) && k0 + kBN <= hi_i) {
           // Every key of the tile is visible to this row: the hardware max.
           row_max = ptx::max3(qmax[0], qmax[1], fmaxf(qmax[2], qmax[3]));
         } else {
           // Boundary tile for this row: mask keys outside [lo_i, hi_i) and
           // reduce in software (the hardware max is over the unmasked S).
-          const unsigned span = (unsigned)(hi_i - lo_i);
+          if constexpr (kMasked) {
+            // A word of visible keys for each 32 columns.
 #pragma unroll
-          for (int c = 0; c < kBN; ++c)
-            s[c] = ((unsigned)(k0 + c - lo_i) < span) ? s[c] : neg_inf;
+            for (int q = 0; q < kBN / 32; ++q) {
+              const int at = k0 + 32 * q;
+              uint32_t seen =
+                  (low_bits(hi_i - at) & ~low_bits(lo_i - at)) | low_bits(sink_i - at);
+              const int p = at - off;  // node of the first column
+              if (mask_row && p > -32 && (p >> 5) < args.tree_words) {
+                const int k = p >> 5;
+                const uint32_t a = k >= 0 ? __ldg(mask_row + k) : 0u;
+                const uint32_t b = k + 1 < args.tree_words ? __ldg(mask_row + k + 1) : 0u;
+                seen |= __funnelshift_r(a, b, p & 31) & low_bits(w.lk - at);
+              }
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                s[32 * q + c] = (seen >> c) & 1 ? s[32 * q + c] : neg_inf;
+            }
+          } else {
+            const unsigned span = (unsigned)(hi_i - lo_i);
+#pragma unroll
+            for (int c = 0; c < kBN; ++c)
+              s[c] = ((unsigned)(k0 + c - lo_i) < span) ? s[c] : neg_inf;
+          }
           float mx[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) mx[k] = fmaxf(s[k], s[k + 4]);
@@ -1652,13 +1764,17 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
       // the Q tiles and K/V rings are dead: the partial goes there.
       ptx::named_bar_sync_n(1, 256);
       const int it = (int)blockIdx.x / split;
-      const WorkItem w = it < total_items ? decode_item(it, args, s_prefix, s_sorted, split, pshift) : WorkItem{};
+      const Item w =
+          it < total_items ? decode_item<kMasked>(it, args, s_prefix, s_sorted, split, pshift) : Item{};
       if (it < total_items && t < w.n_qt) {
         ptx::tc_fence_after();
         const int r = t * kBM + row_in_tile;  // row within the item
         uint8_t* row = smem + r * SplitStash<D_V>::kRowBytes;
         int jlo = 0, jhi = w.n_kv;
-        if (C::tile_ranges) tile_kv_range(w, t, args.wl, args.wr, pshift, jlo, jhi);
+        if constexpr (C::tile_ranges && kMasked)
+          masked_kv_range(w, t, args, pshift, jlo, jhi);
+        else if (C::tile_ranges)
+          tile_kv_range(w, t, args.wl, args.wr, pshift, jlo, jhi);
         const bool has_o = jhi > jlo;
         float sp_m = neg_inf, sp_l = 0.f;
         if (has_o) {
@@ -1720,7 +1836,7 @@ struct VarlenLaunch {
 // Largest number of clusters of `split` CTAs of this kernel that can be
 // resident at once on the current device (0 if none), queried once per
 // device and cluster size.
-template <int D_QK, int D_V>
+template <int D_QK, int D_V, bool kMasked>
 int varlen_max_clusters(int dev, int split) {
   static std::atomic<int> cache[64][kMaxSplit + 1];  // value + 1; 0 = not yet queried
   const int c = cache[dev][split].load(std::memory_order_acquire);
@@ -1738,7 +1854,7 @@ int varlen_max_clusters(int dev, int split) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, varlen_fwd_kernel<D_QK, D_V, true>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, varlen_fwd_kernel<D_QK, D_V, true, kMasked>, &cfg) != cudaSuccess) {
     cudaGetLastError();  // not a sticky error: clear it and report no cluster
     n = 0;
   }
@@ -1750,12 +1866,12 @@ int varlen_max_clusters(int dev, int split) {
 // cluster size (at most kMaxSplit, 8 where larger clusters are unavailable)
 // whose clusters, one per item, are all resident at once and whose parts
 // keep at least four KV tiles.  1 = no split.
-template <int D_QK, int D_V>
+template <int D_QK, int D_V, bool kMasked>
 int varlen_split_choice(int dev, const VarlenLaunch& L, bool large_clusters) {
   if (L.item_bound < 1 || L.item_bound * 2 > L.sm_count || L.kv_tiles < 8) return 1;
   for (int s = large_clusters ? kMaxSplit : 8; s >= 2; --s) {
     if (L.kv_tiles < 4LL * s || L.item_bound * s > L.sm_count) continue;
-    if (L.item_bound <= varlen_max_clusters<D_QK, D_V>(dev, s)) return s;
+    if (L.item_bound <= varlen_max_clusters<D_QK, D_V, kMasked>(dev, s)) return s;
   }
   return 1;
 }
@@ -1769,14 +1885,14 @@ cudaError_t varlen_plan_impl(const VarlenLaunch& L, int* grid, int* split) {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   // Without the non-portable cluster-size permission set (the launcher sets
   // it on first use) the query still reports what is possible.
-  cudaFuncSetAttribute(varlen_fwd_kernel<D_QK, D_V, true>,
+  cudaFuncSetAttribute(varlen_fwd_kernel<D_QK, D_V, true, false>,
                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                        (int)varlen_smem_bytes<D_QK, D_V>(kMaxBatch));
-  const bool large = cudaFuncSetAttribute(varlen_fwd_kernel<D_QK, D_V, true>,
+  const bool large = cudaFuncSetAttribute(varlen_fwd_kernel<D_QK, D_V, true, false>,
                                           cudaFuncAttributeNonPortableClusterSizeAllowed,
                                           1) == cudaSuccess;
   cudaGetLastError();
-  *split = varlen_split_choice<D_QK, D_V>(dev, L, large);
+  *split = varlen_split_choice<D_QK, D_V, false>(dev, L, large);
   long long g = *split > 1 ? L.item_bound * *split
                            : (L.item_bound < L.sm_count ? L.item_bound : L.sm_count);
   *grid = (int)(g < 1 ? 1 : g);
@@ -1788,7 +1904,7 @@ cudaError_t varlen_plan_impl(const VarlenLaunch& L, int* grid, int* split) {
 // limit (for the largest supported batch) and the cluster-size permission
 // are set once per device; concurrent first calls may both set them (the
 // calls are idempotent), the flags themselves are atomic.
-template <int D_QK, int D_V>
+template <int D_QK, int D_V, bool kMasked>
 cudaError_t launch_varlen_impl(const VarlenMaps& maps, const VarlenArgs& args_in,
                                const VarlenLaunch& L, cudaStream_t stream) {
   static std::atomic<int> attr_done[64];  // 0 = not set, 1 = set, 2 = set with large clusters
@@ -1798,15 +1914,15 @@ cudaError_t launch_varlen_impl(const VarlenMaps& maps, const VarlenArgs& args_in
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   int attrs = attr_done[dev].load(std::memory_order_acquire);
   if (attrs == 0) {
-    e = cudaFuncSetAttribute(varlen_fwd_kernel<D_QK, D_V, false>,
+    e = cudaFuncSetAttribute(varlen_fwd_kernel<D_QK, D_V, false, kMasked>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)varlen_smem_bytes<D_QK, D_V>(kMaxBatch));
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(varlen_fwd_kernel<D_QK, D_V, true>,
+    e = cudaFuncSetAttribute(varlen_fwd_kernel<D_QK, D_V, true, kMasked>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)varlen_smem_bytes<D_QK, D_V>(kMaxBatch));
     if (e != cudaSuccess) return e;
-    const bool large = cudaFuncSetAttribute(varlen_fwd_kernel<D_QK, D_V, true>,
+    const bool large = cudaFuncSetAttribute(varlen_fwd_kernel<D_QK, D_V, true, kMasked>,
                                             cudaFuncAttributeNonPortableClusterSizeAllowed,
                                             1) == cudaSuccess;
     if (!large) cudaGetLastError();
@@ -1814,15 +1930,15 @@ cudaError_t launch_varlen_impl(const VarlenMaps& maps, const VarlenArgs& args_in
     attr_done[dev].store(attrs, std::memory_order_release);
   }
   VarlenArgs args = args_in;
-  args.split = varlen_split_choice<D_QK, D_V>(dev, L, attrs == 2);
+  args.split = varlen_split_choice<D_QK, D_V, kMasked>(dev, L, attrs == 2);
   const size_t smem = varlen_smem_bytes<D_QK, D_V>(args.batch);
   if (args.split == 1) {
     long long grid = L.item_bound < L.sm_count ? L.item_bound : L.sm_count;
     if (grid < 1) grid = 1;
     if (args.pack_shift == 0)
-      varlen_fwd_kernel<D_QK, D_V, false><<<(int)grid, kVarlenThreads, smem, stream>>>(maps, args);
+      varlen_fwd_kernel<D_QK, D_V, false, kMasked><<<(int)grid, kVarlenThreads, smem, stream>>>(maps, args);
     else
-      varlen_fwd_kernel<D_QK, D_V, true><<<(int)grid, kVarlenThreads, smem, stream>>>(maps, args);
+      varlen_fwd_kernel<D_QK, D_V, true, kMasked><<<(int)grid, kVarlenThreads, smem, stream>>>(maps, args);
     return cudaGetLastError();
   }
   cudaLaunchConfig_t cfg;
@@ -1838,7 +1954,7 @@ cudaError_t launch_varlen_impl(const VarlenMaps& maps, const VarlenArgs& args_in
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, varlen_fwd_kernel<D_QK, D_V, true>, maps, args);
+  return cudaLaunchKernelEx(&cfg, varlen_fwd_kernel<D_QK, D_V, true, kMasked>, maps, args);
 }
 
 }  // namespace fa
@@ -1847,9 +1963,17 @@ cudaError_t launch_varlen_impl(const VarlenMaps& maps, const VarlenArgs& args_in
   namespace fa {                                                                         \
   cudaError_t launch_varlen_##DQK##_##DV(const VarlenMaps& maps, const VarlenArgs& args, \
                                          const VarlenLaunch& L, cudaStream_t stream) {  \
-    return launch_varlen_impl<DQK, DV>(maps, args, L, stream);                           \
+    return launch_varlen_impl<DQK, DV, false>(maps, args, L, stream);                           \
   }                                                                                      \
   cudaError_t plan_varlen_##DQK##_##DV(const VarlenLaunch& L, int* grid, int* split) {   \
     return varlen_plan_impl<DQK, DV>(L, grid, split);                                    \
+  }                                                                                      \
+  }
+
+#define FA_DEFINE_MASKED_LAUNCHER(DQK, DV)                                               \
+  namespace fa {                                                                         \
+  cudaError_t launch_masked_##DQK##_##DV(const VarlenMaps& maps, const VarlenArgs& args, \
+                                         const VarlenLaunch& L, cudaStream_t stream) {  \
+    return launch_varlen_impl<DQK, DV, true>(maps, args, L, stream);                     \
   }                                                                                      \
   }
