@@ -612,6 +612,45 @@ fa_status fa_paged_attn_plan(int batch, int total_q, int num_heads, int num_head
                              size_t* workspace_bytes);
 
 /*
+ * Eviction from the cache by attention weight: fa_paged_key_weights adds up what
+ * weight each key gets, fa_paged_kv_select names the keys to keep, and
+ * fa_paged_kv_compact moves them together in place; the pages behind are then
+ * the caller's again.
+ *
+ * fa_paged_key_weights -- the attention weights of the rows, summed for each key
+ * of the cache and kv head:
+ *     W[b, hk, j] = decay * W[b, hk, j] + sum_i sum_h exp(softmax_scale q_ih k_j
+ *                   - lse_hi)
+ * over the query rows i of sequence b and the query heads h of group hk, where
+ * the row sees the key (the mask of fa_paged_attn, with sinks).
+ *
+ *   q, cu_seqlens_q, seq_lens, page_table, k_cache, k_scale, causal,
+ *   window_left, sink_tokens   as the attention call of the same rows.
+ *   lse           fp32 [num_heads, total_q]: what that call returned.  A row
+ *                 with -inf adds nothing.
+ *   decay         0 .. 1.  0: W is not read (it may hold anything).
+ *   weights       fp32 [batch, num_heads_k, capacity], updated: row b is that of
+ *                 sequence b.  The last n of its keys, the rows' own, count as
+ *                 new: their old sums are not read.  Sums are written for the
+ *                 keys [0, seq_len) that the page table has entries for, below
+ *                 capacity; sequences without rows, and what lies behind a
+ *                 length, stay as they were.
+ *
+ * Precision: the scores and weights in fp32 (a row of q as in fa_paged_attn),
+ * added in a fixed order.
+ *
+ * Host errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED (head_dim, sizes past
+ * 32-bit indices), FA_ERR_ARCH, FA_ERR_LAUNCH.
+ */
+fa_status fa_paged_key_weights(const void* q, long long q_row_stride, long long q_head_stride,
+                               const float* lse, const void* k_cache, const float* k_scale,
+                               const int* cu_seqlens_q, const int* seq_lens,
+                               const int* page_table, int batch, int total_q, int num_heads,
+                               int num_heads_k, int head_dim, int num_pages, int max_pages_per_seq,
+                               float softmax_scale, int causal, int window_left, int sink_tokens,
+                               float decay, float* weights, int capacity, fa_stream_t stream);
+
+/*
  * fa_paged_kv_gather -- the first n = cu_seqlens[b + 1] - cu_seqlens[b]
  * cached tokens of every sequence as packed bf16 tensors, the k and v (with
  * cu_seqlens as cu_seqlens_k) of a fa_varlen_fwd call: a long chunk of

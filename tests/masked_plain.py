@@ -115,3 +115,37 @@ def paged_attention(q, kc, vc, ks, vs, cu, lens, pages, scale, causal=True, wind
                     o[t, h], lse[h, t], w[t, h], big[h, t] = attend(q[t, h], k, v, seen[i] & held,
                                                                     scale)
     return o, lse, w, big
+
+
+def key_weights(q, lse, kc, ks, cu, lens, pages, sums, scale, causal=True, window=-1, sinks=0,
+                decay=1.0):
+    """(sums, tolerance) after the call, fp64; sums [batch, Hk, capacity].  A
+    weight's exponent is off by the score's dx = 2^-15 A, A = scale * sum |q k|,
+    and 2^-20 of the score and the LSE; each sum of R weights by (R + 8) 2^-23."""
+    T, H, d = q.shape
+    hks, cap = sums.shape[1:]
+    out, tol = sums.double().clone(), torch.zeros_like(sums, dtype=torch.float64)
+    for b, length in enumerate(lens):
+        n = cu[b + 1] - cu[b]
+        keys = min(max(length, 0), pages.shape[1] * 64, cap)
+        if n <= 0 or keys == 0:
+            continue
+        old = out[b, :, :keys] * decay if decay else torch.zeros((hks, keys), dtype=torch.float64)
+        old[:, max(length - n, 0):] = 0
+        out[b, :, :keys] = old
+        tol[b, :, :keys] = old.abs() * 2.0 ** -22
+        for hk in range(hks):
+            k, held = plain.keys_of(b, keys, pages, kc, ks, hk)
+            for i in range(n):
+                seen = seen_keys(i, n, length, keys, causal, window, -1, sinks) & held
+                for h in range(hk * (H // hks), (hk + 1) * (H // hks)):
+                    row, l = q[cu[b] + i, h].double(), lse[h, cu[b] + i].double()
+                    if l == -math.inf or not seen.any():
+                        continue
+                    x = k[seen] @ row * scale
+                    p = torch.exp(x - l)
+                    dx = 2.0 ** -15 * scale * (k[seen].abs() @ row.abs())
+                    err = 1.1 * dx + 2.0 ** -20 * (x.abs() + l.abs())
+                    out[b, hk, :keys][seen] += p
+                    tol[b, hk, :keys][seen] += p * (err + (n * (H // hks) + 8) * 2.0 ** -23)
+    return out, tol + 1e-37

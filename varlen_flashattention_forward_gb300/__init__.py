@@ -33,6 +33,9 @@ Entry points (same names as the C ABI):
   fa_draft_tree(parents, cu_seqlens, seq_lens, max_nodes=64, tree_mask=None, positions=None,
                 stream=None)
   fa_paged_attn_plan(batch, total_q, num_heads, num_heads_k, head_dim, max_seqlen_q=0)
+  fa_paged_key_weights(q, lse, k_cache, k_scale, cu_seqlens_q, seq_lens, page_table, weights,
+                       softmax_scale=None, causal=True, window_left=-1, sink_tokens=0, decay=1.0,
+                       stream=None)
   fa_paged_kv_gather(k_cache, v_cache, k_scale, v_scale, cu_seqlens, page_table, total_k,
                      k_out=None, v_out=None, stream=None)
   fa_get_device_status()
@@ -62,7 +65,8 @@ EXPORTS = ("fa_varlen_fwd", "fa_varlen_fwd_plan", "fa_varlen_fwd_strided", "fa_v
            "fa_sparse_mla_decode",
            "fa_sparse_mla_decode_plan", "fa_sparse_mla_decode_noalloc", "fa_merge_attn_states",
            "fa_qk_norm_rope", "fa_paged_kv_append", "fa_paged_attn", "fa_paged_attn_plan",
-           "fa_paged_attn_masked", "fa_draft_tree", "fa_paged_kv_gather", "fa_get_device_status",
+           "fa_paged_attn_masked", "fa_draft_tree", "fa_paged_key_weights", "fa_paged_kv_gather",
+           "fa_get_device_status",
            "fa_set_wait_limit_ns", "fa_status_string")
 
 _lib = None
@@ -128,6 +132,9 @@ def load_library():
     lib.fa_paged_attn_masked.restype = i32
     lib.fa_draft_tree.argtypes = [p, p, p, i32, i32, i32, p, p, p]
     lib.fa_draft_tree.restype = i32
+    lib.fa_paged_key_weights.argtypes = [p, i64, i64, p, p, p, p, p, p, i32, i32, i32, i32, i32, i32,
+                                         i32, f32, i32, i32, i32, f32, p, i32, p]
+    lib.fa_paged_key_weights.restype = i32
     lib.fa_paged_attn_plan.argtypes = [i32, i32, i32, i32, i32, i32, pi, pi,
                                        ctypes.POINTER(size)]
     lib.fa_paged_attn_plan.restype = i32
@@ -752,6 +759,54 @@ def fa_paged_kv_gather(k_cache, v_cache, k_scale, v_scale, cu_seqlens, page_tabl
     if st != FA_OK:
         raise FaError(st, "fa_paged_kv_gather")
     return k_out, v_out
+
+
+def _check_weights(weights, batch, hk):
+    """Keys that a [batch, H_k, capacity] fp32 tensor of weights has room for."""
+    import torch
+    _check(weights, "weights", torch.float32, 3)
+    capacity = weights.shape[2]
+    _shape(weights, "weights", (batch, hk, capacity))
+    return capacity
+
+
+def fa_paged_key_weights(q, lse, k_cache, k_scale, cu_seqlens_q, seq_lens, page_table, weights,
+                         softmax_scale=None, causal=True, window_left=-1, sink_tokens=0, decay=1.0,
+                         stream=None):
+    """Adds the attention weights of the rows to the sums of the keys they see;
+    see fa_paged_key_weights in include/fa_gb300.h.
+
+    q [total_q, H, d] bf16 (strided view allowed) and lse [H, total_q] fp32 of
+    a fa_paged_attn call with the same cache, lengths and mask; weights [batch,
+    H_k, capacity] fp32, updated in place: decay * weights plus the new ones (the
+    rows' own keys start from 0; decay=0 reads nothing).
+    """
+    import torch
+    lib = load_library()
+    _check(q, "q", torch.bfloat16, 3, view=True)
+    batch, pages, hk, d, width = _check_cache(k_cache, k_cache, k_scale, k_scale, cu_seqlens_q,
+                                              page_table)
+    _check(seq_lens, "seq_lens", torch.int32, 1)
+    _shape(seq_lens, "seq_lens", (batch,))
+    T, H, dq = q.shape
+    if dq != d:
+        raise ValueError(f"q has head dim {dq}, the cache {d}")
+    _check(lse, "lse", torch.float32, 2)
+    _shape(lse, "lse", (H, T))
+    capacity = _check_weights(weights, batch, hk)
+    if softmax_scale is None:
+        softmax_scale = d ** -0.5
+    index, here = _device(stream, q, lse, k_cache, k_scale, cu_seqlens_q, seq_lens, page_table,
+                          weights)
+    qr, qh, _ = q.stride()
+    with here:
+        st = lib.fa_paged_key_weights(
+            q.data_ptr(), qr, qh, lse.data_ptr(), k_cache.data_ptr(), k_scale.data_ptr(),
+            cu_seqlens_q.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(), batch, T, H, hk, d,
+            pages, width, softmax_scale, bool(causal), _window(window_left), _sinks(sink_tokens),
+            decay, weights.data_ptr(), capacity, _raw_stream(index))
+    if st != FA_OK:
+        raise FaError(st, "fa_paged_key_weights")
 
 
 def fa_set_wait_limit_ns(ns: int) -> None:

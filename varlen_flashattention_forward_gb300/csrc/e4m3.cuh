@@ -48,4 +48,28 @@ __device__ __forceinline__ float2 f16x2_floats(uint32_t h) {
   return f;
 }
 
+// A row of queries as two e4m3 terms: scaled by 2^(7 - e), e the exponent of
+// its largest value mx, which puts that in [128, 256), it is hi + lo with hi =
+// rn(q) and lo = rn(q - hi).  (Rows below 2^-100 keep a smaller size; their
+// scores are zero in fp32 all the same.  mx may be infinite, see terms_scale.)
+__device__ __forceinline__ int terms_exponent(float mx) {
+  return imax((int)(__float_as_uint(mx) >> 23) - 127, -100);
+}
+__device__ __forceinline__ void split_terms(const float* x, int e, uint32_t* hi, uint32_t* lo) {
+  const float f = __uint_as_float((uint32_t)(7 - e + 127) << 23);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float y0 = x[2 * k] * f, y1 = x[2 * k + 1] * f;
+    hi[k] = pack_e4m3x2(y0, y1);
+    const float2 h2 = f16x2_floats(unpack_e4m3x2(hi[k]));
+    lo[k] = pack_e4m3x2(y0 - h2.x, y1 - h2.y);
+  }
+}
+// What the terms' products are to be multiplied by, for scores times `scale`:
+// NaN for a row with an infinity or a NaN (mx infinite).
+__device__ __forceinline__ float terms_scale(float mx, int e, float scale) {
+  return mx < __int_as_float(0x7f800000) ? scale * __uint_as_float((uint32_t)(e - 7 + 127) << 23)
+                                         : __int_as_float(0x7fffffff);
+}
+
 }  // namespace fa

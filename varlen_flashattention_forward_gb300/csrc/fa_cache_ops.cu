@@ -2,6 +2,7 @@
 // the eviction from the paged cache.  Argument checks, launch shapes,
 // launches; nothing here copies data, synchronises or allocates.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -9,10 +10,44 @@
 
 #include "draft_tree_kernel.cuh"
 #include "host_common.h"
+#include "key_weights_kernel.cuh"
+#include "paged_host.h"
 
 using fa::is_aligned;
 
 namespace {
+
+template <int D, int N>
+cudaError_t launch_weights(const CUtensorMap& map, const fa::KeyWeightsArgs& a, int sm_count,
+                           cudaStream_t stream) {
+  // Set once per device; concurrent first calls may both set it (the call is
+  // idempotent), the flag itself is atomic.
+  static std::atomic<bool> attr_done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  const int smem = (int)fa::weights_smem<D, N>();
+  if (!attr_done[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(fa::key_weights_kernel<D, N>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    attr_done[dev].store(true, std::memory_order_release);
+  }
+  fa::key_weights_kernel<D, N>
+      <<<sm_count * fa::WeightsCfg<D, N>::kResident, fa::kWeightThreads, smem, stream>>>(map, a);
+  return cudaGetLastError();
+}
+template <int D>
+cudaError_t launch_weights_rows(const CUtensorMap& map, const fa::KeyWeightsArgs& a, int sm_count,
+                                cudaStream_t stream) {
+  switch (a.shape.rows) {
+    case 16: return launch_weights<D, 16>(map, a, sm_count, stream);
+    case 32: return launch_weights<D, 32>(map, a, sm_count, stream);
+    case 64: return launch_weights<D, 64>(map, a, sm_count, stream);
+    default: return launch_weights<D, 128>(map, a, sm_count, stream);
+  }
+}
 
 fa_status launched() { return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH; }
 
@@ -42,4 +77,70 @@ extern "C" fa_status fa_draft_tree(const int* parents, const int* cu_seqlens, co
     fa::draft_tree_kernel<<<dim3(blocks, std::min(batch - b0, 65535)), fa::kTreeThreads, 0, s>>>(a);
   }
   return launched();
+}
+
+extern "C" fa_status fa_paged_key_weights(
+    const void* q, long long q_row_stride, long long q_head_stride, const float* lse,
+    const void* k_cache, const float* k_scale, const int* cu_seqlens_q, const int* seq_lens,
+    const int* page_table, int batch, int total_q, int num_heads, int num_heads_k, int head_dim,
+    int num_pages, int max_pages_per_seq, float softmax_scale, int causal, int window_left,
+    int sink_tokens, float decay, float* weights, int capacity, fa_stream_t stream) {
+  if ((total_q > 0 && (!q || !lse)) || !seq_lens || !weights) return FA_ERR_INVALID_ARG;
+  fa_status st = fa::check_cache(k_cache, k_cache, k_scale, k_scale, cu_seqlens_q, page_table, batch,
+                                 total_q, num_heads_k, head_dim, num_pages, max_pages_per_seq);
+  if (st != FA_OK) return st;
+  if (num_heads < 1 || num_heads % num_heads_k != 0 || window_left < -1 || sink_tokens < 0 ||
+      capacity < 1 || !(softmax_scale > 0.f) || !std::isfinite(softmax_scale) ||
+      !(decay >= 0.f && decay <= 1.f))
+    return FA_ERR_INVALID_ARG;
+  if (!is_aligned(q, 16) || !is_aligned(lse, 4) || !is_aligned(seq_lens, 4) ||
+      !is_aligned(weights, 4))
+    return FA_ERR_INVALID_ARG;
+  if (total_q > 0 && !fa::settle_view(total_q, num_heads, head_dim, &q_row_stride, &q_head_stride))
+    return FA_ERR_INVALID_ARG;
+  if ((int64_t)total_q * num_heads > INT32_MAX || num_heads > 65535) return FA_ERR_UNSUPPORTED;
+  fa::DeviceFacts dev;
+  st = fa::device_facts(&dev);
+  if (st != FA_OK) return st;
+  if (total_q == 0) return FA_OK;
+  CUtensorMap map;
+  const int dim = head_dim <= 64 ? 64 : 128;
+  if (!fa::encode_cache(&map, k_cache, head_dim, num_pages * num_heads_k, dim)) return FA_ERR_LAUNCH;
+  // Rows of a chunk: what holds the mean sequence's, at most 128.
+  const int group = num_heads / num_heads_k;
+  const long long rows = (((int64_t)total_q + batch - 1) / batch) * group;
+  const int n = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  fa::KeyWeightsArgs a;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_row = q_row_stride;
+  a.q_head = q_head_stride;
+  a.lse = lse;
+  a.k_scale = k_scale;
+  a.total_q = total_q;
+  a.dim = head_dim;
+  a.max_pages = max_pages_per_seq;
+  a.num_pages = num_pages;
+  a.keys = std::min(max_pages_per_seq * fa::kPageTokens, capacity);
+  a.shape = {num_heads_k, group, n, causal != 0, window_left, a.keys, sink_tokens, 0};
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.decay = decay;
+  a.capacity = capacity;
+  a.status = dev.status;
+  a.wait_limit_ns = dev.wait_limit_ns;
+  // Costs of a launch are counted in 32 bits (see fa_paged_attn).
+  const long long most = (long long)num_heads_k * (a.keys / fa::kTileKeys + 1 + fa::kUnitCost);
+  if (most > fa::kMaxCost) return FA_ERR_UNSUPPORTED;
+  const int step = (int)std::min<long long>(fa::kWeightMaxBatch, fa::kMaxCost / most);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  for (int b0 = 0; b0 < batch; b0 += step) {
+    a.batch = std::min(batch - b0, step);
+    a.cu = cu_seqlens_q + b0;
+    a.seq_lens = seq_lens + b0;
+    a.page_table = page_table + (size_t)b0 * max_pages_per_seq;
+    a.weights = weights + (size_t)b0 * num_heads_k * capacity;
+    const cudaError_t e = dim == 64 ? launch_weights_rows<64>(map, a, dev.sm_count, s)
+                                    : launch_weights_rows<128>(map, a, dev.sm_count, s);
+    if (e != cudaSuccess) return FA_ERR_LAUNCH;
+  }
+  return FA_OK;
 }

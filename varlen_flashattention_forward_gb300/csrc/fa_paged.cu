@@ -12,10 +12,14 @@
 #include <cuda_runtime.h>
 
 #include "host_common.h"
+#include "paged_host.h"
 #include "paged_kv_kernels.cuh"
 #include "paged_launch.cuh"
 #include "qk_norm_rope_kernel.cuh"
 
+using fa::cache_dim;
+using fa::check_cache;
+using fa::encode_cache;
 using fa::is_aligned;
 using fa::settle_view;
 
@@ -49,23 +53,6 @@ AttnLaunch attn_launch(int sm_count, int batch, int total_q, int group, int head
   return l;
 }
 
-// The cache as [num_pages * heads, 64, head_dim] bytes; a box is one (page,
-// head), its rows padded with zeros to the kernel's head dim.
-bool encode_cache(CUtensorMap* m, const void* base, int head_dim, int cells, int row) {
-  const fa::EncodeTiledFn fn = fa::tensor_map_encoder();
-  if (!fn) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)fa::kPageTokens, (cuuint64_t)cells};
-  cuuint64_t strides[2] = {(cuuint64_t)head_dim, (cuuint64_t)head_dim * fa::kPageTokens};
-  cuuint32_t box[3] = {(cuuint32_t)row, (cuuint32_t)fa::kPageTokens, 1u};
-  cuuint32_t estr[3] = {1u, 1u, 1u};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE,
-            row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-bool cache_dim(int d) { return d == 64 || d == 80 || d == 96 || d == 128; }
-
 // fa_qk_norm_rope takes kNormRopeRows heads of a token together where an SM has
 // kNormRopeWide threads' work (8 dims of a row each), else one.  64 tokens x 40
 // heads of 128 dims: one 2.25 us, four 2.83; 8192 tokens: 49.2 against 30.1;
@@ -86,24 +73,6 @@ fa_status launched() { return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR
 bool valid_rope(const float* cos_sin, int rot_dim, int max_pos, int head_dim) {
   if (rot_dim < 0 || rot_dim % 16 != 0 || rot_dim > head_dim || max_pos < 0) return false;
   return rot_dim == 0 || (cos_sin != nullptr && is_aligned(cos_sin, 16) && max_pos > 0);
-}
-
-// Sizes of the cache and the arrays that come with it.
-fa_status check_cache(const void* k_cache, const void* v_cache, const float* k_scale,
-                      const float* v_scale, const int* cu, const int* page_table, int batch,
-                      int total, int heads_k, int head_dim, int num_pages, int max_pages) {
-  if (!k_cache || !v_cache || !k_scale || !v_scale || !cu || !page_table) return FA_ERR_INVALID_ARG;
-  if (batch < 1 || total < 0 || heads_k < 1 || num_pages < 1 || max_pages < 1)
-    return FA_ERR_INVALID_ARG;
-  if (!is_aligned(k_cache, 16) || !is_aligned(v_cache, 16) || !is_aligned(k_scale, 4) ||
-      !is_aligned(v_scale, 4) || !is_aligned(cu, 4) || !is_aligned(page_table, 4))
-    return FA_ERR_INVALID_ARG;
-  if (!cache_dim(head_dim)) return FA_ERR_UNSUPPORTED;
-  // Positions of a sequence, (page, head) cells and packed rows are 32-bit.
-  if ((int64_t)max_pages * fa::kPageTokens > INT32_MAX || (int64_t)num_pages * heads_k > INT32_MAX ||
-      (int64_t)total * heads_k > INT32_MAX || heads_k > 32767)
-    return FA_ERR_UNSUPPORTED;
-  return FA_OK;
 }
 
 }  // namespace

@@ -1,0 +1,454 @@
+// key_weights_kernel.cuh -- attention weights that each cached key has got,
+// for sm_103a:
+//
+//   W[b, h, j] = decay * W[b, h, j] + sum over the rows i of sequence b and the
+//                heads of group h of exp(scale q_i k_j - LSE_i)
+//
+// over the keys that a row sees (a key that is among the rows' own starts from
+// 0).  The LSE is that of the rows' attention, so the weights are final as they
+// come: no maximum, no V and no second pass.
+//
+// The transposed form of paged_attn_kernel: St[key, row] = K[key, d] Q[row, d]t
+// as e4m3 products of K as it lies in the cache and Q as two e4m3 terms, here
+// one after the other into the same fp32 accumulator.  A thread has a key: its
+// weights' sum over the rows stays in the thread, in a fixed order, and no two
+// threads write the same place.
+//
+// Work: every (sequence, kv head) has its 128-key tiles; their costs are cut
+// into equal contiguous ranges (paged_index.h), one for each CTA, so a tile is
+// one CTA's alone.  More rows than N go in chunks, tile by tile again.
+//
+//   warps 0-3  stage the rows of Q, then a thread for each key: exp2, sum,
+//              the weight's update
+//   warp 4     S MMAs into two buffers of N columns
+//   warp 5     TMA of the pages into a ring of K tiles, ahead of both
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "e4m3.cuh"
+#include "named_bar.cuh"
+#include "paged_attn_kernel.cuh"  // bounded waits
+#include "paged_index.h"
+#include "rope_row.cuh"
+#include "sm103_ptx.cuh"
+
+namespace fa {
+
+constexpr int kWeightThreads = 192;
+constexpr int kWeightMaxBatch = 512;  // sequences of a launch
+
+struct KeyWeightsArgs {
+  const uint16_t* q;
+  long long q_row, q_head;
+  const float* lse;  // [heads, total_q], natural
+  const float* k_scale;
+  const int *cu, *seq_lens, *page_table;
+  int batch, total_q, dim, max_pages, num_pages;
+  AttnShape shape;   // rows: N
+  int keys;          // positions of a sequence that have a page and a weight
+  float scale_log2, decay;
+  float* weights;    // [batch, kv heads, capacity]
+  long long capacity;
+  unsigned int* status;
+  uint64_t wait_limit_ns;
+};
+
+template <int D, int N>
+struct WeightsCfg {
+  static constexpr uint32_t kSwK = D == 128 ? ptx::kLayoutSw128 : ptx::kLayoutSw64;
+  static constexpr int kTileBytes = kTileKeys * D;
+  static constexpr int kPageBytes = kPageTokens * D;
+  static constexpr int kSlots = 3;
+  static constexpr int kQBytes = 2 * N * D;
+  static constexpr uint32_t kTmemCols = 2 * N < 32 ? 32 : 2 * N;
+  static constexpr int kQ = kSlots * kTileBytes;
+  static constexpr int kCtl = kQ + kQBytes;
+  // Resident CTAs (by shared memory: 56 to 86 KB at 128 dims).
+  static constexpr int kResident = N <= 16 ? 4 : N <= 64 ? 3 : 2;
+};
+
+template <int N>
+struct alignas(16) WeightsCtl {
+  uint64_t k_full[3], k_free[3];  // K slot landed / read
+  uint64_t s_full[2], s_free[2];  // St computed / loaded (128)
+  uint64_t q_full;                // rows of a chunk staged (128)
+  uint64_t drain;
+  uint32_t tmem_base;
+  volatile int abort_flag;
+  alignas(16) float4 row[N / 2];  // of two rows: score factors, then -LSE log2(e)
+  alignas(16) int token[N];       // of a row, from the chunk's first; -1: no row
+  long long warp_sum[4];
+  int before[kWeightMaxBatch + 1];
+};
+template <int D, int N>
+constexpr size_t weights_smem() {
+  return 1024 + WeightsCfg<D, N>::kCtl + sizeof(WeightsCtl<N>);
+}
+// (Of an SM's 228 KB, each CTA takes 1 KB more than its own.)
+template <int N>
+constexpr bool weights_fit() {
+  return WeightsCfg<128, N>::kResident * (weights_smem<128, N>() + 1024) <= 228 * 1024;
+}
+static_assert(weights_fit<16>() && weights_fit<32>() && weights_fit<64>() && weights_fit<128>(),
+              "resident CTAs");
+
+// A chunk of a sequence's rows against its keys.
+struct WeightChunk {
+  KeyRange keys;
+  long long at0;   // position of its first row's token
+  int span;        // from there to its last row's token
+  // Whether some row may see a key of the tile; of the tiles [j0, j1).
+  __device__ __forceinline__ bool seen(int j0) const { return any(j0, (long long)j0 + kTileKeys); }
+  __device__ __forceinline__ bool any(int j0, long long j1) const {
+    return (keys.hi > keys.lo && j0 < keys.hi && j1 > keys.lo) || j0 < keys.sink;
+  }
+  // Whether every row sees every key of the tile.
+  __device__ __forceinline__ bool whole(int j0, const AttnShape& s) const {
+    return (!s.causal || (long long)j0 + kTileKeys - 1 <= at0) &&
+           (s.window < 0 || (long long)j0 >= at0 + span - s.window ||
+            (long long)j0 + kTileKeys <= s.sinks);
+  }
+};
+__device__ __forceinline__ WeightChunk weight_chunk(const AttnShape& s, int c, int n, int len) {
+  WeightChunk w;
+  w.keys = tile_keys<true>(s, c, n, len);
+  const unsigned r0 = (unsigned)c * s.rows;
+  unsigned r1 = r0 + s.rows;
+  if (r1 > (unsigned)n * s.group) r1 = (unsigned)n * s.group;
+  const int t0 = token_of(s, r0);
+  w.at0 = (long long)len - n + t0;
+  w.span = token_of(s, r1 - 1) - t0;
+  return w;
+}
+
+template <int D, int N>
+__global__ void __launch_bounds__(kWeightThreads, WeightsCfg<D, N>::kResident)
+    key_weights_kernel(const __grid_constant__ CUtensorMap k_map, const KeyWeightsArgs a) {
+  using C = WeightsCfg<D, N>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  WeightsCtl<N>* cb = reinterpret_cast<WeightsCtl<N>*>(smem + C::kCtl);
+  volatile int* abort_flag = &cb->abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const AttnShape& sh = a.shape;
+  // The split sees one unit for each (sequence with rows, head), of all its keys.
+  const AttnShape whole = {sh.heads_k, 1, 1, 0, -1, a.keys, 0, 0};
+  auto seq_of = [&](int b, RowRange* q, int* len) {
+    *q = row_range(__ldg(a.cu + b), __ldg(a.cu + b + 1), a.total_q);
+    q->n = q->n > 0 ? 1 : 0;
+    *len = __ldg(a.seq_lens + b);
+  };
+
+  if (tid == 128) {
+    auto init = [&](uint64_t& b, uint32_t n) { ptx::mbar_init(ptx::smem_u32(&b), n); };
+    for (int s = 0; s < C::kSlots; ++s) {
+      init(cb->k_full[s], 1);
+      init(cb->k_free[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      init(cb->s_full[s], 1);
+      init(cb->s_free[s], 128);
+    }
+    init(cb->q_full, 128);
+    init(cb->drain, 1);
+    cb->abort_flag = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&k_map);
+  }
+  if (warp == 5) {
+    ptx::tmem_alloc(ptx::smem_u32(&cb->tmem_base), C::kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  if (warp < 4) {
+    if (tid == 0) cb->before[0] = 0;
+    long long base = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < a.batch; b0 += 128) {
+      const int b = b0 + tid;
+      int n = 0;
+      if (b < a.batch) {
+        RowRange q;
+        int len;
+        seq_of(b, &q, &len);
+        n = capped_cost(sh.heads_k * head_cost(whole, q.n, len));
+      }
+      long long sum = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+      }
+      if (lane == 31) cb->warp_sum[warp] = sum;
+      named_bar_sync(1, 128);
+      long long all = 0, lo = base;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        if (w < warp) lo += cb->warp_sum[w];
+        all += cb->warp_sum[w];
+      }
+      if (b < a.batch) cb->before[b + 1] = capped_cost(lo + sum);
+      base += all;
+      named_bar_sync(1, 128);
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = cb->tmem_base;
+  auto before = [&](int b) { return cb->before[b]; };
+  const int total = cb->before[a.batch];
+  auto wait = [&](uint64_t& b, int parity) {
+    return paged_wait(ptx::smem_u32(&b), (uint32_t)parity, abort_flag, a.status, a.wait_limit_ns);
+  };
+  // Every role walks the CTA's segments by itself.
+  SegmentWalk walk;
+  Segment g = {};
+  walk_begin(&walk, range_start(total, gridDim.x, blockIdx.x),
+             range_start(total, gridDim.x, blockIdx.x + 1), a.batch, before);
+  int rows = 0, row0 = 0;  // of the segment's sequence
+  auto next = [&]() {
+    if (!walk_next(&walk, whole, before, seq_of, &g)) return false;
+    const RowRange r = row_range(__ldg(a.cu + g.seq), __ldg(a.cu + g.seq + 1), a.total_q);
+    row0 = r.lo;
+    rows = r.n;
+    return true;
+  };
+  bool ok = true;
+
+  if (warp == 5) {
+    // ------------------------------------------------------------ producer
+    test_load_delay(a.wait_limit_ns);
+    int loads = 0;
+    while (ok && next()) {
+      const int chunks = row_tiles(sh, rows);
+      for (int c = 0; ok && c < chunks; ++c) {
+        const WeightChunk wc = weight_chunk(sh, c, rows, g.len);
+#pragma unroll 1
+        for (int t0 = 0; ok && t0 < g.count; t0 += 16) {
+          // Lane l: page l of the next 16 tiles, as its cell, or -1.
+          int cell = -1;
+          const long long p = (long long)(g.tile0 + t0) * 2 + lane;
+          if (t0 + lane / 2 < g.count && p * kPageTokens < g.keys.hi) {
+            const int id = checked_page(
+                __ldg(a.page_table + (size_t)g.seq * a.max_pages + p), a.num_pages);
+            if (id >= 0) cell = id * sh.heads_k + g.head;
+          }
+          const int end = imin(16, g.count - t0);
+#pragma unroll 1
+          for (int t = 0; t < end; ++t) {
+            if (!wc.seen((g.tile0 + t0 + t) * kTileKeys)) continue;
+            const int mine = __shfl_sync(0xffffffffu, cell, 2 * t + (lane & 1));
+            const unsigned held = __ballot_sync(0xffffffffu, mine >= 0) & 3;
+            const int s = loads % C::kSlots;
+            if (loads >= C::kSlots) ok = wait(cb->k_free[s], (loads / C::kSlots - 1) & 1);
+            if (!ok) break;
+            const uint32_t bar = ptx::smem_u32(&cb->k_full[s]);
+            if (lane == 0)
+              ptx::mbar_arrive_expect_tx(bar, ((held & 1) + (held >> 1)) * C::kPageBytes);
+            __syncwarp();
+            if (lane < 2 && mine >= 0)
+              ptx::tma_load_3d(ptx::smem_u32(smem + s * C::kTileBytes) + lane * C::kPageBytes,
+                               &k_map, bar, 0, 0, mine);
+            ++loads;
+          }
+        }
+      }
+    }
+    // Every copy this CTA started lands before it exits.
+    for (int s = 0; s < C::kSlots && s < loads; ++s)
+      wait_drain_warp(ptx::smem_u32(&cb->k_full[s]), ((loads - 1 - s) / C::kSlots) & 1, a.status);
+  } else if (warp == 4) {
+    // ---------------------------------------------------------- MMA issuer
+    constexpr uint32_t idesc = ptx::idesc_e4m3_f32(128, N);
+    const uint64_t q_hi = ptx::smem_desc(ptx::smem_u32(smem + C::kQ), 16, 8 * D, C::kSwK);
+    const uint64_t q_lo = ptx::smem_desc(ptx::smem_u32(smem + C::kQ + N * D), 16, 8 * D, C::kSwK);
+    int i = 0, staged = 0;
+    while (ok && next()) {
+      const int chunks = row_tiles(sh, rows);
+      for (int c = 0; ok && c < chunks; ++c) {
+        const WeightChunk wc = weight_chunk(sh, c, rows, g.len);
+        if (!wc.any(g.tile0 * kTileKeys, (g.tile0 + g.count) * (long long)kTileKeys)) continue;
+        ok = wait(cb->q_full, staged++ & 1);
+#pragma unroll 1
+        for (int t = 0; ok && t < g.count; ++t) {
+          if (!wc.seen((g.tile0 + t) * kTileKeys)) continue;
+          const int s = i % C::kSlots, sb = i & 1;
+          ok = wait(cb->k_full[s], (i / C::kSlots) & 1);
+          if (ok && i >= 2) ok = wait(cb->s_free[sb], ((i >> 1) - 1) & 1);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint64_t kd =
+              ptx::smem_desc(ptx::smem_u32(smem + s * C::kTileBytes), 16, 8 * D, C::kSwK);
+          ptx::mma_f8_elect<D / 32>(tmem + sb * N, kd, q_hi, idesc);
+          ptx::mma_f8_elect<D / 32, true>(tmem + sb * N, kd, q_lo, idesc);
+          ptx::mma_commit_elect(ptx::smem_u32(&cb->s_full[sb]));
+          ptx::mma_commit_elect(ptx::smem_u32(&cb->k_free[s]));
+          ++i;
+        }
+      }
+    }
+    ptx::mma_commit_elect(ptx::smem_u32(&cb->drain));
+    wait_drain_warp(ptx::smem_u32(&cb->drain), 0, a.status);
+  } else {
+    // ------------------------------------------------------------- weights
+    const float neg_inf = -__int_as_float(0x7f800000);
+    constexpr int kLanes = D / 8;  // lanes of a row of Q, 8 dims each
+    const uint32_t s_lane = tmem + ((uint32_t)(warp * 32) << 16);
+    const int key = tid;
+    int i = 0;
+    while (ok && next()) {
+      const int chunks = row_tiles(sh, rows);
+      float* out = a.weights + ((long long)g.seq * sh.heads_k + g.head) * a.capacity;
+      // The rows' own keys have no weight yet.
+      const long long fresh = (long long)g.len - rows;
+      for (int c = 0; ok && c < chunks; ++c) {
+        const WeightChunk wc = weight_chunk(sh, c, rows, g.len);
+        // ---- the chunk's rows of Q, if one is needed.  (The last chunk's MMAs
+        // are done: every thread has waited for them.  So the issuer has taken
+        // each staging before the next one.)
+        const int n_rows = imin(N, rows * sh.group - c * N);
+        if (wc.any(g.tile0 * kTileKeys, (g.tile0 + g.count) * (long long)kTileKeys)) {
+          const int sub = tid % kLanes, dim0 = sub * 8;
+          uint8_t* q_s = smem + C::kQ;
+#pragma unroll 2
+          for (int n = tid / kLanes; n < N; n += 128 / kLanes) {
+            const int row = c * N + n, tok = token_of(sh, row);
+            const int h = g.head * sh.group + row - tok * sh.group;
+            uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+            float lse = 0.f;
+            if (n < n_rows && dim0 < a.dim)
+              raw = __ldg(reinterpret_cast<const uint4*>(
+                  a.q + (long long)(row0 + tok) * a.q_row + (long long)h * a.q_head + dim0));
+            if (n < n_rows && sub == 0) lse = __ldg(a.lse + (size_t)h * a.total_q + row0 + tok);
+            float x[8];
+            unpack_bf16x8(raw, x);
+            float mx = 0.f;
+            bool finite = true;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              finite = finite && fabsf(x[k]) <= 3.402823466e38f;
+              mx = fmaxf(mx, fabsf(x[k]));
+            }
+            if (!finite) mx = __int_as_float(0x7f800000);
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1)
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const int e = terms_exponent(mx);
+            uint32_t hi[4], lo[4];
+            split_terms(x, e, hi, lo);
+            const int unit = dim0 >> 4;
+            const int us = D == 128 ? (unit ^ (n & 7)) : (unit ^ ((n >> 1) & 3));
+            uint8_t* at = q_s + n * D + us * 16 + (dim0 & 8);
+            *reinterpret_cast<uint2*>(at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+            *reinterpret_cast<uint2*>(at + N * D) =
+                make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+            if (sub == 0) {
+              // A row that sees nothing (LSE -inf), or that is none, adds 0.
+              const bool none = n >= n_rows || lse == neg_inf;
+              float* r = reinterpret_cast<float*>(cb->row + n / 2) + (n & 1);
+              r[0] = none ? 0.f : terms_scale(mx, e, a.scale_log2);
+              r[2] = none ? neg_inf : lse * -1.4426950408889634f;
+              cb->token[n] = n < n_rows ? tok - token_of(sh, c * N) : -1;
+            }
+          }
+          ptx::fence_proxy_async_smem();
+          ptx::mbar_arrive(ptx::smem_u32(&cb->q_full));
+          named_bar_sync(1, 128);
+        }
+        // ---- the tiles
+#pragma unroll 1
+        for (int t0 = 0; ok && t0 < g.count; t0 += 16) {
+          // Lane l: page l of 16 tiles, its scale, NaN where there is none.
+          float scale = __int_as_float(0x7fffffff);
+          const long long p = (long long)(g.tile0 + t0) * 2 + lane;
+          if (t0 + lane / 2 < g.count && p * kPageTokens < g.keys.hi) {
+            const int id = checked_page(
+                __ldg(a.page_table + (size_t)g.seq * a.max_pages + p), a.num_pages);
+            if (id >= 0) scale = __ldg(a.k_scale + (size_t)id * sh.heads_k + g.head);
+          }
+          const int end = imin(16, g.count - t0);
+#pragma unroll 1
+          for (int t = 0; t < end; ++t) {
+            const int j0 = (g.tile0 + t0 + t) * kTileKeys, j = j0 + key;
+            const bool here = j < g.keys.hi;
+            const float ks = __shfl_sync(0xffffffffu, scale, 2 * t + (warp >> 1));
+            const bool seen = wc.seen(j0);
+            // What stands there already, and whether it changes.
+            const bool add = c > 0 || (a.decay != 0.f && j < fresh);
+            if (!seen && (c > 0 || (add && a.decay == 1.f))) continue;
+            float old = 0.f;
+            if (here && add) old = out[j];
+            if (c == 0) old *= a.decay;
+            float sum = 0.f;
+            if (seen) {
+              const int sb = i & 1;
+              ok = wait(cb->s_full[sb], (i >> 1) & 1);
+              if (!ok) break;
+              ptx::tc_fence_after();
+              const bool all = wc.whole(j0, sh);
+              // Rows that see the key: tokens [lo, hi].
+              int lo = 0, hi = 0x7fffffff;
+              if (!all) {
+                const long long r = (long long)j - wc.at0;
+                if (sh.causal) lo = (int)(r > 0 ? (r < 0x7fffffff ? r : 0x7fffffff) : 0);
+                if (sh.window >= 0 && j >= sh.sinks) {
+                  const long long w = r + sh.window;
+                  hi = (int)(w < 0x7fffffff ? (w > -1 ? w : -1) : 0x7fffffff);
+                }
+              }
+              const uint64_t ks2 = ptx::f2_pack(ks, ks);
+              uint64_t acc[2] = {0ull, 0ull};
+#pragma unroll
+              for (int n0 = 0; n0 < N; n0 += 16) {
+                uint32_t s[16];
+                ptx::tmem_ld16(s_lane + sb * N + n0, s);
+                ptx::tmem_wait_ld();
+                ptx::reg_fence16(s);
+                if (n0 + 16 == N) {
+                  ptx::tc_fence_before();
+                  ptx::mbar_arrive(ptx::smem_u32(&cb->s_free[sb]));
+                }
+#pragma unroll
+                for (int n = 0; n < 16; n += 2) {
+                  const ulonglong2 f =
+                      *reinterpret_cast<const ulonglong2*>(cb->row + (n0 + n) / 2);
+                  const uint64_t s2 =
+                      ptx::f2_pack(__uint_as_float(s[n]), __uint_as_float(s[n + 1]));
+                  float u, v;
+                  ptx::f2_unpack(ptx::fma2(s2, ptx::mul2(f.x, ks2), f.y), u, v);
+                  if (!all) {
+                    const int2 tok = *reinterpret_cast<const int2*>(cb->token + n0 + n);
+                    u = tok.x >= lo && tok.x <= hi ? u : neg_inf;
+                    v = tok.y >= lo && tok.y <= hi ? v : neg_inf;
+                  }
+                  acc[(n >> 1) & 1] =
+                      ptx::add2(acc[(n >> 1) & 1], ptx::f2_pack(ptx::ex2(u), ptx::ex2(v)));
+                }
+              }
+              float u, v;
+              ptx::f2_unpack(ptx::add2(acc[0], acc[1]), u, v);
+              sum = u + v;
+              if (__isnanf(ks)) sum = 0.f;  // (no page)
+              ++i;
+            }
+            if (here) out[j] = old + sum;
+          }
+        }
+        // (A warp whose wait has given up joins the others here, and all leave.)
+        ok = named_bar_and(1, 128, ok);
+      }
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+}  // namespace fa

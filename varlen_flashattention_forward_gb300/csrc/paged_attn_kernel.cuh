@@ -790,19 +790,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
 #pragma unroll
                 for (int o = kLanes / 2; o > 0; o >>= 1)
                   mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                // mx in [2^e, 2^(e+1)) goes to [128, 256).  (Rows below 2^-100
-                // keep a smaller size; their scores are zero in fp32 all the
-                // same.)
-                const int e = imax((int)(__float_as_uint(mx) >> 23) - 127, -100);
-                const float f = __uint_as_float((uint32_t)(7 - e + 127) << 23);
+                const int e = terms_exponent(mx);
                 uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const float y0 = x[2 * k] * f, y1 = x[2 * k + 1] * f;
-                  hi[k] = pack_e4m3x2(y0, y1);
-                  const float2 h2 = f16x2_floats(unpack_e4m3x2(hi[k]));
-                  lo[k] = pack_e4m3x2(y0 - h2.x, y1 - h2.y);
-                }
+                split_terms(x, e, hi, lo);
                 // (Rows n and N + n have the same place in the swizzle.)
                 const int unit = dim0 >> 4;
                 const int us = D == 128 ? (unit ^ (n & 7)) : (unit ^ ((n >> 1) & 3));
@@ -812,10 +802,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
                 *reinterpret_cast<uint2*>(at + N * C::kRow) =
                     make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
                 if (sub == 0)
-                  cb->qs[seg % kPagedPlans][n] =
-                      mx < __int_as_float(0x7f800000)
-                          ? a.scale_log2 * __uint_as_float((uint32_t)(e - 7 + 127) << 23)
-                          : __int_as_float(0x7fffffff);
+                  cb->qs[seg % kPagedPlans][n] = terms_scale(mx, e, a.scale_log2);
               }
             }
             ptx::fence_proxy_async_smem();

@@ -267,15 +267,15 @@ __device__ __forceinline__ void mma_ss4_elect(uint32_t d_tmem, uint64_t a_desc, 
 
 // kSteps K=32 steps D (+)= A * B of 8-bit floats (kind::f8f6f4), both operands
 // K-major in shared memory, from one elected lane of a converged warp; the
-// first step overwrites D.  A step is 32 bytes further along each row.
-template <int kSteps>
+// first step overwrites D unless kAdd.  A step is 32 bytes further along each row.
+template <int kSteps, bool kAdd = false>
 __device__ __forceinline__ void mma_f8_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                              uint32_t idesc) {
   static_assert(kSteps == 2 || kSteps == 4, "64 or 128 bytes of a row");
   if constexpr (kSteps == 4) {
     asm volatile(
         "{\n\t.reg .pred e, one, zero;\n\t.reg .b64 da, db;\n\t"
-        "setp.eq.u32 one, 0, 0;\n\tsetp.ne.u32 zero, 0, 0;\n\t"
+        "setp.eq.u32 one, 0, 0;\n\tsetp.ne.u32 zero, %4, 0;\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, zero;\n\t"
         "add.s64 da, %1, 2;\n\tadd.s64 db, %2, 2;\n\t"
@@ -284,17 +284,17 @@ __device__ __forceinline__ void mma_f8_elect(uint32_t d_tmem, uint64_t a_desc, u
         "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, one;\n\t"
         "add.s64 da, %1, 6;\n\tadd.s64 db, %2, 6;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, one;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc)
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "n"(kAdd ? 1 : 0)
         : "memory");
   } else {
     asm volatile(
         "{\n\t.reg .pred e, one, zero;\n\t.reg .b64 da, db;\n\t"
-        "setp.eq.u32 one, 0, 0;\n\tsetp.ne.u32 zero, 0, 0;\n\t"
+        "setp.eq.u32 one, 0, 0;\n\tsetp.ne.u32 zero, %4, 0;\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, zero;\n\t"
         "add.s64 da, %1, 2;\n\tadd.s64 db, %2, 2;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, one;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc)
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "n"(kAdd ? 1 : 0)
         : "memory");
   }
 }
