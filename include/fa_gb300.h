@@ -651,6 +651,73 @@ fa_status fa_paged_key_weights(const void* q, long long q_row_stride, long long 
                                float decay, float* weights, int capacity, fa_stream_t stream);
 
 /*
+ * fa_paged_kv_select -- the keys of each sequence and kv head to keep: its first
+ * sink_tokens, its last recent_tokens, and of those between the ones with the
+ * largest weights, budget in all.
+ *
+ *   weights       fp32 [batch, num_heads_k, capacity], as fa_paged_key_weights
+ *                 keeps them; any numbers.  Of equal ones (-0 and 0 too) the
+ *                 lower position is kept; a NaN counts below all numbers.
+ *   seq_lens      int32 [batch], clamped to [0, capacity].
+ *   budget        at least 1 and at least sink_tokens + recent_tokens.
+ *   keep          int32 [batch, num_heads_k, budget], written: the kept
+ *                 positions in ascending order, -1 behind the last.  A sequence
+ *                 of at most `budget` keys keeps them all.
+ *   new_lens      int32 [batch], written: min(seq_len, budget).  It may be
+ *                 another buffer than seq_lens only.
+ *
+ * Host errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED (sizes past 32-bit
+ * indices), FA_ERR_ARCH, FA_ERR_LAUNCH.
+ */
+fa_status fa_paged_kv_select(const float* weights, const int* seq_lens, int batch, int num_heads_k,
+                             int capacity, int budget, int sink_tokens, int recent_tokens,
+                             int* keep, int* new_lens, fa_stream_t stream);
+
+/*
+ * fa_paged_kv_compact -- moves rows of the cache together, in place: slot
+ * first[b] + j of sequence b gets, for each kv head, the key and the value of
+ * slot keep[b, h, j], j < counts[b].  After fa_paged_kv_select with its keep and
+ * new_lens (first = NULL), or for the accepted path of a drafted tree (first:
+ * where its nodes start, keep: the slots of the path's nodes, one list for all
+ * heads); first[b] + counts[b] is then the sequence's length.
+ *
+ *   keep          int32 [batch, keep_heads, keep_row], keep_heads 1 (all heads
+ *                 alike) or num_heads_k.  A row comes from its own slot or one
+ *                 behind it: an entry below first[b] + j, past the table's pages
+ *                 or on a page that is not in the cache gives a row of zeros.
+ *                 Slots may be named several times.
+ *   first         int32 [batch] or NULL (0); negative counts as 0.
+ *   counts        int32 [batch], clamped to [0, keep_row] and to the slots of
+ *                 the page table.
+ *   weights       fp32 [batch, num_heads_k, capacity] or NULL: moved along with
+ *                 the keys (below capacity; of a row of zeros 0).
+ *
+ * Scale of a (page, head) whose rows move: the smallest power of two that holds
+ * its finite new rows (as fa_paged_kv_append's), or for the page of first[b],
+ * where earlier slots stay, the larger of that and its old one; codes are
+ * rounded to it once, exactly but for bits below its smallest code.  A page none
+ * of whose rows moves (keep names each its own slot) is left as it is, for that
+ * head; slots behind the last row keep their codes.  Page ids that name no page
+ * are not written.
+ *
+ * Nothing of it moves a key's rotation: a key keeps the angle of the position
+ * that it was stored with.  Further keys go in with cos_sin = NULL, rotated by
+ * fa_qk_norm_rope at the position the caller counts, and causal masks and
+ * windows count slots from then on.
+ *
+ * A page that moves may belong to one sequence of a call only (as for
+ * fa_paged_kv_append); shared pages are safe where their rows stay.
+ *
+ * Host errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED (head_dim, sizes past
+ * 32-bit indices), FA_ERR_ARCH, FA_ERR_LAUNCH.
+ */
+fa_status fa_paged_kv_compact(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                              const int* page_table, const int* keep, const int* first,
+                              const int* counts, int batch, int num_heads_k, int keep_heads,
+                              int keep_row, int head_dim, int num_pages, int max_pages_per_seq,
+                              float* weights, int capacity, fa_stream_t stream);
+
+/*
  * fa_paged_kv_gather -- the first n = cu_seqlens[b + 1] - cu_seqlens[b]
  * cached tokens of every sequence as packed bf16 tensors, the k and v (with
  * cu_seqlens as cu_seqlens_k) of a fa_varlen_fwd call: a long chunk of

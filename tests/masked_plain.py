@@ -149,3 +149,86 @@ def key_weights(q, lse, kc, ks, cu, lens, pages, sums, scale, causal=True, windo
                     out[b, hk, :keys][seen] += p
                     tol[b, hk, :keys][seen] += p * (err + (n * (H // hks) + 8) * 2.0 ** -23)
     return out, tol + 1e-37
+
+
+def select(sums, lens, budget, sinks, recent):
+    """(keep, new lengths), by sorting."""
+    batch, hk, cap = sums.shape
+    keep = torch.full((batch, hk, budget), -1, dtype=torch.int32)
+    new = []
+    for b, n in enumerate(lens):
+        n = min(max(n, 0), cap)
+        new.append(min(n, budget))
+        for h in range(hk):
+            if n <= budget:
+                kept = list(range(n))
+            else:
+                x = [-math.inf if v != v else v for v in sums[b, h, :n].tolist()]
+                nan = [v != v for v in sums[b, h, :n].tolist()]
+                order = sorted(range(sinks, n - recent), key=lambda j: (nan[j], -x[j], j))
+                kept = sorted(list(range(sinks)) + list(range(n - recent, n))
+                              + order[:budget - sinks - recent])
+            keep[b, h, :len(kept)] = torch.tensor(kept, dtype=torch.int32)
+    return keep, torch.tensor(new, dtype=torch.int32)
+
+
+def compact(codes, scale, pages, keep, first, counts):
+    """fp64 codes and scales after the move, page by page from the values
+    before it; codes [pages, Hk, 64, d] fp64 (NaN codes as NaN)."""
+    num, hks, _, d = codes.shape
+    was, factor = codes.clone(), scale.clone()
+    codes, scale = codes.clone(), scale.clone()
+    width = pages.shape[1]
+    for b in range(pages.shape[0]):
+        f = max(int(first[b]), 0)
+        n = min(max(int(counts[b]), 0), keep.shape[2], max(width * 64 - f, 0))
+        for h in range(hks):
+            src = keep[b, h if keep.shape[1] > 1 else 0].tolist()
+            slot = f
+            while slot < f + n:
+                off, m = slot % 64, min(64 - slot % 64, f + n - slot)
+                page = int(pages[b, slot // 64])
+                rows = torch.zeros((m, d), dtype=torch.float64)
+                moved = False
+                for i in range(m):
+                    s = src[slot - f + i]
+                    moved |= s != slot + i
+                    if s < slot + i or s >= width * 64:
+                        continue
+                    p = int(pages[b, s // 64])
+                    if 0 <= p < num:
+                        rows[i] = was[p, h, s % 64] * factor[p, h]
+                if moved and 0 <= page < num:
+                    mag = torch.where(torch.isnan(rows), 0.0, rows.abs())
+                    new = plain.page_scale(mag.amax())
+                    if off:
+                        new = torch.maximum(new, factor[page, h])
+                        if new > factor[page, h]:
+                            codes[page, h, :off] = plain.e4m3(was[page, h, :off] * factor[page, h] / new)
+                    codes[page, h, off:off + m] = plain.e4m3(rows / new)
+                    scale[page, h] = new
+                slot += m
+    return codes, scale
+
+
+def move_weights(sums, keep, first, counts, pages, num):
+    """Sums after the move; a row of zeros (an entry that names no slot at its
+    own or behind it, on a page of the cache) has 0."""
+    out = sums.clone()
+    batch, hks, cap = sums.shape
+    slots = pages.shape[1] * 64
+    for b in range(batch):
+        f = max(int(first[b]), 0)
+        n = min(max(int(counts[b]), 0), keep.shape[2], max(slots - f, 0))
+        for h in range(hks):
+            src = keep[b, h if keep.shape[1] > 1 else 0].tolist()
+            for p0 in range(f // 64 * 64, f + n, 64):
+                at = [d for d in range(max(p0, f), min(p0 + 64, f + n))]
+                if all(src[d - f] == d for d in at):
+                    continue
+                for d in at:
+                    if d < cap:
+                        s = src[d - f]
+                        here = d <= s < min(cap, slots) and 0 <= int(pages[b, s // 64]) < num
+                        out[b, h, d] = sums[b, h, s] if here else 0.0
+    return out

@@ -214,3 +214,103 @@ def test_python_refuses_packed_masks(lib):
                  torch.zeros((3, 0), dtype=torch.int32)):
         with pytest.raises((TypeError, ValueError)):
             fa.fa_varlen_fwd(q, q, q, cu, cu, tree_mask=mask)
+
+
+# ---------------------------------------------------------------- eviction
+def weights(lib, **kw):
+    a = dict(q=P(0x7000), qr=256, qh=64, lse=P(0x9000), kc=P(0x1000), ks=P(0x3000), cu=P(0x5000),
+             sl=P(0x8000), pt=P(0x6000), B=2, T=4, H=4, Hk=2, d=64, pages=8, width=4, scale=0.125,
+             causal=1, wl=-1, sinks=0, decay=1.0, w=P(0xa000), cap=256)
+    a.update(kw)
+    return lib.fa_paged_key_weights(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(q=None), INV), (dict(lse=None), INV), (dict(kc=None), INV), (dict(ks=None), INV),
+    (dict(cu=None), INV), (dict(sl=None), INV), (dict(pt=None), INV), (dict(w=None), INV),
+    (dict(B=0), INV), (dict(T=-1), INV), (dict(H=3), INV), (dict(Hk=0), INV), (dict(wl=-2), INV),
+    (dict(sinks=-1), INV), (dict(decay=-0.1), INV), (dict(decay=1.5), INV),
+    (dict(decay=float("nan")), INV), (dict(cap=0), INV), (dict(scale=0.0), INV),
+    (dict(w=P(0xa002)), INV), (dict(lse=P(0x9001)), INV), (dict(q=P(0x7008)), INV),
+    (dict(qh=60), INV), (dict(d=72), UNS), (dict(width=2 ** 25), UNS),
+])
+def test_weights_refusals(lib, kw, expect):
+    assert weights(lib, **kw) == expect
+
+
+def select(lib, **kw):
+    a = dict(w=P(0x1000), sl=P(0x2000), B=2, Hk=2, cap=256, budget=64, sinks=4, recent=16,
+             keep=P(0x3000), new=P(0x4000))
+    a.update(kw)
+    return lib.fa_paged_kv_select(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(w=None), INV), (dict(sl=None), INV), (dict(keep=None), INV), (dict(new=None), INV),
+    (dict(B=0), INV), (dict(Hk=0), INV), (dict(cap=0), INV), (dict(budget=0), INV),
+    (dict(sinks=-1), INV), (dict(recent=-1), INV), (dict(sinks=60), INV),
+    (dict(sinks=2 ** 31 - 1, recent=2 ** 31 - 1), INV), (dict(w=P(0x1002)), INV),
+    (dict(keep=P(0x3001)), INV), (dict(B=2 ** 30, Hk=4), UNS), (dict(cap=2 ** 31 - 1), UNS),
+    (dict(budget=2 ** 31 - 1), UNS),
+])
+def test_select_refusals(lib, kw, expect):
+    assert select(lib, **kw) == expect
+
+
+def compact(lib, **kw):
+    a = dict(kc=P(0x1000), vc=P(0x2000), ks=P(0x3000), vs=P(0x4000), pt=P(0x5000), keep=P(0x6000),
+             first=P(0x7000), counts=P(0x8000), B=2, Hk=2, heads=2, row=64, d=64, pages=8, width=4,
+             w=P(0x9000), cap=256)
+    a.update(kw)
+    return lib.fa_paged_kv_compact(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(kc=None), INV), (dict(vc=None), INV), (dict(ks=None), INV), (dict(vs=None), INV),
+    (dict(pt=None), INV), (dict(keep=None), INV), (dict(counts=None), INV), (dict(B=0), INV),
+    (dict(Hk=0), INV), (dict(heads=3), INV), (dict(heads=0), INV), (dict(row=-1), INV),
+    (dict(pages=0), INV), (dict(width=0), INV), (dict(cap=0), INV), (dict(kc=P(0x1008)), INV),
+    (dict(keep=P(0x6002)), INV), (dict(first=P(0x7001)), INV), (dict(counts=P(0x8002)), INV),
+    (dict(w=P(0x9001)), INV), (dict(d=72), UNS), (dict(width=2 ** 25), UNS),
+    (dict(B=2 ** 27), UNS),
+])
+def test_compact_refusals(lib, kw, expect):
+    assert compact(lib, **kw) == expect
+
+
+def test_valid_eviction_calls_fail_only_for_want_of_a_gpu(lib):
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    none = (fa.FA_ERR_LAUNCH, fa.FA_ERR_ARCH)
+    assert weights(lib) in none and weights(lib, T=0, q=None, lse=None) in none
+    assert select(lib) in none and select(lib, budget=20) in none
+    assert compact(lib) in none and compact(lib, first=None, w=None, cap=0, heads=1) in none
+
+
+def test_python_refuses_eviction_arguments(lib):
+    t = tensors()
+    kc, vc, ks, vs = t["cache"]
+    w = torch.zeros((1, 2, 128))
+    lse = torch.zeros((4, 3))
+    keep = torch.zeros((1, 2, 3), dtype=torch.int32)
+    bad = (TypeError, ValueError)
+    for fn in (lambda: fa.fa_paged_key_weights(t["q"], lse[:3], kc, ks, t["cu"], t["lens"], t["pt"], w),
+               lambda: fa.fa_paged_key_weights(t["q"], lse, kc, ks, t["cu"], t["lens"], t["pt"], w[0]),
+               lambda: fa.fa_paged_key_weights(t["q"], lse, kc, ks, t["cu"], t["lens"], t["pt"],
+                                               w.double()),
+               lambda: fa.fa_paged_kv_select(w, t["lens"].long(), 5),
+               lambda: fa.fa_paged_kv_select(w[0], t["lens"], 5),
+               lambda: fa.fa_paged_kv_select(w, t["lens"].expand(2), 5),
+               lambda: fa.fa_paged_kv_compact(*t["cache"], t["pt"], keep[0], t["lens"]),
+               lambda: fa.fa_paged_kv_compact(*t["cache"], t["pt"], keep.expand(2, 2, 3), t["lens"]),
+               lambda: fa.fa_paged_kv_compact(*t["cache"], t["pt"], keep, t["lens"].long()),
+               lambda: fa.fa_paged_kv_compact(*t["cache"], t["pt"], keep, t["lens"], weights=w[0]),
+               lambda: fa.fa_paged_kv_compact(*t["cache"], t["pt"], keep, t["lens"],
+                                              first=t["cu"])):
+        with pytest.raises(bad):
+            fn()
+    for fn in (lambda: fa.fa_paged_key_weights(t["q"], lse, kc, ks, t["cu"], t["lens"], t["pt"], w),
+               lambda: fa.fa_paged_kv_select(w, t["lens"], 5),
+               lambda: fa.fa_paged_kv_compact(*t["cache"], t["pt"], keep, t["lens"])):
+        with pytest.raises(ValueError, match="CUDA"):
+            fn()

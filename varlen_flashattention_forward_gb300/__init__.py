@@ -36,6 +36,10 @@ Entry points (same names as the C ABI):
   fa_paged_key_weights(q, lse, k_cache, k_scale, cu_seqlens_q, seq_lens, page_table, weights,
                        softmax_scale=None, causal=True, window_left=-1, sink_tokens=0, decay=1.0,
                        stream=None)
+  fa_paged_kv_select(weights, seq_lens, budget, sink_tokens=0, recent_tokens=0, keep=None,
+                     new_lens=None, stream=None)
+  fa_paged_kv_compact(k_cache, v_cache, k_scale, v_scale, page_table, keep, counts, first=None,
+                      weights=None, stream=None)
   fa_paged_kv_gather(k_cache, v_cache, k_scale, v_scale, cu_seqlens, page_table, total_k,
                      k_out=None, v_out=None, stream=None)
   fa_get_device_status()
@@ -65,8 +69,8 @@ EXPORTS = ("fa_varlen_fwd", "fa_varlen_fwd_plan", "fa_varlen_fwd_strided", "fa_v
            "fa_sparse_mla_decode",
            "fa_sparse_mla_decode_plan", "fa_sparse_mla_decode_noalloc", "fa_merge_attn_states",
            "fa_qk_norm_rope", "fa_paged_kv_append", "fa_paged_attn", "fa_paged_attn_plan",
-           "fa_paged_attn_masked", "fa_draft_tree", "fa_paged_key_weights", "fa_paged_kv_gather",
-           "fa_get_device_status",
+           "fa_paged_attn_masked", "fa_draft_tree", "fa_paged_key_weights", "fa_paged_kv_select",
+           "fa_paged_kv_compact", "fa_paged_kv_gather", "fa_get_device_status",
            "fa_set_wait_limit_ns", "fa_status_string")
 
 _lib = None
@@ -135,6 +139,11 @@ def load_library():
     lib.fa_paged_key_weights.argtypes = [p, i64, i64, p, p, p, p, p, p, i32, i32, i32, i32, i32, i32,
                                          i32, f32, i32, i32, i32, f32, p, i32, p]
     lib.fa_paged_key_weights.restype = i32
+    lib.fa_paged_kv_select.argtypes = [p, p, i32, i32, i32, i32, i32, i32, p, p, p]
+    lib.fa_paged_kv_select.restype = i32
+    lib.fa_paged_kv_compact.argtypes = [p, p, p, p, p, p, p, p, i32, i32, i32, i32, i32, i32, i32, p,
+                                        i32, p]
+    lib.fa_paged_kv_compact.restype = i32
     lib.fa_paged_attn_plan.argtypes = [i32, i32, i32, i32, i32, i32, pi, pi,
                                        ctypes.POINTER(size)]
     lib.fa_paged_attn_plan.restype = i32
@@ -449,8 +458,9 @@ def _check_rope(cos_sin, weights, d):
     return cos_sin.shape[1], cos_sin.shape[0]
 
 
-def _check_cache(k_cache, v_cache, k_scale, v_scale, cu_seqlens, page_table):
-    """(batch, pages, kv heads, head dim, pages of a sequence) of a cache."""
+def _check_cache(k_cache, v_cache, k_scale, v_scale, cu_seqlens, page_table, batch=None):
+    """(batch, pages, kv heads, head dim, pages of a sequence) of a cache; batch
+    is that of cu_seqlens unless given (cu_seqlens is then any int32 array)."""
     import torch
     f8, f32, i32 = torch.float8_e4m3fn, torch.float32, torch.int32
     # (In one expression: these calls are made at every decode step.)
@@ -477,7 +487,7 @@ def _check_cache(k_cache, v_cache, k_scale, v_scale, cu_seqlens, page_table):
         _shape(k_scale, "k_scale", scales)
         _shape(v_scale, "v_scale", scales)
     rows, width = page_table.shape
-    batch = cu_seqlens.shape[0] - 1
+    batch = cu_seqlens.shape[0] - 1 if batch is None else batch
     if rows != batch:
         raise ValueError("page_table must have one row per sequence")
     return batch, pages, hk, d, width
@@ -807,6 +817,79 @@ def fa_paged_key_weights(q, lse, k_cache, k_scale, cu_seqlens_q, seq_lens, page_
             decay, weights.data_ptr(), capacity, _raw_stream(index))
     if st != FA_OK:
         raise FaError(st, "fa_paged_key_weights")
+
+
+def fa_paged_kv_select(weights, seq_lens, budget, sink_tokens=0, recent_tokens=0, keep=None,
+                       new_lens=None, stream=None):
+    """The keys to keep: the first sink_tokens, the last recent_tokens and those
+    of the largest weights between, budget in all; see fa_paged_kv_select in
+    include/fa_gb300.h.
+
+    weights [batch, H_k, capacity] fp32, seq_lens [batch] int32.  Returns (keep
+    [batch, H_k, budget] int32, ascending, -1 behind the last; new_lens [batch]
+    int32).
+    """
+    import torch
+    lib = load_library()
+    i32 = torch.int32
+    _check(weights, "weights", torch.float32, 3)
+    _check(seq_lens, "seq_lens", i32, 1)
+    batch, hk, capacity = weights.shape
+    _shape(seq_lens, "seq_lens", (batch,))
+    budget = _sinks(budget)
+    index, here = _device(stream, weights, seq_lens, keep, new_lens)
+    with here:
+        if keep is None:
+            keep = torch.empty((batch, hk, max(budget, 0)), dtype=i32, device=weights.device)
+        else:
+            _check(keep, "keep", i32, 3)
+            _shape(keep, "keep", (batch, hk, budget))
+        if new_lens is None:
+            new_lens = torch.empty((batch,), dtype=i32, device=weights.device)
+        else:
+            _check(new_lens, "new_lens", i32, 1)
+            _shape(new_lens, "new_lens", (batch,))
+            if new_lens.data_ptr() == seq_lens.data_ptr():
+                raise ValueError("new_lens must be another tensor than seq_lens")
+        st = lib.fa_paged_kv_select(weights.data_ptr(), seq_lens.data_ptr(), batch, hk, capacity,
+                                    budget, _sinks(sink_tokens), _sinks(recent_tokens), _p(keep),
+                                    new_lens.data_ptr(), _raw_stream(index))
+    if st != FA_OK:
+        raise FaError(st, "fa_paged_kv_select")
+    return keep, new_lens
+
+
+def fa_paged_kv_compact(k_cache, v_cache, k_scale, v_scale, page_table, keep, counts, first=None,
+                        weights=None, stream=None):
+    """Moves rows of the cache together, in place: slot first[b] + j of sequence
+    b gets slot keep[b, h, j], j < counts[b]; see fa_paged_kv_compact in
+    include/fa_gb300.h.
+
+    keep [batch, H_k or 1, n] int32 (ascending), counts and first [batch] int32
+    (first None: 0), weights [batch, H_k, capacity] fp32 or None, moved along.
+    """
+    import torch
+    lib = load_library()
+    _check(counts, "counts", torch.int32, 1)
+    batch, pages, hk, d, width = _check_cache(k_cache, v_cache, k_scale, v_scale, counts,
+                                              page_table, batch=counts.shape[0])
+    _check(keep, "keep", torch.int32, 3)
+    heads, row = keep.shape[1:]
+    if keep.shape[0] != batch or heads not in (1, hk):
+        raise ValueError(f"keep must have shape ({batch}, {hk} or 1, n), got {tuple(keep.shape)}")
+    if first is not None:
+        _check(first, "first", torch.int32, 1)
+        _shape(first, "first", (batch,))
+    capacity = 0 if weights is None else _check_weights(weights, batch, hk)
+    index, here = _device(stream, k_cache, v_cache, k_scale, v_scale, page_table, keep, counts,
+                          first, weights)
+    with here:
+        st = lib.fa_paged_kv_compact(
+            k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            page_table.data_ptr(), keep.data_ptr(), _p(first), counts.data_ptr(), batch, hk, heads,
+            row, d, pages, width, _p(weights), capacity, _raw_stream(index))
+    if st != FA_OK:
+        raise FaError(st, "fa_paged_kv_compact")
 
 
 def fa_set_wait_limit_ns(ns: int) -> None:

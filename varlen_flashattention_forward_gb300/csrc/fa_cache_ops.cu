@@ -5,12 +5,14 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 
 #include <cuda_runtime.h>
 
 #include "draft_tree_kernel.cuh"
 #include "host_common.h"
 #include "key_weights_kernel.cuh"
+#include "kv_evict_kernels.cuh"
 #include "paged_host.h"
 
 using fa::is_aligned;
@@ -143,4 +145,86 @@ extern "C" fa_status fa_paged_key_weights(
     if (e != cudaSuccess) return FA_ERR_LAUNCH;
   }
   return FA_OK;
+}
+
+extern "C" fa_status fa_paged_kv_select(const float* weights, const int* seq_lens, int batch,
+                                        int num_heads_k, int capacity, int budget, int sink_tokens,
+                                        int recent_tokens, int* keep, int* new_lens,
+                                        fa_stream_t stream) {
+  if (!weights || !seq_lens || !keep || !new_lens) return FA_ERR_INVALID_ARG;
+  if (batch < 1 || num_heads_k < 1 || capacity < 1 || budget < 1 || sink_tokens < 0 ||
+      recent_tokens < 0 || (int64_t)sink_tokens + recent_tokens > budget)
+    return FA_ERR_INVALID_ARG;
+  if (!is_aligned(weights, 4) || !is_aligned(seq_lens, 4) || !is_aligned(keep, 4) ||
+      !is_aligned(new_lens, 4))
+    return FA_ERR_INVALID_ARG;
+  if ((int64_t)batch * num_heads_k > INT32_MAX || capacity > INT32_MAX - fa::kSelectThreads ||
+      budget > INT32_MAX - fa::kSelectThreads)
+    return FA_ERR_UNSUPPORTED;
+  fa::DeviceFacts dev;
+  const fa_status st = fa::device_facts(&dev);
+  if (st != FA_OK) return st;
+  const fa::KvSelectArgs a = {weights, seq_lens,    num_heads_k,   capacity,
+                              budget,  sink_tokens, recent_tokens, keep, new_lens};
+  fa::kv_select_kernel<<<batch * num_heads_k, fa::kSelectThreads, 0,
+                         reinterpret_cast<cudaStream_t>(stream)>>>(a);
+  return launched();
+}
+
+extern "C" fa_status fa_paged_kv_compact(void* k_cache, void* v_cache, float* k_scale,
+                                         float* v_scale, const int* page_table, const int* keep,
+                                         const int* first, const int* counts, int batch,
+                                         int num_heads_k, int keep_heads, int keep_row, int head_dim,
+                                         int num_pages, int max_pages_per_seq, float* weights,
+                                         int capacity, fa_stream_t stream) {
+  if ((keep_row > 0 && !keep) || !counts) return FA_ERR_INVALID_ARG;
+  fa_status st = fa::check_cache(k_cache, v_cache, k_scale, v_scale, counts, page_table, batch, 0,
+                                 num_heads_k, head_dim, num_pages, max_pages_per_seq);
+  if (st != FA_OK) return st;
+  if (keep_row < 0 || (keep_heads != 1 && keep_heads != num_heads_k) || (weights && capacity < 1))
+    return FA_ERR_INVALID_ARG;
+  if (!is_aligned(keep, 4) || !is_aligned(first, 4) || !is_aligned(weights, 4))
+    return FA_ERR_INVALID_ARG;
+  const int64_t units = 2ll * batch * num_heads_k;
+  if (units * 8 > INT32_MAX) return FA_ERR_UNSUPPORTED;
+  fa::DeviceFacts dev;
+  st = fa::device_facts(&dev);
+  if (st != FA_OK) return st;
+  if (keep_row == 0) return FA_OK;
+  fa::KvCompactArgs a;
+  a.page_table = page_table;
+  a.keep = keep;
+  a.first = first;
+  a.counts = counts;
+  a.batch = batch;
+  a.heads = num_heads_k;
+  a.keep_heads = keep_heads;
+  a.keep_row = keep_row;
+  a.dim = head_dim;
+  a.max_pages = max_pages_per_seq;
+  a.num_pages = num_pages;
+  a.cache[0] = static_cast<uint8_t*>(k_cache);
+  a.cache[1] = static_cast<uint8_t*>(v_cache);
+  a.scale[0] = k_scale;
+  a.scale[1] = v_scale;
+  a.weights = weights;
+  a.capacity = weights ? capacity : 0;
+  // CTAs of a cluster: more while all units' are resident at once (four an SM)
+  // and have a page each.
+  const int pages = (int)std::min<int64_t>(((int64_t)keep_row + 126) / 64, max_pages_per_seq);
+  int ctas = 8;
+  while (ctas > 1 && (units * ctas > 4ll * dev.sm_count || ctas / 2 >= pages)) ctas /= 2;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = dim3((unsigned)(units * ctas));
+  cfg.blockDim = dim3(fa::kCompactThreads);
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fa::kv_compact_kernel, a) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
