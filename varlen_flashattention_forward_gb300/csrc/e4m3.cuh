@@ -16,13 +16,11 @@ constexpr int kScaleExpMax = 64;
 
 // Smallest power of two s with amax <= 448 s, clamped (amax finite, >= 0).
 __device__ __forceinline__ float scale_for(float amax) {
-  // amax / 512 = m 2^e with m in [0.5, 1), and 448 = 512 * 0.875.
-  int e;
-  const float m = frexpf(amax * (1.f / 512.f), &e);
-  if (m > 0.875f) ++e;
-  if (!(amax > 0.f)) e = -kScaleExpMax;
+  // amax = 1.m 2^e and 448 = 1.75 2^8.  (Below 2^-126 the exponent is clamped.)
+  const uint32_t u = __float_as_uint(amax);
+  int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
   e = imin(imax(e, -kScaleExpMax), kScaleExpMax);
-  return ldexpf(1.f, e);
+  return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
 // Two fp32 values as e4m3 codes (round to nearest even, saturating at 448,

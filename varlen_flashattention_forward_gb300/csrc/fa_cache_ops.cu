@@ -166,9 +166,31 @@ extern "C" fa_status fa_paged_kv_select(const float* weights, const int* seq_len
   if (st != FA_OK) return st;
   const fa::KvSelectArgs a = {weights, seq_lens,    num_heads_k,   capacity,
                               budget,  sink_tokens, recent_tokens, keep, new_lens};
-  fa::kv_select_kernel<<<batch * num_heads_k, fa::kSelectThreads, 0,
-                         reinterpret_cast<cudaStream_t>(stream)>>>(a);
-  return launched();
+  // CTAs of a cluster: what holds a row's keys in registers, and more while each
+  // keeps 2048 and all are resident at once.
+  const int64_t units = (int64_t)batch * num_heads_k;
+  constexpr int kHeld = fa::kSelectThreads * fa::kSelectItems;
+  int ctas = 1;
+  while (ctas < fa::kSelectCtas && ((int64_t)ctas * kHeld < capacity ||
+                      (units * ctas <= dev.sm_count && capacity / ctas > 2048)))
+    ctas *= 2;
+  if (units * ctas > INT32_MAX) return FA_ERR_UNSUPPORTED;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = dim3((unsigned)(units * ctas));
+  cfg.blockDim = dim3(fa::kSelectThreads);
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = (int64_t)ctas * kHeld >= capacity
+                            ? cudaLaunchKernelEx(&cfg, fa::kv_select_kernel<fa::kSelectItems>, a)
+                            : cudaLaunchKernelEx(&cfg, fa::kv_select_kernel<0>, a);
+  return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
 extern "C" fa_status fa_paged_kv_compact(void* k_cache, void* v_cache, float* k_scale,
@@ -210,10 +232,11 @@ extern "C" fa_status fa_paged_kv_compact(void* k_cache, void* v_cache, float* k_
   a.weights = weights;
   a.capacity = weights ? capacity : 0;
   // CTAs of a cluster: more while all units' are resident at once (four an SM)
-  // and have a page each.
-  const int pages = (int)std::min<int64_t>(((int64_t)keep_row + 126) / 64, max_pages_per_seq);
+  // and have pages of their own.
+  const int64_t pages = std::min<int64_t>(((int64_t)keep_row + 126) / 64, max_pages_per_seq);
   int ctas = 8;
-  while (ctas > 1 && (units * ctas > 4ll * dev.sm_count || ctas / 2 >= pages)) ctas /= 2;
+  while (ctas > 1 && (units * ctas > 4ll * dev.sm_count || ctas / 2 * fa::kCompactPages >= pages))
+    ctas /= 2;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof cfg);
   cfg.gridDim = dim3((unsigned)(units * ctas));

@@ -374,7 +374,7 @@ extern "C" fa_status fa_paged_attn_masked(
   const long long row_tiles = (long long)total_q * group / l.rows;
   const long long fit = fa::kMaxCost / per_row_tile - row_tiles;
   // (Sinks say nothing without a window.)
-  const bool masked = tree_words > 0 || (sink_tokens > 0 && window_left >= 0);
+  const bool sinks = sink_tokens > 0 && window_left >= 0;
   if (fit < 1) return FA_ERR_UNSUPPORTED;
   const int step = (int)std::min<long long>(fa::kPagedMaxBatch, fit);
   for (int b0 = 0; b0 < batch; b0 += step) {
@@ -382,9 +382,10 @@ extern "C" fa_status fa_paged_attn_masked(
     a.cu = cu_seqlens_q + b0;
     a.seq_lens = seq_lens + b0;
     a.page_table = page_table + (size_t)b0 * max_pages_per_seq;
-    const cudaError_t e = masked ? fa::launch_attn_masked(l.dim, l.rows, k_map, v_map, a, l.grid, s)
-                                 : fa::launch_attn_shape<false>(l.dim, l.rows, k_map, v_map, a,
-                                                                l.grid, s);
+    const cudaError_t e =
+        tree_words > 0 ? fa::launch_attn_tree(l.dim, l.rows, k_map, v_map, a, l.grid, s)
+        : sinks        ? fa::launch_attn_sinks(l.dim, l.rows, k_map, v_map, a, l.grid, s)
+                       : fa::launch_attn_shape<fa::kNoMask>(l.dim, l.rows, k_map, v_map, a, l.grid, s);
     if (e != cudaSuccess) return FA_ERR_LAUNCH;
   }
   return FA_OK;

@@ -1,0 +1,11 @@
+// Instantiations of the paged attention kernel for rows that are nodes of a tree.
+#include "paged_launch.cuh"
+
+namespace fa {
+
+cudaError_t launch_attn_tree(int dim, int rows, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                             const PagedAttnArgs& a, int grid, cudaStream_t stream) {
+  return launch_attn_shape<kTreeMask>(dim, rows, k_map, v_map, a, grid, stream);
+}
+
+}  // namespace fa

@@ -283,8 +283,9 @@ __global__ void __launch_bounds__(kWeightThreads, WeightsCfg<D, N>::kResident)
           ptx::tc_fence_after();
           const uint64_t kd =
               ptx::smem_desc(ptx::smem_u32(smem + s * C::kTileBytes), 16, 8 * D, C::kSwK);
-          ptx::mma_f8_elect<D / 32>(tmem + sb * N, kd, q_hi, idesc);
-          ptx::mma_f8_elect<D / 32, true>(tmem + sb * N, kd, q_lo, idesc);
+          // (The small terms first: each step rounds at the sum's size so far.)
+          ptx::mma_f8_elect<D / 32>(tmem + sb * N, kd, q_lo, idesc);
+          ptx::mma_f8_elect<D / 32, true>(tmem + sb * N, kd, q_hi, idesc);
           ptx::mma_commit_elect(ptx::smem_u32(&cb->s_full[sb]));
           ptx::mma_commit_elect(ptx::smem_u32(&cb->k_free[s]));
           ++i;

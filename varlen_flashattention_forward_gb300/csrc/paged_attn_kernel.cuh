@@ -274,14 +274,16 @@ __device__ __forceinline__ float warp_transpose_reduce16(float* x, int lane) {
 // for each key) where another one that it joins is down to 2^-57.
 __device__ __forceinline__ float root_ex2(float d) { return ptx::ex2(0.5f * d); }
 
-// kMasked: keys that a sliding window leaves behind but for the first ones
-// (shape.sinks), and rows that are nodes of a tree (shape.tree).  The other
-// instantiations are as if there were neither.
-template <int D, int N, bool kMasked>
+// kMask: kSinkMask for keys that a sliding window leaves behind but for the first
+// ones (shape.sinks), kTreeMask for rows that are nodes of a tree (shape.tree) as
+// well.  An instantiation is as if there were nothing else.
+constexpr int kNoMask = 0, kSinkMask = 1, kTreeMask = 2;
+template <int D, int N, int kMask>
 __global__ void __launch_bounds__(kPagedThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap k_map,
                       const __grid_constant__ CUtensorMap v_map, const PagedAttnArgs a) {
   using C = PagedCfg<D, N>;
+  constexpr bool kMasked = kMask != kNoMask, kTree = kMask == kTreeMask;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -678,8 +680,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
               plan.lse[lane] = row_h * a.total_q + row_q;
               plan.token[lane] = tok - token_of(sh, g.row_tile * N);
             }
-            if constexpr (kMasked) {
-              if (sh.tree) {
+            if constexpr (kTree) {
+              {
                 // The nodes' depths: the bits of their masks, less their own.
                 // (A row past the last has the first row's mask.)
                 const int at = (lane < rows ? row_q : g.q.lo) * a.tree_words;
@@ -720,7 +722,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             plan.rows = rows;
             plan.tok0 = token_of(sh, row0);
             plan.tok1 = token_of(sh, row0 + rows - 1);
-            plan.at0 = (long long)g.len - g.q.n + (kMasked && sh.tree ? 0 : plan.tok0);
+            plan.at0 = (long long)g.len - g.q.n + (kTree ? 0 : plan.tok0);
             plan.tiles = g.count;
             plan.whole = g.count == g.unit_count;
             plan.unit_end =
@@ -954,6 +956,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       const int count = plan.count, tile0 = plan.tile0, rows = plan.rows;
       const int tok0 = plan.tok0, tok1 = plan.tok1;
       const long long at0 = plan.at0;
+      const int gap_at = kMasked ? plan.gap_at : 0, gap = kMasked ? plan.gap : 0;
+      const int sink = kMasked ? plan.sink : 0, deepest = kTree ? plan.deepest : 0;
       if (plan.first) seg0 = i;
       // This warpgroup's first tile of the batch and of the segment.
       const int first = (i & 1) == wg ? 0 : 1;
@@ -1004,8 +1008,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
           const PagePlan pp = plan.page[2 * t + page];
           lv = pp.lv;
           const int j0 =
-              (tile0 + t + (kMasked && t >= plan.gap_at ? plan.gap : 0)) * kTileKeys;
-          const bool seen = (j0 + key >= plan.lo || (kMasked && j0 + key < plan.sink)) &&
+              (tile0 + t + (kMasked && t >= gap_at ? gap : 0)) * kTileKeys;
+          const bool seen = (j0 + key >= plan.lo || (kMasked && j0 + key < sink)) &&
                             (unsigned)(j0 + key) < (unsigned)plan.hi && pp.held;
           // Rows of several tokens see different keys: the tiles at the edges
           // are masked row by row.
@@ -1013,11 +1017,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
               tok0 != tok1 &&
               ((sh.causal && (long long)j0 + kTileKeys - 1 > at0) ||
                (sh.window >= 0 && (long long)j0 < at0 + (tok1 - tok0) - sh.window));
-          if constexpr (kMasked) {
-            if (sh.tree)
-              edge = (long long)j0 + kTileKeys > at0 ||
-                     (sh.window >= 0 && (long long)j0 < at0 + plan.deepest - sh.window);
-          }
+          if constexpr (kTree)
+            edge = (long long)j0 + kTileKeys > at0 ||
+                   (sh.window >= 0 && (long long)j0 < at0 + deepest - sh.window);
           // (A warp whose wait has given up still joins the votes below,
           // after which the whole warpgroup leaves.)
           const int sb = at % C::NS;
@@ -1046,7 +1048,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             const uint64_t l2 = ptx::f2_pack(__uint_as_float(ql[n]), __uint_as_float(ql[n + 1]));
             x[n / 2] = ptx::fma2(ptx::add2(h2, l2), ptx::mul2(f.x, ks2), f.y);
           }
-          if (kMasked && edge && sh.tree && (long long)j0 + key >= at0) {
+          if (kTree && edge && (long long)j0 + key >= at0) {
             // Keys of the nodes: bit r of each row's mask.
             const long long r = (long long)j0 + key - at0;
             const bool named = r < 32ll * a.tree_words;
@@ -1064,7 +1066,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             // Row n stands at at0 + token[n].
             const long long r = (long long)j0 + key - at0;
             const long long w = r + sh.window;
-            const int lo = sh.causal ? (int)(r < kMaxCost ? (r > -1 ? r : -1) : kMaxCost) : -1;
+            const int lo = sh.causal && !kTree ? (int)(r < kMaxCost ? (r > -1 ? r : -1) : kMaxCost) : -1;
             const int hi = sh.window < 0 || (kMasked && j0 + key < sh.sinks)
                                ? kMaxCost
                                : (int)(w < kMaxCost ? (w > -1 ? w : -1) : kMaxCost);

@@ -8,7 +8,7 @@
 
 namespace fa {
 
-template <int D, int N, bool kMasked>
+template <int D, int N, int kMask>
 cudaError_t launch_attn(const CUtensorMap& k_map, const CUtensorMap& v_map, const PagedAttnArgs& a,
                         int grid, cudaStream_t stream) {
   // Set once per device; concurrent first calls may both set it (the call is
@@ -20,12 +20,12 @@ cudaError_t launch_attn(const CUtensorMap& k_map, const CUtensorMap& v_map, cons
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   const int smem = (int)paged_smem<D, N>();
   if (!attr_done[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(paged_attn_kernel<D, N, kMasked>,
+    e = cudaFuncSetAttribute(paged_attn_kernel<D, N, kMask>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     attr_done[dev].store(true, std::memory_order_release);
   }
-  paged_attn_kernel<D, N, kMasked><<<grid, kPagedThreads, smem, stream>>>(k_map, v_map, a);
+  paged_attn_kernel<D, N, kMask><<<grid, kPagedThreads, smem, stream>>>(k_map, v_map, a);
   e = cudaGetLastError();
   if (e != cudaSuccess || grid < 2) return e;
   cudaLaunchConfig_t cfg;
@@ -42,18 +42,19 @@ cudaError_t launch_attn(const CUtensorMap& k_map, const CUtensorMap& v_map, cons
 }
 
 // The instantiation for padded head dim `dim` and `rows` rows a tile.
-template <bool kMasked>
+template <int kMask>
 cudaError_t launch_attn_shape(int dim, int rows, const CUtensorMap& k_map, const CUtensorMap& v_map,
                               const PagedAttnArgs& a, int grid, cudaStream_t stream) {
   if (dim == 64)
-    return rows == 16 ? launch_attn<64, 16, kMasked>(k_map, v_map, a, grid, stream)
-                      : launch_attn<64, 32, kMasked>(k_map, v_map, a, grid, stream);
-  return rows == 16 ? launch_attn<128, 16, kMasked>(k_map, v_map, a, grid, stream)
-                    : launch_attn<128, 32, kMasked>(k_map, v_map, a, grid, stream);
+    return rows == 16 ? launch_attn<64, 16, kMask>(k_map, v_map, a, grid, stream)
+                      : launch_attn<64, 32, kMask>(k_map, v_map, a, grid, stream);
+  return rows == 16 ? launch_attn<128, 16, kMask>(k_map, v_map, a, grid, stream)
+                    : launch_attn<128, 32, kMask>(k_map, v_map, a, grid, stream);
 }
-// That of the masked ones, in a translation unit of its own.
-cudaError_t launch_attn_masked(int dim, int rows, const CUtensorMap& k_map,
-                               const CUtensorMap& v_map, const PagedAttnArgs& a, int grid,
-                               cudaStream_t stream);
+// Those of the masked ones, in translation units of their own.
+cudaError_t launch_attn_sinks(int dim, int rows, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                              const PagedAttnArgs& a, int grid, cudaStream_t stream);
+cudaError_t launch_attn_tree(int dim, int rows, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                             const PagedAttnArgs& a, int grid, cudaStream_t stream);
 
 }  // namespace fa

@@ -556,6 +556,11 @@ __device__ __forceinline__ float4 ld_shared_cluster_v4(uint32_t caddr) {
                : "memory");
   return v;
 }
+__device__ __forceinline__ int ld_shared_cluster_s32(uint32_t caddr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(caddr) : "memory");
+  return v;
+}
 __device__ __forceinline__ float2 ld_shared_cluster_v2(uint32_t caddr) {
   float2 v;
   asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
