@@ -37,7 +37,7 @@ cudaError_t launch_weights(const CUtensorMap& map, const fa::KeyWeightsArgs& a, 
     attr_done[dev].store(true, std::memory_order_release);
   }
   fa::key_weights_kernel<D, N>
-      <<<sm_count * fa::WeightsCfg<D, N>::kResident, fa::kWeightThreads, smem, stream>>>(map, a);
+      <<<sm_count * fa::WeightsCfg<D, N>::kResident, fa::WeightsCfg<D, N>::kThreads, smem, stream>>>(map, a);
   return cudaGetLastError();
 }
 template <int D>

@@ -18,10 +18,12 @@
 // into equal contiguous ranges (paged_index.h), one for each CTA, so a tile is
 // one CTA's alone.  More rows than N go in chunks, tile by tile again.
 //
-//   warps 0-3  stage the rows of Q, then a thread for each key: exp2, sum,
-//              the weight's update
-//   warp 4     S MMAs into two buffers of N columns
-//   warp 5     TMA of the pages into a ring of K tiles, ahead of both
+//   issuer     S MMAs into two buffers of N columns
+//   producer   TMA of the pages into a ring of K tiles, ahead of both
+//   the rest   stage the rows of Q, then a thread for each key: exp2, sum, the
+//              weight's update.  Where a tile has 64 or 128 rows, whose
+//              exponentials take longer than its bytes, two warpgroups take
+//              tiles by turns.
 #pragma once
 
 #include <cstdint>
@@ -37,7 +39,6 @@
 
 namespace fa {
 
-constexpr int kWeightThreads = 192;
 constexpr int kWeightMaxBatch = 512;  // sequences of a launch
 
 struct KeyWeightsArgs {
@@ -66,6 +67,8 @@ struct WeightsCfg {
   static constexpr uint32_t kTmemCols = 2 * N < 32 ? 32 : 2 * N;
   static constexpr int kQ = kSlots * kTileBytes;
   static constexpr int kCtl = kQ + kQBytes;
+  static constexpr int kKeyThreads = N >= 64 ? 256 : 128;
+  static constexpr int kThreads = kKeyThreads + 64;
   // Resident CTAs (by shared memory: 56 to 86 KB at 128 dims).
   static constexpr int kResident = N <= 16 ? 4 : N <= 64 ? 3 : 2;
 };
@@ -74,7 +77,7 @@ template <int N>
 struct alignas(16) WeightsCtl {
   uint64_t k_full[3], k_free[3];  // K slot landed / read
   uint64_t s_full[2], s_free[2];  // St computed / loaded (128)
-  uint64_t q_full;                // rows of a chunk staged (128)
+  uint64_t q_full;                // rows of a chunk staged (all key threads)
   uint64_t drain;
   uint32_t tmem_base;
   volatile int abort_flag;
@@ -125,9 +128,10 @@ __device__ __forceinline__ WeightChunk weight_chunk(const AttnShape& s, int c, i
 }
 
 template <int D, int N>
-__global__ void __launch_bounds__(kWeightThreads, WeightsCfg<D, N>::kResident)
+__global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::kResident)
     key_weights_kernel(const __grid_constant__ CUtensorMap k_map, const KeyWeightsArgs a) {
   using C = WeightsCfg<D, N>;
+  constexpr int kIssuer = C::kKeyThreads / 32, kProducer = kIssuer + 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -143,7 +147,7 @@ __global__ void __launch_bounds__(kWeightThreads, WeightsCfg<D, N>::kResident)
     *len = __ldg(a.seq_lens + b);
   };
 
-  if (tid == 128) {
+  if (tid == C::kKeyThreads) {
     auto init = [&](uint64_t& b, uint32_t n) { ptx::mbar_init(ptx::smem_u32(&b), n); };
     for (int s = 0; s < C::kSlots; ++s) {
       init(cb->k_full[s], 1);
@@ -153,13 +157,13 @@ __global__ void __launch_bounds__(kWeightThreads, WeightsCfg<D, N>::kResident)
       init(cb->s_full[s], 1);
       init(cb->s_free[s], 128);
     }
-    init(cb->q_full, 128);
+    init(cb->q_full, C::kKeyThreads);
     init(cb->drain, 1);
     cb->abort_flag = 0;
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&k_map);
   }
-  if (warp == 5) {
+  if (warp == kProducer) {
     ptx::tmem_alloc(ptx::smem_u32(&cb->tmem_base), C::kTmemCols);
     ptx::tmem_relinquish();
   }
@@ -219,7 +223,7 @@ __global__ void __launch_bounds__(kWeightThreads, WeightsCfg<D, N>::kResident)
   };
   bool ok = true;
 
-  if (warp == 5) {
+  if (warp == kProducer) {
     // ------------------------------------------------------------ producer
     test_load_delay(a.wait_limit_ns);
     int loads = 0;
@@ -261,7 +265,7 @@ __global__ void __launch_bounds__(kWeightThreads, WeightsCfg<D, N>::kResident)
     // Every copy this CTA started lands before it exits.
     for (int s = 0; s < C::kSlots && s < loads; ++s)
       wait_drain_warp(ptx::smem_u32(&cb->k_full[s]), ((loads - 1 - s) / C::kSlots) & 1, a.status);
-  } else if (warp == 4) {
+  } else if (warp == kIssuer) {
     // ---------------------------------------------------------- MMA issuer
     constexpr uint32_t idesc = ptx::idesc_e4m3_f32(128, N);
     const uint64_t q_hi = ptx::smem_desc(ptx::smem_u32(smem + C::kQ), 16, 8 * D, C::kSwK);
@@ -298,8 +302,8 @@ __global__ void __launch_bounds__(kWeightThreads, WeightsCfg<D, N>::kResident)
     // ------------------------------------------------------------- weights
     const float neg_inf = -__int_as_float(0x7f800000);
     constexpr int kLanes = D / 8;  // lanes of a row of Q, 8 dims each
-    const uint32_t s_lane = tmem + ((uint32_t)(warp * 32) << 16);
-    const int key = tid;
+    const uint32_t s_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const int key = tid & 127, group = tid >> 7;
     int i = 0;
     while (ok && next()) {
       const int chunks = row_tiles(sh, rows);
@@ -315,18 +319,31 @@ __global__ void __launch_bounds__(kWeightThreads, WeightsCfg<D, N>::kResident)
         if (wc.any(g.tile0 * kTileKeys, (g.tile0 + g.count) * (long long)kTileKeys)) {
           const int sub = tid % kLanes, dim0 = sub * 8;
           uint8_t* q_s = smem + C::kQ;
-#pragma unroll 2
-          for (int n = tid / kLanes; n < N; n += 128 / kLanes) {
-            const int row = c * N + n, tok = token_of(sh, row);
-            const int h = g.head * sh.group + row - tok * sh.group;
-            uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-            float lse = 0.f;
+          constexpr int kStep = C::kKeyThreads / kLanes;    // rows at once
+          constexpr int kTurns = N / kStep;                 // of each thread, all under way
+          static_assert(N % kStep == 0, "rows of a chunk");
+          uint4 raw[kTurns];
+          float lse_of[kTurns];
+          int token[kTurns];
+#pragma unroll
+          for (int k = 0; k < kTurns; ++k) {
+            const int n = tid / kLanes + k * kStep, row = c * N + n;
+            token[k] = token_of(sh, row);
+            const int h = g.head * sh.group + row - token[k] * sh.group;
+            raw[k] = make_uint4(0u, 0u, 0u, 0u);
+            lse_of[k] = 0.f;
             if (n < n_rows && dim0 < a.dim)
-              raw = __ldg(reinterpret_cast<const uint4*>(
-                  a.q + (long long)(row0 + tok) * a.q_row + (long long)h * a.q_head + dim0));
-            if (n < n_rows && sub == 0) lse = __ldg(a.lse + (size_t)h * a.total_q + row0 + tok);
+              raw[k] = __ldg(reinterpret_cast<const uint4*>(
+                  a.q + (long long)(row0 + token[k]) * a.q_row + (long long)h * a.q_head + dim0));
+            if (n < n_rows && sub == 0)
+              lse_of[k] = __ldg(a.lse + (size_t)h * a.total_q + row0 + token[k]);
+          }
+#pragma unroll
+          for (int k = 0; k < kTurns; ++k) {
+            const int n = tid / kLanes + k * kStep, tok = token[k];
+            const float lse = lse_of[k];
             float x[8];
-            unpack_bf16x8(raw, x);
+            unpack_bf16x8(raw[k], x);
             float mx = 0.f;
             bool finite = true;
 #pragma unroll
@@ -358,7 +375,7 @@ __global__ void __launch_bounds__(kWeightThreads, WeightsCfg<D, N>::kResident)
           }
           ptx::fence_proxy_async_smem();
           ptx::mbar_arrive(ptx::smem_u32(&cb->q_full));
-          named_bar_sync(1, 128);
+          named_bar_sync(1, C::kKeyThreads);
         }
         // ---- the tiles
 #pragma unroll 1
@@ -376,8 +393,14 @@ __global__ void __launch_bounds__(kWeightThreads, WeightsCfg<D, N>::kResident)
           for (int t = 0; t < end; ++t) {
             const int j0 = (g.tile0 + t0 + t) * kTileKeys, j = j0 + key;
             const bool here = j < g.keys.hi;
-            const float ks = __shfl_sync(0xffffffffu, scale, 2 * t + (warp >> 1));
+            const float ks = __shfl_sync(0xffffffffu, scale, 2 * t + ((warp >> 1) & 1));
             const bool seen = wc.seen(j0);
+            // (Two groups: by turns.  What a chunk writes, the next may read in
+            // the other group, behind the barrier between them.)
+            if (C::kKeyThreads > 128 && (seen ? i & 1 : t & 1) != group) {
+              i += seen;
+              continue;
+            }
             // What stands there already, and whether it changes.
             const bool add = c > 0 || (a.decay != 0.f && j < fresh);
             if (!seen && (c > 0 || (add && a.decay == 1.f))) continue;
@@ -403,33 +426,42 @@ __global__ void __launch_bounds__(kWeightThreads, WeightsCfg<D, N>::kResident)
               }
               const uint64_t ks2 = ptx::f2_pack(ks, ks);
               uint64_t acc[2] = {0ull, 0ull};
+              // (Twice: the whole tile without a test for each row.)
+              auto add_up = [&](auto masked) {
+                // The next 16 columns load while these are summed.
+                uint32_t s[2][16];
+                ptx::tmem_ld16(s_lane + sb * N, s[0]);
 #pragma unroll
-              for (int n0 = 0; n0 < N; n0 += 16) {
-                uint32_t s[16];
-                ptx::tmem_ld16(s_lane + sb * N + n0, s);
-                ptx::tmem_wait_ld();
-                ptx::reg_fence16(s);
-                if (n0 + 16 == N) {
-                  ptx::tc_fence_before();
-                  ptx::mbar_arrive(ptx::smem_u32(&cb->s_free[sb]));
-                }
-#pragma unroll
-                for (int n = 0; n < 16; n += 2) {
-                  const ulonglong2 f =
-                      *reinterpret_cast<const ulonglong2*>(cb->row + (n0 + n) / 2);
-                  const uint64_t s2 =
-                      ptx::f2_pack(__uint_as_float(s[n]), __uint_as_float(s[n + 1]));
-                  float u, v;
-                  ptx::f2_unpack(ptx::fma2(s2, ptx::mul2(f.x, ks2), f.y), u, v);
-                  if (!all) {
-                    const int2 tok = *reinterpret_cast<const int2*>(cb->token + n0 + n);
-                    u = tok.x >= lo && tok.x <= hi ? u : neg_inf;
-                    v = tok.y >= lo && tok.y <= hi ? v : neg_inf;
+                for (int n0 = 0; n0 < N; n0 += 16) {
+                  uint32_t* now = s[(n0 >> 4) & 1];
+                  ptx::tmem_wait_ld();
+                  ptx::reg_fence16(now);
+                  if (n0 + 16 < N) {
+                    ptx::tmem_ld16(s_lane + sb * N + n0 + 16, s[((n0 >> 4) & 1) ^ 1]);
+                  } else {
+                    ptx::tc_fence_before();
+                    ptx::mbar_arrive(ptx::smem_u32(&cb->s_free[sb]));
                   }
-                  acc[(n >> 1) & 1] =
-                      ptx::add2(acc[(n >> 1) & 1], ptx::f2_pack(ptx::ex2(u), ptx::ex2(v)));
+#pragma unroll
+                  for (int n = 0; n < 16; n += 2) {
+                    const ulonglong2 f =
+                        *reinterpret_cast<const ulonglong2*>(cb->row + (n0 + n) / 2);
+                    const uint64_t s2 =
+                        ptx::f2_pack(__uint_as_float(now[n]), __uint_as_float(now[n + 1]));
+                    float u, v;
+                    ptx::f2_unpack(ptx::fma2(s2, ptx::mul2(f.x, ks2), f.y), u, v);
+                    if constexpr (decltype(masked)::value != 0) {
+                      const int2 tok = *reinterpret_cast<const int2*>(cb->token + n0 + n);
+                      u = tok.x >= lo && tok.x <= hi ? u : neg_inf;
+                      v = tok.y >= lo && tok.y <= hi ? v : neg_inf;
+                    }
+                    acc[(n >> 1) & 1] =
+                        ptx::add2(acc[(n >> 1) & 1], ptx::f2_pack(ptx::ex2(u), ptx::ex2(v)));
+                  }
                 }
-              }
+              };
+              if (all) add_up(IntTag<0>{});
+              else add_up(IntTag<1>{});
               float u, v;
               ptx::f2_unpack(ptx::add2(acc[0], acc[1]), u, v);
               sum = u + v;
@@ -440,13 +472,13 @@ __global__ void __launch_bounds__(kWeightThreads, WeightsCfg<D, N>::kResident)
           }
         }
         // (A warp whose wait has given up joins the others here, and all leave.)
-        ok = named_bar_and(1, 128, ok);
+        ok = named_bar_and(1, C::kKeyThreads, ok);
       }
     }
   }
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == kProducer) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, C::kTmemCols);
   }
