@@ -534,8 +534,9 @@ fa_status fa_paged_attn(const void* q, long long q_row_stride, long long q_head_
                         size_t workspace_bytes, fa_stream_t stream);
 
 /*
- * fa_paged_attn_masked -- fa_paged_attn with two more masks.  Arguments, rules,
- * workspace (fa_paged_attn_plan's) and errors as there, and
+ * fa_paged_attn_masked -- fa_paged_attn with two more masks.  Arguments, rules
+ * and errors as there, the workspace as fa_paged_attn_masked_plan gives it (that
+ * of fa_paged_attn_plan will do where sink_tokens and tree_words are 0), and
  *
  *   sink_tokens   the keys j < sink_tokens stay visible to rows whose window
  *                 has left them behind (attention sinks): row i sees key j iff
@@ -571,6 +572,15 @@ fa_status fa_paged_attn_masked(const void* q, long long q_row_stride, long long 
                                int window_left, int sink_tokens, const int* tree_mask,
                                int tree_words, void* out, float* lse, void* workspace,
                                size_t workspace_bytes, fa_stream_t stream);
+
+/*
+ * fa_paged_attn_masked_plan -- fa_paged_attn_plan for a fa_paged_attn_masked call
+ * under sinks or a tree: more than 32 rows (tokens x heads of one group) of a
+ * sequence then go 256 to a tile.
+ */
+fa_status fa_paged_attn_masked_plan(int batch, int total_q, int num_heads, int num_heads_k,
+                                    int head_dim, int max_seqlen_q, int* grid, int* rows_per_tile,
+                                    size_t* workspace_bytes);
 
 /*
  * fa_draft_tree -- the ancestor masks and the positions of drafted trees, from

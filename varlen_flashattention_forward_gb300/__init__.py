@@ -32,7 +32,8 @@ Entry points (same names as the C ABI):
                 stream=None, sink_tokens=0, tree_mask=None)
   fa_draft_tree(parents, cu_seqlens, seq_lens, max_nodes=64, tree_mask=None, positions=None,
                 stream=None)
-  fa_paged_attn_plan(batch, total_q, num_heads, num_heads_k, head_dim, max_seqlen_q=0)
+  fa_paged_attn_plan(batch, total_q, num_heads, num_heads_k, head_dim, max_seqlen_q=0,
+                     masked=False)
   fa_paged_key_weights(q, lse, k_cache, k_scale, cu_seqlens_q, seq_lens, page_table, weights,
                        softmax_scale=None, causal=True, window_left=-1, sink_tokens=0, decay=1.0,
                        stream=None)
@@ -69,7 +70,7 @@ EXPORTS = ("fa_varlen_fwd", "fa_varlen_fwd_plan", "fa_varlen_fwd_strided", "fa_v
            "fa_sparse_mla_decode",
            "fa_sparse_mla_decode_plan", "fa_sparse_mla_decode_noalloc", "fa_merge_attn_states",
            "fa_qk_norm_rope", "fa_paged_kv_append", "fa_paged_attn", "fa_paged_attn_plan",
-           "fa_paged_attn_masked", "fa_draft_tree", "fa_paged_key_weights", "fa_paged_kv_select",
+           "fa_paged_attn_masked", "fa_paged_attn_masked_plan", "fa_draft_tree", "fa_paged_key_weights", "fa_paged_kv_select",
            "fa_paged_kv_compact", "fa_paged_kv_gather", "fa_get_device_status",
            "fa_set_wait_limit_ns", "fa_status_string")
 
@@ -147,6 +148,8 @@ def load_library():
     lib.fa_paged_attn_plan.argtypes = [i32, i32, i32, i32, i32, i32, pi, pi,
                                        ctypes.POINTER(size)]
     lib.fa_paged_attn_plan.restype = i32
+    lib.fa_paged_attn_masked_plan.argtypes = lib.fa_paged_attn_plan.argtypes
+    lib.fa_paged_attn_masked_plan.restype = i32
     lib.fa_paged_kv_gather.argtypes = [p, p, p, p, p, p, i32, i32, i32, i32, i32, i32, p, p, p]
     lib.fa_paged_kv_gather.restype = i32
     lib.fa_set_wait_limit_ns.argtypes = [ctypes.c_ulonglong]
@@ -592,15 +595,17 @@ def fa_paged_kv_append(k, v, cu_seqlens, seq_lens, page_table, k_cache, v_cache,
         raise FaError(st, "fa_paged_kv_append")
 
 
-def fa_paged_attn_plan(batch, total_q, num_heads, num_heads_k, head_dim, max_seqlen_q=0):
+def fa_paged_attn_plan(batch, total_q, num_heads, num_heads_k, head_dim, max_seqlen_q=0,
+                       masked=False):
     """(grid, rows_per_tile, workspace_bytes) of a fa_paged_attn call of these
-    sizes on the current device; see fa_paged_attn_plan in
+    sizes on the current device (masked: with sinks behind a window or a
+    tree_mask); see fa_paged_attn_plan and fa_paged_attn_masked_plan in
     include/fa_gb300.h."""
     lib = load_library()
     g, r, w = ctypes.c_int(0), ctypes.c_int(0), ctypes.c_size_t(0)
-    st = lib.fa_paged_attn_plan(int(batch), int(total_q), int(num_heads), int(num_heads_k),
-                                int(head_dim), int(max_seqlen_q), ctypes.byref(g),
-                                ctypes.byref(r), ctypes.byref(w))
+    plan = lib.fa_paged_attn_masked_plan if masked else lib.fa_paged_attn_plan
+    st = plan(int(batch), int(total_q), int(num_heads), int(num_heads_k), int(head_dim),
+              int(max_seqlen_q), ctypes.byref(g), ctypes.byref(r), ctypes.byref(w))
     if st != FA_OK:
         raise FaError(st, "fa_paged_attn_plan")
     return g.value, r.value, w.value
@@ -611,9 +616,9 @@ def fa_paged_attn(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, seq_lens,
                   window_left=-1, out=None, lse=None, return_lse=False, workspace=None,
                   stream=None, sink_tokens=0, tree_mask=None):
     """Attention of a few query rows per sequence over the paged 8-bit cache;
-    see fa_paged_attn and fa_paged_attn_masked in include/fa_gb300.h.  (From
-    about 64 rows a sequence on, fa_paged_kv_gather and fa_varlen_fwd are
-    faster.)
+    see fa_paged_attn and fa_paged_attn_masked in include/fa_gb300.h.  (Without
+    these masks fa_paged_kv_gather and fa_varlen_fwd are faster from about 64
+    rows a sequence on.)
 
     q [total_q, H, d] bf16 (strided view allowed), caches and scales as
     fa_paged_kv_append, cu_seqlens_q [batch+1], seq_lens [batch] and
@@ -656,7 +661,8 @@ def fa_paged_attn(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, seq_lens,
         elif return_lse:
             lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
         if workspace is None:
-            need = _attn_workspace(index, batch, T, H, hk, d, max_seqlen_q)
+            need = _attn_workspace(index, batch, T, H, hk, d, max_seqlen_q,
+                                   words > 0 or sink_tokens > 0)
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         else:
             _check(workspace, "workspace", torch.uint8, 1)
@@ -733,9 +739,10 @@ def fa_draft_tree(parents, cu_seqlens, seq_lens, max_nodes=64, tree_mask=None, p
 
 
 @functools.lru_cache(maxsize=1024)
-def _attn_workspace(index, batch, total_q, num_heads, num_heads_k, head_dim, max_seqlen_q):
+def _attn_workspace(index, batch, total_q, num_heads, num_heads_k, head_dim, max_seqlen_q, masked):
     """Workspace bytes of a fa_paged_attn call on the current device `index`."""
-    return fa_paged_attn_plan(batch, total_q, num_heads, num_heads_k, head_dim, max_seqlen_q)[2]
+    return fa_paged_attn_plan(batch, total_q, num_heads, num_heads_k, head_dim, max_seqlen_q,
+                              masked)[2]
 
 
 def fa_paged_kv_gather(k_cache, v_cache, k_scale, v_scale, cu_seqlens, page_table, total_k,

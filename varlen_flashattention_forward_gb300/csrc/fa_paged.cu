@@ -15,6 +15,7 @@
 #include "paged_host.h"
 #include "paged_kv_kernels.cuh"
 #include "paged_launch.cuh"
+#include "paged_wide_kernel.cuh"
 #include "qk_norm_rope_kernel.cuh"
 
 using fa::cache_dim;
@@ -38,13 +39,16 @@ struct AttnLaunch {
   size_t o_bytes, lse_bytes, meta_bytes;
   size_t bytes() const { return o_bytes + lse_bytes + meta_bytes; }
 };
+// masked: under sinks or a tree, where more than kNarrowRows rows go 256 to a tile
+// (paged_wide_kernel).
+constexpr int kNarrowRows = 32;
 AttnLaunch attn_launch(int sm_count, int batch, int total_q, int group, int head_dim,
-                       int max_seqlen_q) {
+                       int max_seqlen_q, bool masked) {
   AttnLaunch l;
   const long long tokens =
       max_seqlen_q > 0 ? max_seqlen_q : ((long long)total_q + batch - 1) / batch;
   const long long rows = tokens * group;
-  l.rows = rows <= 16 ? 16 : 32;
+  l.rows = rows <= 16 ? 16 : masked && rows > kNarrowRows ? fa::kWideRows : 32;
   l.dim = head_dim <= 64 ? 64 : 128;
   l.grid = std::min(sm_count, fa::kPagedMaxGrid);
   l.o_bytes = (size_t)2 * l.grid * l.rows * l.dim * sizeof(float);
@@ -268,9 +272,11 @@ extern "C" fa_status fa_paged_kv_gather(const void* k_cache, const void* v_cache
   return launched();
 }
 
-extern "C" fa_status fa_paged_attn_plan(int batch, int total_q, int num_heads, int num_heads_k,
-                                        int head_dim, int max_seqlen_q, int* grid,
-                                        int* rows_per_tile, size_t* workspace_bytes) {
+namespace {
+
+fa_status plan_attn(int batch, int total_q, int num_heads, int num_heads_k, int head_dim,
+                    int max_seqlen_q, bool masked, int* grid, int* rows_per_tile,
+                    size_t* workspace_bytes) {
   if (!grid || !rows_per_tile || !workspace_bytes) return FA_ERR_INVALID_ARG;
   if (batch < 1 || total_q < 0 || num_heads < 1 || num_heads_k < 1 ||
       num_heads % num_heads_k != 0 || max_seqlen_q < 0)
@@ -280,11 +286,29 @@ extern "C" fa_status fa_paged_attn_plan(int batch, int total_q, int num_heads, i
   const fa_status st = fa::device_facts(&dev);
   if (st != FA_OK) return st;
   const AttnLaunch l =
-      attn_launch(dev.sm_count, batch, total_q, num_heads / num_heads_k, head_dim, max_seqlen_q);
+      attn_launch(dev.sm_count, batch, total_q, num_heads / num_heads_k, head_dim, max_seqlen_q,
+                  masked);
   *grid = total_q > 0 ? l.grid : 0;
   *rows_per_tile = l.rows;
   *workspace_bytes = total_q > 0 ? l.bytes() : 0;
   return FA_OK;
+}
+
+}  // namespace
+
+extern "C" fa_status fa_paged_attn_plan(int batch, int total_q, int num_heads, int num_heads_k,
+                                        int head_dim, int max_seqlen_q, int* grid,
+                                        int* rows_per_tile, size_t* workspace_bytes) {
+  return plan_attn(batch, total_q, num_heads, num_heads_k, head_dim, max_seqlen_q, false, grid,
+                   rows_per_tile, workspace_bytes);
+}
+
+extern "C" fa_status fa_paged_attn_masked_plan(int batch, int total_q, int num_heads,
+                                               int num_heads_k, int head_dim, int max_seqlen_q,
+                                               int* grid, int* rows_per_tile,
+                                               size_t* workspace_bytes) {
+  return plan_attn(batch, total_q, num_heads, num_heads_k, head_dim, max_seqlen_q, true, grid,
+                   rows_per_tile, workspace_bytes);
 }
 
 extern "C" fa_status fa_paged_attn(const void* q, long long q_row_stride, long long q_head_stride,
@@ -334,7 +358,10 @@ extern "C" fa_status fa_paged_attn_masked(
   if (st != FA_OK) return st;
   if (total_q == 0) return FA_OK;
   const int group = num_heads / num_heads_k;
-  const AttnLaunch l = attn_launch(dev.sm_count, batch, total_q, group, head_dim, max_seqlen_q);
+  // (Sinks say nothing without a window.)
+  const bool sinks = sink_tokens > 0 && window_left >= 0, masked = sinks || tree_words > 0;
+  const AttnLaunch l =
+      attn_launch(dev.sm_count, batch, total_q, group, head_dim, max_seqlen_q, masked);
   if (!workspace || workspace_bytes < l.bytes()) return FA_ERR_INVALID_ARG;
   CUtensorMap k_map, v_map;
   if (!encode_cache(&k_map, k_cache, head_dim, num_pages * num_heads_k, l.dim) ||
@@ -373,8 +400,6 @@ extern "C" fa_status fa_paged_attn_masked(
       ((long long)max_pages_per_seq * fa::kPageTokens / fa::kTileKeys + 1 + fa::kUnitCost);
   const long long row_tiles = (long long)total_q * group / l.rows;
   const long long fit = fa::kMaxCost / per_row_tile - row_tiles;
-  // (Sinks say nothing without a window.)
-  const bool sinks = sink_tokens > 0 && window_left >= 0;
   if (fit < 1) return FA_ERR_UNSUPPORTED;
   const int step = (int)std::min<long long>(fa::kPagedMaxBatch, fit);
   for (int b0 = 0; b0 < batch; b0 += step) {
@@ -383,7 +408,8 @@ extern "C" fa_status fa_paged_attn_masked(
     a.seq_lens = seq_lens + b0;
     a.page_table = page_table + (size_t)b0 * max_pages_per_seq;
     const cudaError_t e =
-        tree_words > 0 ? fa::launch_attn_tree(l.dim, l.rows, k_map, v_map, a, l.grid, s)
+        l.rows == fa::kWideRows ? fa::launch_attn_wide(l.dim, k_map, v_map, a, l.grid, s)
+        : tree_words > 0 ? fa::launch_attn_tree(l.dim, l.rows, k_map, v_map, a, l.grid, s)
         : sinks        ? fa::launch_attn_sinks(l.dim, l.rows, k_map, v_map, a, l.grid, s)
                        : fa::launch_attn_shape<fa::kNoMask>(l.dim, l.rows, k_map, v_map, a, l.grid, s);
     if (e != cudaSuccess) return FA_ERR_LAUNCH;

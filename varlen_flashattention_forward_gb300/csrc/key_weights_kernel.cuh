@@ -30,6 +30,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "cost_scan.cuh"
 #include "e4m3.cuh"
 #include "named_bar.cuh"
 #include "paged_attn_kernel.cuh"  // bounded waits
@@ -168,36 +169,12 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
     ptx::tmem_relinquish();
   }
   if (warp < 4) {
-    if (tid == 0) cb->before[0] = 0;
-    long long base = 0;
-#pragma unroll 1
-    for (int b0 = 0; b0 < a.batch; b0 += 128) {
-      const int b = b0 + tid;
-      int n = 0;
-      if (b < a.batch) {
-        RowRange q;
-        int len;
-        seq_of(b, &q, &len);
-        n = capped_cost(sh.heads_k * head_cost(whole, q.n, len));
-      }
-      long long sum = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += v;
-      }
-      if (lane == 31) cb->warp_sum[warp] = sum;
-      named_bar_sync(1, 128);
-      long long all = 0, lo = base;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        if (w < warp) lo += cb->warp_sum[w];
-        all += cb->warp_sum[w];
-      }
-      if (b < a.batch) cb->before[b + 1] = capped_cost(lo + sum);
-      base += all;
-      named_bar_sync(1, 128);
-    }
+    scan_costs<128>(cb->before, cb->warp_sum, a.batch, [&](int b) {
+      RowRange q;
+      int len;
+      seq_of(b, &q, &len);
+      return (long long)capped_cost(sh.heads_k * head_cost(whole, q.n, len));
+    });
   }
   ptx::tc_fence_before();
   __syncthreads();

@@ -57,4 +57,8 @@ cudaError_t launch_attn_sinks(int dim, int rows, const CUtensorMap& k_map, const
 cudaError_t launch_attn_tree(int dim, int rows, const CUtensorMap& k_map, const CUtensorMap& v_map,
                              const PagedAttnArgs& a, int grid, cudaStream_t stream);
 
+// Those of paged_wide_kernel and its merge (256 rows a tile), for any of the masks.
+cudaError_t launch_attn_wide(int dim, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                             const PagedAttnArgs& a, int grid, cudaStream_t stream);
+
 }  // namespace fa
