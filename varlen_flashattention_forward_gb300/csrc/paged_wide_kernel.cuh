@@ -45,10 +45,10 @@ namespace fa {
 constexpr int kWideRows = 256;  // of a unit's row tile
 constexpr int kWideThreads = 512;
 constexpr int kWideConvertWarp = 8, kWideIssueWarp = 12, kWideLoadWarp = 14, kWidePlanWarp = 15;
-// Register split (launch: 128 x 512 = 65536): softmax 256 x 176, converters and
-// control 128 x 80 each = 65536.
-constexpr uint32_t kWideSoftmaxRegs = 176;
-constexpr uint32_t kWideOtherRegs = 80;
+// Register split (launch: 128 x 512 = 65536): softmax 256 x 192, converters and
+// control 128 x 64 each = 65536.
+constexpr uint32_t kWideSoftmaxRegs = 192;
+constexpr uint32_t kWideOtherRegs = 64;
 
 // Up to kPlanTiles tiles of one segment; count = 0 ends the range.
 struct alignas(16) WidePlan {
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_addr = tmem + lane_base + 128 * t;
     const uint32_t o_addr = tmem + lane_base + C::kOt + 128 * t;
-    uint8_t* q_row = smem + C::kQ + 2 * t * C::kTermBytes + r * D;
+    uint8_t* q_tile = smem + C::kQ + 2 * t * C::kTermBytes;
     bool ok = true;
     int tiles = 0, seg = 0, segs = 0;  // of this row tile; segments of the CTA
     // The segment's row: scale of its terms, the keys it sees ([lo, hi), [0,
@@ -457,43 +457,56 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const int row = plan.row0 + t * 128 + r, tok = valid ? token_of(sh, row) : 0;
         row_q = plan.q0 + tok;
         row_h = plan.head * sh.group + (valid ? row - tok * sh.group : 0);
-        const uint16_t* q = a.q + (long long)row_q * a.q_row + (long long)row_h * a.q_head;
-        float mx = 0.f;
-        bool finite = true;
-        uint4 raw[D / 8];
-#pragma unroll
-        for (int k = 0; k < D / 8; ++k)
-          raw[k] = valid && 8 * k < a.dim ? __ldg(reinterpret_cast<const uint4*>(q) + k)
-                                          : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int k = 0; k < D / 8; ++k) {
-          float x[8];
-          unpack_bf16x8(raw[k], x);
+        // The warp's 32 rows come together, as bf16 into the place of their two
+        // terms, a half of the dims each; then kLanes lanes take a row at a time.
+        // (In short loops: the code runs once a segment, and is fetched each time.)
+        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+        const int sub = lane % kLanes, dim0 = sub * 8;
+        const long long mine_at =
+            valid ? (long long)row_q * a.q_row + (long long)row_h * a.q_head : -1;
+        // (Raw: 16 bytes of dims dim0 .., in the term of their half.)
+        uint8_t* warp_q = q_tile + (warp & 3) * 32 * D;
+        uint8_t* raw0 = warp_q + (sub >= kLanes / 2 ? C::kTermBytes : 0) + (sub % (kLanes / 2)) * 16;
+#pragma unroll 1
+        for (int n = lane / kLanes; n < 32; n += kAtOnce) {
+          const long long at = __shfl_sync(0xffffffffu, mine_at, n);
+          const bool some = at >= 0 && dim0 < a.dim;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                           ptx::smem_u32(raw0 + n * D)),
+                       "l"(a.q + (some ? at + dim0 : 0)), "r"(some ? 16 : 0)
+                       : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        const int unit = dim0 >> 4;
+#pragma unroll 1
+        for (int k = 0; k < kLanes; ++k) {
+          const int n = k * kAtOnce + lane / kLanes;
+          float x[8], mx = 0.f;
+          bool finite = true;
+          unpack_bf16x8(*reinterpret_cast<const uint4*>(raw0 + n * D), x);
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             finite = finite && fabsf(x[c]) <= 3.402823466e38f;
             mx = fmaxf(mx, fabsf(x[c]));
           }
-        }
-        if (!finite) mx = __int_as_float(0x7f800000);
-        const int e = terms_exponent(mx);
-        qs = terms_scale(mx, e, a.scale_log2);
+          if (!finite) mx = __int_as_float(0x7f800000);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          uint32_t hi[8], lo[8];
-          float x[8];
-          unpack_bf16x8(raw[2 * k], x);
+          for (int o = kLanes / 2; o > 0; o >>= 1)
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));  // (the row is read)
+          const int e = terms_exponent(mx);
+          uint32_t hi[4], lo[4];
           split_terms(x, e, hi, lo);
-          unpack_bf16x8(raw[2 * k + 1], x);
-          split_terms(x, e, hi + 4, lo + 4);
-          const int us = D == 128 ? (k ^ (r & 7)) : (k ^ ((r >> 1) & 3));
-          uint8_t* at = q_row + us * 16;
-          *reinterpret_cast<uint4*>(at) =
-              make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16,
-                         hi[6] | hi[7] << 16);
-          *reinterpret_cast<uint4*>(at + C::kTermBytes) =
-              make_uint4(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16,
-                         lo[6] | lo[7] << 16);
+          // (n and the row's number in the tile agree modulo 32.)
+          const int us = D == 128 ? (unit ^ (n & 7)) : (unit ^ ((n >> 1) & 3));
+          uint8_t* at = warp_q + n * D + us * 16 + (dim0 & 8);
+          *reinterpret_cast<uint2*>(at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+          *reinterpret_cast<uint2*>(at + C::kTermBytes) =
+              make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+          // Its scale to the row's thread.
+          const float scale = __shfl_sync(0xffffffffu, terms_scale(mx, e, a.scale_log2),
+                                          (lane % kAtOnce) * kLanes);
+          if (lane / kAtOnce == k) qs = scale;
         }
         ptx::fence_proxy_async_smem();
         ptx::mbar_arrive(ptx::smem_u32(&cb->q_full[t]));
@@ -585,7 +598,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           if (!plan.first || n > 0) {
             // O_t holds the earlier tiles: their P V ended before this S.
             const float alpha = root * root;
-#pragma unroll
+#pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 16) {
               uint32_t o[16];
               ptx::tmem_ld16(o_addr + c0, o);
@@ -662,37 +675,61 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         else if (a.lse)
           a.lse[(size_t)row_h * a.total_q + row_q] = l2 * 0.69314718055994531f;
       }
+      // Through the rows' place in shared memory (Q's terms, read by the last S),
+      // 2 D bytes of each: D values as bf16, or half of them as fp32 by turns.  A
+      // warp's rows are its own.
+      constexpr int kUnits = D / 8;  // of 16 bytes
+      uint8_t* mine_s = q_tile + r * (2 * D);
+      const uint64_t dst =
+          !valid ? 0
+          : whole ? reinterpret_cast<uint64_t>(a.out + ((size_t)row_q * a.heads + row_h) * a.dim)
+                  : reinterpret_cast<uint64_t>(a.part_o +
+                                               ((size_t)slot * kWideRows + t * 128 + r) * D);
+      const int units = whole ? a.dim / 8 : kUnits;
+      // (Weight 0: O_t may hold anything.)
+      auto value = [&](uint32_t o) { return inv == 0.f ? 0.f : __uint_as_float(o) * inv; };
 #pragma unroll 1
-      for (int c0 = 0; c0 < D; c0 += 32) {
-        uint32_t o[32];
-        ptx::tmem_ld16(o_addr + c0, o);
-        ptx::tmem_ld16(o_addr + c0 + 16, o + 16);
-        ptx::tmem_wait_ld();
-        ptx::reg_fence16(o);
-        ptx::reg_fence16(o + 16);
-        if (c0 + 32 >= D) {
+      for (int turn = 0; turn < (whole ? 1 : 2); ++turn) {
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          if (!whole && (c0 >= D / 2) != (turn != 0)) continue;
+          uint32_t o[32];
+          ptx::tmem_ld16(o_addr + c0, o);
+          ptx::tmem_ld16(o_addr + c0 + 16, o + 16);
+          ptx::tmem_wait_ld();
+          ptx::reg_fence16(o);
+          ptx::reg_fence16(o + 16);
+          if (whole) {
+#pragma unroll
+            for (int c = 0; c < 32; c += 8)
+              *reinterpret_cast<uint4*>(mine_s + ((((c0 + c) / 8) ^ (r & 7)) * 16)) = make_uint4(
+                  ptx::pack_bf16x2(value(o[c]), value(o[c + 1])),
+                  ptx::pack_bf16x2(value(o[c + 2]), value(o[c + 3])),
+                  ptx::pack_bf16x2(value(o[c + 4]), value(o[c + 5])),
+                  ptx::pack_bf16x2(value(o[c + 6]), value(o[c + 7])));
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; c += 4)
+              *reinterpret_cast<float4*>(mine_s + ((((c0 - turn * (D / 2) + c) / 4) ^ (r & 7)) * 16)) =
+                  make_float4(value(o[c]), value(o[c + 1]), value(o[c + 2]), value(o[c + 3]));
+          }
+        }
+        if (turn == (whole ? 0 : 1)) {
           ptx::tc_fence_before();
           ptx::mbar_arrive(ptx::smem_u32(&cb->o_free[t]));
         }
-        if (!valid) continue;
-        // (Weight 0: O_t may hold anything.)
-        auto value = [&](int c) { return inv == 0.f ? 0.f : __uint_as_float(o[c]) * inv; };
-        if (whole) {
-          uint16_t* out = a.out + ((size_t)row_q * a.heads + row_h) * a.dim + c0;
-#pragma unroll
-          for (int c = 0; c < 32; c += 8)
-            if (c0 + c < a.dim)
-              *reinterpret_cast<uint4*>(out + c) = make_uint4(
-                  ptx::pack_bf16x2(value(c), value(c + 1)), ptx::pack_bf16x2(value(c + 2), value(c + 3)),
-                  ptx::pack_bf16x2(value(c + 4), value(c + 5)),
-                  ptx::pack_bf16x2(value(c + 6), value(c + 7)));
-        } else {
-          float* out = a.part_o + ((size_t)slot * kWideRows + t * 128 + r) * D + c0;
-#pragma unroll
-          for (int c = 0; c < 32; c += 4)
-            *reinterpret_cast<float4*>(out + c) =
-                make_float4(value(c), value(c + 1), value(c + 2), value(c + 3));
+        __syncwarp();
+#pragma unroll 2
+        for (int k = 0; k < kUnits; ++k) {
+          // 32 units at a time, kUnits of a row next to each other.
+          const int n = (k * 32 + lane) / kUnits, u = lane % kUnits;
+          const uint64_t to = __shfl_sync(0xffffffffu, dst, n);
+          const int row_n = (warp & 3) * 32 + n;
+          if (to != 0 && u < units)
+            *reinterpret_cast<uint4*>(to + turn * D * 2 + u * 16) =
+                *reinterpret_cast<const uint4*>(q_tile + row_n * (2 * D) + ((u ^ (row_n & 7)) * 16));
         }
+        __syncwarp();
       }
     }
   }
