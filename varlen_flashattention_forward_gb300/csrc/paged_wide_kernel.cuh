@@ -24,12 +24,14 @@
 //                    scales of their pages
 //   producer warp    TMA of K and V pages into two rings
 //   converter warps  V to f16, rows nobody sees as zeros
-//   two issuers      of a row tile each: S_t, then O_t once P_t and V are there;
-//                    one's MMAs run under the other's softmax
+//   two issuers      of a row tile each: S_t of a page (64 keys) into one half of
+//                    its columns while the softmax has the other, O_t once P_t
+//                    and V are there
 //   two softmax      warpgroups, of a row tile each: its rows of Q in two terms
-//                    at a segment's start, the softmax, the output at its end
+//                    at a segment's start, the softmax page by page, the output
+//                    at its end
 //
-// TMEM: S_0 / P_0, S_1 / P_1, O_0, O_1, 128 columns each.
+// TMEM: S_0 / P_0, S_1 / P_1 (two pages each), O_0, O_1, 128 columns each.
 #pragma once
 
 #include <cstddef>
@@ -86,7 +88,8 @@ struct alignas(16) WideCtl {
   uint64_t v_full[4], v_free[4];      // V slot landed / converted (128)
   uint64_t vh_full[2], vh_free[2];    // f16 V written (128) / read by both issuers' P V
   uint64_t q_full[2];                 // rows of Q staged (128)
-  uint64_t s_full[2], p_full[2];      // S_t computed / P_t written (128)
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // of a row tile and half: S_t
+                                      // computed, P_t written (128), P V complete
   uint64_t o_full[2], o_free[2];      // O_t complete / read out (128)
   uint64_t drain;
   uint32_t tmem_base;
@@ -138,8 +141,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       init(cb->vh_full[s], 128);
       init(cb->vh_free[s], 2);
       init(cb->q_full[s], 128);
-      init(cb->s_full[s], 1);
-      init(cb->p_full[s], 128);
+      for (int h = 0; h < 2; ++h) {
+        init(cb->s_full[s][h], 1);
+        init(cb->p_full[s][h], 128);
+        init(cb->pv_done[s][h], 1);
+      }
       init(cb->o_full[s], 1);
       init(cb->o_free[s], 128);
     }
@@ -256,14 +262,34 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     if (warp < kWideLoadWarp) {
       // ------------------------------------------------------------- issuers
       const int t = warp - kWideIssueWarp;
-      constexpr uint32_t idesc_s = ptx::idesc_e4m3_f32(128, 128);
+      constexpr uint32_t idesc_s = ptx::idesc_e4m3_f32(128, kPageTokens);
       constexpr uint32_t idesc_pv = ptx::idesc_f16_f32(128, D, false, true);
       const uint32_t q_s = ptx::smem_u32(smem + C::kQ + 2 * t * C::kTermBytes);
       const uint64_t q_hi = ptx::smem_desc(q_s, 16, 8 * D, C::kSwK);
       const uint64_t q_lo = ptx::smem_desc(q_s + C::kTermBytes, 16, 8 * D, C::kSwK);
       const uint32_t s_col = tmem + 128 * t, o_col = tmem + C::kOt + 128 * t;
       bool ok = true;
-      int i = 0, tiles = 0, seg = 0;  // tiles of the CTA, and of this row tile; its segments
+      int i = 0, ki = 0, tiles = 0, seg = 0;  // tiles done and S'ed, tiles and segments of this row tile
+      // S of a page of tile `ki`.  (Its columns: P_t of the page two before has been
+      // taken by its P V, which this warp issued first.)
+      auto issue_s = [&](int half) {
+        const int slot = ki % C::NK;
+        const uint64_t kd = ptx::smem_desc(
+            ptx::smem_u32(smem + C::kK + slot * C::kTileBytes + half * C::kPageBytes), 16, 8 * D,
+            C::kSwK);
+        ptx::mma_f8_elect<D / 32>(s_col + 64 * half, q_lo, kd, idesc_s);
+        ptx::mma_f8_elect<D / 32, true>(s_col + 64 * half, q_hi, kd, idesc_s);
+        ptx::mma_commit_elect(ptx::smem_u32(&cb->s_full[t][half]));
+        if (half == 1) {
+          ptx::mma_commit_elect(ptx::smem_u32(&cb->k_free[slot]));
+          ++ki;
+        }
+      };
+      auto wait_k = [&]() {
+        const bool landed = wait(cb->k_full[ki % C::NK], (ki / C::NK) & 1);
+        ptx::tc_fence_after();
+        return landed;
+      };
       for (int b = 0; ok; ++b) {
         const WidePlan& plan = plan_of(b, &ok);
         if (!ok) break;
@@ -271,43 +297,51 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const bool mine = plan.rows > 128 * t;
         plan_done(b);
         if (count == 0) break;
-        if (first && mine) {
+        if (!mine) {
+          // (A row tile that the unit has not: the slots are let go all the same.)
+          for (int n = 0; ok && n < count; ++n, ++i, ++ki) {
+            ok = wait_k();
+            if (!ok) break;
+            ptx::mma_commit_elect(ptx::smem_u32(&cb->k_free[ki % C::NK]));
+            ok = wait(cb->vh_full[i & 1], (i >> 1) & 1);
+            if (ok) ptx::mma_commit_elect(ptx::smem_u32(&cb->vh_free[i & 1]));
+          }
+          continue;
+        }
+        if (first) {
           ok = wait(cb->q_full[t], seg & 1);
+          if (ok) ok = wait_k();
           if (!ok) break;
+          issue_s(0);
+          issue_s(1);
+          if (seg > 0) ok = wait(cb->o_free[t], (seg - 1) & 1);
         }
 #pragma unroll 1
-        for (int n = 0; n < count; ++n, ++i) {
-          const int slot = i % C::NK, hb = i & 1;
-          ok = wait(cb->k_full[slot], (i / C::NK) & 1);
-          if (!ok) break;
-          if (mine) {
-            ptx::tc_fence_after();
-            const uint64_t kd =
-                ptx::smem_desc(ptx::smem_u32(smem + C::kK + slot * C::kTileBytes), 16, 8 * D, C::kSwK);
-            // (S_t's columns: P_t of the tile before has been taken by its P V,
-            // which this warp issued first.)
-            ptx::mma_f8_elect<D / 32>(s_col, q_lo, kd, idesc_s);
-            ptx::mma_f8_elect<D / 32, true>(s_col, q_hi, kd, idesc_s);
-            ptx::mma_commit_elect(ptx::smem_u32(&cb->s_full[t]));
-          }
-          ptx::mma_commit_elect(ptx::smem_u32(&cb->k_free[slot]));
+        for (int n = 0; ok && n < count; ++n, ++i, ++tiles) {
+          const int hb = i & 1;
+          const bool end = last && n + 1 == count;  // of the segment
+          const uint64_t vd = ptx::smem_desc(ptx::smem_u32(smem + C::kVh + hb * C::kVhBytes),
+                                             kTileKeys * 128, 1024, ptx::kLayoutSw128);
           ok = wait(cb->vh_full[hb], (i >> 1) & 1);
-          if (!ok) break;
-          if (mine) {
-            const bool fresh = first && n == 0;
-            if (fresh && seg > 0) ok = wait(cb->o_free[t], (seg - 1) & 1);
-            if (ok) ok = wait(cb->p_full[t], tiles & 1);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (ok) ok = wait(cb->p_full[t][half], tiles & 1);
             if (!ok) break;
             ptx::tc_fence_after();
-            const uint64_t vd = ptx::smem_desc(ptx::smem_u32(smem + C::kVh + hb * C::kVhBytes),
-                                               kTileKeys * 128, 1024, ptx::kLayoutSw128);
-            issue_pv_group<128>(o_col, s_col, vd, idesc_pv, fresh ? 0u : 1u);
-            ++tiles;
-            if (last && n + 1 == count) ptx::mma_commit_elect(ptx::smem_u32(&cb->o_full[t]));
+            // (issue_pv_half counts from a 128-key tile's P; this page's is its own.)
+            issue_pv_half<128>(o_col, s_col + 64 * half - 32 * half, vd, idesc_pv,
+                               first && n == 0 && half == 0 ? 0u : 1u, half);
+            ptx::mma_commit_elect(ptx::smem_u32(&cb->pv_done[t][half]));
+            if (end && half == 1) ptx::mma_commit_elect(ptx::smem_u32(&cb->o_full[t]));
+            if (!end) {
+              if (half == 0) ok = wait_k();
+              if (ok) issue_s(half);
+            }
           }
+          if (!ok) break;
           ptx::mma_commit_elect(ptx::smem_u32(&cb->vh_free[hb]));
         }
-        if (last && mine) ++seg;
+        if (last) ++seg;
       }
       ptx::mma_commit_elect(ptx::smem_u32(&cb->drain));
       wait_drain_warp(ptx::smem_u32(&cb->drain), 0, a.status);
@@ -433,7 +467,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const uint32_t o_addr = tmem + lane_base + C::kOt + 128 * t;
     uint8_t* q_tile = smem + C::kQ + 2 * t * C::kTermBytes;
     bool ok = true;
-    int tiles = 0, seg = 0, segs = 0;  // of this row tile; segments of the CTA
+    int tiles = 0, seg = 0, segs = 0;  // key tiles and segments of this row tile; segments of the CTA
     // The segment's row: scale of its terms, the keys it sees ([lo, hi), [0,
     // sink) and those its mask names from key ctx on), maximum and sum.
     float qs = 0.f, m_used = neg_inf, l = 0.f;
@@ -542,30 +576,32 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       ok = wait(cb->scale_full[b % kPagedPlans], (b / kPagedPlans) & 1);
       if (!ok) break;
 #pragma unroll 1
-      for (int n = 0; n < count; ++n, ++tiles) {
-        const PagePlan g0 = plan.page[2 * n], g1 = plan.page[2 * n + 1];
-        const int k0 = (tile0 + n + (n >= gap_at ? gap : 0)) * kTileKeys;
-        ok = wait(cb->s_full[t], tiles & 1);
+      for (int step = 0; step < 2 * count; ++step) {
+        const int half = step & 1;
+        const PagePlan g = plan.page[step];
+        const int k0 = (tile0 + (step >> 1) + ((step >> 1) >= gap_at ? gap : 0)) * kTileKeys +
+                       half * kPageTokens;
+        const uint32_t s_half = s_addr + 64 * half;
+        ok = wait(cb->s_full[t][half], tiles & 1);
         if (!ok) break;
         ptx::tc_fence_after();
-        float s[kTileKeys], qmax[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) ptx::tmem_ld32_max(s_addr + q * 32, s + q * 32, qmax[q]);
+        float s[kPageTokens], qmax[2];
+        ptx::tmem_ld32_max(s_half, s, qmax[0]);
+        ptx::tmem_ld32_max(s_half + 32, s + 32, qmax[1]);
         ptx::tmem_wait_ld();
 #pragma unroll
-        for (int q = 0; q < 8; ++q) ptx::reg_fence16f(s + q * 16);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) ptx::reg_fence1f(qmax[q]);
-        float f0 = qs * g0.ks, f1 = qs * g1.ks;
+        for (int q = 0; q < 4; ++q) ptx::reg_fence16f(s + q * 16);
+        ptx::reg_fence1f(qmax[0]);
+        ptx::reg_fence1f(qmax[1]);
+        float f = qs * g.ks;
         float top;
-        if ((k0 >= lo_i || k0 + kTileKeys <= sink_i) && k0 + kTileKeys <= hi_i &&
-            (g0.held & g1.held)) {
-          top = fmaxf(fmaxf(qmax[0], qmax[1]) * f0 + g0.lv, fmaxf(qmax[2], qmax[3]) * f1 + g1.lv);
+        if ((k0 >= lo_i || k0 + kPageTokens <= sink_i) && k0 + kPageTokens <= hi_i && g.held) {
+          top = fmaxf(qmax[0], qmax[1]) * f;
         } else {
           // A word of visible keys for each 32; the scores themselves from here on.
           top = neg_inf;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < 2; ++q) {
             const int at = k0 + 32 * q;
             uint32_t seen = (low_bits(hi_i - at) & ~low_bits(lo_i - at)) | low_bits(sink_i - at);
             const int p = at - ctx;  // node of the first key
@@ -575,8 +611,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
               const uint32_t w1 = k + 1 < a.tree_words ? __ldg(mask_row + k + 1) : 0u;
               seen |= __funnelshift_r(w0, w1, p & 31) & low_bits(keys_hi - at);
             }
-            if (!(q < 2 ? g0.held : g1.held)) seen = 0;
-            const float f = q < 2 ? f0 : f1;
+            if (!g.held) seen = 0;
             float m4[4] = {neg_inf, neg_inf, neg_inf, neg_inf};
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
@@ -584,29 +619,33 @@ __global__ void __launch_bounds__(kWideThreads, 1)
               s[32 * q + c] = x;
               m4[c & 3] = fmaxf(m4[c & 3], x);
             }
-            const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-            top = fmaxf(top, m + (q < 2 ? g0.lv : g1.lv));
+            top = fmaxf(top, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
           }
-          f0 = 1.f;
-          f1 = 1.f;
+          f = 1.f;
         }
-        const float m_tile = top - kPagedBias;
+        const float m_tile = top + g.lv - kPagedBias;
         const bool need = m_tile > m_used + kRescaleLog2;
         if (__any_sync(0xffffffffu, need)) {
           const float m_new = fmaxf(m_used, m_tile);
           const float root = m_used == neg_inf ? 0.f : root_ex2(m_used - m_new);
-          if (!plan.first || n > 0) {
-            // O_t holds the earlier tiles: their P V ended before this S.
+          if (!plan.first || step > 0) {
+            // O_t holds the earlier pages once the last one's P V is complete.  (Its
+            // barrier cannot have gone on: that takes this warp's next P.)
+            ok = wait(cb->pv_done[t][half ^ 1], (half ? tiles : tiles - 1) & 1);
+            if (!ok) break;
+            ptx::tc_fence_after();
             const float alpha = root * root;
 #pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 16) {
-              uint32_t o[16];
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              uint32_t o[32];
               ptx::tmem_ld16(o_addr + c0, o);
+              ptx::tmem_ld16(o_addr + c0 + 16, o + 16);
               ptx::tmem_wait_ld();
               ptx::reg_fence16(o);
+              ptx::reg_fence16(o + 16);
 #pragma unroll
-              for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-              ptx::tmem_st16(o_addr + c0, o);
+              for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+              ptx::tmem_st32(o_addr + c0, o);
             }
           }
           if (m_new != neg_inf) {
@@ -615,22 +654,18 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           }
         }
         const float base = m_used == neg_inf ? 0.f : m_used;
-        const uint64_t nb2 = ptx::f2_pack(-base, -base);
+        const uint64_t nb2 = ptx::f2_pack(-base, -base), f2 = ptx::f2_pack(f, f);
+        const uint64_t v2 = ptx::f2_pack(g.vs, g.vs);
         uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
-        uint32_t pr[kTileKeys / 2];
+        uint32_t pr[kPageTokens / 2];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const float f = half ? f1 : f0, vs = half ? g1.vs : g0.vs;
-          const uint64_t f2 = ptx::f2_pack(f, f), v2 = ptx::f2_pack(vs, vs);
-#pragma unroll
-          for (int c = 64 * half; c < 64 * half + 64; c += 2) {
-            float u, v;
-            ptx::f2_unpack(ptx::fma2(ptx::f2_pack(s[c], s[c + 1]), f2, nb2), u, v);
-            const uint64_t p2 = ptx::f2_pack(ptx::ex2(u), ptx::ex2(v));
-            ls[(c >> 1) & 3] = ptx::add2(ls[(c >> 1) & 3], p2);
-            ptx::f2_unpack(ptx::mul2(p2, v2), u, v);
-            pr[c >> 1] = ptx::pack_f16x2(u, v);
-          }
+        for (int c = 0; c < kPageTokens; c += 2) {
+          float u, v;
+          ptx::f2_unpack(ptx::fma2(ptx::f2_pack(s[c], s[c + 1]), f2, nb2), u, v);
+          const uint64_t p2 = ptx::f2_pack(ptx::ex2(u), ptx::ex2(v));
+          ls[(c >> 1) & 3] = ptx::add2(ls[(c >> 1) & 3], p2);
+          ptx::f2_unpack(ptx::mul2(p2, v2), u, v);
+          pr[c >> 1] = ptx::pack_f16x2(u, v);
         }
         {
           float a0, a1, b0, b1;
@@ -638,11 +673,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           ptx::f2_unpack(ptx::add2(ls[2], ls[3]), b0, b1);
           l += (a0 + b0) + (a1 + b1);
         }
-        ptx::tmem_st32(s_addr, pr);
-        ptx::tmem_st32(s_addr + 32, pr + 32);
+        ptx::tmem_st32(s_half, pr);
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
-        ptx::mbar_arrive(ptx::smem_u32(&cb->p_full[t]));
+        ptx::mbar_arrive(ptx::smem_u32(&cb->p_full[t][half]));
+        tiles += half;
       }
       if (!ok) break;
       if (!ends) {
