@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include "paged_index.h"
+#include "sm103_ptx.cuh"
 
 namespace fa {
 
@@ -54,13 +55,19 @@ __device__ __forceinline__ int terms_exponent(float mx) {
   return imax((int)(__float_as_uint(mx) >> 23) - 127, -100);
 }
 __device__ __forceinline__ void split_terms(const float* x, int e, uint32_t* hi, uint32_t* lo) {
+  // As f16 pairs, which hold a scaled bf16 exactly down to 2^-14, far below e4m3's
+  // last step, and its difference to hi.  (A conversion takes longer than any
+  // product: four of them for two values, through fp32 five.)
   const float f = __uint_as_float((uint32_t)(7 - e + 127) << 23);
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const float y0 = x[2 * k] * f, y1 = x[2 * k + 1] * f;
-    hi[k] = pack_e4m3x2(y0, y1);
-    const float2 h2 = f16x2_floats(unpack_e4m3x2(hi[k]));
-    lo[k] = pack_e4m3x2(y0 - h2.x, y1 - h2.y);
+    uint32_t y = ptx::pack_f16x2(x[2 * k] * f, x[2 * k + 1] * f);
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(y));
+    hi[k] = c;
+    asm("sub.f16x2 %0, %0, %1;" : "+r"(y) : "r"(unpack_e4m3x2(hi[k])));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(y));
+    lo[k] = c;
   }
 }
 // What the terms' products are to be multiplied by, for scores times `scale`:

@@ -27,7 +27,7 @@ cudaError_t launch(const CUtensorMap& k_map, const CUtensorMap& v_map, const Pag
   if (e != cudaSuccess || grid < 2) return e;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof cfg);
-  cfg.gridDim = dim3(grid - 1, 8);
+  cfg.gridDim = dim3(grid - 1, 16);
   cfg.blockDim = dim3(kWideMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

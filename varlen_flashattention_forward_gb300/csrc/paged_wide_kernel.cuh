@@ -494,49 +494,60 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         // The warp's 32 rows come together, as bf16 into the place of their two
         // terms, a half of the dims each; then kLanes lanes take a row at a time.
         // (In short loops: the code runs once a segment, and is fetched each time.)
-        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
-        const int sub = lane % kLanes, dim0 = sub * 8;
+        constexpr int kLanes = D / 16, kAtOnce = 32 / kLanes;
+        const int sub = lane % kLanes, dim0 = sub * 16;
         const long long mine_at =
             valid ? (long long)row_q * a.q_row + (long long)row_h * a.q_head : -1;
-        // (Raw: 16 bytes of dims dim0 .., in the term of their half.)
+        // (Raw: 32 bytes of dims dim0 .., in the term of their half.)
         uint8_t* warp_q = q_tile + (warp & 3) * 32 * D;
-        uint8_t* raw0 = warp_q + (sub >= kLanes / 2 ? C::kTermBytes : 0) + (sub % (kLanes / 2)) * 16;
-#pragma unroll 1
-        for (int n = lane / kLanes; n < 32; n += kAtOnce) {
+        uint8_t* raw0 = warp_q + (sub >= kLanes / 2 ? C::kTermBytes : 0) + (sub % (kLanes / 2)) * 32;
+#pragma unroll 2
+        for (int k = 0; k < kLanes; ++k) {
+          const int n = k * kAtOnce + lane / kLanes;
           const long long at = __shfl_sync(0xffffffffu, mine_at, n);
-          const bool some = at >= 0 && dim0 < a.dim;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                           ptx::smem_u32(raw0 + n * D)),
-                       "l"(a.q + (some ? at + dim0 : 0)), "r"(some ? 16 : 0)
-                       : "memory");
+          const uint16_t* from = a.q + (at >= 0 ? at + dim0 : 0);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const bool some = at >= 0 && dim0 + 8 * c < a.dim;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             ptx::smem_u32(raw0 + n * D + 16 * c)),
+                         "l"(some ? from + 8 * c : a.q), "r"(some ? 16 : 0)
+                         : "memory");
+          }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
-        const int unit = dim0 >> 4;
-#pragma unroll 1
+#pragma unroll 2
         for (int k = 0; k < kLanes; ++k) {
           const int n = k * kAtOnce + lane / kLanes;
-          float x[8], mx = 0.f;
-          bool finite = true;
-          unpack_bf16x8(*reinterpret_cast<const uint4*>(raw0 + n * D), x);
+          const uint4 r0 = *reinterpret_cast<const uint4*>(raw0 + n * D);
+          const uint4 r1 = *reinterpret_cast<const uint4*>(raw0 + n * D + 16);
+          // The largest magnitude, as bits of bf16 (those past infinity's are NaN).
+          const uint32_t w[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+          uint32_t top = 0;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            finite = finite && fabsf(x[c]) <= 3.402823466e38f;
-            mx = fmaxf(mx, fabsf(x[c]));
-          }
-          if (!finite) mx = __int_as_float(0x7f800000);
+          for (int c = 0; c < 8; ++c) top = __vmaxu2(top, w[c] & 0x7fff7fffu);
+          top = max(top & 0xffffu, top >> 16);
 #pragma unroll
           for (int o = kLanes / 2; o > 0; o >>= 1)
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));  // (the row is read)
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, o));  // (the row is read)
+          const float mx = __uint_as_float(min(top, 0x7f80u) << 16);
           const int e = terms_exponent(mx);
-          uint32_t hi[4], lo[4];
+          float x[8];
+          uint32_t hi[8], lo[8];
+          unpack_bf16x8(r0, x);
           split_terms(x, e, hi, lo);
+          unpack_bf16x8(r1, x);
+          split_terms(x, e, hi + 4, lo + 4);
           // (n and the row's number in the tile agree modulo 32.)
-          const int us = D == 128 ? (unit ^ (n & 7)) : (unit ^ ((n >> 1) & 3));
-          uint8_t* at = warp_q + n * D + us * 16 + (dim0 & 8);
-          *reinterpret_cast<uint2*>(at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-          *reinterpret_cast<uint2*>(at + C::kTermBytes) =
-              make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+          const int us = D == 128 ? (sub ^ (n & 7)) : (sub ^ ((n >> 1) & 3));
+          uint8_t* at = warp_q + n * D + us * 16;
+          *reinterpret_cast<uint4*>(at) =
+              make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16,
+                         hi[6] | hi[7] << 16);
+          *reinterpret_cast<uint4*>(at + C::kTermBytes) =
+              make_uint4(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16,
+                         lo[6] | lo[7] << 16);
           // Its scale to the row's thread.
           const float scale = __shfl_sync(0xffffffffu, terms_scale(mx, e, a.scale_log2),
                                           (lane % kAtOnce) * kLanes);
