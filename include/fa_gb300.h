@@ -575,7 +575,7 @@ fa_status fa_paged_attn_masked(const void* q, long long q_row_stride, long long 
 
 /*
  * fa_paged_attn_masked_plan -- fa_paged_attn_plan for a fa_paged_attn_masked call
- * under sinks or a tree: more than 32 rows (tokens x heads of one group) of a
+ * under sinks or a tree: more than 16 rows (tokens x heads of one group) of a
  * sequence then go 256 to a tile.
  */
 fa_status fa_paged_attn_masked_plan(int batch, int total_q, int num_heads, int num_heads_k,

@@ -39,16 +39,17 @@ struct AttnLaunch {
   size_t o_bytes, lse_bytes, meta_bytes;
   size_t bytes() const { return o_bytes + lse_bytes + meta_bytes; }
 };
-// masked: under sinks or a tree, where more than kNarrowRows rows go 256 to a tile
-// (paged_wide_kernel).
-constexpr int kNarrowRows = 32;
+// masked: under sinks or a tree, where more than 16 rows go 256 to a tile
+// (paged_wide_kernel): trees of 5 and 8 nodes, 4 heads of a group (20 and 32 rows),
+// 24 sequences of 517 to 5000 keys, 8 kv heads of 128 dims 64 and 65 us, 32 to a
+// tile 70 and 76; 4 nodes (16 rows) 16 to a tile 54 us; 64 nodes 86 against 384.
 AttnLaunch attn_launch(int sm_count, int batch, int total_q, int group, int head_dim,
                        int max_seqlen_q, bool masked) {
   AttnLaunch l;
   const long long tokens =
       max_seqlen_q > 0 ? max_seqlen_q : ((long long)total_q + batch - 1) / batch;
   const long long rows = tokens * group;
-  l.rows = rows <= 16 ? 16 : masked && rows > kNarrowRows ? fa::kWideRows : 32;
+  l.rows = rows <= 16 ? 16 : masked ? fa::kWideRows : 32;
   l.dim = head_dim <= 64 ? 64 : 128;
   l.grid = std::min(sm_count, fa::kPagedMaxGrid);
   l.o_bytes = (size_t)2 * l.grid * l.rows * l.dim * sizeof(float);

@@ -41,15 +41,19 @@ cudaError_t launch_attn(const CUtensorMap& k_map, const CUtensorMap& v_map, cons
   return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, N>, a);
 }
 
-// The instantiation for padded head dim `dim` and `rows` rows a tile.
+// The instantiation for padded head dim `dim` and `rows` rows a tile (16 under a
+// mask: more rows go to paged_wide_kernel).
 template <int kMask>
 cudaError_t launch_attn_shape(int dim, int rows, const CUtensorMap& k_map, const CUtensorMap& v_map,
                               const PagedAttnArgs& a, int grid, cudaStream_t stream) {
-  if (dim == 64)
-    return rows == 16 ? launch_attn<64, 16, kMask>(k_map, v_map, a, grid, stream)
-                      : launch_attn<64, 32, kMask>(k_map, v_map, a, grid, stream);
-  return rows == 16 ? launch_attn<128, 16, kMask>(k_map, v_map, a, grid, stream)
-                    : launch_attn<128, 32, kMask>(k_map, v_map, a, grid, stream);
+  if constexpr (kMask == kNoMask) {
+    if (rows == 32)
+      return dim == 64 ? launch_attn<64, 32, kMask>(k_map, v_map, a, grid, stream)
+                       : launch_attn<128, 32, kMask>(k_map, v_map, a, grid, stream);
+  }
+  if (rows != 16) return cudaErrorInvalidValue;
+  return dim == 64 ? launch_attn<64, 16, kMask>(k_map, v_map, a, grid, stream)
+                   : launch_attn<128, 16, kMask>(k_map, v_map, a, grid, stream);
 }
 // Those of the masked ones, in translation units of their own.
 cudaError_t launch_attn_sinks(int dim, int rows, const CUtensorMap& k_map, const CUtensorMap& v_map,
