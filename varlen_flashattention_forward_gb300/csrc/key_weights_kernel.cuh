@@ -18,8 +18,10 @@
 // into equal contiguous ranges (paged_index.h), one for each CTA, so a tile is
 // one CTA's alone.  More rows than N go in chunks, tile by tile again.
 //
+//   producer   walks the CTA's segments of key tiles and publishes them, 16 tiles
+//              at a time with their pages' scales, then loads the pages by TMA
+//              into a ring of K tiles
 //   issuer     S MMAs into two buffers of N columns
-//   producer   TMA of the pages into a ring of K tiles, ahead of both
 //   the rest   stage the rows of Q, then a thread for each key: exp2, sum, the
 //              weight's update.  Where a tile has 64 or 128 rows, whose
 //              exponentials take longer than its bytes, two warpgroups take
@@ -40,7 +42,7 @@
 
 namespace fa {
 
-constexpr int kWeightMaxBatch = 512;  // sequences of a launch
+constexpr int kWeightMaxBatch = 256;  // sequences of a launch
 
 struct KeyWeightsArgs {
   const uint16_t* q;
@@ -74,36 +76,11 @@ struct WeightsCfg {
   static constexpr int kResident = N <= 16 ? 4 : N <= 64 ? 3 : 2;
 };
 
-template <int N>
-struct alignas(16) WeightsCtl {
-  uint64_t k_full[3], k_free[3];  // K slot landed / read
-  uint64_t s_full[2], s_free[2];  // St computed / loaded (128)
-  uint64_t q_full;                // rows of a chunk staged (all key threads)
-  uint64_t drain;
-  uint32_t tmem_base;
-  volatile int abort_flag;
-  alignas(16) float4 row[N / 2];  // of two rows: score factors, then -LSE log2(e)
-  alignas(16) int token[N];       // of a row, from the chunk's first; -1: no row
-  long long warp_sum[4];
-  int before[kWeightMaxBatch + 1];
-};
-template <int D, int N>
-constexpr size_t weights_smem() {
-  return 1024 + WeightsCfg<D, N>::kCtl + sizeof(WeightsCtl<N>);
-}
-// (Of an SM's 228 KB, each CTA takes 1 KB more than its own.)
-template <int N>
-constexpr bool weights_fit() {
-  return WeightsCfg<128, N>::kResident * (weights_smem<128, N>() + 1024) <= 228 * 1024;
-}
-static_assert(weights_fit<16>() && weights_fit<32>() && weights_fit<64>() && weights_fit<128>(),
-              "resident CTAs");
-
 // A chunk of a sequence's rows against its keys.
 struct WeightChunk {
   KeyRange keys;
+  int span;        // from its first row's token to its last row's
   long long at0;   // position of its first row's token
-  int span;        // from there to its last row's token
   // Whether some row may see a key of the tile; of the tiles [j0, j1).
   __device__ __forceinline__ bool seen(int j0) const { return any(j0, (long long)j0 + kTileKeys); }
   __device__ __forceinline__ bool any(int j0, long long j1) const {
@@ -128,6 +105,44 @@ __device__ __forceinline__ WeightChunk weight_chunk(const AttnShape& s, int c, i
   return w;
 }
 
+// Up to 16 tiles of a segment for one chunk of its rows; count = 0 ends the range.
+struct alignas(16) WeightPlan {
+  float scale[32];      // of the tiles' pages, NaN where there is none
+  WeightChunk chunk;
+  int seq, head, len, keys_hi;
+  int row0, rows, c;    // the sequence's first row and rows, number of the chunk
+  int tile0, count;
+  int first, any;       // it begins the chunk; some tile of the segment is seen in it
+};
+constexpr int kWeightPlans = 4;
+
+template <int N>
+struct alignas(16) WeightsCtl {
+  uint64_t plan_full[kWeightPlans], plan_free[kWeightPlans];  // published / read by every warp
+  uint64_t k_full[3], k_free[3];  // K slot landed / read
+  uint64_t s_full[2], s_free[2];  // St computed / loaded (128)
+  uint64_t q_full;                // rows of a chunk staged (all key threads)
+  uint64_t drain;
+  uint32_t tmem_base;
+  volatile int abort_flag;
+  alignas(16) float4 row[N / 2];  // of two rows: score factors, then -LSE log2(e)
+  alignas(16) int token[N];       // of a row, from the chunk's first; -1: no row
+  WeightPlan plan[kWeightPlans];
+  long long warp_sum[4];
+  int before[kWeightMaxBatch + 1];
+};
+template <int D, int N>
+constexpr size_t weights_smem() {
+  return 1024 + WeightsCfg<D, N>::kCtl + sizeof(WeightsCtl<N>);
+}
+// (Of an SM's 228 KB, each CTA takes 1 KB more than its own.)
+template <int N>
+constexpr bool weights_fit() {
+  return WeightsCfg<128, N>::kResident * (weights_smem<128, N>() + 1024) <= 228 * 1024;
+}
+static_assert(weights_fit<16>() && weights_fit<32>() && weights_fit<64>() && weights_fit<128>(),
+              "resident CTAs");
+
 template <int D, int N>
 __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::kResident)
     key_weights_kernel(const __grid_constant__ CUtensorMap k_map, const KeyWeightsArgs a) {
@@ -150,6 +165,10 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
 
   if (tid == C::kKeyThreads) {
     auto init = [&](uint64_t& b, uint32_t n) { ptx::mbar_init(ptx::smem_u32(&b), n); };
+    for (int s = 0; s < kWeightPlans; ++s) {
+      init(cb->plan_full[s], 1);
+      init(cb->plan_free[s], kProducer);  // the warps before it
+    }
     for (int s = 0; s < C::kSlots; ++s) {
       init(cb->k_full[s], 1);
       init(cb->k_free[s], 1);
@@ -185,58 +204,101 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
   auto wait = [&](uint64_t& b, int parity) {
     return paged_wait(ptx::smem_u32(&b), (uint32_t)parity, abort_flag, a.status, a.wait_limit_ns);
   };
-  // Every role walks the CTA's segments by itself.
-  SegmentWalk walk;
-  Segment g = {};
-  walk_begin(&walk, range_start(total, gridDim.x, blockIdx.x),
-             range_start(total, gridDim.x, blockIdx.x + 1), a.batch, before);
-  int rows = 0, row0 = 0;  // of the segment's sequence
-  auto next = [&]() {
-    if (!walk_next(&walk, whole, before, seq_of, &g)) return false;
-    const RowRange r = row_range(__ldg(a.cu + g.seq), __ldg(a.cu + g.seq + 1), a.total_q);
-    row0 = r.lo;
-    rows = r.n;
-    return true;
+  // Batch number b; every warp but the producer's reads it and lets it go.
+  auto plan_of = [&](int b, bool* ok) -> const WeightPlan& {
+    *ok = wait(cb->plan_full[b % kWeightPlans], (b / kWeightPlans) & 1);
+    return cb->plan[b % kWeightPlans];
+  };
+  auto plan_done = [&](int b) {
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->plan_free[b % kWeightPlans]));
   };
   bool ok = true;
 
   if (warp == kProducer) {
     // ------------------------------------------------------------ producer
     test_load_delay(a.wait_limit_ns);
+    SegmentWalk walk;
+    walk_begin(&walk, range_start(total, gridDim.x, blockIdx.x),
+               range_start(total, gridDim.x, blockIdx.x + 1), a.batch, before);
+    Segment g = {};
+    int rows = 0, row0 = 0;       // of the segment's sequence
+    int c = 0, chunks = 0, t0 = 0;  // of the batch at hand
+    auto next_segment = [&]() {
+      if (!walk_next(&walk, whole, before, seq_of, &g)) return false;
+      const RowRange r = row_range(__ldg(a.cu + g.seq), __ldg(a.cu + g.seq + 1), a.total_q);
+      row0 = r.lo;
+      rows = r.n;
+      chunks = row_tiles(sh, rows);
+      c = 0;
+      t0 = 0;
+      return true;
+    };
+    bool more = next_segment();
     int loads = 0;
-    while (ok && next()) {
-      const int chunks = row_tiles(sh, rows);
-      for (int c = 0; ok && c < chunks; ++c) {
-        const WeightChunk wc = weight_chunk(sh, c, rows, g.len);
-#pragma unroll 1
-        for (int t0 = 0; ok && t0 < g.count; t0 += 16) {
-          // Lane l: page l of the next 16 tiles, as its cell, or -1.
-          int cell = -1;
-          const long long p = (long long)(g.tile0 + t0) * 2 + lane;
-          if (t0 + lane / 2 < g.count && p * kPageTokens < g.keys.hi) {
-            const int id = checked_page(
-                __ldg(a.page_table + (size_t)g.seq * a.max_pages + p), a.num_pages);
-            if (id >= 0) cell = id * sh.heads_k + g.head;
-          }
-          const int end = imin(16, g.count - t0);
-#pragma unroll 1
-          for (int t = 0; t < end; ++t) {
-            if (!wc.seen((g.tile0 + t0 + t) * kTileKeys)) continue;
-            const int mine = __shfl_sync(0xffffffffu, cell, 2 * t + (lane & 1));
-            const unsigned held = __ballot_sync(0xffffffffu, mine >= 0) & 3;
-            const int s = loads % C::kSlots;
-            if (loads >= C::kSlots) ok = wait(cb->k_free[s], (loads / C::kSlots - 1) & 1);
-            if (!ok) break;
-            const uint32_t bar = ptx::smem_u32(&cb->k_full[s]);
-            if (lane == 0)
-              ptx::mbar_arrive_expect_tx(bar, ((held & 1) + (held >> 1)) * C::kPageBytes);
-            __syncwarp();
-            if (lane < 2 && mine >= 0)
-              ptx::tma_load_3d(ptx::smem_u32(smem + s * C::kTileBytes) + lane * C::kPageBytes,
-                               &k_map, bar, 0, 0, mine);
-            ++loads;
+    for (int b = 0;; ++b) {
+      const int slot = b % kWeightPlans;
+      WeightPlan& plan = cb->plan[slot];
+      // Lane l: page l of the batch's tiles, as its cell, or -1, and its scale.
+      int cell = -1;
+      float scale = __int_as_float(0x7fffffff);
+      int tile0 = 0, count = 0;
+      WeightChunk wc = {};
+      if (more) {
+        tile0 = g.tile0 + t0;
+        count = imin(16, g.count - t0);
+        const long long p = (long long)tile0 * 2 + lane;
+        if (lane / 2 < count && p * kPageTokens < g.keys.hi) {
+          const int id = checked_page(
+              __ldg(a.page_table + (size_t)g.seq * a.max_pages + p), a.num_pages);
+          if (id >= 0) {
+            cell = id * sh.heads_k + g.head;
+            scale = __ldg(a.k_scale + cell);
           }
         }
+        wc = weight_chunk(sh, c, rows, g.len);
+      }
+      if (b >= kWeightPlans) ok = wait(cb->plan_free[slot], (b / kWeightPlans - 1) & 1);
+      if (!ok) break;
+      if (lane == 0) {
+        plan.count = count;
+        plan.chunk = wc;
+        plan.seq = g.seq;
+        plan.head = g.head;
+        plan.len = g.len;
+        plan.keys_hi = g.keys.hi;
+        plan.row0 = row0;
+        plan.rows = rows;
+        plan.c = c;
+        plan.tile0 = tile0;
+        plan.first = t0 == 0;
+        plan.any = wc.any(g.tile0 * kTileKeys, (g.tile0 + g.count) * (long long)kTileKeys);
+      }
+      plan.scale[lane] = scale;
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->plan_full[slot]));
+      if (!more) break;
+#pragma unroll 1
+      for (int t = 0; t < count; ++t) {
+        if (!wc.seen((tile0 + t) * kTileKeys)) continue;
+        const int mine = __shfl_sync(0xffffffffu, cell, 2 * t + (lane & 1));
+        const unsigned held = __ballot_sync(0xffffffffu, mine >= 0) & 3;
+        const int s = loads % C::kSlots;
+        if (loads >= C::kSlots) ok = wait(cb->k_free[s], (loads / C::kSlots - 1) & 1);
+        if (!ok) break;
+        const uint32_t bar = ptx::smem_u32(&cb->k_full[s]);
+        if (lane == 0) ptx::mbar_arrive_expect_tx(bar, ((held & 1) + (held >> 1)) * C::kPageBytes);
+        __syncwarp();
+        if (lane < 2 && mine >= 0)
+          ptx::tma_load_3d(ptx::smem_u32(smem + s * C::kTileBytes) + lane * C::kPageBytes, &k_map,
+                           bar, 0, 0, mine);
+        ++loads;
+      }
+      if (!ok) break;
+      t0 += 16;
+      if (t0 >= g.count) {
+        t0 = 0;
+        if (++c == chunks) more = next_segment();
       }
     }
     // Every copy this CTA started lands before it exits.
@@ -248,29 +310,30 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
     const uint64_t q_hi = ptx::smem_desc(ptx::smem_u32(smem + C::kQ), 16, 8 * D, C::kSwK);
     const uint64_t q_lo = ptx::smem_desc(ptx::smem_u32(smem + C::kQ + N * D), 16, 8 * D, C::kSwK);
     int i = 0, staged = 0;
-    while (ok && next()) {
-      const int chunks = row_tiles(sh, rows);
-      for (int c = 0; ok && c < chunks; ++c) {
-        const WeightChunk wc = weight_chunk(sh, c, rows, g.len);
-        if (!wc.any(g.tile0 * kTileKeys, (g.tile0 + g.count) * (long long)kTileKeys)) continue;
-        ok = wait(cb->q_full, staged++ & 1);
+    for (int b = 0; ok; ++b) {
+      const WeightPlan& plan = plan_of(b, &ok);
+      if (!ok || plan.count == 0) break;
+      const int count = plan.count, tile0 = plan.tile0;
+      const WeightChunk wc = plan.chunk;
+      const bool stage = plan.first && plan.any;
+      plan_done(b);
+      if (stage) ok = wait(cb->q_full, staged++ & 1);
 #pragma unroll 1
-        for (int t = 0; ok && t < g.count; ++t) {
-          if (!wc.seen((g.tile0 + t) * kTileKeys)) continue;
-          const int s = i % C::kSlots, sb = i & 1;
-          ok = wait(cb->k_full[s], (i / C::kSlots) & 1);
-          if (ok && i >= 2) ok = wait(cb->s_free[sb], ((i >> 1) - 1) & 1);
-          if (!ok) break;
-          ptx::tc_fence_after();
-          const uint64_t kd =
-              ptx::smem_desc(ptx::smem_u32(smem + s * C::kTileBytes), 16, 8 * D, C::kSwK);
-          // (The small terms first: each step rounds at the sum's size so far.)
-          ptx::mma_f8_elect<D / 32>(tmem + sb * N, kd, q_lo, idesc);
-          ptx::mma_f8_elect<D / 32, true>(tmem + sb * N, kd, q_hi, idesc);
-          ptx::mma_commit_elect(ptx::smem_u32(&cb->s_full[sb]));
-          ptx::mma_commit_elect(ptx::smem_u32(&cb->k_free[s]));
-          ++i;
-        }
+      for (int t = 0; ok && t < count; ++t) {
+        if (!wc.seen((tile0 + t) * kTileKeys)) continue;
+        const int s = i % C::kSlots, sb = i & 1;
+        ok = wait(cb->k_full[s], (i / C::kSlots) & 1);
+        if (ok && i >= 2) ok = wait(cb->s_free[sb], ((i >> 1) - 1) & 1);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint64_t kd =
+            ptx::smem_desc(ptx::smem_u32(smem + s * C::kTileBytes), 16, 8 * D, C::kSwK);
+        // (The small terms first: each step rounds at the sum's size so far.)
+        ptx::mma_f8_elect<D / 32>(tmem + sb * N, kd, q_lo, idesc);
+        ptx::mma_f8_elect<D / 32, true>(tmem + sb * N, kd, q_hi, idesc);
+        ptx::mma_commit_elect(ptx::smem_u32(&cb->s_full[sb]));
+        ptx::mma_commit_elect(ptx::smem_u32(&cb->k_free[s]));
+        ++i;
       }
     }
     ptx::mma_commit_elect(ptx::smem_u32(&cb->drain));
@@ -282,18 +345,20 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
     const uint32_t s_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const int key = tid & 127, group = tid >> 7;
     int i = 0;
-    while (ok && next()) {
-      const int chunks = row_tiles(sh, rows);
-      float* out = a.weights + ((long long)g.seq * sh.heads_k + g.head) * a.capacity;
-      // The rows' own keys have no weight yet.
-      const long long fresh = (long long)g.len - rows;
-      for (int c = 0; ok && c < chunks; ++c) {
-        const WeightChunk wc = weight_chunk(sh, c, rows, g.len);
-        // ---- the chunk's rows of Q, if one is needed.  (The last chunk's MMAs
-        // are done: every thread has waited for them.  So the issuer has taken
-        // each staging before the next one.)
+    for (int b = 0;; ++b) {
+      // (A warp whose wait has given up joins the others here, and all leave.  So
+      // does every chunk's last tile before the next one's rows are staged.)
+      bool got;
+      const WeightPlan& plan = plan_of(b, &got);
+      ok = named_bar_and(1, C::kKeyThreads, ok && got);
+      if (!ok || plan.count == 0) break;
+      if (plan.first && plan.any) {
+        // ---- the chunk's rows of Q.  (The last chunk's MMAs are done: every thread
+        // has waited for them.  So the issuer has taken each staging before the
+        // next one.)
+        const int rows = plan.rows, row0 = plan.row0, c = plan.c, head = plan.head;
         const int n_rows = imin(N, rows * sh.group - c * N);
-        if (wc.any(g.tile0 * kTileKeys, (g.tile0 + g.count) * (long long)kTileKeys)) {
+        {
           const int sub = tid % kLanes, dim0 = sub * 8;
           uint8_t* q_s = smem + C::kQ;
           constexpr int kStep = C::kKeyThreads / kLanes;    // rows at once
@@ -306,7 +371,7 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
           for (int k = 0; k < kTurns; ++k) {
             const int n = tid / kLanes + k * kStep, row = c * N + n;
             token[k] = token_of(sh, row);
-            const int h = g.head * sh.group + row - token[k] * sh.group;
+            const int h = head * sh.group + row - token[k] * sh.group;
             raw[k] = make_uint4(0u, 0u, 0u, 0u);
             lse_of[k] = 0.f;
             if (n < n_rows && dim0 < a.dim)
@@ -354,103 +419,96 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
           ptx::mbar_arrive(ptx::smem_u32(&cb->q_full));
           named_bar_sync(1, C::kKeyThreads);
         }
-        // ---- the tiles
-#pragma unroll 1
-        for (int t0 = 0; ok && t0 < g.count; t0 += 16) {
-          // Lane l: page l of 16 tiles, its scale, NaN where there is none.
-          float scale = __int_as_float(0x7fffffff);
-          const long long p = (long long)(g.tile0 + t0) * 2 + lane;
-          if (t0 + lane / 2 < g.count && p * kPageTokens < g.keys.hi) {
-            const int id = checked_page(
-                __ldg(a.page_table + (size_t)g.seq * a.max_pages + p), a.num_pages);
-            if (id >= 0) scale = __ldg(a.k_scale + (size_t)id * sh.heads_k + g.head);
-          }
-          const int end = imin(16, g.count - t0);
-#pragma unroll 1
-          for (int t = 0; t < end; ++t) {
-            const int j0 = (g.tile0 + t0 + t) * kTileKeys, j = j0 + key;
-            const bool here = j < g.keys.hi;
-            const float ks = __shfl_sync(0xffffffffu, scale, 2 * t + ((warp >> 1) & 1));
-            const bool seen = wc.seen(j0);
-            // (Two groups: by turns.  What a chunk writes, the next may read in
-            // the other group, behind the barrier between them.)
-            if (C::kKeyThreads > 128 && (seen ? i & 1 : t & 1) != group) {
-              i += seen;
-              continue;
-            }
-            // What stands there already, and whether it changes.
-            const bool add = c > 0 || (a.decay != 0.f && j < fresh);
-            if (!seen && (c > 0 || (add && a.decay == 1.f))) continue;
-            float old = 0.f;
-            if (here && add) old = out[j];
-            if (c == 0) old *= a.decay;
-            float sum = 0.f;
-            if (seen) {
-              const int sb = i & 1;
-              ok = wait(cb->s_full[sb], (i >> 1) & 1);
-              if (!ok) break;
-              ptx::tc_fence_after();
-              const bool all = wc.whole(j0, sh);
-              // Rows that see the key: tokens [lo, hi].
-              int lo = 0, hi = 0x7fffffff;
-              if (!all) {
-                const long long r = (long long)j - wc.at0;
-                if (sh.causal) lo = (int)(r > 0 ? (r < 0x7fffffff ? r : 0x7fffffff) : 0);
-                if (sh.window >= 0 && j >= sh.sinks) {
-                  const long long w = r + sh.window;
-                  hi = (int)(w < 0x7fffffff ? (w > -1 ? w : -1) : 0x7fffffff);
-                }
-              }
-              const uint64_t ks2 = ptx::f2_pack(ks, ks);
-              uint64_t acc[2] = {0ull, 0ull};
-              // (Twice: the whole tile without a test for each row.)
-              auto add_up = [&](auto masked) {
-                // The next 16 columns load while these are summed.
-                uint32_t s[2][16];
-                ptx::tmem_ld16(s_lane + sb * N, s[0]);
-#pragma unroll
-                for (int n0 = 0; n0 < N; n0 += 16) {
-                  uint32_t* now = s[(n0 >> 4) & 1];
-                  ptx::tmem_wait_ld();
-                  ptx::reg_fence16(now);
-                  if (n0 + 16 < N) {
-                    ptx::tmem_ld16(s_lane + sb * N + n0 + 16, s[((n0 >> 4) & 1) ^ 1]);
-                  } else {
-                    ptx::tc_fence_before();
-                    ptx::mbar_arrive(ptx::smem_u32(&cb->s_free[sb]));
-                  }
-#pragma unroll
-                  for (int n = 0; n < 16; n += 2) {
-                    const ulonglong2 f =
-                        *reinterpret_cast<const ulonglong2*>(cb->row + (n0 + n) / 2);
-                    const uint64_t s2 =
-                        ptx::f2_pack(__uint_as_float(now[n]), __uint_as_float(now[n + 1]));
-                    float u, v;
-                    ptx::f2_unpack(ptx::fma2(s2, ptx::mul2(f.x, ks2), f.y), u, v);
-                    if constexpr (decltype(masked)::value != 0) {
-                      const int2 tok = *reinterpret_cast<const int2*>(cb->token + n0 + n);
-                      u = tok.x >= lo && tok.x <= hi ? u : neg_inf;
-                      v = tok.y >= lo && tok.y <= hi ? v : neg_inf;
-                    }
-                    acc[(n >> 1) & 1] =
-                        ptx::add2(acc[(n >> 1) & 1], ptx::f2_pack(ptx::ex2(u), ptx::ex2(v)));
-                  }
-                }
-              };
-              if (all) add_up(IntTag<0>{});
-              else add_up(IntTag<1>{});
-              float u, v;
-              ptx::f2_unpack(ptx::add2(acc[0], acc[1]), u, v);
-              sum = u + v;
-              if (__isnanf(ks)) sum = 0.f;  // (no page)
-              ++i;
-            }
-            if (here) out[j] = old + sum;
-          }
-        }
-        // (A warp whose wait has given up joins the others here, and all leave.)
-        ok = named_bar_and(1, C::kKeyThreads, ok);
       }
+      // ---- the tiles
+      const int count = plan.count, tile0 = plan.tile0, keys_hi = plan.keys_hi;
+      const bool first_chunk = plan.c == 0;
+      float* out = a.weights + ((long long)plan.seq * sh.heads_k + plan.head) * a.capacity;
+      // The rows' own keys have no weight yet.
+      const long long fresh = (long long)plan.len - plan.rows;
+      const WeightChunk& wc = plan.chunk;
+#pragma unroll 1
+      for (int t = 0; t < count; ++t) {
+        const int j0 = (tile0 + t) * kTileKeys, j = j0 + key;
+        const bool here = j < keys_hi;
+        const float ks = plan.scale[2 * t + ((warp >> 1) & 1)];
+        const bool seen = wc.seen(j0);
+        // (Two groups: by turns.  What a chunk writes, the next may read in
+        // the other group, behind the barrier between them.)
+        if (C::kKeyThreads > 128 && (seen ? i & 1 : t & 1) != group) {
+          i += seen;
+          continue;
+        }
+        // What stands there already, and whether it changes.
+        const bool add = !first_chunk || (a.decay != 0.f && j < fresh);
+        if (!seen && (!first_chunk || (add && a.decay == 1.f))) continue;
+        float old = 0.f;
+        if (here && add) old = out[j];
+        if (first_chunk) old *= a.decay;
+        float sum = 0.f;
+        if (seen) {
+          const int sb = i & 1;
+          ok = wait(cb->s_full[sb], (i >> 1) & 1);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const bool all = wc.whole(j0, sh);
+          // Rows that see the key: tokens [lo, hi].
+          int lo = 0, hi = 0x7fffffff;
+          if (!all) {
+            const long long r = (long long)j - wc.at0;
+            if (sh.causal) lo = (int)(r > 0 ? (r < 0x7fffffff ? r : 0x7fffffff) : 0);
+            if (sh.window >= 0 && j >= sh.sinks) {
+              const long long w = r + sh.window;
+              hi = (int)(w < 0x7fffffff ? (w > -1 ? w : -1) : 0x7fffffff);
+            }
+          }
+          const uint64_t ks2 = ptx::f2_pack(ks, ks);
+          uint64_t acc[2] = {0ull, 0ull};
+          // (Twice: the whole tile without a test for each row.)
+          auto add_up = [&](auto masked) {
+            // The next 16 columns load while these are summed.
+            uint32_t s[2][16];
+            ptx::tmem_ld16(s_lane + sb * N, s[0]);
+#pragma unroll
+            for (int n0 = 0; n0 < N; n0 += 16) {
+              uint32_t* now = s[(n0 >> 4) & 1];
+              ptx::tmem_wait_ld();
+              ptx::reg_fence16(now);
+              if (n0 + 16 < N) {
+                ptx::tmem_ld16(s_lane + sb * N + n0 + 16, s[((n0 >> 4) & 1) ^ 1]);
+              } else {
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(ptx::smem_u32(&cb->s_free[sb]));
+              }
+#pragma unroll
+              for (int n = 0; n < 16; n += 2) {
+                const ulonglong2 f =
+                    *reinterpret_cast<const ulonglong2*>(cb->row + (n0 + n) / 2);
+                const uint64_t s2 =
+                    ptx::f2_pack(__uint_as_float(now[n]), __uint_as_float(now[n + 1]));
+                float u, v;
+                ptx::f2_unpack(ptx::fma2(s2, ptx::mul2(f.x, ks2), f.y), u, v);
+                if constexpr (decltype(masked)::value != 0) {
+                  const int2 tok = *reinterpret_cast<const int2*>(cb->token + n0 + n);
+                  u = tok.x >= lo && tok.x <= hi ? u : neg_inf;
+                  v = tok.y >= lo && tok.y <= hi ? v : neg_inf;
+                }
+                acc[(n >> 1) & 1] =
+                    ptx::add2(acc[(n >> 1) & 1], ptx::f2_pack(ptx::ex2(u), ptx::ex2(v)));
+              }
+            }
+          };
+          if (all) add_up(IntTag<0>{});
+          else add_up(IntTag<1>{});
+          float u, v;
+          ptx::f2_unpack(ptx::add2(acc[0], acc[1]), u, v);
+          sum = u + v;
+          if (__isnanf(ks)) sum = 0.f;  // (no page)
+          ++i;
+        }
+        if (here) out[j] = old + sum;
+      }
+      plan_done(b);
     }
   }
   ptx::tc_fence_before();
