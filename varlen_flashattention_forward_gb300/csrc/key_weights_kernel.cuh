@@ -25,7 +25,8 @@
 //   the rest   stage the rows of Q, then a thread for each key: exp2, sum, the
 //              weight's update.  Where a tile has 64 or 128 rows, whose
 //              exponentials take longer than its bytes, two warpgroups take
-//              tiles by turns.
+//              pairs of tiles by turns: a row's factor and LSE come from shared
+//              memory, whose bandwidth bounds them, once for both.
 #pragma once
 
 #include <cstdint>
@@ -65,15 +66,17 @@ struct WeightsCfg {
   static constexpr uint32_t kSwK = D == 128 ? ptx::kLayoutSw128 : ptx::kLayoutSw64;
   static constexpr int kTileBytes = kTileKeys * D;
   static constexpr int kPageBytes = kPageTokens * D;
-  static constexpr int kSlots = 3;
+  static constexpr int kTiles = N >= 64 ? 2 : 1;  // of a key thread at once
+  static constexpr int kBuffers = 2 * kTiles;     // of St, N columns each
+  static constexpr int kSlots = N <= 32 ? 3 : N == 64 ? 5 : 6;
   static constexpr int kQBytes = 2 * N * D;
-  static constexpr uint32_t kTmemCols = 2 * N < 32 ? 32 : 2 * N;
+  static constexpr uint32_t kTmemCols = kBuffers * N;
   static constexpr int kQ = kSlots * kTileBytes;
   static constexpr int kCtl = kQ + kQBytes;
-  static constexpr int kKeyThreads = N >= 64 ? 256 : 128;
+  static constexpr int kKeyThreads = 128 * kTiles;
   static constexpr int kThreads = kKeyThreads + 64;
-  // Resident CTAs (by shared memory: 56 to 86 KB at 128 dims).
-  static constexpr int kResident = N <= 16 ? 4 : N <= 64 ? 3 : 2;
+  // Resident CTAs (by shared memory, 57 to 133 KB at 128 dims, and columns).
+  static constexpr int kResident = N == 16 ? 4 : N == 32 ? 3 : N == 64 ? 2 : 1;
 };
 
 // A chunk of a sequence's rows against its keys.
@@ -119,8 +122,8 @@ constexpr int kWeightPlans = 4;
 template <int N>
 struct alignas(16) WeightsCtl {
   uint64_t plan_full[kWeightPlans], plan_free[kWeightPlans];  // published / read by every warp
-  uint64_t k_full[3], k_free[3];  // K slot landed / read
-  uint64_t s_full[2], s_free[2];  // St computed / loaded (128)
+  uint64_t k_full[6], k_free[6];  // K slot landed / read
+  uint64_t s_full[4], s_free[4];  // St computed / loaded (128)
   uint64_t q_full;                // rows of a chunk staged (all key threads)
   uint64_t drain;
   uint32_t tmem_base;
@@ -173,7 +176,7 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
       init(cb->k_full[s], 1);
       init(cb->k_free[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < C::kBuffers; ++s) {
       init(cb->s_full[s], 1);
       init(cb->s_free[s], 128);
     }
@@ -321,9 +324,9 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
 #pragma unroll 1
       for (int t = 0; ok && t < count; ++t) {
         if (!wc.seen((tile0 + t) * kTileKeys)) continue;
-        const int s = i % C::kSlots, sb = i & 1;
+        const int s = i % C::kSlots, sb = i % C::kBuffers;
         ok = wait(cb->k_full[s], (i / C::kSlots) & 1);
-        if (ok && i >= 2) ok = wait(cb->s_free[sb], ((i >> 1) - 1) & 1);
+        if (ok && i >= C::kBuffers) ok = wait(cb->s_free[sb], (i / C::kBuffers - 1) & 1);
         if (!ok) break;
         ptx::tc_fence_after();
         const uint64_t kd =
@@ -343,8 +346,8 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
     const float neg_inf = -__int_as_float(0x7f800000);
     constexpr int kLanes = D / 8;  // lanes of a row of Q, 8 dims each
     const uint32_t s_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const int key = tid & 127, group = tid >> 7;
-    int i = 0;
+    const int key = tid & 127, group = tid >> 7;  // key of a tile; warpgroup
+    int i = 0, turn = 0;
     for (int b = 0;; ++b) {
       // (A warp whose wait has given up joins the others here, and all leave.  So
       // does every chunk's last tile before the next one's rows are staged.)
@@ -427,86 +430,121 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
       // The rows' own keys have no weight yet.
       const long long fresh = (long long)plan.len - plan.rows;
       const WeightChunk& wc = plan.chunk;
+      // Sums of the rows' weights for this thread's key in kCount tiles from t on,
+      // whose St are in the buffers from tile i on.
+      auto add_up = [&](auto tiles, int t, float* sum) {
+        constexpr int kCount = decltype(tiles)::value;
+        bool all = true;
+        int lo[kCount], hi[kCount];
+        uint64_t ks2[kCount], acc[kCount][2];
+        uint32_t col[kCount];
+#pragma unroll
+        for (int k = 0; k < kCount; ++k) {
+          const int sb = (i + k) % C::kBuffers, j0 = (tile0 + t + k) * kTileKeys, j = j0 + key;
+          if (ok) ok = wait(cb->s_full[sb], ((i + k) / C::kBuffers) & 1);
+          col[k] = s_lane + sb * N;
+          const float ks = plan.scale[2 * (t + k) + ((warp >> 1) & 1)];
+          ks2[k] = ptx::f2_pack(ks, ks);
+          acc[k][0] = acc[k][1] = 0ull;
+          // Rows that see the key: tokens [lo, hi].
+          lo[k] = 0;
+          hi[k] = 0x7fffffff;
+          if (!wc.whole(j0, sh)) {
+            all = false;
+            const long long r = (long long)j - wc.at0;
+            if (sh.causal) lo[k] = (int)(r > 0 ? (r < 0x7fffffff ? r : 0x7fffffff) : 0);
+            if (sh.window >= 0 && j >= sh.sinks) {
+              const long long w = r + sh.window;
+              hi[k] = (int)(w < 0x7fffffff ? (w > -1 ? w : -1) : 0x7fffffff);
+            }
+          }
+        }
+        if (!ok) return;
+        ptx::tc_fence_after();
+        // (Twice: whole tiles without a test for each row.)
+        auto rows_of = [&](auto masked) {
+#pragma unroll
+          for (int n0 = 0; n0 < N; n0 += 16) {
+            uint32_t now[kCount][16];
+#pragma unroll
+            for (int k = 0; k < kCount; ++k) ptx::tmem_ld16(col[k] + n0, now[k]);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < kCount; ++k) ptx::reg_fence16(now[k]);
+            if (n0 + 16 == N) {
+              ptx::tc_fence_before();
+#pragma unroll
+              for (int k = 0; k < kCount; ++k)
+                ptx::mbar_arrive(ptx::smem_u32(&cb->s_free[(i + k) % C::kBuffers]));
+            }
+#pragma unroll
+            for (int n = 0; n < 16; n += 2) {
+              const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(cb->row + (n0 + n) / 2);
+#pragma unroll
+              for (int k = 0; k < kCount; ++k) {
+                const uint64_t s2 = ptx::f2_pack(__uint_as_float(now[k][n]),
+                                                 __uint_as_float(now[k][n + 1]));
+                float u, v;
+                ptx::f2_unpack(ptx::fma2(s2, ptx::mul2(f.x, ks2[k]), f.y), u, v);
+                if constexpr (decltype(masked)::value != 0) {
+                  const int2 tok = *reinterpret_cast<const int2*>(cb->token + n0 + n);
+                  u = tok.x >= lo[k] && tok.x <= hi[k] ? u : neg_inf;
+                  v = tok.y >= lo[k] && tok.y <= hi[k] ? v : neg_inf;
+                }
+                acc[k][(n >> 1) & 1] =
+                    ptx::add2(acc[k][(n >> 1) & 1], ptx::f2_pack(ptx::ex2(u), ptx::ex2(v)));
+              }
+            }
+          }
+        };
+        if (all) rows_of(IntTag<0>{});
+        else rows_of(IntTag<1>{});
+#pragma unroll
+        for (int k = 0; k < kCount; ++k) {
+          float u, v;
+          ptx::f2_unpack(ptx::add2(acc[k][0], acc[k][1]), u, v);
+          // (No page: no weight.)
+          sum[k] = __isnanf(plan.scale[2 * (t + k) + ((warp >> 1) & 1)]) ? 0.f : u + v;
+        }
+      };
 #pragma unroll 1
-      for (int t = 0; t < count; ++t) {
-        const int j0 = (tile0 + t) * kTileKeys, j = j0 + key;
-        const bool here = j < keys_hi;
-        const float ks = plan.scale[2 * t + ((warp >> 1) & 1)];
-        const bool seen = wc.seen(j0);
-        // (Two groups: by turns.  What a chunk writes, the next may read in
-        // the other group, behind the barrier between them.)
-        if (C::kKeyThreads > 128 && (seen ? i & 1 : t & 1) != group) {
-          i += seen;
+      for (int t = 0; ok && t < count;) {
+        const bool seen = wc.seen((tile0 + t) * kTileKeys);
+        // Two neighbours that are seen go together.
+        const int n_tiles = C::kTiles == 2 && seen && t + 1 < count &&
+                                    wc.seen((tile0 + t + 1) * kTileKeys) ? 2 : 1;
+        // (Two groups: by turns.  What a chunk writes, the next may read in the
+        // other group, behind the barrier between them.)
+        if (C::kTiles == 2 && (turn++ & 1) != group) {
+          i += seen ? n_tiles : 0;
+          t += n_tiles;
           continue;
         }
         // What stands there already, and whether it changes.
-        const bool add = !first_chunk || (a.decay != 0.f && j < fresh);
-        if (!seen && (!first_chunk || (add && a.decay == 1.f))) continue;
-        float old = 0.f;
-        if (here && add) old = out[j];
-        if (first_chunk) old *= a.decay;
-        float sum = 0.f;
-        if (seen) {
-          const int sb = i & 1;
-          ok = wait(cb->s_full[sb], (i >> 1) & 1);
-          if (!ok) break;
-          ptx::tc_fence_after();
-          const bool all = wc.whole(j0, sh);
-          // Rows that see the key: tokens [lo, hi].
-          int lo = 0, hi = 0x7fffffff;
-          if (!all) {
-            const long long r = (long long)j - wc.at0;
-            if (sh.causal) lo = (int)(r > 0 ? (r < 0x7fffffff ? r : 0x7fffffff) : 0);
-            if (sh.window >= 0 && j >= sh.sinks) {
-              const long long w = r + sh.window;
-              hi = (int)(w < 0x7fffffff ? (w > -1 ? w : -1) : 0x7fffffff);
-            }
-          }
-          const uint64_t ks2 = ptx::f2_pack(ks, ks);
-          uint64_t acc[2] = {0ull, 0ull};
-          // (Twice: the whole tile without a test for each row.)
-          auto add_up = [&](auto masked) {
-            // The next 16 columns load while these are summed.
-            uint32_t s[2][16];
-            ptx::tmem_ld16(s_lane + sb * N, s[0]);
+        float old[C::kTiles], sum[C::kTiles];
+        bool change = seen;
 #pragma unroll
-            for (int n0 = 0; n0 < N; n0 += 16) {
-              uint32_t* now = s[(n0 >> 4) & 1];
-              ptx::tmem_wait_ld();
-              ptx::reg_fence16(now);
-              if (n0 + 16 < N) {
-                ptx::tmem_ld16(s_lane + sb * N + n0 + 16, s[((n0 >> 4) & 1) ^ 1]);
-              } else {
-                ptx::tc_fence_before();
-                ptx::mbar_arrive(ptx::smem_u32(&cb->s_free[sb]));
-              }
-#pragma unroll
-              for (int n = 0; n < 16; n += 2) {
-                const ulonglong2 f =
-                    *reinterpret_cast<const ulonglong2*>(cb->row + (n0 + n) / 2);
-                const uint64_t s2 =
-                    ptx::f2_pack(__uint_as_float(now[n]), __uint_as_float(now[n + 1]));
-                float u, v;
-                ptx::f2_unpack(ptx::fma2(s2, ptx::mul2(f.x, ks2), f.y), u, v);
-                if constexpr (decltype(masked)::value != 0) {
-                  const int2 tok = *reinterpret_cast<const int2*>(cb->token + n0 + n);
-                  u = tok.x >= lo && tok.x <= hi ? u : neg_inf;
-                  v = tok.y >= lo && tok.y <= hi ? v : neg_inf;
-                }
-                acc[(n >> 1) & 1] =
-                    ptx::add2(acc[(n >> 1) & 1], ptx::f2_pack(ptx::ex2(u), ptx::ex2(v)));
-              }
-            }
-          };
-          if (all) add_up(IntTag<0>{});
-          else add_up(IntTag<1>{});
-          float u, v;
-          ptx::f2_unpack(ptx::add2(acc[0], acc[1]), u, v);
-          sum = u + v;
-          if (__isnanf(ks)) sum = 0.f;  // (no page)
-          ++i;
+        for (int k = 0; k < C::kTiles; ++k) {
+          const int j = (tile0 + t + k) * kTileKeys + key;
+          const bool add = !first_chunk || (a.decay != 0.f && j < fresh);
+          old[k] = 0.f;
+          sum[k] = 0.f;
+          if (k < n_tiles && j < keys_hi && add) old[k] = out[j];
+          if (first_chunk) old[k] *= a.decay;
+          if (k == 0) change = change || (first_chunk && !(add && a.decay == 1.f));
         }
-        if (here) out[j] = old + sum;
+        if (seen) {
+          if (n_tiles == C::kTiles) add_up(IntTag<C::kTiles>{}, t, sum);
+          else add_up(IntTag<1>{}, t, sum);
+          if (!ok) break;
+          i += n_tiles;
+        }
+#pragma unroll
+        for (int k = 0; k < C::kTiles; ++k) {
+          const int j = (tile0 + t + k) * kTileKeys + key;
+          if (change && k < n_tiles && j < keys_hi) out[j] = old[k] + sum[k];
+        }
+        t += n_tiles;
       }
       plan_done(b);
     }
