@@ -642,7 +642,7 @@ def fa_paged_attn(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, seq_lens,
     T, H, dq = q.shape
     if dq != d:
         raise ValueError(f"q has head dim {dq}, the cache {d}")
-    sink_tokens, words = int(sink_tokens), _tree_words(tree_mask, T)
+    words = 0 if tree_mask is None else _tree_words(tree_mask, T)
     # (Now: the workspace's size is looked up by the values of these sizes.)
     max_seqlen_q, max_seqlen_k = int(max_seqlen_q), int(max_seqlen_k)
     if softmax_scale is None:
@@ -650,8 +650,9 @@ def fa_paged_attn(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, seq_lens,
     index, here = _device(stream, q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, seq_lens,
                           page_table, out, lse, workspace, tree_mask)
     with here:
+        # (new_empty: of the type and device of a tensor at hand, and quicker.)
         if out is None:
-            out = torch.empty((T, H, d), dtype=torch.bfloat16, device=q.device)
+            out = q.new_empty((T, H, d))
         else:
             _check(out, "out", torch.bfloat16, 3)
             _shape(out, "out", (T, H, d))
@@ -659,21 +660,30 @@ def fa_paged_attn(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, seq_lens,
             _check(lse, "lse", torch.float32, 2)
             _shape(lse, "lse", (H, T))
         elif return_lse:
-            lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+            lse = k_scale.new_empty((H, T))
+        masked = words > 0 or sink_tokens != 0
         if workspace is None:
-            need = _attn_workspace(index, batch, T, H, hk, d, max_seqlen_q,
-                                   words > 0 or sink_tokens > 0)
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            need = _attn_workspace(index, batch, T, H, hk, d, max_seqlen_q, masked)
+            workspace = k_scale.new_empty(((need + 3) // 4,))
         else:
             _check(workspace, "workspace", torch.uint8, 1)
             need = workspace.shape[0]
         qr, qh, _ = q.stride()
-        st = lib.fa_paged_attn_masked(
-            q.data_ptr(), qr, qh, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-            v_scale.data_ptr(), cu_seqlens_q.data_ptr(), seq_lens.data_ptr(),
-            page_table.data_ptr(), batch, T, H, hk, d, pages, width, max_seqlen_q, max_seqlen_k,
-            softmax_scale, bool(causal), _window(window_left), _sinks(sink_tokens), _p(tree_mask),
-            words, out.data_ptr(), _p(lse), workspace.data_ptr(), need, _raw_stream(index))
+        if masked:
+            st = lib.fa_paged_attn_masked(
+                q.data_ptr(), qr, qh, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                v_scale.data_ptr(), cu_seqlens_q.data_ptr(), seq_lens.data_ptr(),
+                page_table.data_ptr(), batch, T, H, hk, d, pages, width, max_seqlen_q,
+                max_seqlen_k, softmax_scale, bool(causal), _window(window_left),
+                _sinks(sink_tokens), _p(tree_mask), words, out.data_ptr(), _p(lse),
+                workspace.data_ptr(), need, _raw_stream(index))
+        else:
+            st = lib.fa_paged_attn(
+                q.data_ptr(), qr, qh, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                v_scale.data_ptr(), cu_seqlens_q.data_ptr(), seq_lens.data_ptr(),
+                page_table.data_ptr(), batch, T, H, hk, d, pages, width, max_seqlen_q,
+                max_seqlen_k, softmax_scale, bool(causal), _window(window_left), out.data_ptr(),
+                _p(lse), workspace.data_ptr(), need, _raw_stream(index))
     if st != FA_OK:
         raise FaError(st, "fa_paged_attn")
     return (out, lse) if lse is not None else out
@@ -722,11 +732,12 @@ def fa_draft_tree(parents, cu_seqlens, seq_lens, max_nodes=64, tree_mask=None, p
         if tree_mask is None:
             if max_nodes < 1:
                 raise ValueError(f"max_nodes must be at least 1, got {max_nodes}")
-            tree_mask = torch.empty((total, -(-int(max_nodes) // 32)), dtype=i32,
-                                    device=parents.device)
-        words = _tree_words(tree_mask, total)
+            words = -(-int(max_nodes) // 32)
+            tree_mask = parents.new_empty((total, words))
+        else:
+            words = _tree_words(tree_mask, total)
         if positions is None:
-            positions = torch.empty((total,), dtype=i32, device=parents.device)
+            positions = parents.new_empty((total,))
         else:
             _check(positions, "positions", i32, 1)
             _shape(positions, "positions", (total,))
@@ -847,12 +858,12 @@ def fa_paged_kv_select(weights, seq_lens, budget, sink_tokens=0, recent_tokens=0
     index, here = _device(stream, weights, seq_lens, keep, new_lens)
     with here:
         if keep is None:
-            keep = torch.empty((batch, hk, max(budget, 0)), dtype=i32, device=weights.device)
+            keep = seq_lens.new_empty((batch, hk, max(budget, 0)))
         else:
             _check(keep, "keep", i32, 3)
             _shape(keep, "keep", (batch, hk, budget))
         if new_lens is None:
-            new_lens = torch.empty((batch,), dtype=i32, device=weights.device)
+            new_lens = seq_lens.new_empty((batch,))
         else:
             _check(new_lens, "new_lens", i32, 1)
             _shape(new_lens, "new_lens", (batch,))
