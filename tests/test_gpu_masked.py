@@ -292,6 +292,26 @@ def test_tree_rows_behind_the_last_sequence_and_malformed_cu_seqlens(cuda_device
     assert (out[3:] == 7).all() and not (out[1:3] == 7).any()
 
 
+@pytest.mark.parametrize("d", [64, 80, 128])
+def test_masked_runs_are_bitwise_the_same(cuda_device, d):
+    # Many short units, so that a CTA goes from one to the next under way, its
+    # warps apart; whole ones and parts.
+    gen = torch.Generator().manual_seed(37)
+    q_lens = [1 + i % 9 for i in range(200)]
+    lens = [n + 41 * i % 500 for i, n in enumerate(q_lens)]
+    pages, num = plain.make_pages(lens, gen)
+    (kc, ks), (vc, vs) = (plain.make_cache(lens, pages, num, 2, d, gen) for _ in range(2))
+    q = torch.randn((sum(q_lens), 8, d), generator=gen).bfloat16()
+    mask = masked.tree_masks(trees_of(q_lens, 9), 1)
+    args = dev(q, kc, vc, ks, vs, plain.cum(q_lens), i32(lens), pages)
+    for kw in (dict(tree_mask=dev(mask)), dict(window_left=100, sink_tokens=3)):
+        want = fa.fa_paged_attn(*args, max_seqlen_q=9, return_lse=True, **kw)
+        for _ in range(15):
+            got = fa.fa_paged_attn(*args, max_seqlen_q=9, return_lse=True, **kw)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert fa.fa_get_device_status() == fa.FA_OK
+
+
 def test_masked_wait_limit_runs_out_then_recovers(cuda_device):
     gen = torch.Generator().manual_seed(32)
     lens = [3000] * 4

@@ -723,41 +723,46 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       }
       // Through the rows' place in shared memory (Q's terms, read by the last S),
       // 2 D bytes of each: D values as bf16, or half of them as fp32 by turns.  A
-      // warp's rows are its own.
-      constexpr int kUnits = D / 8;  // of 16 bytes
-      uint8_t* mine_s = q_tile + r * (2 * D);
+      // warp's rows are its own, as they are when it stages the next rows of Q, which
+      // it may do while the others still have outputs there: so a row's bytes lie
+      // where its two terms do.
+      constexpr int kUnits = D / 8;  // of 16 bytes, a half in each term's place
+      auto unit_at = [&](int row, int u) {
+        const int v = u % (kUnits / 2);
+        return q_tile + (u >= kUnits / 2 ? C::kTermBytes : 0) + row * D +
+               (D == 128 ? (v ^ (row & 7)) : (v ^ ((row >> 1) & 3))) * 16;
+      };
       const uint64_t dst =
           !valid ? 0
           : whole ? reinterpret_cast<uint64_t>(a.out + ((size_t)row_q * a.heads + row_h) * a.dim)
                   : reinterpret_cast<uint64_t>(a.part_o +
                                                ((size_t)slot * kWideRows + t * 128 + r) * D);
       const int units = whole ? a.dim / 8 : kUnits;
-      // (Weight 0: O_t may hold anything.)
-      auto value = [&](uint32_t o) { return inv == 0.f ? 0.f : __uint_as_float(o) * inv; };
+      // (Weight 0: O_t may hold anything.  In short loops, as the rows of Q.)
 #pragma unroll 1
       for (int turn = 0; turn < (whole ? 1 : 2); ++turn) {
+        const int c_end = whole ? D : (turn + 1) * (D / 2);
 #pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 32) {
-          if (!whole && (c0 >= D / 2) != (turn != 0)) continue;
-          uint32_t o[32];
+        for (int c0 = turn * (D / 2); c0 < c_end; c0 += 16) {
+          uint32_t o[16];
           ptx::tmem_ld16(o_addr + c0, o);
-          ptx::tmem_ld16(o_addr + c0 + 16, o + 16);
           ptx::tmem_wait_ld();
           ptx::reg_fence16(o);
-          ptx::reg_fence16(o + 16);
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            o[c] = inv == 0.f ? 0u : __float_as_uint(__uint_as_float(o[c]) * inv);
+          // (unit: of the row's first 16 bytes of these)
+          const int unit = whole ? c0 / 8 : (c0 - turn * (D / 2)) / 4;
           if (whole) {
 #pragma unroll
-            for (int c = 0; c < 32; c += 8)
-              *reinterpret_cast<uint4*>(mine_s + ((((c0 + c) / 8) ^ (r & 7)) * 16)) = make_uint4(
-                  ptx::pack_bf16x2(value(o[c]), value(o[c + 1])),
-                  ptx::pack_bf16x2(value(o[c + 2]), value(o[c + 3])),
-                  ptx::pack_bf16x2(value(o[c + 4]), value(o[c + 5])),
-                  ptx::pack_bf16x2(value(o[c + 6]), value(o[c + 7])));
-          } else {
+            for (int c = 0; c < 8; ++c)
+              o[c] = ptx::pack_bf16x2(__uint_as_float(o[2 * c]), __uint_as_float(o[2 * c + 1]));
+          }
 #pragma unroll
-            for (int c = 0; c < 32; c += 4)
-              *reinterpret_cast<float4*>(mine_s + ((((c0 - turn * (D / 2) + c) / 4) ^ (r & 7)) * 16)) =
-                  make_float4(value(o[c]), value(o[c + 1]), value(o[c + 2]), value(o[c + 3]));
+          for (int c = 0; c < 16; c += 4) {
+            if (whole && c >= 8) break;
+            *reinterpret_cast<uint4*>(unit_at(r, unit + c / 4)) =
+                make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
           }
         }
         if (turn == (whole ? 0 : 1)) {
@@ -773,7 +778,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           const int row_n = (warp & 3) * 32 + n;
           if (to != 0 && u < units)
             *reinterpret_cast<uint4*>(to + turn * D * 2 + u * 16) =
-                *reinterpret_cast<const uint4*>(q_tile + row_n * (2 * D) + ((u ^ (row_n & 7)) * 16));
+                *reinterpret_cast<const uint4*>(unit_at(row_n, u));
         }
         __syncwarp();
       }
