@@ -67,10 +67,14 @@ struct WeightsCfg {
   static constexpr int kTileBytes = kTileKeys * D;
   static constexpr int kPageBytes = kPageTokens * D;
   static constexpr int kTiles = N >= 64 ? 2 : 1;  // of a key thread at once
-  static constexpr int kBuffers = 2 * kTiles;     // of St, N columns each
+  static constexpr int kBuffers = 2 * kTiles;     // of St
+  // Columns of a buffer: the products with Q's two terms side by side, so that the
+  // tensor core reads K once, or, where there are many rows, both in one sum.
+  static constexpr bool kApart = N <= 32;
+  static constexpr int kCols = kApart ? 2 * N : N;
   static constexpr int kSlots = N <= 32 ? 3 : N == 64 ? 5 : 6;
   static constexpr int kQBytes = 2 * N * D;
-  static constexpr uint32_t kTmemCols = kBuffers * N;
+  static constexpr uint32_t kTmemCols = kBuffers * kCols;
   static constexpr int kQ = kSlots * kTileBytes;
   static constexpr int kCtl = kQ + kQBytes;
   static constexpr int kKeyThreads = 128 * kTiles;
@@ -309,7 +313,7 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
       wait_drain_warp(ptx::smem_u32(&cb->k_full[s]), ((loads - 1 - s) / C::kSlots) & 1, a.status);
   } else if (warp == kIssuer) {
     // ---------------------------------------------------------- MMA issuer
-    constexpr uint32_t idesc = ptx::idesc_e4m3_f32(128, N);
+    constexpr uint32_t idesc = ptx::idesc_e4m3_f32(128, C::kCols);
     const uint64_t q_hi = ptx::smem_desc(ptx::smem_u32(smem + C::kQ), 16, 8 * D, C::kSwK);
     const uint64_t q_lo = ptx::smem_desc(ptx::smem_u32(smem + C::kQ + N * D), 16, 8 * D, C::kSwK);
     int i = 0, staged = 0;
@@ -331,9 +335,13 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
         ptx::tc_fence_after();
         const uint64_t kd =
             ptx::smem_desc(ptx::smem_u32(smem + s * C::kTileBytes), 16, 8 * D, C::kSwK);
-        // (The small terms first: each step rounds at the sum's size so far.)
-        ptx::mma_f8_elect<D / 32>(tmem + sb * N, kd, q_lo, idesc);
-        ptx::mma_f8_elect<D / 32, true>(tmem + sb * N, kd, q_hi, idesc);
+        if constexpr (C::kApart) {
+          ptx::mma_f8_elect<D / 32>(tmem + sb * C::kCols, kd, q_hi, idesc);
+        } else {
+          // (The small terms first: each step rounds at the sum's size so far.)
+          ptx::mma_f8_elect<D / 32>(tmem + sb * C::kCols, kd, q_lo, idesc);
+          ptx::mma_f8_elect<D / 32, true>(tmem + sb * C::kCols, kd, q_hi, idesc);
+        }
         ptx::mma_commit_elect(ptx::smem_u32(&cb->s_full[sb]));
         ptx::mma_commit_elect(ptx::smem_u32(&cb->k_free[s]));
         ++i;
@@ -442,7 +450,7 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
         for (int k = 0; k < kCount; ++k) {
           const int sb = (i + k) % C::kBuffers, j0 = (tile0 + t + k) * kTileKeys, j = j0 + key;
           if (ok) ok = wait(cb->s_full[sb], ((i + k) / C::kBuffers) & 1);
-          col[k] = s_lane + sb * N;
+          col[k] = s_lane + sb * C::kCols;
           const float ks = plan.scale[2 * (t + k) + ((warp >> 1) & 1)];
           ks2[k] = ptx::f2_pack(ks, ks);
           acc[k][0] = acc[k][1] = 0ull;
@@ -463,14 +471,20 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
         ptx::tc_fence_after();
         // (Twice: whole tiles without a test for each row.)
         auto rows_of = [&](auto masked) {
-#pragma unroll
+#pragma unroll 1
           for (int n0 = 0; n0 < N; n0 += 16) {
-            uint32_t now[kCount][16];
+            uint32_t now[kCount][16], low[C::kApart ? kCount : 1][16];
 #pragma unroll
-            for (int k = 0; k < kCount; ++k) ptx::tmem_ld16(col[k] + n0, now[k]);
+            for (int k = 0; k < kCount; ++k) {
+              ptx::tmem_ld16(col[k] + n0, now[k]);
+              if constexpr (C::kApart) ptx::tmem_ld16(col[k] + N + n0, low[k]);
+            }
             ptx::tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < kCount; ++k) ptx::reg_fence16(now[k]);
+            for (int k = 0; k < kCount; ++k) {
+              ptx::reg_fence16(now[k]);
+              if constexpr (C::kApart) ptx::reg_fence16(low[k]);
+            }
             if (n0 + 16 == N) {
               ptx::tc_fence_before();
 #pragma unroll
@@ -482,8 +496,11 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
               const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(cb->row + (n0 + n) / 2);
 #pragma unroll
               for (int k = 0; k < kCount; ++k) {
-                const uint64_t s2 = ptx::f2_pack(__uint_as_float(now[k][n]),
-                                                 __uint_as_float(now[k][n + 1]));
+                uint64_t s2 =
+                    ptx::f2_pack(__uint_as_float(now[k][n]), __uint_as_float(now[k][n + 1]));
+                if constexpr (C::kApart)
+                  s2 = ptx::add2(s2, ptx::f2_pack(__uint_as_float(low[k][n]),
+                                                  __uint_as_float(low[k][n + 1])));
                 float u, v;
                 ptx::f2_unpack(ptx::fma2(s2, ptx::mul2(f.x, ks2[k]), f.y), u, v);
                 if constexpr (decltype(masked)::value != 0) {
@@ -507,6 +524,14 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
           sum[k] = __isnanf(plan.scale[2 * (t + k) + ((warp >> 1) & 1)]) ? 0.f : u + v;
         }
       };
+      // What stands at this thread's key of tile t already, where it counts.
+      auto held = [&](int t) {
+        const int j = (tile0 + t) * kTileKeys + key;
+        const bool add = !first_chunk || (a.decay != 0.f && j < fresh);
+        return t < count && j < keys_hi && add ? out[j] : 0.f;
+      };
+      // (One tile at a time: the next one's is under way while this is summed.)
+      float ahead = C::kTiles == 1 ? held(0) : 0.f;
 #pragma unroll 1
       for (int t = 0; ok && t < count;) {
         const bool seen = wc.seen((tile0 + t) * kTileKeys);
@@ -522,17 +547,17 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
         }
         // What stands there already, and whether it changes.
         float old[C::kTiles], sum[C::kTiles];
-        bool change = seen;
-#pragma unroll
-        for (int k = 0; k < C::kTiles; ++k) {
-          const int j = (tile0 + t + k) * kTileKeys + key;
-          const bool add = !first_chunk || (a.decay != 0.f && j < fresh);
-          old[k] = 0.f;
-          sum[k] = 0.f;
-          if (k < n_tiles && j < keys_hi && add) old[k] = out[j];
-          if (first_chunk) old[k] *= a.decay;
-          if (k == 0) change = change || (first_chunk && !(add && a.decay == 1.f));
+        if constexpr (C::kTiles == 1) {
+          old[0] = ahead;
+          ahead = held(t + 1);
+        } else {
+          old[0] = held(t);
+          old[1] = n_tiles == 2 ? held(t + 1) : 0.f;
         }
+#pragma unroll
+        for (int k = 0; k < C::kTiles; ++k) sum[k] = 0.f;
+        const bool change = seen || (first_chunk && !(a.decay == 1.f &&
+                                                      (tile0 + t) * kTileKeys + key < fresh));
         if (seen) {
           if (n_tiles == C::kTiles) add_up(IntTag<C::kTiles>{}, t, sum);
           else add_up(IntTag<1>{}, t, sum);
@@ -542,7 +567,8 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
 #pragma unroll
         for (int k = 0; k < C::kTiles; ++k) {
           const int j = (tile0 + t + k) * kTileKeys + key;
-          if (change && k < n_tiles && j < keys_hi) out[j] = old[k] + sum[k];
+          if (change && k < n_tiles && j < keys_hi)
+            out[j] = (first_chunk ? old[k] * a.decay : old[k]) + sum[k];
         }
         t += n_tiles;
       }
