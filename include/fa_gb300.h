@@ -646,8 +646,8 @@ fa_status fa_paged_attn_plan(int batch, int total_q, int num_heads, int num_head
  *                 capacity; sequences without rows, and what lies behind a
  *                 length, stay as they were.
  *
- * Precision: the scores and weights in fp32 (a row of q as in fa_paged_attn),
- * added in a fixed order.
+ * Precision: scores, weights and sums in fp32, a row of q held to 2^-24 of its
+ * largest value, the sums in a fixed order.
  *
  * Host errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED (head_dim, sizes past
  * 32-bit indices), FA_ERR_ARCH, FA_ERR_LAUNCH.
@@ -668,7 +668,8 @@ fa_status fa_paged_key_weights(const void* q, long long q_row_stride, long long 
  *   weights       fp32 [batch, num_heads_k, capacity], as fa_paged_key_weights
  *                 keeps them; any numbers.  Of equal ones (-0 and 0 too) the
  *                 lower position is kept; a NaN counts below all numbers.
- *   seq_lens      int32 [batch], clamped to [0, capacity].
+ *   seq_lens      int32 [batch], clamped to [0, capacity] (capacity holds every
+ *                 sequence: keys past it are not kept).
  *   budget        at least 1 and at least sink_tokens + recent_tokens.
  *   keep          int32 [batch, num_heads_k, budget], written: the kept
  *                 positions in ascending order, -1 behind the last.  A sequence

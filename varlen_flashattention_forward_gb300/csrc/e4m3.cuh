@@ -70,6 +70,21 @@ __device__ __forceinline__ void split_terms(const float* x, int e, uint32_t* hi,
     lo[k] = c;
   }
 }
+// What is left of the row, at most half of e4m3's last step (2^-10): in e5m2, whose
+// last step is 2^-16.
+__device__ __forceinline__ void third_term(const float* x, int e, const uint32_t* hi,
+                                           const uint32_t* lo, uint32_t* rest) {
+  const float f = __uint_as_float((uint32_t)(7 - e + 127) << 23);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t y = ptx::pack_f16x2(x[2 * k] * f, x[2 * k + 1] * f);
+    uint16_t c;
+    asm("sub.f16x2 %0, %0, %1;" : "+r"(y) : "r"(unpack_e4m3x2(hi[k])));
+    asm("sub.f16x2 %0, %0, %1;" : "+r"(y) : "r"(unpack_e4m3x2(lo[k])));
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(c) : "r"(y));
+    rest[k] = c;
+  }
+}
 // What the terms' products are to be multiplied by, for scores times `scale`:
 // NaN for a row with an infinity or a NaN (mx infinite).
 __device__ __forceinline__ float terms_scale(float mx, int e, float scale) {

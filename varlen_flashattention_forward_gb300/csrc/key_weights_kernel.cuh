@@ -9,9 +9,10 @@
 // come: no maximum, no V and no second pass.
 //
 // The transposed form of paged_attn_kernel: St[key, row] = K[key, d] Q[row, d]t
-// as e4m3 products of K as it lies in the cache and Q as two e4m3 terms, here
-// one after the other into the same fp32 accumulator.  A thread has a key: its
-// weights' sum over the rows stays in the thread, in a fixed order, and no two
+// as products of K as it lies in the cache and Q as two e4m3 terms and a third in
+// e5m2 (the weights are kept in fp32, where the two alone are 2^-17 of a row's
+// largest value off: a sum's error of 4e-6 instead of 1e-6).  A thread has a key:
+// its weights' sum over the rows stays in the thread, in a fixed order, and no two
 // threads write the same place.
 //
 // Work: every (sequence, kv head) has its 128-key tiles; their costs are cut
@@ -68,19 +69,19 @@ struct WeightsCfg {
   static constexpr int kPageBytes = kPageTokens * D;
   static constexpr int kTiles = N >= 64 ? 2 : 1;  // of a key thread at once
   static constexpr int kBuffers = 2 * kTiles;     // of St
-  // Columns of a buffer: the products with Q's two terms side by side, so that the
-  // tensor core reads K once, or, where there are many rows, both in one sum.
+  // Columns of a buffer: the products with Q's e4m3 terms side by side, so that the
+  // tensor core reads K once for both, or, where there are many rows, in one sum.
   static constexpr bool kApart = N <= 32;
   static constexpr int kCols = kApart ? 2 * N : N;
-  static constexpr int kSlots = N <= 32 ? 3 : N == 64 ? 5 : 6;
-  static constexpr int kQBytes = 2 * N * D;
+  static constexpr int kSlots = N == 16 ? 4 : N == 32 ? 3 : N == 64 ? 5 : 6;
+  static constexpr int kQBytes = 3 * N * D;  // terms of the rows, one behind the other
   static constexpr uint32_t kTmemCols = kBuffers * kCols;
   static constexpr int kQ = kSlots * kTileBytes;
   static constexpr int kCtl = kQ + kQBytes;
   static constexpr int kKeyThreads = 128 * kTiles;
   static constexpr int kThreads = kKeyThreads + 64;
   // Resident CTAs (by shared memory, 57 to 133 KB at 128 dims, and columns).
-  static constexpr int kResident = N == 16 ? 4 : N == 32 ? 3 : N == 64 ? 2 : 1;
+  static constexpr int kResident = N <= 32 ? 3 : N == 64 ? 2 : 1;
 };
 
 // A chunk of a sequence's rows against its keys.
@@ -316,6 +317,9 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
     constexpr uint32_t idesc = ptx::idesc_e4m3_f32(128, C::kCols);
     const uint64_t q_hi = ptx::smem_desc(ptx::smem_u32(smem + C::kQ), 16, 8 * D, C::kSwK);
     const uint64_t q_lo = ptx::smem_desc(ptx::smem_u32(smem + C::kQ + N * D), 16, 8 * D, C::kSwK);
+    const uint64_t q_rest =
+        ptx::smem_desc(ptx::smem_u32(smem + C::kQ + 2 * N * D), 16, 8 * D, C::kSwK);
+    constexpr uint32_t idesc_rest = ptx::idesc_e4m3_e5m2_f32(128, N);
     int i = 0, staged = 0;
     for (int b = 0; ok; ++b) {
       const WeightPlan& plan = plan_of(b, &ok);
@@ -335,12 +339,15 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
         ptx::tc_fence_after();
         const uint64_t kd =
             ptx::smem_desc(ptx::smem_u32(smem + s * C::kTileBytes), 16, 8 * D, C::kSwK);
+        // (The small terms first: each step rounds at the sum's size so far.)
+        const uint32_t d = tmem + sb * C::kCols;
         if constexpr (C::kApart) {
-          ptx::mma_f8_elect<D / 32>(tmem + sb * C::kCols, kd, q_hi, idesc);
+          ptx::mma_f8_elect<D / 32>(d, kd, q_hi, idesc);  // and q_lo, N columns on
+          ptx::mma_f8_elect<D / 32, true>(d + N, kd, q_rest, idesc_rest);
         } else {
-          // (The small terms first: each step rounds at the sum's size so far.)
-          ptx::mma_f8_elect<D / 32>(tmem + sb * C::kCols, kd, q_lo, idesc);
-          ptx::mma_f8_elect<D / 32, true>(tmem + sb * C::kCols, kd, q_hi, idesc);
+          ptx::mma_f8_elect<D / 32>(d, kd, q_rest, idesc_rest);
+          ptx::mma_f8_elect<D / 32, true>(d, kd, q_lo, idesc);
+          ptx::mma_f8_elect<D / 32, true>(d, kd, q_hi, idesc);
         }
         ptx::mma_commit_elect(ptx::smem_u32(&cb->s_full[sb]));
         ptx::mma_commit_elect(ptx::smem_u32(&cb->k_free[s]));
@@ -409,14 +416,17 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
             for (int o = kLanes / 2; o > 0; o >>= 1)
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             const int e = terms_exponent(mx);
-            uint32_t hi[4], lo[4];
+            uint32_t hi[4], lo[4], rest[4];
             split_terms(x, e, hi, lo);
+            third_term(x, e, hi, lo, rest);
             const int unit = dim0 >> 4;
             const int us = D == 128 ? (unit ^ (n & 7)) : (unit ^ ((n >> 1) & 3));
             uint8_t* at = q_s + n * D + us * 16 + (dim0 & 8);
             *reinterpret_cast<uint2*>(at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
             *reinterpret_cast<uint2*>(at + N * D) =
                 make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+            *reinterpret_cast<uint2*>(at + 2 * N * D) =
+                make_uint2(rest[0] | rest[1] << 16, rest[2] | rest[3] << 16);
             if (sub == 0) {
               // A row that sees nothing (LSE -inf), or that is none, adds 0.
               const bool none = n >= n_rows || lse == neg_inf;

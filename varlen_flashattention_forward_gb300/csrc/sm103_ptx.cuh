@@ -633,6 +633,10 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N, boo
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N) {
   return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
+// The same with B as e5m2 (format 1).
+__host__ __device__ constexpr uint32_t idesc_e4m3_e5m2_f32(uint32_t M, uint32_t N) {
+  return idesc_e4m3_f32(M, N) | (1u << 10);
+}
 
 }  // namespace ptx
 }  // namespace fa
