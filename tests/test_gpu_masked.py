@@ -425,7 +425,8 @@ DIMS = [(64, 64), (72, 72), (80, 80), (96, 96), (128, 128), (192, 128)]
 
 
 @pytest.mark.parametrize("d,dv", DIMS)
-@pytest.mark.parametrize("wl,sinks", [(100, 4), (0, 1), (300, 130), (128, 257), (1, 10000)])
+@pytest.mark.parametrize("wl,sinks", [(100, 4), (0, 1), (300, 130), (128, 257), (1, 10000), (90, 64),
+                                      (90, 65), (200, 192), (200, 193)])
 def test_packed_sinks(cuda_device, d, dv, wl, sinks):
     check_packed([700, 1, 129, 0, 260], [700, 600, 129, 5, 900], 4, 4, d, dv, wl=wl, sinks=sinks,
                  seed=d + wl)

@@ -5,9 +5,8 @@
 // A thread takes a node and walks up to the root.  Parents are smaller
 // numbers, so the walk passes the words of its mask from the last to the
 // first and writes each once; it takes at most as many steps as there are
-// nodes.  Latency alone bounds it: a launch and the chain of loads, which
-// after the first come from L1 (24 trees of 33 to 64 nodes, about 8 deep: see
-// fa_draft_tree in the design notes' table).
+// nodes.  Latency alone bounds it, a launch and the chain of loads, which after
+// the first come from L1: one tree of 16 nodes 3.2 us, 24 of 33 to 64 nodes 3.8.
 #pragma once
 
 #include <cuda_runtime.h>
