@@ -385,6 +385,22 @@ def test_compact_special_codes_and_scales(cuda_device):
     check_compact(caches, pages, keep[..., :70].contiguous(), [70])
 
 
+def test_compact_rows_of_zeros_under_scales_far_apart(cuda_device):
+    # Zeros stay zeros whatever the quotient of the scales, past 32 bits too.
+    gen = torch.Generator().manual_seed(12)
+    pages, num, caches = make_both([256], 2, 64, gen)
+    for c, s in caches:
+        raw = c.view(torch.uint8)
+        raw[pages[0].long()] = 0
+        raw[pages[0, 2].long(), :, 5, 3] = 0x7f
+        s[pages[0].long()] = 2.0 ** 64
+        s[pages[0, 3].long()] = 2.0 ** -64
+        raw[pages[0, 3].long(), 1, 9] = 0x31
+    keep = torch.tensor([64, 67, 130, 133, 192, 200, 201, 255], dtype=torch.int32)[None, None]
+    cards = check_compact(caches, pages, keep, [8])
+    assert (cards[0][1].cpu()[pages[0, 0].long()] == 2.0 ** -64).all()
+
+
 def test_compact_nothing_and_on_another_stream(cuda_device):
     gen = torch.Generator().manual_seed(9)
     pages, num, caches = make_both([100, 90], 2, 96, gen)

@@ -416,7 +416,8 @@ __global__ void __launch_bounds__(kCompactThreads, 4) kv_compact_kernel(const Kv
       for (int k = 0; k < 8; ++k) {
         const int i = row0 + k * step;
         if (k >= lanes || i >= sp.count || byte >= a.dim) continue;
-        const float f = row[i].scale * inv;
+        // (A code that is not 0 has f <= 2^18; a row of zeros may have any.)
+        const float f = fminf(row[i].scale * inv, 1e38f);
         uint32_t w[4] = {code[k].x, code[k].y, code[k].z, code[k].w};
         if (f != 1.f) scale_codes(w, f);
         *reinterpret_cast<uint4*>(codes + (size_t)(sp.slot + i) * a.dim + byte) =
