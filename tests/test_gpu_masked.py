@@ -334,6 +334,82 @@ def test_masked_wait_limit_runs_out_then_recovers(cuda_device):
     assert fa.fa_get_device_status() == fa.FA_OK and torch.equal(got, want)
 
 
+def test_wide_wait_limit_runs_out_then_recovers(cuda_device):
+    # (As above, of a tree with more rows than the 16 of a narrow tile.)
+    gen = torch.Generator().manual_seed(38)
+    q_lens, lens = [40, 9, 30], [3000, 2000, 2500]
+    pages, num = plain.make_pages(lens, gen)
+    (kc, ks), (vc, vs) = (plain.make_cache(lens, pages, num, 2, 128, gen) for _ in range(2))
+    q = torch.randn((79, 8, 128), generator=gen).bfloat16()
+    args = dev(q, kc, vc, ks, vs, plain.cum(q_lens), i32(lens), pages)
+    kw = dict(max_seqlen_q=40, tree_mask=dev(masked.tree_masks(trees_of(q_lens, 6), 2)))
+    want = fa.fa_paged_attn(*args, **kw)
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status() == fa.FA_OK
+    fa.fa_set_wait_limit_ns(2000)
+    try:
+        fa.fa_paged_attn(*args, **kw)
+        assert fa.fa_get_device_status() == fa.FA_ERR_DEVICE_TIMEOUT
+    finally:
+        fa.fa_set_wait_limit_ns(0)
+    got = fa.fa_paged_attn(*args, **kw)
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status() == fa.FA_OK and torch.equal(got, want)
+
+
+def test_masked_calls_with_a_given_workspace(cuda_device):
+    # The plan's bytes do, one fewer is refused, before anything is launched.
+    gen = torch.Generator().manual_seed(39)
+    q_lens, lens = [40, 2], [900, 300]
+    pages, num = plain.make_pages(lens, gen)
+    (kc, ks), (vc, vs) = (plain.make_cache(lens, pages, num, 2, 64, gen) for _ in range(2))
+    q = torch.randn((42, 4, 64), generator=gen).bfloat16()
+    mask = masked.tree_masks(trees_of(q_lens, 7), 2)
+    args = dev(q, kc, vc, ks, vs, plain.cum(q_lens), i32(lens), pages)
+    grid, rows, need = fa.fa_paged_attn_plan(2, 42, 4, 2, 64, 40, masked=True)
+    assert rows == 256 and need > fa.fa_paged_attn_plan(2, 42, 4, 2, 64, 40)[2]
+    for kw in (dict(tree_mask=dev(mask)), dict(window_left=90, sink_tokens=7)):
+        want = fa.fa_paged_attn(*args, max_seqlen_q=40, **kw)
+        held = torch.full((need + 16,), 0xa5, dtype=torch.uint8, device="cuda")
+        got = fa.fa_paged_attn(*args, max_seqlen_q=40, workspace=held[:need], **kw)
+        assert torch.equal(got, want) and (held[need:] == 0xa5).all()
+        out = torch.full_like(got, 7.0)
+        with pytest.raises(fa.FaError):
+            fa.fa_paged_attn(*args, max_seqlen_q=40, workspace=held[:need - 1], out=out, **kw)
+        torch.cuda.synchronize()
+        assert (out == 7).all()
+    assert fa.fa_get_device_status() == fa.FA_OK
+
+
+def test_two_masked_graphs_at_once(cuda_device):
+    # A workspace each: both replay together, on streams of their own.
+    gen = torch.Generator().manual_seed(40)
+    q_lens, lens = [33, 6, 20], [2000, 700, 1500]
+    pages, num = plain.make_pages(lens, gen)
+    (kc, ks), (vc, vs) = (plain.make_cache(lens, pages, num, 2, 128, gen) for _ in range(2))
+    q = torch.randn((59, 8, 128), generator=gen).bfloat16()
+    args = dev(q, kc, vc, ks, vs, plain.cum(q_lens), i32(lens), pages)
+    mask = dev(masked.tree_masks(trees_of(q_lens, 8), 2))
+    calls = (dict(tree_mask=mask), dict(window_left=200, sink_tokens=5))
+    want = [fa.fa_paged_attn(*args, max_seqlen_q=33, **kw) for kw in calls]
+    torch.cuda.synchronize()
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in calls]
+    for kw in calls:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(fa.fa_paged_attn(*args, max_seqlen_q=33, **kw))
+    for _ in range(10):
+        for o in outs:
+            o.fill_(7.0)
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    assert fa.fa_get_device_status() == fa.FA_OK
+
+
 def test_masked_calls_in_a_graph(cuda_device):
     # Lengths, trees and queries change in place between replays.
     gen = torch.Generator().manual_seed(33)
@@ -535,6 +611,32 @@ def test_packed_masked_wait_limit_runs_out_then_recovers(cuda_device):
     got = fa.fa_varlen_fwd(q, k, v, cu, cu, 2000, 2000, **kw)
     torch.cuda.synchronize()
     assert fa.fa_get_device_status() == fa.FA_OK and torch.equal(got, want)
+
+
+def test_packed_masks_on_another_stream_and_in_a_graph(cuda_device):
+    gen = torch.Generator().manual_seed(41)
+    q_lens, k_lens = [33, 5], [700, 90]
+    q = dev(torch.randn((38, 4, 64), generator=gen).bfloat16())
+    k, v = (dev(torch.randn((790, 2, 64), generator=gen).bfloat16()) for _ in range(2))
+    cu_q, cu_k = dev(plain.cum(q_lens), plain.cum(k_lens))
+    mask = dev(masked.tree_masks(trees_of(q_lens, 10), 2))
+    for kw in (dict(tree_mask=mask), dict(window_left=60, sink_tokens=9)):
+        call = lambda **more: fa.fa_varlen_fwd(q, k, v, cu_q, cu_k, 33, 700, causal=True,
+                                               return_lse=True, **kw, **more)
+        want = call()
+        torch.cuda.synchronize()
+        s = torch.cuda.Stream()
+        got = call(stream=s)
+        s.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = call()
+        got[0].fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert fa.fa_get_device_status() == fa.FA_OK
 
 
 def test_packed_rows_behind_the_last_sequence_and_malformed_cu_seqlens(cuda_device):

@@ -51,6 +51,19 @@ def test_masked_attn_refusals(lib, kw, expect):
     assert attn(lib, **kw) == expect
 
 
+@pytest.mark.parametrize("kw,expect", [
+    (dict(B=0), INV), (dict(T=-1), INV), (dict(H=3), INV), (dict(Hk=0), INV), (dict(d=72), UNS),
+    (dict(mq=-1), INV),
+])
+def test_masked_plan_refusals(lib, kw, expect):
+    a = dict(B=2, T=64, H=4, Hk=2, d=64, mq=32)
+    a.update(kw)
+    grid, rows, need = ctypes.c_int(), ctypes.c_int(), ctypes.c_size_t()
+    args = [a[n] for n in "B T H Hk d mq".split()]
+    for plan in (lib.fa_paged_attn_masked_plan, lib.fa_paged_attn_plan):
+        assert plan(*args, ctypes.byref(grid), ctypes.byref(rows), ctypes.byref(need)) == expect
+
+
 def tree(lib, **kw):
     a = dict(par=P(0x1000), cu=P(0x2000), sl=P(0x3000), B=2, T=9, words=1, mask=P(0x4000),
              pos=P(0x5000))
