@@ -134,6 +134,7 @@ constexpr int kWeightPlans = 4;
 template <int N>
 struct alignas(16) WeightsCtl {
   uint64_t plan_full[kWeightPlans], plan_free[kWeightPlans];  // published / read by every warp
+  uint64_t scale_full[kWeightPlans];                          // its pages' scales are there
   uint64_t k_full[6], k_free[6];  // K slot landed / read
   uint64_t s_full[4], s_free[4];  // St computed / loaded (128)
   uint64_t q_full;                // rows of a chunk staged (all key threads)
@@ -183,6 +184,7 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
     for (int s = 0; s < kWeightPlans; ++s) {
       init(cb->plan_full[s], 1);
       init(cb->plan_free[s], kProducer);  // the warps before it
+      init(cb->scale_full[s], 1);
     }
     for (int s = 0; s < C::kSlots; ++s) {
       init(cb->k_full[s], 1);
@@ -254,23 +256,16 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
     for (int b = 0;; ++b) {
       const int slot = b % kWeightPlans;
       WeightPlan& plan = cb->plan[slot];
-      // Lane l: page l of the batch's tiles, as its cell, or -1, and its scale.
-      int cell = -1;
-      float scale = __int_as_float(0x7fffffff);
+      // Lane l: page l of the batch's tiles, as its cell, or -1.
+      int id = -1;
       int tile0 = 0, count = 0;
       WeightChunk wc = {};
       if (more) {
         tile0 = g.tile0 + t0;
         count = imin(16, g.count - t0);
         const long long p = (long long)tile0 * 2 + lane;
-        if (lane / 2 < count && p * kPageTokens < g.keys.hi) {
-          const int id = checked_page(
-              __ldg(a.page_table + (size_t)g.seq * a.max_pages + p), a.num_pages);
-          if (id >= 0) {
-            cell = id * sh.heads_k + g.head;
-            scale = __ldg(a.k_scale + cell);
-          }
-        }
+        if (lane / 2 < count && p * kPageTokens < g.keys.hi)
+          id = __ldg(a.page_table + (size_t)g.seq * a.max_pages + p);
         wc = weight_chunk(sh, c, rows, g.len);
       }
       if (b >= kWeightPlans) ok = wait(cb->plan_free[slot], (b / kWeightPlans - 1) & 1);
@@ -288,26 +283,36 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
         plan.tile0 = tile0;
         plan.first = t0 == 0;
         plan.any = wc.any(g.tile0 * kTileKeys, (g.tile0 + g.count) * (long long)kTileKeys);
+        ptx::mbar_arrive(ptx::smem_u32(&cb->plan_full[slot]));
       }
-      plan.scale[lane] = scale;
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->plan_full[slot]));
       if (!more) break;
+      // (The rows of Q are on their way now; the scales follow the first tile.)
+      id = checked_page(id, a.num_pages);
+      const int cell = id >= 0 ? id * sh.heads_k + g.head : -1;
+      const float scale = cell >= 0 ? __ldg(a.k_scale + cell) : __int_as_float(0x7fffffff);
 #pragma unroll 1
-      for (int t = 0; t < count; ++t) {
-        if (!wc.seen((tile0 + t) * kTileKeys)) continue;
-        const int mine = __shfl_sync(0xffffffffu, cell, 2 * t + (lane & 1));
-        const unsigned held = __ballot_sync(0xffffffffu, mine >= 0) & 3;
-        const int s = loads % C::kSlots;
-        if (loads >= C::kSlots) ok = wait(cb->k_free[s], (loads / C::kSlots - 1) & 1);
-        if (!ok) break;
-        const uint32_t bar = ptx::smem_u32(&cb->k_full[s]);
-        if (lane == 0) ptx::mbar_arrive_expect_tx(bar, ((held & 1) + (held >> 1)) * C::kPageBytes);
-        __syncwarp();
-        if (lane < 2 && mine >= 0)
-          ptx::tma_load_3d(ptx::smem_u32(smem + s * C::kTileBytes) + lane * C::kPageBytes, &k_map,
-                           bar, 0, 0, mine);
-        ++loads;
+      for (int t = 0; ok && t < count; ++t) {
+        if (wc.seen((tile0 + t) * kTileKeys)) {
+          const int mine = __shfl_sync(0xffffffffu, cell, 2 * t + (lane & 1));
+          const unsigned held = __ballot_sync(0xffffffffu, mine >= 0) & 3;
+          const int s = loads % C::kSlots;
+          if (loads >= C::kSlots) ok = wait(cb->k_free[s], (loads / C::kSlots - 1) & 1);
+          if (!ok) break;
+          const uint32_t bar = ptx::smem_u32(&cb->k_full[s]);
+          if (lane == 0)
+            ptx::mbar_arrive_expect_tx(bar, ((held & 1) + (held >> 1)) * C::kPageBytes);
+          __syncwarp();
+          if (lane < 2 && mine >= 0)
+            ptx::tma_load_3d(ptx::smem_u32(smem + s * C::kTileBytes) + lane * C::kPageBytes, &k_map,
+                             bar, 0, 0, mine);
+          ++loads;
+        }
+        if (t == 0) {
+          plan.scale[lane] = scale;
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->scale_full[slot]));
+        }
       }
       if (!ok) break;
       t0 += 16;
@@ -366,7 +371,7 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
   } else {
     // ------------------------------------------------------------- weights
     const float neg_inf = -__int_as_float(0x7f800000);
-    constexpr int kLanes = D / 8;  // lanes of a row of Q, 8 dims each
+    constexpr int kLanes = D / 16;  // lanes of a row of Q, 16 dims each
     const uint32_t s_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const int key = tid & 127, group = tid >> 7;  // key of a tile; warpgroup
     int i = 0, turn = 0;
@@ -384,63 +389,87 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
         const int rows = plan.rows, row0 = plan.row0, c = plan.c, head = plan.head;
         const int n_rows = imin(N, rows * sh.group - c * N);
         {
-          const int sub = tid % kLanes, dim0 = sub * 8;
-          uint8_t* q_s = smem + C::kQ;
-          constexpr int kStep = C::kKeyThreads / kLanes;    // rows at once
-          constexpr int kTurns = N / kStep;                 // of each thread, all under way
-          static_assert(N % kStep == 0, "rows of a chunk");
-          uint4 raw[kTurns];
+          // A warp's kEach rows: as bf16 into the place of their first two terms, a
+          // half of the dims each; then kLanes lanes take a row at a time, 16 dims
+          // each.  (In a short loop: its code is fetched anew for each unit.)
+          constexpr int kEach = N / (C::kKeyThreads / 32), kAtOnce = 32 / kLanes;
+          constexpr int kTurns = (kEach + kAtOnce - 1) / kAtOnce;
+          const int sub = lane % kLanes, dim0 = sub * 16;
+          uint8_t* warp_q = smem + C::kQ + warp * kEach * D;
+          uint8_t* raw0 = warp_q + (sub >= kLanes / 2 ? N * D : 0) + (sub % (kLanes / 2)) * 32;
           float lse_of[kTurns];
-          int token[kTurns];
 #pragma unroll
           for (int k = 0; k < kTurns; ++k) {
-            const int n = tid / kLanes + k * kStep, row = c * N + n;
-            token[k] = token_of(sh, row);
-            const int h = head * sh.group + row - token[k] * sh.group;
-            raw[k] = make_uint4(0u, 0u, 0u, 0u);
-            lse_of[k] = 0.f;
-            if (n < n_rows && dim0 < a.dim)
-              raw[k] = __ldg(reinterpret_cast<const uint4*>(
-                  a.q + (long long)(row0 + token[k]) * a.q_row + (long long)h * a.q_head + dim0));
-            if (n < n_rows && sub == 0)
-              lse_of[k] = __ldg(a.lse + (size_t)h * a.total_q + row0 + token[k]);
+            const int i = k * kAtOnce + lane / kLanes, n = warp * kEach + i, row = c * N + n;
+            const int tok = token_of(sh, row), h = head * sh.group + row - tok * sh.group;
+            const bool some = i < kEach && n < n_rows;
+            const uint16_t* from =
+                a.q + (some ? (long long)(row0 + tok) * a.q_row + (long long)h * a.q_head + dim0 : 0);
+            if (i < kEach) {
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const bool in = some && dim0 + 8 * u < a.dim;
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                 ptx::smem_u32(raw0 + i * D + 16 * u)),
+                             "l"(in ? from + 8 * u : a.q), "r"(in ? 16 : 0)
+                             : "memory");
+              }
+            }
+            // (A row that sees nothing, LSE -inf, or that is none, adds 0.)
+            lse_of[k] = some ? __ldg(a.lse + (size_t)h * a.total_q + row0 + tok) : neg_inf;
+            if (sub == 0 && i < kEach) cb->token[n] = some ? tok - token_of(sh, c * N) : -1;
           }
 #pragma unroll
           for (int k = 0; k < kTurns; ++k) {
-            const int n = tid / kLanes + k * kStep, tok = token[k];
-            const float lse = lse_of[k];
-            float x[8];
-            unpack_bf16x8(raw[k], x);
-            float mx = 0.f;
-            bool finite = true;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              finite = finite && fabsf(x[k]) <= 3.402823466e38f;
-              mx = fmaxf(mx, fabsf(x[k]));
+            const int i = k * kAtOnce + lane / kLanes, n = warp * kEach + i;
+            if (sub == 0 && i < kEach)
+              reinterpret_cast<float*>(cb->row + n / 2)[2 + (n & 1)] =
+                  lse_of[k] == neg_inf ? neg_inf : lse_of[k] * -1.4426950408889634f;
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          __syncwarp();
+#pragma unroll 1
+          for (int k = 0; k < kTurns; ++k) {
+            const int i = k * kAtOnce + lane / kLanes, n = warp * kEach + i;
+            uint4 r0 = make_uint4(0u, 0u, 0u, 0u), r1 = r0;
+            if (i < kEach) {
+              r0 = *reinterpret_cast<const uint4*>(raw0 + i * D);
+              r1 = *reinterpret_cast<const uint4*>(raw0 + i * D + 16);
             }
-            if (!finite) mx = __int_as_float(0x7f800000);
+            // The largest magnitude, as bits of bf16 (those past infinity's are NaN).
+            const uint32_t w[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+            uint32_t top = 0;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) top = __vmaxu2(top, w[u] & 0x7fff7fffu);
+            top = max(top & 0xffffu, top >> 16);
 #pragma unroll
             for (int o = kLanes / 2; o > 0; o >>= 1)
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              top = max(top, __shfl_xor_sync(0xffffffffu, top, o));  // (the row is read)
+            const float mx = __uint_as_float(min(top, 0x7f80u) << 16);
             const int e = terms_exponent(mx);
-            uint32_t hi[4], lo[4], rest[4];
+            float x[8];
+            uint32_t hi[8], lo[8], rest[8];
+            unpack_bf16x8(r0, x);
             split_terms(x, e, hi, lo);
             third_term(x, e, hi, lo, rest);
-            const int unit = dim0 >> 4;
-            const int us = D == 128 ? (unit ^ (n & 7)) : (unit ^ ((n >> 1) & 3));
-            uint8_t* at = q_s + n * D + us * 16 + (dim0 & 8);
-            *reinterpret_cast<uint2*>(at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-            *reinterpret_cast<uint2*>(at + N * D) =
-                make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-            *reinterpret_cast<uint2*>(at + 2 * N * D) =
-                make_uint2(rest[0] | rest[1] << 16, rest[2] | rest[3] << 16);
-            if (sub == 0) {
-              // A row that sees nothing (LSE -inf), or that is none, adds 0.
-              const bool none = n >= n_rows || lse == neg_inf;
-              float* r = reinterpret_cast<float*>(cb->row + n / 2) + (n & 1);
-              r[0] = none ? 0.f : terms_scale(mx, e, a.scale_log2);
-              r[2] = none ? neg_inf : lse * -1.4426950408889634f;
-              cb->token[n] = n < n_rows ? tok - token_of(sh, c * N) : -1;
+            unpack_bf16x8(r1, x);
+            split_terms(x, e, hi + 4, lo + 4);
+            third_term(x, e, hi + 4, lo + 4, rest + 4);
+            const int us = D == 128 ? (sub ^ (n & 7)) : (sub ^ ((n >> 1) & 3));
+            uint8_t* at = warp_q + i * D + us * 16;
+            auto put = [&](int term, const uint32_t* v) {
+              *reinterpret_cast<uint4*>(at + term * N * D) =
+                  make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16,
+                             v[6] | v[7] << 16);
+            };
+            if (i < kEach) {
+              put(0, hi);
+              put(1, lo);
+              put(2, rest);
+              if (sub == 0) {
+                float* r = reinterpret_cast<float*>(cb->row + n / 2) + (n & 1);
+                r[0] = r[2] == neg_inf ? 0.f : terms_scale(mx, e, a.scale_log2);
+              }
             }
           }
           ptx::fence_proxy_async_smem();
@@ -455,6 +484,7 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
       // The rows' own keys have no weight yet.
       const long long fresh = (long long)plan.len - plan.rows;
       const WeightChunk& wc = plan.chunk;
+      ok = wait(cb->scale_full[b % kWeightPlans], (b / kWeightPlans) & 1);
       // Sums of the rows' weights for this thread's key in kCount tiles from t on,
       // whose St are in the buffers from tile i on.
       auto add_up = [&](auto tiles, int t, float* sum) {
