@@ -32,7 +32,7 @@
 // One row of 64 sequences with 100 to 8192 keys, 32 and 4 heads of 128 dims: 34 us,
 // 4.2 TB/s; without any load of keys and weights it would take 24, launch, search,
 // rows and first tile of each CTA.  The last 32 rows of 4 prompts of 20001 to 32768
-// tokens, 8 kv heads (128 rows a unit): 48 us, of which 13 are the exponentials and
+// tokens, 8 kv heads (128 rows a unit): 45.5 us, of which 13 are the exponentials and
 // 17 the tensor core's; the rest is instruction issue and the latency of TMEM loads
 // of eight warps.
 #pragma once
