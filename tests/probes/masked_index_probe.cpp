@@ -40,6 +40,9 @@ extern "C" int probe_masked_walk(const int* cu, const int* lens, int batch, int 
   return found;
 }
 
+extern "C" int probe_range_start(int total, int ctas, int c) { return fa::range_start(total, ctas, c); }
+extern "C" int probe_range_of(int total, int ctas, int p) { return fa::range_of(total, ctas, p); }
+
 // Key tile of the u-th tile of row tile t of a sequence.
 extern "C" int probe_tile_of(int n, int len, int t, int heads_k, int group, int rows, int causal,
                              int window, int held, int sinks, int tree, int u) {

@@ -192,6 +192,18 @@ def test_segments_cover_every_seen_tile_once(probe):
 
 
 # ------------------------------------------------------- packed attention
+def test_a_place_is_in_the_range_that_holds_it(probe):
+    big = 2 ** 31 - 1
+    for total in (1, 2, 5, 151, 152, 153, 400, 4567, big - 1, big):
+        for ctas in (1, 2, 7, 152, 456):
+            starts = [probe.probe_range_start(total, ctas, c) for c in range(ctas + 1)]
+            places = {p for s in starts for p in (s - 1, s, s + 1)} | {0, total // 2, total - 1}
+            for p in places:
+                if 0 <= p < total:
+                    c = probe.probe_range_of(total, ctas, p)
+                    assert starts[c] <= p < starts[c + 1], (total, ctas, p)
+
+
 def packed(lib, **kw):
     a = dict(q=P(0x1000), qr=256, qh=64, k=P(0x2000), kr=256, kh=64, v=P(0x3000), vr=256, vh=64,
              cq=P(0x4000), ck=P(0x5000), batch=2, total_q=10, total_k=10, H=4, Hk=4, dqk=64, dv=64,

@@ -106,7 +106,7 @@ struct PagedAttnArgs {
   float scale_log2;
   uint16_t* out;
   float* lse;
-  float* part_o;    // [2 grid][N][D]
+  float* part_o;    // [2 grid][N][D] (wide: [2 grid][4][N][D / 4])
   float* part_lse;  // [2 grid][N], base 2
   // [grid][2] what the first CTA of a split unit leaves for the merge: (parts,
   // the sequence's first q row, first row of the tile, kv head), parts = 0:
@@ -897,9 +897,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       }
       if (plan.unit_end >= 0 && key == 0 && (alone || wg == 0)) {
         // The unit starts here: tell the merge how many CTAs share it.
-        int parts = 1;
-#pragma unroll 1
-        while (cta + parts < ctas && range_start(total, ctas, cta + parts) < plan.unit_end) ++parts;
+        const int parts = imin(range_of(total, ctas, plan.unit_end - 1), ctas - 1) - cta + 1;
         a.meta[2 * cta + 1] = make_int4(rows, slot, 0, 0);
         a.meta[2 * cta] = make_int4(parts, plan.q0, plan.row0, plan.head);
       }

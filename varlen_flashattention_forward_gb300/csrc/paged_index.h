@@ -195,6 +195,13 @@ FA_HD int range_start(int total, int ctas, int c) {
   return c * q + (c < r ? c : r);
 }
 
+// CTA whose range holds place p of `total` (0 <= p < total).
+FA_HD int range_of(int total, int ctas, int p) {
+  const unsigned q = (unsigned)total / (unsigned)ctas, r = (unsigned)total - q * (unsigned)ctas;
+  const unsigned longer = r * (q + 1), at = (unsigned)p;  // places of the ranges that are one longer
+  return (int)(at < longer ? at / (q + 1) : r + (at - longer) / q);
+}
+
 // Walks the segments of a range: the part of each unit's tiles inside it.
 // before(b) is the cost of the sequences before b (b up to the batch).
 struct Segment {

@@ -92,7 +92,7 @@ struct WideCfg {
 
 struct alignas(16) WideCtl {
   uint64_t plan_full[kPagedPlans], plan_free[kPagedPlans];  // batch published / read (15)
-  uint64_t scale_full[kPagedPlans];
+  uint64_t cell_full[kPagedPlans], scale_full[kPagedPlans];  // its pages, their scales there
   uint64_t k_full[6], k_free[6];      // K slot landed / read by both issuers' S
   uint64_t v_full[4], v_free[4];      // V slot landed / converted (128)
   uint64_t vh_full[2], vh_free[2];    // f16 V written (128) / read by both issuers' P V
@@ -136,6 +136,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     for (int s = 0; s < kPagedPlans; ++s) {
       init(cb->plan_full[s], 1);
       init(cb->plan_free[s], kPlanReaders);
+      init(cb->cell_full[s], 1);
       init(cb->scale_full[s], 1);
     }
     for (int s = 0; s < C::NK; ++s) {
@@ -364,9 +365,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const WidePlan& plan = plan_of(b, &ok);
         if (!ok) break;
         const int count = plan.count;
+        if (count == 0) break;
+        ok = wait(cb->cell_full[b % kPagedPlans], (b / kPagedPlans) & 1);
+        if (!ok) break;
         const int cell = plan.cell[lane];
         plan_done(b);
-        if (count == 0) break;
 #pragma unroll 1
         for (int n = 0; n < count; ++n) {
           const int mine = __shfl_sync(0xffffffffu, cell, 2 * n + (lane & 1));
@@ -406,17 +409,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       for (int b = 0;; ++b) {
         const int slot = b % kPagedPlans;
         WidePlan& plan = cb->plan[slot];
-        // Lane l: page l of the batch's tiles, as its cell of the cache, or -1
-        // where it is not needed or not there.
-        int cell = -1;
+        // Lane l: page l of the batch's tiles, or -1 where it is not needed.
+        int id = -1;
         if (more && n0 + lane / 2 < g.count) {
           const long long p = tile_of(g.tiles, g.part_lo + n0 + lane / 2) * 2ll + (lane & 1);
           if (p * kPageTokens < g.keys.hi &&
-              ((p + 1) * kPageTokens > g.keys.lo || p * kPageTokens < g.keys.sink)) {
-            const int id = checked_page(
-                __ldg(a.page_table + (size_t)g.seq * a.max_pages + p), a.num_pages);
-            if (id >= 0) cell = id * sh.heads_k + g.head;
-          }
+              ((p + 1) * kPageTokens > g.keys.lo || p * kPageTokens < g.keys.sink))
+            id = __ldg(a.page_table + (size_t)g.seq * a.max_pages + p);
         }
         if (b >= kPagedPlans) ok = wait(cb->plan_free[slot], (b / kPagedPlans - 1) & 1);
         if (!ok) break;
@@ -428,7 +427,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           break;
         }
         const bool last = g.count - n0 <= kPlanTiles;
-        plan.cell[lane] = cell;
         if (lane == 0) {
           const int left = g.tiles.head - (g.part_lo + n0);  // tiles before the gap
           plan.count = imin(g.count - n0, kPlanTiles);
@@ -448,9 +446,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           plan.rows = imin(kWideRows, g.q.n * sh.group - g.row_tile * kWideRows);
           plan.whole = g.count == g.unit_count;
           plan.unit_end = g.part_lo == 0 && g.count < g.unit_count ? g.unit_end : -1;
+          ptx::mbar_arrive(ptx::smem_u32(&cb->plan_full[slot]));
         }
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->plan_full[slot]));
+        // (The rows of Q are on their way now; then the pages, then their scales.)
+        id = checked_page(id, a.num_pages);
+        const int cell = id >= 0 ? id * sh.heads_k + g.head : -1;
+        plan.cell[lane] = cell;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&cb->cell_full[slot]));
         float ks = 0.f, vs = 0.f;
         if (cell >= 0) {
           ks = __ldg(a.k_scale + cell);
@@ -716,9 +720,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       ptx::tc_fence_after();
       if (unit_end >= 0 && tid == 0) {
         // The unit starts here: tell the merge how many CTAs share it.
-        int parts = 1;
-#pragma unroll 1
-        while (cta + parts < ctas && range_start(total, ctas, cta + parts) < unit_end) ++parts;
+        const int parts = imin(range_of(total, ctas, unit_end - 1), ctas - 1) - cta + 1;
         a.meta[2 * cta + 1] = make_int4(rows, slot, 0, 0);
         a.meta[2 * cta] = make_int4(parts, q0, row0, head);
       }
@@ -730,68 +732,88 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         else if (a.lse)
           a.lse[(size_t)row_h * a.total_q + row_q] = l2 * 0.69314718055994531f;
       }
-      // Through the rows' place in shared memory (Q's terms, read by the last S),
-      // 2 D bytes of each: D values as bf16, or half of them as fp32 by turns.  A
+      // Through the rows' place in shared memory (Q's terms, read by the last S).  A
       // warp's rows are its own, as they are when it stages the next rows of Q, which
       // it may do while the others still have outputs there: so a row's bytes lie
-      // where its two terms do.
-      constexpr int kUnits = D / 8;  // of 16 bytes, a half in each term's place
-      auto unit_at = [&](int row, int u) {
-        const int v = u % (kUnits / 2);
-        return q_tile + (u >= kUnits / 2 ? C::kTermBytes : 0) + row * D +
+      // where its two terms do, D in each.  (Weight 0: O_t may hold anything.)
+      auto unit_at = [&](int row, int term, int v) {  // 16 bytes
+        return q_tile + term * C::kTermBytes + row * D +
                (D == 128 ? (v ^ (row & 7)) : (v ^ ((row >> 1) & 3))) * 16;
       };
-      const uint64_t dst =
-          !valid ? 0
-          : whole ? reinterpret_cast<uint64_t>(a.out + ((size_t)row_q * a.heads + row_h) * a.dim)
-                  : reinterpret_cast<uint64_t>(a.part_o +
-                                               ((size_t)slot * kWideRows + t * 128 + r) * D);
-      const int units = whole ? a.dim / 8 : kUnits;
-      // (Weight 0: O_t may hold anything.  In short loops, as the rows of Q.)
-#pragma unroll 1
-      for (int turn = 0; turn < (whole ? 1 : 2); ++turn) {
-        const int c_end = whole ? D : (turn + 1) * (D / 2);
-#pragma unroll 1
-        for (int c0 = turn * (D / 2); c0 < c_end; c0 += 16) {
-          uint32_t o[16];
-          ptx::tmem_ld16(o_addr + c0, o);
-          ptx::tmem_wait_ld();
-          ptx::reg_fence16(o);
+      auto o_of = [&](int c0, uint32_t* o) {  // 16 dims
+        ptx::tmem_ld16(o_addr + c0, o);
+        ptx::tmem_wait_ld();
+        ptx::reg_fence16(o);
 #pragma unroll
-          for (int c = 0; c < 16; ++c)
-            o[c] = inv == 0.f ? 0u : __float_as_uint(__uint_as_float(o[c]) * inv);
-          // (unit: of the row's first 16 bytes of these)
-          const int unit = whole ? c0 / 8 : (c0 - turn * (D / 2)) / 4;
-          if (whole) {
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              o[c] = ptx::pack_bf16x2(__uint_as_float(o[2 * c]), __uint_as_float(o[2 * c + 1]));
-          }
-#pragma unroll
-          for (int c = 0; c < 16; c += 4) {
-            if (whole && c >= 8) break;
-            *reinterpret_cast<uint4*>(unit_at(r, unit + c / 4)) =
-                make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
-          }
-        }
-        if (turn == (whole ? 0 : 1)) {
-          ptx::tc_fence_before();
-          ptx::mbar_arrive(ptx::smem_u32(&cb->o_free[t]));
-        }
+        for (int c = 0; c < 16; ++c)
+          o[c] = inv == 0.f ? 0u : __float_as_uint(__uint_as_float(o[c]) * inv);
+      };
+      auto o_done = [&]() {
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(ptx::smem_u32(&cb->o_free[t]));
         __syncwarp();
-#pragma unroll 2
-        for (int k = 0; k < kUnits; ++k) {
-          // 32 units at a time, kUnits of a row next to each other.
-          const int n = (k * 32 + lane) / kUnits, u = lane % kUnits;
+      };
+      constexpr int kUnits = D / 16;  // of 16 bytes, in each term's place
+      if (!whole) {
+        // fp32, a quarter of the dims in each place: by two turns, a copy of the
+        // warp's rows for each quarter, as they lie (the merge knows how).
+        float* part = a.part_o + (size_t)slot * kWideRows * D + (t * 128 + (warp & 3) * 32) * (D / 4);
+        const bool some = rows > t * 128 + (warp & 3) * 32;
+#pragma unroll 1
+        for (int turn = 0; turn < 2; ++turn) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < D / 2; c0 += 16) {
+            uint32_t o[16];
+            o_of(turn * (D / 2) + c0, o);
+            const int unit = c0 / 4;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              *reinterpret_cast<uint4*>(unit_at(r, unit / kUnits, unit % kUnits + c)) =
+                  make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+          }
+          ptx::fence_proxy_async_smem();
+          if (turn == 0) __syncwarp();
+          else o_done();
+          if (lane == 0 && some) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              ptx::bulk_store(part + (size_t)(2 * turn + q) * kWideRows * (D / 4),
+                              ptx::smem_u32(q_tile + q * C::kTermBytes + (warp & 3) * 32 * D), 32 * D);
+            ptx::bulk_commit();
+            ptx::bulk_wait_read_all();
+          }
+          __syncwarp();
+        }
+      } else {
+        const uint64_t dst =
+            valid ? reinterpret_cast<uint64_t>(a.out + ((size_t)row_q * a.heads + row_h) * a.dim) : 0;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 16) {
+          uint32_t o[16];
+          o_of(c0, o);
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            o[c] = ptx::pack_bf16x2(__uint_as_float(o[2 * c]), __uint_as_float(o[2 * c + 1]));
+          const int unit = c0 / 8;
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            *reinterpret_cast<uint4*>(unit_at(r, unit / kUnits, unit % kUnits + c)) =
+                make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+        }
+        o_done();
+#pragma unroll 4
+        for (int k = 0; k < 2 * kUnits; ++k) {
+          // 32 units at a time, those of a row next to each other.
+          const int n = (k * 32 + lane) / (2 * kUnits), u = lane % (2 * kUnits);
           const uint64_t to = __shfl_sync(0xffffffffu, dst, n);
-          const int row_n = (warp & 3) * 32 + n;
-          if (to != 0 && u < units)
-            *reinterpret_cast<uint4*>(to + turn * D * 2 + u * 16) =
-                *reinterpret_cast<const uint4*>(unit_at(row_n, u));
+          const uint4 v = *reinterpret_cast<const uint4*>(
+              unit_at((warp & 3) * 32 + n, u / kUnits, u % kUnits));
+          if (to != 0 && u < a.dim / 8) *reinterpret_cast<uint4*>(to + u * 16) = v;
         }
         __syncwarp();
       }
     }
+    ptx::bulk_wait_all();
   }
 
   ptx::tc_fence_before();
@@ -820,6 +842,12 @@ __global__ void __launch_bounds__(kWideMergeThreads) paged_wide_merge_kernel(con
   for (int n = blockIdx.y * (kWideMergeThreads / 32) + warp; n < m1.x;
        n += gridDim.y * (kWideMergeThreads / 32)) {
     auto lse_of = [&](int p) { return a.part_lse[(size_t)slot(p) * kWideRows + n]; };
+    // (A quarter of the dims of all rows, then the next one's, 16 bytes in the order
+    // of the rows' places in shared memory.)
+    constexpr int kUnits = D / 16;
+    const int u = lane * kEach / 4, place = u % kUnits;
+    const int mine = (u / kUnits * kWideRows + n) * (D / 4) + lane * kEach % 4 +
+                     (D == 128 ? (place ^ (n & 7)) : (place ^ ((n >> 1) & 3))) * 4;
     float top = neg_inf;
     for (int p = lane; p < parts; p += 32) top = fmaxf(top, lse_of(p));
 #pragma unroll
@@ -830,7 +858,7 @@ __global__ void __launch_bounds__(kWideMergeThreads) paged_wide_merge_kernel(con
 #pragma unroll 4
     for (int p = 0; p < parts; ++p) {
       const float lp = lse_of(p);
-      const float* o = a.part_o + ((size_t)slot(p) * kWideRows + n) * D + lane * kEach;
+      const float* o = a.part_o + (size_t)slot(p) * kWideRows * D + mine;
       const float w = lp == neg_inf ? 0.f : root_ex2(lp - top);
       sum = fmaf(w, w, sum);
       float v[kEach];
