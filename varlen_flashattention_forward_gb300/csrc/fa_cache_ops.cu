@@ -125,6 +125,9 @@ extern "C" fa_status fa_paged_key_weights(
   a.keys = std::min(max_pages_per_seq * fa::kPageTokens, capacity);
   a.shape = {num_heads_k, group, n, causal != 0, window_left, a.keys, sink_tokens, 0};
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  const double log2e = (double)a.scale_log2 / softmax_scale;
+  a.lse_log2 = (float)log2e;
+  a.lse_log2_rest = (float)(log2e - a.lse_log2);
   a.decay = decay;
   a.capacity = capacity;
   a.status = dev.status;

@@ -62,7 +62,10 @@ struct KeyWeightsArgs {
   int batch, total_q, dim, max_pages, num_pages;
   AttnShape shape;   // rows: N
   int keys;          // positions of a sequence that have a page and a weight
-  float scale_log2, decay;
+  // The scores' factor, and the LSE's in two terms: log2(e) as scale_log2, once
+  // rounded, holds it.  (Large scores and LSE cancel: with a factor 6e-8 off in one of
+  // them, a weight of a score of 40 would be 2e-6 off.)
+  float scale_log2, lse_log2, lse_log2_rest, decay;
   float* weights;    // [batch, kv heads, capacity]
   long long capacity;
   unsigned int* status;
@@ -424,7 +427,9 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
             const int i = k * kAtOnce + lane / kLanes, n = warp * kEach + i;
             if (sub == 0 && i < kEach)
               reinterpret_cast<float*>(cb->row + n / 2)[2 + (n & 1)] =
-                  lse_of[k] == neg_inf ? neg_inf : lse_of[k] * -1.4426950408889634f;
+                  lse_of[k] == neg_inf
+                      ? neg_inf
+                      : -fmaf(lse_of[k], a.lse_log2, lse_of[k] * a.lse_log2_rest);
           }
           asm volatile("cp.async.wait_all;" ::: "memory");
           __syncwarp();
