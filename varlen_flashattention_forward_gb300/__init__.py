@@ -650,9 +650,8 @@ def fa_paged_attn(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, seq_lens,
     index, here = _device(stream, q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, seq_lens,
                           page_table, out, lse, workspace, tree_mask)
     with here:
-        # (new_empty: of the type and device of a tensor at hand, and quicker.)
         if out is None:
-            out = q.new_empty((T, H, d))
+            out = torch.empty((T, H, d), dtype=torch.bfloat16, device=q.device)
         else:
             _check(out, "out", torch.bfloat16, 3)
             _shape(out, "out", (T, H, d))
@@ -660,11 +659,11 @@ def fa_paged_attn(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, seq_lens,
             _check(lse, "lse", torch.float32, 2)
             _shape(lse, "lse", (H, T))
         elif return_lse:
-            lse = k_scale.new_empty((H, T))
+            lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
         masked = words > 0 or sink_tokens != 0
         if workspace is None:
             need = _attn_workspace(index, batch, T, H, hk, d, max_seqlen_q, masked)
-            workspace = k_scale.new_empty(((need + 3) // 4,))
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         else:
             _check(workspace, "workspace", torch.uint8, 1)
             need = workspace.shape[0]
@@ -733,11 +732,11 @@ def fa_draft_tree(parents, cu_seqlens, seq_lens, max_nodes=64, tree_mask=None, p
             if max_nodes < 1:
                 raise ValueError(f"max_nodes must be at least 1, got {max_nodes}")
             words = -(-int(max_nodes) // 32)
-            tree_mask = parents.new_empty((total, words))
+            tree_mask = torch.empty((total, words), dtype=i32, device=parents.device)
         else:
             words = _tree_words(tree_mask, total)
         if positions is None:
-            positions = parents.new_empty((total,))
+            positions = torch.empty(total, dtype=i32, device=parents.device)
         else:
             _check(positions, "positions", i32, 1)
             _shape(positions, "positions", (total,))
@@ -858,12 +857,12 @@ def fa_paged_kv_select(weights, seq_lens, budget, sink_tokens=0, recent_tokens=0
     index, here = _device(stream, weights, seq_lens, keep, new_lens)
     with here:
         if keep is None:
-            keep = seq_lens.new_empty((batch, hk, max(budget, 0)))
+            keep = torch.empty((batch, hk, max(budget, 0)), dtype=i32, device=seq_lens.device)
         else:
             _check(keep, "keep", i32, 3)
             _shape(keep, "keep", (batch, hk, budget))
         if new_lens is None:
-            new_lens = seq_lens.new_empty((batch,))
+            new_lens = torch.empty(batch, dtype=i32, device=seq_lens.device)
         else:
             _check(new_lens, "new_lens", i32, 1)
             _shape(new_lens, "new_lens", (batch,))

@@ -33,14 +33,16 @@
 //
 // TMEM: S_0 / P_0, S_1 / P_1 (two pages each), O_0, O_1, 128 columns each.
 //
-// 24 trees of 33 to 64 nodes over 517 to 5000 keys, 32 and 8 heads of 128 dims: 86
-// us with the merge, 580 TFLOP/s (384 us 32 rows to a tile, 157 us through the
-// gather and the packed forward).  Of some 150 000 cycles of a CTA, 28 tiles take
+// 24 trees of 33 to 64 nodes over 517 to 5000 keys, 32 and 8 heads of 128 dims: 82
+// us with the merge, 610 TFLOP/s (384 us 32 rows to a tile, 157 us through the
+// gather and the packed forward).  Of some 135 000 cycles of a CTA, 28 tiles take
 // 3500 each: softmax 2700 (exponentials 1330, masks and maxima 370, rescaling 450,
 // TMEM 450), waiting for S 500; the tensor core's own share is 2150.  A whole tile
 // of scores at once, with P in its place, took 4200 to 5000, the chain S, softmax,
-// P V of each row tile.  A change of unit takes some 17 000: rows of Q 8000, bound by
-// the conversions to e4m3, output 7000.
+// P V of each row tile.  A change of unit takes some 13 000: rows of Q 8000, bound by
+// the conversions to e4m3, output 3000 (7000 to 10 000 with parts copied by the lanes).
+// One tree of 16 nodes over 4096 keys: 22 us, of 24 000 cycles in the longest CTA 2400
+// up to the split, 3200 for its first unit, 7000 for the rows, 7000 for three tiles.
 #pragma once
 
 #include <cstddef>
