@@ -161,8 +161,10 @@ extern "C" fa_status fa_paged_kv_select(const float* weights, const int* seq_len
   if (!is_aligned(weights, 4) || !is_aligned(seq_lens, 4) || !is_aligned(keep, 4) ||
       !is_aligned(new_lens, 4))
     return FA_ERR_INVALID_ARG;
-  if ((int64_t)batch * num_heads_k > INT32_MAX || capacity > INT32_MAX - fa::kSelectThreads ||
-      budget > INT32_MAX - fa::kSelectThreads)
+  // (A cluster's threads step over keys and budget together: an index passes the end
+  // by as many at most.)
+  constexpr int kMostKeys = INT32_MAX - fa::kSelectThreads * fa::kSelectCtas;
+  if ((int64_t)batch * num_heads_k > INT32_MAX || capacity > kMostKeys || budget > kMostKeys)
     return FA_ERR_UNSUPPORTED;
   fa::DeviceFacts dev;
   const fa_status st = fa::device_facts(&dev);
