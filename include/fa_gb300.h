@@ -601,7 +601,7 @@ fa_status fa_paged_attn_masked_plan(int batch, int total_q, int num_heads, int n
  * Rows behind the last sequence are left as they were.
  *
  * Host errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED (total * tree_words past
- * 2^31 - 1), FA_ERR_ARCH, FA_ERR_LAUNCH.
+ * 2^31 - 1, total past 2^31 - 1 - 65536), FA_ERR_ARCH, FA_ERR_LAUNCH.
  */
 fa_status fa_draft_tree(const int* parents, const int* cu_seqlens, const int* seq_lens, int batch,
                         int total, int tree_words, int* tree_mask, int* positions,

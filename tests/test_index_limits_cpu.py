@@ -42,3 +42,22 @@ def test_select_takes_the_largest_rows_that_fit(lib):
     none = (fa.FA_ERR_LAUNCH, fa.FA_ERR_ARCH)
     assert select(lib, MOST - STRIDE, 64) in none
     assert select(lib, MOST - STRIDE, MOST - STRIDE) in none
+
+
+def tree(lib, total, words=1):
+    return lib.fa_draft_tree(P(0x1000), P(0x2000), P(0x3000), 1, total, words, P(0x4000), None, None)
+
+
+# 1024 blocks of 64 threads go through a sequence's nodes 65536 at a time.
+NODES = 1024 * 64
+
+
+@pytest.mark.parametrize("past", [1, 63, 64, 1000, NODES - 1, NODES])
+def test_draft_tree_refuses_nodes_whose_strides_pass_32_bits(lib, past):
+    assert tree(lib, MOST - NODES + past) == fa.FA_ERR_UNSUPPORTED
+
+
+def test_draft_tree_takes_as_many_nodes_as_fit(lib):
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    assert tree(lib, MOST - NODES) in (fa.FA_ERR_LAUNCH, fa.FA_ERR_ARCH)

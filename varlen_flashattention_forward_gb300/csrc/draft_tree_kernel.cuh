@@ -22,6 +22,7 @@ struct DraftTreeArgs {
 };
 
 constexpr int kTreeThreads = 64;
+constexpr int kTreeBlocks = 1024;  // of a sequence, at most
 
 // Block (x, b): nodes of sequence b from kTreeThreads * x on, in steps of the
 // grid.

@@ -63,14 +63,17 @@ extern "C" fa_status fa_draft_tree(const int* parents, const int* cu_seqlens, co
   if (!is_aligned(parents, 4) || !is_aligned(cu_seqlens, 4) || !is_aligned(seq_lens, 4) ||
       !is_aligned(tree_mask, 4) || !is_aligned(positions, 4))
     return FA_ERR_INVALID_ARG;
-  if ((int64_t)total * tree_words > INT32_MAX) return FA_ERR_UNSUPPORTED;
+  // (A sequence's threads step over its nodes together: a node's number passes the last
+  // by as many at most.)
+  constexpr int kMostNodes = INT32_MAX - fa::kTreeBlocks * fa::kTreeThreads;
+  if ((int64_t)total * tree_words > INT32_MAX || total > kMostNodes) return FA_ERR_UNSUPPORTED;
   fa::DeviceFacts dev;
   const fa_status st = fa::device_facts(&dev);
   if (st != FA_OK) return st;
   if (total == 0) return FA_OK;
   // Blocks for the mean number of nodes; a longer tree's go round.
   const int mean = (int)(((int64_t)total + batch - 1) / batch);
-  const int blocks = std::min((mean + fa::kTreeThreads - 1) / fa::kTreeThreads, 1024);
+  const int blocks = std::min((mean + fa::kTreeThreads - 1) / fa::kTreeThreads, fa::kTreeBlocks);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // (A grid has at most 65535 blocks in y.)
   for (int b0 = 0; b0 < batch; b0 += 65535) {
