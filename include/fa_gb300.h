@@ -213,7 +213,8 @@ fa_status fa_varlen_fwd_strided(const void* q, long long q_row_stride, long long
  *                 nodes' are seen by all of them, within the window: node i
  *                 stands at position Lk - Lq + d_i, d_i its depth, the number
  *                 of bits of its mask less one.  The nodes' own keys are seen by
- *                 the bits alone.  Nodes from 32 * tree_words on, and bits past
+ *                 the bits alone, whatever the window: with one, the masks are
+ *                 those of fa_draft_tree_windowed.  Nodes from 32 * tree_words on, and bits past
  *                 the last node, name no key.  causal is not used then and
  *                 window_right is -1.
  *
@@ -552,7 +553,8 @@ fa_status fa_paged_attn(const void* q, long long q_row_stride, long long q_head_
  *                 them, within the window: node i stands at position
  *                 seq_len - n + d_i, d_i its depth, the number of bits of its
  *                 mask less one.  The nodes' own keys are seen by the bits
- *                 alone, whatever the window.  Nodes from 32 * tree_words on,
+ *                 alone, whatever the window: with one, the masks are those
+ *                 of fa_draft_tree_windowed.  Nodes from 32 * tree_words on,
  *                 and bits past the last node, name no key.  causal is not
  *                 used then.
  *
@@ -606,6 +608,28 @@ fa_status fa_paged_attn_masked_plan(int batch, int total_q, int num_heads, int n
 fa_status fa_draft_tree(const int* parents, const int* cu_seqlens, const int* seq_lens, int batch,
                         int total, int tree_words, int* tree_mask, int* positions,
                         fa_stream_t stream);
+
+/*
+ * fa_draft_tree_windowed -- fa_draft_tree for an attention with a sliding window:
+ * arguments, rules and errors as there, and
+ *
+ *   window_left, sink_tokens   those of the attention call that takes the masks
+ *                 (-1: no window, as fa_draft_tree).  Bit p of node i's mask is set
+ *                 for itself, its ancestors up to window_left nodes back, and those
+ *                 whose position is below sink_tokens.
+ *
+ * Attention under these masks is that of decoding each path token by token under
+ * the window.  (fa_draft_tree's masks name all ancestors, which the attention then
+ * sees whatever its window; the two differ for nodes deeper than the window.)
+ * positions hold every ancestor, left out or not.
+ *
+ * Host errors: as fa_draft_tree; FA_ERR_INVALID_ARG also for a window_left below
+ * -1 and a negative sink_tokens.
+ */
+fa_status fa_draft_tree_windowed(const int* parents, const int* cu_seqlens, const int* seq_lens,
+                                 int batch, int total, int tree_words, int window_left,
+                                 int sink_tokens, int* tree_mask, int* positions,
+                                 fa_stream_t stream);
 
 /*
  * fa_paged_attn_plan -- the launch shape and the workspace of a fa_paged_attn

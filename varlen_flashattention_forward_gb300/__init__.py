@@ -31,7 +31,7 @@ Entry points (same names as the C ABI):
                 window_left=-1, out=None, lse=None, return_lse=False, workspace=None,
                 stream=None, sink_tokens=0, tree_mask=None)
   fa_draft_tree(parents, cu_seqlens, seq_lens, max_nodes=64, tree_mask=None, positions=None,
-                stream=None)
+                stream=None, window_left=-1, sink_tokens=0)
   fa_paged_attn_plan(batch, total_q, num_heads, num_heads_k, head_dim, max_seqlen_q=0,
                      masked=False)
   fa_paged_key_weights(q, lse, k_cache, k_scale, cu_seqlens_q, seq_lens, page_table, weights,
@@ -70,7 +70,8 @@ EXPORTS = ("fa_varlen_fwd", "fa_varlen_fwd_plan", "fa_varlen_fwd_strided", "fa_v
            "fa_sparse_mla_decode",
            "fa_sparse_mla_decode_plan", "fa_sparse_mla_decode_noalloc", "fa_merge_attn_states",
            "fa_qk_norm_rope", "fa_paged_kv_append", "fa_paged_attn", "fa_paged_attn_plan",
-           "fa_paged_attn_masked", "fa_paged_attn_masked_plan", "fa_draft_tree", "fa_paged_key_weights", "fa_paged_kv_select",
+           "fa_paged_attn_masked", "fa_paged_attn_masked_plan", "fa_draft_tree",
+           "fa_draft_tree_windowed", "fa_paged_key_weights", "fa_paged_kv_select",
            "fa_paged_kv_compact", "fa_paged_kv_gather", "fa_get_device_status",
            "fa_set_wait_limit_ns", "fa_status_string")
 
@@ -137,6 +138,8 @@ def load_library():
     lib.fa_paged_attn_masked.restype = i32
     lib.fa_draft_tree.argtypes = [p, p, p, i32, i32, i32, p, p, p]
     lib.fa_draft_tree.restype = i32
+    lib.fa_draft_tree_windowed.argtypes = [p, p, p, i32, i32, i32, i32, i32, p, p, p]
+    lib.fa_draft_tree_windowed.restype = i32
     lib.fa_paged_key_weights.argtypes = [p, i64, i64, p, p, p, p, p, p, i32, i32, i32, i32, i32, i32,
                                          i32, f32, i32, i32, i32, f32, p, i32, p]
     lib.fa_paged_key_weights.restype = i32
@@ -219,8 +222,9 @@ def fa_varlen_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q=0,
 
     sink_tokens: the first keys of a sequence that stay visible behind its
     window.  tree_mask [total_q, words] int32: the query rows are nodes of
-    drafted trees and see the keys of the nodes their bits name (fa_draft_tree),
-    and all keys before; causal is not used then (fa_varlen_fwd_masked).
+    drafted trees and see the keys of the nodes their bits name (fa_draft_tree,
+    given the same window and sinks) and, within the window, all keys before; causal
+    is not used then (fa_varlen_fwd_masked).
     """
     import torch
     lib = load_library()
@@ -629,8 +633,9 @@ def fa_paged_attn(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, seq_lens,
 
     sink_tokens: the first keys of a sequence that stay visible behind its
     window.  tree_mask [total_q, words] int32: the query rows are nodes of
-    drafted trees and see the keys of the nodes their bits name (fa_draft_tree),
-    and all keys before; causal is not used then.
+    drafted trees and see the keys of the nodes their bits name (fa_draft_tree,
+    given the same window and sinks) and, within the window, all keys before; causal
+    is not used then.
     """
     import torch
     lib = load_library()
@@ -708,15 +713,18 @@ def _tree_words(tree_mask, total):
 
 
 def fa_draft_tree(parents, cu_seqlens, seq_lens, max_nodes=64, tree_mask=None, positions=None,
-                  stream=None):
-    """Ancestor masks and positions of drafted trees; see fa_draft_tree in
-    include/fa_gb300.h.
+                  stream=None, window_left=-1, sink_tokens=0):
+    """Ancestor masks and positions of drafted trees; see fa_draft_tree and
+    fa_draft_tree_windowed in include/fa_gb300.h.
 
     parents [total] int32 (within its sequence, -1: follows the context),
     cu_seqlens [batch+1] int32 (each sequence's nodes), seq_lens [batch] int32
     (lengths with the nodes), max_nodes the largest tree's nodes.  Returns
     (tree_mask [total, words] int32, positions [total] int32): the mask of
     fa_paged_attn and fa_varlen_fwd, the positions of fa_qk_norm_rope.
+
+    window_left, sink_tokens: those of the attention call that takes the mask, which
+    then leaves out the ancestors that decoding a path token by token would not see.
     """
     import torch
     lib = load_library()
@@ -740,9 +748,10 @@ def fa_draft_tree(parents, cu_seqlens, seq_lens, max_nodes=64, tree_mask=None, p
         else:
             _check(positions, "positions", i32, 1)
             _shape(positions, "positions", (total,))
-        st = lib.fa_draft_tree(parents.data_ptr(), cu_seqlens.data_ptr(), seq_lens.data_ptr(),
-                               batch, total, words, tree_mask.data_ptr(), positions.data_ptr(),
-                               _raw_stream(index))
+        st = lib.fa_draft_tree_windowed(
+            parents.data_ptr(), cu_seqlens.data_ptr(), seq_lens.data_ptr(), batch, total, words,
+            _window(window_left), _sinks(sink_tokens), tree_mask.data_ptr(), positions.data_ptr(),
+            _raw_stream(index))
     if st != FA_OK:
         raise FaError(st, "fa_draft_tree")
     return tree_mask, positions

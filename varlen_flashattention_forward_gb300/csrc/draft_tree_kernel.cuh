@@ -2,6 +2,12 @@
 //
 //   mask(i) = { i } + mask(parent(i)),   position(i) = seq_len - n + depth(i)
 //
+// and under a window w, for an attention with the same one, of these only the nodes
+// that i sees when its path is decoded one after another: itself and its ancestors up
+// to w nodes back, and those whose position is below `sinks`.  (The attention takes a
+// node's depth from the bits of its mask.  Where some are left out there are w + 1 of
+// them or more, and that window ends behind the context as the node's own does.)
+//
 // A thread takes a node and walks up to the root.  Parents are smaller
 // numbers, so the walk passes the words of its mask from the last to the
 // first and writes each once; it takes at most as many steps as there are
@@ -18,6 +24,7 @@ namespace fa {
 struct DraftTreeArgs {
   const int *parents, *cu, *seq_lens;
   int total, words;
+  int window, sinks;  // window: 0x7fffffff for none
   int *mask, *positions;
 };
 
@@ -32,9 +39,23 @@ __global__ void __launch_bounds__(kTreeThreads) draft_tree_kernel(const DraftTre
   const long long context = (long long)__ldg(a.seq_lens + b) - r.n;
   for (int i = blockIdx.x * kTreeThreads + threadIdx.x; i < r.n; i += gridDim.x * kTreeThreads) {
     int* row = a.mask + (size_t)(r.lo + i) * a.words;
+    auto parent = [&](int node) {
+      const int up = __ldg(a.parents + r.lo + node);
+      return up < node ? up : -1;
+    };
+    // Ancestors more than `late` nodes back are sinks.  (Only where the sinks reach
+    // past the context.)
+    int late = 0x7fffffff;
+    if (a.window != 0x7fffffff && a.sinks > context) {
+      long long d = 0;
+      for (int node = parent(i); node >= 0; node = parent(node)) ++d;
+      d += context - a.sinks;
+      late = (int)(d > -1 ? d : -1);
+    }
     int node = i, depth = -1, word = a.words - 1;
     unsigned bits = 0;
     while (node >= 0) {
+      ++depth;
       const int w = node >> 5;
       // (Nodes past the mask's words leave no bit.)
       if (w <= word) {
@@ -42,11 +63,9 @@ __global__ void __launch_bounds__(kTreeThreads) draft_tree_kernel(const DraftTre
           row[word] = (int)bits;
           bits = 0;
         }
-        bits |= 1u << (node & 31);
+        if (depth <= a.window || depth > late) bits |= 1u << (node & 31);
       }
-      ++depth;
-      const int up = __ldg(a.parents + r.lo + node);
-      node = up < node ? up : -1;
+      node = parent(node);
     }
     for (; word >= 0; --word) {
       row[word] = (int)bits;

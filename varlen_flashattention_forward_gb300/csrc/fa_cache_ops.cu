@@ -58,8 +58,17 @@ fa_status launched() { return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR
 extern "C" fa_status fa_draft_tree(const int* parents, const int* cu_seqlens, const int* seq_lens,
                                    int batch, int total, int tree_words, int* tree_mask,
                                    int* positions, fa_stream_t stream) {
+  return fa_draft_tree_windowed(parents, cu_seqlens, seq_lens, batch, total, tree_words, -1, 0,
+                                tree_mask, positions, stream);
+}
+
+extern "C" fa_status fa_draft_tree_windowed(const int* parents, const int* cu_seqlens,
+                                            const int* seq_lens, int batch, int total,
+                                            int tree_words, int window_left, int sink_tokens,
+                                            int* tree_mask, int* positions, fa_stream_t stream) {
   if (!cu_seqlens || !seq_lens || (total > 0 && (!parents || !tree_mask))) return FA_ERR_INVALID_ARG;
-  if (batch < 1 || total < 0 || tree_words < 1) return FA_ERR_INVALID_ARG;
+  if (batch < 1 || total < 0 || tree_words < 1 || window_left < -1 || sink_tokens < 0)
+    return FA_ERR_INVALID_ARG;
   if (!is_aligned(parents, 4) || !is_aligned(cu_seqlens, 4) || !is_aligned(seq_lens, 4) ||
       !is_aligned(tree_mask, 4) || !is_aligned(positions, 4))
     return FA_ERR_INVALID_ARG;
@@ -74,11 +83,12 @@ extern "C" fa_status fa_draft_tree(const int* parents, const int* cu_seqlens, co
   // Blocks for the mean number of nodes; a longer tree's go round.
   const int mean = (int)(((int64_t)total + batch - 1) / batch);
   const int blocks = std::min((mean + fa::kTreeThreads - 1) / fa::kTreeThreads, fa::kTreeBlocks);
+  const int window = window_left < 0 ? INT32_MAX : window_left;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // (A grid has at most 65535 blocks in y.)
   for (int b0 = 0; b0 < batch; b0 += 65535) {
-    const fa::DraftTreeArgs a = {parents,    cu_seqlens + b0, seq_lens + b0, total,
-                                 tree_words, tree_mask,       positions};
+    const fa::DraftTreeArgs a = {parents, cu_seqlens + b0, seq_lens + b0, total,    tree_words,
+                                 window,  sink_tokens,     tree_mask,     positions};
     fa::draft_tree_kernel<<<dim3(blocks, std::min(batch - b0, 65535)), fa::kTreeThreads, 0, s>>>(a);
   }
   return launched();
