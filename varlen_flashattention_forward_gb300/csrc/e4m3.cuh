@@ -31,11 +31,17 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
   return d;
 }
-// Two e4m3 codes as f16x2 (exact).
+// Two e4m3 (e5m2) codes as f16x2 (exact).
 __device__ __forceinline__ uint32_t unpack_e4m3x2(uint32_t codes) {
   uint32_t d;
   const uint16_t c = (uint16_t)codes;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t unpack_e5m2x2(uint32_t codes) {
+  uint32_t d;
+  const uint16_t c = (uint16_t)codes;
+  asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(d) : "h"(c));
   return d;
 }
 __device__ __forceinline__ float2 f16x2_floats(uint32_t h) {
@@ -70,17 +76,24 @@ __device__ __forceinline__ void split_terms(const float* x, int e, uint32_t* hi,
     lo[k] = c;
   }
 }
-// What is left of the row, at most half of e4m3's last step (2^-10): in e5m2, whose
-// last step is 2^-16.
-__device__ __forceinline__ void third_term(const float* x, int e, const uint32_t* hi,
-                                           const uint32_t* lo, uint32_t* rest) {
+// The same row in three terms, hi in e4m3 and two in e5m2, off by at most 2^-17 (2^-24
+// of the row's largest).  A bf16 has four bits behind hi's where hi is normal, which
+// e5m2's three hold: they are 0 to 8 steps.  Below that hi leaves up to 2^-10, mid up to
+// 2^-14 of it, and rest, whose last step is 2^-16, half of that.  (With mid in e4m3, whose
+// last step is 2^-9, 2^-10 would be left to rest, and 2^-14 behind it.)
+__device__ __forceinline__ void split_three(const float* x, int e, uint32_t* hi, uint32_t* mid,
+                                            uint32_t* rest) {
   const float f = __uint_as_float((uint32_t)(7 - e + 127) << 23);
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     uint32_t y = ptx::pack_f16x2(x[2 * k] * f, x[2 * k + 1] * f);
     uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(y));
+    hi[k] = c;
     asm("sub.f16x2 %0, %0, %1;" : "+r"(y) : "r"(unpack_e4m3x2(hi[k])));
-    asm("sub.f16x2 %0, %0, %1;" : "+r"(y) : "r"(unpack_e4m3x2(lo[k])));
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(c) : "r"(y));
+    mid[k] = c;
+    asm("sub.f16x2 %0, %0, %1;" : "+r"(y) : "r"(unpack_e5m2x2(mid[k])));
     asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(c) : "r"(y));
     rest[k] = c;
   }

@@ -9,9 +9,9 @@
 // come: no maximum, no V and no second pass.
 //
 // The transposed form of paged_attn_kernel: St[key, row] = K[key, d] Q[row, d]t
-// as products of K as it lies in the cache and Q as two e4m3 terms and a third in
-// e5m2 (the weights are kept in fp32, where the two alone are 2^-17 of a row's
-// largest value off: a sum's error of 4e-6 instead of 1e-6).  A thread has a key:
+// as products of K as it lies in the cache and Q as three terms, one in e4m3 and two in
+// e5m2, off by 2^-24 of a row's largest value (split_three; two e4m3 terms, 2^-17 off, gave
+// sums an error of 4e-6 instead of 1e-6).  A thread has a key:
 // its weights' sum over the rows stays in the thread, in a fixed order, and no two
 // threads write the same place.
 //
@@ -82,7 +82,7 @@ struct WeightsCfg {
   static constexpr int kPageBytes = kPageTokens * D;
   static constexpr int kTiles = N >= 64 ? 2 : 1;  // of a key thread at once
   static constexpr int kBuffers = 2 * kTiles;     // of St
-  // Columns of a buffer: the products with Q's e4m3 terms side by side, so that the
+  // Columns of a buffer: the products with Q's e5m2 terms side by side, so that the
   // tensor core reads K once for both, or, where there are many rows, in one sum.
   static constexpr bool kApart = N <= 32;
   static constexpr int kCols = kApart ? 2 * N : N;
@@ -332,12 +332,12 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
       wait_drain_warp(ptx::smem_u32(&cb->k_full[s]), ((loads - 1 - s) / C::kSlots) & 1, a.status);
   } else if (warp == kIssuer) {
     // ---------------------------------------------------------- MMA issuer
-    constexpr uint32_t idesc = ptx::idesc_e4m3_f32(128, C::kCols);
+    constexpr uint32_t idesc = ptx::idesc_e4m3_f32(128, N);
+    constexpr uint32_t idesc_e5m2 = ptx::idesc_e4m3_e5m2_f32(128, C::kCols);
     const uint64_t q_hi = ptx::smem_desc(ptx::smem_u32(smem + C::kQ), 16, 8 * D, C::kSwK);
-    const uint64_t q_lo = ptx::smem_desc(ptx::smem_u32(smem + C::kQ + N * D), 16, 8 * D, C::kSwK);
+    const uint64_t q_mid = ptx::smem_desc(ptx::smem_u32(smem + C::kQ + N * D), 16, 8 * D, C::kSwK);
     const uint64_t q_rest =
         ptx::smem_desc(ptx::smem_u32(smem + C::kQ + 2 * N * D), 16, 8 * D, C::kSwK);
-    constexpr uint32_t idesc_rest = ptx::idesc_e4m3_e5m2_f32(128, N);
     int i = 0, staged = 0;
     for (int b = 0; ok; ++b) {
       const WeightPlan& plan = plan_of(b, &ok);
@@ -360,11 +360,11 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
         // (The small terms first: each step rounds at the sum's size so far.)
         const uint32_t d = tmem + sb * C::kCols;
         if constexpr (C::kApart) {
-          ptx::mma_f8_elect<D / 32>(d, kd, q_hi, idesc);  // and q_lo, N columns on
-          ptx::mma_f8_elect<D / 32, true>(d + N, kd, q_rest, idesc_rest);
+          ptx::mma_f8_elect<D / 32>(d, kd, q_mid, idesc_e5m2);  // and q_rest, N columns on
+          ptx::mma_f8_elect<D / 32, true>(d, kd, q_hi, idesc);
         } else {
-          ptx::mma_f8_elect<D / 32>(d, kd, q_rest, idesc_rest);
-          ptx::mma_f8_elect<D / 32, true>(d, kd, q_lo, idesc);
+          ptx::mma_f8_elect<D / 32>(d, kd, q_rest, idesc_e5m2);
+          ptx::mma_f8_elect<D / 32, true>(d, kd, q_mid, idesc_e5m2);
           ptx::mma_f8_elect<D / 32, true>(d, kd, q_hi, idesc);
         }
         ptx::mma_commit_elect(ptx::smem_u32(&cb->s_full[sb]));
@@ -456,13 +456,11 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
             const float mx = __uint_as_float(min(top, 0x7f80u) << 16);
             const int e = terms_exponent(mx);
             float x[8];
-            uint32_t hi[8], lo[8], rest[8];
+            uint32_t hi[8], mid[8], rest[8];
             unpack_bf16x8(r0, x);
-            split_terms(x, e, hi, lo);
-            third_term(x, e, hi, lo, rest);
+            split_three(x, e, hi, mid, rest);
             unpack_bf16x8(r1, x);
-            split_terms(x, e, hi + 4, lo + 4);
-            third_term(x, e, hi + 4, lo + 4, rest + 4);
+            split_three(x, e, hi + 4, mid + 4, rest + 4);
             const int us = D == 128 ? (sub ^ (n & 7)) : (sub ^ ((n >> 1) & 3));
             uint8_t* at = warp_q + i * D + us * 16;
             auto put = [&](int term, const uint32_t* v) {
@@ -472,7 +470,7 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
             };
             if (i < kEach) {
               put(0, hi);
-              put(1, lo);
+              put(1, mid);
               put(2, rest);
               if (sub == 0) {
                 float* r = reinterpret_cast<float*>(cb->row + n / 2) + (n & 1);
