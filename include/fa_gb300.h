@@ -197,7 +197,8 @@ fa_status fa_varlen_fwd_strided(const void* q, long long q_row_stride, long long
 
 /*
  * fa_varlen_fwd_masked -- fa_varlen_fwd_strided with two more masks.  Arguments,
- * rules, launch shape (fa_varlen_fwd_plan's) and errors as there, and
+ * rules and errors as there (the launch shape is fa_varlen_fwd_plan's, but for a
+ * split-KV cluster size that counts the sinks' keys and a tree's as well), and
  *
  *   sink_tokens   the first keys of each sequence, which stay visible to rows
  *                 whose window has left them behind (attention sinks): row i at

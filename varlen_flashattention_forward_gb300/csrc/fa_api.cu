@@ -27,6 +27,7 @@
 #include "merge_kernel.cuh"
 #include "sparse_decode_kernel.cuh"
 #include "varlen_fwd_kernel.cuh"
+#include "varlen_shape.h"
 
 namespace fa {
 cudaError_t launch_varlen_64_64(const VarlenMaps&, const VarlenArgs&, const VarlenLaunch&,
@@ -194,8 +195,8 @@ fa_status stream_workspace(cudaStream_t stream, size_t need, void** out) {
 // heads per group), and the sum of the ceilings is at most
 // floor((total_q + (t - 1) batch) / t), so no more work items than
 // item_bound exist (packed short segments only make fewer).  The KV tiles of one item
-// are estimated from the max_seqlen_k hint (else total_k) and the window;
-// they only steer the split-KV choice, never correctness.
+// are estimated (item_key_tiles); they only steer the split-KV choice, never
+// correctness.
 // GQA head-group packing factor (log2): the largest power of two P <= 16
 // that divides the group size num_heads / num_heads_k and still leaves a
 // work item (256 / P tokens) at least as many tokens as a sequence is
@@ -213,21 +214,15 @@ int pack_shift_for(int batch, int total_q, int num_heads, int num_heads_k, int m
 
 fa::VarlenLaunch launch_shape(int sm_count, int batch, int total_q, int total_k, int num_heads,
                               int max_seqlen_k, int causal, int window_left, int window_right,
-                              int pack_shift) {
+                              int sinks, long long tree_nodes, int pack_shift) {
   fa::VarlenLaunch L;
   L.sm_count = sm_count;
   // With packing an item holds 256 / P tokens of P heads.
   const long long tpi = fa::kRowsPerItem >> pack_shift;
   L.item_bound = (long long)(num_heads >> pack_shift) *
                  (((long long)total_q + (tpi - 1) * batch) / tpi);
-  long long kv = total_k;
-  if (max_seqlen_k > 0 && max_seqlen_k < kv) kv = max_seqlen_k;
-  if (window_left >= 0 && (causal || window_right >= 0)) {
-    const long long span =
-        (long long)window_left + (causal ? 0 : window_right) + fa::kRowsPerItem;
-    if (span < kv) kv = span;
-  }
-  L.kv_tiles = (kv + fa::kBN - 1) / fa::kBN;
+  L.kv_tiles = fa::item_key_tiles(total_k, max_seqlen_k, causal, window_left, window_right, sinks,
+                                  tree_nodes, fa::kRowsPerItem, fa::kBN);
   return L;
 }
 
@@ -396,6 +391,10 @@ extern "C" fa_status fa_varlen_fwd_masked(
   args.pack_shift = pack_shift;
   args.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
 
+  // (A tree's: the hint, else the mean.)
+  const long long tree_nodes =
+      !tree ? 0 : max_seqlen_q > 0 ? max_seqlen_q : ((long long)total_q + batch - 1) / batch;
+
   // One launch per chunk of at most kMaxBatch sequences (the kernel keeps a
   // chunk's work list in shared memory).  cu_seqlens hold absolute token
   // offsets, so a chunk is the same arrays from its first sequence on; the
@@ -407,7 +406,7 @@ extern "C" fa_status fa_varlen_fwd_masked(
     args.batch = nb;
     const fa::VarlenLaunch L = launch_shape(dev->sm_count, nb, total_q, total_k, num_heads,
                                             max_seqlen_k, causal, window_left, window_right,
-                                            pack_shift);
+                                            sink_tokens, tree_nodes, pack_shift);
     const cudaError_t e = launch(maps, args, L, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return FA_ERR_LAUNCH;
   }
@@ -442,7 +441,7 @@ extern "C" fa_status fa_varlen_fwd_plan(int batch, int total_q, int total_k, int
   if (total_q == 0) return FA_OK;
   const fa::VarlenLaunch L =
       launch_shape(dev->sm_count, std::min(batch, fa::kMaxBatch), total_q, total_k, num_heads,
-                   max_seqlen_k, causal, window_left, window_right, pack_shift);
+                   max_seqlen_k, causal, window_left, window_right, 0, 0, pack_shift);
   return plan(L, grid, split) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
