@@ -748,10 +748,15 @@ def fa_draft_tree(parents, cu_seqlens, seq_lens, max_nodes=64, tree_mask=None, p
         else:
             _check(positions, "positions", i32, 1)
             _shape(positions, "positions", (total,))
-        st = lib.fa_draft_tree_windowed(
-            parents.data_ptr(), cu_seqlens.data_ptr(), seq_lens.data_ptr(), batch, total, words,
-            _window(window_left), _sinks(sink_tokens), tree_mask.data_ptr(), positions.data_ptr(),
-            _raw_stream(index))
+        if window_left == -1 and sink_tokens == 0:
+            st = lib.fa_draft_tree(parents.data_ptr(), cu_seqlens.data_ptr(), seq_lens.data_ptr(),
+                                   batch, total, words, tree_mask.data_ptr(), positions.data_ptr(),
+                                   _raw_stream(index))
+        else:
+            st = lib.fa_draft_tree_windowed(
+                parents.data_ptr(), cu_seqlens.data_ptr(), seq_lens.data_ptr(), batch, total, words,
+                _window(window_left), _sinks(sink_tokens), tree_mask.data_ptr(),
+                positions.data_ptr(), _raw_stream(index))
     if st != FA_OK:
         raise FaError(st, "fa_draft_tree")
     return tree_mask, positions
