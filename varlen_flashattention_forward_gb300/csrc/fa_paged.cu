@@ -42,7 +42,11 @@ struct AttnLaunch {
 // masked: under sinks or a tree, where more than 16 rows go 256 to a tile
 // (paged_wide_kernel): trees of 5 and 8 nodes, 4 heads of a group (20 and 32 rows),
 // 24 sequences of 517 to 5000 keys, 8 kv heads of 128 dims 64 and 65 us, 32 to a
-// tile 70 and 76; 4 nodes (16 rows) 16 to a tile 54 us; 64 nodes 86 against 384.
+// tile 70 and 76; 4 nodes (16 rows) 16 to a tile 54 us; 64 nodes 82 against 384.  A
+// step behind sinks, windows of 4095 keys, 17, 32 and 64 heads of 128 dims on one kv
+// head: 64 sequences of 100 to 16384 keys 38, 38 and 38 us, 16 to a tile 47, 49 and 77; but
+// 4 sequences of 8000 to 16384 keys 28, 28 and 29 against 20, 20 and 22 (the change of
+// unit, where a CTA has one).
 AttnLaunch attn_launch(int sm_count, int batch, int total_q, int group, int head_dim,
                        int max_seqlen_q, bool masked) {
   AttnLaunch l;

@@ -33,7 +33,7 @@
 // One row of 64 sequences with 100 to 8192 keys, 32 and 4 heads of 128 dims: 34 us,
 // 4.2 TB/s; without any load of keys and weights it would take 24, launch, search,
 // rows and first tile of each CTA.  The last 32 rows of 4 prompts of 20001 to 32768
-// tokens, 8 kv heads (128 rows a unit): 45.5 us, of which 13 are the exponentials and
+// tokens, 8 kv heads (128 rows a unit): 46 us, of which 13 are the exponentials and
 // 17 the tensor core's, and 9 the way to the first tile.  A pair's products and its
 // sums follow each other (four buffers fill TMEM), so that no part is hidden well:
 // without the rows' factors 6 us less, without exponentials 5, without two of three
@@ -67,7 +67,9 @@ struct KeyWeightsArgs {
   int keys;          // positions of a sequence that have a page and a weight
   // The scores' factor, and the LSE's in two terms: log2(e) as scale_log2, once
   // rounded, holds it.  (Large scores and LSE cancel: with a factor 6e-8 off in one of
-  // them, a weight of a score of 40 would be 2e-6 off.)
+  // them, a weight of a score of 40 would be 2e-6 off.  What is left at 128 dims, 1.1e-6
+  // of a sum, is mostly the products' sums, which the tensor core cuts: 7e-7 too small;
+  // 4e-7 at 64 dims, half as many steps.)
   float scale_log2, lse_log2, lse_log2_rest, decay;
   float* weights;    // [batch, kv heads, capacity]
   long long capacity;
@@ -93,7 +95,7 @@ struct WeightsCfg {
   static constexpr int kCtl = kQ + kQBytes;
   static constexpr int kKeyThreads = 128 * kTiles;
   static constexpr int kThreads = kKeyThreads + 64;
-  // Resident CTAs (by shared memory, 57 to 133 KB at 128 dims, and columns).
+  // Resident CTAs (by shared memory, 64 to 149 KB at 128 dims, and columns).
   static constexpr int kResident = N <= 32 ? 3 : N == 64 ? 2 : 1;
 };
 

@@ -282,8 +282,8 @@ __device__ __forceinline__ uint32_t largest_code(const uint4& c) {
 // and write them under it.
 //
 // 64 caches of 1000 to 8192 tokens, 8 heads of 128 dims, to 2048 kept rows each:
-// 107 us, 5.0 TB/s read and written, bound by instruction issue (codes' maxima and
-// new scales) and DRAM's turns between reads and writes.  One cache of 32768 to 4097
+// 107 us, 5.0 TB/s read and written (a copy 6.8), bound by instruction issue, codes'
+// maxima and new scales.  One cache of 32768 to 4097
 // rows of 96 dims: 16 us, four rounds of a cluster of eight.  Entries, pages and
 // scales looked up round by round made the first 186 us, a page's rows spread over
 // the whole block 129, copies through shared memory a round ahead 156.
