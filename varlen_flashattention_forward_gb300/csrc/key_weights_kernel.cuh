@@ -442,7 +442,8 @@ __global__ void __launch_bounds__(WeightsCfg<D, N>::kThreads, WeightsCfg<D, N>::
           for (int k = 0; k < kTurns; ++k) {
             const int i = k * kAtOnce + lane / kLanes, n = warp * kEach + i;
             uint4 r0 = make_uint4(0u, 0u, 0u, 0u), r1 = r0;
-            if (i < kEach) {
+            // (A row that adds nothing is zeros: a NaN of its would stay one times 0.)
+            if (i < kEach && reinterpret_cast<const float*>(cb->row + n / 2)[2 + (n & 1)] != neg_inf) {
               r0 = *reinterpret_cast<const uint4*>(raw0 + i * D);
               r1 = *reinterpret_cast<const uint4*>(raw0 + i * D + 16);
             }
