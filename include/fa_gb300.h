@@ -119,6 +119,10 @@ typedef enum {
  *   out           bf16 [total_q, num_heads, d_v]  (written)
  *   lse           fp32 [num_heads, total_q] natural-log LSE, or NULL.
  *
+ * V has to be finite, between and behind the sequences too: keys go 128 at a
+ * time, one that a row does not see has weight 0, and 0 times an infinity or a NaN
+ * is NaN.  K may hold anything there.
+ *
  * A query row with no visible key gets O = 0 and LSE = -inf.  With
  * total_q = 0 nothing is launched (q, out and lse may then be NULL); with
  * total_k = 0 every row has no visible key (k and v may then be NULL).
