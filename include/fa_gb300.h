@@ -669,7 +669,8 @@ fa_status fa_paged_attn_plan(int batch, int total_q, int num_heads, int num_head
  *   q, cu_seqlens_q, seq_lens, page_table, k_cache, k_scale, causal,
  *   window_left, sink_tokens   as the attention call of the same rows.
  *   lse           fp32 [num_heads, total_q]: what that call returned.  A row
- *                 with -inf adds nothing.
+ *                 with -inf adds nothing, whatever its q (to a key that is NaN
+ *                 itself, NaN).
  *   decay         0 .. 1.  0: W is not read (it may hold anything).
  *   weights       fp32 [batch, num_heads_k, capacity], updated: row b is that of
  *                 sequence b.  The last n of its keys, the rows' own, count as
